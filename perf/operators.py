@@ -5,7 +5,7 @@ or, where ``own`` is true, with the package's calls.
 
 MX4, the 4-bit cache: uint8 [num_blocks, Hkv, block_size / 16, 18 * D].  One record holds 16 tokens of one KV head:
 K codes [16, D / 2] (e2m1, the even channel in the low nibble), K block scales [16, D / 16] (e4m3), V codes [16, D / 2],
-V block scales [D / 16, 16].  value = scale * block scale * e2m1 value, scale one number or one per (head, channel).
+V block scales [16, D / 16].  value = scale * block scale * e2m1 value, scale one number or one per (head, channel).
 """
 import math
 import random
@@ -166,11 +166,11 @@ def _unpack(b):
 
 
 def _fields(rec, D):
-    """Views of the fields of records [..., 18 D]: K codes, K scales, V codes, V scales (token-major)."""
+    """Views of the fields of records [..., 18 D]: K codes, K scales, V codes, V scales."""
     kc = rec[..., :8 * D].unflatten(-1, (16, D // 2))
     ks = rec[..., 8 * D:9 * D].unflatten(-1, (16, D // 16))
     vc = rec[..., 9 * D:17 * D].unflatten(-1, (16, D // 2))
-    vs = rec[..., 17 * D:].unflatten(-1, (D // 16, 16)).transpose(-1, -2)
+    vs = rec[..., 17 * D:].unflatten(-1, (16, D // 16))
     return kc, ks, vc, vs
 
 
@@ -481,7 +481,7 @@ def _exact_record(rec, D):
     k = e2m1(nibbles(at(0, 8 * D, (16, D // 2))))
     ks = e4m3(at(8 * D, D, (16, D // 16)))
     v = e2m1(nibbles(at(9 * D, 8 * D, (16, D // 2))))
-    vs = e4m3(at(17 * D, D, (D // 16, 16))).transpose(-1, -2)
+    vs = e4m3(at(17 * D, D, (16, D // 16)))
     return k * ks.repeat_interleave(16, -1), v * vs.repeat_interleave(16, -1)
 
 
