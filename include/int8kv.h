@@ -71,6 +71,13 @@ typedef enum {
                              dequantised with the scales (onnxruntime PR 29912, Schema:
                              cache element type float8e4m3fn) */
 
+#define I8KV_CACHE_MX4 4  /* paged_decode_mx4 / rope_and_cache / gather_cache only: 4-bit e2m1
+                             codes in blocks of 16 channels, an e4m3 scale for each (the record
+                             layout below), times the scales */
+
+#define I8KV_ROPE_HALVES 0      /* rope_and_cache: channels i and i + rot_dim / 2 turn together */
+#define I8KV_ROPE_INTERLEAVED 1 /* rope_and_cache: channels 2i and 2i + 1 turn together         */
+
 #define I8KV_GEOM_WAVE 0       /* onnx-genai PR 1350 rule (num_splits from one wave)        */
 #define I8KV_GEOM_POW2_TILES 1 /* onnxruntime PR 33707 rule (power-of-two tiles per split)  */
 #define I8KV_GEOM_BALANCED 2   /* decode_plan, paged path: balanced pieces (see paged_decode) */
@@ -92,6 +99,9 @@ typedef enum {
 #define I8KV_FLAG_WAIT_TIMEOUT 0x20u /* dsa_prefill's tensor-core kernel: a CTA gave up waiting
                                         (about a second) for its own asynchronous copies or
                                         tensor-core products; its outputs are NaN          */
+
+#define I8KV_FLAG_BAD_POSITION 0x40u /* rope_and_cache: a position outside [0, max_pos): that token
+                                        was skipped                                         */
 
 /* Human-readable name of a status code (static storage). */
 const char* i8kv_status_string(int status);
@@ -144,15 +154,16 @@ size_t split_workspace_bytes(int32_t units, int32_t num_splits, int32_t G, int32
 /*
  * decode_plan -- the geometry a decode call uses when it is given
  * num_splits = 0 (automatic), for the current device.
- *   path: I8KV_PATH_DSA or I8KV_PATH_PAGED; cache_dtype: I8KV_CACHE_INT8 or
- *   I8KV_CACHE_FP16 (paged only); cap: max_sel (DSA) or max_blocks*block_size
- *   (paged); rows: S (DSA) or B (paged); mode / override_value as in
- *   split_geometry.  wave_ctas = SM count x resident CTAs per SM of the
+ *   path: I8KV_PATH_DSA or I8KV_PATH_PAGED; cache_dtype: I8KV_CACHE_INT8, or
+ *   (paged only) I8KV_CACHE_FP16, I8KV_CACHE_FP8 or I8KV_CACHE_MX4; cap: max_sel
+ *   (DSA) or max_blocks*block_size (paged); rows: S (DSA) or B (paged); mode /
+ *   override_value as in split_geometry.  wave_ctas = SM count x resident CTAs per SM of the
  *   selected decode kernel (queried from the CUDA occupancy API and cached per
  *   device); granule = 64 (POW2_TILES) or 16 (WAVE); min_chunk = 128;
  *   mode I8KV_GEOM_BALANCED (paged path only, else I8KV_EUNSUPPORTED):
  *   num_splits = min(32, max(2, 2 x the WAVE rule's automatic count)) partial
- *   slots and chunk = 0, for paged_decode's balanced pieces;
+ *   slots and chunk = 0, for paged_decode's balanced pieces (an MX4 cache with
+ *   cap <= 256: one split);
  *   max_splits = I8KV_MAX_SPLITS.  For the paged path in WAVE mode with
  *   override_value 0 the chunk is then moved to the multiple of one round of
  *   the paged kernel's CTA (4 warps x its step: 128 positions for an int8 or
@@ -403,6 +414,126 @@ i8kv_status reshape_and_cache(const uint16_t* k_new, const uint16_t* v_new,
                               int32_t D, void* k_cache, void* v_cache, int64_t num_slots,
                               const float* k_scale, const float* v_scale, int32_t scale_kind,
                               int32_t cache_dtype, uint32_t* flags, void* stream);
+
+/*
+ * The MX4 cache -- 4-bit keys and values with a scale for every 16 channels.
+ *   cache [num_blocks, Hkv, block_size / 16, 18 * D] bytes, 16-byte aligned,
+ *   block_size a multiple of 16.  One record of 18 * D bytes holds 16
+ *   consecutive tokens of a block for one KV head (one contiguous copy):
+ *     [0, 8D)    K codes   [16, D / 2]   e2m1, channel 2j in the low nibble of
+ *                                        byte j, channel 2j + 1 in the high one
+ *     [8D, 9D)   K scales  [16, D / 16]  float8 e4m3fn, >= 0, one per 16 channels
+ *     [9D, 17D)  V codes   [16, D / 2]
+ *     [17D, 18D) V scales  [16, D / 16]
+ *   K[t, g, d] = k_scale * (block scale * code value), V likewise, with k_scale
+ *   and v_scale per tensor ([1]) or per channel ([Hkv, D]) as everywhere here.
+ *   The product block scale * code value has 6 significant bits: it is exact in
+ *   fp16 and fp32.  9 / 16 of a byte per value.
+ *   D: 64, 128 or 256.
+ * mx4_cache_bytes -- bytes of such a cache, 0 for sizes it does not take.  Host
+ * arithmetic only.
+ */
+size_t mx4_cache_bytes(int64_t num_blocks, int32_t block_size, int32_t Hkv, int32_t D);
+
+/*
+ * rope_and_cache -- append new rows to a paged cache, the position rotation
+ * applied on the way: q and k rotated, q written out, k and v written into the
+ * cache in its type, all in one launch.  With p = positions[n], R = rot_dim and
+ * the pair (a, b) = channels (i, i + R/2) (I8KV_ROPE_HALVES) or (2i, 2i + 1)
+ * (I8KV_ROPE_INTERLEAVED), i = 0 .. R/2 - 1:
+ *     a' = a cos[p, i] - b sin[p, i]     b' = b cos[p, i] + a sin[p, i]
+ * in fp32, each product and the sum rounded on its own (no fused
+ * multiply-add: the stored codes follow from the formula bit for bit).
+ * Channels >= R are not turned.
+ *     q_out = fp16(q')
+ *     I8KV_CACHE_FP16: cache row = fp16(k'), v; the scales are not used
+ *     I8KV_CACHE_INT8, I8KV_CACHE_FP8: the codes that reshape_and_cache stores of
+ *        k' (in fp32, not rounded to fp16 first) and v
+ *     I8KV_CACHE_MX4: y = x * fl(1 / scale); per block of 16 channels the scale
+ *        s = the e4m3fn value nearest max |y| * fl(1 / 6) (ties to even, at most
+ *        448), code = the e2m1 value nearest y * fl(1 / s) (ties to even, at most
+ *        +-6); s = 0 stores codes 0.  A NaN stores 0 and does not count in the
+ *        maximum.
+ *   q, k_new, v_new [num_tokens, H, D] fp16, H = Hq, Hkv, Hkv: the heads of a
+ *                  token contiguous, the tokens q_stride / k_stride / v_stride
+ *                  elements apart (multiples of 8: the three may be slices of one
+ *                  projection's output).  q may be NULL with Hq = 0.
+ *   positions      [num_tokens] int32; may be NULL with rot_dim = 0
+ *   cos_sin        [max_pos, rot_dim] fp32: rot_dim / 2 cosines, then the sines;
+ *                  16-byte aligned; may be NULL with rot_dim = 0
+ *   rot_dim        0 .. D, a multiple of 16; with I8KV_ROPE_HALVES and an MX4
+ *                  cache a multiple of 32 (I8KV_EUNSUPPORTED otherwise)
+ *   slot_mapping   [num_tokens] int32, as for reshape_and_cache: < 0 writes no
+ *                  cache row (q is still rotated); >= num_slots: the same, and
+ *                  I8KV_FLAG_BAD_SLOT.  A slot named twice ends up with either
+ *                  row, or a mixture of the two.
+ *   q_out          [num_tokens, Hq, D] fp16, dense; may be q itself where
+ *                  q_stride = Hq * D
+ *   k_cache, v_cache [num_slots, Hkv, D] of the cache type; with I8KV_CACHE_MX4
+ *                  k_cache is the record cache and v_cache is NULL
+ *   block_size     of an MX4 cache (num_slots = num_blocks * block_size); not
+ *                  looked at otherwise
+ *   D a multiple of 16 (64, 128 or 256 for MX4).
+ * A token whose position is outside [0, max_pos) is skipped (its q_out and cache
+ * rows stay as they were) and raises I8KV_FLAG_BAD_POSITION unless its slot is
+ * < 0 (padding).
+ */
+i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                           int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
+                           const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                           int32_t rot_dim, int32_t rot_style, const int32_t* slot_mapping,
+                           int32_t num_tokens, int32_t Hq, int32_t Hkv, int32_t D,
+                           uint16_t* q_out, void* k_cache, void* v_cache, int32_t cache_dtype,
+                           int64_t num_slots, int32_t block_size, const float* k_scale,
+                           const float* v_scale, int32_t scale_kind, uint32_t* flags,
+                           void* stream);
+
+/*
+ * gather_cache -- cache rows back as fp16 values (the inverse of the append, for
+ * a dense prefill over a cached prefix, or to look at what is stored):
+ *     out[n, g, :] = fp16(scale * value of the cache row (slot_mapping[n], g)),
+ * the fp32 product rounded once; a row of zeros for a slot < 0, and for a slot
+ * >= num_slots, which raises I8KV_FLAG_BAD_SLOT.  An fp16 cache is copied.
+ *   slot_mapping [num_rows] int32, any order, repeats allowed
+ *   k_out, v_out [num_rows, Hkv, D] fp16, 16-byte aligned; either may be NULL
+ *   caches, cache_dtype, num_slots, block_size, scales and D as for
+ *   rope_and_cache (all four cache types).
+ */
+i8kv_status gather_cache(const int32_t* slot_mapping, int32_t num_rows, int32_t Hkv, int32_t D,
+                         const void* k_cache, const void* v_cache, int32_t cache_dtype,
+                         int64_t num_slots, int32_t block_size, const float* k_scale,
+                         const float* v_scale, int32_t scale_kind, uint16_t* k_out,
+                         uint16_t* v_out, uint32_t* flags, void* stream);
+
+/*
+ * paged_decode_mx4 -- paged_decode_ex over an MX4 cache: one new token per
+ * sequence, split over the cache's length and joined.
+ *   cache        [num_blocks, Hkv, block_size / 16, 18 * D] (see above)
+ *   num_splits, chunk  as for paged_decode; num_splits = 0: automatic, the values
+ *                of decode_plan(I8KV_PATH_PAGED, I8KV_CACHE_MX4,
+ *                I8KV_WINDOW_SPAN(cap, window), ..., I8KV_GEOM_BALANCED): one split
+ *                for a short span, else balanced pieces (chunk 0).  Balanced pieces
+ *                take any batch size here: the live lengths are cut on the device
+ *                into pieces of about equal length, about one occupancy wave of
+ *                them over the batch, at most num_splits per row.
+ *   other arguments as for paged_decode_ex, without slots_out; the partials in
+ *   the workspace have the same layout.
+ * Numerics: the K and V values of the cache are exact in the fp16 products;
+ * Q * k_scale is rounded to fp16 with one power of two per head taken out (per
+ * channel scales; a scale per tensor is applied to the fp32 scores), so its
+ * range is not limited, and I8KV_FLAG_QUERY_RANGE and I8KV_FLAG_FP32_PATH are not
+ * raised; the probabilities are rounded to fp16 (a relative 2^-12), the sums
+ * are fp32.
+ */
+i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* k_scale,
+                             const float* v_scale, int32_t scale_kind,
+                             const int32_t* block_table, const int32_t* seq_lens, int32_t B,
+                             int32_t Hq, int32_t Hkv, int32_t D, int32_t block_size,
+                             int32_t max_blocks, int64_t num_blocks, float softmax_scale,
+                             const float* head_sink, float softcap, int32_t window,
+                             int32_t num_splits, int32_t chunk, void* workspace,
+                             size_t workspace_bytes, uint16_t* out, float* lse, uint32_t* flags,
+                             void* stream);
 
 /*
  * dsa_decode_static_workspace -- dsa_decode without a caller-supplied

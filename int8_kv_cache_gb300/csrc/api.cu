@@ -31,6 +31,13 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 
 int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// log2 of a power of two, -1 of any other number.
+int32_t log2_of(int32_t x) {
+  for (int32_t sh = 0; sh < 31; ++sh)
+    if (x == (1 << sh)) return sh;
+  return -1;
+}
+
 bool supported_head_dim(int32_t D) { return D == 64 || D == 128 || D == 256; }
 
 // Shape checks shared by the decode / prefill calls.
@@ -64,6 +71,7 @@ KernelKey make_key(Path path, int32_t D, int32_t G, int32_t cache_dtype, bool p_
   k.fp16_cache = cache_dtype == I8KV_CACHE_FP16;
   k.fp8_cache = cache_dtype == I8KV_CACHE_FP8;
   k.p_lo = p_lo;
+  k.mx4_cache = cache_dtype == I8KV_CACHE_MX4;
   return k;
 }
 
@@ -73,6 +81,7 @@ cudaError_t launch_key(const KernelKey& key, const DecodeParams& p, cudaStream_t
     return key.p_lo ? i8kv::launch_dsa_decode(key, p, s, info)
                     : i8kv::launch_dsa_prefill(key, p, s, info);
   }
+  if (key.mx4_cache) return i8kv::launch_paged_mx4(key, p, s, info);
   if (key.fp16_cache) return i8kv::launch_paged_fp16(key, p, s, info);
   if (key.fp8_cache) return i8kv::launch_paged_fp8(key, p, s, info);
   return i8kv::launch_paged_int8(key, p, s, info);
@@ -88,13 +97,13 @@ struct WaveInfo {
 
 i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
   static std::mutex mu;
-  static std::map<std::tuple<int, int, int, int, int, int, int>, WaveInfo> cache;
+  static std::map<std::tuple<int, int, int, int, int, int, int, int>, WaveInfo> cache;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return cuda_fail(e);
   const auto k = std::make_tuple(dev, static_cast<int>(key.path), key.D, key.nt,
                                  static_cast<int>(key.fp16_cache), static_cast<int>(key.fp8_cache),
-                                 static_cast<int>(key.p_lo));
+                                 static_cast<int>(key.p_lo), static_cast<int>(key.mx4_cache));
   {
     std::lock_guard<std::mutex> lock(mu);
     auto it = cache.find(k);
@@ -200,6 +209,20 @@ i8kv_status plan(const KernelKey& key, int64_t cap, int32_t units, int32_t mode,
   if (key.path == Path::kPaged && mode == I8KV_GEOM_WAVE && ovr == 0 && cap > 0 && *ns > 1)
     snap_to_round(cap, w.round, ns, chunk);
   return I8KV_OK;
+}
+
+// The automatic geometry of the MX4 decode, from the wave rule's count *ns: one
+// split where a row's span is short (the join would cost more than it spreads),
+// else balanced pieces with twice the count as partial slots.
+constexpr int64_t kMx4OneSplit = 256;
+void mx4_auto(int64_t span, int32_t units, int32_t* ns, int32_t* chunk) {
+  if (span <= kMx4OneSplit) {
+    *ns = 1;
+    *chunk = static_cast<int32_t>(std::max<int64_t>(16, cdiv(span, 16) * 16));
+    return;
+  }
+  *ns = std::min<int32_t>(I8KV_MAX_SPLITS, std::max<int32_t>(2, 2 * *ns));
+  *chunk = 0;
 }
 
 // Geometry given by the caller: num_splits in [1, 32], chunk a positive
@@ -360,7 +383,7 @@ i8kv_status decode_plan(int32_t path, int32_t cache_dtype, int64_t cap, int32_t 
   if (num_splits == nullptr || chunk == nullptr || workspace_bytes == nullptr) return I8KV_EINVAL;
   if (path != I8KV_PATH_DSA && path != I8KV_PATH_PAGED) return I8KV_EINVAL;
   if (cache_dtype != I8KV_CACHE_INT8 && cache_dtype != I8KV_CACHE_FP16 &&
-      cache_dtype != I8KV_CACHE_FP8)
+      cache_dtype != I8KV_CACHE_FP8 && cache_dtype != I8KV_CACHE_MX4)
     return I8KV_EINVAL;
   if (path == I8KV_PATH_DSA && cache_dtype != I8KV_CACHE_INT8) return I8KV_EUNSUPPORTED;
   if (rows < 0 || cap < 0) return I8KV_EINVAL;
@@ -376,6 +399,11 @@ i8kv_status decode_plan(int32_t path, int32_t cache_dtype, int64_t cap, int32_t 
     if (path != I8KV_PATH_PAGED) return I8KV_EUNSUPPORTED;
     if ((st = plan(key, cap, units, I8KV_GEOM_WAVE, 0, num_splits, chunk, wave_ctas)) != I8KV_OK)
       return st;
+    if (key.mx4_cache) {
+      mx4_auto(cap, units, num_splits, chunk);
+      *workspace_bytes = split_workspace_bytes(rows * Hkv, *num_splits, G, D);
+      return I8KV_OK;
+    }
     *num_splits = std::min<int32_t>(I8KV_MAX_SPLITS, std::max<int32_t>(2, 2 * *num_splits));
     *chunk = 0;
   } else if ((st = plan(key, cap, units, mode, override_value, num_splits, chunk, wave_ctas)) !=
@@ -622,6 +650,93 @@ i8kv_status paged_decode_ex(const uint16_t* q, const void* k_cache, const void* 
                       out, lse, slots_out, flags, stream);
 }
 
+i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* k_scale,
+                             const float* v_scale, int32_t scale_kind,
+                             const int32_t* block_table, const int32_t* seq_lens, int32_t B,
+                             int32_t Hq, int32_t Hkv, int32_t D, int32_t block_size,
+                             int32_t max_blocks, int64_t num_blocks, float softmax_scale,
+                             const float* head_sink, float softcap, int32_t window,
+                             int32_t num_splits, int32_t chunk, void* workspace,
+                             size_t workspace_bytes, uint16_t* out, float* lse, uint32_t* flags,
+                             void* stream) {
+  if (B < 0 || max_blocks < 0 || num_blocks < 0 || block_size < 1 || num_splits < 0)
+    return I8KV_EINVAL;
+  if (!(softcap >= 0.f) || !std::isfinite(softcap) || window < -1) return I8KV_EINVAL;
+  i8kv_status st = check_heads(Hq, Hkv, D);
+  if (st != I8KV_OK) return st;
+  if (block_size % 16 != 0) return I8KV_EUNSUPPORTED;
+  if ((st = check_sigma(softmax_scale)) != I8KV_OK) return st;
+  if ((st = check_scales(k_scale, v_scale, scale_kind)) != I8KV_OK) return st;
+  if (B > 0 && (q == nullptr || cache == nullptr || seq_lens == nullptr ||
+                (max_blocks > 0 && block_table == nullptr)))
+    return I8KV_EINVAL;
+  if (!aligned(q, 16) || !aligned(out, 16) || !aligned(cache, 16)) return I8KV_EALIGN;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse, 4) ||
+      !aligned(head_sink, 4) || !aligned(flags, 4))
+    return I8KV_EALIGN;
+  const int64_t cap = static_cast<int64_t>(max_blocks) * block_size;
+  // positions, and CTA numbers, are 32-bit on the device
+  if (cap > INT32_MAX - 16 || static_cast<int64_t>(B) * Hkv * I8KV_MAX_SPLITS > INT32_MAX)
+    return I8KV_EUNSUPPORTED;
+  const int32_t units = std::max(1, B * Hkv);
+  const KernelKey key = make_key(Path::kPaged, D, Hq / Hkv, I8KV_CACHE_MX4, false);
+  const int64_t span = I8KV_WINDOW_SPAN(cap, window);
+  if (num_splits == 0) {
+    st = plan(key, span, units, I8KV_GEOM_WAVE, 0, &num_splits, &chunk, nullptr);
+    if (st != I8KV_OK) return st;
+    mx4_auto(span, units, &num_splits, &chunk);
+  }
+  DecodeParams p{};
+  p.balanced = num_splits > 1 && chunk == 0;
+  if (p.balanced) {
+    if (num_splits > I8KV_MAX_SPLITS) return I8KV_EINVAL;
+  } else if ((st = check_geometry(span, num_splits, chunk, window >= 0 ? cap : 0)) != I8KV_OK) {
+    return st;
+  }
+  if ((st = set_workspace(p, workspace, workspace_bytes, B * Hkv, num_splits, Hq / Hkv, D)) !=
+      I8KV_OK)
+    return st;
+  if (out == nullptr && num_splits == 1 && B > 0) return I8KV_EINVAL;  // nowhere to write
+  if (B == 0) return I8KV_OK;
+  p.q = q;
+  p.k = cache;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.per_channel = scale_kind == I8KV_SCALE_PER_CHANNEL;
+  p.block_table = block_table;
+  p.seq_lens = seq_lens;
+  p.sink = head_sink;
+  p.out = out;
+  p.lse = lse;
+  p.flags = flags;
+  p.cache_rows = num_blocks;
+  p.rows = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.bs = block_size;
+  p.bs_log2 = log2_of(block_size);
+  p.max_blocks = max_blocks;
+  p.num_splits = num_splits;
+  p.chunk = chunk;
+  p.sigma = softmax_scale;
+  p.softcap = softcap;
+  p.window = window;
+  if (p.balanced) {
+    WaveInfo w{0, 0};
+    if ((st = wave_of(key, &w)) != I8KV_OK) return st;
+    p.bal_pieces = std::max(w.wave - units, w.wave / 2);
+  }
+  return run(key, p, static_cast<cudaStream_t>(stream));
+}
+
+size_t mx4_cache_bytes(int64_t num_blocks, int32_t block_size, int32_t Hkv, int32_t D) {
+  if (num_blocks < 1 || block_size < 16 || block_size % 16 != 0 || Hkv < 1 ||
+      !supported_head_dim(D))
+    return 0;
+  return static_cast<size_t>(num_blocks) * Hkv * (block_size / 16) * 18 * D;
+}
+
 i8kv_status split_combine(const float* acc, const float* m, const float* l, int32_t units,
                           int32_t num_splits, int32_t Hq, int32_t Hkv, int32_t D,
                           const float* head_sink, uint16_t* out, float* lse, void* stream) {
@@ -660,6 +775,127 @@ i8kv_status reshape_and_cache(const uint16_t* k_new, const uint16_t* v_new,
       k_new, v_new, slot_mapping, num_tokens, Hkv, D, k_cache, v_cache, num_slots, k_scale, v_scale,
       scale_kind == I8KV_SCALE_PER_CHANNEL, cache_dtype == I8KV_CACHE_FP8, flags,
       static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
+}
+
+// What rope_and_cache and gather_cache check alike: the cache and its scales.
+static i8kv_status check_cache(const void* k_cache, const void* v_cache, int32_t cache_dtype,
+                               int64_t num_slots, int32_t block_size, const float* k_scale,
+                               const float* v_scale, int32_t scale_kind, int32_t Hkv, int32_t D,
+                               bool used) {
+  if (Hkv < 1 || D < 1 || num_slots < 0) return I8KV_EINVAL;
+  if (cache_dtype < I8KV_CACHE_INT8 || cache_dtype > I8KV_CACHE_MX4) return I8KV_EINVAL;
+  const bool mx4 = cache_dtype == I8KV_CACHE_MX4;
+  if (D % 16 != 0 || (mx4 && !supported_head_dim(D))) return I8KV_EUNSUPPORTED;
+  if (mx4) {
+    if (block_size < 1 || v_cache != nullptr) return I8KV_EINVAL;
+    if (block_size % 16 != 0) return I8KV_EUNSUPPORTED;
+    if (num_slots % block_size != 0) return I8KV_EINVAL;
+  }
+  if (cache_dtype != I8KV_CACHE_FP16) {
+    const i8kv_status st = check_scales(k_scale, v_scale, scale_kind);
+    if (st != I8KV_OK) return st;
+  }
+  if (used && (k_cache == nullptr || (!mx4 && v_cache == nullptr))) return I8KV_EINVAL;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return I8KV_EALIGN;
+  return I8KV_OK;
+}
+
+i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                           int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
+                           const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                           int32_t rot_dim, int32_t rot_style, const int32_t* slot_mapping,
+                           int32_t num_tokens, int32_t Hq, int32_t Hkv, int32_t D,
+                           uint16_t* q_out, void* k_cache, void* v_cache, int32_t cache_dtype,
+                           int64_t num_slots, int32_t block_size, const float* k_scale,
+                           const float* v_scale, int32_t scale_kind, uint32_t* flags,
+                           void* stream) {
+  if (num_tokens < 0 || Hq < 0 || max_pos < 0) return I8KV_EINVAL;
+  if (rot_style != I8KV_ROPE_HALVES && rot_style != I8KV_ROPE_INTERLEAVED) return I8KV_EINVAL;
+  i8kv_status st = check_cache(k_cache, v_cache, cache_dtype, num_slots, block_size, k_scale,
+                               v_scale, scale_kind, Hkv, D, num_tokens > 0);
+  if (st != I8KV_OK) return st;
+  if (rot_dim < 0 || rot_dim > D) return I8KV_EINVAL;
+  if (rot_dim % 16 != 0 || (cache_dtype == I8KV_CACHE_MX4 && rot_style == I8KV_ROPE_HALVES &&
+                            rot_dim % 32 != 0))
+    return I8KV_EUNSUPPORTED;
+  if (num_tokens > 0) {
+    if (k_new == nullptr || v_new == nullptr || slot_mapping == nullptr) return I8KV_EINVAL;
+    if (Hq > 0 && (q == nullptr || q_out == nullptr)) return I8KV_EINVAL;
+    if (rot_dim > 0 && (positions == nullptr || cos_sin == nullptr)) return I8KV_EINVAL;
+  }
+  if (num_tokens > 1 && (q_stride < (Hq > 0 ? static_cast<int64_t>(Hq) * D : 0) ||
+                         k_stride < static_cast<int64_t>(Hkv) * D ||
+                         v_stride < static_cast<int64_t>(Hkv) * D))
+    return I8KV_EINVAL;
+  if (num_tokens > 1 && ((Hq > 0 && q_stride % 8 != 0) || k_stride % 8 != 0 || v_stride % 8 != 0))
+    return I8KV_EALIGN;
+  if (!aligned(q, 16) || !aligned(k_new, 16) || !aligned(v_new, 16) || !aligned(q_out, 16) ||
+      !aligned(cos_sin, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 4) ||
+      !aligned(flags, 4))
+    return I8KV_EALIGN;
+  if (num_tokens == 0) return I8KV_OK;
+  i8kv::AppendParams p{};
+  p.q = reinterpret_cast<const __half*>(q);
+  p.k = reinterpret_cast<const __half*>(k_new);
+  p.v = reinterpret_cast<const __half*>(v_new);
+  p.q_stride = q_stride;
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.positions = positions;
+  p.cos_sin = cos_sin;
+  p.max_pos = max_pos;
+  p.R = rot_dim;
+  p.interleaved = rot_style == I8KV_ROPE_INTERLEAVED;
+  p.slots = slot_mapping;
+  p.num_tokens = num_tokens;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.q_out = reinterpret_cast<__half*>(q_out);
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.num_slots = num_slots;
+  p.bs = block_size;
+  p.bs_shift = log2_of(block_size);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.per_channel = scale_kind == I8KV_SCALE_PER_CHANNEL;
+  p.flags = flags;
+  cudaError_t e = i8kv::launch_rope_and_cache(p, cache_dtype, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
+}
+
+i8kv_status gather_cache(const int32_t* slot_mapping, int32_t num_rows, int32_t Hkv, int32_t D,
+                         const void* k_cache, const void* v_cache, int32_t cache_dtype,
+                         int64_t num_slots, int32_t block_size, const float* k_scale,
+                         const float* v_scale, int32_t scale_kind, uint16_t* k_out,
+                         uint16_t* v_out, uint32_t* flags, void* stream) {
+  if (num_rows < 0) return I8KV_EINVAL;
+  i8kv_status st = check_cache(k_cache, v_cache, cache_dtype, num_slots, block_size, k_scale,
+                               v_scale, scale_kind, Hkv, D, num_rows > 0);
+  if (st != I8KV_OK) return st;
+  if (num_rows > 0 && slot_mapping == nullptr) return I8KV_EINVAL;
+  if (!aligned(slot_mapping, 4) || !aligned(k_out, 16) || !aligned(v_out, 16) ||
+      !aligned(flags, 4))
+    return I8KV_EALIGN;
+  if (num_rows == 0 || (k_out == nullptr && v_out == nullptr)) return I8KV_OK;
+  i8kv::AppendParams p{};
+  p.slots = slot_mapping;
+  p.num_tokens = num_rows;
+  p.Hkv = Hkv;
+  p.D = D;
+  p.k_cache = const_cast<void*>(k_cache);
+  p.v_cache = const_cast<void*>(v_cache);
+  p.num_slots = num_slots;
+  p.bs = block_size;
+  p.bs_shift = log2_of(block_size);
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.per_channel = scale_kind == I8KV_SCALE_PER_CHANNEL;
+  p.flags = flags;
+  cudaError_t e = i8kv::launch_gather_cache(p, cache_dtype, k_out, v_out,
+                                            static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
 }
 

@@ -2,6 +2,7 @@
 // translation units.  Not part of the public ABI.
 #pragma once
 
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
 
@@ -59,6 +60,7 @@ struct KernelKey {
   bool fp16_cache;
   bool fp8_cache;  // float8 e4m3fn codes (same tile as int8, other conversion)
   bool p_lo;       // probability tile as fp16 high + low parts
+  bool mx4_cache = false;  // 4-bit records (mx4_decode.cu; DecodeParams::k is the record cache)
 };
 
 // What the geometry needs to know of a decode kernel instantiation.
@@ -80,6 +82,35 @@ cudaError_t launch_paged_fp16(const KernelKey& key, const DecodeParams& p, cudaS
                               KernelInfo* info);
 cudaError_t launch_paged_fp8(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                              KernelInfo* info);
+
+cudaError_t launch_paged_mx4(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
+                             KernelInfo* info);
+
+// rope_and_cache and gather_cache (append.cu); the cache type picks the kernel.
+struct AppendParams {
+  const __half* q;           // [num_tokens, Hq, D], tokens q_stride elements apart
+  const __half* k;
+  const __half* v;
+  long long q_stride, k_stride, v_stride;
+  const int32_t* positions;
+  const float* cos_sin;      // [max_pos, R]: R / 2 cosines, then the sines
+  long long max_pos;
+  int32_t R, interleaved;
+  const int32_t* slots;
+  int32_t num_tokens, Hq, Hkv, D;
+  __half* q_out;
+  void* k_cache;             // MX4: the record cache
+  void* v_cache;
+  long long num_slots;
+  int32_t bs, bs_shift;      // MX4: block size, its log2 or -1
+  const float* k_scale;
+  const float* v_scale;
+  int32_t per_channel;
+  uint32_t* flags;
+};
+cudaError_t launch_rope_and_cache(const AppendParams& p, int cache_dtype, cudaStream_t stream);
+cudaError_t launch_gather_cache(const AppendParams& p, int cache_dtype, void* k_out, void* v_out,
+                                cudaStream_t stream);
 
 // The dense tensor-core prefill (prefill_tc.cu): whether it serves a shape
 // (and with how much shared memory / how many mask rows), and its launch.

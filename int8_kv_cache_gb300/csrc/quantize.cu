@@ -23,6 +23,7 @@
 #include <cuda_runtime.h>
 
 #include "../../include/int8kv.h"
+#include "codes.cuh"
 #include "device.cuh"
 #include "internal.h"
 
@@ -32,24 +33,6 @@ namespace {
 
 constexpr float kLoBound = 1.f - 0x1p-21f;
 constexpr float kHiBound = 1.f + 0x1p-21f;
-
-__device__ __forceinline__ float int8_code(float q) {
-  return fminf(fmaxf(rintf(q), -127.f), 127.f);
-}
-
-// Two floats -> two float8 e4m3fn bytes (lo in bits 0..7), nearest even,
-// saturating to the largest finite magnitude.
-__device__ __forceinline__ uint32_t e4m3x2_of(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-
-__device__ __forceinline__ float nan_to_zero(float q) { return q != q ? 0.f : q; }
-
-__device__ __forceinline__ uint32_t int8_byte(float c) {
-  return static_cast<uint32_t>(static_cast<int32_t>(c)) & 0xFFu;
-}
 
 // Codes of 8 fp16 values (channel j in byte j % 4 of word j / 4) from the
 // fp32 quotients x[j] / s[j * s_step] themselves: the exact path, taken for a

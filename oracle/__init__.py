@@ -24,3 +24,8 @@ from .quantize import e4m3fn_encode, quantize_rows, quantize_rows_fp8, reshape_a
 __all__ += ["quantize_rows", "reshape_and_cache", "e4m3fn_value", "e4m3fn_encode",
             "quantize_rows_fp8", "scores", "window_chunk_bounds",
             "window_span", "window_start", "prefill_block_ranges", "prefill_split_partials"]
+from .mx4 import (e2m1_encode, e2m1_value, mx4_append, mx4_encode, mx4_paged_attention,  # noqa: E402
+                  mx4_row, mx4_store, rotate)
+
+__all__ += ["e2m1_encode", "e2m1_value", "mx4_append", "mx4_encode", "mx4_paged_attention",
+            "mx4_row", "mx4_store", "rotate"]
