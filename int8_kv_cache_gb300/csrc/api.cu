@@ -725,7 +725,8 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
   if (p.balanced) {
     WaveInfo w{0, 0};
     if ((st = wave_of(key, &w)) != I8KV_OK) return st;
-    p.bal_pieces = std::max(w.wave - units, w.wave / 2);
+    // (at least one piece per row and KV head, and one to spare)
+    p.bal_pieces = std::max(w.wave, units + std::max(w.wave / 2, Hkv));
   }
   return run(key, p, static_cast<cudaStream_t>(stream));
 }

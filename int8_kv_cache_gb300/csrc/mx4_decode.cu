@@ -41,25 +41,40 @@ __device__ __forceinline__ int tiles_of(const DecodeParams& p, int r, int cap, i
 }
 
 // Balanced pieces.  With t_b the 16-token tiles of row b's live range, S the
-// partial slots of a row and W the pieces the batch should have (one occupancy
-// wave of CTAs), every row is cut into n_b = clamp(ceil(t_b / L), 1, S) pieces of
-// ceil(t_b / n_b) tiles, L = max(kMinTiles, ceil(Hkv sum t_b / max(W - U, W / 2))),
-// U = B * Hkv.  The pieces number at most max(W - U, W / 2) + U (and U * S), which
-// bounds the grid by the arguments alone; CTAs past the last piece return.  Item c:
-// rows in order, a row's pieces in order, the KV heads of a piece next to each
-// other.
+// partial slots of a row and P the pieces the grid has room for (one occupancy
+// wave of CTAs, or U + half a wave where the U = B * Hkv rows and heads are more
+// than that), every row is cut into n_b = clamp(ceil(t_b / L), 1, S) pieces of
+// ceil(t_b / n_b) tiles, with the smallest L >= kMinTiles for which the pieces
+// number at most P (found by bisection: sum t_b Hkv / P is a lower bound, sum t_b
+// Hkv / (P - U) always does).  The grid follows from the arguments alone; CTAs
+// past the last piece return.  Item c: rows in order, a row's pieces in order, the
+// KV heads of a piece next to each other.
 __device__ Mx4Item balanced_piece(const DecodeParams& p, int c) {
   const int lane = threadIdx.x & 31;
   const int B = p.rows, Hkv = p.Hkv, S = p.num_splits;
   const int cap = p.max_blocks * p.bs;
   int len, wlo;
-  long long tot = 0;
-  for (int r = lane; r < B; r += 32) tot += tiles_of(p, r, cap, len, wlo);
+  const int t0 = lane < B ? tiles_of(p, lane, cap, len, wlo) : 0;  // the only rows if B <= 32
+  long long tot = t0;
+  for (int r = 32 + lane; r < B; r += 32) tot += tiles_of(p, r, cap, len, wlo);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-  const long long target = p.bal_pieces;
-  const long long want = (tot * Hkv + target - 1) / target;
-  const int L = want < kMinTiles ? kMinTiles : (int)want;
+  const int room = p.bal_pieces / Hkv;  // pieces of one KV head (> B)
+  // bisection in units of kMinTiles (one tile per warp)
+  int lo = max(1, (int)((tot + (long long)room * kMinTiles - 1) / ((long long)room * kMinTiles)));
+  int up = max(lo, (int)((tot + (long long)(room - B) * kMinTiles - 1) / ((long long)(room - B) * kMinTiles)));
+  while (lo < up) {
+    const int mid = (lo + up) >> 1, len_mid = mid * kMinTiles;
+    int n = lane < B ? min(max((t0 + len_mid - 1) / len_mid, 1), S) : 0;
+    for (int r = 32 + lane; r < B; r += 32)
+      n += min(max((tiles_of(p, r, cap, len, wlo) + len_mid - 1) / len_mid, 1), S);
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n <= room)
+      up = mid;
+    else
+      lo = mid + 1;
+  }
+  const int L = lo * kMinTiles;
   long long base = 0;
   for (int r0 = 0; r0 < B; r0 += 32) {
     const int r = r0 + lane;
@@ -129,7 +144,7 @@ template <int D, int NT>
 struct Mx4Tile {
   static constexpr int kRec = 18 * D;                    // bytes of a 16-token record
   static constexpr int kSub = D <= 128 ? 2 : 1;          // records per stage
-  static constexpr int kStages = D <= 128 ? 3 : 4;       // ring depth per warp
+  static constexpr int kStages = 2 * (3 - kSub);         // ring depth per warp: 4 records
   static constexpr int kStageBytes = kSub * kRec;
   static constexpr int kRing = kStages * kStageBytes;    // a multiple of 128
   static constexpr int kRow = D + 4;                     // floats of a merged row (padded)
@@ -137,9 +152,12 @@ struct Mx4Tile {
   static constexpr int kBars = kWarps * kRing;           // mbarriers [warps][stages]
   static constexpr int kMasks = kBars + kWarps * kStages * 8;      // [warps][stages][sub]
   static constexpr int kScal = kMasks + kWarps * kStages * kSub * 4;  // [2][warps][16]
-  static constexpr int kSmem = kScal + 2 * kWarps * 16 * 4;
+  static constexpr int kQRow = D + 8;                    // halves of a staged query row (padded)
+  static constexpr int kQ = kScal + 2 * kWarps * 16 * 4;           // [8 NT][kQRow] fp16
+  static constexpr int kInv = kQ + 8 * NT * kQRow * 2;             // [16] score factors
+  static constexpr int kSmem = kInv + 16 * 4;
   // resident CTAs per SM the registers are cut for
-  static constexpr int kBlocks = D * NT >= 512 ? 2 : D * NT >= 256 ? 3 : 4;
+  static constexpr int kBlocks = D * NT >= 512 ? 2 : D * NT >= 256 ? 3 : D * NT >= 128 ? 4 : 5;
   static_assert(kMerge <= kRing, "the merge fits the ring");
 };
 
@@ -262,62 +280,65 @@ mx4_decode_kernel(const DecodeParams p) {
     }
   }
 
-  // ---- query fragments: head grp (+ 8), channels tig D/4 ... of it ----
-  // B operand of step i: channels 4i, 4i+1 and 4i+2, 4i+3 of the lane's part.
-  uint32_t qf[NT][KC][2];
-  float fac[NT][2];  // accumulator -> score in log2 units (natural units with a softcap)
-  {
-    const float unit = p.softcap > 0.f ? p.sigma : p.sigma * kLog2e;
+  // ---- the group's queries, scales folded in, staged in shared memory: 8 channels of a head
+  // per thread and pass ----
+  __half* sq = reinterpret_cast<__half*>(smem + T::kQ);
+  float* sinv = reinterpret_cast<float*>(smem + T::kInv);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const int h = grp + 8 * nt;
-      const uint4* src = reinterpret_cast<const uint4*>(
-          static_cast<const __half*>(p.q) + ((long long)it.row * p.Hq + it.g * G + h) * D +
-          tig * (D / 4));
+  for (int e = threadIdx.x; e < D * NT; e += kThreads) {
+    const int h = e / (D / 8), d = 8 * (e % (D / 8));
+    uint4 v = make_uint4(0u, 0u, 0u, 0u);
+    if (h < G)
+      v = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) +
+                                          ((long long)it.row * p.Hq + it.g * G + h) * D + d);
+    float inv = 1.f;
+    if (p.per_channel) {
+      // one power of two per head taken out, so that the largest element is in
+      // [2^8, 2^9): nothing overflows fp16, and what goes below its normal range is
+      // less than 2^-22 of the largest
+      const float4 k0 = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d);
+      const float4 k1 = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d + 4);
+      const __half2* q2 = reinterpret_cast<const __half2*>(&v);
+      const float2 a0 = __half22float2(q2[0]), a1 = __half22float2(q2[1]);
+      const float2 a2 = __half22float2(q2[2]), a3 = __half22float2(q2[3]);
+      const float x[8] = {a0.x * k0.x, a0.y * k0.y, a1.x * k0.z, a1.y * k0.w,
+                          a2.x * k1.x, a2.y * k1.y, a3.x * k1.z, a3.y * k1.w};
+      float amax = 0.f;
 #pragma unroll
-      for (int i = 0; i < KC / 2; ++i) {
-        const uint4 v = h < G ? src[i] : make_uint4(0u, 0u, 0u, 0u);
-        qf[nt][2 * i][0] = v.x;
-        qf[nt][2 * i][1] = v.y;
-        qf[nt][2 * i + 1][0] = v.z;
-        qf[nt][2 * i + 1][1] = v.w;
-      }
-      float inv = 1.f;
-      if (p.per_channel) {
-        // fold the scales in, one power of two per head taken out so that the
-        // largest element is in [2^8, 2^9): nothing overflows fp16, and what goes
-        // below its normal range is less than 2^-22 of the largest
-        const float4* ks = reinterpret_cast<const float4*>(p.k_scale + it.g * D + tig * (D / 4));
-        float amax = 0.f;
+      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
-        for (int i = 0; i < KC; ++i) {
-          const float4 k = ks[i];
-          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][i][0]));
-          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][i][1]));
-          amax = fmaxf(fmaxf(amax, fmaxf(fabsf(a.x * k.x), fabsf(a.y * k.y))),
-                       fmaxf(fabsf(b.x * k.z), fabsf(b.y * k.w)));
-        }
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-        const int e = __float_as_int(amax) >> 23;  // biased exponent (amax >= 0)
-        const bool scaled = e >= 9 && e < 255;
-        const float up = scaled ? __int_as_float((262 - e) << 23) : 1.f;
-        inv = scaled ? __int_as_float((e - 8) << 23) : 1.f;
-#pragma unroll
-        for (int i = 0; i < KC; ++i) {
-          const float4 k = ks[i];
-          const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][i][0]));
-          const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&qf[nt][i][1]));
-          qf[nt][i][0] = pack_h2(a.x * k.x * up, a.y * k.y * up);
-          qf[nt][i][1] = pack_h2(b.x * k.z * up, b.y * k.w * up);
-        }
-      } else {
-        inv = p.k_scale[0];
-      }
-      // this lane's score columns are heads 2 tig, 2 tig + 1
-      fac[nt][0] = __shfl_sync(0xffffffffu, inv, 8 * tig) * unit;
-      fac[nt][1] = __shfl_sync(0xffffffffu, inv, 8 * tig + 4) * unit;
+      for (int o = 1; o < D / 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      const int ex = __float_as_int(amax) >> 23;  // biased exponent (amax >= 0)
+      const bool scaled = ex >= 9 && ex < 255;
+      const float up = scaled ? __int_as_float((262 - ex) << 23) : 1.f;
+      inv = scaled ? __int_as_float((ex - 8) << 23) : 1.f;
+      v = make_uint4(pack_h2(x[0] * up, x[1] * up), pack_h2(x[2] * up, x[3] * up),
+                     pack_h2(x[4] * up, x[5] * up), pack_h2(x[6] * up, x[7] * up));
+    } else {
+      inv = p.k_scale[0];
     }
+    *reinterpret_cast<uint4*>(sq + h * T::kQRow + d) = v;
+    // accumulator -> score in log2 units (natural units with a softcap)
+    if (d == 0) sinv[h] = inv * (p.softcap > 0.f ? p.sigma : p.sigma * kLog2e);
+  }
+  __syncthreads();
+  // B operand of step i: channels 4i, 4i+1 and 4i+2, 4i+3 of the lane's part, which starts
+  // at channel tig D/4 of head grp (+ 8); the lane's score columns are heads 2 tig, 2 tig + 1
+  uint32_t qf[NT][KC][2];
+  float fac[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt) {
+    const uint4* src = reinterpret_cast<const uint4*>(sq + (grp + 8 * nt) * T::kQRow + tig * (D / 4));
+#pragma unroll
+    for (int i = 0; i < KC / 2; ++i) {
+      const uint4 v = src[i];
+      qf[nt][2 * i][0] = v.x;
+      qf[nt][2 * i][1] = v.y;
+      qf[nt][2 * i + 1][0] = v.z;
+      qf[nt][2 * i + 1][1] = v.w;
+    }
+    fac[nt][0] = sinv[8 * nt + 2 * tig];
+    fac[nt][1] = sinv[8 * nt + 2 * tig + 1];
   }
 
   float acc[KC][NT][4];
@@ -363,40 +384,37 @@ mx4_decode_kernel(const DecodeParams p) {
       uint32_t wa[KW], wb[KW];
       lds<KW>(r + k_off, wa);
       lds<KW>(r + k_off + 8 * (D / 2), wb);
-      // block scales of the lane's channels (D / 64 of a token), as fp16 pairs
-      uint32_t xa, xb;
+      // block scales of the lane's channels (D / 64 of a token), each as an fp16 pair
+      constexpr int KB = D / 64;
+      uint32_t fa[KB < 2 ? 2 : KB], fb[KB < 2 ? 2 : KB];
       if constexpr (D == 64) {
-        xa = lds_u8(r + ks_off);
-        xb = lds_u8(r + ks_off + 8 * (D / 16));
+        e4m3x4_to_h2x2(lds_u8(r + ks_off) * 0x0101u, fa[0], fa[1]);
+        e4m3x4_to_h2x2(lds_u8(r + ks_off + 8 * (D / 16)) * 0x0101u, fb[0], fb[1]);
       } else if constexpr (D == 128) {
-        xa = lds_u16(r + ks_off);
-        xb = lds_u16(r + ks_off + 8 * (D / 16));
+        e4m3x4_to_h2x2(prmt(lds_u16(r + ks_off), 0u, 0x1100u), fa[0], fa[1]);
+        e4m3x4_to_h2x2(prmt(lds_u16(r + ks_off + 8 * (D / 16)), 0u, 0x1100u), fb[0], fb[1]);
       } else {
-        uint32_t t[1];
-        lds<1>(r + ks_off, t);
-        xa = t[0];
-        lds<1>(r + ks_off + 8 * (D / 16), t);
-        xb = t[0];
+        uint32_t x[1];
+        lds<1>(r + ks_off, x);
+        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x1100u), fa[0], fa[1]);
+        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x3322u), fa[2], fa[3]);
+        lds<1>(r + ks_off + 8 * (D / 16), x);
+        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x1100u), fb[0], fb[1]);
+        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x3322u), fb[2], fb[3]);
       }
-      uint32_t sa[2], sb[2];
-      e4m3x4_to_h2x2(xa, sa[0], sa[1]);
-      e4m3x4_to_h2x2(xb, sb[0], sb[1]);
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) sc[s][nt][e] = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {  // 8 channels of a lane: two steps
-        const int blk = w / 2;
-        const uint32_t fa = prmt(sa[blk / 2], 0u, blk & 1 ? 0x3232u : 0x1010u);
-        const uint32_t fb = prmt(sb[blk / 2], 0u, blk & 1 ? 0x3232u : 0x1010u);
         uint32_t a[4], b[4];
         e2m1x8_to_h2x4(wa[w], a[0], a[1], a[2], a[3]);
         e2m1x8_to_h2x4(wb[w], b[0], b[1], b[2], b[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a[i] = hmul2(a[i], fa);
-          b[i] = hmul2(b[i], fb);
+          a[i] = hmul2(a[i], fa[w / 2]);
+          b[i] = hmul2(b[i], fb[w / 2]);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -411,25 +429,57 @@ mx4_decode_kernel(const DecodeParams p) {
     int mask[T::kSub];
 #pragma unroll
     for (int s = 0; s < T::kSub; ++s) mask[s] = masks[st * T::kSub + s];
-    bool high = false;
+    // z: scores less the head's base, in log2 units
+    float z[T::kSub][NT][4];
+    auto scores_less_base = [&]() {
+      if (p.softcap > 0.f) {
+#pragma unroll
+        for (int s = 0; s < T::kSub; ++s)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              z[s][nt][e] = fmaf(soft_cap(sc[s][nt][e] * fac[nt][e & 1], p.softcap, cap_k), kLog2e,
+                                 -base[nt][e & 1]);
+      } else {
+#pragma unroll
+        for (int s = 0; s < T::kSub; ++s)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              z[s][nt][e] = fmaf(sc[s][nt][e], fac[nt][e & 1], -base[nt][e & 1]);
+      }
+#pragma unroll
+      for (int s = 0; s < T::kSub; ++s) {
+        if (mask[s] != 0xFFFF) {  // uniform
+          const bool upper = (mask[s] >> tok) & 1, lower = (mask[s] >> (tok + 8)) & 1;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (!upper) z[s][nt][0] = z[s][nt][1] = neg_inf();
+            if (!lower) z[s][nt][2] = z[s][nt][3] = neg_inf();
+          }
+        }
+      }
+    };
+    scores_less_base();
+    float top = neg_inf();
 #pragma unroll
     for (int s = 0; s < T::kSub; ++s)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x = sc[s][nt][e] * fac[nt][e & 1];
-          if (p.softcap > 0.f) x = soft_cap(x, p.softcap, cap_k) * kLog2e;
-          sc[s][nt][e] = x;
-        }
-        if (mask[s] != 0xFFFF) {  // uniform
-          if (!((mask[s] >> tok) & 1)) sc[s][nt][0] = sc[s][nt][1] = neg_inf();
-          if (!((mask[s] >> (tok + 8)) & 1)) sc[s][nt][2] = sc[s][nt][3] = neg_inf();
-        }
+        for (int e = 0; e < 4; ++e) top = fmaxf(top, z[s][nt][e]);
+    if (__any_sync(0xffffffffu, top > kHead)) {
+      float old[NT][2];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) high |= sc[s][nt][e] - base[nt][e & 1] > kHead;
-      }
-    if (__any_sync(0xffffffffu, high)) {
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          old[nt][j] = base[nt][j];
+          if (base[nt][j] == kUnset) base[nt][j] = 0.f;  // (kUnset would swallow the score)
+        }
+      scores_less_base();
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float alpha[2];
@@ -437,15 +487,18 @@ mx4_decode_kernel(const DecodeParams p) {
         for (int j = 0; j < 2; ++j) {
           float mx = neg_inf();
 #pragma unroll
-          for (int s = 0; s < T::kSub; ++s) mx = fmaxf(mx, fmaxf(sc[s][nt][j], sc[s][nt][2 + j]));
+          for (int s = 0; s < T::kSub; ++s) mx = fmaxf(mx, fmaxf(z[s][nt][j], z[s][nt][2 + j]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const float b = fmaxf(base[nt][j], mx - kRoom);
-          alpha[j] = fast_exp2(base[nt][j] - b);
-          base[nt][j] = b;
-          lrun[nt][j] *= alpha[j];
+          const bool unset = old[nt][j] == kUnset;
+          // up by what the largest is above the room left, down too on the first score
+          const float up = unset ? mx - kRoom : fmaxf(mx - kRoom, 0.f);
+          alpha[j] = unset ? 0.f : fast_exp2(-up);
+          base[nt][j] = unset && mx == neg_inf() ? kUnset : base[nt][j] + up;
         }
+        lrun[nt][0] *= alpha[0];
+        lrun[nt][1] *= alpha[1];
 #pragma unroll
         for (int t = 0; t < KC; ++t) {
           acc[t][nt][0] *= alpha[0];
@@ -454,6 +507,7 @@ mx4_decode_kernel(const DecodeParams p) {
           acc[t][nt][3] *= alpha[1];
         }
       }
+      scores_less_base();
     }
     uint32_t ph[T::kSub][NT][2];
 #pragma unroll
@@ -463,7 +517,7 @@ mx4_decode_kernel(const DecodeParams p) {
         float pr[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          pr[e] = fast_exp2(sc[s][nt][e] - base[nt][e & 1]);
+          pr[e] = fast_exp2(z[s][nt][e]);
           lrun[nt][e & 1] += pr[e];
         }
         ph[s][nt][0] = movm_t(pack_h2(pr[0], pr[1]));
@@ -484,13 +538,21 @@ mx4_decode_kernel(const DecodeParams p) {
         } else {
           x[i] = lds_u8(r + vs_off + i * 4 * (D / 16));
         }
-        // a token that is not attended: nothing of its bytes counts
-        if (mask[s] != 0xFFFF && !((mask[s] >> (tig + 4 * i)) & 1)) x[i] = 0u;
       }
-      // scales of token pairs (0, 1) and (2, 3): block 0 (and 1) of the lane's channels
+      if (mask[s] != 0xFFFF) {  // a token that is not attended: nothing of its bytes counts
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (!((mask[s] >> (tig + 4 * i)) & 1)) x[i] = 0u;
+      }
+      // scales of token pairs (0, 1) and (2, 3) for each block of the lane's channels
       uint32_t s01[2], s23[2];
-      e4m3x4_to_h2x2(prmt(x[0], x[1], 0x5140u), s01[0], s01[1]);
-      e4m3x4_to_h2x2(prmt(x[2], x[3], 0x5140u), s23[0], s23[1]);
+      if constexpr (D == 256) {
+        e4m3x4_to_h2x2(prmt(x[0], x[1], 0x5140u), s01[0], s01[1]);
+        e4m3x4_to_h2x2(prmt(x[2], x[3], 0x5140u), s23[0], s23[1]);
+      } else {
+        const uint32_t y = prmt(x[0] | (x[1] << 8), x[2] | (x[3] << 8), 0x5410u);
+        e4m3x4_to_h2x2(y, s01[0], s23[0]);
+      }
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
         const int blk = w / 2;
@@ -546,6 +608,8 @@ mx4_decode_kernel(const DecodeParams p) {
               make_float4(acc[t][nt][j], acc[t][nt][2 + j], acc[t + 1][nt][j], acc[t + 1][nt][2 + j]);
       }
     }
+  // the join may be launched now: its CTAs wait for this grid's writes
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __syncthreads();
   const bool direct = p.num_splits == 1;
   const long long head0 = (long long)it.row * p.Hq + it.g * G;
@@ -622,7 +686,7 @@ cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
   }
   const long long units = (long long)p.rows * p.Hkv;
   long long ctas = units * p.num_splits;
-  if (p.balanced && ctas > p.bal_pieces + units) ctas = p.bal_pieces + units;
+  if (p.balanced && ctas > p.bal_pieces) ctas = p.bal_pieces;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(kThreads);
