@@ -12,12 +12,15 @@
 //   MX4           y = x fl(1/scale); block scale s = e4m3(min(max|y| fl(1/6), 448)),
 //                 code = e2m1(y fl(1/s))
 //
-// One thread takes an item: 16 channels of one head of one token, as two pieces
-// of 8 (two 16-byte loads).  In the turned part with the halves rotated
-// together the pieces are channels 8j .. 8j+7 and their partners rot_dim / 2
-// further on; everywhere else they are adjacent.  An MX4 block of 16 channels is
-// then either the thread's own two pieces or (halves) one piece of each of two
-// adjacent lanes, which exchange their maxima with one shuffle.
+// Bound: HBM, rows in and rows out once each.  A thread keeps one item -- 16 channels
+// of a head as two pieces of 8, so that every access is 16 bytes and neighbouring
+// lanes touch neighbouring pieces -- and walks the tokens, so that the reciprocals of
+// its 16 scales are formed once and no index is divided in the loop.  In a turned
+// range of R channels with the halves rotated together the pieces are channels 8j ..
+// 8j + 7 and their partners R / 2 further on; every other range is cut the same way.
+// Queries take several heads of a token per thread (they share the sines and
+// cosines: 64 of the 192 bytes that a head would load).  An MX4 block of 16 channels is
+// one piece of each of two neighbouring lanes, which exchange their maxima.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -31,6 +34,8 @@ namespace i8kv {
 namespace {
 
 constexpr int kAppendThreads = 256;
+constexpr float kLoBound = 1.f - 0x1p-21f;
+constexpr float kHiBound = 1.f + 0x1p-21f;
 
 __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   const __half2* h = reinterpret_cast<const __half2*>(&r);
@@ -53,10 +58,12 @@ __device__ __forceinline__ void turn(float& a, float& b, float c, float s) {
   a = ta;
 }
 
-// Codes of 8 channels for an int8 or e4m3fn cache: s the scales of the channels.
+// Codes of 8 channels for an int8 or e4m3fn cache from the fp32 quotients
+// themselves: s the scales of the channels.
 template <bool FP8>
-__device__ __forceinline__ uint2 codes8(const float (&x)[8], const float* __restrict__ s,
-                                        int s_step) {
+__device__ __noinline__ uint2 codes8_exact(float4 lo, float4 hi, const float* __restrict__ s,
+                                           int s_step) {
+  const float x[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
   uint32_t w[2] = {0u, 0u};
 #pragma unroll
   for (int j = 0; j < 8; j += 2) {
@@ -69,200 +76,383 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], const float* __rest
   return make_uint2(w[0], w[1]);
 }
 
-template <int CACHE>
-__global__ void __launch_bounds__(kAppendThreads)
-rope_and_cache_kernel(const AppendParams p) {
-  grid_dependency_wait();
-  const int ipr = p.D >> 4;                  // items per row
-  const int ipt = (p.Hq + 2 * p.Hkv) * ipr;  // items per token
-  const long long flat = blockIdx.x * (long long)kAppendThreads + threadIdx.x;
-  const long long n = flat / ipt;
-  if (n >= p.num_tokens) return;
-  const int item = (int)(flat - n * ipt);
-  const int head = item / ipr, j = item - (item / ipr) * ipr;
-  const bool is_q = head < p.Hq, is_v = head >= p.Hq + p.Hkv;
-  const int h = is_q ? head : (is_v ? head - p.Hq - p.Hkv : head - p.Hq);
-  const int slot = p.slots[n];
+// The same codes from the products with the rounded reciprocals r, which are within
+// |q| 2^-22 of the rounded quotients: where a product lies within |q| 2^-21 of a
+// rounding boundary (about one piece in a thousand) the quotients decide.
+template <bool FP8>
+__device__ __forceinline__ uint2 codes8(const float (&x)[8], const float (&r)[8],
+                                        const float* __restrict__ s, int s_step) {
+  uint32_t w[2] = {0u, 0u};
+  bool near = false;
+#pragma unroll
+  for (int j = 0; j < 8; j += 2) {
+    const float q0 = nan_to_zero(x[j] * r[j]), q1 = nan_to_zero(x[j + 1] * r[j + 1]);
+    uint32_t b;
+    if constexpr (FP8) {
+      b = e4m3x2_of(q0 * kLoBound, q1 * kLoBound);
+      near |= b != e4m3x2_of(q0 * kHiBound, q1 * kHiBound);
+    } else {
+      const float n0 = rintf(q0), n1 = rintf(q1);
+      near |= fabsf(fabsf(q0 - n0) - 0.5f) <= fabsf(q0) * 0x1p-21f;
+      near |= fabsf(fabsf(q1 - n1) - 0.5f) <= fabsf(q1) * 0x1p-21f;
+      b = int8_byte(fminf(fmaxf(n0, -127.f), 127.f)) |
+          (int8_byte(fminf(fmaxf(n1, -127.f), 127.f)) << 8);
+    }
+    w[j / 4] |= b << (8 * (j % 4));
+  }
+  if (near)
+    return codes8_exact<FP8>(make_float4(x[0], x[1], x[2], x[3]),
+                             make_float4(x[4], x[5], x[6], x[7]), s, s_step);
+  return make_uint2(w[0], w[1]);
+}
+
+// The two pieces of item j of a row: channels c0 .. c0 + 7 and c1 .. c1 + 7, and, where
+// they are turned, the angles (pairs) of each: index ta of the first and tb of the second.
+struct Pieces {
+  int c0, c1;
+  bool turned;
+  bool block;  // the two pieces are one MX4 block (else a piece is half of one)
+};
+__device__ __forceinline__ Pieces pieces_of(const AppendParams& p, int j, bool rotates) {
+  Pieces x;
+  const int R = rotates ? p.R : 0;
+  x.turned = j < (R >> 4);
+  const int first = x.turned ? 0 : R, len = x.turned ? R : p.D - R;
+  const int i = x.turned ? j : j - (R >> 4);
+  // (an interleaved range that is no multiple of 32 keeps its pieces next to each other,
+  // so that an MX4 block never straddles two items' lanes unevenly)
+  x.block = (p.R & 31) != 0 && p.interleaved;
+  x.c0 = first + (x.block ? 16 : 8) * i;
+  x.c1 = x.block ? x.c0 + 8 : x.c0 + (len >> 1);
+  return x;
+}
+
+// Sines and cosines of an item at one position.
+struct Angles {
+  float4 c[2], s[2];
+};
+__device__ __forceinline__ Angles angles_of(const AppendParams& p, const Pieces& x, int pos) {
+  const float* row = p.cos_sin + (long long)pos * p.R;
   const int half = p.R >> 1;
-  const bool turned = !is_v && j < (p.R >> 4);
-  const bool split = turned && !p.interleaved;  // the pieces are half apart
-  const int c0 = split ? 8 * j : 16 * j;
-  const int c1 = split ? c0 + half : c0 + 8;
-
-  const __half* row = is_q ? p.q + n * p.q_stride : is_v ? p.v + n * p.v_stride : p.k + n * p.k_stride;
-  row += (long long)h * p.D;
-  float a[8], b[8];
-  unpack8(*reinterpret_cast<const uint4*>(row + c0), a);
-  unpack8(*reinterpret_cast<const uint4*>(row + c1), b);
-
-  if (p.R > 0) {
-    const int pos = p.positions[n];
-    if (pos < 0 || (long long)pos >= p.max_pos) {
-      if (item == 0 && slot >= 0) flag_or(p.flags, I8KV_FLAG_BAD_POSITION);
-      return;
-    }
-    if (turned) {
-      const float4* cs = reinterpret_cast<const float4*>(p.cos_sin + (long long)pos * p.R + 8 * j);
-      const float4* sn = reinterpret_cast<const float4*>(p.cos_sin + (long long)pos * p.R + half + 8 * j);
-      const float4 q0 = cs[0], q1 = cs[1], r0 = sn[0], r1 = sn[1];
-      const float c[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-      const float s[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
-      if (split) {
+  // halves: pairs c0 .. c0 + 7; interleaved: pairs c0 / 2 .. + 3 and c1 / 2 .. + 3
+  const int t0 = p.interleaved ? x.c0 >> 1 : x.c0, t1 = p.interleaved ? x.c1 >> 1 : x.c0 + 4;
+  Angles a;
+  a.c[0] = __ldg(reinterpret_cast<const float4*>(row + t0));
+  a.c[1] = __ldg(reinterpret_cast<const float4*>(row + t1));
+  a.s[0] = __ldg(reinterpret_cast<const float4*>(row + half + t0));
+  a.s[1] = __ldg(reinterpret_cast<const float4*>(row + half + t1));
+  return a;
+}
+__device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], const Angles& g,
+                                          bool interleaved) {
+  const float c[8] = {g.c[0].x, g.c[0].y, g.c[0].z, g.c[0].w, g.c[1].x, g.c[1].y, g.c[1].z, g.c[1].w};
+  const float s[8] = {g.s[0].x, g.s[0].y, g.s[0].z, g.s[0].w, g.s[1].x, g.s[1].y, g.s[1].z, g.s[1].w};
+  if (interleaved) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) turn(a[i], b[i], c[i], s[i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          turn(a[2 * i], a[2 * i + 1], c[i], s[i]);
-          turn(b[2 * i], b[2 * i + 1], c[4 + i], s[4 + i]);
-        }
-      }
+    for (int i = 0; i < 4; ++i) {
+      turn(a[2 * i], a[2 * i + 1], c[i], s[i]);
+      turn(b[2 * i], b[2 * i + 1], c[4 + i], s[4 + i]);
     }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(a[i], b[i], c[i], s[i]);
   }
-  if (is_q) {
-    __half* o = p.q_out + (n * p.Hq + h) * p.D;
-    *reinterpret_cast<uint4*>(o + c0) = pack8(a);
-    *reinterpret_cast<uint4*>(o + c1) = pack8(b);
-    return;
-  }
-  if (slot < 0) return;
-  if ((long long)slot >= p.num_slots) {
-    if (item == p.Hq * ipr) flag_or(p.flags, I8KV_FLAG_BAD_SLOT);
-    return;
-  }
-  const float* sc = is_v ? p.v_scale : p.k_scale;
-  const int step = p.per_channel ? 1 : 0;
-  const int ch = p.per_channel ? h * p.D : 0;
+}
+
+// One row's item into the cache.  r0, r1: reciprocals of the scales of the two pieces.
+template <int CACHE>
+__device__ __forceinline__ void store_item(const AppendParams& p, const Pieces& x, int h, bool is_v,
+                                           int slot, float (&a)[8], float (&b)[8],
+                                           const float (&r0)[8], const float (&r1)[8],
+                                           const float* sc, int step) {
   if constexpr (CACHE == I8KV_CACHE_FP16) {
     __half* o = static_cast<__half*>(is_v ? p.v_cache : p.k_cache) +
                 ((long long)slot * p.Hkv + h) * p.D;
-    *reinterpret_cast<uint4*>(o + c0) = pack8(a);
-    *reinterpret_cast<uint4*>(o + c1) = pack8(b);
+    *reinterpret_cast<uint4*>(o + x.c0) = pack8(a);
+    *reinterpret_cast<uint4*>(o + x.c1) = pack8(b);
   } else if constexpr (CACHE == I8KV_CACHE_MX4) {
     float ma = 0.f, mb = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      a[i] = nan_to_zero(__fmul_rn(a[i], __frcp_rn(sc[ch + (c0 + i) * step])));
-      b[i] = nan_to_zero(__fmul_rn(b[i], __frcp_rn(sc[ch + (c1 + i) * step])));
+      a[i] = nan_to_zero(__fmul_rn(a[i], r0[i]));
+      b[i] = nan_to_zero(__fmul_rn(b[i], r1[i]));
       ma = fmaxf(ma, fabsf(a[i]));
       mb = fmaxf(mb, fabsf(b[i]));
     }
-    if (split) {
-      // adjacent lanes hold the two halves of a block (same token, same row)
-      const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31;
+    if (x.block) {
+      ma = mb = fmaxf(ma, mb);
+    } else {
+      // neighbouring lanes hold the two halves of each block (same token, same row)
       const unsigned pair = 3u << (lane & ~1);
       ma = fmaxf(ma, __shfl_xor_sync(pair, ma, 1));
       mb = fmaxf(mb, __shfl_xor_sync(pair, mb, 1));
-    } else {
-      ma = mb = fmaxf(ma, mb);
     }
     const uint32_t sb = e4m3x2_of(__fmul_rn(ma, 1.f / 6.f), __fmul_rn(mb, 1.f / 6.f));
-    const float sa = e4m3_value(sb & 0xFFu), sbv = e4m3_value(sb >> 8);
-    const float ra = sa > 0.f ? __frcp_rn(sa) : 0.f, rb = sbv > 0.f ? __frcp_rn(sbv) : 0.f;
+    uint32_t s2, unused;
+    e4m3x4_to_h2x2(sb, s2, unused);
+    const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&s2));
+    const float ra = s.x > 0.f ? __frcp_rn(s.x) : 0.f, rb = s.y > 0.f ? __frcp_rn(s.y) : 0.f;
+    const bool za = s.x > 0.f, zb = s.y > 0.f;  // (a zero scale stores zeros, of an infinity too)
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      a[i] = sa > 0.f ? __fmul_rn(a[i], ra) : 0.f;
-      b[i] = sbv > 0.f ? __fmul_rn(b[i], rb) : 0.f;
+      a[i] = za ? __fmul_rn(a[i], ra) : 0.f;
+      b[i] = zb ? __fmul_rn(b[i], rb) : 0.f;
     }
     int tok;
     uint8_t* rec = static_cast<uint8_t*>(p.k_cache) +
                    mx4_record(slot, h, p.Hkv, p.D, p.bs, p.bs_shift, tok) + (is_v ? 9 * p.D : 0);
     uint8_t* code = rec + tok * (p.D >> 1);
-    *reinterpret_cast<uint32_t*>(code + (c0 >> 1)) = e2m1x8_of(a);
-    *reinterpret_cast<uint32_t*>(code + (c1 >> 1)) = e2m1x8_of(b);
-    uint8_t* scale = rec + 8 * p.D + tok * ipr;
-    // one writer per block: the lane that holds the block's first 8 channels
-    if ((c0 & 15) == 0) scale[c0 >> 4] = (uint8_t)sb;
-    if (split && (c1 & 15) == 0) scale[c1 >> 4] = (uint8_t)(sb >> 8);
+    *reinterpret_cast<uint32_t*>(code + (x.c0 >> 1)) = e2m1x8_of(a);
+    *reinterpret_cast<uint32_t*>(code + (x.c1 >> 1)) = e2m1x8_of(b);
+    uint8_t* scale = rec + 8 * p.D + tok * (p.D >> 4);
+    // one writer per block: the lane that holds its first 8 channels
+    if ((x.c0 & 15) == 0) {
+      scale[x.c0 >> 4] = (uint8_t)sb;
+      if (!x.block) scale[x.c1 >> 4] = (uint8_t)(sb >> 8);
+    }
   } else {
     constexpr bool FP8 = CACHE == I8KV_CACHE_FP8;
     uint8_t* o = static_cast<uint8_t*>(is_v ? p.v_cache : p.k_cache) +
                  ((long long)slot * p.Hkv + h) * p.D;
-    *reinterpret_cast<uint2*>(o + c0) = codes8<FP8>(a, sc + ch + c0 * step, step);
-    *reinterpret_cast<uint2*>(o + c1) = codes8<FP8>(b, sc + ch + c1 * step, step);
+    *reinterpret_cast<uint2*>(o + x.c0) = codes8<FP8>(a, r0, sc + x.c0 * step, step);
+    *reinterpret_cast<uint2*>(o + x.c1) = codes8<FP8>(b, r1, sc + x.c1 * step, step);
   }
 }
 
-// One thread: 16 channels of one row, K or V.
-template <int CACHE>
-__global__ void __launch_bounds__(kAppendThreads)
-gather_cache_kernel(const AppendParams p, __half* __restrict__ k_out, __half* __restrict__ v_out) {
+// HQ: query heads per thread (1: a few tokens, where threads are short; else 4).
+template <int CACHE, int HQ>
+__global__ void __launch_bounds__(kAppendThreads, 2)
+rope_and_cache_kernel(const AppendParams p, long long lanes) {
   grid_dependency_wait();
-  const int ipr = p.D >> 4;
-  const int ipt = 2 * p.Hkv * ipr;
+  const int ipr = p.D >> 4;                           // items per row
+  const int groups = (p.Hq + HQ - 1) / HQ;
+  const int ipt = (groups + 2 * p.Hkv) * ipr;         // items per token
   const long long flat = blockIdx.x * (long long)kAppendThreads + threadIdx.x;
-  const long long n = flat / ipt;
-  if (n >= p.num_tokens) return;
-  const int item = (int)(flat - n * ipt);
-  const int head = item / ipr, j = item - (item / ipr) * ipr;
-  const bool is_v = head >= p.Hkv;
-  const int h = is_v ? head - p.Hkv : head;
-  __half* out = is_v ? v_out : k_out;
-  const int slot = p.slots[n];
-  if (item == 0 && (long long)slot >= p.num_slots) flag_or(p.flags, I8KV_FLAG_BAD_SLOT);
-  if (out == nullptr) return;
-  uint4* o = reinterpret_cast<uint4*>(out + (n * p.Hkv + h) * p.D + 16 * j);
-  if (slot < 0 || (long long)slot >= p.num_slots) {
-    o[0] = o[1] = make_uint4(0u, 0u, 0u, 0u);
+  const long long n0 = flat / ipt;
+  if (n0 >= lanes) return;
+  const int item = (int)(flat - n0 * ipt);
+  const int unit = item / ipr, j = item - (item / ipr) * ipr;
+  const bool il = p.interleaved != 0;
+
+  if (unit < groups) {  // queries: HQ heads of a token
+    const Pieces x = pieces_of(p, j, true);
+    const int h0 = unit * HQ;
+    for (long long n = n0; n < p.num_tokens; n += lanes) {
+      const __half* row = p.q + n * p.q_stride + (long long)h0 * p.D;
+      uint4 ra[HQ], rb[HQ];
+#pragma unroll
+      for (int i = 0; i < HQ; ++i)
+        if (h0 + i < p.Hq) {
+          ra[i] = *reinterpret_cast<const uint4*>(row + i * p.D + x.c0);
+          rb[i] = *reinterpret_cast<const uint4*>(row + i * p.D + x.c1);
+        }
+      Angles g;
+      if (p.R > 0) {
+        const int pos = __ldg(p.positions + n);
+        if (pos < 0 || (long long)pos >= p.max_pos) continue;
+        if (x.turned) g = angles_of(p, x, pos);
+      }
+      __half* out = p.q_out + (n * p.Hq + h0) * p.D;
+#pragma unroll
+      for (int i = 0; i < HQ; ++i)
+        if (h0 + i < p.Hq) {
+          if (x.turned) {
+            float a[8], b[8];
+            unpack8(ra[i], a);
+            unpack8(rb[i], b);
+            turn_item(a, b, g, il);
+            ra[i] = pack8(a);
+            rb[i] = pack8(b);
+          }
+          *reinterpret_cast<uint4*>(out + i * p.D + x.c0) = ra[i];
+          *reinterpret_cast<uint4*>(out + i * p.D + x.c1) = rb[i];
+        }
+    }
     return;
   }
-  if constexpr (CACHE == I8KV_CACHE_FP16) {
-    const uint4* src = reinterpret_cast<const uint4*>(
-        static_cast<const __half*>(is_v ? p.v_cache : p.k_cache) +
-        ((long long)slot * p.Hkv + h) * p.D + 16 * j);
-    o[0] = src[0];
-    o[1] = src[1];
-  } else {
-    const float* sc = is_v ? p.v_scale : p.k_scale;
-    const int step = p.per_channel ? 1 : 0;
-    sc += p.per_channel ? h * p.D + 16 * j : 0;
-    float x[16];
-    if constexpr (CACHE == I8KV_CACHE_MX4) {
-      int tok;
-      const uint8_t* rec = static_cast<const uint8_t*>(p.k_cache) +
-                           mx4_record(slot, h, p.Hkv, p.D, p.bs, p.bs_shift, tok) +
-                           (is_v ? 9 * p.D : 0);
-      const uint2 w = *reinterpret_cast<const uint2*>(rec + tok * (p.D >> 1) + 8 * j);
-      const float s = e4m3_value(rec[8 * p.D + tok * ipr + j]);
-      uint32_t hv[8];
-      e2m1x8_to_h2x4(w.x, hv[0], hv[1], hv[2], hv[3]);
-      e2m1x8_to_h2x4(w.y, hv[4], hv[5], hv[6], hv[7]);
+
+  // keys and values: two tokens at a time
+  const int kv = unit - groups;
+  const bool is_v = kv >= p.Hkv;
+  const int h = is_v ? kv - p.Hkv : kv;
+  const Pieces x = pieces_of(p, j, !is_v);
+  const float* sc = is_v ? p.v_scale : p.k_scale;
+  const int step = p.per_channel ? 1 : 0;
+  if (p.per_channel) sc += h * p.D;
+  float r0[8], r1[8];
+  if constexpr (CACHE != I8KV_CACHE_FP16) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hv[i]));
-        x[2 * i] = __fmul_rn(f.x, s);  // exact: 6 significant bits
-        x[2 * i + 1] = __fmul_rn(f.y, s);
+    for (int i = 0; i < 8; ++i) {
+      r0[i] = __frcp_rn(sc[(x.c0 + i) * step]);
+      r1[i] = __frcp_rn(sc[(x.c1 + i) * step]);
+    }
+  }
+  const __half* src = (is_v ? p.v : p.k) + (long long)h * p.D;
+  const long long stride = is_v ? p.v_stride : p.k_stride;
+  for (long long n = n0; n < p.num_tokens; n += 2 * lanes) {
+    uint4 ra[2], rb[2];
+    int slot[2], pos[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const long long m = n + i * lanes;
+      slot[i] = -1;
+      pos[i] = 0;
+      if (m < p.num_tokens) {
+        ra[i] = *reinterpret_cast<const uint4*>(src + m * stride + x.c0);
+        rb[i] = *reinterpret_cast<const uint4*>(src + m * stride + x.c1);
+        slot[i] = __ldg(p.slots + m);
+        if (p.R > 0) pos[i] = __ldg(p.positions + m);
       }
-    } else {
-      const uint4 w = *reinterpret_cast<const uint4*>(
-          static_cast<const uint8_t*>(is_v ? p.v_cache : p.k_cache) +
-          ((long long)slot * p.Hkv + h) * p.D + 16 * j);
-      const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
+    }
+    Angles g[2];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t lo, hi;
-        if constexpr (CACHE == I8KV_CACHE_FP8) {
-          e4m3x4_to_h2x2(ww[i], lo, hi);
+    for (int i = 0; i < 2; ++i) {
+      if (p.R > 0 && (pos[i] < 0 || (long long)pos[i] >= p.max_pos)) {
+        // (one key item reports it)
+        if (kv == 0 && j == 0 && slot[i] >= 0) flag_or(p.flags, I8KV_FLAG_BAD_POSITION);
+        slot[i] = -1;
+      } else if ((long long)slot[i] >= p.num_slots) {
+        if (kv == 0 && j == 0) flag_or(p.flags, I8KV_FLAG_BAD_SLOT);
+        slot[i] = -1;
+      }
+      if (slot[i] >= 0 && x.turned) g[i] = angles_of(p, x, pos[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      if (slot[i] < 0) continue;
+      float a[8], b[8];
+      unpack8(ra[i], a);
+      unpack8(rb[i], b);
+      if (x.turned) turn_item(a, b, g[i], il);
+      store_item<CACHE>(p, x, h, is_v, slot[i], a, b, r0, r1, sc, step);
+    }
+  }
+}
+
+// Read-back: a thread keeps 8 channels of one key or value head, with their scales,
+// and walks the rows four at a time (slots, then codes, then 16-byte stores).
+constexpr int kGatherRows = 4;
+
+template <int CACHE>
+__global__ void __launch_bounds__(kAppendThreads)
+gather_cache_kernel(const AppendParams p, __half* __restrict__ k_out, __half* __restrict__ v_out,
+                    long long lanes) {
+  grid_dependency_wait();
+  const int ipr = p.D >> 3;
+  const int ipt = 2 * p.Hkv * ipr;
+  const long long flat = blockIdx.x * (long long)kAppendThreads + threadIdx.x;
+  const long long n0 = flat / ipt;
+  if (n0 >= lanes) return;
+  const int item = (int)(flat - n0 * ipt);
+  const int unit = item / ipr, c = 8 * (item - (item / ipr) * ipr);
+  const bool is_v = unit >= p.Hkv;
+  const int h = is_v ? unit - p.Hkv : unit;
+  __half* out = is_v ? v_out : k_out;
+  float sc[8];
+  if constexpr (CACHE != I8KV_CACHE_FP16) {
+    const float* s = is_v ? p.v_scale : p.k_scale;
+    if (p.per_channel) {
+      const float4 s0 = *reinterpret_cast<const float4*>(s + h * p.D + c);
+      const float4 s1 = *reinterpret_cast<const float4*>(s + h * p.D + c + 4);
+      sc[0] = s0.x, sc[1] = s0.y, sc[2] = s0.z, sc[3] = s0.w;
+      sc[4] = s1.x, sc[5] = s1.y, sc[6] = s1.z, sc[7] = s1.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc[i] = s[0];
+    }
+  }
+  const uint8_t* base = static_cast<const uint8_t*>(
+      CACHE == I8KV_CACHE_MX4 || !is_v ? p.k_cache : p.v_cache);
+  for (long long n = n0; n < p.num_tokens; n += kGatherRows * lanes) {
+    int slot[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+      const long long m = n + i * lanes;
+      slot[i] = m < p.num_tokens ? __ldg(p.slots + m) : -1;
+      if ((long long)slot[i] >= p.num_slots) {
+        if (item == 0) flag_or(p.flags, I8KV_FLAG_BAD_SLOT);
+        slot[i] = -1;
+      }
+    }
+    if (out == nullptr) continue;
+    uint4 raw[kGatherRows];
+    uint32_t bs[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+      raw[i] = make_uint4(0u, 0u, 0u, 0u);
+      bs[i] = 0u;
+      if (slot[i] < 0) continue;
+      if constexpr (CACHE == I8KV_CACHE_MX4) {
+        int tok;
+        const uint8_t* rec = base + mx4_record(slot[i], h, p.Hkv, p.D, p.bs, p.bs_shift, tok) +
+                             (is_v ? 9 * p.D : 0);
+        raw[i].x = *reinterpret_cast<const uint32_t*>(rec + tok * (p.D >> 1) + (c >> 1));
+        bs[i] = rec[8 * p.D + tok * (p.D >> 4) + (c >> 4)];
+      } else {
+        const long long at = ((long long)slot[i] * p.Hkv + h) * p.D + c;
+        if constexpr (CACHE == I8KV_CACHE_FP16) {
+          raw[i] = *reinterpret_cast<const uint4*>(base + 2 * at);
         } else {
-          const uint32_t f = flip_i8x4(ww[i]);
-          lo = i8x2_to_h2(f, 0x4140u);
-          hi = i8x2_to_h2(f, 0x4342u);
+          const uint2 w = *reinterpret_cast<const uint2*>(base + at);
+          raw[i].x = w.x;
+          raw[i].y = w.y;
         }
-        const float2 f0 = __half22float2(*reinterpret_cast<const __half2*>(&lo));
-        const float2 f1 = __half22float2(*reinterpret_cast<const __half2*>(&hi));
-        x[4 * i] = f0.x;
-        x[4 * i + 1] = f0.y;
-        x[4 * i + 2] = f1.x;
-        x[4 * i + 3] = f1.y;
       }
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) x[i] = __fmul_rn(x[i], sc[i * step]);
-    o[0] = make_uint4(pack_h2(x[0], x[1]), pack_h2(x[2], x[3]), pack_h2(x[4], x[5]),
-                      pack_h2(x[6], x[7]));
-    o[1] = make_uint4(pack_h2(x[8], x[9]), pack_h2(x[10], x[11]), pack_h2(x[12], x[13]),
-                      pack_h2(x[14], x[15]));
+    for (int i = 0; i < kGatherRows; ++i) {
+      const long long m = n + i * lanes;
+      if (m >= p.num_tokens) break;
+      uint4 v = raw[i];
+      if constexpr (CACHE != I8KV_CACHE_FP16) {
+        uint32_t hv[4] = {0u, 0u, 0u, 0u};
+        if (slot[i] >= 0) {
+          if constexpr (CACHE == I8KV_CACHE_MX4) {
+            e2m1x8_to_h2x4(raw[i].x, hv[0], hv[1], hv[2], hv[3]);
+            uint32_t s2, unused;
+            e4m3x4_to_h2x2(bs[i] * 0x0101u, s2, unused);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)  // exact: 6 significant bits
+              asm("mul.f16x2 %0, %0, %1;\n" : "+r"(hv[k]) : "r"(s2));
+          } else if constexpr (CACHE == I8KV_CACHE_FP8) {
+            e4m3x4_to_h2x2(raw[i].x, hv[0], hv[1]);
+            e4m3x4_to_h2x2(raw[i].y, hv[2], hv[3]);
+          } else {
+            const uint32_t f0 = flip_i8x4(raw[i].x), f1 = flip_i8x4(raw[i].y);
+            hv[0] = i8x2_to_h2(f0, 0x4140u);
+            hv[1] = i8x2_to_h2(f0, 0x4342u);
+            hv[2] = i8x2_to_h2(f1, 0x4140u);
+            hv[3] = i8x2_to_h2(f1, 0x4342u);
+          }
+          uint32_t o[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hv[k]));
+            o[k] = pack_h2(__fmul_rn(f.x, sc[2 * k]), __fmul_rn(f.y, sc[2 * k + 1]));
+          }
+          v = make_uint4(o[0], o[1], o[2], o[3]);
+        } else {
+          v = make_uint4(0u, 0u, 0u, 0u);
+        }
+      }
+      *reinterpret_cast<uint4*>(out + (m * p.Hkv + h) * p.D + c) = v;
+    }
   }
+}
+
+// Token lanes of a grid: about `ctas` CTAs of threads, at most one lane per token.
+long long lanes_of(long long tokens, long long per_token, long long ctas) {
+  long long lanes = ctas * kAppendThreads / per_token;
+  if (lanes < 1) lanes = 1;
+  return lanes < tokens ? lanes : tokens;
+}
+
+cudaError_t sm_count(int* sms) {
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  return cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
 }
 
 cudaLaunchConfig_t config_of(long long threads, cudaLaunchAttribute* attr, cudaStream_t stream) {
@@ -279,31 +469,61 @@ cudaLaunchConfig_t config_of(long long threads, cudaLaunchAttribute* attr, cudaS
 
 }  // namespace
 
-cudaError_t launch_rope_and_cache(const AppendParams& p, int cache_dtype, cudaStream_t stream) {
-  const long long threads = (long long)p.num_tokens * (p.Hq + 2 * p.Hkv) * (p.D / 16);
+namespace {
+
+template <int CACHE, int HQ>
+cudaError_t append_with(const AppendParams& p, int sms, cudaStream_t stream) {
+  const long long ipt = ((p.Hq + HQ - 1) / HQ + 2LL * p.Hkv) * (p.D / 16);
+  const long long lanes = lanes_of(p.num_tokens, ipt, 4LL * sms);
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config_of(threads, &attr, stream);
+  const cudaLaunchConfig_t cfg = config_of(lanes * ipt, &attr, stream);
+  return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<CACHE, HQ>, p, lanes);
+}
+
+// Four query heads per thread where one head each would fill the GPU more than once
+// over (64 of 192 bytes saved per head); one head each spreads fewer tokens wider.
+template <int CACHE>
+cudaError_t append_of(const AppendParams& p, cudaStream_t stream) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const long long items = (long long)p.num_tokens * (p.Hq + 2 * p.Hkv) * (p.D / 16);
+  return items > 4LL * sms * kAppendThreads ? append_with<CACHE, 4>(p, sms, stream)
+                                            : append_with<CACHE, 1>(p, sms, stream);
+}
+
+template <int CACHE>
+cudaError_t gather_of(const AppendParams& p, void* k_out, void* v_out, cudaStream_t stream) {
+  int sms = 0;
+  const cudaError_t e = sm_count(&sms);
+  if (e != cudaSuccess) return e;
+  const long long ipt = 2LL * p.Hkv * (p.D / 8);
+  const long long lanes = lanes_of(p.num_tokens, ipt, 8LL * sms);
+  cudaLaunchAttribute attr;
+  const cudaLaunchConfig_t cfg = config_of(lanes * ipt, &attr, stream);
+  return cudaLaunchKernelEx(&cfg, gather_cache_kernel<CACHE>, p, static_cast<__half*>(k_out),
+                            static_cast<__half*>(v_out), lanes);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_and_cache(const AppendParams& p, int cache_dtype, cudaStream_t stream) {
   switch (cache_dtype) {
-    case I8KV_CACHE_INT8: return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<I8KV_CACHE_INT8>, p);
-    case I8KV_CACHE_FP16: return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<I8KV_CACHE_FP16>, p);
-    case I8KV_CACHE_FP8: return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<I8KV_CACHE_FP8>, p);
-    case I8KV_CACHE_MX4: return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<I8KV_CACHE_MX4>, p);
+    case I8KV_CACHE_INT8: return append_of<I8KV_CACHE_INT8>(p, stream);
+    case I8KV_CACHE_FP16: return append_of<I8KV_CACHE_FP16>(p, stream);
+    case I8KV_CACHE_FP8: return append_of<I8KV_CACHE_FP8>(p, stream);
+    case I8KV_CACHE_MX4: return append_of<I8KV_CACHE_MX4>(p, stream);
     default: return cudaErrorInvalidValue;
   }
 }
 
 cudaError_t launch_gather_cache(const AppendParams& p, int cache_dtype, void* k_out, void* v_out,
                                 cudaStream_t stream) {
-  const long long threads = (long long)p.num_tokens * 2 * p.Hkv * (p.D / 16);
-  cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config_of(threads, &attr, stream);
-  __half* k = static_cast<__half*>(k_out);
-  __half* v = static_cast<__half*>(v_out);
   switch (cache_dtype) {
-    case I8KV_CACHE_INT8: return cudaLaunchKernelEx(&cfg, gather_cache_kernel<I8KV_CACHE_INT8>, p, k, v);
-    case I8KV_CACHE_FP16: return cudaLaunchKernelEx(&cfg, gather_cache_kernel<I8KV_CACHE_FP16>, p, k, v);
-    case I8KV_CACHE_FP8: return cudaLaunchKernelEx(&cfg, gather_cache_kernel<I8KV_CACHE_FP8>, p, k, v);
-    case I8KV_CACHE_MX4: return cudaLaunchKernelEx(&cfg, gather_cache_kernel<I8KV_CACHE_MX4>, p, k, v);
+    case I8KV_CACHE_INT8: return gather_of<I8KV_CACHE_INT8>(p, k_out, v_out, stream);
+    case I8KV_CACHE_FP16: return gather_of<I8KV_CACHE_FP16>(p, k_out, v_out, stream);
+    case I8KV_CACHE_FP8: return gather_of<I8KV_CACHE_FP8>(p, k_out, v_out, stream);
+    case I8KV_CACHE_MX4: return gather_of<I8KV_CACHE_MX4>(p, k_out, v_out, stream);
     default: return cudaErrorInvalidValue;
   }
 }
