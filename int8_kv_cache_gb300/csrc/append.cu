@@ -220,6 +220,22 @@ __device__ __forceinline__ void store_item(const AppendParams& p, const Pieces& 
   }
 }
 
+// The scales of 8 channels from channel `at` of s (or the one scale, eight times).
+template <int CACHE>
+__device__ __forceinline__ void scales8(const AppendParams& p, const float* s, int at, float (&sc)[8]) {
+  if constexpr (CACHE != I8KV_CACHE_FP16) {
+    if (p.per_channel) {
+      const float4 a = *reinterpret_cast<const float4*>(s + at);
+      const float4 b = *reinterpret_cast<const float4*>(s + at + 4);
+      sc[0] = a.x, sc[1] = a.y, sc[2] = a.z, sc[3] = a.w;
+      sc[4] = b.x, sc[5] = b.y, sc[6] = b.z, sc[7] = b.w;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sc[i] = s[0];
+    }
+  }
+}
+
 // HQ: query heads per thread (1: a few tokens, where threads are short; else 4).
 template <int CACHE, int HQ>
 __global__ void __launch_bounds__(kAppendThreads, 2)
@@ -228,10 +244,10 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
   const int ipr = p.D >> 4;                           // items per row
   const int groups = (p.Hq + HQ - 1) / HQ;
   const int ipt = (groups + 2 * p.Hkv) * ipr;         // items per token
-  const long long flat = blockIdx.x * (long long)kAppendThreads + threadIdx.x;
-  const long long n0 = flat / ipt;
-  if (n0 >= lanes) return;
-  const int item = (int)(flat - n0 * ipt);
+  const unsigned flat = blockIdx.x * kAppendThreads + threadIdx.x;
+  const unsigned n0 = flat / (unsigned)ipt;
+  if (n0 >= (unsigned)lanes) return;
+  const int item = flat - n0 * ipt;
   const int unit = item / ipr, j = item - (item / ipr) * ipr;
   const bool il = p.interleaved != 0;
 
@@ -282,10 +298,18 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
   if (p.per_channel) sc += h * p.D;
   float r0[8], r1[8];
   if constexpr (CACHE != I8KV_CACHE_FP16) {
+    scales8<CACHE>(p, sc, x.c0, r0);
+    scales8<CACHE>(p, sc, x.c1, r1);
+    if (p.per_channel) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      r0[i] = __frcp_rn(sc[(x.c0 + i) * step]);
-      r1[i] = __frcp_rn(sc[(x.c1 + i) * step]);
+      for (int i = 0; i < 8; ++i) {
+        r0[i] = __frcp_rn(r0[i]);
+        r1[i] = __frcp_rn(r1[i]);
+      }
+    } else {
+      const float r = __frcp_rn(r0[0]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) r0[i] = r1[i] = r;
     }
   }
   const __half* src = (is_v ? p.v : p.k) + (long long)h * p.D;
@@ -330,113 +354,118 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
   }
 }
 
-// Read-back: a thread keeps 8 channels of one key or value head, with their scales,
-// and walks the rows four at a time (slots, then codes, then 16-byte stores).
-constexpr int kGatherRows = 4;
+// Read-back: a thread keeps 8 channels of a head, for keys and values alike (one slot,
+// one address, two rows), with their scales, and walks the rows a few at a time: the
+// slots of the next ones are on their way while these are converted; 16-byte stores.
+constexpr int kGatherRows = 2;
+
+// fp16 values of 8 channels: codes raw, block scale byte bs, scales sc.
+template <int CACHE>
+__device__ __forceinline__ uint4 values8(uint4 raw, uint32_t bs, const float (&sc)[8]) {
+  if constexpr (CACHE == I8KV_CACHE_FP16) {
+    return raw;
+  } else {
+    uint32_t hv[4];
+    if constexpr (CACHE == I8KV_CACHE_MX4) {
+      e2m1x8_to_h2x4(raw.x, hv[0], hv[1], hv[2], hv[3]);
+      uint32_t s2, unused;
+      e4m3x4_to_h2x2(bs * 0x0101u, s2, unused);
+#pragma unroll
+      for (int k = 0; k < 4; ++k)  // exact: 6 significant bits
+        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(hv[k]) : "r"(s2));
+    } else if constexpr (CACHE == I8KV_CACHE_FP8) {
+      e4m3x4_to_h2x2(raw.x, hv[0], hv[1]);
+      e4m3x4_to_h2x2(raw.y, hv[2], hv[3]);
+    } else {
+      const uint32_t f0 = flip_i8x4(raw.x), f1 = flip_i8x4(raw.y);
+      hv[0] = i8x2_to_h2(f0, 0x4140u);
+      hv[1] = i8x2_to_h2(f0, 0x4342u);
+      hv[2] = i8x2_to_h2(f1, 0x4140u);
+      hv[3] = i8x2_to_h2(f1, 0x4342u);
+    }
+    uint32_t o[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hv[k]));
+      o[k] = pack_h2(__fmul_rn(f.x, sc[2 * k]), __fmul_rn(f.y, sc[2 * k + 1]));
+    }
+    return make_uint4(o[0], o[1], o[2], o[3]);
+  }
+}
 
 template <int CACHE>
 __global__ void __launch_bounds__(kAppendThreads)
 gather_cache_kernel(const AppendParams p, __half* __restrict__ k_out, __half* __restrict__ v_out,
-                    long long lanes) {
+                    int lanes) {
+  constexpr bool MX = CACHE == I8KV_CACHE_MX4;
+  constexpr int N = kGatherRows;
   grid_dependency_wait();
-  const int ipr = p.D >> 3;
-  const int ipt = 2 * p.Hkv * ipr;
-  const long long flat = blockIdx.x * (long long)kAppendThreads + threadIdx.x;
-  const long long n0 = flat / ipt;
-  if (n0 >= lanes) return;
-  const int item = (int)(flat - n0 * ipt);
-  const int unit = item / ipr, c = 8 * (item - (item / ipr) * ipr);
-  const bool is_v = unit >= p.Hkv;
-  const int h = is_v ? unit - p.Hkv : unit;
-  __half* out = is_v ? v_out : k_out;
-  float sc[8];
-  if constexpr (CACHE != I8KV_CACHE_FP16) {
-    const float* s = is_v ? p.v_scale : p.k_scale;
-    if (p.per_channel) {
-      const float4 s0 = *reinterpret_cast<const float4*>(s + h * p.D + c);
-      const float4 s1 = *reinterpret_cast<const float4*>(s + h * p.D + c + 4);
-      sc[0] = s0.x, sc[1] = s0.y, sc[2] = s0.z, sc[3] = s0.w;
-      sc[4] = s1.x, sc[5] = s1.y, sc[6] = s1.z, sc[7] = s1.w;
-    } else {
+  const unsigned ipr = p.D >> 3;
+  const unsigned ipt = p.Hkv * ipr;
+  const unsigned flat = blockIdx.x * kAppendThreads + threadIdx.x;
+  const unsigned n0 = flat / ipt;
+  if (n0 >= (unsigned)lanes) return;
+  const unsigned item = flat - n0 * ipt;
+  const int h = item / ipr, c = 8 * (item - h * ipr);
+  const int at = h * p.D + c;  // in a row of the outputs (and of a plain cache)
+  const long long row = (long long)p.Hkv * p.D;
+  float ks[8], vs[8];
+  scales8<CACHE>(p, p.k_scale, at, ks);
+  scales8<CACHE>(p, p.v_scale, at, vs);
+  auto slot_of = [&](long long m) -> int {
+    if (m >= p.num_tokens) return -1;
+    const int s = __ldg(p.slots + m);
+    if ((long long)s < p.num_slots) return s;
+    if (item == 0) flag_or(p.flags, I8KV_FLAG_BAD_SLOT);
+    return -1;
+  };
+  int next[N];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sc[i] = s[0];
-    }
-  }
-  const uint8_t* base = static_cast<const uint8_t*>(
-      CACHE == I8KV_CACHE_MX4 || !is_v ? p.k_cache : p.v_cache);
-  for (long long n = n0; n < p.num_tokens; n += kGatherRows * lanes) {
-    int slot[kGatherRows];
+  for (int i = 0; i < N; ++i) next[i] = slot_of(n0 + (long long)i * lanes);
+  for (long long n = n0; n < p.num_tokens; n += (long long)N * lanes) {
+    uint4 rk[N], rv[N];
+    uint32_t bk[N], bv[N];
+    bool some[N];
 #pragma unroll
-    for (int i = 0; i < kGatherRows; ++i) {
-      const long long m = n + i * lanes;
-      slot[i] = m < p.num_tokens ? __ldg(p.slots + m) : -1;
-      if ((long long)slot[i] >= p.num_slots) {
-        if (item == 0) flag_or(p.flags, I8KV_FLAG_BAD_SLOT);
-        slot[i] = -1;
-      }
-    }
-    if (out == nullptr) continue;
-    uint4 raw[kGatherRows];
-    uint32_t bs[kGatherRows];
-#pragma unroll
-    for (int i = 0; i < kGatherRows; ++i) {
-      raw[i] = make_uint4(0u, 0u, 0u, 0u);
-      bs[i] = 0u;
-      if (slot[i] < 0) continue;
-      if constexpr (CACHE == I8KV_CACHE_MX4) {
+    for (int i = 0; i < N; ++i) {
+      rk[i] = rv[i] = make_uint4(0u, 0u, 0u, 0u);
+      bk[i] = bv[i] = 0u;
+      some[i] = next[i] >= 0;
+      if (!some[i]) continue;
+      if constexpr (MX) {
         int tok;
-        const uint8_t* rec = base + mx4_record(slot[i], h, p.Hkv, p.D, p.bs, p.bs_shift, tok) +
-                             (is_v ? 9 * p.D : 0);
-        raw[i].x = *reinterpret_cast<const uint32_t*>(rec + tok * (p.D >> 1) + (c >> 1));
-        bs[i] = rec[8 * p.D + tok * (p.D >> 4) + (c >> 4)];
+        const uint8_t* rec = static_cast<const uint8_t*>(p.k_cache) +
+                             mx4_record(next[i], h, p.Hkv, p.D, p.bs, p.bs_shift, tok);
+        const uint8_t* code = rec + tok * (p.D >> 1) + (c >> 1);
+        const uint8_t* scale = rec + 8 * p.D + tok * (p.D >> 4) + (c >> 4);
+        rk[i].x = *reinterpret_cast<const uint32_t*>(code);
+        rv[i].x = *reinterpret_cast<const uint32_t*>(code + 9 * p.D);
+        bk[i] = scale[0];
+        bv[i] = scale[9 * p.D];
       } else {
-        const long long at = ((long long)slot[i] * p.Hkv + h) * p.D + c;
+        const long long o = next[i] * row + at;
         if constexpr (CACHE == I8KV_CACHE_FP16) {
-          raw[i] = *reinterpret_cast<const uint4*>(base + 2 * at);
+          rk[i] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.k_cache) + o);
+          rv[i] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.v_cache) + o);
         } else {
-          const uint2 w = *reinterpret_cast<const uint2*>(base + at);
-          raw[i].x = w.x;
-          raw[i].y = w.y;
+          const uint2 a = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.k_cache) + o);
+          const uint2 b = *reinterpret_cast<const uint2*>(static_cast<const uint8_t*>(p.v_cache) + o);
+          rk[i].x = a.x, rk[i].y = a.y;
+          rv[i].x = b.x, rv[i].y = b.y;
         }
       }
     }
 #pragma unroll
-    for (int i = 0; i < kGatherRows; ++i) {
-      const long long m = n + i * lanes;
+    for (int i = 0; i < N; ++i) next[i] = slot_of(n + (long long)(N + i) * lanes);
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const long long m = n + (long long)i * lanes;
       if (m >= p.num_tokens) break;
-      uint4 v = raw[i];
-      if constexpr (CACHE != I8KV_CACHE_FP16) {
-        uint32_t hv[4] = {0u, 0u, 0u, 0u};
-        if (slot[i] >= 0) {
-          if constexpr (CACHE == I8KV_CACHE_MX4) {
-            e2m1x8_to_h2x4(raw[i].x, hv[0], hv[1], hv[2], hv[3]);
-            uint32_t s2, unused;
-            e4m3x4_to_h2x2(bs[i] * 0x0101u, s2, unused);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)  // exact: 6 significant bits
-              asm("mul.f16x2 %0, %0, %1;\n" : "+r"(hv[k]) : "r"(s2));
-          } else if constexpr (CACHE == I8KV_CACHE_FP8) {
-            e4m3x4_to_h2x2(raw[i].x, hv[0], hv[1]);
-            e4m3x4_to_h2x2(raw[i].y, hv[2], hv[3]);
-          } else {
-            const uint32_t f0 = flip_i8x4(raw[i].x), f1 = flip_i8x4(raw[i].y);
-            hv[0] = i8x2_to_h2(f0, 0x4140u);
-            hv[1] = i8x2_to_h2(f0, 0x4342u);
-            hv[2] = i8x2_to_h2(f1, 0x4140u);
-            hv[3] = i8x2_to_h2(f1, 0x4342u);
-          }
-          uint32_t o[4];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hv[k]));
-            o[k] = pack_h2(__fmul_rn(f.x, sc[2 * k]), __fmul_rn(f.y, sc[2 * k + 1]));
-          }
-          v = make_uint4(o[0], o[1], o[2], o[3]);
-        } else {
-          v = make_uint4(0u, 0u, 0u, 0u);
-        }
-      }
-      *reinterpret_cast<uint4*>(out + (m * p.Hkv + h) * p.D + c) = v;
+      const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+      if (k_out != nullptr)
+        *reinterpret_cast<uint4*>(k_out + m * row + at) = some[i] ? values8<CACHE>(rk[i], bk[i], ks) : zero;
+      if (v_out != nullptr)
+        *reinterpret_cast<uint4*>(v_out + m * row + at) = some[i] ? values8<CACHE>(rv[i], bv[i], vs) : zero;
     }
   }
 }
@@ -497,12 +526,12 @@ cudaError_t gather_of(const AppendParams& p, void* k_out, void* v_out, cudaStrea
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
-  const long long ipt = 2LL * p.Hkv * (p.D / 8);
-  const long long lanes = lanes_of(p.num_tokens, ipt, 8LL * sms);
+  const long long ipt = (long long)p.Hkv * (p.D / 8);
+  const long long lanes = lanes_of(p.num_tokens, ipt, 4LL * sms);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = config_of(lanes * ipt, &attr, stream);
   return cudaLaunchKernelEx(&cfg, gather_cache_kernel<CACHE>, p, static_cast<__half*>(k_out),
-                            static_cast<__half*>(v_out), lanes);
+                            static_cast<__half*>(v_out), (int)lanes);
 }
 
 }  // namespace
