@@ -5,7 +5,8 @@ Every function here has the name and the meaning of the C entry point of the
 same name in ``include/int8kv.h``.  The binding only marshals arguments: it
 reads shapes from the tensors, checks dtype / device / contiguity, passes raw
 device pointers and the current CUDA stream, and turns a non-zero status into
-an exception.  All computation runs in the library's CUDA kernels; there is
+an exception; for the calls of a decode step over the 4-bit cache a compiled
+module does the same.  All computation runs in the library's CUDA kernels; there is
 no fallback.  PyTorch provides device memory and streams.
 """
 from __future__ import annotations
@@ -376,59 +377,21 @@ def reshape_and_cache(k_new, v_new, slot_mapping, k_cache, v_cache, k_scale, v_s
 # rotating append, read-back, and the 4-bit cache
 # --------------------------------------------------------------------------
 
-def _ptr(x, dtype, name: str, dev: int, shape=None) -> Optional[int]:
-    """Device pointer of a dense tensor of the given dtype (and shape) on device
-    dev, the current one; None -> NULL."""
-    if x is None:
-        return None
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype is not dtype:
-        raise TypeError(f"{name}: expected {dtype}, got {x.dtype}")
-    if x.get_device() != dev:
-        raise ValueError(f"{name} is on {x.device}, but the current device is cuda:{dev}")
-    if not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    if shape is not None and x.shape != shape:
-        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(x.shape)}")
-    return x.data_ptr()
+_BINDING = None
 
 
-def _rows(x, name: str, dev: int, T: int, D: int):
-    """(pointer, heads, token stride in elements) of new rows [T, H, D] fp16: the
-    heads of a token contiguous, the tokens any distance apart."""
-    if not isinstance(x, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype is not torch.float16:
-        raise TypeError(f"{name}: expected {torch.float16}, got {x.dtype}")
-    if x.get_device() != dev:
-        raise ValueError(f"{name} is on {x.device}, but the current device is cuda:{dev}")
-    if x.dim() != 3 or x.shape[0] != T or x.shape[2] != D:
-        raise ValueError(f"{name}: expected [{T}, heads, {D}], got {tuple(x.shape)}")
-    st, sh, sd = x.stride()
-    H = x.shape[1]
-    if x.numel() and ((sd != 1 and D > 1) or (sh != D and H > 1)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return x.data_ptr(), H, st
-
-
-def _scale_ptrs(k_scale, v_scale, scale_kind: int, cache_dtype: int, Hkv: int, D: int, dev: int):
-    if cache_dtype == CACHE_FP16:
-        return None, None
-    if k_scale is None or v_scale is None:
-        raise ValueError("k_scale and v_scale are needed for a quantised cache")
-    n = Hkv * D if scale_kind == SCALE_PER_CHANNEL else 1
-    for x, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if x.numel() != n:
-            raise ValueError(f"{name}: expected {n} values, got {x.numel()}")
-    return (_ptr(k_scale, torch.float32, "k_scale", dev),
-            _ptr(v_scale, torch.float32, "v_scale", dev))
-
-
-def _raw_stream(stream, dev: int) -> int:
-    if stream is None:
-        return torch._C._cuda_getCurrentRawStream(dev)
-    return _stream(stream)
+def _compiled():
+    """The compiled half of the binding (csrc/binding.cpp): checks of the tensors and
+    the call, for the functions below."""
+    global _BINDING
+    if _BINDING is None:
+        load()
+        if not os.path.exists(os.path.join(_HERE, "_binding.so")):
+            raise RuntimeError("_binding.so is missing: build the CUDA library first "
+                               "(python -c 'import __graft_entry__ as g; g.build()')")
+        from . import _binding
+        _BINDING = _binding
+    return _BINDING
 
 
 def mx4_cache_shape(num_blocks: int, block_size: int, Hkv: int, D: int):
@@ -438,33 +401,6 @@ def mx4_cache_shape(num_blocks: int, block_size: int, Hkv: int, D: int):
         raise ValueError("an MX4 cache wants at least one block, a block_size that is a multiple "
                          "of 16 and D in (64, 128, 256)")
     return num_blocks, Hkv, block_size // 16, 18 * D
-
-
-def _mx4_dims(cache, name: str, dev: int):
-    """(pointer, num_blocks, Hkv, block_size, D) of an MX4 cache."""
-    p = _ptr(cache, torch.uint8, name, dev)
-    if cache.dim() != 4 or cache.shape[3] % 18:
-        raise ValueError(f"{name}: expected [num_blocks, Hkv, block_size / 16, 18 * D], got "
-                         f"{tuple(cache.shape)}")
-    nb, Hkv, tiles, rec = cache.shape
-    return p, nb, Hkv, 16 * tiles, rec // 18
-
-
-def _cache_args(k_cache, v_cache, dev: int):
-    """(k pointer, v pointer, cache dtype, num_slots, block_size, Hkv, D): an MX4
-    record cache where v_cache is None, else a key and a value cache
-    [num_slots, Hkv, D] or [num_blocks, block_size, Hkv, D]."""
-    if v_cache is None:
-        p, nb, Hkv, bs, D = _mx4_dims(k_cache, "k_cache", dev)
-        return p, None, CACHE_MX4, nb * bs, bs, Hkv, D
-    cd = _cache_dtype(k_cache)
-    if k_cache.dim() not in (3, 4):
-        raise ValueError("k_cache: expected [num_slots, Hkv, D] or [num_blocks, block_size, Hkv, D], "
-                         f"got {tuple(k_cache.shape)}")
-    Hkv, D = k_cache.shape[-2:]
-    return (_ptr(k_cache, k_cache.dtype, "k_cache", dev),
-            _ptr(v_cache, k_cache.dtype, "v_cache", dev, k_cache.shape), cd,
-            k_cache.numel() // max(Hkv * D, 1), 16, Hkv, D)
 
 
 def rope_and_cache(q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale,
@@ -478,61 +414,24 @@ def rope_and_cache(q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v
     (``mx4_cache_shape``) with v_cache None; an fp16 cache takes no scales.
     Returns the rotated queries [T, Hq, D] (``q_out``, which may be a dense q
     itself), or None without q."""
-    dev = torch.cuda.current_device()
-    kc, vc, cd, num_slots, bs, Hkv, D = _cache_args(k_cache, v_cache, dev)
-    T = k_new.shape[0]
-    kp, hk, ks = _rows(k_new, "k_new", dev, T, D)
-    vp, hv, vs = _rows(v_new, "v_new", dev, T, D)
-    if hk != Hkv or hv != Hkv:
-        raise ValueError(f"k_new / v_new have {hk} / {hv} heads, the cache {Hkv}")
-    qp, Hq, qs, op = None, 0, 0, None
-    if q is not None:
-        qp, Hq, qs = _rows(q, "q", dev, T, D)
-        if q_out is None:
-            q_out = torch.empty((T, Hq, D), dtype=torch.float16, device=q.device)
-        op = _ptr(q_out, torch.float16, "q_out", dev, q.shape)
-    elif q_out is not None:
-        raise ValueError("q_out without q")
-    if cos_sin is None:
-        pp, cp, max_pos, R = None, None, 0, 0
-    else:
-        if cos_sin.dim() != 2:
-            raise ValueError("cos_sin must be [max_pos, rot_dim]")
-        max_pos, R = cos_sin.shape
-        pp = _ptr(positions, torch.int32, "positions", dev, (T,))
-        cp = _ptr(cos_sin, torch.float32, "cos_sin", dev)
-    ksc, vsc = _scale_ptrs(k_scale, v_scale, scale_kind, cd, Hkv, D, dev)
-    st = load().rope_and_cache(
-        qp, qs, kp, ks, vp, vs, pp, cp, max_pos, R, 1 if interleaved else 0,
-        _ptr(slot_mapping, torch.int32, "slot_mapping", dev, (T,)), T, Hq, Hkv, D, op, kc, vc, cd,
-        num_slots, bs, ksc, vsc, scale_kind, _ptr(flags, torch.int32, "flags", dev),
-        _raw_stream(stream, dev))
-    if st:
-        _check("rope_and_cache", st)
-    return q_out
+    r = (_BINDING or _compiled()).rope_and_cache(
+        q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+        scale_kind, interleaved, q_out, flags, None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check("rope_and_cache", r)
+    return r
 
 
 def gather_cache(slot_mapping, k_cache, v_cache, k_scale, v_scale, scale_kind: int, k_out=None,
                  v_out=None, flags=None, stream=None):
     """Rows slot_mapping [N] of a paged cache (as ``rope_and_cache`` takes it) as
     fp16 values: (k_out, v_out), each [N, Hkv, D]; zeros for a slot < 0."""
-    dev = torch.cuda.current_device()
-    kc, vc, cd, num_slots, bs, Hkv, D = _cache_args(k_cache, v_cache, dev)
-    N = slot_mapping.shape[0]
-    shape = (N, Hkv, D)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=torch.float16, device=k_cache.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=torch.float16, device=k_cache.device)
-    ksc, vsc = _scale_ptrs(k_scale, v_scale, scale_kind, cd, Hkv, D, dev)
-    st = load().gather_cache(
-        _ptr(slot_mapping, torch.int32, "slot_mapping", dev, (N,)), N, Hkv, D, kc, vc, cd,
-        num_slots, bs, ksc, vsc, scale_kind, _ptr(k_out, torch.float16, "k_out", dev, shape),
-        _ptr(v_out, torch.float16, "v_out", dev, shape), _ptr(flags, torch.int32, "flags", dev),
-        _raw_stream(stream, dev))
-    if st:
-        _check("gather_cache", st)
-    return k_out, v_out
+    r = (_BINDING or _compiled()).gather_cache(
+        slot_mapping, k_cache, v_cache, k_scale, v_scale, scale_kind, k_out, v_out, flags,
+        None if stream is None else _stream(stream))
+    if type(r) is int:
+        _check("gather_cache", r)
+    return r
 
 
 def paged_decode_mx4(q, cache, k_scale, v_scale, scale_kind: int, block_table, seq_lens,
@@ -542,32 +441,13 @@ def paged_decode_mx4(q, cache, k_scale, v_scale, scale_kind: int, block_table, s
     """``paged_decode`` over an MX4 cache [num_blocks, Hkv, block_size / 16, 18 D]
     (uint8): q [B, Hq, D] fp16, one new token per sequence.  num_splits = 0 takes
     decode_plan's GEOM_BALANCED values for CACHE_MX4."""
-    dev = torch.cuda.current_device()
-    cp, nb, Hkv, bs, D = _mx4_dims(cache, "cache", dev)
-    if q.dim() != 3 or q.shape[2] != D:
-        raise ValueError(f"q: expected [B, Hq, {D}], got {tuple(q.shape)}")
-    B, Hq, _ = q.shape
-    if block_table.dim() != 2 or block_table.shape[0] != B:
-        raise ValueError(f"block_table: expected [{B}, max_blocks], got {tuple(block_table.shape)}")
-    qp = _ptr(q, torch.float16, "q", dev)
-    if out is None and not partials_only:
-        out = torch.empty_like(q)
-    ws_bytes = 0
-    if workspace is not None:
-        ws_bytes = workspace.numel() * workspace.element_size()
-    ksc, vsc = _scale_ptrs(k_scale, v_scale, scale_kind, CACHE_MX4, Hkv, D, dev)
-    st = load().paged_decode_mx4(
-        qp, cp, ksc, vsc, scale_kind, _ptr(block_table, torch.int32, "block_table", dev),
-        _ptr(seq_lens, torch.int32, "seq_lens", dev, (B,)), B, Hq, Hkv, D, bs,
-        block_table.shape[1], nb, softmax_scale,
-        _ptr(head_sink, torch.float32, "head_sink", dev, (Hq,)), softcap, window, num_splits, chunk,
-        None if workspace is None else _ptr(workspace, workspace.dtype, "workspace", dev), ws_bytes,
-        None if partials_only else _ptr(out, torch.float16, "out", dev, q.shape),
-        _ptr(lse, torch.float32, "lse", dev, (B, Hq)), _ptr(flags, torch.int32, "flags", dev),
-        _raw_stream(stream, dev))
-    if st:
-        _check("paged_decode_mx4", st)
-    return None if partials_only else out
+    r = (_BINDING or _compiled()).paged_decode_mx4(
+        q, cache, k_scale, v_scale, scale_kind, block_table, seq_lens, softmax_scale, head_sink,
+        num_splits, chunk, workspace, out, lse, flags,
+        None if stream is None else _stream(stream), partials_only, softcap, window)
+    if type(r) is int:
+        _check("paged_decode_mx4", r)
+    return r
 
 
 def fp8_to_fp16(x, out=None, stream=None):

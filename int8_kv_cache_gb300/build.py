@@ -1,9 +1,12 @@
-"""Build libint8kv.so in-tree with nvcc for sm_103a.
+"""Build libint8kv.so in-tree with nvcc for sm_103a, and the compiled half of
+the Python binding with the host compiler.
 
-Every translation unit under ``csrc/`` is compiled to an object file in
+Every CUDA translation unit under ``csrc/`` is compiled to an object file in
 parallel (one ``-gencode`` for sm_103a), then linked into
-``int8_kv_cache_gb300/libint8kv.so``.  An object is rebuilt when its source,
-any header of ``csrc/``, the public header or the flags changed.
+``int8_kv_cache_gb300/libint8kv.so``; ``csrc/binding.cpp`` becomes
+``int8_kv_cache_gb300/_binding.so``, which uses that library.  An object is
+rebuilt when its source, any header of ``csrc/``, the public header, the flags
+(or, for the binding, the PyTorch version) changed.
 """
 from __future__ import annotations
 
@@ -12,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -20,6 +24,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libint8kv.so")
 HEADER = os.path.join(ROOT, "include", "int8kv.h")
+BINDING = os.path.join(PKG, "_binding.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
@@ -63,12 +68,53 @@ def _compile(src: str, verbose: bool):
     return obj, r.stderr if verbose else ""
 
 
+def _compile_binding():
+    """The object of csrc/binding.cpp and whether it is new."""
+    import torch
+    base = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    inc = [os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    src, obj = os.path.join(CSRC, "binding.cpp"), os.path.join(BUILD, "binding.o")
+    flags = ["-O1", "-std=c++17", "-fPIC",
+             f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}"]
+    h = hashlib.sha256(" ".join(flags + inc + [torch.__version__, sys.version]).encode())
+    for f in (src, HEADER):
+        with open(f, "rb") as fh:
+            h.update(fh.read())
+    stamp = obj + ".sha"
+    if os.path.exists(obj) and os.path.exists(stamp) and open(stamp).read() == h.hexdigest():
+        return obj, False
+    cmd = ["g++"] + flags + [x for p in inc for x in ("-isystem", p)] + ["-c", src, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
+    with open(stamp, "w") as fh:
+        fh.write(h.hexdigest())
+    return obj, True
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    cmd = ["g++", "-shared", "-o", tmp, obj, "-L", PKG, "-l:libint8kv.so", "-L", lib, "-ltorch_python",
+           "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False, jobs: int = 0) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = _sources()
-    jobs = jobs or min(len(srcs), max(1, os.cpu_count() or 1))
+    jobs = jobs or min(len(srcs) + 1, max(1, os.cpu_count() or 1))
     with ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose), srcs))
+        binding_obj, binding_new = binding.result()
     objs = [o for o, _ in results]
     if verbose:
         for o, log in results:
@@ -80,6 +126,8 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    if binding_new or not os.path.exists(BINDING):
+        _link_binding(binding_obj)
     return LIB
 
 
