@@ -96,9 +96,10 @@ typedef enum {
 #define I8KV_FLAG_BAD_SLOT 0x8u    /* reshape_and_cache: a slot >= num_slots was skipped      */
 #define I8KV_FLAG_FP32_PATH 0x10u  /* some CTA evaluated its heads on the FP32 path (see the
                                       numerical eligibility rules below)                     */
-#define I8KV_FLAG_WAIT_TIMEOUT 0x20u /* dsa_prefill's tensor-core kernel: a CTA gave up waiting
-                                        (about a second) for its own asynchronous copies or
-                                        tensor-core products; its outputs are NaN          */
+#define I8KV_FLAG_WAIT_TIMEOUT 0x20u /* dsa_prefill's tensor-core kernel and paged_decode_mx4: a
+                                        CTA gave up waiting (about a second) for its own
+                                        asynchronous copies or tensor-core products; its
+                                        outputs are NaN                                    */
 
 #define I8KV_FLAG_BAD_POSITION 0x40u /* rope_and_cache: a position outside [0, max_pos): that token
                                         was skipped                                         */
@@ -162,8 +163,8 @@ size_t split_workspace_bytes(int32_t units, int32_t num_splits, int32_t G, int32
  *   device); granule = 64 (POW2_TILES) or 16 (WAVE); min_chunk = 128;
  *   mode I8KV_GEOM_BALANCED (paged path only, else I8KV_EUNSUPPORTED):
  *   num_splits = min(32, max(2, 2 x the WAVE rule's automatic count)) partial
- *   slots and chunk = 0, for paged_decode's balanced pieces (an MX4 cache with
- *   cap <= 256: one split);
+ *   slots and chunk = 0, for paged_decode's balanced pieces (for an MX4 cache 1,
+ *   2, 4 or 8 where spans are short: see paged_decode_mx4);
  *   max_splits = I8KV_MAX_SPLITS.  For the paged path in WAVE mode with
  *   override_value 0 the chunk is then moved to the multiple of one round of
  *   the paged kernel's CTA (4 warps x its step: 128 positions for an int8 or
@@ -511,13 +512,18 @@ i8kv_status gather_cache(const int32_t* slot_mapping, int32_t num_rows, int32_t 
  *   cache        [num_blocks, Hkv, block_size / 16, 18 * D] (see above)
  *   num_splits, chunk  as for paged_decode; num_splits = 0: automatic, the values
  *                of decode_plan(I8KV_PATH_PAGED, I8KV_CACHE_MX4,
- *                I8KV_WINDOW_SPAN(cap, window), ..., I8KV_GEOM_BALANCED): one split
- *                for a short span, else balanced pieces (chunk 0).  Balanced pieces
- *                take any batch size here: the live lengths are cut on the device
- *                into pieces of about equal length, about one occupancy wave of
- *                them over the batch, at most num_splits per row.
- *   other arguments as for paged_decode_ex, without slots_out; the partials in
- *   the workspace have the same layout.
+ *                I8KV_WINDOW_SPAN(cap, window), ..., I8KV_GEOM_BALANCED).
+ *                One split, and balanced pieces (chunk 0) of 2, 4 or 8 slots for
+ *                few rows and out given, run as one kernel: a CTA, or a cluster
+ *                of num_splits CTAs, per row and KV head, which deals the row's
+ *                tiles out in turn and joins in shared memory; the workspace is
+ *                not written then.  Other balanced pieces take any batch size:
+ *                the live lengths are cut on the device into pieces of about
+ *                equal length, about one occupancy wave of them over the batch,
+ *                at most num_splits per row, and the combine kernel joins them.
+ *   other arguments as for paged_decode_ex, without slots_out; partials in the
+ *   workspace have the same layout (a workspace of their size is asked for
+ *   whenever num_splits > 1).
  * Numerics: the K and V values of the cache are exact in the fp16 products;
  * Q * k_scale is rounded to fp16 with one power of two per head taken out (per
  * channel scales; a scale per tensor is applied to the fp32 scores), so its

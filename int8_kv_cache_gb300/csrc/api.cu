@@ -81,6 +81,7 @@ cudaError_t launch_key(const KernelKey& key, const DecodeParams& p, cudaStream_t
     return key.p_lo ? i8kv::launch_dsa_decode(key, p, s, info)
                     : i8kv::launch_dsa_prefill(key, p, s, info);
   }
+  if (key.cluster) return i8kv::launch_paged_mx4_cluster(key, p, s, info);
   if (key.mx4_cache) return i8kv::launch_paged_mx4(key, p, s, info);
   if (key.fp16_cache) return i8kv::launch_paged_fp16(key, p, s, info);
   if (key.fp8_cache) return i8kv::launch_paged_fp8(key, p, s, info);
@@ -103,7 +104,7 @@ i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
   if (e != cudaSuccess) return cuda_fail(e);
   const auto k = std::make_tuple(dev, static_cast<int>(key.path), key.D, key.nt,
                                  static_cast<int>(key.fp16_cache), static_cast<int>(key.fp8_cache),
-                                 static_cast<int>(key.p_lo), static_cast<int>(key.mx4_cache));
+                                 static_cast<int>(key.p_lo), key.mx4_cache + 2 * key.cluster);
   {
     std::lock_guard<std::mutex> lock(mu);
     auto it = cache.find(k);
@@ -211,18 +212,48 @@ i8kv_status plan(const KernelKey& key, int64_t cap, int32_t units, int32_t mode,
   return I8KV_OK;
 }
 
-// The automatic geometry of the MX4 decode, from the wave rule's count *ns: one
-// split where a row's span is short (the join would cost more than it spreads),
-// else balanced pieces with twice the count as partial slots.
-constexpr int64_t kMx4OneSplit = 256;
-void mx4_auto(int64_t span, int32_t units, int32_t* ns, int32_t* chunk) {
-  if (span <= kMx4OneSplit) {
-    *ns = 1;
-    *chunk = static_cast<int32_t>(std::max<int64_t>(16, cdiv(span, 16) * 16));
-    return;
+// Resident CTAs of the MX4 decode's cluster kernel (the key with `cluster` set).
+i8kv_status cluster_wave(KernelKey key, int32_t* wave) {
+  key.cluster = true;
+  WaveInfo w{0, 0};
+  const i8kv_status st = wave_of(key, &w);
+  *wave = w.wave;
+  return st;
+}
+
+// The automatic geometry of the MX4 decode, from the wave rule's count *ns.  A
+// row and KV head is one CTA of 8 warps, or a cluster of 2, 4 or 8 of them that join
+// without a second kernel, where that gives a warp at most 8 tiles of 16 tokens and
+// all clusters are resident at once; the fewest CTAs that leave a warp 2 tiles.
+// Longer spans, where the second kernel (about 3 us) is less than the
+// imbalance of equal clusters: balanced pieces, twice the wave rule's count as
+// partial slots.
+constexpr int64_t kMx4WarpTiles = 8;
+i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t* ns,
+                     int32_t* chunk) {
+  int32_t wave = 0;
+  const i8kv_status st = cluster_wave(key, &wave);
+  if (st != I8KV_OK) return st;
+  const int64_t tiles = cdiv(span, 16);
+  int32_t c = 1;
+  while (c < i8kv::kMx4MaxCluster && c * i8kv::kMx4ClusterWarps * 2 < tiles &&
+         2LL * c * units <= wave)
+    c *= 2;
+  if (tiles <= kMx4WarpTiles * i8kv::kMx4ClusterWarps * c) {
+    *ns = c;
+    *chunk = c > 1 ? 0 : static_cast<int32_t>(std::max<int64_t>(16, tiles * 16));
+    return I8KV_OK;
   }
   *ns = std::min<int32_t>(I8KV_MAX_SPLITS, std::max<int32_t>(2, 2 * *ns));
   *chunk = 0;
+  return I8KV_OK;
+}
+
+// Whether balanced pieces of the MX4 decode run as clusters: a cluster's size, and
+// all of them resident at once.
+bool mx4_clusters(int32_t units, int32_t ns, int32_t wave) {
+  return ns <= i8kv::kMx4MaxCluster && (ns & (ns - 1)) == 0 &&
+         static_cast<int64_t>(units) * ns <= wave;
 }
 
 // Geometry given by the caller: num_splits in [1, 32], chunk a positive
@@ -400,7 +431,7 @@ i8kv_status decode_plan(int32_t path, int32_t cache_dtype, int64_t cap, int32_t 
     if ((st = plan(key, cap, units, I8KV_GEOM_WAVE, 0, num_splits, chunk, wave_ctas)) != I8KV_OK)
       return st;
     if (key.mx4_cache) {
-      mx4_auto(cap, units, num_splits, chunk);
+      if ((st = mx4_auto(key, cap, units, num_splits, chunk)) != I8KV_OK) return st;
       *workspace_bytes = split_workspace_bytes(rows * Hkv, *num_splits, G, D);
       return I8KV_OK;
     }
@@ -684,7 +715,7 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
   if (num_splits == 0) {
     st = plan(key, span, units, I8KV_GEOM_WAVE, 0, &num_splits, &chunk, nullptr);
     if (st != I8KV_OK) return st;
-    mx4_auto(span, units, &num_splits, &chunk);
+    if ((st = mx4_auto(key, span, units, &num_splits, &chunk)) != I8KV_OK) return st;
   }
   DecodeParams p{};
   p.balanced = num_splits > 1 && chunk == 0;
@@ -722,11 +753,22 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
   p.sigma = softmax_scale;
   p.softcap = softcap;
   p.window = window;
+  // one split, and balanced pieces that fit clusters, join inside the kernel
+  bool cluster = num_splits == 1;
   if (p.balanced) {
+    int32_t resident = 0;
+    if ((st = cluster_wave(key, &resident)) != I8KV_OK) return st;
+    cluster = out != nullptr && mx4_clusters(units, num_splits, resident);
     WaveInfo w{0, 0};
     if ((st = wave_of(key, &w)) != I8KV_OK) return st;
     // (at least one piece per row and KV head, and one to spare)
     p.bal_pieces = std::max(w.wave, units + std::max(w.wave / 2, Hkv));
+  }
+  if (cluster) {
+    KernelKey ckey = key;
+    ckey.cluster = true;
+    const cudaError_t e = launch_key(ckey, p, static_cast<cudaStream_t>(stream), nullptr);
+    return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
   }
   return run(key, p, static_cast<cudaStream_t>(stream));
 }

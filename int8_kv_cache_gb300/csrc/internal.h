@@ -60,7 +60,8 @@ struct KernelKey {
   bool fp16_cache;
   bool fp8_cache;  // float8 e4m3fn codes (same tile as int8, other conversion)
   bool p_lo;       // probability tile as fp16 high + low parts
-  bool mx4_cache = false;  // 4-bit records (mx4_decode.cu; DecodeParams::k is the record cache)
+  bool mx4_cache = false;  // 4-bit records (mx4_kernel.cuh; DecodeParams::k is the record cache)
+  bool cluster = false;    // mx4_cache: a cluster of num_splits CTAs per (row, KV head)
 };
 
 // What the geometry needs to know of a decode kernel instantiation.
@@ -85,6 +86,10 @@ cudaError_t launch_paged_fp8(const KernelKey& key, const DecodeParams& p, cudaSt
 
 cudaError_t launch_paged_mx4(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                              KernelInfo* info);
+cudaError_t launch_paged_mx4_cluster(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
+                                     KernelInfo* info);
+constexpr int kMx4MaxCluster = 8;  // CTAs of a portable cluster
+constexpr int kMx4ClusterWarps = 8;
 
 // rope_and_cache and gather_cache (append.cu); the cache type picks the kernel.
 struct AppendParams {

@@ -1,718 +1,10 @@
-// Paged decode over an MX4 cache (4-bit e2m1 codes, an e4m3 scale per 16
-// channels): one new token per sequence, split over the cache's length; the
-// partials are joined by the combine kernel.
-//
-//   s_t = sigma * k_scale * sum_d q_d * (block scale * code)_t,d   (softcap, mask)
-//   partial of a piece: m = max s_t, l = sum e^(s_t - m), acc = v_scale sum e^(s_t - m) v_t
-//
-// One warp per query head, lanes over channels, fp32 throughout.
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
-#include <atomic>
-
-#include "../../include/int8kv.h"
-#include "codes.cuh"
-#include "device.cuh"
-#include "internal.h"
-#include "tc.cuh"
+// Instantiations of the MX4 decode: 4-warp CTAs over pieces (or chunks) of rows, whose
+// partials the combine kernel joins.
+#include "mx4_kernel.cuh"
 
 namespace i8kv {
-
-namespace {
-
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kMinTiles = 4;  // tiles of 16 tokens per piece at least
-
-struct Mx4Item {
-  int unit, row, g, slot;
-  int lo, hi;    // positions of the piece; lo a multiple of 16
-  int wlo;       // first attended position (sliding window)
-  int pieces;    // pieces of this row (balanced), or 0
-  bool valid;
-};
-
-// Live range of row r: [wlo, len), cut from base = wlo rounded down to 16.
-__device__ __forceinline__ int tiles_of(const DecodeParams& p, int r, int cap, int& len, int& wlo) {
-  len = min(max(p.seq_lens[r], 0), cap);
-  wlo = p.window >= 0 ? max(0, len - 1 - p.window) : 0;
-  return len > 0 ? ((len + 15) >> 4) - (wlo >> 4) : 0;
-}
-
-// Balanced pieces.  With t_b the 16-token tiles of row b's live range, S the
-// partial slots of a row and P the pieces the grid has room for (one occupancy
-// wave of CTAs, or U + half a wave where the U = B * Hkv rows and heads are more
-// than that), every row is cut into n_b = clamp(ceil(t_b / L), 1, S) pieces of
-// ceil(t_b / n_b) tiles, with the smallest L >= kMinTiles for which the pieces
-// number at most P (found by bisection: sum t_b Hkv / P is a lower bound, sum t_b
-// Hkv / (P - U) always does).  The grid follows from the arguments alone; CTAs
-// past the last piece return.  Item c: rows in order, a row's pieces in order, the
-// KV heads of a piece next to each other.
-__device__ Mx4Item balanced_piece(const DecodeParams& p, int c) {
-  const int lane = threadIdx.x & 31;
-  const int B = p.rows, Hkv = p.Hkv, S = p.num_splits;
-  const int cap = p.max_blocks * p.bs;
-  int len, wlo;
-  const int t0 = lane < B ? tiles_of(p, lane, cap, len, wlo) : 0;  // the only rows if B <= 32
-  long long tot = t0;
-  for (int r = 32 + lane; r < B; r += 32) tot += tiles_of(p, r, cap, len, wlo);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
-  const int room = p.bal_pieces / Hkv;  // pieces of one KV head (> B)
-  // bisection in units of kMinTiles (one tile per warp)
-  int lo = max(1, (int)((tot + (long long)room * kMinTiles - 1) / ((long long)room * kMinTiles)));
-  int up = max(lo, (int)((tot + (long long)(room - B) * kMinTiles - 1) / ((long long)(room - B) * kMinTiles)));
-  while (lo < up) {
-    const int mid = (lo + up) >> 1, len_mid = mid * kMinTiles;
-    int n = lane < B ? min(max((t0 + len_mid - 1) / len_mid, 1), S) : 0;
-    for (int r = 32 + lane; r < B; r += 32)
-      n += min(max((tiles_of(p, r, cap, len, wlo) + len_mid - 1) / len_mid, 1), S);
-    n = __reduce_add_sync(0xffffffffu, n);
-    if (n <= room)
-      up = mid;
-    else
-      lo = mid + 1;
-  }
-  const int L = lo * kMinTiles;
-  long long base = 0;
-  for (int r0 = 0; r0 < B; r0 += 32) {
-    const int r = r0 + lane;
-    int t = 0, n = 0;
-    len = wlo = 0;
-    if (r < B) {
-      t = tiles_of(p, r, cap, len, wlo);
-      n = min(max((t + L - 1) / L, 1), S);
-    }
-    const int per = t > 0 ? (t + n - 1) / n : 0;  // tiles per piece
-    if (t > 0) n = (t + per - 1) / per;           // (no empty last pieces)
-    int inc = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int v = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc += v;
-    }
-    const int total = __shfl_sync(0xffffffffu, inc, 31);
-    if (c < (base + total) * Hkv) {
-      const int q = (int)(c - base * Hkv);  // item among these rows
-      const int piece = q / Hkv;
-      const unsigned m = __ballot_sync(0xffffffffu, piece < inc);
-      const int src = __ffs(m) - 1;
-      Mx4Item it;
-      const int n_s = __shfl_sync(0xffffffffu, n, src);
-      const int inc_s = __shfl_sync(0xffffffffu, inc, src);
-      const int per_s = __shfl_sync(0xffffffffu, per, src);
-      const int len_s = __shfl_sync(0xffffffffu, len, src);
-      it.wlo = __shfl_sync(0xffffffffu, wlo, src);
-      it.row = r0 + src;
-      it.g = q - piece * Hkv;
-      it.slot = piece - (inc_s - n_s);
-      it.unit = it.row * Hkv + it.g;
-      it.lo = (it.wlo & ~15) + it.slot * per_s * 16;
-      it.hi = min(it.lo + per_s * 16, len_s);
-      it.pieces = n_s;
-      it.valid = true;
-      return it;
-    }
-    base += total;
-  }
-  Mx4Item none{};
-  none.valid = false;
-  return none;
-}
-
-__device__ Mx4Item item_of(const DecodeParams& p, int c) {
-  if (p.balanced) return balanced_piece(p, c);
-  const int units = p.rows * p.Hkv;
-  const int cap = p.max_blocks * p.bs;
-  Mx4Item it;
-  it.slot = c / units;
-  it.unit = c - it.slot * units;
-  it.row = it.unit / p.Hkv;
-  it.g = it.unit - it.row * p.Hkv;
-  int len;
-  tiles_of(p, it.row, cap, len, it.wlo);
-  it.lo = (it.wlo & ~15) + it.slot * p.chunk;
-  it.hi = min(min(it.lo + p.chunk, cap), len);
-  it.pieces = 0;
-  it.valid = true;
-  return it;
-}
-
-// Shape of the kernel for head dimension D and NT groups of 8 query heads.
-template <int D, int NT>
-struct Mx4Tile {
-  static constexpr int kRec = 18 * D;                    // bytes of a 16-token record
-  static constexpr int kSub = D <= 128 ? 2 : 1;          // records per stage
-  static constexpr int kStages = 2 * (3 - kSub);         // ring depth per warp: 4 records
-  static constexpr int kStageBytes = kSub * kRec;
-  static constexpr int kRing = kStages * kStageBytes;    // a multiple of 128
-  static constexpr int kRow = D + 4;                     // floats of a merged row (padded)
-  static constexpr int kMerge = 8 * NT * kRow * 4;       // a warp's rows, in its ring
-  static constexpr int kBars = kWarps * kRing;           // mbarriers [warps][stages]
-  static constexpr int kMasks = kBars + kWarps * kStages * 8;      // [warps][stages][sub]
-  static constexpr int kScal = kMasks + kWarps * kStages * kSub * 4;  // [2][warps][16]
-  static constexpr int kQRow = D + 8;                    // halves of a staged query row (padded)
-  static constexpr int kQ = kScal + 2 * kWarps * 16 * 4;           // [8 NT][kQRow] fp16
-  static constexpr int kInv = kQ + 8 * NT * kQRow * 2;             // [16] score factors
-  static constexpr int kSmem = kInv + 16 * 4;
-  // resident CTAs per SM the registers are cut for
-  static constexpr int kBlocks = D * NT >= 512 ? 2 : D * NT >= 256 ? 3 : D * NT >= 128 ? 4 : 5;
-  static_assert(kMerge <= kRing, "the merge fits the ring");
-};
-
-__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
-  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&b));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
-
-template <int N>  // 4 N bytes
-__device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
-  if constexpr (N == 1) {
-    asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(w[0]) : "r"(addr));
-  } else if constexpr (N == 2) {
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];\n" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; i += 4)
-      asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n"
-                   : "=r"(w[i]), "=r"(w[i + 1]), "=r"(w[i + 2]), "=r"(w[i + 3])
-                   : "r"(addr + 4 * i));
-  }
-}
-__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];\n" : "=r"(v) : "r"(addr));
-  return v;
-}
-__device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
-  uint32_t v;
-  asm volatile("ld.shared.u16 %0, [%1];\n" : "=r"(v) : "r"(addr));
-  return v;
-}
-
-constexpr float kUnset = -3.0e38f;  // exponent base of a head without a score yet
-constexpr float kHead = 15.f;       // log2 of the largest probability the fp16 tile takes
-constexpr float kRoom = 8.f;        // log2 of the largest one right after the base is set
-
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, (Mx4Tile<D, NT>::kBlocks))
-mx4_decode_kernel(const DecodeParams p) {
-  using T = Mx4Tile<D, NT>;
-  constexpr int KC = D / 16;   // MMA steps of QK^T, and 16-channel tiles of PV
-  constexpr int KW = D / 32;   // 32-bit words of a lane's key channels (D / 4 of a token)
-  constexpr int VW = D / 64;   // and of its value channels (D / 8 of a token)
-  extern __shared__ __align__(128) uint8_t smem[];
-  grid_dependency_wait();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int grp = lane >> 2, tig = lane & 3;
-  const int G = p.G;
-  const Mx4Item it = item_of(p, blockIdx.x);
-  if (!it.valid) return;
-
-  // ---- the warp's records: tile j of the warp is tile warp + kWarps j of the piece; lane
-  // j % 32 holds where it is and copies it in ----
-  const int tiles = it.hi > it.lo ? (it.hi - it.lo + 15) >> 4 : 0;
-  const int mine = tiles > warp ? (tiles - warp + kWarps - 1) / kWarps : 0;
-  const int rpb = p.bs >> 4;  // records per block
-  const uint8_t* cache = static_cast<const uint8_t*>(p.k);
-  auto locate = [&](int j) -> long long {  // byte offset of tile j's record, -1: none
-    if (j >= mine) return -1;
-    const int tile = (it.lo >> 4) + warp + kWarps * j;
-    const int b = p.bs_log2 >= 4 ? tile >> (p.bs_log2 - 4) : tile / rpb;
-    const int blk = __ldg(p.block_table + (long long)it.row * p.max_blocks + b);
-    if (blk < 0 || (long long)blk >= p.cache_rows) {
-      flag_or(p.flags, I8KV_FLAG_BAD_BLOCK);
-      return -1;
-    }
-    return (((long long)blk * p.Hkv + it.g) * rpb + (tile - b * rpb)) * T::kRec;
-  };
-  const uint32_t ring = smem_addr(smem + warp * T::kRing);
-  const uint32_t bars = smem_addr(smem + T::kBars) + warp * T::kStages * 8;
-  int* masks = reinterpret_cast<int*>(smem + T::kMasks) + warp * T::kStages * T::kSub;
-  long long cur = locate(lane), nxt = locate(32 + lane);
-  const int stages = (mine + T::kSub - 1) / T::kSub;
-  auto issue = [&](int k) {  // stage k into its slot of the ring
-    if (k >= stages) return;
-    const int j0 = k * T::kSub;
-    if (j0 > 0 && (j0 & 31) == 0) {
-      cur = nxt;
-      nxt = locate(j0 + 32 + lane);
-    }
-    const int s = lane - (j0 & 31);
-    if (s >= 0 && s < T::kSub) {
-      const int st = k % T::kStages;
-      const uint32_t bar = bars + st * 8;
-      int mask = 0;  // attended tokens (stored before the arrival that publishes it)
-      if (cur >= 0) {
-        const int pos = it.lo + 16 * (warp + kWarps * (j0 + s));
-        mask = it.hi - pos >= 16 ? 0xFFFF : (1 << (it.hi - pos)) - 1;
-        if (pos < it.wlo) mask &= 0xFFFF << (it.wlo - pos);
-      }
-      masks[st * T::kSub + s] = mask;
-      if (cur >= 0) {
-        tc::mbar_arrive_expect_tx(bar, T::kRec);
-        tc::bulk_g2s(ring + st * T::kStageBytes + s * T::kRec, cache + cur, T::kRec, bar);
-      } else {
-        tc::mbar_arrive(bar);
-      }
-    }
-  };
-  if (lane == 0) {
-#pragma unroll
-    for (int i = 0; i < T::kStages; ++i) tc::mbar_init(bars + 8 * i, T::kSub);
-    tc::fence_mbar_init();
-  }
-  __syncwarp();
-#pragma unroll
-  for (int k = 0; k < T::kStages; ++k) issue(k);
-
-  if (it.slot == 0 && threadIdx.x == 0 && it.g == 0) {
-    const int live = p.seq_lens[it.row];
-    if (live < 0 || live > p.max_blocks * p.bs) flag_or(p.flags, I8KV_FLAG_LEN_CLAMPED);
-  }
-  // slots that no piece fills: empty
-  if (it.pieces > 0 && it.slot == 0) {
-    for (int e = threadIdx.x; e < (p.num_splits - it.pieces) * G; e += kThreads) {
-      const long long b = ((long long)it.unit * p.num_splits + it.pieces) * G + e;
-      p.ws_m[b] = neg_inf();
-      p.ws_l[b] = 0.f;
-    }
-  }
-
-  // ---- the group's queries, scales folded in, staged in shared memory: 8 channels of a head
-  // per thread and pass ----
-  __half* sq = reinterpret_cast<__half*>(smem + T::kQ);
-  float* sinv = reinterpret_cast<float*>(smem + T::kInv);
-#pragma unroll
-  for (int e = threadIdx.x; e < D * NT; e += kThreads) {
-    const int h = e / (D / 8), d = 8 * (e % (D / 8));
-    uint4 v = make_uint4(0u, 0u, 0u, 0u);
-    if (h < G)
-      v = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) +
-                                          ((long long)it.row * p.Hq + it.g * G + h) * D + d);
-    float inv = 1.f;
-    if (p.per_channel) {
-      // one power of two per head taken out, so that the largest element is in
-      // [2^8, 2^9): nothing overflows fp16, and what goes below its normal range is
-      // less than 2^-22 of the largest
-      const float4 k0 = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d);
-      const float4 k1 = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d + 4);
-      const __half2* q2 = reinterpret_cast<const __half2*>(&v);
-      const float2 a0 = __half22float2(q2[0]), a1 = __half22float2(q2[1]);
-      const float2 a2 = __half22float2(q2[2]), a3 = __half22float2(q2[3]);
-      const float x[8] = {a0.x * k0.x, a0.y * k0.y, a1.x * k0.z, a1.y * k0.w,
-                          a2.x * k1.x, a2.y * k1.y, a3.x * k1.z, a3.y * k1.w};
-      float amax = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) amax = fmaxf(amax, fabsf(x[i]));
-#pragma unroll
-      for (int o = 1; o < D / 8; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      const int ex = __float_as_int(amax) >> 23;  // biased exponent (amax >= 0)
-      const bool scaled = ex >= 9 && ex < 255;
-      const float up = scaled ? __int_as_float((262 - ex) << 23) : 1.f;
-      inv = scaled ? __int_as_float((ex - 8) << 23) : 1.f;
-      v = make_uint4(pack_h2(x[0] * up, x[1] * up), pack_h2(x[2] * up, x[3] * up),
-                     pack_h2(x[4] * up, x[5] * up), pack_h2(x[6] * up, x[7] * up));
-    } else {
-      inv = p.k_scale[0];
-    }
-    *reinterpret_cast<uint4*>(sq + h * T::kQRow + d) = v;
-    // accumulator -> score in log2 units (natural units with a softcap)
-    if (d == 0) sinv[h] = inv * (p.softcap > 0.f ? p.sigma : p.sigma * kLog2e);
-  }
-  __syncthreads();
-  // B operand of step i: channels 4i, 4i+1 and 4i+2, 4i+3 of the lane's part, which starts
-  // at channel tig D/4 of head grp (+ 8); the lane's score columns are heads 2 tig, 2 tig + 1
-  uint32_t qf[NT][KC][2];
-  float fac[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const uint4* src = reinterpret_cast<const uint4*>(sq + (grp + 8 * nt) * T::kQRow + tig * (D / 4));
-#pragma unroll
-    for (int i = 0; i < KC / 2; ++i) {
-      const uint4 v = src[i];
-      qf[nt][2 * i][0] = v.x;
-      qf[nt][2 * i][1] = v.y;
-      qf[nt][2 * i + 1][0] = v.z;
-      qf[nt][2 * i + 1][1] = v.w;
-    }
-    fac[nt][0] = sinv[8 * nt + 2 * tig];
-    fac[nt][1] = sinv[8 * nt + 2 * tig + 1];
-  }
-
-  float acc[KC][NT][4];
-  float base[NT][2], lrun[NT][2];
-#pragma unroll
-  for (int t = 0; t < KC; ++t)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[t][nt][e] = 0.f;
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      base[nt][j] = kUnset;
-      lrun[nt][j] = 0.f;
-    }
-  // score row r of a tile (0..7; +8 below) is token (r >> 1) + 4 (r & 1), so that a lane's
-  // contraction indices 2tig, 2tig+1, 2tig+8, 2tig+9 in PV are tokens tig + 0, 4, 8, 12
-  const int tok = (grp >> 1) + 4 * (grp & 1);
-  const uint32_t k_off = tok * (D / 2) + tig * (D / 8);
-  const uint32_t ks_off = 8 * D + tok * (D / 16) + tig * (D / 64);
-  const uint32_t v_off = 9 * D + tig * (D / 2) + grp * (D / 16);
-  const uint32_t vs_off = 17 * D + tig * (D / 16) + (grp * D) / 128;
-  const float cap_k = 2.f * kLog2e / p.softcap;  // used only when softcap > 0
-  bool timeout = false;
-
-  int k = 0;
-  for (; k < stages; ++k) {
-    const int st = k % T::kStages;
-    const bool ok = tc::mbar_wait(bars + st * 8, (k / T::kStages) & 1);
-    if (!__all_sync(0xffffffffu, ok)) {
-      timeout = true;
-      break;
-    }
-    const uint32_t rec0 = ring + st * T::kStageBytes;
-
-    // ---- S = K Q'^T, one 16-token tile at a time ----
-    float sc[T::kSub][NT][4];
-#pragma unroll
-    for (int s = 0; s < T::kSub; ++s) {
-      const uint32_t r = rec0 + s * T::kRec;
-      uint32_t wa[KW], wb[KW];
-      lds<KW>(r + k_off, wa);
-      lds<KW>(r + k_off + 8 * (D / 2), wb);
-      // block scales of the lane's channels (D / 64 of a token), each as an fp16 pair
-      constexpr int KB = D / 64;
-      uint32_t fa[KB < 2 ? 2 : KB], fb[KB < 2 ? 2 : KB];
-      if constexpr (D == 64) {
-        e4m3x4_to_h2x2(lds_u8(r + ks_off) * 0x0101u, fa[0], fa[1]);
-        e4m3x4_to_h2x2(lds_u8(r + ks_off + 8 * (D / 16)) * 0x0101u, fb[0], fb[1]);
-      } else if constexpr (D == 128) {
-        e4m3x4_to_h2x2(prmt(lds_u16(r + ks_off), 0u, 0x1100u), fa[0], fa[1]);
-        e4m3x4_to_h2x2(prmt(lds_u16(r + ks_off + 8 * (D / 16)), 0u, 0x1100u), fb[0], fb[1]);
-      } else {
-        uint32_t x[1];
-        lds<1>(r + ks_off, x);
-        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x1100u), fa[0], fa[1]);
-        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x3322u), fa[2], fa[3]);
-        lds<1>(r + ks_off + 8 * (D / 16), x);
-        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x1100u), fb[0], fb[1]);
-        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x3322u), fb[2], fb[3]);
-      }
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[s][nt][e] = 0.f;
-#pragma unroll
-      for (int w = 0; w < KW; ++w) {  // 8 channels of a lane: two steps
-        uint32_t a[4], b[4];
-        e2m1x8_to_h2x4(wa[w], a[0], a[1], a[2], a[3]);
-        e2m1x8_to_h2x4(wb[w], b[0], b[1], b[2], b[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          a[i] = hmul2(a[i], fa[w / 2]);
-          b[i] = hmul2(b[i], fb[w / 2]);
-        }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma16816(sc[s][nt], a[0], b[0], a[1], b[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
-          mma16816(sc[s][nt], a[2], b[2], a[3], b[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
-        }
-      }
-    }
-
-    // ---- online softmax: the exponent base of a head moves only when a score leaves the
-    // range that the fp16 probabilities cover ----
-    int mask[T::kSub];
-#pragma unroll
-    for (int s = 0; s < T::kSub; ++s) mask[s] = masks[st * T::kSub + s];
-    // z: scores less the head's base, in log2 units
-    float z[T::kSub][NT][4];
-    auto scores_less_base = [&]() {
-      if (p.softcap > 0.f) {
-#pragma unroll
-        for (int s = 0; s < T::kSub; ++s)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              z[s][nt][e] = fmaf(soft_cap(sc[s][nt][e] * fac[nt][e & 1], p.softcap, cap_k), kLog2e,
-                                 -base[nt][e & 1]);
-      } else {
-#pragma unroll
-        for (int s = 0; s < T::kSub; ++s)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              z[s][nt][e] = fmaf(sc[s][nt][e], fac[nt][e & 1], -base[nt][e & 1]);
-      }
-#pragma unroll
-      for (int s = 0; s < T::kSub; ++s) {
-        if (mask[s] != 0xFFFF) {  // uniform
-          const bool upper = (mask[s] >> tok) & 1, lower = (mask[s] >> (tok + 8)) & 1;
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            if (!upper) z[s][nt][0] = z[s][nt][1] = neg_inf();
-            if (!lower) z[s][nt][2] = z[s][nt][3] = neg_inf();
-          }
-        }
-      }
-    };
-    scores_less_base();
-    float top = neg_inf();
-#pragma unroll
-    for (int s = 0; s < T::kSub; ++s)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) top = fmaxf(top, z[s][nt][e]);
-    if (__any_sync(0xffffffffu, top > kHead)) {
-      float old[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          old[nt][j] = base[nt][j];
-          if (base[nt][j] == kUnset) base[nt][j] = 0.f;  // (kUnset would swallow the score)
-        }
-      scores_less_base();
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float alpha[2];
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float mx = neg_inf();
-#pragma unroll
-          for (int s = 0; s < T::kSub; ++s) mx = fmaxf(mx, fmaxf(z[s][nt][j], z[s][nt][2 + j]));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const bool unset = old[nt][j] == kUnset;
-          // up by what the largest is above the room left, down too on the first score
-          const float up = unset ? mx - kRoom : fmaxf(mx - kRoom, 0.f);
-          alpha[j] = unset ? 0.f : fast_exp2(-up);
-          base[nt][j] = unset && mx == neg_inf() ? kUnset : base[nt][j] + up;
-        }
-        lrun[nt][0] *= alpha[0];
-        lrun[nt][1] *= alpha[1];
-#pragma unroll
-        for (int t = 0; t < KC; ++t) {
-          acc[t][nt][0] *= alpha[0];
-          acc[t][nt][2] *= alpha[0];
-          acc[t][nt][1] *= alpha[1];
-          acc[t][nt][3] *= alpha[1];
-        }
-      }
-      scores_less_base();
-    }
-    uint32_t ph[T::kSub][NT][2];
-#pragma unroll
-    for (int s = 0; s < T::kSub; ++s)
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          pr[e] = fast_exp2(z[s][nt][e]);
-          lrun[nt][e & 1] += pr[e];
-        }
-        ph[s][nt][0] = movm_t(pack_h2(pr[0], pr[1]));
-        ph[s][nt][1] = movm_t(pack_h2(pr[2], pr[3]));
-      }
-
-    // ---- O^T += V^T P^T: rows are the channels of group grp, D / 8 from grp D / 8 ----
-#pragma unroll
-    for (int s = 0; s < T::kSub; ++s) {
-      const uint32_t r = rec0 + s * T::kRec;
-      uint32_t v[4][VW];  // tokens tig, tig + 4, tig + 8, tig + 12
-      uint32_t x[4];      // their block scales
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        lds<VW>(r + v_off + i * 4 * (D / 2), v[i]);
-        if constexpr (D == 256) {
-          x[i] = lds_u16(r + vs_off + i * 4 * (D / 16));
-        } else {
-          x[i] = lds_u8(r + vs_off + i * 4 * (D / 16));
-        }
-      }
-      if (mask[s] != 0xFFFF) {  // a token that is not attended: nothing of its bytes counts
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (!((mask[s] >> (tig + 4 * i)) & 1)) x[i] = 0u;
-      }
-      // scales of token pairs (0, 1) and (2, 3) for each block of the lane's channels
-      uint32_t s01[2], s23[2];
-      if constexpr (D == 256) {
-        e4m3x4_to_h2x2(prmt(x[0], x[1], 0x5140u), s01[0], s01[1]);
-        e4m3x4_to_h2x2(prmt(x[2], x[3], 0x5140u), s23[0], s23[1]);
-      } else {
-        const uint32_t y = prmt(x[0] | (x[1] << 8), x[2] | (x[3] << 8), 0x5410u);
-        e4m3x4_to_h2x2(y, s01[0], s23[0]);
-      }
-#pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const int blk = w / 2;
-        // nibble pairs (token 0, token 1) of the even and of the odd channels
-        uint32_t e01[4], o01[4], e23[4], o23[4];
-        e2m1x8_to_h2x4((v[0][w] & 0x0F0F0F0Fu) | ((v[1][w] << 4) & 0xF0F0F0F0u), e01[0], e01[1], e01[2], e01[3]);
-        e2m1x8_to_h2x4(((v[0][w] >> 4) & 0x0F0F0F0Fu) | (v[1][w] & 0xF0F0F0F0u), o01[0], o01[1], o01[2], o01[3]);
-        e2m1x8_to_h2x4((v[2][w] & 0x0F0F0F0Fu) | ((v[3][w] << 4) & 0xF0F0F0F0u), e23[0], e23[1], e23[2], e23[3]);
-        e2m1x8_to_h2x4(((v[2][w] >> 4) & 0x0F0F0F0Fu) | (v[3][w] & 0xF0F0F0F0u), o23[0], o23[1], o23[2], o23[3]);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t a0 = hmul2(e01[i], s01[blk]), a1 = hmul2(o01[i], s01[blk]);
-          const uint32_t a2 = hmul2(e23[i], s23[blk]), a3 = hmul2(o23[i], s23[blk]);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-            mma16816(acc[4 * w + i][nt], a0, a1, a2, a3, ph[s][nt][0], ph[s][nt][1]);
-        }
-      }
-    }
-    __syncwarp();  // every lane has read the stage
-    issue(k + T::kStages);
-  }
-  if (timeout) {
-    // the copies still in flight must not land in memory that others use
-    if (lane == 0) flag_or(p.flags, I8KV_FLAG_WAIT_TIMEOUT);
-    for (int i = k; i < min(k + T::kStages, stages); ++i)
-      tc::mbar_wait(bars + (i % T::kStages) * 8, (i / T::kStages) & 1);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) lrun[nt][0] = lrun[nt][1] = __int_as_float(0x7fc00000);
-  }
-
-  // ---- merge the warps: rows [head][channel] in each warp's ring, then one sum ----
-  float* bw = reinterpret_cast<float*>(smem + T::kScal);  // [warps][16] exponent bases
-  float* lw = bw + kWarps * 16;                           // [warps][16] sums
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      float l = lrun[nt][j];
-      l += __shfl_xor_sync(0xffffffffu, l, 4);
-      l += __shfl_xor_sync(0xffffffffu, l, 8);
-      l += __shfl_xor_sync(0xffffffffu, l, 16);
-      const int h = nt * 8 + 2 * tig + j;
-      if (grp == 0) {
-        bw[warp * 16 + h] = base[nt][j];
-        lw[warp * 16 + h] = l;
-      }
-      if (h < G) {
-        float* row = reinterpret_cast<float*>(smem + warp * T::kRing) + h * T::kRow + grp * (D / 8);
-#pragma unroll
-        for (int t = 0; t < KC; t += 2)
-          *reinterpret_cast<float4*>(row + 2 * t) =
-              make_float4(acc[t][nt][j], acc[t][nt][2 + j], acc[t + 1][nt][j], acc[t + 1][nt][2 + j]);
-      }
-    }
-  // the join may be launched now: its CTAs wait for this grid's writes
-  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-  __syncthreads();
-  const bool direct = p.num_splits == 1;
-  const long long head0 = (long long)it.row * p.Hq + it.g * G;
-  const long long part0 = ((long long)it.unit * p.num_splits + it.slot) * G;
-  for (int e = threadIdx.x; e < G * (D / 4); e += kThreads) {
-    const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
-    float M = bw[h];
-#pragma unroll
-    for (int w = 1; w < kWarps; ++w) M = fmaxf(M, bw[w * 16 + h]);
-    float L = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = fast_exp2(bw[w * 16 + h] - M);
-      const float4 x = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(smem + w * T::kRing) + h * T::kRow + d);
-      L += f * lw[w * 16 + h];
-      o.x += f * x.x;
-      o.y += f * x.y;
-      o.z += f * x.z;
-      o.w += f * x.w;
-    }
-    // (a NaN sum is not an empty one)
-    const bool some = !(L <= 0.f);
-    const float m = M * (1.f / kLog2e);
-    float4 vs;
-    if (p.per_channel) {
-      vs = *reinterpret_cast<const float4*>(p.v_scale + it.g * D + d);
-    } else {
-      vs.x = vs.y = vs.z = vs.w = p.v_scale[0];
-    }
-    if (direct) {
-      float scale = some ? 1.f / L : 0.f;
-      if (p.sink != nullptr && some) scale *= 1.f / (1.f + expf(p.sink[it.g * G + h] - (m + logf(L))));
-      uint2 v = make_uint2(0u, 0u);
-      if (some)
-        v = make_uint2(pack_h2(o.x * scale * vs.x, o.y * scale * vs.y),
-                       pack_h2(o.z * scale * vs.z, o.w * scale * vs.w));
-      *reinterpret_cast<uint2*>(static_cast<__half*>(p.out) + (head0 + h) * D + d) = v;
-      if (d == 0 && p.lse != nullptr) p.lse[head0 + h] = some ? m + logf(L) : neg_inf();
-    } else {
-      if (some)
-        *reinterpret_cast<float4*>(p.ws_acc + (part0 + h) * D + d) =
-            make_float4(o.x * vs.x, o.y * vs.y, o.z * vs.z, o.w * vs.w);
-      if (d == 0) {
-        p.ws_m[part0 + h] = some ? m : neg_inf();
-        p.ws_l[part0 + h] = some ? L : 0.f;
-      }
-    }
-  }
-}
-
-template <int D, int NT>
-cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
-  using T = Mx4Tile<D, NT>;
-  auto kern = mx4_decode_kernel<D, NT>;
-  // the opt-in shared-memory size is a per-function attribute: set it once per device
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = 1ull << (dev & 63);
-  if (!(done.load() & bit)) {
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, T::kSmem);
-    if (e != cudaSuccess) return e;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout,
-                             cudaSharedmemCarveoutMaxShared);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit);
-  }
-  if (info != nullptr) {
-    info->round = 16 * kWarps;
-    return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&info->occupancy, kern, kThreads, T::kSmem);
-  }
-  const long long units = (long long)p.rows * p.Hkv;
-  long long ctas = units * p.num_splits;
-  if (p.balanced && ctas > p.bal_pieces) ctas = p.bal_pieces;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)ctas);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = T::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kern, p);
-}
-
-}  // namespace
-
 cudaError_t launch_paged_mx4(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                              KernelInfo* info) {
-  switch (key.D * 10 + key.nt) {
-    case 641: return run_mx4<64, 1>(p, s, info);
-    case 642: return run_mx4<64, 2>(p, s, info);
-    case 1281: return run_mx4<128, 1>(p, s, info);
-    case 1282: return run_mx4<128, 2>(p, s, info);
-    case 2561: return run_mx4<256, 1>(p, s, info);
-    case 2562: return run_mx4<256, 2>(p, s, info);
-    default: return cudaErrorInvalidValue;
-  }
+  return dispatch_mx4<4, false>(key, p, s, info);
 }
-
 }  // namespace i8kv
