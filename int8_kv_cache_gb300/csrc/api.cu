@@ -94,6 +94,7 @@ cudaError_t launch_key(const KernelKey& key, const DecodeParams& p, cudaStream_t
 struct WaveInfo {
   int32_t wave;
   int32_t round;
+  int32_t clusters[4] = {0, 0, 0, 0};  // cluster kernels: resident clusters of 1, 2, 4, 8 CTAs
 };
 
 i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
@@ -117,10 +118,11 @@ i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e);
   DecodeParams dummy{};
-  KernelInfo info{0, 0};
+  KernelInfo info{};
   e = launch_key(key, dummy, nullptr, &info);
   if (e != cudaSuccess) return cuda_fail(e);
-  const WaveInfo w{std::max(1, sms * std::max(info.occupancy, 1)), std::max(info.round, 16)};
+  WaveInfo w{std::max(1, sms * std::max(info.occupancy, 1)), std::max(info.round, 16)};
+  std::copy(info.clusters, info.clusters + 4, w.clusters);
   {
     std::lock_guard<std::mutex> lock(mu);
     cache[k] = w;
@@ -212,34 +214,39 @@ i8kv_status plan(const KernelKey& key, int64_t cap, int32_t units, int32_t mode,
   return I8KV_OK;
 }
 
-// Resident CTAs of the MX4 decode's cluster kernel (the key with `cluster` set).
-i8kv_status cluster_wave(KernelKey key, int32_t* wave) {
+// Whether the MX4 decode takes `units` clusters of c CTAs (a power of two, at most
+// kMx4MaxCluster) with all of them resident at once; a single CTA always.
+i8kv_status mx4_clusters(KernelKey key, int32_t units, int32_t c, bool* fits) {
+  *fits = c == 1;
+  if (c < 2 || c > i8kv::kMx4MaxCluster || (c & (c - 1)) != 0) return I8KV_OK;
   key.cluster = true;
   WaveInfo w{0, 0};
   const i8kv_status st = wave_of(key, &w);
-  *wave = w.wave;
+  *fits = units <= w.clusters[log2_of(c)];
   return st;
 }
 
 // The automatic geometry of the MX4 decode, from the wave rule's count *ns.  A
 // row and KV head is one CTA of 8 warps, or a cluster of 2, 4 or 8 of them that join
-// without a second kernel, where that gives a warp at most 8 tiles of 16 tokens and
-// all clusters are resident at once; the fewest CTAs that leave a warp 2 tiles.
+// without a second kernel, where that gives a warp at most 8 tiles of 16 tokens (4 at
+// head_dim 256) and all clusters are resident at once; the fewest CTAs that leave a warp 2 tiles.
 // Longer spans, where the second kernel (about 3 us) is less than the
 // imbalance of equal clusters: balanced pieces, twice the wave rule's count as
 // partial slots.
 constexpr int64_t kMx4WarpTiles = 8;
 i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t* ns,
                      int32_t* chunk) {
-  int32_t wave = 0;
-  const i8kv_status st = cluster_wave(key, &wave);
-  if (st != I8KV_OK) return st;
   const int64_t tiles = cdiv(span, 16);
   int32_t c = 1;
-  while (c < i8kv::kMx4MaxCluster && c * i8kv::kMx4ClusterWarps * 2 < tiles &&
-         2LL * c * units <= wave)
+  while (c < i8kv::kMx4MaxCluster && c * i8kv::kMx4ClusterWarps * 2 < tiles) {
+    bool fits = false;
+    const i8kv_status st = mx4_clusters(key, units, 2 * c, &fits);
+    if (st != I8KV_OK) return st;
+    if (!fits) break;
     c *= 2;
-  if (tiles <= kMx4WarpTiles * i8kv::kMx4ClusterWarps * c) {
+  }
+  const int64_t most = key.D > 128 ? kMx4WarpTiles / 2 : kMx4WarpTiles;
+  if (tiles <= most * i8kv::kMx4ClusterWarps * c) {
     *ns = c;
     *chunk = c > 1 ? 0 : static_cast<int32_t>(std::max<int64_t>(16, tiles * 16));
     return I8KV_OK;
@@ -247,13 +254,6 @@ i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t*
   *ns = std::min<int32_t>(I8KV_MAX_SPLITS, std::max<int32_t>(2, 2 * *ns));
   *chunk = 0;
   return I8KV_OK;
-}
-
-// Whether balanced pieces of the MX4 decode run as clusters: a cluster's size, and
-// all of them resident at once.
-bool mx4_clusters(int32_t units, int32_t ns, int32_t wave) {
-  return ns <= i8kv::kMx4MaxCluster && (ns & (ns - 1)) == 0 &&
-         static_cast<int64_t>(units) * ns <= wave;
 }
 
 // Geometry given by the caller: num_splits in [1, 32], chunk a positive
@@ -706,8 +706,9 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
       !aligned(head_sink, 4) || !aligned(flags, 4))
     return I8KV_EALIGN;
   const int64_t cap = static_cast<int64_t>(max_blocks) * block_size;
-  // positions, and CTA numbers, are 32-bit on the device
-  if (cap > INT32_MAX - 16 || static_cast<int64_t>(B) * Hkv * I8KV_MAX_SPLITS > INT32_MAX)
+  // positions, CTA numbers and the batch's 16-token tiles are 32-bit on the device
+  if (cap > INT32_MAX - 16 || static_cast<int64_t>(B) * Hkv * I8KV_MAX_SPLITS > INT32_MAX ||
+      static_cast<int64_t>(B) * (cap / 16 + 1) > INT32_MAX - 64)
     return I8KV_EUNSUPPORTED;
   const int32_t units = std::max(1, B * Hkv);
   const KernelKey key = make_key(Path::kPaged, D, Hq / Hkv, I8KV_CACHE_MX4, false);
@@ -756,9 +757,8 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
   // one split, and balanced pieces that fit clusters, join inside the kernel
   bool cluster = num_splits == 1;
   if (p.balanced) {
-    int32_t resident = 0;
-    if ((st = cluster_wave(key, &resident)) != I8KV_OK) return st;
-    cluster = out != nullptr && mx4_clusters(units, num_splits, resident);
+    if ((st = mx4_clusters(key, units, num_splits, &cluster)) != I8KV_OK) return st;
+    cluster = cluster && out != nullptr;
     WaveInfo w{0, 0};
     if ((st = wave_of(key, &w)) != I8KV_OK) return st;
     // (at least one piece per row and KV head, and one to spare)

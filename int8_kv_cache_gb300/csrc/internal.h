@@ -68,6 +68,7 @@ struct KernelKey {
 struct KernelInfo {
   int occupancy;  // resident CTAs per SM (the CUDA occupancy API)
   int round;      // positions one round of the CTA's warps covers (warps x step)
+  int clusters[4] = {0, 0, 0, 0};  // cluster kernels: resident clusters of 1, 2, 4, 8 CTAs
 };
 
 // Per-path launchers (one per translation unit): grid (rows * Hkv, num_splits);

@@ -57,17 +57,19 @@ __device__ Mx4Item balanced_piece(const DecodeParams& p, int c) {
   const int cap = p.max_blocks * p.bs;
   int len, wlo;
   const int t0 = lane < B ? tiles_of(p, lane, cap, len, wlo) : 0;  // the only rows if B <= 32
-  long long tot = t0;
+  int tot = t0;  // (the host keeps B * cap / 16 within 31 bits)
+#pragma unroll 1
   for (int r = 32 + lane; r < B; r += 32) tot += tiles_of(p, r, cap, len, wlo);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) tot += __shfl_xor_sync(0xffffffffu, tot, o);
+  tot = __reduce_add_sync(0xffffffffu, tot);
   const int room = p.bal_pieces / Hkv;  // pieces of one KV head (> B)
   // bisection in units of kMinTiles (one tile per warp)
-  int lo = max(1, (int)((tot + (long long)room * kMinTiles - 1) / ((long long)room * kMinTiles)));
-  int up = max(lo, (int)((tot + (long long)(room - B) * kMinTiles - 1) / ((long long)(room - B) * kMinTiles)));
+  const int need = (tot + kMinTiles - 1) / kMinTiles;
+  int lo = max(1, (need + room - 1) / room);
+  int up = max(lo, (need + room - B - 1) / (room - B));
   while (lo < up) {
     const int mid = (lo + up) >> 1, len_mid = mid * kMinTiles;
     int n = lane < B ? min(max((t0 + len_mid - 1) / len_mid, 1), S) : 0;
+#pragma unroll 1
     for (int r = 32 + lane; r < B; r += 32)
       n += min(max((tiles_of(p, r, cap, len, wlo) + len_mid - 1) / len_mid, 1), S);
     n = __reduce_add_sync(0xffffffffu, n);
@@ -77,7 +79,8 @@ __device__ Mx4Item balanced_piece(const DecodeParams& p, int c) {
       lo = mid + 1;
   }
   const int L = lo * kMinTiles;
-  long long base = 0;
+  int base = 0;
+#pragma unroll 1
   for (int r0 = 0; r0 < B; r0 += 32) {
     const int r = r0 + lane;
     int t = 0, n = 0;
@@ -96,7 +99,7 @@ __device__ Mx4Item balanced_piece(const DecodeParams& p, int c) {
     }
     const int total = __shfl_sync(0xffffffffu, inc, 31);
     if (c < (base + total) * Hkv) {
-      const int q = (int)(c - base * Hkv);  // item among these rows
+      const int q = c - base * Hkv;  // item among these rows
       const int piece = q / Hkv;
       const unsigned m = __ballot_sync(0xffffffffu, piece < inc);
       const int src = __ffs(m) - 1;
@@ -201,9 +204,12 @@ __device__ __forceinline__ uint32_t lds_u16(uint32_t addr) {
   return v;
 }
 
-constexpr float kUnset = -3.0e38f;  // exponent base of a head without a score yet
+constexpr float kUnset = -3.0e38f;  // exponent base of a warp that attended nothing
 constexpr float kHead = 15.f;       // log2 of the largest probability the fp16 tile takes
 constexpr float kRoom = 8.f;        // log2 of the largest one right after the base is set
+
+// (out of line: block sizes that are no power of two)
+static __device__ __noinline__ int quotient(int a, int b) { return a / b; }
 
 __device__ __forceinline__ void cluster_sync() {
   asm volatile("barrier.cluster.arrive.release;\n barrier.cluster.wait.acquire;\n" ::: "memory");
@@ -244,7 +250,7 @@ mx4_decode_kernel(const DecodeParams p) {
   const int grp = lane >> 2, tig = lane & 3;
   const int G = p.G;
   const int rpb = p.bs >> 4;  // records per block
-  auto block_of = [&](int tile) { return p.bs_log2 >= 4 ? tile >> (p.bs_log2 - 4) : tile / rpb; };
+  auto block_of = [&](int tile) { return p.bs_log2 >= 4 ? tile >> (p.bs_log2 - 4) : quotient(tile, rpb); };
   Mx4Item it;
   if constexpr (CLUSTER) {
     it.unit = blockIdx.x / p.num_splits;
@@ -318,40 +324,39 @@ mx4_decode_kernel(const DecodeParams p) {
     if (32 + lane < mine) e1 = entry(32 + lane);
   }
   const uint8_t* cache = static_cast<const uint8_t*>(p.k);
-  auto place = [&](int j, int blk) -> long long {  // byte offset of tile j's record, -1: none
-    if (j >= mine) return -1;
+  // what a lane copies: the record of its tile (nullptr: none) and the attended tokens of it
+  const uint8_t* rec_at = nullptr;
+  int rec_mask = 0;
+  auto place = [&](int j, int blk) {
+    rec_at = nullptr;
+    rec_mask = 0;
+    if (j >= mine) return;
     if (blk < 0 || (long long)blk >= p.cache_rows) {
       flag_or(p.flags, I8KV_FLAG_BAD_BLOCK);
-      return -1;
+      return;
     }
-    const int tile = first + it.stride * j;
-    return (((long long)blk * p.Hkv + it.g) * rpb + (tile - block_of(tile) * rpb)) * T::kRec;
+    const int tile = first + it.stride * j, pos = 16 * tile;
+    rec_mask = it.hi - pos >= 16 ? 0xFFFF : (1 << (it.hi - pos)) - 1;
+    if (pos < it.wlo) rec_mask &= 0xFFFF << (it.wlo - pos);
+    rec_at = cache + (((long long)blk * p.Hkv + it.g) * rpb + (tile - block_of(tile) * rpb)) * T::kRec;
   };
   const uint32_t ring = smem_addr(smem + warp * T::kRing);
   const uint32_t bars = smem_addr(smem + T::kBars) + warp * T::kStages * 8;
   int* masks = reinterpret_cast<int*>(smem + T::kMasks) + warp * T::kStages * T::kSub;
-  long long cur = place(lane, e0);
-  auto issue = [&](int k) {  // stage k into its slot of the ring
-    if (k >= stages) return;
+  place(lane, e0);
+  auto issue = [&](int k, int st) {  // stage k into slot st of the ring
     const int j0 = k * T::kSub;
     if (j0 > 0 && (j0 & 31) == 0) {
-      cur = place(j0 + lane, e1);
+      place(j0 + lane, e1);
       e1 = j0 + 32 + lane < mine ? entry(j0 + 32 + lane) : -1;
     }
-    const int s = lane - (j0 & 31);
-    if (s >= 0 && s < T::kSub) {
-      const int st = k % T::kStages;
+    const unsigned s = lane - (j0 & 31);
+    if (s < T::kSub) {
       const uint32_t bar = bars + st * 8;
-      int mask = 0;  // attended tokens (stored before the arrival that publishes it)
-      if (cur >= 0) {
-        const int pos = 16 * (first + it.stride * (j0 + s));
-        mask = it.hi - pos >= 16 ? 0xFFFF : (1 << (it.hi - pos)) - 1;
-        if (pos < it.wlo) mask &= 0xFFFF << (it.wlo - pos);
-      }
-      masks[st * T::kSub + s] = mask;
-      if (cur >= 0) {
+      masks[st * T::kSub + s] = rec_mask;  // (before the arrival that publishes it)
+      if (rec_at != nullptr) {
         tc::mbar_arrive_expect_tx(bar, T::kRec);
-        tc::bulk_g2s(ring + st * T::kStageBytes + s * T::kRec, cache + cur, T::kRec, bar);
+        tc::bulk_g2s(ring + st * T::kStageBytes + s * T::kRec, rec_at, T::kRec, bar);
       } else {
         tc::mbar_arrive(bar);
       }
@@ -363,11 +368,12 @@ mx4_decode_kernel(const DecodeParams p) {
     tc::fence_mbar_init();
   }
   __syncwarp();
-#pragma unroll
-  for (int k = 0; k < T::kStages; ++k) issue(k);
+#pragma unroll 1
+  for (int k = 0; k < min(T::kStages, stages); ++k) issue(k, k);
 
   // slots that no piece fills: empty
   if (it.pieces > 0 && it.slot == 0) {
+#pragma unroll 1
     for (int e = threadIdx.x; e < (p.num_splits - it.pieces) * G; e += kThreads) {
       const long long b = ((long long)it.unit * p.num_splits + it.pieces) * G + e;
       p.ws_m[b] = neg_inf();
@@ -450,7 +456,7 @@ mx4_decode_kernel(const DecodeParams p) {
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      base[nt][j] = kUnset;
+      base[nt][j] = 0.f;
       lrun[nt][j] = 0.f;
     }
   // score row r of a tile (0..7; +8 below) is token (r >> 1) + 4 (r & 1), so that a lane's
@@ -461,9 +467,11 @@ mx4_decode_kernel(const DecodeParams p) {
   const uint32_t v_off = 9 * D + tig * (D / 2) + grp * (D / 16);
   const uint32_t vs_off = 17 * D + tig * (D / 16) + (grp * D) / 128;
   const float cap_k = 2.f * kLog2e / p.softcap;  // used only when softcap > 0
+  bool unset = true;  // no score yet: the bases are not set
   bool timeout = false;
 
   int k = 0;
+#pragma unroll 1
   for (; k < stages; ++k) {
     const int st = k % T::kStages;
     const bool ok = tc::mbar_wait(bars + st * 8, (k / T::kStages) & 1);
@@ -523,9 +531,14 @@ mx4_decode_kernel(const DecodeParams p) {
 
     // ---- online softmax: the exponent base of a head moves only when a score leaves the
     // range that the fp16 probabilities cover ----
-    int mask[T::kSub];
+    int mask[T::kSub], all = 0xFFFF, live_any = 0;
 #pragma unroll
-    for (int s = 0; s < T::kSub; ++s) mask[s] = masks[st * T::kSub + s];
+    for (int s = 0; s < T::kSub; ++s) {
+      mask[s] = masks[st * T::kSub + s];
+      all &= mask[s];
+      live_any |= mask[s];
+    }
+    const bool partial = all != 0xFFFF, any_live = live_any != 0;  // uniform
     // z: scores less the head's base, in log2 units
     float z[T::kSub][NT][4];
     auto scores_less_base = [&]() {
@@ -547,9 +560,9 @@ mx4_decode_kernel(const DecodeParams p) {
             for (int e = 0; e < 4; ++e)
               z[s][nt][e] = fmaf(sc[s][nt][e], fac[nt][e & 1], -base[nt][e & 1]);
       }
+      if (partial) {
 #pragma unroll
-      for (int s = 0; s < T::kSub; ++s) {
-        if (mask[s] != 0xFFFF) {  // uniform
+        for (int s = 0; s < T::kSub; ++s) {
           const bool upper = (mask[s] >> tok) & 1, lower = (mask[s] >> (tok + 8)) & 1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -567,16 +580,7 @@ mx4_decode_kernel(const DecodeParams p) {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) top = fmaxf(top, z[s][nt][e]);
-    if (__any_sync(0xffffffffu, top > kHead)) {
-      float old[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          old[nt][j] = base[nt][j];
-          if (base[nt][j] == kUnset) base[nt][j] = 0.f;  // (kUnset would swallow the score)
-        }
-      scores_less_base();
+    if (unset || __any_sync(0xffffffffu, top > kHead)) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float alpha[2];
@@ -588,11 +592,10 @@ mx4_decode_kernel(const DecodeParams p) {
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          const bool unset = old[nt][j] == kUnset;
-          // up by what the largest is above the room left, down too on the first score
-          const float up = unset ? mx - kRoom : fmaxf(mx - kRoom, 0.f);
-          alpha[j] = unset ? 0.f : fast_exp2(-up);
-          base[nt][j] = unset && mx == neg_inf() ? kUnset : base[nt][j] + up;
+          // up by what the largest is above the room left; down too on the first scores
+          const float up = unset ? (any_live ? mx - kRoom : 0.f) : fmaxf(mx - kRoom, 0.f);
+          alpha[j] = unset ? 1.f : fast_exp2(-up);
+          base[nt][j] += up;
         }
         lrun[nt][0] *= alpha[0];
         lrun[nt][1] *= alpha[1];
@@ -604,7 +607,16 @@ mx4_decode_kernel(const DecodeParams p) {
           acc[t][nt][3] *= alpha[1];
         }
       }
+      unset = unset && !any_live;
       scores_less_base();
+      // (a score so large that its own rounding exceeds the room still fits fp16)
+#pragma unroll
+      for (int s = 0; s < T::kSub; ++s)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (z[s][nt][e] > kHead) z[s][nt][e] = kHead;
     }
     uint32_t ph[T::kSub][NT][2];
 #pragma unroll
@@ -636,7 +648,7 @@ mx4_decode_kernel(const DecodeParams p) {
           x[i] = lds_u8(r + vs_off + i * 4 * (D / 16));
         }
       }
-      if (mask[s] != 0xFFFF) {  // a token that is not attended: nothing of its bytes counts
+      if (partial) {  // a token that is not attended: nothing of its bytes counts
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (!((mask[s] >> (tig + 4 * i)) & 1)) x[i] = 0u;
@@ -670,7 +682,7 @@ mx4_decode_kernel(const DecodeParams p) {
       }
     }
     __syncwarp();  // every lane has read the stage
-    issue(k + T::kStages);
+    if (k + T::kStages < stages) issue(k + T::kStages, st);
   }
   if (timeout) {
     // the copies still in flight must not land in memory that others use
@@ -694,7 +706,7 @@ mx4_decode_kernel(const DecodeParams p) {
       l += __shfl_xor_sync(0xffffffffu, l, 16);
       const int h = nt * 8 + 2 * tig + j;
       if (grp == 0) {
-        bw[warp * 16 + h] = base[nt][j];
+        bw[warp * 16 + h] = unset ? kUnset : base[nt][j];
         lw[warp * 16 + h] = l;
       }
       if (h < G) {
@@ -725,6 +737,7 @@ mx4_decode_kernel(const DecodeParams p) {
     if (d == 0 && p.lse != nullptr) p.lse[head0 + h] = some ? m + logf(L) : neg_inf();
   };
   float* jm = reinterpret_cast<float*>(smem + T::kJoin);  // [16] base, [16] sum
+#pragma unroll 1
   for (int e = threadIdx.x; e < G * (D / 4); e += kThreads) {
     const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
     float M = bw[h];
@@ -767,6 +780,7 @@ mx4_decode_kernel(const DecodeParams p) {
     cluster_sync();  // every CTA's sum is there
     const int C = p.num_splits;
     const uint32_t rows = smem_addr(smem), join = smem_addr(smem + T::kJoin);
+#pragma unroll 1
     for (int e = it.slot * kThreads + threadIdx.x; e < G * (D / 4); e += C * kThreads) {
       const int h = e / (D / 4), d = 4 * (e - h * (D / 4));
       float m[8], l[8], M = kUnset, L = 0.f;
@@ -819,6 +833,22 @@ cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
   }
   if (info != nullptr) {
     info->round = 16 * W;
+    if constexpr (CLUSTER) {
+      // clusters live inside a part of the GPU: fewer fit than the CTAs alone
+      for (int i = 0; i < 4; ++i) {
+        cudaLaunchConfig_t c = {};
+        c.gridDim = dim3(1024u << i);
+        c.blockDim = dim3(32 * W);
+        c.dynamicSmemBytes = T::kSmem;
+        cudaLaunchAttribute a;
+        a.id = cudaLaunchAttributeClusterDimension;
+        a.val.clusterDim.x = 1u << i;
+        a.val.clusterDim.y = a.val.clusterDim.z = 1;
+        c.attrs = &a;
+        c.numAttrs = 1;
+        if ((e = cudaOccupancyMaxActiveClusters(&info->clusters[i], kern, &c)) != cudaSuccess) return e;
+      }
+    }
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&info->occupancy, kern, 32 * W, T::kSmem);
   }
   const long long units = (long long)p.rows * p.Hkv;
