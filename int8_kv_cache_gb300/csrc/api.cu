@@ -228,25 +228,34 @@ i8kv_status mx4_clusters(KernelKey key, int32_t units, int32_t c, bool* fits) {
 
 // The automatic geometry of the MX4 decode, from the wave rule's count *ns.  A
 // row and KV head is one CTA of 8 warps, or a cluster of 2, 4 or 8 of them that join
-// without a second kernel, where that gives a warp at most 8 tiles of 16 tokens (4 at
-// head_dim 256) and all clusters are resident at once; the fewest CTAs that leave a warp 2 tiles.
-// Longer spans, where the second kernel (about 3 us) is less than the
-// imbalance of equal clusters: balanced pieces, twice the wave rule's count as
-// partial slots.
+// without a second kernel (the fewest CTAs that leave a warp 2 tiles of 16 tokens, all
+// clusters resident at once),
+//   - where that gives a warp at most 8 tiles, 4 at head_dim 256 (16 rows x 2 KV
+//     heads of 2600 tokens: 9.7 us against 11.7 for pieces; 8 x 2 heads of 4096 at
+//     head_dim 256: 18.7 against 16.9, hence the 4), or
+//   - where the rows and heads alone fill the GPU and spans are at most 8192 tokens,
+//     so that a long row among short ones is not what is waited for (128 rows x 8 heads
+//     of 128 to 4096 tokens: 79 us against 96; 32 x 8 heads, which do not fill it,
+//     of 128 to 2048: 17.9 against 16.4).
+// Else balanced pieces, twice the wave rule's count as partial slots, and the join
+// kernel (about 3 us).
 constexpr int64_t kMx4WarpTiles = 8;
+constexpr int64_t kMx4RowTiles = 512;
 i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t* ns,
                      int32_t* chunk) {
   const int64_t tiles = cdiv(span, 16);
+  KernelKey one = key;
+  one.cluster = true;
+  WaveInfo w{0, 0};
+  const i8kv_status st = wave_of(one, &w);
+  if (st != I8KV_OK) return st;
+  const bool fills = units >= w.clusters[0] && tiles <= kMx4RowTiles;
   int32_t c = 1;
-  while (c < i8kv::kMx4MaxCluster && c * i8kv::kMx4ClusterWarps * 2 < tiles) {
-    bool fits = false;
-    const i8kv_status st = mx4_clusters(key, units, 2 * c, &fits);
-    if (st != I8KV_OK) return st;
-    if (!fits) break;
+  while (!fills && c < i8kv::kMx4MaxCluster && c * i8kv::kMx4ClusterWarps * 2 < tiles &&
+         units <= w.clusters[log2_of(2 * c)])
     c *= 2;
-  }
   const int64_t most = key.D > 128 ? kMx4WarpTiles / 2 : kMx4WarpTiles;
-  if (tiles <= most * i8kv::kMx4ClusterWarps * c) {
+  if (fills || tiles <= most * i8kv::kMx4ClusterWarps * c) {
     *ns = c;
     *chunk = c > 1 ? 0 : static_cast<int32_t>(std::max<int64_t>(16, tiles * 16));
     return I8KV_OK;
