@@ -179,6 +179,19 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+// Both halves of a times one half of b.
+__device__ __forceinline__ uint32_t hmul2_half(uint32_t a, uint32_t b, bool high) {
+  const __half2 s = *reinterpret_cast<const __half2*>(&b);
+  const __half2 r = __hmul2(*reinterpret_cast<__half2*>(&a), high ? __high2half2(s) : __low2half2(s));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// The values of the two float8 e4m3fn bytes in bits 0 .. 15, exact.
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint32_t w) {
+  uint32_t r;
+  asm("{\n .reg .b16 l, h;\n mov.b32 {l, h}, %1;\n cvt.rn.f16x2.e4m3x2 %0, l;\n}\n" : "=r"(r) : "r"(w));
+  return r;
+}
+
 template <int N>  // 4 N bytes
 __device__ __forceinline__ void lds(uint32_t addr, uint32_t (&w)[N]) {
   if constexpr (N == 1) {
@@ -490,22 +503,21 @@ mx4_decode_kernel(const DecodeParams p) {
       lds<KW>(r + k_off, wa);
       lds<KW>(r + k_off + 8 * (D / 2), wb);
       // block scales of the lane's channels (D / 64 of a token), each as an fp16 pair
-      constexpr int KB = D / 64;
-      uint32_t fa[KB < 2 ? 2 : KB], fb[KB < 2 ? 2 : KB];
+      // (two to a register: the products take the half they need of it)
+      constexpr int KB = D / 64, KP = (KB + 1) / 2;
+      uint32_t fa[KP], fb[KP];
       if constexpr (D == 64) {
-        e4m3x4_to_h2x2(lds_u8(r + ks_off) * 0x0101u, fa[0], fa[1]);
-        e4m3x4_to_h2x2(lds_u8(r + ks_off + 8 * (D / 16)) * 0x0101u, fb[0], fb[1]);
+        fa[0] = e4m3x2_to_h2(lds_u8(r + ks_off));
+        fb[0] = e4m3x2_to_h2(lds_u8(r + ks_off + 8 * (D / 16)));
       } else if constexpr (D == 128) {
-        e4m3x4_to_h2x2(prmt(lds_u16(r + ks_off), 0u, 0x1100u), fa[0], fa[1]);
-        e4m3x4_to_h2x2(prmt(lds_u16(r + ks_off + 8 * (D / 16)), 0u, 0x1100u), fb[0], fb[1]);
+        fa[0] = e4m3x2_to_h2(lds_u16(r + ks_off));
+        fb[0] = e4m3x2_to_h2(lds_u16(r + ks_off + 8 * (D / 16)));
       } else {
         uint32_t x[1];
         lds<1>(r + ks_off, x);
-        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x1100u), fa[0], fa[1]);
-        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x3322u), fa[2], fa[3]);
+        e4m3x4_to_h2x2(x[0], fa[0], fa[1]);
         lds<1>(r + ks_off + 8 * (D / 16), x);
-        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x1100u), fb[0], fb[1]);
-        e4m3x4_to_h2x2(prmt(x[0], 0u, 0x3322u), fb[2], fb[3]);
+        e4m3x4_to_h2x2(x[0], fb[0], fb[1]);
       }
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -518,8 +530,8 @@ mx4_decode_kernel(const DecodeParams p) {
         e2m1x8_to_h2x4(wb[w], b[0], b[1], b[2], b[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          a[i] = hmul2(a[i], fa[w / 2]);
-          b[i] = hmul2(b[i], fb[w / 2]);
+          a[i] = hmul2_half(a[i], fa[w / 4], (w / 2) % 2);
+          b[i] = hmul2_half(b[i], fb[w / 4], (w / 2) % 2);
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -659,8 +671,8 @@ mx4_decode_kernel(const DecodeParams p) {
         e4m3x4_to_h2x2(prmt(x[0], x[1], 0x5140u), s01[0], s01[1]);
         e4m3x4_to_h2x2(prmt(x[2], x[3], 0x5140u), s23[0], s23[1]);
       } else {
-        const uint32_t y = prmt(x[0] | (x[1] << 8), x[2] | (x[3] << 8), 0x5410u);
-        e4m3x4_to_h2x2(y, s01[0], s23[0]);
+        s01[0] = e4m3x2_to_h2(prmt(x[0], x[1], 0x0040u));
+        s23[0] = e4m3x2_to_h2(prmt(x[2], x[3], 0x0040u));
       }
 #pragma unroll
       for (int w = 0; w < VW; ++w) {
