@@ -76,29 +76,54 @@ __device__ __noinline__ uint2 codes8_exact(float4 lo, float4 hi, const float* __
   return make_uint2(w[0], w[1]);
 }
 
+// max(a, |b|), NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(fabsf(b)));
+  return r;
+}
+
 // The same codes from the products with the rounded reciprocals r, which are within
-// |q| 2^-22 of the rounded quotients: where a product lies within |q| 2^-21 of a
-// rounding boundary (about one piece in a thousand) the quotients decide.
+// |q| 2^-22 of the rounded quotients: where a product is nearer to a rounding boundary
+// than that allows (about one piece in a thousand), or a NaN, the quotients decide.
 template <bool FP8>
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], const float (&r)[8],
                                         const float* __restrict__ s, int s_step) {
   uint32_t w[2] = {0u, 0u};
-  bool near = false;
+  bool near;
+  if constexpr (FP8) {
+    // both ends of the product's error interval must have the same code
+    float top = 0.f;
+    uint32_t differ = 0u;
 #pragma unroll
-  for (int j = 0; j < 8; j += 2) {
-    const float q0 = nan_to_zero(x[j] * r[j]), q1 = nan_to_zero(x[j + 1] * r[j + 1]);
-    uint32_t b;
-    if constexpr (FP8) {
-      b = e4m3x2_of(q0 * kLoBound, q1 * kLoBound);
-      near |= b != e4m3x2_of(q0 * kHiBound, q1 * kHiBound);
-    } else {
-      const float n0 = rintf(q0), n1 = rintf(q1);
-      near |= fabsf(fabsf(q0 - n0) - 0.5f) <= fabsf(q0) * 0x1p-21f;
-      near |= fabsf(fabsf(q1 - n1) - 0.5f) <= fabsf(q1) * 0x1p-21f;
-      b = int8_byte(fminf(fmaxf(n0, -127.f), 127.f)) |
-          (int8_byte(fminf(fmaxf(n1, -127.f), 127.f)) << 8);
+    for (int j = 0; j < 8; j += 2) {
+      const float q0 = x[j] * r[j], q1 = x[j + 1] * r[j + 1];
+      const uint32_t b = e4m3x2_of(q0 * kLoBound, q1 * kLoBound);
+      differ |= b ^ e4m3x2_of(q0 * kHiBound, q1 * kHiBound);
+      top = max_nan(max_nan(top, q0), q1);
+      w[j / 4] |= b << (8 * (j % 4));
     }
-    w[j / 4] |= b << (8 * (j % 4));
+    near = differ != 0u || top != top;
+  } else {
+    // rounding by adding 1.5 * 2^23: the code is the low byte of the sum.  |q| <= 127 here, so
+    // a boundary (a half-integer) is nearer than |q| 2^-21 only if |q - code| > 1/2 - 2^-14
+    constexpr float kMagic = 12582912.f;
+    float far = 0.f;
+    uint32_t m[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      float q;
+      asm("{\n .reg .f32 t;\n max.NaN.f32 t, %1, 0fC2FE0000;\n min.NaN.f32 %0, t, 0f42FE0000;\n}\n"
+          : "=f"(q)
+          : "f"(x[j] * r[j]));  // clamped to +-127
+      const float t = __fadd_rn(q, kMagic);
+      m[j] = __float_as_uint(t);
+      far = max_nan(far, __fsub_rn(q, __fsub_rn(t, kMagic)));
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      w[i] = prmt(prmt(m[4 * i], m[4 * i + 1], 0x0040u), prmt(m[4 * i + 2], m[4 * i + 3], 0x0040u), 0x5410u);
+    near = !(far <= 0.5f - 0x1p-14f);
   }
   if (near)
     return codes8_exact<FP8>(make_float4(x[0], x[1], x[2], x[3]),
@@ -159,12 +184,13 @@ __device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], const An
   }
 }
 
-// One row's item into the cache.  r0, r1: reciprocals of the scales of the two pieces.
+// One row's item into the cache.  r0, r1: reciprocals of the scales of the two pieces;
+// inv_scale (MX4): the rounded reciprocals of the 127 block scales, by their byte.
 template <int CACHE>
 __device__ __forceinline__ void store_item(const AppendParams& p, const Pieces& x, int h, bool is_v,
                                            int slot, float (&a)[8], float (&b)[8],
                                            const float (&r0)[8], const float (&r1)[8],
-                                           const float* sc, int step) {
+                                           const float* sc, int step, const float* inv_scale) {
   if constexpr (CACHE == I8KV_CACHE_FP16) {
     __half* o = static_cast<__half*>(is_v ? p.v_cache : p.k_cache) +
                 ((long long)slot * p.Hkv + h) * p.D;
@@ -174,10 +200,20 @@ __device__ __forceinline__ void store_item(const AppendParams& p, const Pieces& 
     float ma = 0.f, mb = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      a[i] = nan_to_zero(__fmul_rn(a[i], r0[i]));
-      b[i] = nan_to_zero(__fmul_rn(b[i], r1[i]));
-      ma = fmaxf(ma, fabsf(a[i]));
-      mb = fmaxf(mb, fabsf(b[i]));
+      a[i] = __fmul_rn(a[i], r0[i]);
+      b[i] = __fmul_rn(b[i], r1[i]);
+      ma = max_nan(ma, a[i]);
+      mb = max_nan(mb, b[i]);
+    }
+    if (ma != ma || mb != mb) {  // a NaN counts as a zero
+      ma = mb = 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        a[i] = nan_to_zero(a[i]);
+        b[i] = nan_to_zero(b[i]);
+        ma = fmaxf(ma, fabsf(a[i]));
+        mb = fmaxf(mb, fabsf(b[i]));
+      }
     }
     const int lane = threadIdx.x & 31;
     if (x.block) {
@@ -189,22 +225,19 @@ __device__ __forceinline__ void store_item(const AppendParams& p, const Pieces& 
       mb = fmaxf(mb, __shfl_xor_sync(pair, mb, 1));
     }
     const uint32_t sb = e4m3x2_of(__fmul_rn(ma, 1.f / 6.f), __fmul_rn(mb, 1.f / 6.f));
-    uint32_t s2, unused;
-    e4m3x4_to_h2x2(sb, s2, unused);
-    const float2 s = __half22float2(*reinterpret_cast<const __half2*>(&s2));
-    const float ra = s.x > 0.f ? __frcp_rn(s.x) : 0.f, rb = s.y > 0.f ? __frcp_rn(s.y) : 0.f;
-    const bool za = s.x > 0.f, zb = s.y > 0.f;  // (a zero scale stores zeros, of an infinity too)
+    const float ra = inv_scale[sb & 0x7Fu], rb = inv_scale[(sb >> 8) & 0x7Fu];  // 0 of a zero
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      a[i] = za ? __fmul_rn(a[i], ra) : 0.f;
-      b[i] = zb ? __fmul_rn(b[i], rb) : 0.f;
+      a[i] = __fmul_rn(a[i], ra);
+      b[i] = __fmul_rn(b[i], rb);
     }
     int tok;
     uint8_t* rec = static_cast<uint8_t*>(p.k_cache) +
                    mx4_record(slot, h, p.Hkv, p.D, p.bs, p.bs_shift, tok) + (is_v ? 9 * p.D : 0);
     uint8_t* code = rec + tok * (p.D >> 1);
-    *reinterpret_cast<uint32_t*>(code + (x.c0 >> 1)) = e2m1x8_of(a);
-    *reinterpret_cast<uint32_t*>(code + (x.c1 >> 1)) = e2m1x8_of(b);
+    // (a zero scale stores zeros, not the signs of what vanished)
+    *reinterpret_cast<uint32_t*>(code + (x.c0 >> 1)) = ra != 0.f ? e2m1x8_of(a) : 0u;
+    *reinterpret_cast<uint32_t*>(code + (x.c1 >> 1)) = rb != 0.f ? e2m1x8_of(b) : 0u;
     uint8_t* scale = rec + 8 * p.D + tok * (p.D >> 4);
     // one writer per block: the lane that holds its first 8 channels
     if ((x.c0 & 15) == 0) {
@@ -240,6 +273,11 @@ __device__ __forceinline__ void scales8(const AppendParams& p, const float* s, i
 template <int CACHE, int HQ>
 __global__ void __launch_bounds__(kAppendThreads, 2)
 rope_and_cache_kernel(const AppendParams p, long long lanes) {
+  __shared__ float inv_scale[CACHE == I8KV_CACHE_MX4 ? 128 : 1];
+  if constexpr (CACHE == I8KV_CACHE_MX4) {
+    if (threadIdx.x < 128) inv_scale[threadIdx.x] = threadIdx.x ? __frcp_rn(e4m3_value(threadIdx.x)) : 0.f;
+    __syncthreads();
+  }
   grid_dependency_wait();
   const int ipr = p.D >> 4;                           // items per row
   const int groups = (p.Hq + HQ - 1) / HQ;
@@ -349,7 +387,7 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
       unpack8(ra[i], a);
       unpack8(rb[i], b);
       if (x.turned) turn_item(a, b, g[i], il);
-      store_item<CACHE>(p, x, h, is_v, slot[i], a, b, r0, r1, sc, step);
+      store_item<CACHE>(p, x, h, is_v, slot[i], a, b, r0, r1, sc, step, inv_scale);
     }
   }
 }
