@@ -292,7 +292,10 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
   if (unit < groups) {  // queries: HQ heads of a token
     const Pieces x = pieces_of(p, j, true);
     const int h0 = unit * HQ;
+    int next = p.R > 0 ? __ldg(p.positions + n0) : 0;  // a position ahead of its angles
     for (long long n = n0; n < p.num_tokens; n += lanes) {
+      const int pos = next;
+      if (p.R > 0 && n + lanes < p.num_tokens) next = __ldg(p.positions + n + lanes);
       const __half* row = p.q + n * p.q_stride + (long long)h0 * p.D;
       uint4 ra[HQ], rb[HQ];
 #pragma unroll
@@ -303,7 +306,6 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
         }
       Angles g;
       if (p.R > 0) {
-        const int pos = __ldg(p.positions + n);
         if (pos < 0 || (long long)pos >= p.max_pos) continue;
         if (x.turned) g = angles_of(p, x, pos);
       }
@@ -541,7 +543,7 @@ namespace {
 template <int CACHE, int HQ>
 cudaError_t append_with(const AppendParams& p, int sms, cudaStream_t stream) {
   const long long ipt = ((p.Hq + HQ - 1) / HQ + 2LL * p.Hkv) * (p.D / 16);
-  const long long lanes = lanes_of(p.num_tokens, ipt, 4LL * sms);
+  const long long lanes = lanes_of(p.num_tokens, ipt, 2LL * sms);  // the resident CTAs
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg = config_of(lanes * ipt, &attr, stream);
   return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<CACHE, HQ>, p, lanes);
