@@ -525,11 +525,11 @@ i8kv_status gather_cache(const int32_t* slot_mapping, int32_t num_rows, int32_t 
  *   workspace have the same layout (a workspace of their size is asked for
  *   whenever num_splits > 1).
  * Numerics: the K and V values of the cache are exact in the fp16 products;
- * Q * k_scale is rounded to fp16 with one power of two per head taken out (per
- * channel scales; a scale per tensor is applied to the fp32 scores), so its
- * range is not limited, and I8KV_FLAG_QUERY_RANGE and I8KV_FLAG_FP32_PATH are not
- * raised; the probabilities are rounded to fp16 (a relative 2^-12), the sums
- * are fp32.
+ * Q * k_scale is held as two fp16 numbers with one power of two per head taken
+ * out (per channel scales; a scale per tensor is applied to the fp32 scores), so
+ * its range is not limited, and I8KV_FLAG_QUERY_RANGE and I8KV_FLAG_FP32_PATH are
+ * not raised; the probabilities are rounded to fp16 (by at most a relative
+ * 2^-11), the sums are fp32.
  */
 i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* k_scale,
                              const float* v_scale, int32_t scale_kind,

@@ -163,7 +163,8 @@ struct Mx4Tile {
   static constexpr int kScal = kMasks + W * kStages * kSub * 4;  // [2][warps][16]
   static constexpr int kQRow = D + 8;                    // halves of a staged query row (padded)
   static constexpr int kQ = kScal + 2 * W * 16 * 4;           // [8 NT][kQRow] fp16
-  static constexpr int kInv = kQ + 8 * NT * kQRow * 2;             // [16] score factors
+  static constexpr int kQLo = kQ + 8 * NT * kQRow * 2;             // the rest below fp16, likewise
+  static constexpr int kInv = kQLo + 8 * NT * kQRow * 2;           // [16] score factors
   static constexpr int kVs = kInv + 16 * 4;              // [D] value scales
   static constexpr int kSink = kVs + D * 4;              // [16] sink logits
   static constexpr int kJoin = kSink + 16 * 4;           // [2][16] base and sum of the CTA (cluster)
@@ -247,9 +248,11 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   return v;
 }
 
-// W warps.  CLUSTER: the p.num_splits CTAs of a cluster share one (row, KV head), its tiles
+// W warps.  FOLD: scales per channel, folded into the queries, which then take two fp16
+// numbers each (22 bits: rounding them to one would move the scores by as much as all
+// else together).  CLUSTER: the p.num_splits CTAs of a cluster share one (row, KV head), its tiles
 // dealt to their warps in turn, and join through distributed shared memory.
-template <int D, int NT, int W, bool CLUSTER>
+template <int D, int NT, int W, bool CLUSTER, bool FOLD>
 __global__ void __launch_bounds__(32 * W, (Mx4Tile<D, NT, W>::kBlocks))
 mx4_decode_kernel(const DecodeParams p) {
   using T = Mx4Tile<D, NT, W>;
@@ -304,14 +307,14 @@ mx4_decode_kernel(const DecodeParams p) {
     if (e < D * NT && h < G)
       q_raw[i] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) +
                                                  ((long long)it.row * p.Hq + it.g * G + h) * D + d);
-    if (e < D * NT && p.per_channel) {
+    if (FOLD && e < D * NT) {
       ks_raw[i][0] = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d);
       ks_raw[i][1] = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d + 4);
     }
   }
   float4 vs_raw;
   if (threadIdx.x < D / 4) {
-    if (p.per_channel)
+    if constexpr (FOLD)
       vs_raw = *reinterpret_cast<const float4*>(p.v_scale + it.g * D + 4 * threadIdx.x);
     else
       vs_raw.x = vs_raw.y = vs_raw.z = vs_raw.w = p.v_scale[0];
@@ -407,10 +410,10 @@ mx4_decode_kernel(const DecodeParams p) {
     const int h = e / (D / 8), d = 8 * (e % (D / 8));
     uint4 v = q_raw[i];
     float inv = 1.f;
-    if (p.per_channel) {
+    if constexpr (FOLD) {
       // one power of two per head taken out, so that the largest element is in
-      // [2^8, 2^9): nothing overflows fp16, and what goes below its normal range is
-      // less than 2^-22 of the largest
+      // [2^8, 2^9): nothing overflows fp16, and what the second number loses below fp16's
+      // smallest step is less than 2^-32 of the largest
       const float4 k0 = ks_raw[i][0], k1 = ks_raw[i][1];
       const __half2* q2 = reinterpret_cast<const __half2*>(&v);
       const float2 a0 = __half22float2(q2[0]), a1 = __half22float2(q2[1]);
@@ -426,8 +429,17 @@ mx4_decode_kernel(const DecodeParams p) {
       const bool scaled = ex >= 9 && ex < 255;
       const float up = scaled ? __int_as_float((262 - ex) << 23) : 1.f;
       inv = scaled ? __int_as_float((ex - 8) << 23) : 1.f;
-      v = make_uint4(pack_h2(x[0] * up, x[1] * up), pack_h2(x[2] * up, x[3] * up),
-                     pack_h2(x[4] * up, x[5] * up), pack_h2(x[6] * up, x[7] * up));
+      uint32_t hi[4], lo[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float y0 = x[2 * k] * up, y1 = x[2 * k + 1] * up;
+        hi[k] = pack_h2(y0, y1);
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[k]));
+        lo[k] = pack_h2(y0 - f.x, y1 - f.y);
+      }
+      v = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+      *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(smem + T::kQLo) + h * T::kQRow + d) =
+          make_uint4(lo[0], lo[1], lo[2], lo[3]);
     } else {
       inv = p.k_scale[0];
     }
@@ -456,6 +468,8 @@ mx4_decode_kernel(const DecodeParams p) {
     fac[nt][0] = sinv[8 * nt + 2 * tig];
     fac[nt][1] = sinv[8 * nt + 2 * tig + 1];
   }
+
+  const uint32_t q_lo = smem_addr(smem + T::kQLo) + (grp * T::kQRow + tig * (D / 4)) * 2;
 
   float acc[KC][NT][4];
   float base[NT][2], lrun[NT][2];
@@ -499,6 +513,7 @@ mx4_decode_kernel(const DecodeParams p) {
 #pragma unroll
     for (int s = 0; s < T::kSub; ++s) {
       const uint32_t r = rec0 + s * T::kRec;
+      float rest[NT][4];  // of the queries' second numbers
       uint32_t wa[KW], wb[KW];
       lds<KW>(r + k_off, wa);
       lds<KW>(r + k_off + 8 * (D / 2), wb);
@@ -522,7 +537,7 @@ mx4_decode_kernel(const DecodeParams p) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) sc[s][nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) sc[s][nt][e] = rest[nt][e] = 0.f;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {  // 8 channels of a lane: two steps
         uint32_t a[4], b[4];
@@ -537,7 +552,19 @@ mx4_decode_kernel(const DecodeParams p) {
         for (int nt = 0; nt < NT; ++nt) {
           mma16816(sc[s][nt], a[0], b[0], a[1], b[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
           mma16816(sc[s][nt], a[2], b[2], a[3], b[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
+          if constexpr (FOLD) {
+            uint32_t l[4];
+            lds<4>(q_lo + nt * 8 * T::kQRow * 2 + 16 * w, l);
+            mma16816(rest[nt], a[0], b[0], a[1], b[1], l[0], l[1]);
+            mma16816(rest[nt], a[2], b[2], a[3], b[3], l[2], l[3]);
+          }
         }
+      }
+      if constexpr (FOLD) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[s][nt][e] += rest[nt][e];
       }
     }
 
@@ -825,10 +852,10 @@ mx4_decode_kernel(const DecodeParams p) {
   }
 }
 
-template <int D, int NT, int W, bool CLUSTER>
-cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
+template <int D, int NT, int W, bool CLUSTER, bool FOLD>
+cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
   using T = Mx4Tile<D, NT, W>;
-  auto kern = mx4_decode_kernel<D, NT, W, CLUSTER>;
+  auto kern = mx4_decode_kernel<D, NT, W, CLUSTER, FOLD>;
   // the opt-in shared-memory size is a per-function attribute: set it once per device
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
@@ -883,6 +910,13 @@ cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
     cfg.numAttrs = 2;
   }
   return cudaLaunchKernelEx(&cfg, kern, p);
+}
+
+// (the occupancy the geometry uses is the folding kernel's, whatever the scales)
+template <int D, int NT, int W, bool CLUSTER>
+cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
+  return p.per_channel || info != nullptr ? run_mx4_with<D, NT, W, CLUSTER, true>(p, s, info)
+                                          : run_mx4_with<D, NT, W, CLUSTER, false>(p, s, info);
 }
 
 template <int W, bool CLUSTER>

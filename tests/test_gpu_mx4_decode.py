@@ -1,8 +1,9 @@
 """paged_decode_mx4 on the GPU against attention over the cache's values in 64 bits.
 
 Tolerances.  The cache's values are exact in the kernel's products.  What is rounded:
-  - Q * k_scale to fp16, where the scales are per channel (half a step: 2^-11 of each
-    element): every score moves by at most e = 2^-11 E, E = max_t sigma sum_d |q_d K_t,d|;
+  - Q * k_scale to two fp16 numbers, where the scales are per channel (the first is half a step,
+    2^-11, off, the second 2^-11 of that; 2^-20 with room for what the second loses below its
+    smallest step): every score moves by at most e = 2^-20 E, E = max_t sigma sum_d |q_d K_t,d|;
     so the probabilities change by a factor within e^(+-2 e), and the lse by e;
   - the probabilities to fp16 (2^-11 each), with those below 2^-24 of the largest rounded
     to a multiple of 2^-32 at worst;
@@ -73,7 +74,7 @@ def reference(c, softcap=0.0, window=-1):
 def compare(c, got, ref, softcap=0.0, what=""):
     (o, l), (O, L, W, E) = got, ref
     D = c["q"].shape[2]
-    e = 2.0 ** -11 * E if c["sk"] == 2 else 0.0 * E
+    e = 2.0 ** -20 * E if c["sk"] == 2 else 0.0 * E
     f = (D + 16) * 2.0 ** -23 * (E + softcap) + 1e-6
     tol = W * ((2.0 ** -11 + 2 * (e + f)) * (1 + 2.0 ** -6))[..., None] + 2.0 ** -11 * np.abs(O) + 2.0 ** -24
     assert np.isfinite(o).all(), what
