@@ -529,7 +529,8 @@ i8kv_status gather_cache(const int32_t* slot_mapping, int32_t num_rows, int32_t 
  * out (per channel scales; a scale per tensor is applied to the fp32 scores), so
  * its range is not limited, and I8KV_FLAG_QUERY_RANGE and I8KV_FLAG_FP32_PATH are
  * not raised; the probabilities are rounded to fp16 (by at most a relative
- * 2^-11), the sums are fp32.
+ * 2^-11), the sums are fp32.  A head whose query is not finite gives NaN outputs,
+ * the others of its group what they give without it.
  */
 i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* k_scale,
                              const float* v_scale, int32_t scale_kind,

@@ -830,6 +830,9 @@ i8kv_status reshape_and_cache(const uint16_t* k_new, const uint16_t* v_new,
   return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
 }
 
+// Elements of a token's row that 32-bit item numbers take with room to spare.
+static constexpr int64_t kMaxRow = 1 << 28;
+
 // What rope_and_cache and gather_cache check alike: the cache and its scales.
 static i8kv_status check_cache(const void* k_cache, const void* v_cache, int32_t cache_dtype,
                                int64_t num_slots, int32_t block_size, const float* k_scale,
@@ -839,6 +842,7 @@ static i8kv_status check_cache(const void* k_cache, const void* v_cache, int32_t
   if (cache_dtype < I8KV_CACHE_INT8 || cache_dtype > I8KV_CACHE_MX4) return I8KV_EINVAL;
   const bool mx4 = cache_dtype == I8KV_CACHE_MX4;
   if (D % 16 != 0 || (mx4 && !supported_head_dim(D))) return I8KV_EUNSUPPORTED;
+  if (static_cast<int64_t>(Hkv) * D > kMaxRow) return I8KV_EUNSUPPORTED;
   if (mx4) {
     if (block_size < 1 || v_cache != nullptr) return I8KV_EINVAL;
     if (block_size % 16 != 0) return I8KV_EUNSUPPORTED;
@@ -868,6 +872,7 @@ i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* 
                                v_scale, scale_kind, Hkv, D, num_tokens > 0);
   if (st != I8KV_OK) return st;
   if (rot_dim < 0 || rot_dim > D) return I8KV_EINVAL;
+  if (static_cast<int64_t>(Hq) * D > kMaxRow) return I8KV_EUNSUPPORTED;
   if (rot_dim % 16 != 0 || (cache_dtype == I8KV_CACHE_MX4 && rot_style == I8KV_ROPE_HALVES &&
                             rot_dim % 32 != 0))
     return I8KV_EUNSUPPORTED;

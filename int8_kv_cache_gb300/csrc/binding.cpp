@@ -9,8 +9,10 @@
 
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAFunctions.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 
+#include <optional>
 #include <string>
 
 #include "../../include/int8kv.h"
@@ -178,11 +180,21 @@ int32_t size32(int64_t v, const char* name) {
   return static_cast<int32_t>(v);
 }
 
-// The stream to work on: None is the current one, else a cudaStream_t as an int.
-void* stream_of(PyObject* o, int dev) {
-  if (o == Py_None) return c10::cuda::getCurrentCUDAStream(static_cast<c10::DeviceIndex>(dev)).stream();
-  return PyLong_AsVoidPtr(o);
-}
+// The stream to work on: None is the current one, else a cudaStream_t as an int, which
+// is then current for the outputs made here (their memory must not be in use on another).
+struct Stream {
+  void* handle;
+  std::optional<c10::cuda::CUDAStreamGuard> guard;
+  Stream(PyObject* o, int dev) {
+    const auto index = static_cast<c10::DeviceIndex>(dev);
+    if (o == Py_None) {
+      handle = c10::cuda::getCurrentCUDAStream(index).stream();
+    } else {
+      handle = PyLong_AsVoidPtr(o);
+      guard.emplace(c10::cuda::getStreamFromExternal(static_cast<cudaStream_t>(handle), index));
+    }
+  }
+};
 
 // The current device; a tensor on the host is refused before the device is asked for.
 int device_of(PyObject* o, const char* name) {
@@ -234,6 +246,7 @@ PyObject* py_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int style = PyObject_IsTrue(a[11]);
     if (style < 0) return nullptr;
     void* flags = dense(a[13], "flags", at::kInt, dev);
+    const Stream stream(a[14], dev);
     Rows q{nullptr, 0, 0};
     PyObject* out = a[12];
     at::Tensor made;
@@ -255,7 +268,7 @@ PyObject* py_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
         style ? I8KV_ROPE_INTERLEAVED : I8KV_ROPE_HALVES, static_cast<const int32_t*>(slots),
         size32(T, "T"), size32(q.heads, "Hq"), size32(c.Hkv, "Hkv"), size32(c.D, "D"),
         static_cast<uint16_t*>(qo), c.k, c.v, c.dtype, c.slots, c.block_size, s.k, s.v, kind,
-        static_cast<uint32_t*>(flags), stream_of(a[14], dev));
+        static_cast<uint32_t*>(flags), stream.handle);
     if (st != I8KV_OK) return status(st);
     if (made.defined()) return THPVariable_Wrap(made);
     return Py_NewRef(out);
@@ -281,6 +294,7 @@ PyObject* py_gather_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int32_t kind = int_of(a[5], "scale_kind");
     const Scales s = scales_of(a[3], a[4], kind, c, dev);
     void* flags = dense(a[8], "flags", at::kInt, dev);
+    const Stream stream(a[9], dev);
     const auto options = THPVariable_Unpack(a[1]).options().dtype(at::kHalf);
     at::Tensor made[2];
     void* p[2];
@@ -296,7 +310,7 @@ PyObject* py_gather_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const i8kv_status st = gather_cache(
         static_cast<const int32_t*>(slots), size32(N, "N"), size32(c.Hkv, "Hkv"), size32(c.D, "D"),
         c.k, c.v, c.dtype, c.slots, c.block_size, s.k, s.v, kind, static_cast<uint16_t*>(p[0]),
-        static_cast<uint16_t*>(p[1]), static_cast<uint32_t*>(flags), stream_of(a[9], dev));
+        static_cast<uint16_t*>(p[1]), static_cast<uint32_t*>(flags), stream.handle);
     if (st != I8KV_OK) return status(st);
     PyObject* r = PyTuple_New(2);
     if (r == nullptr) return nullptr;
@@ -345,6 +359,7 @@ PyObject* py_paged_decode_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
     void* flags = dense(a[14], "flags", at::kInt, dev);
     const int partials = PyObject_IsTrue(a[16]);
     if (partials < 0) return nullptr;
+    const Stream stream(a[15], dev);
     at::Tensor made;
     void* out = nullptr;
     if (!partials) {
@@ -362,7 +377,7 @@ PyObject* py_paged_decode_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         float_of(a[7], "softmax_scale"), static_cast<const float*>(sink), float_of(a[17], "softcap"),
         int_of(a[18], "window"), int_of(a[9], "num_splits"), int_of(a[10], "chunk"), ws, ws_bytes,
         static_cast<uint16_t*>(out), static_cast<float*>(lse), static_cast<uint32_t*>(flags),
-        stream_of(a[15], dev));
+        stream.handle);
     if (st != I8KV_OK) return status(st);
     if (made.defined()) return THPVariable_Wrap(made);
     return Py_NewRef(partials ? Py_None : a[12]);

@@ -1,11 +1,37 @@
-// Paged decode over an MX4 cache (4-bit e2m1 codes, an e4m3 scale per 16
-// channels): one new token per sequence, split over the cache's length; the
-// partials are joined by the combine kernel.
+// Paged decode over an MX4 cache (4-bit e2m1 codes, an e4m3 scale per 16 channels): one
+// new token per sequence, split over the cache's length and joined.
 //
-//   s_t = sigma * k_scale * sum_d q_d * (block scale * code)_t,d   (softcap, mask)
-//   partial of a piece: m = max s_t, l = sum e^(s_t - m), acc = v_scale sum e^(s_t - m) v_t
+// What it computes, for the G query heads of a KV head over the tokens t of a piece:
+//   s_t = sigma * k_scale * sum_d q_d * (block scale * code)_t,d    (softcap, mask)
+//   m = reference exponent, l = sum e^(s_t - m), acc = v_scale sum e^(s_t - m) v_t
+// and from the pieces of a row O = sum acc e^(m - M) / sum l e^(m - M), the sink, the lse.
 //
-// One warp per query head, lanes over channels, fp32 throughout.
+// Bound: HBM in bytes, the integer pipe in practice.  A record of 16 tokens is 18 D bytes
+// (2304 at head_dim 128) and one bulk copy into the ring of the warp that works on it: two
+// stages of two records per warp, 16 warps per SM, about 110 KB in flight.  At 6.8 TB/s an SM
+// gets a record every 98 cycles; what it issues for one is about 295 instructions (136 of them
+// for the integer pipe, which takes one every second cycle: 68 cycles of its four
+// schedulers' time), so instructions are what was worked on:
+//   - Matrix fragments straight from shared memory.  S = K Q'^T takes tokens as rows and a
+//     lane's 32 (head_dim 128) consecutive channels of a token as its part of the contraction:
+//     two 16-byte loads, no transposition; the queries are permuted to match.  O^T = V^T P^T
+//     takes channels as rows: a lane's 16 channels of four tokens, whose nibbles are paired
+//     across tokens with one shift and one select per 8 codes.
+//   - Codes to fp16 with one conversion per pair (64 a cycle and SM), times the block scale:
+//     code * scale has 6 significant bits, so the fp16 products are exact.
+//   - The exponent base of a head moves only when a score exceeds it by 15 bits, so a
+//     stage needs no shuffles: 2^8 .. 2^15 is the room that fp16 probabilities leave above
+//     the largest so far.  The probabilities are rounded to fp16 (relative 2^-11 at most; the
+//     output itself is fp16); their sum and everything accumulated is fp32.
+//   - Copy descriptions (address, attended tokens) are formed 32 tiles at a time, a lane each.
+// Measured on one GB300 (graph of calls, inputs larger than L2): 16 x 8192-32768 tokens, 32/8
+// heads, head_dim 128: 64.5 us, 5.04 TB/s, 74 % of the measured copy rate (integer pipe 55 %
+// of its cycles, issue 60 %).  Tried and slower there: one record per stage (78 us), three stages
+// (73), 8-warp CTAs (76), 5 CTAs per SM (71).
+//
+// Three ways over the work, chosen by the host from sizes alone (mx4_auto in api.cu): 4-warp
+// CTAs over balanced pieces or chunks of rows, joined by the combine kernel; clusters of
+// 8-warp CTAs per row and KV head, joined in distributed shared memory; one such CTA each.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -631,8 +657,9 @@ mx4_decode_kernel(const DecodeParams p) {
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-          // up by what the largest is above the room left; down too on the first scores
-          const float up = unset ? (any_live ? mx - kRoom : 0.f) : fmaxf(mx - kRoom, 0.f);
+          // up by what the largest is above the room left; down too on the first scores (a
+          // head of NaNs, which has no largest, keeps a finite base and a NaN sum)
+          const float up = unset ? (mx > neg_inf() ? mx - kRoom : 0.f) : fmaxf(mx - kRoom, 0.f);
           alpha[j] = unset ? 1.f : fast_exp2(-up);
           base[nt][j] += up;
         }

@@ -46,7 +46,7 @@ MX = dict(cd=4, vc=None)
     (dict(cs=P8), 3), (dict(pos=P2), 3), (dict(slots=P2), 3), (dict(kc=P8), 3), (dict(vc=P8), 3),
     (dict(flags=P2), 3), (dict(ksc=P8, kind=2), 3),
     (dict(MX, vc=P), 1), (dict(MX, bs=0), 1), (dict(MX, bs=24, ns=240), 2), (dict(MX, ns=120), 1),
-    (dict(MX, D=80, qs=640, ks=160, vs=160), 2), (dict(MX, R=48), 2), (dict(MX, R=16), 2),
+    (dict(Hkv=1 << 26), 2), (dict(Hq=1 << 26), 2), (dict(MX, D=80, qs=640, ks=160, vs=160), 2), (dict(MX, R=48), 2), (dict(MX, R=16), 2),
 ])
 def test_append_validation(K, kw, status):
     assert _append(K, **kw) == status

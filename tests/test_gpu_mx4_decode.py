@@ -382,3 +382,73 @@ def test_a_serving_loop_appends_and_attends(K):
             W = torch.einsum("hgt,thd->hgd", p, v.abs()).reshape(Hq, D)
             tol = 2.0 ** -10 * W + 2.0 ** -11 * want.abs() + 1e-5
             assert ((out[b].double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("per_channel", [False, True])
+def test_a_head_that_is_not_finite_spoils_itself_only(K, per_channel):
+    c = case(40, 2, 8, 1, 128, 16, 40, [600, 33], per_channel)
+    ref = reference(c)
+    c["q"][0, 2, 5], c["q"][0, 6, 7] = np.nan, np.inf
+    good = np.ones((2, 8), bool)
+    good[0, [2, 6]] = False
+    for ns, chunk in ((0, 0), (1, 640), (5, 0), (10, 64)):
+        o, l = run(K, c, ns=ns, chunk=chunk)
+        assert np.isnan(o[0, [2, 6]]).all()
+        pick = lambda x: x[good][None]
+        compare(dict(c, q=c["q"][good][None]), (pick(o), pick(l)), [pick(x) for x in ref], what=f"{ns} splits of {chunk}")
+
+
+def test_very_negative_scores_and_late_maxima(K):
+    # all scores far below zero; then rows whose scores climb towards the end, in steps beyond the room
+    c = case(41, 2, 4, 1, 64, 16, 40, [640, 500], per_channel=False, sigma=1.0)
+    c["q"] = (np.abs(c["q"].astype(np.float32)) * 20).astype(np.float16)
+    D = 64
+    for b in range(2):
+        for t in range(640):
+            blk, r = c["table"][b, t // 16], t % 16
+            row = c["cache"][blk, 0, 0]
+            row[r * D // 2:(r + 1) * D // 2] = 0xAA  # code -1.0 in every channel
+            row[8 * D + r * D // 16:8 * D + (r + 1) * D // 16] = 0x38 - (t // 100 if b else 0)
+    ref = reference(c)
+    assert ref[1].max() < -100
+    for ns, chunk in ((0, 0), (1, 640), (3, 0), (40 // 2, 32)):
+        compare(c, run(K, c, ns=ns, chunk=chunk), ref, what=f"{ns} splits of {chunk}")
+
+
+def test_an_explicit_stream(K):
+    c = case(42, 4, 8, 2, 128, 16, 20, [300, 17, 0, 320])
+    d = on_device(c)
+    want = run(K, c, d)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ws = workspace(K, 4, 8, 128)
+    torch.cuda.synchronize()
+    for stream in (s, s.cuda_stream):
+        out = K.paged_decode_mx4(d["q"], d["cache"], d["ks"], d["vs"], 2, d["table"], d["lens"], c["sigma"],
+                                 workspace=ws, stream=stream)
+        slots = torch.arange(40, dtype=torch.int32, device="cuda")
+        torch.cuda.synchronize()
+        k, v = K.gather_cache(slots, d["cache"], None, d["ks"], d["vs"], 2, stream=stream)
+        s.synchronize()
+        assert np.array_equal(out.double().cpu().numpy(), want[0])
+        k2, v2 = K.gather_cache(slots, d["cache"], None, d["ks"], d["vs"], 2)
+        assert torch.equal(k, k2) and torch.equal(v, v2)
+
+
+def test_two_streams_at_once(K):
+    # two batches decoded concurrently, each with its own workspace, many times
+    cs = [case(50 + i, 3, 16, 2, 128, 16, 60, [900, 100, 960]) for i in range(2)]
+    ds = [on_device(c) for c in cs]
+    wants = [run(K, c, d) for c, d in zip(cs, ds)]
+    ss = [torch.cuda.Stream() for _ in cs]
+    wss = [workspace(K, 3, 16, 128) for _ in cs]
+    outs = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for i, (c, d, s, ws) in enumerate(zip(cs, ds, ss, wss)):
+            with torch.cuda.stream(s):
+                outs[i].append(K.paged_decode_mx4(d["q"], d["cache"], d["ks"], d["vs"], 2, d["table"], d["lens"],
+                                                  c["sigma"], workspace=ws))
+    torch.cuda.synchronize()
+    for o, w in zip(outs, wants):
+        assert all(np.array_equal(x.double().cpu().numpy(), w[0]) for x in o)
