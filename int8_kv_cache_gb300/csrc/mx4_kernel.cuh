@@ -274,11 +274,16 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   return v;
 }
 
-// W warps.  FOLD: scales per channel, folded into the queries, which then take two fp16
-// numbers each (22 bits: rounding them to one would move the scores by as much as all
-// else together).  CLUSTER: the p.num_splits CTAs of a cluster share one (row, KV head), its tiles
+// How the scales come in.  kPlain: one per tensor, applied to the scores.  Per channel they are
+// folded into the queries, which then take two fp16 numbers each (22 bits: rounding them to
+// one would move the scores by as much as all else together): with at most 4 heads the
+// second numbers are the idle columns 4 .. 7 of the product and are added with a shuffle
+// (kColumns), else they take products of their own (kProducts).
+enum Fold { kPlain = 0, kProducts = 1, kColumns = 2 };
+
+// W warps.  CLUSTER: the p.num_splits CTAs of a cluster share one (row, KV head), its tiles
 // dealt to their warps in turn, and join through distributed shared memory.
-template <int D, int NT, int W, bool CLUSTER, bool FOLD>
+template <int D, int NT, int W, bool CLUSTER, Fold FOLD>
 __global__ void __launch_bounds__(32 * W, (Mx4Tile<D, NT, W>::kBlocks))
 mx4_decode_kernel(const DecodeParams p) {
   using T = Mx4Tile<D, NT, W>;
@@ -333,14 +338,14 @@ mx4_decode_kernel(const DecodeParams p) {
     if (e < D * NT && h < G)
       q_raw[i] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) +
                                                  ((long long)it.row * p.Hq + it.g * G + h) * D + d);
-    if (FOLD && e < D * NT) {
+    if (FOLD != kPlain && e < D * NT) {
       ks_raw[i][0] = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d);
       ks_raw[i][1] = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d + 4);
     }
   }
   float4 vs_raw;
   if (threadIdx.x < D / 4) {
-    if constexpr (FOLD)
+    if constexpr (FOLD != kPlain)
       vs_raw = *reinterpret_cast<const float4*>(p.v_scale + it.g * D + 4 * threadIdx.x);
     else
       vs_raw.x = vs_raw.y = vs_raw.z = vs_raw.w = p.v_scale[0];
@@ -436,7 +441,7 @@ mx4_decode_kernel(const DecodeParams p) {
     const int h = e / (D / 8), d = 8 * (e % (D / 8));
     uint4 v = q_raw[i];
     float inv = 1.f;
-    if constexpr (FOLD) {
+    if constexpr (FOLD != kPlain) {
       // one power of two per head taken out, so that the largest element is in
       // [2^8, 2^9): nothing overflows fp16, and what the second number loses below fp16's
       // smallest step is less than 2^-32 of the largest
@@ -464,8 +469,14 @@ mx4_decode_kernel(const DecodeParams p) {
         lo[k] = pack_h2(y0 - f.x, y1 - f.y);
       }
       v = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-      *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(smem + T::kQLo) + h * T::kQRow + d) =
-          make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      const uint4 rest = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+      if constexpr (FOLD == kColumns) {
+        if (h >= 4) continue;  // (the first four heads' threads fill these)
+        *reinterpret_cast<uint4*>(sq + (h + 4) * T::kQRow + d) = rest;
+        if (d == 0) sinv[h + 4] = inv * (p.softcap > 0.f ? p.sigma : p.sigma * kLog2e);
+      } else {
+        *reinterpret_cast<uint4*>(reinterpret_cast<__half*>(smem + T::kQLo) + h * T::kQRow + d) = rest;
+      }
     } else {
       inv = p.k_scale[0];
     }
@@ -578,7 +589,7 @@ mx4_decode_kernel(const DecodeParams p) {
         for (int nt = 0; nt < NT; ++nt) {
           mma16816(sc[s][nt], a[0], b[0], a[1], b[1], qf[nt][2 * w][0], qf[nt][2 * w][1]);
           mma16816(sc[s][nt], a[2], b[2], a[3], b[3], qf[nt][2 * w + 1][0], qf[nt][2 * w + 1][1]);
-          if constexpr (FOLD) {
+          if constexpr (FOLD == kProducts) {
             uint32_t l[4];
             lds<4>(q_lo + nt * 8 * T::kQRow * 2 + 16 * w, l);
             mma16816(rest[nt], a[0], b[0], a[1], b[1], l[0], l[1]);
@@ -586,12 +597,14 @@ mx4_decode_kernel(const DecodeParams p) {
           }
         }
       }
-      if constexpr (FOLD) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+      for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[s][nt][e] += rest[nt][e];
-      }
+        for (int e = 0; e < 4; ++e) {
+          if constexpr (FOLD == kProducts) sc[s][nt][e] += rest[nt][e];
+          // (both columns of a head then hold its score; only the first is read in the end)
+          if constexpr (FOLD == kColumns) sc[s][nt][e] += __shfl_xor_sync(0xffffffffu, sc[s][nt][e], 2);
+        }
     }
 
     // ---- online softmax: the exponent base of a head moves only when a score leaves the
@@ -879,7 +892,7 @@ mx4_decode_kernel(const DecodeParams p) {
   }
 }
 
-template <int D, int NT, int W, bool CLUSTER, bool FOLD>
+template <int D, int NT, int W, bool CLUSTER, Fold FOLD>
 cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
   using T = Mx4Tile<D, NT, W>;
   auto kern = mx4_decode_kernel<D, NT, W, CLUSTER, FOLD>;
@@ -939,11 +952,15 @@ cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// (the occupancy the geometry uses is the folding kernel's, whatever the scales)
+// (the occupancy the geometry uses is one kernel's, whatever the scales)
 template <int D, int NT, int W, bool CLUSTER>
 cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
-  return p.per_channel || info != nullptr ? run_mx4_with<D, NT, W, CLUSTER, true>(p, s, info)
-                                          : run_mx4_with<D, NT, W, CLUSTER, false>(p, s, info);
+  if (info != nullptr) return run_mx4_with<D, NT, W, CLUSTER, kProducts>(p, s, info);
+  if (!p.per_channel) return run_mx4_with<D, NT, W, CLUSTER, kPlain>(p, s, info);
+  if constexpr (NT == 1) {
+    if (p.G <= 4) return run_mx4_with<D, NT, W, CLUSTER, kColumns>(p, s, info);
+  }
+  return run_mx4_with<D, NT, W, CLUSTER, kProducts>(p, s, info);
 }
 
 template <int W, bool CLUSTER>
