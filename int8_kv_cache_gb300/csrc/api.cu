@@ -214,14 +214,34 @@ i8kv_status plan(const KernelKey& key, int64_t cap, int32_t units, int32_t mode,
   return I8KV_OK;
 }
 
-// Whether the MX4 decode takes `units` clusters of c CTAs (a power of two, at most
-// kMx4MaxCluster) with all of them resident at once; a single CTA always.
-i8kv_status mx4_clusters(KernelKey key, int32_t units, int32_t c, bool* fits) {
+// Whether the MX4 decode takes `units` (row, KV head) pairs as clusters of c CTAs (a power of
+// two, at most kMx4MaxCluster) with all of them resident at once; a single CTA always.  *run is
+// the kernel: groups of more than 8 query heads run as two units of half of them each
+// (*groups = 2) where those are resident too, on the kernel for at most 8, which takes a
+// tile in about two thirds of the time (8 rows x 2 groups of 12 heads, head_dim 256, 2064
+// tokens: 13.2 us in one unit, 10.3 for half of it; the keys and values come from L2 twice).
+i8kv_status mx4_clusters(const KernelKey& key, int32_t units, int32_t c, bool* fits, KernelKey* run,
+                         int32_t* groups) {
+  *run = key;
+  run->cluster = true;
+  *groups = 1;
   *fits = c == 1;
-  if (c < 2 || c > i8kv::kMx4MaxCluster || (c & (c - 1)) != 0) return I8KV_OK;
-  key.cluster = true;
+  if (c < 1 || c > i8kv::kMx4MaxCluster || (c & (c - 1)) != 0) return I8KV_OK;
   WaveInfo w{0, 0};
-  const i8kv_status st = wave_of(key, &w);
+  i8kv_status st;
+  if (key.nt == 2) {
+    KernelKey half = *run;
+    half.nt = 1;
+    if ((st = wave_of(half, &w)) != I8KV_OK) return st;
+    if (2LL * units <= w.clusters[log2_of(c)]) {
+      *run = half;
+      *groups = 2;
+      *fits = true;
+      return I8KV_OK;
+    }
+  }
+  if (c == 1) return I8KV_OK;
+  st = wave_of(*run, &w);
   *fits = units <= w.clusters[log2_of(c)];
   return st;
 }
@@ -230,16 +250,17 @@ i8kv_status mx4_clusters(KernelKey key, int32_t units, int32_t c, bool* fits) {
 // row and KV head is one CTA of 8 warps, or a cluster of 2, 4 or 8 of them that join
 // without a second kernel (the fewest CTAs that leave a warp 2 tiles of 16 tokens, all
 // clusters resident at once),
-//   - where that gives a warp at most 8 tiles, 4 at head_dim 256 (16 rows x 2 KV
-//     heads of 2600 tokens: 9.7 us against 11.7 for pieces; 8 x 2 heads of 4096 at
-//     head_dim 256: 18.7 against 16.9, hence the 4), or
+//   - where that gives a warp at most 8 tiles (16 rows x 2 KV heads of 2600 tokens:
+//     9.7 us against 11.7 for pieces; 8 x 2 groups of 12 heads of 4096 at head_dim 256:
+//     14.1 against 17.1), 6 at head_dim 256 in clusters of 8 (4 x 2 such groups of 8000: 18.7
+//     against 15.7), or
 //   - where the rows and heads alone fill the GPU and spans are at most 8192 tokens,
 //     so that a long row among short ones is not what is waited for (128 rows x 8 heads
 //     of 128 to 4096 tokens: 79 us against 96; 32 x 8 heads, which do not fill it,
 //     of 128 to 2048: 17.9 against 16.4).
 // Else balanced pieces, twice the wave rule's count as partial slots, and the join
 // kernel (about 3 us).
-constexpr int64_t kMx4WarpTiles = 8;
+constexpr int64_t kMx4WarpTiles = 8, kMx4WarpTilesWide = 6;
 constexpr int64_t kMx4RowTiles = 512;
 i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t* ns,
                      int32_t* chunk) {
@@ -247,14 +268,20 @@ i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t*
   KernelKey one = key;
   one.cluster = true;
   WaveInfo w{0, 0};
-  const i8kv_status st = wave_of(one, &w);
+  i8kv_status st = wave_of(one, &w);
   if (st != I8KV_OK) return st;
   const bool fills = units >= w.clusters[0] && tiles <= kMx4RowTiles;
-  int32_t c = 1;
-  while (!fills && c < i8kv::kMx4MaxCluster && c * i8kv::kMx4ClusterWarps * 2 < tiles &&
-         units <= w.clusters[log2_of(2 * c)])
+  int32_t c = 1, groups = 1;
+  bool fits = false;
+  if ((st = mx4_clusters(key, units, 1, &fits, &one, &groups)) != I8KV_OK) return st;
+  while (!fills && c < i8kv::kMx4MaxCluster && c * i8kv::kMx4ClusterWarps * 2 < tiles) {
+    int32_t more = 1;
+    if ((st = mx4_clusters(key, units, 2 * c, &fits, &one, &more)) != I8KV_OK) return st;
+    // (two units of half the heads in smaller clusters are faster than one in larger ones)
+    if (!fits || more < groups) break;
     c *= 2;
-  const int64_t most = key.D > 128 ? kMx4WarpTiles / 2 : kMx4WarpTiles;
+  }
+  const int64_t most = key.D > 128 && c == i8kv::kMx4MaxCluster ? kMx4WarpTilesWide : kMx4WarpTiles;
   if (fills || tiles <= most * i8kv::kMx4ClusterWarps * c) {
     *ns = c;
     *chunk = c > 1 ? 0 : static_cast<int32_t>(std::max<int64_t>(16, tiles * 16));
@@ -764,20 +791,21 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
   p.softcap = softcap;
   p.window = window;
   // one split, and balanced pieces that fit clusters, join inside the kernel
-  bool cluster = num_splits == 1;
+  if (num_splits == 1 || (p.balanced && out != nullptr)) {
+    bool fits = false;
+    KernelKey ckey;
+    if ((st = mx4_clusters(key, units, num_splits, &fits, &ckey, &p.head_groups)) != I8KV_OK)
+      return st;
+    if (fits) {
+      const cudaError_t e = launch_key(ckey, p, static_cast<cudaStream_t>(stream), nullptr);
+      return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
+    }
+  }
   if (p.balanced) {
-    if ((st = mx4_clusters(key, units, num_splits, &cluster)) != I8KV_OK) return st;
-    cluster = cluster && out != nullptr;
     WaveInfo w{0, 0};
     if ((st = wave_of(key, &w)) != I8KV_OK) return st;
     // (at least one piece per row and KV head, and one to spare)
     p.bal_pieces = std::max(w.wave, units + std::max(w.wave / 2, Hkv));
-  }
-  if (cluster) {
-    KernelKey ckey = key;
-    ckey.cluster = true;
-    const cudaError_t e = launch_key(ckey, p, static_cast<cudaStream_t>(stream), nullptr);
-    return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
   }
   return run(key, p, static_cast<cudaStream_t>(stream));
 }

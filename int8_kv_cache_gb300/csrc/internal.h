@@ -43,6 +43,7 @@ struct DecodeParams {
   // num_splits per row (the partial slots), bal_pieces (row, piece) pairs in
   // all, each a multiple of bal_round positions; the grid has
   // ceil(num_splits / 2) CTAs per unit (decode_kernel.cuh, balanced_item)
+  int32_t head_groups;       // MX4 clusters: 2: each half of a group's query heads is a unit of its own
   int32_t balanced;
   int32_t bal_round;
   int32_t bal_pieces;

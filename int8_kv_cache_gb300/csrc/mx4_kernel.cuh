@@ -295,13 +295,19 @@ mx4_decode_kernel(const DecodeParams p) {
   grid_dependency_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int grp = lane >> 2, tig = lane & 3;
-  const int G = p.G;
+  int G = p.G, h0 = 0;  // the query heads h0 .. h0 + G - 1 of the group are this CTA's
   const int rpb = p.bs >> 4;  // records per block
   auto block_of = [&](int tile) { return p.bs_log2 >= 4 ? tile >> (p.bs_log2 - 4) : quotient(tile, rpb); };
   Mx4Item it;
   if constexpr (CLUSTER) {
     it.unit = blockIdx.x / p.num_splits;
     it.slot = blockIdx.x - it.unit * p.num_splits;
+    if (p.head_groups == 2) {
+      const int half = (p.G + 1) >> 1;
+      h0 = it.unit & 1 ? half : 0;
+      G = it.unit & 1 ? p.G - half : half;
+      it.unit >>= 1;
+    }
     it.row = it.unit / p.Hkv;
     it.g = it.unit - it.row * p.Hkv;
     it.stride = W * p.num_splits;
@@ -337,7 +343,7 @@ mx4_decode_kernel(const DecodeParams p) {
     q_raw[i] = make_uint4(0u, 0u, 0u, 0u);
     if (e < D * NT && h < G)
       q_raw[i] = *reinterpret_cast<const uint4*>(static_cast<const __half*>(p.q) +
-                                                 ((long long)it.row * p.Hq + it.g * G + h) * D + d);
+                                                 ((long long)it.row * p.Hq + it.g * p.G + h0 + h) * D + d);
     if (FOLD != kPlain && e < D * NT) {
       ks_raw[i][0] = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d);
       ks_raw[i][1] = *reinterpret_cast<const float4*>(p.k_scale + it.g * D + d + 4);
@@ -351,7 +357,7 @@ mx4_decode_kernel(const DecodeParams p) {
       vs_raw.x = vs_raw.y = vs_raw.z = vs_raw.w = p.v_scale[0];
   }
   float sink_raw = 0.f;
-  if (p.sink != nullptr && threadIdx.x < G) sink_raw = p.sink[it.g * G + threadIdx.x];
+  if (p.sink != nullptr && threadIdx.x < G) sink_raw = p.sink[it.g * p.G + h0 + threadIdx.x];
 
   if constexpr (CLUSTER) {
     it.hi = min(max(live, 0), p.max_blocks * p.bs);
@@ -799,7 +805,7 @@ mx4_decode_kernel(const DecodeParams p) {
   // a join kernel may be launched now: its CTAs wait for this grid's writes
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __syncthreads();
-  const long long head0 = (long long)it.row * p.Hq + it.g * G;
+  const long long head0 = (long long)it.row * p.Hq + it.g * p.G + h0;
   // the normalised output of 4 channels of head h, or zeros without a score
   auto finish = [&](int h, int d, float4 o, float M, float L) {
     const bool some = !(L <= 0.f);  // (a NaN sum is not an empty one)
@@ -930,7 +936,7 @@ cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info
     }
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&info->occupancy, kern, 32 * W, T::kSmem);
   }
-  const long long units = (long long)p.rows * p.Hkv;
+  const long long units = (long long)p.rows * p.Hkv * (CLUSTER && p.head_groups == 2 ? 2 : 1);
   long long ctas = units * p.num_splits;
   if (!CLUSTER && p.balanced && ctas > p.bal_pieces) ctas = p.bal_pieces;
   cudaLaunchConfig_t cfg = {};
@@ -958,7 +964,8 @@ cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
   if (info != nullptr) return run_mx4_with<D, NT, W, CLUSTER, kProducts>(p, s, info);
   if (!p.per_channel) return run_mx4_with<D, NT, W, CLUSTER, kPlain>(p, s, info);
   if constexpr (NT == 1) {
-    if (p.G <= 4) return run_mx4_with<D, NT, W, CLUSTER, kColumns>(p, s, info);
+    if ((p.head_groups == 2 ? (p.G + 1) / 2 : p.G) <= 4)
+      return run_mx4_with<D, NT, W, CLUSTER, kColumns>(p, s, info);
   }
   return run_mx4_with<D, NT, W, CLUSTER, kProducts>(p, s, info);
 }
