@@ -21,6 +21,10 @@
 // Queries take several heads of a token per thread (they share the sines and
 // cosines: 64 of the 192 bytes that a head would load).  An MX4 block of 16 channels is
 // one piece of each of two neighbouring lanes, which exchange their maxima.
+// Measured on one GB300 (graph of calls): 32768 tokens, 32/8 heads, head_dim 128, all of it
+// turned, into MX4: 132 us for 726 MB, 5.5 TB/s, 81 % of the measured copy rate (not turned:
+// 117 us, 89 %); 16 tokens 2.6 us.  What is short of the rate are loads in flight, at 16
+// warps per SM; more per thread (rows a token ahead, a shared-memory ring) measured no faster.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -131,8 +135,8 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8], const float (&r)[8]
   return make_uint2(w[0], w[1]);
 }
 
-// The two pieces of item j of a row: channels c0 .. c0 + 7 and c1 .. c1 + 7, and, where
-// they are turned, the angles (pairs) of each: index ta of the first and tb of the second.
+// The two pieces of item j of a row: channels c0 .. c0 + 7 and c1 .. c1 + 7, and whether
+// they are turned.
 struct Pieces {
   int c0, c1;
   bool turned;
@@ -397,6 +401,8 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
 // Read-back: a thread keeps 8 channels of a head, for keys and values alike (one slot,
 // one address, two rows), with their scales, and walks the rows a few at a time: the
 // slots of the next ones are on their way while these are converted; 16-byte stores.
+// Bound: HBM writes.  16384 MX4 rows of 8 heads, head_dim 128: 19.0 us for 19 MB read and
+// 67 MB written (a plain fill of 67 MB: 17.1 us); 1 or 4 rows at a time 19.6 and 28 us.
 constexpr int kGatherRows = 2;
 
 // fp16 values of 8 channels: codes raw, block scale byte bs, scales sc.

@@ -144,6 +144,30 @@ def test_other_sizes(K, kind, D, R, bs):
         check(K, make(D, kind, 40, 2, 3, D, R, True, nb=5, bs=bs), il)
 
 
+@pytest.mark.parametrize("D,R", [(64, 16), (64, 48), (128, 80), (256, 144)])
+def test_blocks_of_a_range_that_is_no_multiple_of_32(K, D, R):
+    check(K, make(D + R, "mx4", 40, 3, 2, D, R, True), True)
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_many_tokens_store_what_few_at_a_time_store(K, kind, interleaved):
+    # enough tokens for four query heads per thread and several tokens per thread, 6 heads (a
+    # group and a half), in place; against calls of 90 tokens, one head per thread
+    T = 8001
+    c = make(21, kind, T, 6, 2, 64, 32, True, nb=510, max_pos=900)
+    d, e = on_device(c), on_device(c)
+    d["pos"][77], e["pos"][77] = 900, 900
+    got = append(K, c, d, interleaved=interleaved, q_out=d["q"])
+    for i in range(0, T, 90):
+        f = {n: (x[i:i + 90] if n in ("q", "k", "v", "pos", "slots") else x) for n, x in e.items()}
+        append(K, c, f, interleaved=interleaved, q_out=f["q"])
+    for a, b in ((got, e["q"]), (d["kc"], e["kc"]), (d["vc"], e["vc"])):
+        if a is not None:
+            bits = lambda x: x.view(torch.int16) if x.dtype == torch.float16 else x
+            assert torch.equal(bits(a), bits(b))
+
+
 @pytest.mark.parametrize("kind", KINDS)
 def test_a_larger_batch(K, kind):
     # several tokens per thread: 1500 tokens against the oracle on every head
