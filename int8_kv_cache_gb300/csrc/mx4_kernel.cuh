@@ -38,6 +38,7 @@
 #include <cuda_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "../../include/int8kv.h"
 #include "codes.cuh"
@@ -540,21 +541,18 @@ mx4_decode_kernel(const DecodeParams p) {
   bool unset = true;  // no score yet: the bases are not set
   bool timeout = false;
 
-  int k = 0;
-#pragma unroll 1
-  for (; k < stages; ++k) {
+  // The first N records of stage k; false if they did not arrive.
+  auto work = [&](auto records, int k) -> bool {
+    constexpr int N = decltype(records)::value;
     const int st = k % T::kStages;
     const bool ok = tc::mbar_wait(bars + st * 8, (k / T::kStages) & 1);
-    if (!__all_sync(0xffffffffu, ok)) {
-      timeout = true;
-      break;
-    }
+    if (!__all_sync(0xffffffffu, ok)) return false;
     const uint32_t rec0 = ring + st * T::kStageBytes;
 
     // ---- S = K Q'^T, one 16-token tile at a time ----
-    float sc[T::kSub][NT][4];
+    float sc[N][NT][4];
 #pragma unroll
-    for (int s = 0; s < T::kSub; ++s) {
+    for (int s = 0; s < N; ++s) {
       const uint32_t r = rec0 + s * T::kRec;
       float rest[NT][4];  // of the queries' second numbers
       uint32_t wa[KW], wb[KW];
@@ -615,20 +613,20 @@ mx4_decode_kernel(const DecodeParams p) {
 
     // ---- online softmax: the exponent base of a head moves only when a score leaves the
     // range that the fp16 probabilities cover ----
-    int mask[T::kSub], all = 0xFFFF, live_any = 0;
+    int mask[N], all = 0xFFFF, live_any = 0;
 #pragma unroll
-    for (int s = 0; s < T::kSub; ++s) {
+    for (int s = 0; s < N; ++s) {
       mask[s] = masks[st * T::kSub + s];
       all &= mask[s];
       live_any |= mask[s];
     }
     const bool partial = all != 0xFFFF, any_live = live_any != 0;  // uniform
     // z: scores less the head's base, in log2 units
-    float z[T::kSub][NT][4];
+    float z[N][NT][4];
     auto scores_less_base = [&]() {
       if (p.softcap > 0.f) {
 #pragma unroll
-        for (int s = 0; s < T::kSub; ++s)
+        for (int s = 0; s < N; ++s)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -637,7 +635,7 @@ mx4_decode_kernel(const DecodeParams p) {
                                  -base[nt][e & 1]);
       } else {
 #pragma unroll
-        for (int s = 0; s < T::kSub; ++s)
+        for (int s = 0; s < N; ++s)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -646,7 +644,7 @@ mx4_decode_kernel(const DecodeParams p) {
       }
       if (partial) {
 #pragma unroll
-        for (int s = 0; s < T::kSub; ++s) {
+        for (int s = 0; s < N; ++s) {
           const bool upper = (mask[s] >> tok) & 1, lower = (mask[s] >> (tok + 8)) & 1;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
@@ -659,7 +657,7 @@ mx4_decode_kernel(const DecodeParams p) {
     scores_less_base();
     float top = neg_inf();
 #pragma unroll
-    for (int s = 0; s < T::kSub; ++s)
+    for (int s = 0; s < N; ++s)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -672,7 +670,7 @@ mx4_decode_kernel(const DecodeParams p) {
         for (int j = 0; j < 2; ++j) {
           float mx = neg_inf();
 #pragma unroll
-          for (int s = 0; s < T::kSub; ++s) mx = fmaxf(mx, fmaxf(z[s][nt][j], z[s][nt][2 + j]));
+          for (int s = 0; s < N; ++s) mx = fmaxf(mx, fmaxf(z[s][nt][j], z[s][nt][2 + j]));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
           mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
@@ -696,16 +694,16 @@ mx4_decode_kernel(const DecodeParams p) {
       scores_less_base();
       // (a score so large that its own rounding exceeds the room still fits fp16)
 #pragma unroll
-      for (int s = 0; s < T::kSub; ++s)
+      for (int s = 0; s < N; ++s)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             if (z[s][nt][e] > kHead) z[s][nt][e] = kHead;
     }
-    uint32_t ph[T::kSub][NT][2];
+    uint32_t ph[N][NT][2];
 #pragma unroll
-    for (int s = 0; s < T::kSub; ++s)
+    for (int s = 0; s < N; ++s)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float pr[4];
@@ -720,7 +718,7 @@ mx4_decode_kernel(const DecodeParams p) {
 
     // ---- O^T += V^T P^T: rows are the channels of group grp, D / 8 from grp D / 8 ----
 #pragma unroll
-    for (int s = 0; s < T::kSub; ++s) {
+    for (int s = 0; s < N; ++s) {
       const uint32_t r = rec0 + s * T::kRec;
       uint32_t v[4][VW];  // tokens tig, tig + 4, tig + 8, tig + 12
       uint32_t x[4];      // their block scales
@@ -768,6 +766,19 @@ mx4_decode_kernel(const DecodeParams p) {
     }
     __syncwarp();  // every lane has read the stage
     if (k + T::kStages < stages) issue(k + T::kStages, st);
+    return true;
+  };
+  const int full = mine / T::kSub;  // stages of kSub records; an odd record at the end is worked alone
+  int k = 0;
+#pragma unroll 1
+  for (; k < full; ++k) {
+    if (!work(std::integral_constant<int, T::kSub>{}, k)) {
+      timeout = true;
+      break;
+    }
+  }
+  if constexpr (T::kSub > 1) {
+    if (!timeout && k < stages) timeout = !work(std::integral_constant<int, 1>{}, k);
   }
   if (timeout) {
     // the copies still in flight must not land in memory that others use
