@@ -105,7 +105,7 @@ i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
   if (e != cudaSuccess) return cuda_fail(e);
   const auto k = std::make_tuple(dev, static_cast<int>(key.path), key.D, key.nt,
                                  static_cast<int>(key.fp16_cache), static_cast<int>(key.fp8_cache),
-                                 static_cast<int>(key.p_lo), key.mx4_cache + 2 * key.cluster);
+                                 static_cast<int>(key.p_lo), key.mx4_cache + 2 * key.cluster + 4 * key.per_channel);
   {
     std::lock_guard<std::mutex> lock(mu);
     auto it = cache.find(k);
@@ -118,6 +118,8 @@ i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
   e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return cuda_fail(e);
   DecodeParams dummy{};
+  dummy.per_channel = key.per_channel;
+  dummy.G = 8 * key.nt;
   KernelInfo info{};
   e = launch_key(key, dummy, nullptr, &info);
   if (e != cudaSuccess) return cuda_fail(e);
@@ -803,7 +805,9 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
   }
   if (p.balanced) {
     WaveInfo w{0, 0};
-    if ((st = wave_of(key, &w)) != I8KV_OK) return st;
+    KernelKey own = key;  // (the plan, which does not know the scales, sets the slots only)
+    own.per_channel = p.per_channel;
+    if ((st = wave_of(own, &w)) != I8KV_OK) return st;
     // (at least one piece per row and KV head, and one to spare)
     p.bal_pieces = std::max(w.wave, units + std::max(w.wave / 2, Hkv));
   }

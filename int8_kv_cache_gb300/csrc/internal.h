@@ -63,6 +63,7 @@ struct KernelKey {
   bool p_lo;       // probability tile as fp16 high + low parts
   bool mx4_cache = false;  // 4-bit records (mx4_kernel.cuh; DecodeParams::k is the record cache)
   bool cluster = false;    // mx4_cache: a cluster of num_splits CTAs per (row, KV head)
+  bool per_channel = false;  // mx4_cache, KernelInfo only: the kernel for scales per channel
 };
 
 // What the geometry needs to know of a decode kernel instantiation.

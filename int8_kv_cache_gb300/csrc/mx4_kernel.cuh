@@ -282,10 +282,17 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
 // (kColumns), else they take products of their own (kProducts).
 enum Fold { kPlain = 0, kProducts = 1, kColumns = 2 };
 
+// Resident CTAs per SM the registers are cut for.  The separate products of two head groups
+// at head_dim 128 spill at three (16 x 16000 tokens, 64/4 heads: 72 us; 56 at two).
+template <int D, int NT, int W, Fold FOLD>
+constexpr int mx4_blocks() {
+  return FOLD == kProducts && NT == 2 && D == 128 && W == 4 ? 2 : Mx4Tile<D, NT, W>::kBlocks;
+}
+
 // W warps.  CLUSTER: the p.num_splits CTAs of a cluster share one (row, KV head), its tiles
 // dealt to their warps in turn, and join through distributed shared memory.
 template <int D, int NT, int W, bool CLUSTER, Fold FOLD>
-__global__ void __launch_bounds__(32 * W, (Mx4Tile<D, NT, W>::kBlocks))
+__global__ void __launch_bounds__(32 * W, (mx4_blocks<D, NT, W, FOLD>()))
 mx4_decode_kernel(const DecodeParams p) {
   using T = Mx4Tile<D, NT, W>;
   constexpr int kThreads = 32 * W;
@@ -554,7 +561,7 @@ mx4_decode_kernel(const DecodeParams p) {
 #pragma unroll
     for (int s = 0; s < N; ++s) {
       const uint32_t r = rec0 + s * T::kRec;
-      float rest[NT][4];  // of the queries' second numbers
+      float rest[NT][4];  // of the queries' second numbers (a chain of their own, where registers allow)
       uint32_t wa[KW], wb[KW];
       lds<KW>(r + k_off, wa);
       lds<KW>(r + k_off + 8 * (D / 2), wb);
@@ -596,8 +603,9 @@ mx4_decode_kernel(const DecodeParams p) {
           if constexpr (FOLD == kProducts) {
             uint32_t l[4];
             lds<4>(q_lo + nt * 8 * T::kQRow * 2 + 16 * w, l);
-            mma16816(rest[nt], a[0], b[0], a[1], b[1], l[0], l[1]);
-            mma16816(rest[nt], a[2], b[2], a[3], b[3], l[2], l[3]);
+            float(&to)[4] = NT == 1 ? rest[nt] : sc[s][nt];
+            mma16816(to, a[0], b[0], a[1], b[1], l[0], l[1]);
+            mma16816(to, a[2], b[2], a[3], b[3], l[2], l[3]);
           }
         }
       }
@@ -605,7 +613,7 @@ mx4_decode_kernel(const DecodeParams p) {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          if constexpr (FOLD == kProducts) sc[s][nt][e] += rest[nt][e];
+          if constexpr (FOLD == kProducts && NT == 1) sc[s][nt][e] += rest[nt][e];
           // (both columns of a head then hold its score; only the first is read in the end)
           if constexpr (FOLD == kColumns) sc[s][nt][e] += __shfl_xor_sync(0xffffffffu, sc[s][nt][e], 2);
         }
@@ -969,10 +977,8 @@ cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-// (the occupancy the geometry uses is one kernel's, whatever the scales)
 template <int D, int NT, int W, bool CLUSTER>
 cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
-  if (info != nullptr) return run_mx4_with<D, NT, W, CLUSTER, kProducts>(p, s, info);
   if (!p.per_channel) return run_mx4_with<D, NT, W, CLUSTER, kPlain>(p, s, info);
   if constexpr (NT == 1) {
     if ((p.head_groups == 2 ? (p.G + 1) / 2 : p.G) <= 4)
