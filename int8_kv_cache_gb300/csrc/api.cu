@@ -250,10 +250,12 @@ i8kv_status mx4_clusters(const KernelKey& key, int32_t units, int32_t c, bool* f
 
 // The automatic geometry of the MX4 decode, from the wave rule's count *ns.  A
 // row and KV head is one CTA of 8 warps, or a cluster of 2, 4 or 8 of them that join
-// without a second kernel (the fewest CTAs that leave a warp 2 tiles of 16 tokens, all
+// without a second kernel (as many as leave each warp a tile of 16 tokens while every CTA has
+// an SM of its own, 7 tiles where they share: 1 row x 8 heads of 300 tokens 4.9 us in 4
+// CTAs each, 5.4 in 2; 16 rows x 2 heads of 2600 8.2 us in 4, one per SM, 9.0 in 8; all
 // clusters resident at once),
-//   - where that gives a warp at most 8 tiles (16 rows x 2 KV heads of 2600 tokens:
-//     9.7 us against 11.7 for pieces; 8 x 2 groups of 12 heads of 4096 at head_dim 256:
+//   - where that gives a warp at most 8 tiles (16 rows x 2 KV heads of 2600 tokens: 8.2 us
+//     against 11.7 for pieces; 8 x 2 groups of 12 heads of 4096 at head_dim 256:
 //     14.1 against 17.1), 6 at head_dim 256 in clusters of 8 (4 x 2 such groups of 8000: 18.7
 //     against 15.7), or
 //   - where the rows and heads alone fill the GPU and spans are at most 8192 tokens,
@@ -264,6 +266,7 @@ i8kv_status mx4_clusters(const KernelKey& key, int32_t units, int32_t c, bool* f
 // kernel (about 3 us).
 constexpr int64_t kMx4WarpTiles = 8, kMx4WarpTilesWide = 6;
 constexpr int64_t kMx4RowTiles = 512;
+constexpr int32_t kMx4SharedTiles = 7;
 i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t* ns,
                      int32_t* chunk) {
   const int64_t tiles = cdiv(span, 16);
@@ -276,7 +279,12 @@ i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t*
   int32_t c = 1, groups = 1;
   bool fits = false;
   if ((st = mx4_clusters(key, units, 1, &fits, &one, &groups)) != I8KV_OK) return st;
-  while (!fills && c < i8kv::kMx4MaxCluster && c * i8kv::kMx4ClusterWarps * 2 < tiles) {
+  int sms = 0;
+  if ((st = sm_count(&sms)) != I8KV_OK) return st;
+  while (!fills && c < i8kv::kMx4MaxCluster) {
+    // a tile per warp while every CTA has an SM of its own, else more of them
+    const int32_t each = 2LL * c * units > sms ? kMx4SharedTiles : 1;
+    if (c * i8kv::kMx4ClusterWarps * each >= tiles) break;
     int32_t more = 1;
     if ((st = mx4_clusters(key, units, 2 * c, &fits, &one, &more)) != I8KV_OK) return st;
     // (two units of half the heads in smaller clusters are faster than one in larger ones)
