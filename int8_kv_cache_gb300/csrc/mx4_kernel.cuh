@@ -9,8 +9,8 @@
 // Bound: HBM in bytes, the integer pipe in practice.  A record of 16 tokens is 18 D bytes
 // (2304 at head_dim 128) and one bulk copy into the ring of the warp that works on it: two
 // stages of two records per warp, 16 warps per SM, about 110 KB in flight.  At 6.8 TB/s an SM
-// gets a record every 98 cycles; what it issues for one is about 295 instructions (136 of them
-// for the integer pipe, which takes one every second cycle: 68 cycles of its four
+// gets a record every 98 cycles; what it issues for one is about 277 instructions (123 of them
+// for the integer pipe, which takes one every second cycle: 62 cycles of its four
 // schedulers' time), so instructions are what was worked on:
 //   - Matrix fragments straight from shared memory.  S = K Q'^T takes tokens as rows and a
 //     lane's 32 (head_dim 128) consecutive channels of a token as its part of the contraction:
@@ -25,9 +25,10 @@
 //     output itself is fp16); their sum and everything accumulated is fp32.
 //   - Copy descriptions (address, attended tokens) are formed 32 tiles at a time, a lane each.
 // Measured on one GB300 (graph of calls, inputs larger than L2): 16 x 8192-32768 tokens, 32/8
-// heads, head_dim 128: 64.5 us, 5.04 TB/s, 74 % of the measured copy rate (integer pipe 55 %
-// of its cycles, issue 60 %).  Tried and slower there: one record per stage (78 us), three stages
-// (73), 8-warp CTAs (76), 5 CTAs per SM (71).
+// heads, head_dim 128: 62.5 us, 5.2 TB/s, 77 % of the measured copy rate (integer pipe 53 %
+// of its cycles, issue 60 %).  Tried and slower than its 64 to 70 us of then: one record per stage
+// (78 us), three stages (73), 8-warp CTAs (76), 5 CTAs per SM (71).  An odd record at a warp's
+// end is worked alone (a pair with nothing in its second half costs as much as two).
 //
 // Three ways over the work, chosen by the host from sizes alone (mx4_auto in api.cu): 4-warp
 // CTAs over balanced pieces or chunks of rows, joined by the combine kernel; clusters of
