@@ -82,6 +82,7 @@ cudaError_t launch_key(const KernelKey& key, const DecodeParams& p, cudaStream_t
                     : i8kv::launch_dsa_prefill(key, p, s, info);
   }
   if (key.cluster) return i8kv::launch_paged_mx4_cluster(key, p, s, info);
+  if (key.wide) return i8kv::launch_paged_mx4_wide(key, p, s, info);
   if (key.mx4_cache) return i8kv::launch_paged_mx4(key, p, s, info);
   if (key.fp16_cache) return i8kv::launch_paged_fp16(key, p, s, info);
   if (key.fp8_cache) return i8kv::launch_paged_fp8(key, p, s, info);
@@ -105,7 +106,7 @@ i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
   if (e != cudaSuccess) return cuda_fail(e);
   const auto k = std::make_tuple(dev, static_cast<int>(key.path), key.D, key.nt,
                                  static_cast<int>(key.fp16_cache), static_cast<int>(key.fp8_cache),
-                                 static_cast<int>(key.p_lo), key.mx4_cache + 2 * key.cluster + 4 * key.per_channel);
+                                 static_cast<int>(key.p_lo), key.mx4_cache + 2 * key.cluster + 4 * key.per_channel + 8 * key.wide);
   {
     std::lock_guard<std::mutex> lock(mu);
     auto it = cache.find(k);
@@ -248,6 +249,27 @@ i8kv_status mx4_clusters(const KernelKey& key, int32_t units, int32_t c, bool* f
   return st;
 }
 
+// The kernel for balanced pieces of the MX4 decode, and its wave: 8-warp CTAs where the partial
+// slots keep the 4-warp ones from filling the GPU and the wider ones put more warps to work (one
+// row of 131072 tokens, 8 groups of 4 heads: 35.9 us against 41.3; of 65536, 4 groups of 4 heads at
+// head_dim 256: 26.7 against 34.4; two of 65536, 8 groups: 33.3 against 36.5).  Where the GPU
+// is full of either, 4 warps wait less for each other (16 x 8192-32768 tokens, 8 groups: 64.5 us
+// against 76).
+i8kv_status mx4_pieces(KernelKey* key, int32_t units, int32_t num_splits, WaveInfo* w) {
+  i8kv_status st = wave_of(*key, w);
+  const int64_t slots = static_cast<int64_t>(units) * num_splits;
+  if (st != I8KV_OK || slots >= w->wave) return st;
+  KernelKey wide = *key;
+  wide.wide = true;
+  WaveInfo w8{0, 0};
+  if ((st = wave_of(wide, &w8)) != I8KV_OK) return st;
+  if (std::min<int64_t>(slots, w8.wave) * i8kv::kMx4WideWarps > slots * i8kv::kMx4PieceWarps) {
+    *key = wide;
+    *w = w8;
+  }
+  return I8KV_OK;
+}
+
 // The automatic geometry of the MX4 decode, from the wave rule's count *ns.  A
 // row and KV head is one CTA of 8 warps, or a cluster of 2, 4 or 8 of them that join
 // without a second kernel (as many as leave each warp a tile of 16 tokens while every CTA has
@@ -260,8 +282,7 @@ i8kv_status mx4_clusters(const KernelKey& key, int32_t units, int32_t c, bool* f
 //     against 15.7), or
 //   - where the rows and heads alone fill the GPU and spans are at most 8192 tokens,
 //     so that a long row among short ones is not what is waited for (128 rows x 8 heads
-//     of 128 to 4096 tokens: 79 us against 96; 32 x 8 heads, which do not fill it,
-//     of 128 to 2048: 17.9 against 16.4).
+//     of 128 to 4096 tokens: 75 us against 93; 80 rows: 54 against 64).
 // Else balanced pieces, twice the wave rule's count as partial slots, and the join
 // kernel (about 3 us).
 constexpr int64_t kMx4WarpTiles = 8, kMx4WarpTilesWide = 6;
@@ -811,15 +832,15 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
       return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
     }
   }
+  KernelKey own = key;  // (the plan, which does not know the scales, sets the slots only)
   if (p.balanced) {
-    WaveInfo w{0, 0};
-    KernelKey own = key;  // (the plan, which does not know the scales, sets the slots only)
     own.per_channel = p.per_channel;
-    if ((st = wave_of(own, &w)) != I8KV_OK) return st;
+    WaveInfo w{0, 0};
+    if ((st = mx4_pieces(&own, units, num_splits, &w)) != I8KV_OK) return st;
     // (at least one piece per row and KV head, and one to spare)
     p.bal_pieces = std::max(w.wave, units + std::max(w.wave / 2, Hkv));
   }
-  return run(key, p, static_cast<cudaStream_t>(stream));
+  return run(own, p, static_cast<cudaStream_t>(stream));
 }
 
 size_t mx4_cache_bytes(int64_t num_blocks, int32_t block_size, int32_t Hkv, int32_t D) {

@@ -63,6 +63,7 @@ struct KernelKey {
   bool p_lo;       // probability tile as fp16 high + low parts
   bool mx4_cache = false;  // 4-bit records (mx4_kernel.cuh; DecodeParams::k is the record cache)
   bool cluster = false;    // mx4_cache: a cluster of num_splits CTAs per (row, KV head)
+  bool wide = false;       // mx4_cache: pieces by 8-warp CTAs
   bool per_channel = false;  // mx4_cache, KernelInfo only: the kernel for scales per channel
 };
 
@@ -89,10 +90,12 @@ cudaError_t launch_paged_fp8(const KernelKey& key, const DecodeParams& p, cudaSt
 
 cudaError_t launch_paged_mx4(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                              KernelInfo* info);
+cudaError_t launch_paged_mx4_wide(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
+                                  KernelInfo* info);
 cudaError_t launch_paged_mx4_cluster(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                                      KernelInfo* info);
 constexpr int kMx4MaxCluster = 8;  // CTAs of a portable cluster
-constexpr int kMx4ClusterWarps = 8;
+constexpr int kMx4ClusterWarps = 8, kMx4PieceWarps = 4, kMx4WideWarps = 8;
 
 // rope_and_cache and gather_cache (append.cu); the cache type picks the kernel.
 struct AppendParams {

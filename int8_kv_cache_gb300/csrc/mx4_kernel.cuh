@@ -30,8 +30,9 @@
 // (78 us), three stages (73), 8-warp CTAs (76), 5 CTAs per SM (71).  An odd record at a warp's
 // end is worked alone (a pair with nothing in its second half costs as much as two).
 //
-// Three ways over the work, chosen by the host from sizes alone (mx4_auto in api.cu): 4-warp
-// CTAs over balanced pieces or chunks of rows, joined by the combine kernel; clusters of
+// Ways over the work, chosen by the host from sizes alone (mx4_auto and mx4_pieces in api.cu):
+// 4-warp CTAs (8-warp ones for few long rows) over balanced pieces of rows, or 4-warp ones over
+// chunks, joined by the combine kernel; clusters of
 // 8-warp CTAs per row and KV head, joined in distributed shared memory; one such CTA each.
 #pragma once
 
@@ -50,8 +51,6 @@
 namespace i8kv {
 
 namespace {
-
-constexpr int kMinTiles = 4;  // tiles of 16 tokens per balanced piece at least
 
 struct Mx4Item {
   int unit, row, g, slot;
@@ -73,7 +72,7 @@ __device__ __forceinline__ int tiles_of(const DecodeParams& p, int r, int cap, i
 // partial slots of a row and P the pieces the grid has room for (one occupancy
 // wave of CTAs, or U + half a wave where the U = B * Hkv rows and heads are more
 // than that), every row is cut into n_b = clamp(ceil(t_b / L), 1, S) pieces of
-// ceil(t_b / n_b) tiles, with the smallest L >= kMinTiles for which the pieces
+// ceil(t_b / n_b) tiles, with the smallest multiple L of W for which the pieces
 // number at most P (found by bisection: sum t_b Hkv / P is a lower bound, sum t_b
 // Hkv / (P - U) always does).  The grid follows from the arguments alone; CTAs
 // past the last piece return.  Item c: rows in order, a row's pieces in order, the
@@ -90,12 +89,12 @@ __device__ Mx4Item balanced_piece(const DecodeParams& p, int c) {
   for (int r = 32 + lane; r < B; r += 32) tot += tiles_of(p, r, cap, len, wlo);
   tot = __reduce_add_sync(0xffffffffu, tot);
   const int room = p.bal_pieces / Hkv;  // pieces of one KV head (> B)
-  // bisection in units of kMinTiles (one tile per warp)
-  const int need = (tot + kMinTiles - 1) / kMinTiles;
+  // bisection in units of W tiles (one per warp)
+  const int need = (tot + W - 1) / W;
   int lo = max(1, (need + room - 1) / room);
   int up = max(lo, (need + room - B - 1) / (room - B));
   while (lo < up) {
-    const int mid = (lo + up) >> 1, len_mid = mid * kMinTiles;
+    const int mid = (lo + up) >> 1, len_mid = mid * W;
     int n = lane < B ? min(max((t0 + len_mid - 1) / len_mid, 1), S) : 0;
 #pragma unroll 1
     for (int r = 32 + lane; r < B; r += 32)
@@ -106,7 +105,7 @@ __device__ Mx4Item balanced_piece(const DecodeParams& p, int c) {
     else
       lo = mid + 1;
   }
-  const int L = lo * kMinTiles;
+  const int L = lo * W;
   int base = 0;
 #pragma unroll 1
   for (int r0 = 0; r0 < B; r0 += 32) {

@@ -231,6 +231,21 @@ def test_large_batches(K, B, Hkv):
     compare(c, run(K, c, ns=32, chunk=0), reference(c))
 
 
+@pytest.mark.parametrize("Hq,D", [(4, 64), (12, 64), (4, 128), (7, 128), (16, 128), (3, 256), (8, 256), (13, 256)])
+@pytest.mark.parametrize("per_channel", [False, True])
+def test_pieces_of_many_rows_and_of_few(K, Hq, D, per_channel):
+    # the partial slots of 50 rows fill any GPU, those of one to three do not
+    rng = np.random.default_rng(Hq)
+    c = case(Hq * D, 50, Hq, 1, D, 16, 14, rng.integers(0, 225, 50), per_channel)
+    c["lens"][:3] = [224, 0, 193]
+    ref = reference(c, window=199)
+    compare(c, run(K, c, ns=32, chunk=0, window=199), ref)
+    for B in (1, 3):
+        part = dict(c, q=c["q"][:B], table=c["table"][:B], lens=c["lens"][:B])
+        for ns in (3, 14, 31):
+            compare(part, run(K, part, ns=ns, chunk=0, window=199), [x[:B] for x in ref], what=f"{B} {ns}")
+
+
 def reference_on_device(c, d, rows, window=-1):
     """Attention of some sequences in 64 bits with torch on the device."""
     bs, D, Hkv = c["cache"].shape[2] * 16, c["q"].shape[2], c["cache"].shape[1]
