@@ -282,12 +282,13 @@ i8kv_status mx4_pieces(KernelKey* key, int32_t units, int32_t num_splits, WaveIn
 //     against 15.7), or
 //   - where the rows and heads alone fill the GPU and spans are at most 8192 tokens,
 //     so that a long row among short ones is not what is waited for (128 rows x 8 heads
-//     of 128 to 4096 tokens: 75 us against 93; 80 rows: 54 against 64).
+//     of 128 to 4096 tokens: 65 us against 93; 80 rows: 46 against 64).
 // Else balanced pieces, twice the wave rule's count as partial slots, and the join
 // kernel (about 3 us).
 constexpr int64_t kMx4WarpTiles = 8, kMx4WarpTilesWide = 6;
 constexpr int64_t kMx4RowTiles = 512;
 constexpr int32_t kMx4SharedTiles = 7;
+constexpr int64_t kMx4RankSpan = 1024;
 i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t* ns,
                      int32_t* chunk) {
   const int64_t tiles = cdiv(span, 16);
@@ -828,6 +829,16 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
     if ((st = mx4_clusters(key, units, num_splits, &fits, &ckey, &p.head_groups)) != I8KV_OK)
       return st;
     if (fits) {
+      // One CTA per row and head, and more of them than are resident: long rows start first,
+      // so that none is what the rest waits for (50 rows x 8 heads of 128 to 4096 tokens: 29 us
+      // against 40 in the rows' order, 128 rows: 65 against 75).  Finding the row costs a CTA
+      // 0.8 us (128 rows of 2048 tokens each: 67 us against 65), so not for short spans.
+      if (num_splits == 1 && B <= i8kv::kMx4RankRows && span >= kMx4RankSpan) {
+        ckey.per_channel = p.per_channel;
+        WaveInfo w{0, 0};
+        if ((st = wave_of(ckey, &w)) != I8KV_OK) return st;
+        p.longest_first = static_cast<int64_t>(units) * p.head_groups > w.wave;
+      }
       const cudaError_t e = launch_key(ckey, p, static_cast<cudaStream_t>(stream), nullptr);
       return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
     }

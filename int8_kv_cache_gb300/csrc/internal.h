@@ -43,6 +43,7 @@ struct DecodeParams {
   // num_splits per row (the partial slots), bal_pieces (row, piece) pairs in
   // all, each a multiple of bal_round positions; the grid has
   // ceil(num_splits / 2) CTAs per unit (decode_kernel.cuh, balanced_item)
+  int32_t longest_first;     // MX4 clusters: rows are taken in the order of falling lengths
   int32_t head_groups;       // MX4 clusters: 2: each half of a group's query heads is a unit of its own
   int32_t balanced;
   int32_t bal_round;
@@ -95,6 +96,7 @@ cudaError_t launch_paged_mx4_wide(const KernelKey& key, const DecodeParams& p, c
 cudaError_t launch_paged_mx4_cluster(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                                      KernelInfo* info);
 constexpr int kMx4MaxCluster = 8;  // CTAs of a portable cluster
+constexpr int kMx4RankRows = 256;  // rows that longest_first takes at most
 constexpr int kMx4ClusterWarps = 8, kMx4PieceWarps = 4, kMx4WideWarps = 8;
 
 // rope_and_cache and gather_cache (append.cu); the cache type picks the kernel.

@@ -175,6 +175,45 @@ __device__ Mx4Item item_of(const DecodeParams& p, int c) {
   return it;
 }
 
+// The row with `rank` rows before it when they are put in the order of falling lengths, to
+// about an eighth of the longest (sixteen classes at most; rows of a class by their numbers).  Every
+// warp finds it by itself.
+__device__ __forceinline__ int row_of_rank(const DecodeParams& p, int rank) {
+  constexpr int N = kMx4RankRows / 32;
+  const int lane = threadIdx.x & 31, B = p.rows;
+  int v[N], top = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const int r = lane + 32 * i;
+    v[i] = r < B ? min(max(p.seq_lens[r], 0), p.max_blocks * p.bs) : -1;
+    top = max(top, v[i]);
+  }
+  top = __reduce_max_sync(0xffffffffu, top);
+  const int shift = max(0, 28 - __clz(top));  // the longest is in class 8 to 15
+  int cls = 0, before = 0;
+#pragma unroll
+  for (int bit = 8; bit > 0; bit >>= 1) {
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) n += (v[i] >> shift) >= cls + bit;
+    n = __reduce_add_sync(0xffffffffu, n);
+    if (n > rank)
+      cls += bit;
+    else
+      before = n;
+  }
+  int k = rank - before, row = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const bool in = (v[i] >> shift) == cls;
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    const unsigned it = __ballot_sync(0xffffffffu, in && __popc(m & ((1u << lane) - 1u)) == k);
+    if (it != 0u) row = 32 * i + __ffs(it) - 1;
+    k -= __popc(m);
+  }
+  return row;
+}
+
 // Shape of the kernel for head dimension D, NT groups of 8 query heads and W warps.
 template <int D, int NT, int W>
 struct Mx4Tile {
@@ -318,6 +357,10 @@ mx4_decode_kernel(const DecodeParams p) {
     }
     it.row = it.unit / p.Hkv;
     it.g = it.unit - it.row * p.Hkv;
+    if (p.longest_first) {
+      it.row = row_of_rank(p, it.row);
+      it.unit = it.row * p.Hkv + it.g;
+    }
     it.stride = W * p.num_splits;
     it.tile0 = it.slot * W;
     it.pieces = 0;

@@ -246,6 +246,22 @@ def test_pieces_of_many_rows_and_of_few(K, Hq, D, per_channel):
             compare(part, run(K, part, ns=ns, chunk=0, window=199), [x[:B] for x in ref], what=f"{B} {ns}")
 
 
+@pytest.mark.parametrize("B,D,Hq,Hkv", [(160, 64, 8, 2), (256, 64, 4, 2), (257, 64, 4, 2), (97, 128, 16, 4), (81, 128, 48, 4),
+                                        (50, 256, 8, 8)])
+def test_one_cta_per_row_for_more_rows_than_are_resident(K, B, D, Hq, Hkv):
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 60, B)
+    lens[rng.permutation(B)[:12]] = [1024, 1023, 1024, 512, 511, 0, -7, 1 << 30, 900, 1, 16, 17]
+    c = case(B, B, Hq, Hkv, D, 64, 16, lens)
+    ref = reference(c)
+    compare(c, run(K, c, ns=1, chunk=1024), ref)
+    compare(c, run(K, c), ref)
+    c["lens"][:] = 33  # all alike, then all empty
+    compare(c, run(K, c, ns=1, chunk=1024), reference(c))
+    c["lens"][:] = 0
+    compare(c, run(K, c, ns=1, chunk=1024), reference(c))
+
+
 def reference_on_device(c, d, rows, window=-1):
     """Attention of some sequences in 64 bits with torch on the device."""
     bs, D, Hkv = c["cache"].shape[2] * 16, c["q"].shape[2], c["cache"].shape[1]
