@@ -18,6 +18,7 @@ namespace {
 using i8kv::DecodeParams;
 using i8kv::KernelInfo;
 using i8kv::KernelKey;
+using i8kv::Mx4Way;
 using i8kv::Path;
 
 thread_local int g_last_cuda_error = 0;
@@ -81,9 +82,14 @@ cudaError_t launch_key(const KernelKey& key, const DecodeParams& p, cudaStream_t
     return key.p_lo ? i8kv::launch_dsa_decode(key, p, s, info)
                     : i8kv::launch_dsa_prefill(key, p, s, info);
   }
-  if (key.cluster) return i8kv::launch_paged_mx4_cluster(key, p, s, info);
-  if (key.wide) return i8kv::launch_paged_mx4_wide(key, p, s, info);
-  if (key.mx4_cache) return i8kv::launch_paged_mx4(key, p, s, info);
+  if (key.mx4_cache) {
+    if (key.way == Mx4Way::kCluster) return i8kv::launch_paged_mx4_cluster(key, p, s, info);
+    if (key.way == Mx4Way::kRows)
+      return key.wide ? i8kv::launch_paged_mx4_rows_wide(key, p, s, info)
+                      : i8kv::launch_paged_mx4_rows(key, p, s, info);
+    return key.wide ? i8kv::launch_paged_mx4_wide(key, p, s, info)
+                    : i8kv::launch_paged_mx4(key, p, s, info);
+  }
   if (key.fp16_cache) return i8kv::launch_paged_fp16(key, p, s, info);
   if (key.fp8_cache) return i8kv::launch_paged_fp8(key, p, s, info);
   return i8kv::launch_paged_int8(key, p, s, info);
@@ -95,7 +101,7 @@ cudaError_t launch_key(const KernelKey& key, const DecodeParams& p, cudaStream_t
 struct WaveInfo {
   int32_t wave;
   int32_t round;
-  int32_t clusters[4] = {0, 0, 0, 0};  // cluster kernels: resident clusters of 1, 2, 4, 8 CTAs
+  int32_t clusters[4] = {0, 0, 0, 0};  // cluster kernels: resident clusters of 2, 4, 8 CTAs, from [1]
 };
 
 i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
@@ -106,7 +112,9 @@ i8kv_status wave_of(const KernelKey& key, WaveInfo* out) {
   if (e != cudaSuccess) return cuda_fail(e);
   const auto k = std::make_tuple(dev, static_cast<int>(key.path), key.D, key.nt,
                                  static_cast<int>(key.fp16_cache), static_cast<int>(key.fp8_cache),
-                                 static_cast<int>(key.p_lo), key.mx4_cache + 2 * key.cluster + 4 * key.per_channel + 8 * key.wide);
+                                 static_cast<int>(key.p_lo),
+                                 key.mx4_cache + 2 * key.wide + 4 * key.per_channel +
+                                     8 * static_cast<int>(key.way));
   {
     std::lock_guard<std::mutex> lock(mu);
     auto it = cache.find(k);
@@ -217,19 +225,57 @@ i8kv_status plan(const KernelKey& key, int64_t cap, int32_t units, int32_t mode,
   return I8KV_OK;
 }
 
-// Whether the MX4 decode takes `units` (row, KV head) pairs as clusters of c CTAs (a power of
-// two, at most kMx4MaxCluster) with all of them resident at once; a single CTA always.  *run is
-// the kernel: groups of more than 8 query heads run as two units of half of them each
-// (*groups = 2) where those are resident too, on the kernel for at most 8, which takes a
-// tile in about two thirds of the time (8 rows x 2 groups of 12 heads, head_dim 256, 2064
-// tokens: 13.2 us in one unit, 10.3 for half of it; the keys and values come from L2 twice).
+// The kernel of the MX4 decode for one CTA per (row, KV head), `units` of them.  Groups of more
+// than 8 query heads run as two units of half of them each (*groups = 2) where those are
+// resident at once, on the kernel for at most 8, which takes a tile in about two thirds of the
+// time (8 rows x 2 groups of 12 heads, head_dim 256, 2064 tokens: 13.2 us in one unit, 10.3 for half
+// of it; the keys and values come from L2 twice).
+// CTAs of 8 warps where all of them are resident.  Beyond that 4 warps, whose CTAs come and go
+// in smaller steps: for spans of at most 1024 tokens (160 rows x 8 heads of 16: 8.6 us against
+// 14.4, of 1024: 41 against 47), and for any where they number 4/3 waves or more (128 rows of 128 to
+// 8192: 96 us against 100; 160 x 4 groups of 16 heads of 4096: 106 against 127).  Fewer long
+// ones are uneven over the SMs (50 rows x 8 heads of 2048: 40 us, in 8 warps 30).
+constexpr int64_t kMx4NarrowSpan = 1024;
+i8kv_status mx4_rows(const KernelKey& key, int32_t units, int64_t span, KernelKey* run,
+                     int32_t* groups, WaveInfo* w) {
+  *run = key;
+  run->way = Mx4Way::kRows;
+  run->wide = true;
+  *groups = 1;
+  i8kv_status st;
+  if (key.nt == 2) {
+    KernelKey half = *run;
+    half.nt = 1;
+    if ((st = wave_of(half, w)) != I8KV_OK) return st;
+    if (2LL * units <= w->wave) {
+      *run = half;
+      *groups = 2;
+      return I8KV_OK;
+    }
+  }
+  if ((st = wave_of(*run, w)) != I8KV_OK) return st;
+  if (units <= w->wave) return I8KV_OK;
+  KernelKey narrow = *run;
+  narrow.wide = false;
+  WaveInfo w4{0, 0};
+  if ((st = wave_of(narrow, &w4)) != I8KV_OK) return st;
+  if (span <= kMx4NarrowSpan || 3LL * units >= 4LL * w4.wave) {
+    *run = narrow;
+    *w = w4;
+  }
+  return I8KV_OK;
+}
+
+// Whether clusters of c CTAs (a power of two, at most kMx4MaxCluster) per (row, KV head) are all
+// resident at once, and their kernel; groups of more than 8 query heads as above.
 i8kv_status mx4_clusters(const KernelKey& key, int32_t units, int32_t c, bool* fits, KernelKey* run,
                          int32_t* groups) {
   *run = key;
-  run->cluster = true;
+  run->way = Mx4Way::kCluster;
+  run->wide = true;
   *groups = 1;
-  *fits = c == 1;
-  if (c < 1 || c > i8kv::kMx4MaxCluster || (c & (c - 1)) != 0) return I8KV_OK;
+  *fits = false;
+  if (c < 2 || c > i8kv::kMx4MaxCluster || (c & (c - 1)) != 0) return I8KV_OK;
   WaveInfo w{0, 0};
   i8kv_status st;
   if (key.nt == 2) {
@@ -243,7 +289,6 @@ i8kv_status mx4_clusters(const KernelKey& key, int32_t units, int32_t c, bool* f
       return I8KV_OK;
     }
   }
-  if (c == 1) return I8KV_OK;
   st = wave_of(*run, &w);
   *fits = units <= w.clusters[log2_of(c)];
   return st;
@@ -263,7 +308,7 @@ i8kv_status mx4_pieces(KernelKey* key, int32_t units, int32_t num_splits, WaveIn
   wide.wide = true;
   WaveInfo w8{0, 0};
   if ((st = wave_of(wide, &w8)) != I8KV_OK) return st;
-  if (std::min<int64_t>(slots, w8.wave) * i8kv::kMx4WideWarps > slots * i8kv::kMx4PieceWarps) {
+  if (std::min<int64_t>(slots, w8.wave) * i8kv::kMx4WideWarps > slots * i8kv::kMx4Warps) {
     *key = wide;
     *w = w8;
   }
@@ -282,7 +327,7 @@ i8kv_status mx4_pieces(KernelKey* key, int32_t units, int32_t num_splits, WaveIn
 //     against 15.7), or
 //   - where the rows and heads alone fill the GPU and spans are at most 8192 tokens,
 //     so that a long row among short ones is not what is waited for (128 rows x 8 heads
-//     of 128 to 4096 tokens: 65 us against 93; 80 rows: 46 against 64).
+//     of 128 to 4096 tokens: 55 us against 93; 80 rows: 42 against 64).
 // Else balanced pieces, twice the wave rule's count as partial slots, and the join
 // kernel (about 3 us).
 constexpr int64_t kMx4WarpTiles = 8, kMx4WarpTilesWide = 6;
@@ -292,29 +337,30 @@ constexpr int64_t kMx4RankSpan = 1024;
 i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t* ns,
                      int32_t* chunk) {
   const int64_t tiles = cdiv(span, 16);
-  KernelKey one = key;
-  one.cluster = true;
+  KernelKey run = key;
+  run.way = Mx4Way::kRows;
+  run.wide = true;
   WaveInfo w{0, 0};
-  i8kv_status st = wave_of(one, &w);
+  i8kv_status st = wave_of(run, &w);
   if (st != I8KV_OK) return st;
-  const bool fills = units >= w.clusters[0] && tiles <= kMx4RowTiles;
+  const bool fills = units >= w.wave && tiles <= kMx4RowTiles;
   int32_t c = 1, groups = 1;
+  if ((st = mx4_rows(key, units, span, &run, &groups, &w)) != I8KV_OK) return st;
   bool fits = false;
-  if ((st = mx4_clusters(key, units, 1, &fits, &one, &groups)) != I8KV_OK) return st;
   int sms = 0;
   if ((st = sm_count(&sms)) != I8KV_OK) return st;
   while (!fills && c < i8kv::kMx4MaxCluster) {
     // a tile per warp while every CTA has an SM of its own, else more of them
     const int32_t each = 2LL * c * units > sms ? kMx4SharedTiles : 1;
-    if (c * i8kv::kMx4ClusterWarps * each >= tiles) break;
+    if (c * i8kv::kMx4WideWarps * each >= tiles) break;
     int32_t more = 1;
-    if ((st = mx4_clusters(key, units, 2 * c, &fits, &one, &more)) != I8KV_OK) return st;
+    if ((st = mx4_clusters(key, units, 2 * c, &fits, &run, &more)) != I8KV_OK) return st;
     // (two units of half the heads in smaller clusters are faster than one in larger ones)
     if (!fits || more < groups) break;
     c *= 2;
   }
   const int64_t most = key.D > 128 && c == i8kv::kMx4MaxCluster ? kMx4WarpTilesWide : kMx4WarpTiles;
-  if (fills || tiles <= most * i8kv::kMx4ClusterWarps * c) {
+  if (fills || tiles <= most * i8kv::kMx4WideWarps * c) {
     *ns = c;
     *chunk = c > 1 ? 0 : static_cast<int32_t>(std::max<int64_t>(16, tiles * 16));
     return I8KV_OK;
@@ -823,27 +869,26 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
   p.softcap = softcap;
   p.window = window;
   // one split, and balanced pieces that fit clusters, join inside the kernel
-  if (num_splits == 1 || (p.balanced && out != nullptr)) {
-    bool fits = false;
-    KernelKey ckey;
-    if ((st = mx4_clusters(key, units, num_splits, &fits, &ckey, &p.head_groups)) != I8KV_OK)
+  KernelKey own;
+  bool joins = num_splits == 1;
+  if (num_splits == 1) {
+    WaveInfo w{0, 0};
+    if ((st = mx4_rows(key, units, span, &own, &p.head_groups, &w)) != I8KV_OK) return st;
+    // More rows and heads than are resident: long rows start first, so that none is what the
+    // rest waits for (50 rows x 8 heads of 128 to 4096 tokens: 29 us against 40 in the rows'
+    // order, 128 rows: 65 against 75; in all 3 us less now).  Finding the row costs a CTA
+    // 0.8 us (128 rows of 2048 tokens each: 67 us against 65), so not for short spans.
+    p.longest_first = B <= i8kv::kMx4RankRows && span >= kMx4RankSpan &&
+                      static_cast<int64_t>(units) * p.head_groups > w.wave;
+  } else if (p.balanced && out != nullptr) {
+    if ((st = mx4_clusters(key, units, num_splits, &joins, &own, &p.head_groups)) != I8KV_OK)
       return st;
-    if (fits) {
-      // One CTA per row and head, and more of them than are resident: long rows start first,
-      // so that none is what the rest waits for (50 rows x 8 heads of 128 to 4096 tokens: 29 us
-      // against 40 in the rows' order, 128 rows: 65 against 75).  Finding the row costs a CTA
-      // 0.8 us (128 rows of 2048 tokens each: 67 us against 65), so not for short spans.
-      if (num_splits == 1 && B <= i8kv::kMx4RankRows && span >= kMx4RankSpan) {
-        ckey.per_channel = p.per_channel;
-        WaveInfo w{0, 0};
-        if ((st = wave_of(ckey, &w)) != I8KV_OK) return st;
-        p.longest_first = static_cast<int64_t>(units) * p.head_groups > w.wave;
-      }
-      const cudaError_t e = launch_key(ckey, p, static_cast<cudaStream_t>(stream), nullptr);
-      return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
-    }
   }
-  KernelKey own = key;  // (the plan, which does not know the scales, sets the slots only)
+  if (joins) {
+    const cudaError_t e = launch_key(own, p, static_cast<cudaStream_t>(stream), nullptr);
+    return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
+  }
+  own = key;  // (the plan, which does not know the scales, sets the slots only)
   if (p.balanced) {
     own.per_channel = p.per_channel;
     WaveInfo w{0, 0};

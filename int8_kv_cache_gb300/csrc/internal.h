@@ -43,8 +43,8 @@ struct DecodeParams {
   // num_splits per row (the partial slots), bal_pieces (row, piece) pairs in
   // all, each a multiple of bal_round positions; the grid has
   // ceil(num_splits / 2) CTAs per unit (decode_kernel.cuh, balanced_item)
-  int32_t longest_first;     // MX4 clusters: rows are taken in the order of falling lengths
-  int32_t head_groups;       // MX4 clusters: 2: each half of a group's query heads is a unit of its own
+  int32_t longest_first;     // MX4 rows: they are taken in the order of falling lengths
+  int32_t head_groups;       // MX4 rows and clusters: 2: each half of a group's query heads is a unit of its own
   int32_t balanced;
   int32_t bal_round;
   int32_t bal_pieces;
@@ -55,6 +55,10 @@ struct DecodeParams {
 constexpr int kLptMaxRows = 128;
 constexpr int kLptMinChunk = 1280;
 
+// What a CTA of the MX4 decode works on: a piece (or chunk) of a row and KV head, all of it, or
+// its part in the cluster of num_splits CTAs that shares it.
+enum class Mx4Way : int { kPieces = 0, kRows = 1, kCluster = 2 };
+
 struct KernelKey {
   Path path;
   int D;
@@ -63,8 +67,8 @@ struct KernelKey {
   bool fp8_cache;  // float8 e4m3fn codes (same tile as int8, other conversion)
   bool p_lo;       // probability tile as fp16 high + low parts
   bool mx4_cache = false;  // 4-bit records (mx4_kernel.cuh; DecodeParams::k is the record cache)
-  bool cluster = false;    // mx4_cache: a cluster of num_splits CTAs per (row, KV head)
-  bool wide = false;       // mx4_cache: pieces by 8-warp CTAs
+  Mx4Way way = Mx4Way::kPieces;
+  bool wide = false;       // mx4_cache: 8-warp CTAs (clusters always are)
   bool per_channel = false;  // mx4_cache, KernelInfo only: the kernel for scales per channel
 };
 
@@ -72,7 +76,7 @@ struct KernelKey {
 struct KernelInfo {
   int occupancy;  // resident CTAs per SM (the CUDA occupancy API)
   int round;      // positions one round of the CTA's warps covers (warps x step)
-  int clusters[4] = {0, 0, 0, 0};  // cluster kernels: resident clusters of 1, 2, 4, 8 CTAs
+  int clusters[4] = {0, 0, 0, 0};  // cluster kernels: resident clusters of 2, 4, 8 CTAs, from [1]
 };
 
 // Per-path launchers (one per translation unit): grid (rows * Hkv, num_splits);
@@ -93,11 +97,15 @@ cudaError_t launch_paged_mx4(const KernelKey& key, const DecodeParams& p, cudaSt
                              KernelInfo* info);
 cudaError_t launch_paged_mx4_wide(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                                   KernelInfo* info);
+cudaError_t launch_paged_mx4_rows(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
+                                  KernelInfo* info);
+cudaError_t launch_paged_mx4_rows_wide(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
+                                       KernelInfo* info);
 cudaError_t launch_paged_mx4_cluster(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                                      KernelInfo* info);
 constexpr int kMx4MaxCluster = 8;  // CTAs of a portable cluster
 constexpr int kMx4RankRows = 256;  // rows that longest_first takes at most
-constexpr int kMx4ClusterWarps = 8, kMx4PieceWarps = 4, kMx4WideWarps = 8;
+constexpr int kMx4Warps = 4, kMx4WideWarps = 8;  // of a CTA
 
 // rope_and_cache and gather_cache (append.cu); the cache type picks the kernel.
 struct AppendParams {

@@ -5,6 +5,6 @@
 namespace i8kv {
 cudaError_t launch_paged_mx4_cluster(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                                      KernelInfo* info) {
-  return dispatch_mx4<kMx4ClusterWarps, true>(key, p, s, info);
+  return dispatch_mx4<kMx4WideWarps, Mx4Way::kCluster>(key, p, s, info);
 }
 }  // namespace i8kv

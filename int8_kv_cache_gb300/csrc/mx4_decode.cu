@@ -5,6 +5,6 @@
 namespace i8kv {
 cudaError_t launch_paged_mx4(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                              KernelInfo* info) {
-  return dispatch_mx4<kMx4PieceWarps, false>(key, p, s, info);
+  return dispatch_mx4<kMx4Warps, Mx4Way::kPieces>(key, p, s, info);
 }
 }  // namespace i8kv

@@ -30,10 +30,10 @@
 // (78 us), three stages (73), 8-warp CTAs (76), 5 CTAs per SM (71).  An odd record at a warp's
 // end is worked alone (a pair with nothing in its second half costs as much as two).
 //
-// Ways over the work, chosen by the host from sizes alone (mx4_auto and mx4_pieces in api.cu):
-// 4-warp CTAs (8-warp ones for few long rows) over balanced pieces of rows, or 4-warp ones over
-// chunks, joined by the combine kernel; clusters of
-// 8-warp CTAs per row and KV head, joined in distributed shared memory; one such CTA each.
+// Ways over the work, chosen by the host from sizes alone (api.cu): balanced pieces of rows (4-warp
+// CTAs, 8-warp ones for few long rows) or chunks, joined by the combine kernel; clusters of 8-warp
+// CTAs per row and KV head, joined in distributed shared memory; one CTA each, of 4 or 8 warps
+// (without the cluster's barriers, which cost such a CTA 1.5 us).
 #pragma once
 
 #include <cuda_fp16.h>
@@ -328,12 +328,14 @@ constexpr int mx4_blocks() {
   return FOLD == kProducts && NT == 2 && D == 128 && W == 4 ? 2 : Mx4Tile<D, NT, W>::kBlocks;
 }
 
-// W warps.  CLUSTER: the p.num_splits CTAs of a cluster share one (row, KV head), its tiles
+// W warps.  In a cluster the p.num_splits CTAs share one (row, KV head), its tiles
 // dealt to their warps in turn, and join through distributed shared memory.
-template <int D, int NT, int W, bool CLUSTER, Fold FOLD>
+template <int D, int NT, int W, Mx4Way WAY, Fold FOLD>
 __global__ void __launch_bounds__(32 * W, (mx4_blocks<D, NT, W, FOLD>()))
 mx4_decode_kernel(const DecodeParams p) {
   using T = Mx4Tile<D, NT, W>;
+  constexpr bool ROW = WAY != Mx4Way::kPieces;  // (the length is all that the item follows from)
+  constexpr bool CLUSTER = WAY == Mx4Way::kCluster;
   constexpr int kThreads = 32 * W;
   constexpr int KC = D / 16;   // MMA steps of QK^T, and 16-channel tiles of PV
   constexpr int KW = D / 32;   // 32-bit words of a lane's key channels (D / 4 of a token)
@@ -346,9 +348,10 @@ mx4_decode_kernel(const DecodeParams p) {
   const int rpb = p.bs >> 4;  // records per block
   auto block_of = [&](int tile) { return p.bs_log2 >= 4 ? tile >> (p.bs_log2 - 4) : quotient(tile, rpb); };
   Mx4Item it;
-  if constexpr (CLUSTER) {
-    it.unit = blockIdx.x / p.num_splits;
-    it.slot = blockIdx.x - it.unit * p.num_splits;
+  if constexpr (ROW) {
+    const int ctas = CLUSTER ? p.num_splits : 1;  // of a row and head
+    it.unit = blockIdx.x / ctas;
+    it.slot = blockIdx.x - it.unit * ctas;
     if (p.head_groups == 2) {
       const int half = (p.G + 1) >> 1;
       h0 = it.unit & 1 ? half : 0;
@@ -357,11 +360,11 @@ mx4_decode_kernel(const DecodeParams p) {
     }
     it.row = it.unit / p.Hkv;
     it.g = it.unit - it.row * p.Hkv;
-    if (p.longest_first) {
+    if (!CLUSTER && p.longest_first) {
       it.row = row_of_rank(p, it.row);
       it.unit = it.row * p.Hkv + it.g;
     }
-    it.stride = W * p.num_splits;
+    it.stride = W * ctas;
     it.tile0 = it.slot * W;
     it.pieces = 0;
   } else {
@@ -376,8 +379,8 @@ mx4_decode_kernel(const DecodeParams p) {
     return b < p.max_blocks ? __ldg(table + b) : -1;
   };
   int e0 = -1, e1 = -1;  // entries of the warp's tiles lane and 32 + lane
-  const int live = CLUSTER || (it.slot == 0 && it.g == 0) ? p.seq_lens[it.row] : 0;
-  if constexpr (CLUSTER) {
+  const int live = ROW || (it.slot == 0 && it.g == 0) ? p.seq_lens[it.row] : 0;
+  if constexpr (ROW) {
     if (p.window < 0) {  // on their way with the length
       e0 = entry(lane);
       e1 = entry(32 + lane);
@@ -410,7 +413,7 @@ mx4_decode_kernel(const DecodeParams p) {
   float sink_raw = 0.f;
   if (p.sink != nullptr && threadIdx.x < G) sink_raw = p.sink[it.g * p.G + h0 + threadIdx.x];
 
-  if constexpr (CLUSTER) {
+  if constexpr (ROW) {
     it.hi = min(max(live, 0), p.max_blocks * p.bs);
     it.wlo = p.window >= 0 ? max(0, it.hi - 1 - p.window) : 0;
     it.tile0 += it.wlo >> 4;
@@ -423,7 +426,7 @@ mx4_decode_kernel(const DecodeParams p) {
   const int end = (it.hi + 15) >> 4;
   const int mine = end > first ? (end - first + it.stride - 1) / it.stride : 0;
   const int stages = (mine + T::kSub - 1) / T::kSub;
-  if (!CLUSTER || p.window >= 0) {
+  if (!ROW || p.window >= 0) {
     if (lane < mine) e0 = entry(lane);
     if (32 + lane < mine) e1 = entry(32 + lane);
   }
@@ -903,7 +906,9 @@ mx4_decode_kernel(const DecodeParams p) {
       o.z += f * x.z;
       o.w += f * x.w;
     }
-    if constexpr (CLUSTER) {
+    if constexpr (WAY == Mx4Way::kRows) {
+      finish(h, d, o, M, L);
+    } else if constexpr (CLUSTER) {
       // the CTA's sum, in the place of its first warp's (which no other thread reads)
       *reinterpret_cast<float4*>(reinterpret_cast<float*>(smem) + h * T::kRow + d) = o;
       if (d == 0) {
@@ -960,10 +965,10 @@ mx4_decode_kernel(const DecodeParams p) {
   }
 }
 
-template <int D, int NT, int W, bool CLUSTER, Fold FOLD>
+template <int D, int NT, int W, Mx4Way WAY, Fold FOLD>
 cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
   using T = Mx4Tile<D, NT, W>;
-  auto kern = mx4_decode_kernel<D, NT, W, CLUSTER, FOLD>;
+  auto kern = mx4_decode_kernel<D, NT, W, WAY, FOLD>;
   // the opt-in shared-memory size is a per-function attribute: set it once per device
   static std::atomic<unsigned long long> done{0};
   int dev = 0;
@@ -980,9 +985,9 @@ cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info
   }
   if (info != nullptr) {
     info->round = 16 * W;
-    if constexpr (CLUSTER) {
+    if constexpr (WAY == Mx4Way::kCluster) {
       // clusters live inside a part of the GPU: fewer fit than the CTAs alone
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 1; i < 4; ++i) {
         cudaLaunchConfig_t c = {};
         c.gridDim = dim3(1024u << i);
         c.blockDim = dim3(32 * W);
@@ -998,9 +1003,10 @@ cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info
     }
     return cudaOccupancyMaxActiveBlocksPerMultiprocessor(&info->occupancy, kern, 32 * W, T::kSmem);
   }
-  const long long units = (long long)p.rows * p.Hkv * (CLUSTER && p.head_groups == 2 ? 2 : 1);
-  long long ctas = units * p.num_splits;
-  if (!CLUSTER && p.balanced && ctas > p.bal_pieces) ctas = p.bal_pieces;
+  constexpr bool PIECES = WAY == Mx4Way::kPieces;
+  const long long units = (long long)p.rows * p.Hkv * (!PIECES && p.head_groups == 2 ? 2 : 1);
+  long long ctas = units * (WAY == Mx4Way::kRows ? 1 : p.num_splits);
+  if (PIECES && p.balanced && ctas > p.bal_pieces) ctas = p.bal_pieces;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)ctas);
   cfg.blockDim = dim3(32 * W);
@@ -1011,7 +1017,7 @@ cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if constexpr (CLUSTER) {
+  if constexpr (WAY == Mx4Way::kCluster) {
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = (unsigned)p.num_splits;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
@@ -1020,26 +1026,26 @@ cudaError_t run_mx4_with(const DecodeParams& p, cudaStream_t s, KernelInfo* info
   return cudaLaunchKernelEx(&cfg, kern, p);
 }
 
-template <int D, int NT, int W, bool CLUSTER>
+template <int D, int NT, int W, Mx4Way WAY>
 cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
-  if (!p.per_channel) return run_mx4_with<D, NT, W, CLUSTER, kPlain>(p, s, info);
+  if (!p.per_channel) return run_mx4_with<D, NT, W, WAY, kPlain>(p, s, info);
   if constexpr (NT == 1) {
     if ((p.head_groups == 2 ? (p.G + 1) / 2 : p.G) <= 4)
-      return run_mx4_with<D, NT, W, CLUSTER, kColumns>(p, s, info);
+      return run_mx4_with<D, NT, W, WAY, kColumns>(p, s, info);
   }
-  return run_mx4_with<D, NT, W, CLUSTER, kProducts>(p, s, info);
+  return run_mx4_with<D, NT, W, WAY, kProducts>(p, s, info);
 }
 
-template <int W, bool CLUSTER>
+template <int W, Mx4Way WAY>
 cudaError_t dispatch_mx4(const KernelKey& key, const DecodeParams& p, cudaStream_t s,
                          KernelInfo* info) {
   switch (key.D * 10 + key.nt) {
-    case 641: return run_mx4<64, 1, W, CLUSTER>(p, s, info);
-    case 642: return run_mx4<64, 2, W, CLUSTER>(p, s, info);
-    case 1281: return run_mx4<128, 1, W, CLUSTER>(p, s, info);
-    case 1282: return run_mx4<128, 2, W, CLUSTER>(p, s, info);
-    case 2561: return run_mx4<256, 1, W, CLUSTER>(p, s, info);
-    case 2562: return run_mx4<256, 2, W, CLUSTER>(p, s, info);
+    case 641: return run_mx4<64, 1, W, WAY>(p, s, info);
+    case 642: return run_mx4<64, 2, W, WAY>(p, s, info);
+    case 1281: return run_mx4<128, 1, W, WAY>(p, s, info);
+    case 1282: return run_mx4<128, 2, W, WAY>(p, s, info);
+    case 2561: return run_mx4<256, 1, W, WAY>(p, s, info);
+    case 2562: return run_mx4<256, 2, W, WAY>(p, s, info);
     default: return cudaErrorInvalidValue;
   }
 }

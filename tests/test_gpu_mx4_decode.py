@@ -262,6 +262,18 @@ def test_one_cta_per_row_for_more_rows_than_are_resident(K, B, D, Hq, Hkv):
     compare(c, run(K, c, ns=1, chunk=1024), reference(c))
 
 
+@pytest.mark.parametrize("B,D,Hq,Hkv", [(90, 64, 12, 4), (160, 64, 48, 4), (50, 128, 24, 8), (90, 128, 32, 2), (160, 128, 44, 4),
+                                        (80, 256, 20, 2), (60, 256, 12, 4), (130, 256, 48, 4)])
+@pytest.mark.parametrize("per_channel", [False, True])
+def test_one_cta_per_row_over_a_longer_span(K, B, D, Hq, Hkv, per_channel):
+    rng = np.random.default_rng(B)
+    lens = rng.integers(0, 40, B)
+    lens[rng.permutation(B)[:5]] = [1200, 1199, 0, 500, 1041]
+    c = case(B, B, Hq, Hkv, D, 16, 75, lens, per_channel, sink=True)
+    compare(c, run(K, c, ns=1, chunk=1200), reference(c))
+    compare(c, run(K, c, softcap=3.0, window=30), reference(c, 3.0, 30), 3.0)
+
+
 def reference_on_device(c, d, rows, window=-1):
     """Attention of some sequences in 64 bits with torch on the device."""
     bs, D, Hkv = c["cache"].shape[2] * 16, c["q"].shape[2], c["cache"].shape[1]
