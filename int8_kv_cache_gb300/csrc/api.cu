@@ -315,24 +315,26 @@ i8kv_status mx4_pieces(KernelKey* key, int32_t units, int32_t num_splits, WaveIn
   return I8KV_OK;
 }
 
-// The automatic geometry of the MX4 decode, from the wave rule's count *ns.  A
-// row and KV head is one CTA of 8 warps, or a cluster of 2, 4 or 8 of them that join
-// without a second kernel (as many as leave each warp a tile of 16 tokens while every CTA has
-// an SM of its own, 7 tiles where they share: 1 row x 8 heads of 300 tokens 4.9 us in 4
-// CTAs each, 5.4 in 2; 16 rows x 2 heads of 2600 8.2 us in 4, one per SM, 9.0 in 8; all
-// clusters resident at once),
-//   - where that gives a warp at most 8 tiles (16 rows x 2 KV heads of 2600 tokens: 8.2 us
+// The automatic geometry of the MX4 decode, from the wave rule's count *ns.  A row and KV head
+// is one CTA, or a cluster of 2, 4 or 8 of 8 warps that join without a second kernel: the
+// most that are resident at once and leave each warp a tile of 16 tokens while every CTA has an SM of
+// its own, 7 tiles where they share (16 rows x 2 heads of 2600: 8.2 us in 4 CTAs, one per SM, 9.0 in
+// 8), but for spans that give the warps of one CTA at most 4 tiles (2 at head_dim 256) just that one:
+// a cluster's launch and join cost 1.2 us (1 row x 8 heads of 300 tokens: 4.5 us, 4.8 in 4 CTAs;
+// of 800 6.5 and 5.3).  This is the way
+//   - where it gives a warp of a cluster at most 8 tiles (16 rows x 2 KV heads of 2600 tokens: 8.2 us
 //     against 11.7 for pieces; 8 x 2 groups of 12 heads of 4096 at head_dim 256:
 //     14.1 against 17.1), 6 at head_dim 256 in clusters of 8 (4 x 2 such groups of 8000: 18.7
-//     against 15.7), or
+//     against 15.7), and of a single CTA 16 (36 rows x 8 heads of 2000: 18.8 us against 26.7; of
+//     64 to 4000: 27.8 against 27.1), or
 //   - where the rows and heads alone fill the GPU and spans are at most 8192 tokens,
 //     so that a long row among short ones is not what is waited for (128 rows x 8 heads
 //     of 128 to 4096 tokens: 55 us against 93; 80 rows: 42 against 64).
 // Else balanced pieces, twice the wave rule's count as partial slots, and the join
 // kernel (about 3 us).
-constexpr int64_t kMx4WarpTiles = 8, kMx4WarpTilesWide = 6;
+constexpr int64_t kMx4WarpTiles = 8, kMx4WarpTilesWide = 6, kMx4WarpTilesRow = 16;
 constexpr int64_t kMx4RowTiles = 512;
-constexpr int32_t kMx4SharedTiles = 7;
+constexpr int32_t kMx4SharedTiles = 7, kMx4RowTilesOne = 4, kMx4RowTilesWide = 2;
 constexpr int64_t kMx4RankSpan = 1024;
 i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t* ns,
                      int32_t* chunk) {
@@ -350,8 +352,8 @@ i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t*
   int sms = 0;
   if ((st = sm_count(&sms)) != I8KV_OK) return st;
   while (!fills && c < i8kv::kMx4MaxCluster) {
-    // a tile per warp while every CTA has an SM of its own, else more of them
-    const int32_t each = 2LL * c * units > sms ? kMx4SharedTiles : 1;
+    int32_t each = 2LL * c * units > sms ? kMx4SharedTiles : 1;
+    if (c == 1) each = std::max(each, key.D > 128 ? kMx4RowTilesWide : kMx4RowTilesOne);
     if (c * i8kv::kMx4WideWarps * each >= tiles) break;
     int32_t more = 1;
     if ((st = mx4_clusters(key, units, 2 * c, &fits, &run, &more)) != I8KV_OK) return st;
@@ -359,7 +361,9 @@ i8kv_status mx4_auto(const KernelKey& key, int64_t span, int32_t units, int32_t*
     if (!fits || more < groups) break;
     c *= 2;
   }
-  const int64_t most = key.D > 128 && c == i8kv::kMx4MaxCluster ? kMx4WarpTilesWide : kMx4WarpTiles;
+  const int64_t most = c == 1                                          ? kMx4WarpTilesRow
+                       : key.D > 128 && c == i8kv::kMx4MaxCluster ? kMx4WarpTilesWide
+                                                                  : kMx4WarpTiles;
   if (fills || tiles <= most * i8kv::kMx4WideWarps * c) {
     *ns = c;
     *chunk = c > 1 ? 0 : static_cast<int32_t>(std::max<int64_t>(16, tiles * 16));
