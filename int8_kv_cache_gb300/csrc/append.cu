@@ -273,6 +273,12 @@ __device__ __forceinline__ void scales8(const AppendParams& p, const float* s, i
   }
 }
 
+__host__ __device__ __forceinline__ long long warps_of(long long threads) { return (threads + 31) / 32; }
+// floor(w part / all)
+__device__ __forceinline__ unsigned share_of(unsigned w, unsigned part, unsigned all) {
+  return all < 65536u ? w * part / all : (unsigned)((unsigned long long)w * part / all);
+}
+
 // HQ: query heads per thread (1: a few tokens, where threads are short; else 4).
 template <int CACHE, int HQ>
 __global__ void __launch_bounds__(kAppendThreads, 2)
@@ -283,17 +289,24 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
     __syncthreads();
   }
   grid_dependency_wait();
-  const int ipr = p.D >> 4;                           // items per row
-  const int groups = (p.Hq + HQ - 1) / HQ;
-  const int ipt = (groups + 2 * p.Hkv) * ipr;         // items per token
-  const unsigned flat = blockIdx.x * kAppendThreads + threadIdx.x;
-  const unsigned n0 = flat / (unsigned)ipt;
+  const int ipr = p.D >> 4;  // items per row
+  // Warps for queries and warps for keys and values (their loops differ, so none does both),
+  // spread evenly over the grid: `lanes` tokens of each at a time.
+  const unsigned q_items = (p.Hq + HQ - 1) / HQ * ipr, kv_items = 2 * p.Hkv * ipr;  // of a token
+  const unsigned q_warps = warps_of(lanes * q_items), warps = q_warps + warps_of(lanes * kv_items);
+  const unsigned w = blockIdx.x * (kAppendThreads / 32) + threadIdx.x / 32;
+  const unsigned before = share_of(w, q_warps, warps);  // warps for queries among those before
+  const bool queries = share_of(w + 1, q_warps, warps) != before;
+  const unsigned flat = (queries ? before : w - before) * 32 + (threadIdx.x & 31);
+  const unsigned items = queries ? q_items : kv_items;
+  if (w >= warps) return;
+  const unsigned n0 = flat / items;
   if (n0 >= (unsigned)lanes) return;
-  const int item = flat - n0 * ipt;
+  const int item = flat - n0 * items;
   const int unit = item / ipr, j = item - (item / ipr) * ipr;
   const bool il = p.interleaved != 0;
 
-  if (unit < groups) {  // queries: HQ heads of a token
+  if (queries) {  // HQ heads of a token
     const Pieces x = pieces_of(p, j, true);
     const int h0 = unit * HQ;
     int next = p.R > 0 ? __ldg(p.positions + n0) : 0;  // a position ahead of its angles
@@ -333,7 +346,7 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
   }
 
   // keys and values: two tokens at a time
-  const int kv = unit - groups;
+  const int kv = unit;
   const bool is_v = kv >= p.Hkv;
   const int h = is_v ? kv - p.Hkv : kv;
   const Pieces x = pieces_of(p, j, !is_v);
@@ -358,42 +371,55 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
   }
   const __half* src = (is_v ? p.v : p.k) + (long long)h * p.D;
   const long long stride = is_v ? p.v_stride : p.k_stride;
-  for (long long n = n0; n < p.num_tokens; n += 2 * lanes) {
-    uint4 ra[2], rb[2];
-    int slot[2], pos[2];
+  constexpr int N = 2;
+  int slot[N], pos[N];  // of the next tokens
+  auto look = [&](long long n) {
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N; ++i) {
       const long long m = n + i * lanes;
       slot[i] = -1;
       pos[i] = 0;
       if (m < p.num_tokens) {
-        ra[i] = *reinterpret_cast<const uint4*>(src + m * stride + x.c0);
-        rb[i] = *reinterpret_cast<const uint4*>(src + m * stride + x.c1);
         slot[i] = __ldg(p.slots + m);
         if (p.R > 0) pos[i] = __ldg(p.positions + m);
       }
     }
-    Angles g[2];
+  };
+  look(n0);
+  for (long long n = n0; n < p.num_tokens; n += N * lanes) {
+    uint4 ra[N], rb[N];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
+    for (int i = 0; i < N; ++i) {
+      const long long m = n + i * lanes;
+      if (m < p.num_tokens) {
+        ra[i] = *reinterpret_cast<const uint4*>(src + m * stride + x.c0);
+        rb[i] = *reinterpret_cast<const uint4*>(src + m * stride + x.c1);
+      }
+    }
+    Angles g[N];
+    int at[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      at[i] = slot[i];
       if (p.R > 0 && (pos[i] < 0 || (long long)pos[i] >= p.max_pos)) {
         // (one key item reports it)
         if (kv == 0 && j == 0 && slot[i] >= 0) flag_or(p.flags, I8KV_FLAG_BAD_POSITION);
-        slot[i] = -1;
+        at[i] = -1;
       } else if ((long long)slot[i] >= p.num_slots) {
         if (kv == 0 && j == 0) flag_or(p.flags, I8KV_FLAG_BAD_SLOT);
-        slot[i] = -1;
+        at[i] = -1;
       }
-      if (slot[i] >= 0 && x.turned) g[i] = angles_of(p, x, pos[i]);
+      if (at[i] >= 0 && x.turned) g[i] = angles_of(p, x, pos[i]);
     }
+    look(n + N * lanes);
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      if (slot[i] < 0) continue;
+    for (int i = 0; i < N; ++i) {
+      if (at[i] < 0) continue;
       float a[8], b[8];
       unpack8(ra[i], a);
       unpack8(rb[i], b);
       if (x.turned) turn_item(a, b, g[i], il);
-      store_item<CACHE>(p, x, h, is_v, slot[i], a, b, r0, r1, sc, step, inv_scale);
+      store_item<CACHE>(p, x, h, is_v, at[i], a, b, r0, r1, sc, step, inv_scale);
     }
   }
 }
@@ -548,10 +574,11 @@ namespace {
 
 template <int CACHE, int HQ>
 cudaError_t append_with(const AppendParams& p, int sms, cudaStream_t stream) {
-  const long long ipt = ((p.Hq + HQ - 1) / HQ + 2LL * p.Hkv) * (p.D / 16);
-  const long long lanes = lanes_of(p.num_tokens, ipt, 2LL * sms);  // the resident CTAs
+  const long long q_items = (p.Hq + HQ - 1LL) / HQ * (p.D / 16), kv_items = 2LL * p.Hkv * (p.D / 16);
+  const long long lanes = lanes_of(p.num_tokens, q_items + kv_items, 2LL * sms);  // the resident CTAs
   cudaLaunchAttribute attr;
-  const cudaLaunchConfig_t cfg = config_of(lanes * ipt, &attr, stream);
+  const cudaLaunchConfig_t cfg =
+      config_of(32 * (warps_of(lanes * q_items) + warps_of(lanes * kv_items)), &attr, stream);
   return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<CACHE, HQ>, p, lanes);
 }
 
