@@ -28,6 +28,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "../../include/int8kv.h"
 #include "codes.cuh"
 #include "device.cuh"
@@ -282,7 +284,7 @@ __device__ __forceinline__ unsigned share_of(unsigned w, unsigned part, unsigned
 // HQ: query heads per thread (1: a few tokens, where threads are short; else 4).
 template <int CACHE, int HQ>
 __global__ void __launch_bounds__(kAppendThreads, 2)
-rope_and_cache_kernel(const AppendParams p, long long lanes) {
+rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lanes) {
   __shared__ float inv_scale[CACHE == I8KV_CACHE_MX4 ? 128 : 1];
   if constexpr (CACHE == I8KV_CACHE_MX4) {
     if (threadIdx.x < 128) inv_scale[threadIdx.x] = threadIdx.x ? __frcp_rn(e4m3_value(threadIdx.x)) : 0.f;
@@ -291,15 +293,17 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
   grid_dependency_wait();
   const int ipr = p.D >> 4;  // items per row
   // Warps for queries and warps for keys and values (their loops differ, so none does both),
-  // spread evenly over the grid: `lanes` tokens of each at a time.
+  // spread evenly over the grid: as many as `q_lanes` and `kv_lanes` tokens at a time take.
+  // (27242 tokens, 10/2 heads, into MX4: 38 us against 56 with both in a warp.)
   const unsigned q_items = (p.Hq + HQ - 1) / HQ * ipr, kv_items = 2 * p.Hkv * ipr;  // of a token
-  const unsigned q_warps = warps_of(lanes * q_items), warps = q_warps + warps_of(lanes * kv_items);
+  const unsigned q_warps = warps_of(q_lanes * q_items), warps = q_warps + warps_of(kv_lanes * kv_items);
   const unsigned w = blockIdx.x * (kAppendThreads / 32) + threadIdx.x / 32;
   const unsigned before = share_of(w, q_warps, warps);  // warps for queries among those before
   const bool queries = share_of(w + 1, q_warps, warps) != before;
   const unsigned flat = (queries ? before : w - before) * 32 + (threadIdx.x & 31);
   const unsigned items = queries ? q_items : kv_items;
   if (w >= warps) return;
+  const long long lanes = queries ? q_lanes : kv_lanes;
   const unsigned n0 = flat / items;
   if (n0 >= (unsigned)lanes) return;
   const int item = flat - n0 * items;
@@ -345,7 +349,7 @@ rope_and_cache_kernel(const AppendParams p, long long lanes) {
     return;
   }
 
-  // keys and values: two tokens at a time
+  // keys and values: two tokens at a time, their slots and positions a step ahead
   const int kv = unit;
   const bool is_v = kv >= p.Hkv;
   const int h = is_v ? kv - p.Hkv : kv;
@@ -572,14 +576,22 @@ cudaLaunchConfig_t config_of(long long threads, cudaLaunchAttribute* attr, cudaS
 
 namespace {
 
+// Tokens of keys and values at a time for one of queries, so that their warps end together (the
+// former do two a pass; 32768 tokens, 32/8 heads, head_dim 128, at 0.5 / 0.7 / 0.8 / 1: MX4 130 / 120 /
+// 125 / 134 us, int8 142 / 129 / 129 / 136, e4m3fn 133 / 124 / 128 / 136, fp16 128 / 132 / 136 / 142).
+template <int CACHE>
+constexpr double kKvShare = CACHE == I8KV_CACHE_FP16 ? 0.5 : CACHE == I8KV_CACHE_INT8 ? 0.8 : 0.7;
+
 template <int CACHE, int HQ>
 cudaError_t append_with(const AppendParams& p, int sms, cudaStream_t stream) {
   const long long q_items = (p.Hq + HQ - 1LL) / HQ * (p.D / 16), kv_items = 2LL * p.Hkv * (p.D / 16);
-  const long long lanes = lanes_of(p.num_tokens, q_items + kv_items, 2LL * sms);  // the resident CTAs
+  const double per = 2. * sms * kAppendThreads / (q_items + kKvShare<CACHE> * kv_items);  // the resident CTAs
+  const long long q_lanes = std::clamp<long long>((long long)per, 1, p.num_tokens);
+  const long long kv_lanes = std::clamp<long long>((long long)(kKvShare<CACHE> * per), 1, p.num_tokens);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
-      config_of(32 * (warps_of(lanes * q_items) + warps_of(lanes * kv_items)), &attr, stream);
-  return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<CACHE, HQ>, p, lanes);
+      config_of(32 * (warps_of(q_lanes * q_items) + warps_of(kv_lanes * kv_items)), &attr, stream);
+  return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<CACHE, HQ>, p, q_lanes, kv_lanes);
 }
 
 // Four query heads per thread where one head each would fill the GPU more than once
