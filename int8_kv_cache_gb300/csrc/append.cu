@@ -281,6 +281,12 @@ __device__ __forceinline__ unsigned share_of(unsigned w, unsigned part, unsigned
   return all < 65536u ? w * part / all : (unsigned)((unsigned long long)w * part / all);
 }
 
+__device__ __forceinline__ void copy16(uint4* to, const __half* from) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;\n" ::"r"((uint32_t)__cvta_generic_to_shared(to)),
+               "l"(from)
+               : "memory");
+}
+
 // HQ: query heads per thread (1: a few tokens, where threads are short; else 4).
 template <int CACHE, int HQ>
 __global__ void __launch_bounds__(kAppendThreads, 2)
@@ -290,6 +296,7 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
     if (threadIdx.x < 128) inv_scale[threadIdx.x] = threadIdx.x ? __frcp_rn(e4m3_value(threadIdx.x)) : 0.f;
     __syncthreads();
   }
+  __shared__ uint4 ring[CACHE == I8KV_CACHE_FP16 ? 1 : 2][2][2][kAppendThreads];
   grid_dependency_wait();
   const int ipr = p.D >> 4;  // items per row
   // Warps for queries and warps for keys and values (their loops differ, so none does both),
@@ -349,7 +356,10 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
     return;
   }
 
-  // keys and values: two tokens at a time, their slots and positions a step ahead
+  // Keys and values: two tokens at a time, their slots and positions a step ahead, and so are their
+  // rows, in shared memory, on the way to codes (32768 tokens, 8 heads, MX4, not turned: 44 us against
+  // 57, turned 59 against 62; fp16 rows are stored at once and gain nothing: 128 us against 132 with
+  // 32/8 heads).
   const int kv = unit;
   const bool is_v = kv >= p.Hkv;
   const int h = is_v ? kv - p.Hkv : kv;
@@ -389,15 +399,33 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
       }
     }
   };
-  look(n0);
-  for (long long n = n0; n < p.num_tokens; n += N * lanes) {
-    uint4 ra[N], rb[N];
+  constexpr bool RING = CACHE != I8KV_CACHE_FP16;
+  auto fetch = [&](long long n, int st) {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const long long m = n + i * lanes;
       if (m < p.num_tokens) {
-        ra[i] = *reinterpret_cast<const uint4*>(src + m * stride + x.c0);
-        rb[i] = *reinterpret_cast<const uint4*>(src + m * stride + x.c1);
+        copy16(&ring[st][i][0][threadIdx.x], src + m * stride + x.c0);
+        copy16(&ring[st][i][1][threadIdx.x], src + m * stride + x.c1);
+      }
+    }
+    asm volatile("cp.async.commit_group;\n" ::: "memory");
+  };
+  if constexpr (RING) fetch(n0, 0);
+  look(n0);
+  int st = 0;
+  for (long long n = n0; n < p.num_tokens; n += N * lanes, st ^= 1) {
+    uint4 raw[N][2];
+    if constexpr (RING) {
+      fetch(n + N * lanes, st ^ 1);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const long long m = n + i * lanes;
+        if (m < p.num_tokens) {
+          raw[i][0] = *reinterpret_cast<const uint4*>(src + m * stride + x.c0);
+          raw[i][1] = *reinterpret_cast<const uint4*>(src + m * stride + x.c1);
+        }
       }
     }
     Angles g[N];
@@ -416,12 +444,13 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
       if (at[i] >= 0 && x.turned) g[i] = angles_of(p, x, pos[i]);
     }
     look(n + N * lanes);
+    if constexpr (RING) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (at[i] < 0) continue;
       float a[8], b[8];
-      unpack8(ra[i], a);
-      unpack8(rb[i], b);
+      unpack8(RING ? ring[st][i][0][threadIdx.x] : raw[i][0], a);
+      unpack8(RING ? ring[st][i][1][threadIdx.x] : raw[i][1], b);
       if (x.turned) turn_item(a, b, g[i], il);
       store_item<CACHE>(p, x, h, is_v, at[i], a, b, r0, r1, sc, step, inv_scale);
     }
@@ -577,10 +606,11 @@ cudaLaunchConfig_t config_of(long long threads, cudaLaunchAttribute* attr, cudaS
 namespace {
 
 // Tokens of keys and values at a time for one of queries, so that their warps end together (the
-// former do two a pass; 32768 tokens, 32/8 heads, head_dim 128, at 0.5 / 0.7 / 0.8 / 1: MX4 130 / 120 /
-// 125 / 134 us, int8 142 / 129 / 129 / 136, e4m3fn 133 / 124 / 128 / 136, fp16 128 / 132 / 136 / 142).
+// former do two a pass; 32768 tokens, 32/8 heads, head_dim 128, at 0.5 / 0.6 / 0.7 / 0.8: MX4 124 / 118 /
+// 121 / 126 us, int8 129 / 122 / 125 / 129, e4m3fn 118 / 120 / 124 / 129, fp16 128 / 130 / 132 / 136;
+// 4646 tokens, 128/8, 256, int8: 116 / 106 / 104 / 102).
 template <int CACHE>
-constexpr double kKvShare = CACHE == I8KV_CACHE_FP16 ? 0.5 : CACHE == I8KV_CACHE_INT8 ? 0.8 : 0.7;
+constexpr double kKvShare = CACHE == I8KV_CACHE_FP16 ? 0.5 : 0.65;
 
 template <int CACHE, int HQ>
 cudaError_t append_with(const AppendParams& p, int sms, cudaStream_t stream) {
