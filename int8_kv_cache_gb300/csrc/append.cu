@@ -22,9 +22,10 @@
 // cosines: 64 of the 192 bytes that a head would load).  An MX4 block of 16 channels is
 // one piece of each of two neighbouring lanes, which exchange their maxima.
 // Measured on one GB300 (graph of calls): 32768 tokens, 32/8 heads, head_dim 128, all of it
-// turned, into MX4: 132 us for 726 MB, 5.5 TB/s, 81 % of the measured copy rate (not turned:
-// 117 us, 89 %); 16 tokens 2.6 us.  What is short of the rate are loads in flight, at 16
-// warps per SM; more per thread (rows a token ahead, a shared-memory ring) measured no faster.
+// turned, into MX4: 119 us for 726 MB, 6.1 TB/s, 90 % of the measured copy rate; 16 tokens 2.6 us.
+// Keys and values alone are short of the rate (8 heads, MX4: 59 us for 189 MB): what they wait
+// for are sines and cosines, at 16 warps per SM; 24 of fewer registers and one token each
+// measured no faster (62), nor sines and cosines a step ahead (60).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
