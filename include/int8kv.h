@@ -377,6 +377,8 @@ i8kv_status paged_decode_ex(const uint16_t* q, const void* k_cache, const void* 
  *   lse = M + ln L;  O <- O / (1 + exp(s_h - lse)) if a sink is given.
  * Splits with m_k = -inf are skipped (their acc is not read); all skipped:
  * O = 0, lse = -inf.
+ * A split with m_k > -inf and a sum l_k that is NaN (or m_k = +inf or NaN): O
+ * and lse are NaN.
  *   acc [units, num_splits, G, D], m, l [units, num_splits, G] fp32 (the
  *   workspace layout of split_workspace_bytes); unit u = row * Hkv + g;
  *   G = Hq / Hkv; out [units*G, D] fp16 (= [rows, Hq, D]); lse [units*G] or

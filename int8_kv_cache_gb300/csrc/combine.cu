@@ -11,6 +11,8 @@
 // the (m, l) of all splits (lane k holds split k) and reduces M and L with
 // shuffles.  The accumulator of a split with m = -inf (an empty split, never
 // written) is loaded with the others but selected away, never multiplied.
+// A split with m > -inf attended something: a sum of its that is no number (a query that is
+// not finite, a CTA that gave up waiting) makes O and lse NaN, whatever its weight.
 // The head's sink logit is loaded together with the partials.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -63,6 +65,7 @@ combine_kernel(const float* __restrict__ acc, const float* __restrict__ m,
   for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   const float f = (mk == neg_inf()) ? 0.f : fast_exp2((mk - M) * kLog2e);
   float L = f * lk;
+  const bool nan = __any_sync(0xffffffffu, mk != neg_inf() && L != L);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
 
@@ -84,6 +87,8 @@ combine_kernel(const float* __restrict__ acc, const float* __restrict__ m,
     lse_v = M + logf(L);
     scale = 1.f / L;
     if (sink != nullptr) scale *= 1.f / (1.f + expf(sink_h - lse_v));
+  } else if (nan) {
+    lse_v = scale = __int_as_float(0x7fc00000);
   }
   __half* dst = out + (long long)wid * D + c0;
   if constexpr (V == 2) {

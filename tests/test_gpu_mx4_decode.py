@@ -495,3 +495,17 @@ def test_two_streams_at_once(K):
     torch.cuda.synchronize()
     for o, w in zip(outs, wants):
         assert all(np.array_equal(x.double().cpu().numpy(), w[0]) for x in o)
+
+
+@pytest.mark.parametrize("per_channel", [False, True])
+def test_lse_of_a_head_that_is_not_finite(K, per_channel):
+    # NaN whichever way the work is cut, as the outputs are
+    c = case(43, 2, 8, 1, 128, 16, 40, [600, 33], per_channel)
+    c["q"][0, 2, 5], c["q"][0, 6, 7], c["q"][1, 1, 9] = np.nan, np.inf, -np.inf
+    bad = np.zeros((2, 8), bool)
+    bad[0, [2, 6]] = bad[1, 1] = True
+    for ns, chunk in ((0, 0), (1, 640), (2, 0), (5, 0), (8, 0), (10, 64), (32, 0)):
+        o, l = run(K, c, ns=ns, chunk=chunk)
+        assert np.isnan(l[bad]).all(), (ns, chunk)
+        assert np.isnan(o[bad]).all(), (ns, chunk)
+        assert np.isfinite(l[~bad]).all() and np.isfinite(o[~bad]).all(), (ns, chunk)
