@@ -539,6 +539,11 @@ mx4_decode_kernel(const DecodeParams p) {
       }
     } else {
       inv = p.k_scale[0];
+      // an infinity becomes a NaN (as the second numbers make it above): its scores could all be
+      // -inf, which is no sum at all
+      __half2* q2 = reinterpret_cast<__half2*>(&v);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) q2[k] = __hadd2(q2[k], __hsub2(q2[k], q2[k]));
     }
     *reinterpret_cast<uint4*>(sq + h * T::kQRow + d) = v;
     // accumulator -> score in log2 units (natural units with a softcap)

@@ -509,3 +509,20 @@ def test_lse_of_a_head_that_is_not_finite(K, per_channel):
         assert np.isnan(l[bad]).all(), (ns, chunk)
         assert np.isnan(o[bad]).all(), (ns, chunk)
         assert np.isfinite(l[~bad]).all() and np.isfinite(o[~bad]).all(), (ns, chunk)
+
+
+@pytest.mark.parametrize("D,per_channel", [(64, False), (128, False), (256, False), (128, True)])
+@pytest.mark.parametrize("inf", [np.inf, -np.inf])
+def test_an_infinite_query_whose_scores_all_have_one_sign(K, D, per_channel, inf):
+    # every key has the same sign in the channel, so every score is +inf or every one -inf
+    c = case(44 + D, 2, 4, 1, D, 16, 8, [128, 20], per_channel)
+    c["cache"][..., :8 * D] = 0x22  # code 1.0 in every channel of every key
+    ref = reference(c)
+    c["q"][0, 1, 3] = inf
+    bad = np.zeros((2, 4), bool)
+    bad[0, 1] = True
+    for ns, chunk in ((0, 0), (1, 128), (2, 0), (5, 0), (4, 32)):
+        o, l = run(K, c, ns=ns, chunk=chunk)
+        assert np.isnan(o[bad]).all() and np.isnan(l[bad]).all(), (ns, chunk)
+        pick = lambda x: x[~bad][None]
+        compare(dict(c, q=c["q"][~bad][None]), (pick(o), pick(l)), [pick(x) for x in ref], what=f"{ns} splits of {chunk}")
