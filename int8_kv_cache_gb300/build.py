@@ -69,7 +69,7 @@ def _compile(src: str, verbose: bool):
 
 
 def _compile_binding():
-    """The object of csrc/binding.cpp and whether it is new."""
+    """The object of csrc/binding.cpp."""
     import torch
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
@@ -85,14 +85,14 @@ def _compile_binding():
             h.update(fh.read())
     stamp = obj + ".sha"
     if os.path.exists(obj) and os.path.exists(stamp) and open(stamp).read() == h.hexdigest():
-        return obj, False
+        return obj
     cmd = ["g++"] + flags + [x for p in inc for x in ("-isystem", p)] + ["-c", src, "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"g++ failed for {src}:\n{r.stdout}\n{r.stderr}")
     with open(stamp, "w") as fh:
         fh.write(h.hexdigest())
-    return obj, True
+    return obj
 
 
 def _link_binding(obj: str) -> None:
@@ -114,7 +114,7 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding_obj, binding_new = binding.result()
+        binding_obj = binding.result()
     objs = [o for o, _ in results]
     if verbose:
         for o, log in results:
@@ -125,9 +125,12 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    # the binding is linked anew with every library: one left from an earlier header would call
+    # this library's functions with that header's arguments
+    if os.path.exists(BINDING):
+        os.remove(BINDING)
     os.replace(tmp, LIB)
-    if binding_new or not os.path.exists(BINDING):
-        _link_binding(binding_obj)
+    _link_binding(binding_obj)
     return LIB
 
 
