@@ -3,10 +3,11 @@ the Python binding with the host compiler.
 
 Every CUDA translation unit under ``csrc/`` is compiled to an object file in
 parallel (one ``-gencode`` for sm_103a), then linked into
-``int8_kv_cache_gb300/libint8kv.so``; ``csrc/binding.cpp`` becomes
-``int8_kv_cache_gb300/_binding.so``, which uses that library.  An object is
-rebuilt when its source, any header of ``csrc/``, the public header, the flags
-(or, for the binding, the PyTorch version) changed.
+``int8_kv_cache_gb300/libint8kv.so``, which needs nothing but nvcc.  Then
+``csrc/binding.cpp`` becomes ``int8_kv_cache_gb300/_binding.so``, which uses
+that library; it is left out where there is no PyTorch, whose tensors it takes.
+An object is rebuilt when its source, any header of ``csrc/``, the public
+header, the flags (or, for the binding, the PyTorch version) changed.
 """
 from __future__ import annotations
 
@@ -69,8 +70,11 @@ def _compile(src: str, verbose: bool):
 
 
 def _compile_binding():
-    """The object of csrc/binding.cpp."""
-    import torch
+    """The object of csrc/binding.cpp, or None without PyTorch."""
+    try:
+        import torch
+    except ImportError:
+        return None
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     inc = [os.path.join(base, "include"),
@@ -114,7 +118,6 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     with ThreadPoolExecutor(max_workers=jobs) as ex:
         binding = ex.submit(_compile_binding)
         results = list(ex.map(lambda s: _compile(s, verbose), srcs))
-        binding_obj = binding.result()
     objs = [o for o, _ in results]
     if verbose:
         for o, log in results:
@@ -130,7 +133,9 @@ def build(verbose: bool = False, jobs: int = 0) -> str:
     if os.path.exists(BINDING):
         os.remove(BINDING)
     os.replace(tmp, LIB)
-    _link_binding(binding_obj)
+    obj = binding.result()
+    if obj is not None:
+        _link_binding(obj)
     return LIB
 
 

@@ -65,3 +65,19 @@ def test_a_binding_of_another_header_is_never_kept(tree, broken):
     c.fail = lambda cmd: False
     B.build()
     assert (path / "_binding.so").read_text() == old
+
+
+def test_the_library_does_not_wait_for_the_binding(tree):
+    # a binding that does not compile is an error, with the library there for callers in C
+    path, c = tree
+    c.fail = lambda cmd: cmd[cmd.index("-o") + 1].endswith("binding.o")
+    with pytest.raises(RuntimeError):
+        B.build()
+    assert (path / "libint8kv.so").exists()
+
+
+def test_the_library_needs_no_pytorch(tree, monkeypatch):
+    path, c = tree
+    monkeypatch.setitem(sys.modules, "torch", None)
+    assert B.build() == str(path / "libint8kv.so")
+    assert (path / "libint8kv.so").exists() and not (path / "_binding.so").exists()
