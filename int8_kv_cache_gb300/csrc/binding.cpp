@@ -150,9 +150,16 @@ Scales scales_of(PyObject* k, PyObject* v, int32_t kind, const Cache& c, int dev
   const int64_t n = kind == I8KV_SCALE_PER_CHANNEL ? c.Hkv * c.D : 1;
   const auto one = [&](PyObject* o, const char* name) {
     const float* p = static_cast<const float*>(dense(o, name, at::kFloat, dev));
-    if (THPVariable_Unpack(o).numel() != n)
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if (t.numel() != n)
       refuse(PyExc_ValueError, std::string(name) + ": expected " + std::to_string(n) +
-                                   " values, got " + std::to_string(THPVariable_Unpack(o).numel()));
+                                   " values, got " + std::to_string(t.numel()));
+    // [Hkv, D] or the same in a row, dimensions of one aside: the channels are the last
+    int64_t last = 1;
+    for (const int64_t d : t.sizes()) last = d != 1 ? d : last;
+    if (n > 1 && last != c.D && last != n)
+      refuse(PyExc_ValueError, std::string(name) + ": expected shape " + text_of({c.Hkv, c.D}) +
+                                   ", got " + text_of(t.sizes()));
     return p;
   };
   return Scales{one(k, "k_scale"), one(v, "v_scale")};

@@ -319,3 +319,33 @@ def test_append_then_gather_in_a_graph_on_another_stream(K, kind):
         if kind == "mx4":
             err = (v.float() - d["v"].float()).abs()
             assert (err <= d["v"].float().abs().amax() / 4).all()
+
+
+def test_scales_of_another_shape_are_refused(K):
+    # [D, Hkv] has as many values as [Hkv, D]
+    for kind in ("int8", "mx4"):
+        c = make(13, kind, 8, 4, 2, 64, 64, True)
+        d = on_device(c)
+        slots = torch.arange(4, dtype=torch.int32, device="cuda")
+        turned = d["ks"].t().contiguous()
+        before = d["kc"].clone()
+        for kw in (dict(ks=turned), dict(vs=turned)):
+            with pytest.raises(ValueError, match="_scale"):
+                append(K, c, dict(d, **kw))
+            e = dict(d, **kw)
+            with pytest.raises(ValueError, match="_scale"):
+                K.gather_cache(slots, d["kc"], d["vc"], e["ks"], e["vs"], 2)
+            if kind == "mx4":
+                lens = torch.ones(1, dtype=torch.int32, device="cuda")
+                with pytest.raises(ValueError, match="_scale"):
+                    K.paged_decode_mx4(d["q"][:1].contiguous(), d["kc"], e["ks"], e["vs"], 2, lens[:, None] * 0, lens, 0.1)
+        assert torch.equal(before, d["kc"])
+        # the same numbers in a row, or with dimensions of one, are taken
+        want = K.gather_cache(slots, d["kc"], d["vc"], d["ks"], d["vs"], 2)
+        for view in (lambda s: s.view(-1), lambda s: s.view(1, 2, 1, 64), lambda s: s.view(2, 64, 1)):
+            got = K.gather_cache(slots, d["kc"], d["vc"], view(d["ks"]), view(d["vs"]), 2)
+            assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+        one = make(14, kind, 8, 4, 1, 64, 64, True)  # one head: [D, 1] is [1, D]
+        d = on_device(one)
+        d["ks"] = d["ks"].t()
+        append(K, one, dict(d, ks=d["ks"].contiguous()))
