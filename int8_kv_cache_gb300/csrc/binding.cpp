@@ -203,6 +203,13 @@ struct Stream {
   }
 };
 
+// The interpreter runs other threads while the C entry point enqueues: a launch waits where the
+// queue of launches is full.
+struct Unlocked {
+  PyThreadState* state = PyEval_SaveThread();
+  ~Unlocked() { PyEval_RestoreThread(state); }
+};
+
 // The current device; a tensor on the host is refused before the device is asked for.
 int device_of(PyObject* o, const char* name) {
   const at::Tensor& t = tensor_of(o, name);
@@ -269,13 +276,17 @@ PyObject* py_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
     } else if (out != Py_None) {
       refuse(PyExc_ValueError, "q_out without q");
     }
-    const i8kv_status st = rope_and_cache(
-        q.p, q.stride, k.p, k.stride, v.p, v.stride, static_cast<const int32_t*>(pos),
-        static_cast<const float*>(cs), max_pos, size32(R, "rot_dim"),
-        style ? I8KV_ROPE_INTERLEAVED : I8KV_ROPE_HALVES, static_cast<const int32_t*>(slots),
-        size32(T, "T"), size32(q.heads, "Hq"), size32(c.Hkv, "Hkv"), size32(c.D, "D"),
-        static_cast<uint16_t*>(qo), c.k, c.v, c.dtype, c.slots, c.block_size, s.k, s.v, kind,
-        static_cast<uint32_t*>(flags), stream.handle);
+    const int32_t tokens = size32(T, "T"), Hq = size32(q.heads, "Hq"), Hkv = size32(c.Hkv, "Hkv");
+    const int32_t D = size32(c.D, "D"), rot = size32(R, "rot_dim");
+    const i8kv_status st = [&] {
+      const Unlocked other_threads_run;
+      return rope_and_cache(q.p, q.stride, k.p, k.stride, v.p, v.stride,
+                            static_cast<const int32_t*>(pos), static_cast<const float*>(cs), max_pos,
+                            rot, style ? I8KV_ROPE_INTERLEAVED : I8KV_ROPE_HALVES,
+                            static_cast<const int32_t*>(slots), tokens, Hq, Hkv, D,
+                            static_cast<uint16_t*>(qo), c.k, c.v, c.dtype, c.slots, c.block_size,
+                            s.k, s.v, kind, static_cast<uint32_t*>(flags), stream.handle);
+    }();
     if (st != I8KV_OK) return status(st);
     if (made.defined()) return THPVariable_Wrap(made);
     return Py_NewRef(out);
@@ -314,10 +325,14 @@ PyObject* py_gather_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
         p[i] = shaped(a[6 + i], names[i], at::kHalf, dev, {N, c.Hkv, c.D});
       }
     }
-    const i8kv_status st = gather_cache(
-        static_cast<const int32_t*>(slots), size32(N, "N"), size32(c.Hkv, "Hkv"), size32(c.D, "D"),
-        c.k, c.v, c.dtype, c.slots, c.block_size, s.k, s.v, kind, static_cast<uint16_t*>(p[0]),
-        static_cast<uint16_t*>(p[1]), static_cast<uint32_t*>(flags), stream.handle);
+    const int32_t rows = size32(N, "N"), Hkv = size32(c.Hkv, "Hkv"), D = size32(c.D, "D");
+    const i8kv_status st = [&] {
+      const Unlocked other_threads_run;
+      return gather_cache(static_cast<const int32_t*>(slots), rows, Hkv, D, c.k, c.v, c.dtype,
+                          c.slots, c.block_size, s.k, s.v, kind, static_cast<uint16_t*>(p[0]),
+                          static_cast<uint16_t*>(p[1]), static_cast<uint32_t*>(flags),
+                          stream.handle);
+    }();
     if (st != I8KV_OK) return status(st);
     PyObject* r = PyTuple_New(2);
     if (r == nullptr) return nullptr;
@@ -377,14 +392,20 @@ PyObject* py_paged_decode_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
         out = shaped(a[12], "out", at::kHalf, dev, qt.sizes());
       }
     }
-    const i8kv_status st = paged_decode_mx4(
-        static_cast<const uint16_t*>(q), c.k, s.k, s.v, kind, static_cast<const int32_t*>(table),
-        static_cast<const int32_t*>(lens), size32(B, "B"), size32(Hq, "Hq"), size32(c.Hkv, "Hkv"),
-        size32(c.D, "D"), c.block_size, size32(bt.size(1), "max_blocks"), c.blocks,
-        float_of(a[7], "softmax_scale"), static_cast<const float*>(sink), float_of(a[17], "softcap"),
-        int_of(a[18], "window"), int_of(a[9], "num_splits"), int_of(a[10], "chunk"), ws, ws_bytes,
-        static_cast<uint16_t*>(out), static_cast<float*>(lse), static_cast<uint32_t*>(flags),
-        stream.handle);
+    const int32_t rows = size32(B, "B"), heads = size32(Hq, "Hq"), Hkv = size32(c.Hkv, "Hkv");
+    const int32_t D = size32(c.D, "D"), max_blocks = size32(bt.size(1), "max_blocks");
+    const float sigma = float_of(a[7], "softmax_scale"), softcap = float_of(a[17], "softcap");
+    const int32_t window = int_of(a[18], "window"), splits = int_of(a[9], "num_splits");
+    const int32_t chunk = int_of(a[10], "chunk");
+    const i8kv_status st = [&] {
+      const Unlocked other_threads_run;
+      return paged_decode_mx4(static_cast<const uint16_t*>(q), c.k, s.k, s.v, kind,
+                              static_cast<const int32_t*>(table), static_cast<const int32_t*>(lens),
+                              rows, heads, Hkv, D, c.block_size, max_blocks, c.blocks, sigma,
+                              static_cast<const float*>(sink), softcap, window, splits, chunk, ws,
+                              ws_bytes, static_cast<uint16_t*>(out), static_cast<float*>(lse),
+                              static_cast<uint32_t*>(flags), stream.handle);
+    }();
     if (st != I8KV_OK) return status(st);
     if (made.defined()) return THPVariable_Wrap(made);
     return Py_NewRef(partials ? Py_None : a[12]);

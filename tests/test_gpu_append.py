@@ -349,3 +349,38 @@ def test_scales_of_another_shape_are_refused(K):
         d = on_device(one)
         d["ks"] = d["ks"].t()
         append(K, one, dict(d, ks=d["ks"].contiguous()))
+
+
+def test_other_threads_run_while_a_call_waits_for_the_queue(K):
+    # calls behind a kernel that takes a while fill the queue of launches, and one waits for room in it
+    import threading
+    import time
+    c = make(15, "int8", 4, 2, 1, 64, 64, True)
+    d = on_device(c)
+    append(K, c, d, q_out=d["q"])
+    torch.cuda.synchronize()
+    gaps, stop = [0.0], threading.Event()
+
+    def tick():
+        last = time.perf_counter()
+        while not stop.is_set():
+            time.sleep(0.001)
+            now = time.perf_counter()
+            gaps[0] = max(gaps[0], now - last)
+            last = now
+    th = threading.Thread(target=tick)
+    th.start()
+    try:
+        time.sleep(0.05)
+        t0 = time.perf_counter()
+        torch.cuda._sleep(800_000_000)  # cycles: 0.4 s or more
+        for _ in range(3000):
+            append(K, c, d, q_out=d["q"])
+        waited = time.perf_counter() - t0
+        torch.cuda.synchronize()
+    finally:
+        stop.set()
+        th.join()
+    if waited < 0.3:
+        pytest.skip("the queue took every launch")
+    assert gaps[0] < 0.15
