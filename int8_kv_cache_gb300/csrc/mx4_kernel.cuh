@@ -142,7 +142,8 @@ __device__ Mx4Item balanced_piece(const DecodeParams& p, int c) {
       it.unit = it.row * Hkv + it.g;
       it.tile0 = (it.wlo >> 4) + it.slot * per_s;
       it.stride = W;
-      it.hi = min((it.tile0 + per_s) * 16, len_s);
+      // (the last piece's end, rounded up to whole tiles per piece, may be past 2^31 tokens)
+      it.hi = it.tile0 + per_s <= len_s >> 4 ? (it.tile0 + per_s) * 16 : len_s;
       it.pieces = n_s;
       it.valid = true;
       return it;

@@ -526,3 +526,29 @@ def test_an_infinite_query_whose_scores_all_have_one_sign(K, D, per_channel, inf
         assert np.isnan(o[bad]).all() and np.isnan(l[bad]).all(), (ns, chunk)
         pick = lambda x: x[~bad][None]
         compare(dict(c, q=c["q"][~bad][None]), (pick(o), pick(l)), [pick(x) for x in ref], what=f"{ns} splits of {chunk}")
+
+
+@pytest.mark.parametrize("window", [-1, 1 << 30])
+def test_the_longest_sequence(K, window):
+    # 2^31 - 32 tokens, as many as positions of 32 bits take: a table that names one block over and over.
+    # Zero queries and values of 1 make every sum exact: the mean is 1, the lse log of the tokens
+    D, tiles, mb = 64, 6 * 8191, 2731
+    n = 16 * tiles * mb
+    assert n == 2 ** 31 - 32
+    cache = torch.zeros((1, 1, tiles, 18 * D), dtype=torch.uint8, device="cuda")
+    cache[..., 9 * D:17 * D] = 0x22
+    cache[..., 17 * D:] = 0x38
+    one = torch.ones(1, device="cuda")
+    q = torch.zeros((1, 2, D), dtype=torch.float16, device="cuda")
+    table = torch.zeros((1, mb), dtype=torch.int32, device="cuda")
+    ws = workspace(K, 1, 2, D)
+    for length in (n, n - 500):
+        live = length if window < 0 else min(length, window + 1)
+        lens = torch.tensor([length], dtype=torch.int32, device="cuda")
+        for ns in (32, 31, 0):
+            lse = torch.empty((1, 2), device="cuda")
+            out = K.paged_decode_mx4(q, cache, one, one, 1, table, lens, 0.125, num_splits=ns, workspace=ws, lse=lse,
+                                     window=window)
+            assert (out == 1).all()
+            # (the logarithm of 2^31 / 32, and its sum with 8 log 2 and the pieces': a few steps of 2^-20)
+            assert (lse.double() - np.log(live)).abs().max().item() <= 1e-5, (length, ns)
