@@ -93,6 +93,7 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 // The same codes from the products with the rounded reciprocals r, which are within
 // |q| 2^-22 of the rounded quotients: where a product is nearer to a rounding boundary
 // than that allows (about one piece in a thousand), or a NaN, the quotients decide.
+// (A scale below 2^-128 has no finite reciprocal, and a NaN stands for it.)
 template <bool FP8>
 __device__ __forceinline__ uint2 codes8(const float (&x)[8], const float (&r)[8],
                                         const float* __restrict__ s, int s_step) {
@@ -276,6 +277,14 @@ __device__ __forceinline__ void scales8(const AppendParams& p, const float* s, i
   }
 }
 
+// 1 / s as the codes take it: MX4's are defined by the rounded reciprocal, the others by the quotient,
+// of which an infinite reciprocal says nothing.
+template <int CACHE>
+__device__ __forceinline__ float reciprocal(float s) {
+  const float r = __frcp_rn(s);
+  return CACHE != I8KV_CACHE_MX4 && isinf(r) ? __int_as_float(0x7fc00000) : r;
+}
+
 __host__ __device__ __forceinline__ long long warps_of(long long threads) { return (threads + 31) / 32; }
 // floor(w part / all)
 __device__ __forceinline__ unsigned share_of(unsigned w, unsigned part, unsigned all) {
@@ -375,11 +384,11 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
     if (p.per_channel) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        r0[i] = __frcp_rn(r0[i]);
-        r1[i] = __frcp_rn(r1[i]);
+        r0[i] = reciprocal<CACHE>(r0[i]);
+        r1[i] = reciprocal<CACHE>(r1[i]);
       }
     } else {
-      const float r = __frcp_rn(r0[0]);
+      const float r = reciprocal<CACHE>(r0[0]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) r0[i] = r1[i] = r;
     }

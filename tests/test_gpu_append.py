@@ -384,3 +384,21 @@ def test_other_threads_run_while_a_call_waits_for_the_queue(K):
     if waited < 0.3:
         pytest.skip("the queue took every launch")
     assert gaps[0] < 0.15
+
+
+@pytest.mark.parametrize("kind", ["int8", "e4m3"])
+@pytest.mark.parametrize("per_channel", [False, True])
+def test_scales_whose_reciprocal_overflows(K, kind, per_channel):
+    # scales below 2^-128: 1 / scale is infinite in fp32 and x / scale need not be.  Keys turned by
+    # cosines as small (nothing else brings an fp16 number down there); the codes are the quotients'
+    rng = np.random.default_rng(12)
+    T, Hkv, D, R = 24, 2, 64, 64
+    c = make(12, kind, T, 1, Hkv, D, R, per_channel)
+    c["k"] = rng.integers(-3, 4, (T, Hkv, D)).astype(np.float16)
+    c["cs"] = (rng.integers(0, 100, c["cs"].shape) * 2.0 ** -140).astype(np.float32)
+    c["ks"] = (rng.integers(1, 5, c["ks"].shape) * 2.0 ** -139).astype(np.float32)
+    c["v"][1, 0, :4] = 1
+    with np.errstate(all="ignore"):
+        kr = oracle.rotate(c["k"], c["cs"], c["pos"], False)
+        assert np.isinf(np.float32(1) / c["ks"]).all() and (np.abs(kr / c["ks"].max()) < 100).mean() > 0.5
+    check(K, c, False)
