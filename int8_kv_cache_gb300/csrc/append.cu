@@ -41,8 +41,6 @@ namespace i8kv {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr float kLoBound = 1.f - 0x1p-21f;
-constexpr float kHiBound = 1.f + 0x1p-21f;
 
 __device__ __forceinline__ void unpack8(uint4 r, float (&x)[8]) {
   const __half2* h = reinterpret_cast<const __half2*>(&r);

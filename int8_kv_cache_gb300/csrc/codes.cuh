@@ -9,6 +9,11 @@
 
 namespace i8kv {
 
+// A product with a rounded reciprocal is within its 2^-22 of the rounded quotient: codes of
+// both ends of a wider interval that agree are the quotient's.
+constexpr float kLoBound = 1.f - 0x1p-21f;
+constexpr float kHiBound = 1.f + 0x1p-21f;
+
 __device__ __forceinline__ float nan_to_zero(float q) { return q != q ? 0.f : q; }
 
 __device__ __forceinline__ float int8_code(float q) {

@@ -42,12 +42,13 @@ struct DecodeParams {
   // the device into pieces of about equal length across the batch, at most
   // num_splits per row (the partial slots), bal_pieces (row, piece) pairs in
   // all, each a multiple of bal_round positions; the grid has
-  // ceil(num_splits / 2) CTAs per unit (decode_kernel.cuh, balanced_item)
-  int32_t longest_first;     // MX4 rows: they are taken in the order of falling lengths
-  int32_t head_groups;       // MX4 rows and clusters: 2: each half of a group's query heads is a unit of its own
+  // ceil(num_splits / 2) CTAs per unit (decode_kernel.cuh, balanced_item).  MX4: the rule and
+  // the grid (at most bal_pieces CTAs) are mx4_kernel.cuh's balanced_piece; bal_round is not used
   int32_t balanced;
   int32_t bal_round;
   int32_t bal_pieces;
+  int32_t longest_first;     // MX4 rows: they are taken in the order of falling lengths
+  int32_t head_groups;       // MX4 rows and clusters: 2: each half of a group's query heads is a unit of its own
 };
 
 // Longest-first dispatch of the paged decode (decode_kernel.cuh, lpt_item):

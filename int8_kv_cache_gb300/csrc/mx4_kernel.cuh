@@ -873,7 +873,10 @@ mx4_decode_kernel(const DecodeParams p) {
               make_float4(acc[t][nt][j], acc[t][nt][2 + j], acc[t + 1][nt][j], acc[t + 1][nt][2 + j]);
       }
     }
-  // a join kernel may be launched now: its CTAs wait for this grid's writes
+  // The kernel that follows in the stream (the join, or in the other ways whatever comes next) may be
+  // launched now; its CTAs wait for this grid's end before they touch memory.  Graphs of calls,
+  // without / with it: one context of 300 tokens 4.47 / 4.32 us, 16 x 2600 8.82 / 8.59,
+  // one of 32768 17.1 / 16.7, 16 x 512-8192 24.4 / 24.3.
   asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
   __syncthreads();
   const long long head0 = (long long)it.row * p.Hq + it.g * p.G + h0;
@@ -1036,7 +1039,7 @@ template <int D, int NT, int W, Mx4Way WAY>
 cudaError_t run_mx4(const DecodeParams& p, cudaStream_t s, KernelInfo* info) {
   if (!p.per_channel) return run_mx4_with<D, NT, W, WAY, kPlain>(p, s, info);
   if constexpr (NT == 1) {
-    if ((p.head_groups == 2 ? (p.G + 1) / 2 : p.G) <= 4)
+    if (p.G <= 4)  // (groups that run in halves have 9 heads at least, one half 5)
       return run_mx4_with<D, NT, W, WAY, kColumns>(p, s, info);
   }
   return run_mx4_with<D, NT, W, WAY, kProducts>(p, s, info);

@@ -31,9 +31,6 @@ namespace i8kv {
 
 namespace {
 
-constexpr float kLoBound = 1.f - 0x1p-21f;
-constexpr float kHiBound = 1.f + 0x1p-21f;
-
 // Codes of 8 fp16 values (channel j in byte j % 4 of word j / 4) from the
 // fp32 quotients x[j] / s[j * s_step] themselves: the exact path, taken for a
 // piece with a quotient near a rounding boundary.
