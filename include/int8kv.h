@@ -108,7 +108,10 @@ typedef enum {
 const char* i8kv_status_string(int status);
 
 /* Library ABI version (major*100 + minor).  3.0: dsa_prefill_ws and
- * dsa_prefill_workspace_bytes take num_splits; dsa_prefill_auto_splits. */
+ * dsa_prefill_workspace_bytes take num_splits; dsa_prefill_auto_splits.  The
+ * number names the signatures: functions that are added leave it as it is, and
+ * a caller that loads the library finds them by name (rope_and_cache,
+ * gather_cache, paged_decode_mx4, mx4_cache_bytes). */
 int32_t i8kv_version(void);
 
 /* The cudaError_t value behind the calling thread's most recent I8KV_ECUDA
@@ -420,6 +423,9 @@ i8kv_status reshape_and_cache(const uint16_t* k_new, const uint16_t* v_new,
 
 /*
  * The MX4 cache -- 4-bit keys and values with a scale for every 16 channels.
+ * (Blocks of 16 with an e4m3 scale under an fp32 outer scale.  Microscaling
+ * data with blocks of 32 and power-of-two scales is another format and is not
+ * taken.)
  *   cache [num_blocks, Hkv, block_size / 16, 18 * D] bytes, 16-byte aligned,
  *   block_size a multiple of 16.  One record of 18 * D bytes holds 16
  *   consecutive tokens of a block for one KV head (one contiguous copy):

@@ -413,7 +413,9 @@ def rope_and_cache(q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v
     caches are int8, float8_e4m3fn (or uint8), or fp16, or k_cache an MX4 cache
     (``mx4_cache_shape``) with v_cache None; an fp16 cache takes no scales.
     Returns the rotated queries [T, Hq, D] (``q_out``, which may be a dense q
-    itself), or None without q."""
+    itself), or None without q.  A token whose position is outside cos_sin is
+    skipped (FLAG_BAD_POSITION unless it is padding): its row of ``q_out`` stays
+    as it was, which in a q_out made here is whatever the memory held."""
     r = (_BINDING or _compiled()).rope_and_cache(
         q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale,
         scale_kind, interleaved, q_out, flags, None if stream is None else _stream(stream))

@@ -235,6 +235,10 @@ i8kv_status plan(const KernelKey& key, int64_t cap, int32_t units, int32_t mode,
 // 14.4, of 1024: 41 against 47), and for any where they number 4/3 waves or more (128 rows of 128 to
 // 8192: 96 us against 100; 160 x 4 groups of 16 heads of 4096: 106 against 127).  Fewer long
 // ones are uneven over the SMs (50 rows x 8 heads of 2048: 40 us, in 8 warps 30).
+// The waves are those of the kernels for scales per tensor, which is all that the plan knows of; the
+// ones for scales per channel hold as many CTAs but for 4 warps and more than 8 heads at
+// head_dim 128 (2 per SM, not 3), so that such groups stay at 8 warps up to 2 waves of theirs (104 rows
+// x 4 groups of 16 heads of 4096, 1.4 waves: 85 us, in 4 warps 98; 140 rows, 1.8: 113 and 100).
 constexpr int64_t kMx4NarrowSpan = 1024;
 i8kv_status mx4_rows(const KernelKey& key, int32_t units, int64_t span, KernelKey* run,
                      int32_t* groups, WaveInfo* w) {

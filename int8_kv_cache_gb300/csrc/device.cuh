@@ -136,11 +136,15 @@ __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
 
-// No kernel here lets its dependents launch early (griddepcontrol.
-// launch_dependents): measured on graphs of decode calls, an early trigger at
-// decode entry made the calls slower, and one at combine entry took the sparse
-// decode (S = 8) from 11.53 to 11.22 us per call but the ragged paged decode
-// from 37.3 to 40.8 us.
+// One kernel lets its dependents launch early (griddepcontrol.
+// launch_dependents): the 4-bit decode, when its loop is done
+// (mx4_kernel.cuh).  So a kernel that is launched with programmatic stream
+// serialization, whichever it is, may start while a 4-bit decode still
+// writes, and calls grid_dependency_wait before its first access to global
+// memory.  In the other kernels a trigger did not pay: measured on graphs of
+// decode calls, one at decode entry made the calls slower, and one at combine
+// entry took the sparse decode (S = 8) from 11.53 to 11.22 us per call but
+// the ragged paged decode from 37.3 to 40.8 us.
 
 __device__ __forceinline__ void flag_or(uint32_t* flags, uint32_t bits) {
   if (flags != nullptr) atomicOr(flags, bits);
