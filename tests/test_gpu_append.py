@@ -383,7 +383,8 @@ def test_other_threads_run_while_a_call_waits_for_the_queue(K):
         th.join()
     if waited < 0.3:
         pytest.skip("the queue took every launch")
-    assert gaps[0] < 0.15
+    # (one call waits for nearly all of it, once the queue is full)
+    assert gaps[0] < waited / 2
 
 
 @pytest.mark.parametrize("kind", ["int8", "e4m3"])
