@@ -551,6 +551,89 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
                              void* stream);
 
 /*
+ * packed_prefill -- causal attention over whole prompts, packed one after
+ * another: what a prompt's own tokens attend before anything of it is cached.
+ * Sequence b's tokens are the rows seq_start[b] .. seq_start[b + 1] - 1; its
+ * token i attends the tokens [max(0, i - window), i] of the same sequence
+ * (window -1: [0, i]), with
+ *     s_t = softmax_scale * dot(Q[i, h], K[t, g]), softcap * tanh(s_t / softcap)
+ *           where softcap > 0;  O and lse as at the top of this file.
+ *   q            [T, Hq, D] fp16, k, v [T, Hkv, D] fp16: the heads of a token
+ *                contiguous, the tokens q_stride / k_stride / v_stride elements
+ *                apart (multiples of 8: the three may be slices of one
+ *                projection's output); strides of a single token are not used
+ *   seq_start    [B + 1] int32, device memory, not falling, in [0, T].  Values
+ *                outside are clamped (I8KV_FLAG_LEN_CLAMPED); rows before the
+ *                first sequence and behind the last stay as they are in out and
+ *                lse; a sequence may be empty
+ *   head_sink, softcap, window  as for paged_decode_ex
+ *   out          [T, Hq, D] fp16, dense;  lse [T, Hq] fp32 or NULL
+ * Work: one kernel on the tensor cores (tcgen05); its grid depends on T, B and
+ * the heads only.  The probabilities are rounded to fp16 (by at most a relative
+ * 2^-11), scores and sums are fp32.  A value that is not finite reaches the rows
+ * that attend it and no others; a query that is not finite makes its row NaN.
+ */
+i8kv_status packed_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                           int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                           const int32_t* seq_start, int32_t T, int32_t B, int32_t Hq, int32_t Hkv,
+                           int32_t D, float softmax_scale, const float* head_sink, float softcap,
+                           int32_t window, uint16_t* out, float* lse, uint32_t* flags,
+                           void* stream);
+
+/*
+ * paged_prefill -- causal attention of chunks of new tokens over a paged cache
+ * that holds them already (rope_and_cache, norm_rope_and_cache,
+ * reshape_and_cache): the next chunk of a prompt, proposed tokens that are
+ * checked at once, single tokens, and batches that mix them.  Sequence b has
+ * n = query_start[b + 1] - query_start[b] new tokens, the last n of its
+ * seq_lens[b] cached ones: token i sits at position p = seq_lens[b] - n + i and
+ * attends [max(0, p - window), p].  A token at a negative position attends
+ * nothing (O = 0, lse = -inf).
+ *   q            [T, Hq, D] fp16, tokens q_stride elements apart (as above)
+ *   caches, cache_dtype, scales, block_table, block_size, max_blocks, num_blocks
+ *                as for paged_decode (I8KV_CACHE_INT8, _FP8, _FP16), or
+ *                I8KV_CACHE_MX4 with k_cache the record cache and v_cache NULL
+ *   seq_lens     [B] int32, device, clamped to cap = max_blocks * block_size
+ *                (I8KV_FLAG_LEN_CLAMPED); query_start [B + 1] as seq_start above
+ *   num_splits   1: unsplit.  2 .. 32: the batch's blocks of 128 positions are cut
+ *                into pieces of equal length, one per SM, and a (token, head)'s
+ *                partials take up to num_splits slots, which the split_combine
+ *                kernel merges.  0: automatic -- splits where the batch's vectors
+ *                alone would leave SMs idle, as many slots as the workspace holds
+ *                (unsplit where it does not hold two)
+ *   workspace, workspace_bytes  paged_prefill_workspace_bytes(..., num_splits) for
+ *                num_splits > 1 (16-byte aligned, else I8KV_EALIGN; too small
+ *                I8KV_EWORKSPACE); may be NULL for 0 and 1.  Nothing in it
+ *                outlives the call
+ *   out, lse, head_sink, softcap, window  as for packed_prefill
+ * A block-table entry of an attended position outside [0, num_blocks) is skipped
+ * (I8KV_FLAG_BAD_BLOCK); entries of positions that nobody attends are not used.
+ * Numerics: the cache's values are exact in the fp16 products, v_scale is applied
+ * to the fp32 sums, a k_scale per tensor to the fp32 scores; a k_scale per
+ * channel is folded into the query, rounded to fp16 with a power of two taken
+ * out (a relative 2^-11 of each term).  Q * k_scale must be finite in fp32.
+ * The rest as for packed_prefill.
+ */
+i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cache,
+                          const void* v_cache, int32_t cache_dtype, const float* k_scale,
+                          const float* v_scale, int32_t scale_kind, const int32_t* block_table,
+                          const int32_t* seq_lens, const int32_t* query_start, int32_t T,
+                          int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t block_size,
+                          int32_t max_blocks, int64_t num_blocks, float softmax_scale,
+                          const float* head_sink, float softcap, int32_t window,
+                          int32_t num_splits, void* workspace, size_t workspace_bytes,
+                          uint16_t* out, float* lse, uint32_t* flags, void* stream);
+
+/*
+ * paged_prefill_workspace_bytes -- bytes of the workspace of paged_prefill for T
+ * new tokens of B sequences with at most cap positions and the given num_splits
+ * (0: what the automatic choice takes on the current device; 0 bytes: it does
+ * not split): T x Hq x splits x (D + 2) x 4.  0 for bad sizes.  Host only.
+ */
+size_t paged_prefill_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int64_t cap, int32_t num_splits);
+
+/*
  * dsa_decode_static_workspace -- dsa_decode without a caller-supplied
  * workspace, for callers that cannot allocate device memory when they call
  * (an engine's enqueue step that must not allocate, code with no access to the

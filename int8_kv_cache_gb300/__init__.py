@@ -23,7 +23,8 @@ __all__ = [
     "dsa_decode_static_workspace", "STATIC_WORKSPACE_BYTES", "reshape_and_cache",
     "FLAG_BAD_SLOT", "FLAG_FP32_PATH", "FLAG_WAIT_TIMEOUT", "paged_decode_ex", "window_span",
     "CACHE_FP8", "fp8_to_fp16", "CACHE_MX4", "mx4_cache_shape", "rope_and_cache", "gather_cache",
-    "paged_decode_mx4", "FLAG_BAD_POSITION",
+    "paged_decode_mx4", "FLAG_BAD_POSITION", "packed_prefill", "paged_prefill",
+    "paged_prefill_workspace_bytes",
     "SCALE_PER_TENSOR", "SCALE_PER_CHANNEL", "CACHE_INT8", "CACHE_FP16", "GEOM_WAVE",
     "GEOM_POW2_TILES", "GEOM_BALANCED", "PATH_DSA", "PATH_PAGED", "MAX_SPLITS", "FLAG_LEN_CLAMPED",
     "FLAG_QUERY_RANGE", "FLAG_BAD_BLOCK",
@@ -105,6 +106,15 @@ _SIGNATURES = {
                                   _c_i32, _c_i32, _c_i32, _c_i32, _c_i64, _c_f32, _c_vp, _c_f32,
                                   _c_i32, _c_i32, _c_i32, _c_vp, _c_sz, _c_vp, _c_vp, _c_vp,
                                   _c_vp]),
+    "packed_prefill": (_c_i32, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i32, _c_i32,
+                                _c_i32, _c_i32, _c_i32, _c_f32, _c_vp, _c_f32, _c_i32, _c_vp, _c_vp,
+                                _c_vp, _c_vp]),
+    "paged_prefill": (_c_i32, [_c_vp, _c_i64, _c_vp, _c_vp, _c_i32, _c_vp, _c_vp, _c_i32, _c_vp,
+                               _c_vp, _c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i32,
+                               _c_i64, _c_f32, _c_vp, _c_f32, _c_i32, _c_i32, _c_vp, _c_sz, _c_vp,
+                               _c_vp, _c_vp, _c_vp]),
+    "paged_prefill_workspace_bytes": (_c_sz, [_c_i32, _c_i32, _c_i32, _c_i32, _c_i32, _c_i64,
+                                              _c_i32]),
     "dsa_decode_static_workspace": (_c_i32, [_c_vp, _c_vp, _c_vp, _c_vp, _c_vp, _c_i32, _c_vp,
                                              _c_i32, _c_i32, _c_i32, _c_i32, _c_i64, _c_i32,
                                              _c_f32, _c_vp, _c_i32, _c_i32, _c_vp, _c_vp, _c_vp,
@@ -449,6 +459,54 @@ def paged_decode_mx4(q, cache, k_scale, v_scale, scale_kind: int, block_table, s
         None if stream is None else _stream(stream), partials_only, softcap, window)
     if type(r) is int:
         _check("paged_decode_mx4", r)
+    return r
+
+
+# --------------------------------------------------------------------------
+# dense causal attention of new tokens
+# --------------------------------------------------------------------------
+
+def packed_prefill(q, k, v, seq_start, softmax_scale: float, head_sink=None, out=None, lse=None,
+                   flags=None, stream=None, softcap: float = 0.0, window: int = -1):
+    """Causal attention over whole prompts packed one after another: q [T, Hq, D],
+    k / v [T, Hkv, D] fp16, which may be slices of one projection's output;
+    sequence b's tokens are the rows seq_start[b] .. seq_start[b + 1] - 1
+    (seq_start [B + 1] int32, on the device).  Returns ``out`` [T, Hq, D]; rows of
+    no sequence stay as they were, which in an out made here is whatever the
+    memory held."""
+    r = (_BINDING or _compiled()).packed_prefill(
+        q, k, v, seq_start, softmax_scale, head_sink, out, lse, flags,
+        None if stream is None else _stream(stream), softcap, window)
+    if type(r) is int:
+        _check("packed_prefill", r)
+    return r
+
+
+def paged_prefill_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int, cap: int,
+                                  num_splits: int = 0) -> int:
+    """Bytes of paged_prefill's workspace for T new tokens of B sequences whose
+    block tables hold cap positions (0: the automatic choice does not split)."""
+    return int(load().paged_prefill_workspace_bytes(T, B, Hq, Hkv, D, cap, num_splits))
+
+
+def paged_prefill(q, k_cache, v_cache, k_scale, v_scale, scale_kind: int, block_table, seq_lens,
+                  query_start, softmax_scale: float, head_sink=None, num_splits: int = 0,
+                  workspace=None, out=None, lse=None, flags=None, stream=None,
+                  softcap: float = 0.0, window: int = -1):
+    """Causal attention of chunks of new tokens over a paged cache that holds them
+    already.  q [T, Hq, D] fp16 (tokens may be apart); caches [num_blocks,
+    block_size, Hkv, D] int8, float8_e4m3fn (or uint8) or fp16, or k_cache an MX4
+    cache with v_cache None; block_table [B, max_blocks], seq_lens [B] (the new
+    tokens included) and query_start [B + 1] int32 on the device: sequence b's new
+    tokens are the rows query_start[b] .. query_start[b + 1] - 1 of q and the last
+    ones of its seq_lens[b].  With a workspace (paged_prefill_workspace_bytes) few
+    tokens over long caches are split over the GPU.  Returns ``out`` [T, Hq, D]."""
+    r = (_BINDING or _compiled()).paged_prefill(
+        q, k_cache, v_cache, k_scale, v_scale, scale_kind, block_table, seq_lens, query_start,
+        softmax_scale, head_sink, num_splits, workspace, out, lse, flags,
+        None if stream is None else _stream(stream), softcap, window)
+    if type(r) is int:
+        _check("paged_prefill", r)
     return r
 
 

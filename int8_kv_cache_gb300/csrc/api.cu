@@ -11,6 +11,7 @@
 #include <tuple>
 
 #include "../../include/int8kv.h"
+#include "attend.h"
 #include "internal.h"
 
 namespace {
@@ -1078,6 +1079,205 @@ i8kv_status gather_cache(const int32_t* slot_mapping, int32_t num_rows, int32_t 
   p.flags = flags;
   cudaError_t e = i8kv::launch_gather_cache(p, cache_dtype, k_out, v_out,
                                             static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
+}
+
+// What packed_prefill and paged_prefill check alike.
+static i8kv_status check_attend(const uint16_t* q, int64_t q_stride, const int32_t* starts,
+                                int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                float softmax_scale, const float* head_sink, float softcap,
+                                int32_t window, const uint16_t* out, const float* lse,
+                                const uint32_t* flags) {
+  if (T < 0 || B < 0) return I8KV_EINVAL;
+  if (!(softcap >= 0.f) || !std::isfinite(softcap) || window < -1) return I8KV_EINVAL;
+  i8kv_status st = check_heads(Hq, Hkv, D);
+  if (st != I8KV_OK) return st;
+  if ((st = check_sigma(softmax_scale)) != I8KV_OK) return st;
+  if (T > 0 && B > 0 && (q == nullptr || out == nullptr || starts == nullptr)) return I8KV_EINVAL;
+  if (T > 1 && q_stride < static_cast<int64_t>(Hq) * D) return I8KV_EINVAL;
+  if (T > 1 && q_stride % 8 != 0) return I8KV_EALIGN;
+  if (!aligned(q, 16) || !aligned(out, 16)) return I8KV_EALIGN;
+  if (!aligned(starts, 4) || !aligned(lse, 4) || !aligned(head_sink, 4) || !aligned(flags, 4))
+    return I8KV_EALIGN;
+  // a sequence's vectors of a KV head, and the CTAs, are numbered in 32 bits
+  if (static_cast<int64_t>(T) * (Hq / Hkv) > INT32_MAX - 512 ||
+      (static_cast<int64_t>(T) * (Hq / Hkv) / 128 + std::min(B, T)) * Hkv > INT32_MAX)
+    return I8KV_EUNSUPPORTED;
+  return I8KV_OK;
+}
+
+static i8kv::AttendParams attend_params(const uint16_t* q, int64_t q_stride, const int32_t* starts,
+                                        int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                        float softmax_scale, const float* head_sink, float softcap,
+                                        int32_t window, uint16_t* out, float* lse,
+                                        uint32_t* flags) {
+  i8kv::AttendParams p{};
+  p.q = reinterpret_cast<const __half*>(q);
+  p.q_stride = q_stride;
+  p.starts = starts;
+  p.T = T;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.G = Hq / Hkv;
+  p.D = D;
+  p.sigma = softmax_scale;
+  p.sink = head_sink;
+  p.softcap = softcap;
+  p.window = window;
+  p.out = reinterpret_cast<__half*>(out);
+  p.lse = lse;
+  p.flags = flags;
+  p.nsplit = 1;
+  return p;
+}
+
+// Two tiles of 128 vectors per CTA where whole CTAs of them fill the GPU and sequences have that
+// many, else one.  Returns the CTAs of an unsplit call.
+static unsigned attend_tiles(const i8kv::AttendParams& p, int sms, bool* two) {
+  const int64_t vec = static_cast<int64_t>(p.T) * p.G;
+  const int32_t seqs = std::min(p.B, p.T);
+  *two = p.D <= 128 && vec / 256 * p.Hkv >= sms && vec / seqs >= 192;
+  return static_cast<unsigned>((vec / (*two ? 256 : 128) + seqs) * p.Hkv);
+}
+
+i8kv_status packed_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                           int64_t k_stride, const uint16_t* v, int64_t v_stride,
+                           const int32_t* seq_start, int32_t T, int32_t B, int32_t Hq, int32_t Hkv,
+                           int32_t D, float softmax_scale, const float* head_sink, float softcap,
+                           int32_t window, uint16_t* out, float* lse, uint32_t* flags,
+                           void* stream) {
+  i8kv_status st = check_attend(q, q_stride, seq_start, T, B, Hq, Hkv, D, softmax_scale, head_sink,
+                                softcap, window, out, lse, flags);
+  if (st != I8KV_OK) return st;
+  const int64_t row = static_cast<int64_t>(Hkv) * D;
+  if (T > 0 && B > 0 && (k == nullptr || v == nullptr)) return I8KV_EINVAL;
+  if (T > 1 && (k_stride < row || v_stride < row)) return I8KV_EINVAL;
+  if (T > 1 && (k_stride % 8 != 0 || v_stride % 8 != 0)) return I8KV_EALIGN;
+  if (!aligned(k, 16) || !aligned(v, 16)) return I8KV_EALIGN;
+  // (a copy's token stride has 40 bits of bytes)
+  if (T > 1 && (k_stride >= INT64_C(1) << 38 || v_stride >= INT64_C(1) << 38)) return I8KV_EUNSUPPORTED;
+  if (T == 0 || B == 0) return I8KV_OK;
+  i8kv::AttendParams p = attend_params(q, q_stride, seq_start, T, B, Hq, Hkv, D, softmax_scale,
+                                       head_sink, softcap, window, out, lse, flags);
+  p.k = k;
+  p.v = v;
+  p.k_stride = T > 1 ? k_stride : row;
+  p.v_stride = T > 1 ? v_stride : row;
+  p.rows = T;
+  int sms = 0;
+  if ((st = sm_count(&sms)) != I8KV_OK) return st;
+  bool two = false;
+  const unsigned ctas = attend_tiles(p, sms, &two);
+  const cudaError_t e = i8kv::launch_attend_f16(p, two, ctas, static_cast<cudaStream_t>(stream));
+  return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
+}
+
+// Slots of partials that paged_prefill takes by itself: 1 where the batch's vectors fill the GPU
+// without splits or its sequences have one block at most.
+static int32_t attend_slots(int32_t T, int32_t B, int32_t G, int32_t Hkv, int64_t cap, int sms) {
+  const int64_t tiles = static_cast<int64_t>(T) * G / 128;
+  if (T < 1 || B < 1 || cap <= 128 || tiles * Hkv >= sms) return 1;
+  const int64_t units = std::max<int64_t>(tiles, std::min(B, T)) * Hkv;
+  return static_cast<int32_t>(std::min<int64_t>(I8KV_MAX_SPLITS, 2 + cdiv(2 * sms, units)));
+}
+
+size_t paged_prefill_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
+                                     int64_t cap, int32_t num_splits) {
+  if (T < 1 || B < 1 || cap < 0 || num_splits < 0 || num_splits > I8KV_MAX_SPLITS ||
+      check_heads(Hq, Hkv, D) != I8KV_OK)
+    return 0;
+  if (num_splits == 0) {
+    int sms = 0;
+    if (sm_count(&sms) != I8KV_OK) return 0;
+    num_splits = attend_slots(T, B, Hq / Hkv, Hkv, cap, sms);
+  }
+  return num_splits > 1 ? static_cast<size_t>(T) * Hq * num_splits * (D + 2) * 4 : 0;
+}
+
+i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cache,
+                          const void* v_cache, int32_t cache_dtype, const float* k_scale,
+                          const float* v_scale, int32_t scale_kind, const int32_t* block_table,
+                          const int32_t* seq_lens, const int32_t* query_start, int32_t T,
+                          int32_t B, int32_t Hq, int32_t Hkv, int32_t D, int32_t block_size,
+                          int32_t max_blocks, int64_t num_blocks, float softmax_scale,
+                          const float* head_sink, float softcap, int32_t window,
+                          int32_t num_splits, void* workspace, size_t workspace_bytes,
+                          uint16_t* out, float* lse, uint32_t* flags, void* stream) {
+  i8kv_status st = check_attend(q, q_stride, query_start, T, B, Hq, Hkv, D, softmax_scale,
+                                head_sink, softcap, window, out, lse, flags);
+  if (st != I8KV_OK) return st;
+  if (max_blocks < 0 || num_blocks < 0 || block_size < 1) return I8KV_EINVAL;
+  if (num_splits < 0 || num_splits > I8KV_MAX_SPLITS) return I8KV_EINVAL;
+  if (cache_dtype < I8KV_CACHE_INT8 || cache_dtype > I8KV_CACHE_MX4) return I8KV_EINVAL;
+  if (block_size % 16 != 0) return I8KV_EUNSUPPORTED;
+  const bool mx4 = cache_dtype == I8KV_CACHE_MX4, fp16c = cache_dtype == I8KV_CACHE_FP16;
+  if (!fp16c && (st = check_scales(k_scale, v_scale, scale_kind)) != I8KV_OK) return st;
+  const bool works = T > 0 && B > 0;
+  if (works && (k_cache == nullptr || (!mx4 && v_cache == nullptr) || seq_lens == nullptr ||
+                (max_blocks > 0 && block_table == nullptr)))
+    return I8KV_EINVAL;
+  if (mx4 && v_cache != nullptr) return I8KV_EINVAL;
+  if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return I8KV_EALIGN;
+  if (!aligned(block_table, 4) || !aligned(seq_lens, 4)) return I8KV_EALIGN;
+  // positions, rows of 16 tokens and the rows of an fp16 cache are 32-bit on the device
+  const int64_t cap = static_cast<int64_t>(max_blocks) * block_size;
+  if (cap > INT32_MAX - 512 || num_blocks > (INT64_C(1) << 31) ||
+      num_blocks * (block_size / 16) > INT32_MAX ||
+      (fp16c && num_blocks * block_size > INT32_MAX))
+    return I8KV_EUNSUPPORTED;
+  if (!aligned(workspace, 16)) return I8KV_EALIGN;
+  int sms = 0;
+  if (works && (st = sm_count(&sms)) != I8KV_OK) return st;
+  const size_t per_slot = static_cast<size_t>(std::max(T, 1)) * Hq * (D + 2) * 4;
+  if (num_splits == 0) {  // as many as the workspace holds
+    num_splits = works ? attend_slots(T, B, Hq / Hkv, Hkv, cap, sms) : 1;
+    const size_t fit = workspace != nullptr ? workspace_bytes / per_slot : 0;
+    if (fit < static_cast<size_t>(num_splits)) num_splits = static_cast<int32_t>(fit);
+    if (num_splits < 2) num_splits = 1;
+  } else if (num_splits > 1 && works &&
+             (workspace == nullptr || workspace_bytes < per_slot * num_splits)) {
+    return I8KV_EWORKSPACE;
+  }
+  if (!works) return I8KV_OK;
+  i8kv::AttendParams p = attend_params(q, q_stride, query_start, T, B, Hq, Hkv, D, softmax_scale,
+                                       head_sink, softcap, window, out, lse, flags);
+  p.k = k_cache;
+  p.v = v_cache;
+  p.k_scale = fp16c ? nullptr : k_scale;
+  p.v_scale = fp16c ? nullptr : v_scale;
+  p.per_channel = !fp16c && scale_kind == I8KV_SCALE_PER_CHANNEL;
+  // (a table without blocks is not read, and a sequence is empty then)
+  p.table = block_table != nullptr ? block_table : seq_lens;
+  p.lens = seq_lens;
+  p.bs = block_size;
+  p.bs_log2 = log2_of(block_size);
+  p.max_blocks = max_blocks;
+  p.cap = static_cast<int32_t>(cap);
+  p.num_blocks = num_blocks;
+  // (a tensor map has a row at least: without blocks it is not read)
+  p.rows = fp16c ? static_cast<int32_t>(std::max<int64_t>(1, num_blocks * block_size)) : 0;
+  p.nsplit = num_splits;
+  bool two = false;
+  unsigned ctas = attend_tiles(p, sms, &two);
+  if (num_splits > 1) {
+    two = false;
+    ctas = static_cast<unsigned>(sms);
+    p.part_acc = static_cast<float*>(workspace);
+    p.part_m = p.part_acc + static_cast<size_t>(T) * Hq * num_splits * D;
+    p.part_l = p.part_m + static_cast<size_t>(T) * Hq * num_splits;
+  }
+  const cudaStream_t s = static_cast<cudaStream_t>(stream);
+  cudaError_t e = cudaErrorInvalidValue;
+  switch (cache_dtype) {
+    case I8KV_CACHE_INT8: e = i8kv::launch_attend_int8(p, two, ctas, s); break;
+    case I8KV_CACHE_FP8: e = i8kv::launch_attend_fp8(p, two, ctas, s); break;
+    case I8KV_CACHE_MX4: e = i8kv::launch_attend_mx4(p, two, ctas, s); break;
+    default: e = i8kv::launch_attend_f16(p, two, ctas, s);
+  }
+  if (e == cudaSuccess && num_splits > 1)
+    e = i8kv::launch_combine(p.part_acc, p.part_m, p.part_l, T * Hkv, num_splits, Hq, Hkv, D,
+                             head_sink, out, lse, s, query_start, B);
   return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
 }
 

@@ -1,0 +1,46 @@
+// Host-side interface of the dense causal attention (attend_kernel.cuh) between
+// the C-ABI layer and its translation units.  Not part of the public ABI.
+#pragma once
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+namespace i8kv {
+
+struct AttendParams {
+  const __half* q;           // [T, Hq, D], tokens q_stride elements apart
+  long long q_stride;
+  const void* k;             // packed: [T, Hkv, D] fp16 rows; paged: the cache (MX4: the record cache)
+  const void* v;
+  long long k_stride, v_stride;  // packed: elements between tokens
+  const float* k_scale;      // of a quantised cache, [1] or [Hkv, D]
+  const float* v_scale;
+  const int32_t* table;      // paged: [B, max_blocks]; nullptr: packed
+  const int32_t* lens;       // paged: [B] lengths, new tokens included; nullptr: the new tokens are all
+  const int32_t* starts;     // [B + 1] first new token of each sequence
+  const float* sink;         // [Hq] or nullptr
+  __half* out;               // [T, Hq, D]
+  float* lse;                // [T, Hq] or nullptr
+  uint32_t* flags;
+  float* part_acc;           // nsplit > 1: [T * Hkv, nsplit, G, D]
+  float* part_m;             // [T * Hkv, nsplit, G]
+  float* part_l;
+  int32_t nsplit;            // slots of partials per (token, KV head); 1: no splits
+  int32_t T, B, Hq, Hkv, G, D;
+  int32_t per_channel;
+  int32_t bs, bs_log2, max_blocks;
+  int32_t cap;               // max_blocks * bs
+  int64_t num_blocks;
+  int32_t rows;              // of an fp16 source: T, or num_blocks * bs
+  float sigma, softcap;
+  int32_t window;
+};
+
+// two_tiles: 256 vectors per CTA (D = 64 or 128, no splits); ctas: the grid.
+cudaError_t launch_attend_f16(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s);
+cudaError_t launch_attend_int8(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s);
+cudaError_t launch_attend_fp8(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s);
+cudaError_t launch_attend_mx4(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s);
+
+}  // namespace i8kv

@@ -1,0 +1,1134 @@
+// Dense causal attention of new tokens on the tensor cores (tcgen05): a packed batch of whole
+// prompts (packed_prefill), or chunks of new tokens over a paged cache (paged_prefill).
+//
+// What it computes, for token i of a sequence's n new ones, at position p = L - n + i of its L
+// tokens, and query head h (KV head g = h / G):
+//   s_t = sigma dot(Q[i, h], K[t, g]), capped to c tanh(s_t / c) where a cap is given,
+//   O[i, h] = sum_t e^(s_t - m) V[t, g] / sum_t e^(s_t - m),  t in [max(0, p - window), p],
+// then lse = m + ln sum and the sink.  A row that attends nothing gives 0 and lse = -inf.
+//
+// Design: a tile is 128 (token, head) vectors of one KV head -- the G heads of a token share its
+// keys and values, so a tile spans 128 / G tokens -- and walks its range of the sequence in blocks
+// of 128 positions with a running maximum and sum:
+//   S[128 x 128] = Q K^T          tcgen05 kind::f16, both operands from shared memory
+//   P = 2^(s - base) as fp16, over the scores' columns in tensor memory
+//   O[128 x D] += P V             tcgen05 kind::f16, P from tensor memory
+// The base of the exponentials follows the running maximum lazily: it moves once the maximum has
+// outgrown it by kLazy powers of two, so O is rescaled on few blocks; P carries 2^kShift, so that
+// probabilities down to 2^-22 of the base keep the 11 bits of fp16 (they are rounded to it once; sums are fp32).
+//
+// Two forms.  TILES = 2 (head_dim 64 and 128): a CTA owns two tiles; while the softmax of one
+// works, the tensor cores work on the other.  One thread per vector.  TILES = 1 (few vectors, and
+// head_dim 256, whose O fills tensor memory): one tile, scores double-buffered, two threads per
+// vector (64 positions each), which exchange their maxima through shared memory.
+//
+// Warp roles (512 threads, registers dealt out anew with setmaxnreg):
+//   warps 0-7    softmax and epilogue
+//   warps 8-11   fp16 sources: look at the V blocks that some row attends in part, where a NaN or
+//                infinity that is masked for a row must not reach it through 0 * NaN: such values
+//                become 0 and are added back to the rows that do attend them in the epilogue.
+//                int8, e4m3fn, MX4: load the codes a block ahead, convert them exactly to fp16
+//   warp 12      lane 0 issues the MMAs; the warp owns the tensor memory
+//   warp 13      fp16 sources: TMA copies (a box of 128 rows of a packed prompt, or of 16 rows of
+//                a page, by 64 channels, 128-byte swizzle); rows out of range are zeros
+// K is K-major, V MN-major, both as 128-byte rows of 64 channels with the 128-byte swizzle.
+//
+// Scales of a quantised cache: v_scale multiplies the finished sums.  k_scale per tensor joins
+// sigma; per channel it is folded into the queries, Q k_scale 2^-e rounded to fp16 (e per vector:
+// the largest entry comes to 2^14, so no range is lost; a score's error is at most
+// 2^-11 sum |q_d k_d|, what a cache of fp16 keys has).
+//
+// Splits (few vectors over long caches): the batch's blocks are cut into equal contiguous pieces,
+// one per CTA, whose ends fall anywhere in a (tile, KV head)'s range; a CTA works its
+// pieces one after another and writes partials that the combine kernel merges.
+//
+// Every wait is bounded; a CTA that gives up marks its outputs NaN and raises
+// I8KV_FLAG_WAIT_TIMEOUT.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <climits>
+
+#include "../../include/int8kv.h"
+#include "attend.h"
+#include "codes.cuh"
+#include "device.cuh"
+#include "tc.cuh"
+
+namespace i8kv {
+namespace ap {
+
+constexpr int BM = 128;  // vectors of a tile (tensor-memory lanes)
+constexpr int BN = 128;  // positions of a block
+constexpr int kSoftThreads = 256;
+constexpr int kProdThreads = 128;
+constexpr int kThreads = 512;
+constexpr int kMmaWarp = 12, kTmaWarp = 13;
+constexpr float kLazy = 7.f;   // powers of two that the maximum may outgrow the base
+constexpr float kShift = 8.f;  // P holds p 2^kShift: at most 2^15
+constexpr int kPoison = 8;     // blocks that a tile's rows can attend in part (6 at most)
+constexpr float kLn2 = 0.6931471805599453f;
+
+// What a K or V value is read from.
+enum Src { kF16 = 0, kI8 = 1, kE4 = 2, kMx4 = 3 };
+
+template <int D, int TILES>
+struct Layout {
+  static constexpr int kM = BM * TILES;
+  static constexpr int kSlabs = D / 64;
+  static constexpr int kSlab = 128 * 128;  // 64 channels of 128 rows
+  static constexpr int kQ = 0;
+  static constexpr int kQBytes = kM * D * 2;
+  static constexpr int kKV = BN * D * 2;
+  static constexpr int kStages = D == 256 ? 1 : D == 128 ? 2 : 3;
+  static constexpr int kK = kQ + kQBytes;
+  static constexpr int kV = kK + kStages * kKV;
+  static constexpr int kBars = kV + kStages * kKV;
+  static constexpr int kSlots = kBars + 256;
+  static constexpr int kPois = kSlots + 64;              // [kPoison][4] bits of positions
+  static constexpr int kRowScale = kPois + kPoison * 16;  // [kM] 2^e of each vector
+  static constexpr int kXchg = kRowScale + kM * 4;        // TILES == 1: [3][2][BM] floats
+  static constexpr int kVote = kXchg + (TILES == 1 ? 6 * BM * 4 : 0);
+  static constexpr int kBytes = kVote + 64;
+  static constexpr int kOCol = 2 * BN;  // O behind the two score buffers
+  static_assert(kOCol + TILES * D <= 512, "tensor memory");
+  static_assert(kBytes <= 227 * 1024, "shared memory");
+};
+
+// barriers (8 bytes each); s: the stage, w: the tile (or, TILES == 1, the score buffer)
+enum Bar { kKFull = 0, kKFree = 4, kVFull = 8, kVFree = 12, kVOk = 16, kSFull = 20, kPFull = 22, kPVDone = 24, kDone = 26, kNumBars = 27 };
+enum Slot { kTmem, kAbort, kBadPage, kAnyPoison, kNumSlots };
+static_assert(kNumBars * 8 <= 256 && kNumSlots * 4 <= 64, "misc");
+
+__device__ __forceinline__ void sync_all() { asm volatile("bar.sync 0, 512;\n" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void regs_up() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_down() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// B operand, MN-major with the 128-byte swizzle: 128-byte rows of 64 channels, one per position,
+// 8 positions per 1024-byte atom (SBO), 64-channel slabs at LBO.
+__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
+  return tc::smem_desc_sw128(saddr, 1024) + ((uint64_t)((lbo >> 4) - 1) << 16);
+}
+
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c, int h, int row,
+                                        uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, "
+      "{%2, %3, %4}], [%5];\n" ::"r"(dst),
+      "l"(map), "r"(c), "r"(h), "r"(row), "r"(bar)
+      : "memory");
+}
+
+__device__ __forceinline__ void sts16(uint32_t a, uint4 v) {
+  asm volatile("st.shared.v4.u32 [%0], {%1,%2,%3,%4};\n" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z),
+               "r"(v.w)
+               : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];\n"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// Zero the non-finite ones of two fp16 values; returns whether there were any.
+__device__ __forceinline__ bool finite_only(uint32_t& x) {
+  const bool lo = (x & 0x7C00u) == 0x7C00u, hi = (x & 0x7C000000u) == 0x7C000000u;
+  if (lo) x &= 0xFFFF0000u;
+  if (hi) x &= 0x0000FFFFu;
+  return lo || hi;
+}
+__device__ __forceinline__ bool finite_only(uint4& v) {
+  const bool a = finite_only(v.x), b = finite_only(v.y), c = finite_only(v.z), d = finite_only(v.w);
+  return a || b || c || d;
+}
+
+// ---------------------------------------------------------------------------
+// the work
+// ---------------------------------------------------------------------------
+
+struct Seq {
+  int s0, n, len;
+};
+__device__ __forceinline__ Seq seq_of(const AttendParams& p, int b, bool report = false) {
+  const int a0 = __ldg(p.starts + b), a1 = __ldg(p.starts + b + 1);
+  Seq s;
+  s.s0 = min(max(a0, 0), p.T);
+  const int s1 = min(max(a1, s.s0), p.T);
+  s.n = s1 - s.s0;
+  bool bad = s.s0 != a0 || s1 != a1;
+  s.len = s.n;
+  if (p.lens != nullptr) {
+    const int l = __ldg(p.lens + b);
+    s.len = min(max(l, 0), p.cap);
+    bad |= s.len != l;
+  }
+  if (report && bad) flag_or(p.flags, I8KV_FLAG_LEN_CLAMPED);
+  return s;
+}
+
+// One piece of a (tile, KV head)'s blocks.
+struct Item {
+  Seq q;
+  int b, t, g;
+  int first, last;  // tokens of the tile
+  int B0, f0, f1;   // its first block; every row attends all of the blocks [f0, f1)
+  int blk0, blk1;   // the piece
+  int slot;         // of the partials
+  bool ends;        // the piece is the last of its tile's
+  __device__ __forceinline__ bool partial(int blk) const { return blk < f0 || blk >= f1; }
+  __device__ __forceinline__ int ordinal(int blk) const {
+    return min(blk < f0 ? blk - B0 : f0 - B0 + blk - f1, kPoison - 1);
+  }
+};
+
+template <int M>
+__device__ __forceinline__ int tiles_of(const AttendParams& p, int n) {
+  return (n * p.G + M - 1) / M;
+}
+
+// Blocks that stand for each of a sequence's tiles when its pieces are cut: those of its last
+// tile, or, under a window, what a tile can touch.
+template <int M>
+__device__ __forceinline__ int weight_of(const AttendParams& p, const Seq& s) {
+  const int all = (s.len + BN - 1) / BN;
+  if (p.window < 0) return max(all, 1);
+  const long long w = ((long long)p.window + M / p.G + 1) / BN + 2;
+  return max((int)(w < all ? w : all), 1);
+}
+
+// Blocks [x, y) of the tile's range.
+template <int M>
+__device__ __forceinline__ void place(const AttendParams& p, Item& it, int x, int y) {
+  const int v0 = it.t * M, v1 = min(it.q.n * p.G, v0 + M);
+  it.first = v0 / p.G;
+  it.last = (v1 - 1) / p.G;
+  const int p0 = it.q.len - it.q.n + it.first, p1 = it.q.len - it.q.n + it.last;
+  const int hi_min = max(p0 + 1, 0), hi = max(p1 + 1, 0);
+  const int lo = p.window < 0 ? 0 : max(p0 - p.window, 0);
+  const int lo_max = p.window < 0 ? 0 : max(p1 - p.window, 0);
+  it.B0 = lo / BN;
+  const int B1 = (hi + BN - 1) / BN;
+  it.f0 = max(it.B0, (lo_max + BN - 1) / BN);
+  it.f1 = max(it.f0, hi_min / BN);
+  it.blk0 = min(it.B0 + x, max(B1, it.B0));
+  it.blk1 = max(it.blk0, min(B1, it.B0 + y));
+}
+
+// The walk over this CTA's items.
+struct Walk {
+  long long f, end, per, base;  // flat blocks; base: of sequence b's first
+  int wt, tiles;
+};
+
+// Finds the CTA's first item (every warp for itself); false: there is none.
+template <int M>
+__device__ __forceinline__ bool first_item(const AttendParams& p, Item& it, Walk& w) {
+  const int lane = threadIdx.x & 31;
+  auto scan = [&](long long x) -> long long {
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
+    }
+    return x;
+  };
+  long long at = 0;
+  if (p.nsplit > 1) {
+    long long total = 0;
+    int most = 1;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      if (b0 + lane < p.B) {
+        const Seq s = seq_of(p, b0 + lane);
+        const int wt = weight_of<M>(p, s);
+        total += (long long)tiles_of<M>(p, s.n) * p.Hkv * wt;
+        if (s.n > 0) most = max(most, wt);
+      }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+      total += __shfl_xor_sync(0xffffffffu, total, o);
+      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    }
+    // pieces of equal length; a tile's cuts must not need more than nsplit slots
+    w.per = max((total + gridDim.x - 1) / gridDim.x, (long long)(most + p.nsplit - 2) / (p.nsplit - 1));
+    w.f = w.per * blockIdx.x;
+    w.end = min(w.f + w.per, total);
+    at = w.f;
+    if (w.f >= w.end) return false;
+  } else {
+    at = blockIdx.x / p.Hkv;
+  }
+  long long before = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32) {
+    Seq s{0, 0, 0};
+    long long x = 0;
+    int tiles = 0, wt = 1;
+    if (b0 + lane < p.B) {
+      s = seq_of(p, b0 + lane);
+      tiles = tiles_of<M>(p, s.n);
+      wt = weight_of<M>(p, s);
+      x = p.nsplit > 1 ? (long long)tiles * p.Hkv * wt : tiles;
+    }
+    const long long incl = before + scan(x);
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > at);
+    if (hit != 0) {
+      const int l = __ffs(hit) - 1;
+      it.b = b0 + l;
+      it.q.s0 = __shfl_sync(0xffffffffu, s.s0, l);
+      it.q.n = __shfl_sync(0xffffffffu, s.n, l);
+      it.q.len = __shfl_sync(0xffffffffu, s.len, l);
+      w.tiles = __shfl_sync(0xffffffffu, tiles, l);
+      w.wt = __shfl_sync(0xffffffffu, wt, l);
+      w.base = __shfl_sync(0xffffffffu, incl - x, l);
+      return true;
+    }
+    before = __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return false;
+}
+
+// The item at the walk's place; advances it.
+template <int M>
+__device__ __forceinline__ bool next_item(const AttendParams& p, Item& it, Walk& w) {
+  if (p.nsplit <= 1) {
+    if (w.tiles == 0) return false;
+    it.g = blockIdx.x % p.Hkv;
+    // a sequence's last tiles, the longest ones, first
+    it.t = w.tiles - 1 - (int)(blockIdx.x / p.Hkv - w.base);
+    it.slot = 0;
+    it.ends = true;
+    place<M>(p, it, 0, INT_MAX / 2);
+    w.tiles = 0;  // one item
+    return true;
+  }
+  while (w.f < w.end) {
+    const long long in_seq = w.f - w.base;
+    const int unit = (int)(in_seq / w.wt);
+    if (unit >= w.tiles * p.Hkv) {  // the next sequence
+      w.base += (long long)w.tiles * p.Hkv * w.wt;
+      if (++it.b >= p.B) return false;
+      it.q = seq_of(p, it.b);
+      w.tiles = tiles_of<M>(p, it.q.n);
+      w.wt = weight_of<M>(p, it.q);
+      continue;
+    }
+    const int x = (int)(in_seq - (long long)unit * w.wt);
+    const int y = (int)min((long long)w.wt, x + (w.end - w.f));
+    it.t = unit / p.Hkv;
+    it.g = unit - it.t * p.Hkv;
+    it.slot = (int)(blockIdx.x - (w.base + (long long)unit * w.wt) / w.per);
+    it.ends = y == w.wt;
+    place<M>(p, it, x, y);
+    w.f += y - x;
+    return true;
+  }
+  return false;
+}
+
+// The 16-row group that holds position pos of sequence b, as a row number / 16 of the cache; -1
+// where the position is not attended by any (past the end) or its page is out of range.
+__device__ __forceinline__ int group_of(const AttendParams& p, const Item& it, int pos) {
+  if (pos >= it.q.len) return -1;
+  const int page = p.bs_log2 >= 0 ? pos >> p.bs_log2 : pos / p.bs;
+  const int off = pos - page * p.bs;
+  const int blk = __ldg(p.table + (long long)it.b * p.max_blocks + page);
+  if (blk < 0 || blk >= p.num_blocks) return -1;
+  return (int)((long long)blk * (p.bs >> 4)) + (off >> 4);
+}
+
+// V[t, g, d] as stored (without v_scale), for the values that are added back.
+template <int D, int SRC>
+__device__ __noinline__ float v_value(const AttendParams& p, const Item& it, int t, int d) {
+  if (p.table == nullptr)
+    return __half2float(reinterpret_cast<const __half*>(p.v)[(it.q.s0 + (long long)t) * p.v_stride +
+                                                             (long long)it.g * D + d]);
+  const int grp = group_of(p, it, t);
+  if (grp < 0) return 0.f;
+  const long long row = (long long)grp * 16 + (t & 15);
+  if constexpr (SRC == kF16) {
+    return __half2float(reinterpret_cast<const __half*>(p.v)[(row * p.Hkv + it.g) * D + d]);
+  } else if constexpr (SRC == kE4) {
+    return e4m3_value(reinterpret_cast<const uint8_t*>(p.v)[(row * p.Hkv + it.g) * D + d]);
+  } else if constexpr (SRC == kMx4) {
+    // (only the block scale can be no number)
+    const int tiles = p.bs >> 4;
+    const uint8_t* rec = reinterpret_cast<const uint8_t*>(p.k) +
+                         ((long long)(grp / tiles) * p.Hkv * tiles + (long long)it.g * tiles + grp % tiles) * (18LL * D);
+    return e4m3_value(rec[17 * D + (t & 15) * (D / 16) + (d >> 4)]);
+  }
+  return 0.f;
+}
+
+// Adds the non-finite values of the attended positions that were taken out of V to channels d0 .. d1 - 1 of a
+// row that its thread has written: fp16 outputs, or fp32 partials.
+template <int D, int SRC, typename T>
+__device__ __noinline__ void add_poison(const AttendParams& p, const Item& it, const uint32_t* bits,
+                                        int lo, int hi, int d0, int d1, T* o) {
+  for (int blk = it.blk0; blk < it.blk1; ++blk) {
+    if (!it.partial(blk)) continue;
+    const uint32_t* w = bits + 4 * it.ordinal(blk);
+    for (int j = 0; j < BN; ++j) {
+      const int t = blk * BN + j;
+      if (!((w[j >> 5] >> (j & 31)) & 1u) || t < lo || t >= hi) continue;
+      for (int d = d0; d < d1; ++d) {
+        const float x = v_value<D, SRC>(p, it, t, d);
+        if (fabsf(x) <= 65504.f) continue;
+        const float vs = SRC == kF16 ? 1.f : __ldg(p.v_scale + (p.per_channel ? it.g * D + d : 0));
+        o[d] = (T)((float)o[d] + x * vs);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// producers of a quantised cache
+// ---------------------------------------------------------------------------
+
+// Raw codes of one block of K or V, as thread ct of the producers holds them: pieces of 16 bytes,
+// piece k of row (ct + 128 k) / kPer.
+template <int D, int SRC>
+struct Raw {
+  static constexpr int kVals = SRC == kMx4 ? 32 : 16;  // values of a piece
+  static constexpr int kPer = D / kVals;               // pieces of a row
+  static constexpr int kN = BN * kPer / kProdThreads;  // pieces of a thread
+  uint4 x[kN];
+  uint16_t s[SRC == kMx4 ? kN : 1];  // MX4: the two block scales
+};
+
+template <int D, int SRC>
+__device__ __forceinline__ void load_raw(const AttendParams& p, int g, int groups, bool is_v,
+                                         Raw<D, SRC>& r) {
+  using R = Raw<D, SRC>;
+  const int ct = threadIdx.x - kSoftThreads;
+#pragma unroll
+  for (int k = 0; k < R::kN; ++k) {
+    const int q = ct + kProdThreads * k;
+    const int row = q / R::kPer, c = q % R::kPer;
+    const int grp = __shfl_sync(0xffffffffu, groups, row >> 4);
+    r.x[k] = make_uint4(0u, 0u, 0u, 0u);
+    if constexpr (SRC == kMx4) r.s[k] = 0;
+    if (grp >= 0) {
+    if constexpr (SRC == kMx4) {
+      const int tiles = p.bs >> 4;
+      const int blk = p.bs_log2 >= 0 ? grp >> (p.bs_log2 - 4) : grp / tiles;
+      const uint8_t* rec = reinterpret_cast<const uint8_t*>(p.k) +
+                           (((long long)blk * p.Hkv + g) * tiles + (grp - blk * tiles)) * (18LL * D) +
+                           (is_v ? 9 * D : 0);
+      r.x[k] = __ldg(reinterpret_cast<const uint4*>(rec + (row & 15) * (D / 2)) + c);
+      r.s[k] = __ldg(reinterpret_cast<const uint16_t*>(rec + 8 * D + (row & 15) * (D / 16)) + c);
+    } else {
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(is_v ? p.v : p.k) +
+                           (((long long)grp * 16 + (row & 15)) * p.Hkv + g) * D;
+      r.x[k] = __ldg(reinterpret_cast<const uint4*>(src) + c);
+    }
+    }
+  }
+}
+
+// Into a stage, as fp16.  bits: where V's rows with a NaN are noted (nullptr: not looked at).
+template <int D, int SRC>
+__device__ __forceinline__ void store_raw(const Raw<D, SRC>& r, uint32_t dst, uint32_t* bits,
+                                          volatile int* any) {
+  using R = Raw<D, SRC>;
+  const int ct = threadIdx.x - kSoftThreads;
+#pragma unroll
+  for (int k = 0; k < R::kN; ++k) {
+    const int q = ct + kProdThreads * k;
+    const int row = q / R::kPer, c = q % R::kPer;
+    constexpr int kChunks = R::kVals / 8;
+    uint4 h[kChunks];
+    if constexpr (SRC == kI8) {
+      const uint32_t x0 = flip_i8x4(r.x[k].x), x1 = flip_i8x4(r.x[k].y);
+      const uint32_t x2 = flip_i8x4(r.x[k].z), x3 = flip_i8x4(r.x[k].w);
+      h[0] = make_uint4(i8x2_to_h2(x0, 0x4140u), i8x2_to_h2(x0, 0x4342u), i8x2_to_h2(x1, 0x4140u),
+                        i8x2_to_h2(x1, 0x4342u));
+      h[1] = make_uint4(i8x2_to_h2(x2, 0x4140u), i8x2_to_h2(x2, 0x4342u), i8x2_to_h2(x3, 0x4140u),
+                        i8x2_to_h2(x3, 0x4342u));
+    } else if constexpr (SRC == kE4) {
+      e4m3x4_to_h2x2(r.x[k].x, h[0].x, h[0].y);
+      e4m3x4_to_h2x2(r.x[k].y, h[0].z, h[0].w);
+      e4m3x4_to_h2x2(r.x[k].z, h[1].x, h[1].y);
+      e4m3x4_to_h2x2(r.x[k].w, h[1].z, h[1].w);
+    } else {
+      uint32_t s0, s1;  // the block scales, twice each
+      e4m3x4_to_h2x2(prmt(r.s[k], 0u, 0x1100u), s0, s1);
+      e2m1x8_to_h2x4(r.x[k].x, h[0].x, h[0].y, h[0].z, h[0].w);
+      e2m1x8_to_h2x4(r.x[k].y, h[1].x, h[1].y, h[1].z, h[1].w);
+      e2m1x8_to_h2x4(r.x[k].z, h[2].x, h[2].y, h[2].z, h[2].w);
+      e2m1x8_to_h2x4(r.x[k].w, h[3].x, h[3].y, h[3].z, h[3].w);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const uint32_t s = j < 2 ? s0 : s1;
+        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].x) : "r"(s));  // exact: 6 significant bits
+        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].y) : "r"(s));
+        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].z) : "r"(s));
+        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].w) : "r"(s));
+      }
+    }
+    if (SRC != kI8 && bits != nullptr) {
+      bool bad = false;
+#pragma unroll
+      for (int j = 0; j < kChunks; ++j) bad |= finite_only(h[j]);
+      if (bad) {
+        atomicOr(bits + (row >> 5), 1u << (row & 31));
+        *any = 1;
+      }
+    }
+    // chunk j of the row; the lanes of one row in turn from both ends of their pieces, so that the
+    // slabs' rows, which share banks, do not meet
+#pragma unroll
+    for (int j = 0; j < kChunks; ++j) {
+      const int ch = c * kChunks + j;
+      const uint32_t at = dst + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
+      sts16(at, h[j]);
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// the kernel
+// ---------------------------------------------------------------------------
+
+struct Args {
+  CUtensorMap km, vm;  // fp16 sources: [rows, Hkv, D], box 128 (packed) or 16 (pages) x 1 x 64
+  AttendParams p;
+};
+
+template <int D, int TILES, int SRC>
+__global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Args a) {
+  using L = Layout<D, TILES>;
+  constexpr int M = L::kM, S = L::kStages;
+  const AttendParams& p = a.p;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t sbase = smem_addr(smem);
+  auto bar = [&](int k) -> uint32_t { return sbase + L::kBars + 8 * k; };
+  volatile int* slot = reinterpret_cast<volatile int*>(smem + L::kSlots);
+  uint32_t* poison = reinterpret_cast<uint32_t*>(smem + L::kPois);
+  float* rscale = reinterpret_cast<float*>(smem + L::kRowScale);
+
+  grid_dependency_wait();  // inputs may come from the previous kernel of the stream
+  Item it;
+  Walk walk;
+  if (!first_item<M>(p, it, walk)) return;
+
+  if (warp == kMmaWarp) {
+    tc::tmem_alloc(sbase + L::kSlots + 4 * kTmem, 512);
+    tc::tmem_relinquish();
+  }
+  if (tid == 0) {
+    for (int s = 0; s < S; ++s) {
+      tc::mbar_init(bar(kKFull + s), SRC == kF16 ? 1 : kProdThreads);
+      tc::mbar_init(bar(kKFree + s), 1);
+      tc::mbar_init(bar(kVFull + s), 1);
+      tc::mbar_init(bar(kVFree + s), 1);
+      tc::mbar_init(bar(kVOk + s), kProdThreads);
+    }
+    for (int w = 0; w < 2; ++w) {
+      tc::mbar_init(bar(kSFull + w), 1);
+      tc::mbar_init(bar(kPFull + w), TILES == 2 ? kSoftThreads / 2 : kSoftThreads);
+      tc::mbar_init(bar(kPVDone + w), 1);
+    }
+    tc::mbar_init(bar(kDone), 1);
+    tc::fence_mbar_init();
+    slot[kAbort] = (sbase & 1023u) != 0u;  // the swizzled layouts want 1024-byte alignment
+    slot[kBadPage] = 0;
+    slot[kAnyPoison] = 0;
+  }
+  if (tid < kPoison * 4) poison[tid] = 0u;
+  tc::fence_before_sync();
+  sync_all();
+  tc::fence_after_sync();
+  const uint32_t tbase = static_cast<uint32_t>(slot[kTmem]);
+
+  if (warp < kSoftThreads / 32) {
+    // -----------------------------------------------------------------------
+    // softmax and epilogue
+    // -----------------------------------------------------------------------
+    regs_up<TILES == 2 ? 184 : 144>();
+    constexpr int COLS = TILES == 2 ? 128 : 64;  // positions of a block per thread
+    const int half = TILES == 2 ? 0 : warp >> 2;
+    const int tile = TILES == 2 ? warp >> 2 : 0;
+    const int r = 32 * (warp & 3) + lane;  // the vector within its tile
+    const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
+    float* xchg = reinterpret_cast<float*>(smem + L::kXchg);
+    volatile int* votes = reinterpret_cast<volatile int*>(smem + L::kVote);
+    auto pair_sync = [&]() {
+      asm volatile("bar.sync %0, %1;\n" ::"r"(1 + (warp & 3)), "r"(64) : "memory");
+    };
+    auto wait_all = [&](int b, uint32_t parity) -> bool {
+      return __all_sync(0xffffffffu, tc::mbar_wait(bar(b), parity, slot + kAbort));
+    };
+    // TILES == 1: the two warps of a lane quarter take the same branch after every wait
+    int nvote = 0;
+    auto agree = [&](bool ok) -> bool {
+      if constexpr (TILES == 2) {
+        return ok;
+      } else {
+        volatile int* v = votes + (nvote++ & 1) * 8 + (warp & 3) * 2;
+        if (lane == 0) v[half] = ok ? 1 : 0;
+        pair_sync();
+        return v[0] != 0 && v[1] != 0;
+      }
+    };
+    const float cap_k = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
+    const bool folds = SRC != kF16 && p.per_channel;
+    const float ks1 = SRC != kF16 && !p.per_channel ? __ldg(p.k_scale) : 1.f;
+    int n = 0;  // blocks done by this CTA
+    while (next_item<M>(p, it, walk)) {
+      const int v0 = it.t * M, nvec = it.q.n * p.G;
+      // ---- queries into shared memory ----
+      {
+        constexpr int CPR = D / 8;  // 16-byte chunks of a vector
+#pragma unroll 4
+        for (int k = 0; k < M * CPR / kSoftThreads; ++k) {
+          const int idx = tid + kSoftThreads * k;
+          const int row = idx / CPR, c = idx % CPR;
+          const int v = v0 + row;
+          uint4 x = make_uint4(0u, 0u, 0u, 0u);
+          if (v < nvec) {
+            const int tok = v / p.G, j = v - tok * p.G;
+            x = __ldg(reinterpret_cast<const uint4*>(p.q + (it.q.s0 + (long long)tok) * p.q_stride +
+                                                     (long long)(it.g * p.G + j) * D) + c);
+          }
+          // a query that is not finite makes its row NaN whatever its scores come to
+          uint4 y = x;
+          const unsigned odd = __ballot_sync(0xffffffffu, finite_only(y));
+          const unsigned of_row = (CPR == 32 ? 0xffffffffu : ((1u << (CPR & 31)) - 1u) << (lane & ~(CPR - 1)));
+          float rsc = 1.f;
+          if (SRC != kF16) {
+            if (folds) {
+              const float4 k0 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * c));
+              const float4 k1 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * c) + 1);
+              const __half2* h = reinterpret_cast<const __half2*>(&x);
+              float f[8];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 y = __half22float2(h[e]);
+                f[2 * e] = y.x;
+                f[2 * e + 1] = y.y;
+              }
+              f[0] *= k0.x, f[1] *= k0.y, f[2] *= k0.z, f[3] *= k0.w;
+              f[4] *= k1.x, f[5] *= k1.y, f[6] *= k1.z, f[7] *= k1.w;
+              float top = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+              for (int o = CPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+              // 2^e brings the largest entry into [2^14, 2^15): exponent fields, exact
+              const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
+              const int e = ex == 0 || ex == 255 ? 0 : min(max(ex - 127 - 14, -126), 126);
+              const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) f[i] *= down;
+              x = make_uint4(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]), pack_h2(f[4], f[5]), pack_h2(f[6], f[7]));
+              rsc = __uint_as_float((uint32_t)(127 + e) << 23);
+            } else if (ks1 < 0.f) {
+              x = make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u);
+            }
+          }
+          if (c == 0) rscale[row] = odd & of_row ? __int_as_float(0x7fc00000) : rsc;
+          sts16(sbase + L::kQ + ((row >> 7) * L::kSlabs + (c >> 3)) * L::kSlab + (row & 127) * 128 +
+                    (((c & 7) ^ (row & 7)) << 4),
+                x);
+        }
+        // pages out of range among those attended (their tokens are skipped)
+        if (p.table != nullptr) {
+          const int lo = p.window < 0 ? 0 : max(it.q.len - it.q.n + it.first - p.window, 0);
+          const int hi = min(it.blk1 * BN, it.q.len - it.q.n + it.last + 1);
+          const int step = min(p.bs, BN);
+          bool bad = false;
+          for (int t = max(it.blk0 * BN, lo) + step * tid; t < hi; t += step * kSoftThreads)
+            bad |= group_of(p, it, t) < 0;
+          if (tid == 0 && hi > max(it.blk0 * BN, lo)) bad |= group_of(p, it, hi - 1) < 0;
+          if (bad) {
+            slot[kBadPage] = 1;
+            flag_or(p.flags, I8KV_FLAG_BAD_BLOCK);
+          }
+        }
+        tc::fence_smem_to_async();
+      }
+      sync_all();  // queries staged
+      const int v = v0 + tile * BM + r;
+      const bool live = v < nvec;
+      const int tok = live ? v / p.G : 0;
+      const int h = it.g * p.G + (live ? v - tok * p.G : 0);
+      const int pos = it.q.len - it.q.n + tok;
+      const int hi = live ? max(pos + 1, 0) : 0;
+      const int lo = p.window < 0 ? 0 : max(pos - p.window, 0);
+      const bool bad_pages = slot[kBadPage] != 0;
+      // scores to powers of two: s c2 (c2 > 0 keeps an unattended -inf what it is)
+      const float rs = rscale[tile * BM + r] * fabsf(ks1);
+      const float nat = p.sigma * rs;
+      float c2 = p.softcap > 0.f ? kLog2e : nat * kLog2e;
+      if (c2 < 1e-30f) c2 = 1e-30f;
+      // (a second tile without vectors is not worked on; with two tiles there is one item)
+      const int nb = v0 + tile * BM < nvec ? it.blk1 - it.blk0 : 0;
+      const bool warp_live = __any_sync(0xffffffffu, live && hi > lo);
+      float m_run = neg_inf(), m_top = neg_inf(), l_run = 0.f;
+      bool ok = true;
+      for (int i = 0; i < nb; ++i) {
+        const int blk = it.blk0 + i, nn = n + i;
+        const int sb = TILES == 2 ? tile : nn & 1;
+        const uint32_t par = TILES == 2 ? nn & 1 : (nn >> 1) & 1;
+        if (!(ok = agree(wait_all(kSFull + sb, par)))) break;
+        tc::fence_after_sync();
+        if (warp_live) {
+          const uint32_t s_col = tbase + t_lane + sb * BN + 64 * half;
+          float s[COLS];
+#pragma unroll
+          for (int c = 0; c < COLS / 32; ++c) tc::tmem_ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
+          tc::tmem_wait_ld();
+          if (p.softcap > 0.f) {
+#pragma unroll
+            for (int j = 0; j < COLS; ++j) s[j] = soft_cap(s[j] * nat, p.softcap, cap_k);
+          }
+          if (it.partial(blk) || bad_pages) {
+            const int at = blk * BN + 64 * half;
+#pragma unroll
+            for (int c = 0; c < COLS / 32; ++c) {
+              // positions [lo, hi) of these 32
+              const int a0 = min(max(lo - (at + 32 * c), 0), 32), a1 = min(max(hi - (at + 32 * c), 0), 32);
+              uint32_t w = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
+              if (bad_pages) {
+                if (group_of(p, it, at + 32 * c) < 0) w &= 0xffff0000u;
+                if (group_of(p, it, at + 32 * c + 16) < 0) w &= 0x0000ffffu;
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[32 * c + j] = (w >> j) & 1u ? s[32 * c + j] : neg_inf();
+            }
+          }
+          float mx4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+#pragma unroll
+          for (int j = 0; j < COLS; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          if constexpr (TILES == 1) {
+            float* xb = xchg + (nn & 1) * 2 * BM;
+            xb[half * BM + r] = mx;
+            pair_sync();
+            mx = fmaxf(mx, xb[(half ^ 1) * BM + r]);
+          }
+          m_top = fmaxf(m_top, mx);
+          const bool moves = m_top * c2 > m_run * c2 + kLazy;  // (from -inf: any score does)
+          const float m_new = moves ? m_top : m_run;
+          const float base = m_new == neg_inf() ? 0.f : m_new * c2;
+          const float alpha = moves ? fast_exp2(m_run * c2 - base) : 1.f;
+          const float off = kShift - base;
+          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int c = 0; c < COLS / 64; ++c) {
+            uint32_t ph[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              const float p0 = fast_exp2(fmaf(s[64 * c + 2 * j], c2, off));
+              const float p1 = fast_exp2(fmaf(s[64 * c + 2 * j + 1], c2, off));
+              ps[(2 * j) & 3] += p0;
+              ps[(2 * j + 1) & 3] += p1;
+              ph[j] = pack_h2(p0, p1);
+            }
+            tc::tmem_st32u(s_col + 64 * c, ph);
+          }
+          l_run = fmaf(l_run, alpha, (ps[0] + ps[1]) + (ps[2] + ps[3]));
+          const bool rescale = i > 0 && moves;
+          m_run = m_new;
+          // O is current: with two tiles QK(i) was issued after PV(i - 1) had completed
+          if constexpr (TILES == 1) {
+            if (!(ok = agree(i == 0 || wait_all(kPVDone, (nn - 1) & 1)))) break;
+            tc::fence_after_sync();
+          }
+          if (__any_sync(0xffffffffu, rescale)) {
+            constexpr int OC = TILES == 2 ? D : D / 2;  // channels of this thread
+#pragma unroll 1
+            for (int c = 0; c < OC / 32; ++c) {
+              float o[32];
+              const uint32_t oc = tbase + t_lane + L::kOCol + tile * D + half * OC + 32 * c;
+              tc::tmem_ld32(oc, o);
+              tc::tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] *= rescale ? alpha : 1.f;
+              tc::tmem_st32(oc, o);
+            }
+          }
+          tc::tmem_wait_st();
+          tc::fence_before_sync();
+        } else if constexpr (TILES == 1) {
+          if (!(ok = agree(i == 0 || wait_all(kPVDone, (nn - 1) & 1)))) break;
+        }
+        tc::mbar_arrive(bar(kPFull + tile));
+      }
+      n += nb;
+      // ---- epilogue ----
+      const int pv = TILES == 2 ? kPVDone + tile : kPVDone;
+      const bool done = ok && slot[kAbort] == 0;
+      ok = agree(__all_sync(0xffffffffu, done) && (nb == 0 || wait_all(pv, (n - 1) & 1)));
+      tc::fence_after_sync();
+      if constexpr (TILES == 1) {
+        float* lx = xchg + 4 * BM;
+        lx[half * BM + r] = l_run;
+        pair_sync();
+        l_run += lx[(half ^ 1) * BM + r];
+      }
+      const bool attends = live && max(lo, it.blk0 * BN) < min(hi, it.blk1 * BN);
+      const bool some = attends && m_top != neg_inf();
+      const bool nan = attends && l_run != l_run;
+      const float lsum = l_run * 0.00390625f;  // 2^-kShift
+      const float m_nat = m_run * c2 * kLn2;
+      constexpr int OC = TILES == 2 ? D : D / 2;
+      const int c_lo = half * OC;
+      const float kNan = __int_as_float(0x7fc00000);
+      const bool fix = slot[kAnyPoison] != 0;
+      if (p.nsplit > 1) {
+        const long long u = ((it.q.s0 + (long long)tok) * p.Hkv + it.g) * p.nsplit + it.slot;
+        const long long pvec = u * p.G + (h - it.g * p.G);
+        float* acc = p.part_acc + pvec * D;
+#pragma unroll 1
+        for (int c = 0; c < OC / 32; ++c) {
+          if (!ok || nb == 0 || !warp_live) break;
+          float o[32];
+          tc::tmem_ld32(tbase + t_lane + L::kOCol + tile * D + c_lo + 32 * c, o);
+          tc::tmem_wait_ld();
+          if (!some && !nan) continue;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int d = c_lo + 32 * c + 4 * e;
+            float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (SRC != kF16) {
+              if (p.per_channel) vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + it.g * D + d));
+              else vs.x = vs.y = vs.z = vs.w = __ldg(p.v_scale);
+            }
+            const float f = 0.00390625f;
+            *reinterpret_cast<float4*>(acc + d) = make_float4(o[4 * e] * f * vs.x, o[4 * e + 1] * f * vs.y,
+                                                              o[4 * e + 2] * f * vs.z, o[4 * e + 3] * f * vs.w);
+          }
+        }
+        if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, poison, lo, hi, c_lo, c_lo + OC, acc);
+        if (live && half == 0) {
+          // a CTA that gave up, and a sum that is no number, make the merged row NaN
+          p.part_m[pvec] = !ok || nan ? __int_as_float(0x7f800000) : some ? m_nat : neg_inf();
+          p.part_l[pvec] = !ok || nan ? kNan : some ? lsum : 0.f;
+          if (it.ends)
+            for (int k = it.slot + 1; k < p.nsplit; ++k) {
+              p.part_m[pvec + (long long)(k - it.slot) * p.G] = neg_inf();
+              p.part_l[pvec + (long long)(k - it.slot) * p.G] = 0.f;
+            }
+        }
+      } else {
+        float sc = 0.f, lse = neg_inf();
+        if (!ok || nan) {
+          sc = lse = kNan;
+        } else if (some) {
+          lse = m_nat + logf(lsum);
+          sc = 0.00390625f / lsum;
+          if (p.sink != nullptr) sc *= 1.f / (1.f + expf(__ldg(p.sink + h) - lse));
+        }
+        __half* out = p.out + ((it.q.s0 + (long long)tok) * p.Hq + h) * D;
+#pragma unroll 1
+        for (int c = 0; c < OC / 32; ++c) {
+          float o[32];
+          if (ok && nb > 0) {
+            tc::tmem_ld32(tbase + t_lane + L::kOCol + tile * D + c_lo + 32 * c, o);
+            tc::tmem_wait_ld();
+          }
+          if (!live) continue;
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int d = c_lo + 32 * c + 4 * e;
+            float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
+            if (SRC != kF16) {
+              if (p.per_channel) vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + it.g * D + d));
+              else vs.x = vs.y = vs.z = vs.w = __ldg(p.v_scale);
+            }
+            const bool z = sc == 0.f;  // nothing attended: the accumulator may hold anything
+            w[2 * e] = z ? 0u : sc != sc ? 0x7e007e00u : pack_h2(o[4 * e] * sc * vs.x, o[4 * e + 1] * sc * vs.y);
+            w[2 * e + 1] = z ? 0u : sc != sc ? 0x7e007e00u : pack_h2(o[4 * e + 2] * sc * vs.z, o[4 * e + 3] * sc * vs.w);
+          }
+          uint4* dst = reinterpret_cast<uint4*>(out + c_lo + 32 * c);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+        }
+        if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, poison, lo, hi, c_lo, c_lo + OC, out);
+        if (live && half == 0 && p.lse != nullptr)
+          p.lse[(it.q.s0 + (long long)tok) * p.Hq + h] = lse;
+      }
+      if (!ok) slot[kAbort] = 1;
+      tc::fence_before_sync();
+      sync_all();  // the item is done
+      tc::fence_after_sync();
+      if (tid < kPoison * 4) poison[tid] = 0u;
+      if (tid == 0) slot[kBadPage] = slot[kAnyPoison] = 0;
+      if (slot[kAbort] != 0) {
+        if (tid == 0) flag_or(p.flags, I8KV_FLAG_WAIT_TIMEOUT);
+        break;
+      }
+      sync_all();  // (the notes are cleared)
+    }
+  } else if (warp < (kSoftThreads + kProdThreads) / 32) {
+    // -----------------------------------------------------------------------
+    // converters; of fp16 sources: the check of V blocks attended in part
+    // -----------------------------------------------------------------------
+    // (shares add up to the 512 x 128 / 128 registers of the launch: 2 x 184 + 96 + 48, 2 x 144 + 176 + 48)
+    if constexpr (TILES == 2) regs_down<96>(); else regs_up<176>();
+    const int ct = tid - kSoftThreads;
+    int n = 0;
+    while (next_item<M>(p, it, walk)) {
+      const int nb = it.blk1 - it.blk0;
+      bool ok = true;
+      if constexpr (SRC == kF16) {
+        sync_all();
+        for (int i = 0; i < nb; ++i) {
+          const int nn = n + i, st = nn % S;
+          if (!(ok = tc::mbar_wait(bar(kVFull + st), (nn / S) & 1, slot + kAbort))) break;
+          const int blk = it.blk0 + i;
+          if (it.partial(blk)) {
+            const uint32_t at = sbase + L::kV + st * L::kKV;
+            uint32_t* bits = poison + 4 * it.ordinal(blk);
+#pragma unroll 4
+            for (int k = 0; k < L::kKV / 16 / kProdThreads; ++k) {
+              const int q = ct + kProdThreads * k;
+              uint4 x = lds16(at + 16 * q);
+              if (finite_only(x)) {
+                sts16(at + 16 * q, x);
+                const int row = (q >> 3) & 127;
+                atomicOr(bits + (row >> 5), 1u << (row & 31));
+                slot[kAnyPoison] = 1;
+              }
+            }
+            tc::fence_smem_to_async();
+          }
+          tc::mbar_arrive(bar(kVOk + st));
+        }
+      } else {
+        // K runs one block ahead of V; a block's codes are loaded while the one before is at work
+        Raw<D, SRC> kr, vr;
+        auto groups_of = [&](int blk) -> int {
+          return blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
+        };
+        int g0 = groups_of(it.blk0), g1 = groups_of(it.blk0 + 1);
+        if (nb > 0) {
+          load_raw<D, SRC>(p, it.g, g0, false, kr);
+          load_raw<D, SRC>(p, it.g, g0, true, vr);
+        }
+        sync_all();
+        auto put_k = [&](int i) -> bool {
+          const int nn = n + i, st = nn % S;
+          if (nn >= S && !tc::mbar_wait(bar(kKFree + st), ((nn / S) & 1) ^ 1, slot + kAbort)) return false;
+          store_raw<D, SRC>(kr, sbase + L::kK + st * L::kKV, nullptr, nullptr);
+          tc::fence_smem_to_async();
+          tc::mbar_arrive(bar(kKFull + st));
+          return true;
+        };
+        auto put_v = [&](int i) -> bool {
+          const int nn = n + i, st = nn % S;
+          if (nn >= S && !tc::mbar_wait(bar(kVFree + st), ((nn / S) & 1) ^ 1, slot + kAbort)) return false;
+          const int blk = it.blk0 + i;
+          store_raw<D, SRC>(vr, sbase + L::kV + st * L::kKV,
+                            SRC != kI8 && it.partial(blk) ? poison + 4 * it.ordinal(blk) : nullptr,
+                            slot + kAnyPoison);
+          tc::fence_smem_to_async();
+          tc::mbar_arrive(bar(kVOk + st));
+          return true;
+        };
+        if (nb > 0) {
+          ok = __all_sync(0xffffffffu, put_k(0));
+          if (ok) load_raw<D, SRC>(p, it.g, g1, false, kr);
+        }
+        for (int i = 0; ok && i < nb; ++i) {
+          const int g2 = groups_of(it.blk0 + i + 2);
+          if (i + 1 < nb) {
+            if (!(ok = __all_sync(0xffffffffu, put_k(i + 1)))) break;
+            if (i + 2 < nb) load_raw<D, SRC>(p, it.g, g2, false, kr);
+          }
+          if (!(ok = __all_sync(0xffffffffu, put_v(i)))) break;
+          if (i + 1 < nb) load_raw<D, SRC>(p, it.g, g1, true, vr);
+          g1 = g2;
+        }
+      }
+      n += nb;
+      if (!ok) slot[kAbort] = 1;
+      sync_all();
+      if (slot[kAbort] != 0) break;
+      sync_all();
+    }
+  } else {
+    regs_down<48>();
+    if (warp == kMmaWarp) {
+      // ---------------------------------------------------------------------
+      // MMA issue
+      // ---------------------------------------------------------------------
+      constexpr uint32_t kIdQK = tc::idesc_f16(BM, BN, false, false);
+      constexpr uint32_t kIdPV = tc::idesc_f16(BM, D, false, true);
+      int n = 0, items = 0;
+      while (next_item<M>(p, it, walk)) {
+        const int nb = it.blk1 - it.blk0;
+        const int tiles = min(TILES, (it.q.n * p.G - it.t * M + BM - 1) / BM);  // with live vectors
+        sync_all();
+        tc::fence_after_sync();
+        if (lane == 0) {
+          auto qk = [&](int w, int nn) {  // scores of tile w (or into buffer nn & 1)
+            const uint32_t qs = sbase + L::kQ + w * L::kSlabs * L::kSlab;
+            const uint32_t ks = sbase + L::kK + (nn % S) * L::kKV;
+            const int buf = TILES == 2 ? w : nn & 1;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const uint32_t at = (kk >> 2) * L::kSlab + (kk & 3) * 32;
+              tc::mma_f16(tbase + buf * BN, tc::smem_desc_sw128(qs + at, 1024),
+                          tc::smem_desc_sw128(ks + at, 1024), kIdQK, kk > 0);
+            }
+            tc::mma_commit(bar(kSFull + buf));
+          };
+          auto pv = [&](int w, int nn, bool first) {
+            const uint32_t vs = sbase + L::kV + (nn % S) * L::kKV;
+            const int buf = TILES == 2 ? w : nn & 1;
+#pragma unroll
+            for (int kk = 0; kk < BN / 16; ++kk)
+              tc::mma_f16_ts(tbase + L::kOCol + w * D, tbase + buf * BN + 64 * (kk >> 2) + 8 * (kk & 3),
+                             desc_mn_sw128(vs + kk * 2048, L::kSlab), kIdPV, !first || kk > 0);
+            tc::mma_commit(bar(kPVDone + w));
+          };
+          auto wait = [&](int b, uint32_t par) -> bool { return tc::mbar_wait(bar(b), par, slot + kAbort); };
+          bool ok = true;
+          if constexpr (TILES == 2) {
+            for (int i = -1; ok && i < nb; ++i) {
+              const int nn = n + i, nx = nn + 1;
+              const bool more = i + 1 < nb;
+              for (int w = 0; ok && w < tiles; ++w) {
+                if (i >= 0) {
+                  ok = wait(kPFull + w, nn & 1) && (w > 0 || wait(kVOk + nn % S, (nn / S) & 1));
+                  if (!ok) break;
+                  tc::fence_after_sync();
+                  pv(w, nn, i == 0);
+                  if (w == tiles - 1) tc::mma_commit(bar(kVFree + nn % S));
+                }
+                if (more) {
+                  // the scores go over P(i): PV(i) must have read it
+                  ok = (w > 0 || wait(kKFull + nx % S, (nx / S) & 1)) && (i < 0 || wait(kPVDone + w, nn & 1));
+                  if (!ok) break;
+                  tc::fence_after_sync();
+                  qk(w, nx);
+                  if (w == tiles - 1) tc::mma_commit(bar(kKFree + nx % S));
+                }
+              }
+            }
+          } else {
+            // QK(0), QK(1), PV(0), QK(2), PV(1), ...
+            for (int i = 0; ok && i <= nb; ++i) {
+              const int nn = n + i, pr = nn - 1;
+              if (i < nb) {
+                // S(i) goes over P(i - 2)
+                ok = wait(kKFull + nn % S, (nn / S) & 1) && (i < 2 || wait(kPVDone, nn & 1));
+                if (!ok) break;
+                tc::fence_after_sync();
+                qk(0, nn);
+                tc::mma_commit(bar(kKFree + nn % S));
+              }
+              if (i > 0) {
+                ok = wait(kPFull, pr & 1) && wait(kVOk + pr % S, (pr / S) & 1);
+                if (!ok) break;
+                tc::fence_after_sync();
+                pv(0, pr, i == 1);
+                tc::mma_commit(bar(kVFree + pr % S));
+              }
+            }
+          }
+          if (!ok) slot[kAbort] = 1;
+          // everything issued has completed before the item ends
+          tc::mma_commit(bar(kDone));
+          if (!tc::mbar_wait(bar(kDone), items & 1)) slot[kAbort] = 1;
+        }
+        __syncwarp();
+        n += nb;
+        ++items;
+        sync_all();
+        if (slot[kAbort] != 0) break;
+        sync_all();
+      }
+    } else {
+      // ---------------------------------------------------------------------
+      // fp16 sources: copies
+      // ---------------------------------------------------------------------
+      if (blockIdx.x == 0 && warp == kThreads / 32 - 1)  // lengths and starts that had to be clamped
+        for (int b = lane; b < p.B; b += 32) seq_of(p, b, true);
+      int n = 0;
+      while (next_item<M>(p, it, walk)) {
+        const int nb = it.blk1 - it.blk0;
+        sync_all();
+        if (SRC == kF16 && warp == kTmaWarp) {
+          bool ok = true;
+          int nk = 0, nv = 0;  // copies begun
+          const bool paged = p.table != nullptr;
+          // lane: one box (a packed prompt's of 128 rows: the slab; a page's: group and slab)
+          const int box_slab = paged ? lane >> 3 : lane;
+          const int rows_of_box = paged ? 16 : 128;
+          const bool mine = box_slab < L::kSlabs;
+          auto row_of = [&](int blk) -> int {
+            if (!mine || blk >= it.blk1) return 0;
+            if (!paged) return it.q.s0 + blk * BN;
+            const int grp = group_of(p, it, blk * BN + 16 * (lane & 7));
+            return grp < 0 ? p.rows : grp * 16;  // (a row past the end is read as zeros)
+          };
+          auto copy = [&](int nn, int row, bool is_v) {
+            const int st = nn % S, b = (is_v ? kVFull : kKFull) + st;
+            if (lane == 0) tc::mbar_arrive_expect_tx(bar(b), L::kKV);
+            __syncwarp();
+            if (mine)
+              tma_box(sbase + (is_v ? L::kV : L::kK) + st * L::kKV + box_slab * L::kSlab +
+                          (paged ? (lane & 7) * rows_of_box * 128 : 0),
+                      is_v ? &a.vm : &a.km, 64 * box_slab, it.g, row, bar(b));
+          };
+          auto free = [&](int b, int nn) -> bool {
+            return __all_sync(0xffffffffu, nn < S || tc::mbar_wait(bar(b + nn % S), ((nn / S) & 1) ^ 1, slot + kAbort));
+          };
+          int r0 = row_of(it.blk0), r1 = row_of(it.blk0 + 1);
+          if (nb > 0) {
+            ok = free(kKFree, n);
+            if (ok) copy(n, r0, false), ++nk;
+          }
+          for (int i = 0; ok && i < nb; ++i) {
+            const int r2 = row_of(it.blk0 + i + 2);
+            if (i + 1 < nb) {
+              if (!(ok = free(kKFree, n + i + 1))) break;
+              copy(n + i + 1, r1, false), ++nk;
+            }
+            if (!(ok = free(kVFree, n + i))) break;
+            copy(n + i, r0, true), ++nv;
+            r0 = r1;
+            r1 = r2;
+          }
+          if (!ok) slot[kAbort] = 1;
+          // every copy begun has landed before the item ends (the last S of each, by stage)
+          for (int k = max(0, nk - S); k < nk; ++k)
+            if (!tc::mbar_wait(bar(kKFull + (n + k) % S), ((n + k) / S) & 1)) slot[kAbort] = 1;
+          for (int k = max(0, nv - S); k < nv; ++k)
+            if (!tc::mbar_wait(bar(kVFull + (n + k) % S), ((n + k) / S) & 1)) slot[kAbort] = 1;
+          __syncwarp();
+        }
+        n += nb;
+        sync_all();
+        if (slot[kAbort] != 0) break;
+        sync_all();
+      }
+    }
+  }
+  tc::fence_before_sync();
+  sync_all();
+  if (warp == kMmaWarp) {
+    tc::fence_after_sync();
+    tc::tmem_dealloc(tbase, 512);
+  }
+}
+
+}  // namespace ap
+}  // namespace i8kv

@@ -416,10 +416,140 @@ PyObject* py_paged_decode_mx4(PyObject*, PyObject* const* a, Py_ssize_t n) {
   END_HANDLE_TH_ERRORS
 }
 
+// The length of [n + 1] first rows; the tensor.
+int64_t starts_of(PyObject* o, const char* name, int dev, const int32_t** p) {
+  const at::Tensor& t = tensor_of(o, name);
+  *p = static_cast<const int32_t*>(dense(o, name, at::kInt, dev));
+  if (t.dim() != 1 || t.size(0) < 1)
+    refuse(PyExc_ValueError, std::string(name) + ": expected [B + 1], got " + text_of(t.sizes()));
+  return t.size(0) - 1;
+}
+
+// out [T, Hq, D]: the one passed, or one made here.
+void* out_of(PyObject* o, at::Tensor* made, at::IntArrayRef shape, const at::Tensor& like, int dev) {
+  if (o != Py_None) return shaped(o, "out", at::kHalf, dev, shape);
+  *made = at::empty(shape, like.options());
+  return made->data_ptr();
+}
+
+// (q, k, v, seq_start, softmax_scale, head_sink, out, lse, flags, stream, softcap, window)
+PyObject* py_packed_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (wrong_count("packed_prefill", n, 12)) return nullptr;
+  try {
+    const int dev = device_of(a[0], "q");
+    const at::Tensor& qt = tensor_of(a[0], "q");
+    if (qt.dim() != 3) refuse(PyExc_ValueError, "q: expected [T, Hq, D], got " + text_of(qt.sizes()));
+    const int64_t T = qt.size(0), Hq = qt.size(1), Dq = qt.size(2);
+    const Rows q = rows_of(a[0], "q", dev, T, Dq), k = rows_of(a[1], "k", dev, T, Dq),
+               v = rows_of(a[2], "v", dev, T, Dq);
+    if (k.heads != v.heads)
+      refuse(PyExc_ValueError, "k / v have " + std::to_string(k.heads) + " / " + std::to_string(v.heads) + " heads");
+    const int32_t* starts;
+    const int64_t B = starts_of(a[3], "seq_start", dev, &starts);
+    const void* sink = shaped(a[5], "head_sink", at::kFloat, dev, {Hq});
+    void* lse = shaped(a[7], "lse", at::kFloat, dev, {T, Hq});
+    void* flags = dense(a[8], "flags", at::kInt, dev);
+    const Stream stream(a[9], dev);
+    at::Tensor made;
+    void* out = out_of(a[6], &made, {T, Hq, Dq}, qt, dev);
+    const int32_t tokens = size32(T, "T"), seqs = size32(B, "B"), heads = size32(Hq, "Hq"),
+                  Hkv = size32(k.heads, "Hkv"), D = size32(Dq, "D");
+    const float sigma = float_of(a[4], "softmax_scale"), softcap = float_of(a[10], "softcap");
+    const int32_t window = int_of(a[11], "window");
+    const i8kv_status st = [&] {
+      const Unlocked other_threads_run;
+      return packed_prefill(q.p, q.stride, k.p, k.stride, v.p, v.stride, starts, tokens, seqs, heads,
+                            Hkv, D, sigma, static_cast<const float*>(sink), softcap, window,
+                            static_cast<uint16_t*>(out), static_cast<float*>(lse),
+                            static_cast<uint32_t*>(flags), stream.handle);
+    }();
+    if (st != I8KV_OK) return status(st);
+    if (made.defined()) return THPVariable_Wrap(made);
+    return Py_NewRef(a[6]);
+  } catch (const Refusal& r) {
+    PyErr_SetString(r.type, r.text.c_str());
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+// (q, k_cache, v_cache, k_scale, v_scale, scale_kind, block_table, seq_lens, query_start, softmax_scale,
+//  head_sink, num_splits, workspace, out, lse, flags, stream, softcap, window)
+PyObject* py_paged_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (wrong_count("paged_prefill", n, 19)) return nullptr;
+  try {
+    const int32_t dtype = cache_type(a[1], a[2]);
+    const int dev = device_of(a[1], "k_cache");
+    const at::Tensor& kt = tensor_of(a[1], "k_cache");
+    Cache c = cache_of(a[1], a[2], dtype, dev);
+    if (dtype != I8KV_CACHE_MX4) {
+      if (kt.dim() != 4)
+        refuse(PyExc_ValueError, "k_cache: expected [num_blocks, block_size, Hkv, D], got " + text_of(kt.sizes()));
+      c.blocks = kt.size(0);
+      c.block_size = size32(kt.size(1), "block_size");
+    }
+    const at::Tensor& qt = tensor_of(a[0], "q");
+    if (qt.dim() != 3 || qt.size(2) != c.D)
+      refuse(PyExc_ValueError, "q: expected [T, Hq, " + std::to_string(c.D) + "], got " + text_of(qt.sizes()));
+    const int64_t T = qt.size(0), Hq = qt.size(1);
+    const Rows q = rows_of(a[0], "q", dev, T, c.D);
+    const int32_t* starts;
+    const int64_t B = starts_of(a[8], "query_start", dev, &starts);
+    tensor_of(a[6], "block_table");
+    const void* table = dense(a[6], "block_table", at::kInt, dev);
+    const at::Tensor& bt = tensor_of(a[6], "block_table");
+    if (bt.dim() != 2 || bt.size(0) != B)
+      refuse(PyExc_ValueError, "block_table: expected [" + std::to_string(B) + ", max_blocks], got " +
+                                   text_of(bt.sizes()));
+    tensor_of(a[7], "seq_lens");
+    const void* lens = shaped(a[7], "seq_lens", at::kInt, dev, {B});
+    const int32_t kind = int_of(a[5], "scale_kind");
+    const Scales s = scales_of(a[3], a[4], kind, c, dev);
+    const void* sink = shaped(a[10], "head_sink", at::kFloat, dev, {Hq});
+    void* ws = nullptr;
+    size_t ws_bytes = 0;
+    if (a[12] != Py_None) {
+      const at::Tensor& w = tensor_of(a[12], "workspace");
+      ws = dense(a[12], "workspace", w.scalar_type(), dev);
+      ws_bytes = w.nbytes();
+    }
+    void* lse = shaped(a[14], "lse", at::kFloat, dev, {T, Hq});
+    void* flags = dense(a[15], "flags", at::kInt, dev);
+    const Stream stream(a[16], dev);
+    at::Tensor made;
+    void* out = out_of(a[13], &made, {T, Hq, c.D}, qt, dev);
+    const int32_t tokens = size32(T, "T"), seqs = size32(B, "B"), heads = size32(Hq, "Hq"),
+                  Hkv = size32(c.Hkv, "Hkv"), D = size32(c.D, "D"),
+                  max_blocks = size32(bt.size(1), "max_blocks");
+    const float sigma = float_of(a[9], "softmax_scale"), softcap = float_of(a[17], "softcap");
+    const int32_t window = int_of(a[18], "window"), splits = int_of(a[11], "num_splits");
+    const i8kv_status st = [&] {
+      const Unlocked other_threads_run;
+      return paged_prefill(q.p, q.stride, c.k, c.v, c.dtype, s.k, s.v, kind,
+                           static_cast<const int32_t*>(table), static_cast<const int32_t*>(lens), starts,
+                           tokens, seqs, heads, Hkv, D, c.block_size, max_blocks, c.blocks, sigma,
+                           static_cast<const float*>(sink), softcap, window, splits, ws, ws_bytes,
+                           static_cast<uint16_t*>(out), static_cast<float*>(lse),
+                           static_cast<uint32_t*>(flags), stream.handle);
+    }();
+    if (st != I8KV_OK) return status(st);
+    if (made.defined()) return THPVariable_Wrap(made);
+    return Py_NewRef(a[13]);
+  } catch (const Refusal& r) {
+    PyErr_SetString(r.type, r.text.c_str());
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
 PyMethodDef kMethods[] = {
     {"rope_and_cache", reinterpret_cast<PyCFunction>(py_rope_and_cache), METH_FASTCALL, nullptr},
     {"gather_cache", reinterpret_cast<PyCFunction>(py_gather_cache), METH_FASTCALL, nullptr},
     {"paged_decode_mx4", reinterpret_cast<PyCFunction>(py_paged_decode_mx4), METH_FASTCALL, nullptr},
+    {"packed_prefill", reinterpret_cast<PyCFunction>(py_packed_prefill), METH_FASTCALL, nullptr},
+    {"paged_prefill", reinterpret_cast<PyCFunction>(py_paged_prefill), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 PyModuleDef kModule = {PyModuleDef_HEAD_INIT, "_binding", nullptr, -1, kMethods,
                        nullptr, nullptr, nullptr, nullptr};
