@@ -498,6 +498,35 @@ i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* 
                            void* stream);
 
 /*
+ * norm_rope_and_cache -- rope_and_cache with the heads of queries and keys normed
+ * before the rotation, in the same pass.  For every head of D channels, in fp32:
+ *     x' = x * r * weight[d],  r = 1 / sqrt(sum_d x^2 / D + eps)
+ * (r rounded once; the squares are summed 16 channels at a time, then by halves;
+ * each product rounded on its own), then the rotation and the stores as for
+ * rope_and_cache.  Values are not normed.
+ *   q_weight, k_weight  [D] fp32, 16-byte aligned; NULL: not normed
+ *   eps          finite, >= 0
+ *   k_out        [num_tokens, Hkv, D] fp16, dense, or NULL: the normed and turned
+ *                keys, rounded once, as attention over the new tokens alone wants
+ *                them (packed_prefill); written for every token whose position is in
+ *                range, also where the slot is not; may be k_new itself where k_stride
+ *                = Hkv * D
+ *   D 64, 128 or 256 where a weight is given (I8KV_EUNSUPPORTED otherwise).
+ *   The other arguments as for rope_and_cache.  A head with a NaN is NaN, one with an
+ *   infinity is NaN there and zero elsewhere (before it is turned); a NaN stores 0.
+ */
+i8kv_status norm_rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                                int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
+                                const float* q_weight, const float* k_weight, float eps,
+                                const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                                int32_t rot_dim, int32_t rot_style, const int32_t* slot_mapping,
+                                int32_t num_tokens, int32_t Hq, int32_t Hkv, int32_t D,
+                                uint16_t* q_out, uint16_t* k_out, void* k_cache, void* v_cache,
+                                int32_t cache_dtype, int64_t num_slots, int32_t block_size,
+                                const float* k_scale, const float* v_scale, int32_t scale_kind,
+                                uint32_t* flags, void* stream);
+
+/*
  * gather_cache -- cache rows back as fp16 values (the inverse of the append, for
  * a dense prefill over a cached prefix, or to look at what is stored):
  *     out[n, g, :] = fp16(scale * value of the cache row (slot_mapping[n], g)),

@@ -24,7 +24,7 @@ __all__ = [
     "FLAG_BAD_SLOT", "FLAG_FP32_PATH", "FLAG_WAIT_TIMEOUT", "paged_decode_ex", "window_span",
     "CACHE_FP8", "fp8_to_fp16", "CACHE_MX4", "mx4_cache_shape", "rope_and_cache", "gather_cache",
     "paged_decode_mx4", "FLAG_BAD_POSITION", "packed_prefill", "paged_prefill",
-    "paged_prefill_workspace_bytes",
+    "norm_rope_and_cache", "paged_prefill_workspace_bytes",
     "SCALE_PER_TENSOR", "SCALE_PER_CHANNEL", "CACHE_INT8", "CACHE_FP16", "GEOM_WAVE",
     "GEOM_POW2_TILES", "GEOM_BALANCED", "PATH_DSA", "PATH_PAGED", "MAX_SPLITS", "FLAG_LEN_CLAMPED",
     "FLAG_QUERY_RANGE", "FLAG_BAD_BLOCK",
@@ -100,6 +100,10 @@ _SIGNATURES = {
                                 _c_i32, _c_i32, _c_vp, _c_i32, _c_i32, _c_i32, _c_i32, _c_vp,
                                 _c_vp, _c_vp, _c_i32, _c_i64, _c_i32, _c_vp, _c_vp, _c_i32, _c_vp,
                                 _c_vp]),
+    "norm_rope_and_cache": (_c_i32, [_c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_i64, _c_vp, _c_vp, _c_f32,
+                                     _c_vp, _c_vp, _c_i64, _c_i32, _c_i32, _c_vp, _c_i32, _c_i32, _c_i32,
+                                     _c_i32, _c_vp, _c_vp, _c_vp, _c_vp, _c_i32, _c_i64, _c_i32, _c_vp,
+                                     _c_vp, _c_i32, _c_vp, _c_vp]),
     "gather_cache": (_c_i32, [_c_vp, _c_i32, _c_i32, _c_i32, _c_vp, _c_vp, _c_i32, _c_i64, _c_i32,
                               _c_vp, _c_vp, _c_i32, _c_vp, _c_vp, _c_vp, _c_vp]),
     "paged_decode_mx4": (_c_i32, [_c_vp, _c_vp, _c_vp, _c_vp, _c_i32, _c_vp, _c_vp, _c_i32, _c_i32,
@@ -431,6 +435,24 @@ def rope_and_cache(q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v
         scale_kind, interleaved, q_out, flags, None if stream is None else _stream(stream))
     if type(r) is int:
         _check("rope_and_cache", r)
+    return r
+
+
+def norm_rope_and_cache(q, k_new, v_new, q_weight, k_weight, eps: float, positions, cos_sin,
+                        slot_mapping, k_cache, v_cache, k_scale, v_scale, scale_kind: int,
+                        interleaved: bool = False, q_out=None, k_out=None, flags=None, stream=None,
+                        return_keys: bool = False):
+    """``rope_and_cache`` with every head of q and k_new normed before the rotation:
+    x / sqrt(mean(x^2) + eps) * weight, q_weight and k_weight [D] fp32 (None: not
+    normed).  Returns (q_out, k_out): k_out [T, Hkv, D] fp16 holds the normed and
+    turned keys, for ``packed_prefill`` over the new tokens; it is the tensor passed,
+    or one made here with return_keys, else None."""
+    r = (_BINDING or _compiled()).norm_rope_and_cache(
+        q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale,
+        scale_kind, interleaved, q_out, flags, None if stream is None else _stream(stream), q_weight,
+        k_weight, eps, k_out, return_keys)
+    if type(r) is int:
+        _check("norm_rope_and_cache", r)
     return r
 
 

@@ -983,15 +983,16 @@ static i8kv_status check_cache(const void* k_cache, const void* v_cache, int32_t
   return I8KV_OK;
 }
 
-i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
-                           int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
-                           const int32_t* positions, const float* cos_sin, int64_t max_pos,
-                           int32_t rot_dim, int32_t rot_style, const int32_t* slot_mapping,
-                           int32_t num_tokens, int32_t Hq, int32_t Hkv, int32_t D,
-                           uint16_t* q_out, void* k_cache, void* v_cache, int32_t cache_dtype,
-                           int64_t num_slots, int32_t block_size, const float* k_scale,
-                           const float* v_scale, int32_t scale_kind, uint32_t* flags,
-                           void* stream) {
+static i8kv_status append(const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                          int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
+                          const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                          int32_t rot_dim, int32_t rot_style, const int32_t* slot_mapping,
+                          int32_t num_tokens, int32_t Hq, int32_t Hkv, int32_t D,
+                          uint16_t* q_out, void* k_cache, void* v_cache, int32_t cache_dtype,
+                          int64_t num_slots, int32_t block_size, const float* k_scale,
+                          const float* v_scale, int32_t scale_kind, const float* q_weight,
+                          const float* k_weight, float eps, uint16_t* k_out, uint32_t* flags,
+                          void* stream) {
   if (num_tokens < 0 || Hq < 0 || max_pos < 0) return I8KV_EINVAL;
   if (rot_style != I8KV_ROPE_HALVES && rot_style != I8KV_ROPE_INTERLEAVED) return I8KV_EINVAL;
   i8kv_status st = check_cache(k_cache, v_cache, cache_dtype, num_slots, block_size, k_scale,
@@ -1017,6 +1018,7 @@ i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* 
       !aligned(cos_sin, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 4) ||
       !aligned(flags, 4))
     return I8KV_EALIGN;
+  if (!aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(k_out, 16)) return I8KV_EALIGN;
   if (num_tokens == 0) return I8KV_OK;
   i8kv::AppendParams p{};
   p.q = reinterpret_cast<const __half*>(q);
@@ -1045,8 +1047,47 @@ i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* 
   p.v_scale = v_scale;
   p.per_channel = scale_kind == I8KV_SCALE_PER_CHANNEL;
   p.flags = flags;
+  p.q_weight = Hq > 0 ? q_weight : nullptr;
+  p.k_weight = k_weight;
+  p.eps = eps;
+  p.k_out = reinterpret_cast<__half*>(k_out);
   cudaError_t e = i8kv::launch_rope_and_cache(p, cache_dtype, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
+}
+
+i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                           int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
+                           const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                           int32_t rot_dim, int32_t rot_style, const int32_t* slot_mapping,
+                           int32_t num_tokens, int32_t Hq, int32_t Hkv, int32_t D,
+                           uint16_t* q_out, void* k_cache, void* v_cache, int32_t cache_dtype,
+                           int64_t num_slots, int32_t block_size, const float* k_scale,
+                           const float* v_scale, int32_t scale_kind, uint32_t* flags,
+                           void* stream) {
+  return append(q, q_stride, k_new, k_stride, v_new, v_stride, positions, cos_sin, max_pos, rot_dim,
+                rot_style, slot_mapping, num_tokens, Hq, Hkv, D, q_out, k_cache, v_cache,
+                cache_dtype, num_slots, block_size, k_scale, v_scale, scale_kind, nullptr, nullptr,
+                0.f, nullptr, flags, stream);
+}
+
+i8kv_status norm_rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
+                                int64_t k_stride, const uint16_t* v_new, int64_t v_stride,
+                                const float* q_weight, const float* k_weight, float eps,
+                                const int32_t* positions, const float* cos_sin, int64_t max_pos,
+                                int32_t rot_dim, int32_t rot_style, const int32_t* slot_mapping,
+                                int32_t num_tokens, int32_t Hq, int32_t Hkv, int32_t D,
+                                uint16_t* q_out, uint16_t* k_out, void* k_cache, void* v_cache,
+                                int32_t cache_dtype, int64_t num_slots, int32_t block_size,
+                                const float* k_scale, const float* v_scale, int32_t scale_kind,
+                                uint32_t* flags, void* stream) {
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return I8KV_EINVAL;
+  // a head's lanes are a power of two
+  if ((q_weight != nullptr || k_weight != nullptr) && Hkv > 0 && D > 0 && !supported_head_dim(D))
+    return I8KV_EUNSUPPORTED;
+  return append(q, q_stride, k_new, k_stride, v_new, v_stride, positions, cos_sin, max_pos, rot_dim,
+                rot_style, slot_mapping, num_tokens, Hq, Hkv, D, q_out, k_cache, v_cache,
+                cache_dtype, num_slots, block_size, k_scale, v_scale, scale_kind, q_weight, k_weight,
+                eps, k_out, flags, stream);
 }
 
 i8kv_status gather_cache(const int32_t* slot_mapping, int32_t num_rows, int32_t Hkv, int32_t D,

@@ -1,5 +1,6 @@
 // Append of new rows to a paged cache with the position rotation applied on the
-// way (rope_and_cache), and the read-back of cache rows as fp16 (gather_cache).
+// way (rope_and_cache), the same with the heads of queries and keys normed first
+// (norm_rope_and_cache), and the read-back of cache rows as fp16 (gather_cache).
 //
 // Rotation of a pair (a, b) of channels by the angle of its position:
 //   a' = a cos - b sin,  b' = b cos + a sin
@@ -11,6 +12,10 @@
 //   fp16          x rounded once
 //   MX4           y = x fl(1/scale); block scale s = e4m3(min(max|y| fl(1/6), 448)),
 //                 code = e2m1(y fl(1/s))
+//
+// The norm of a head: y = x r w with r = 1 / sqrt(mean x^2 + eps), rounded once, in fp32; the
+// squares of a thread's 16 channels are summed in order, then over the D / 16 lanes that hold the
+// head by halves.
 //
 // Bound: HBM, rows in and rows out once each.  A thread keeps one item -- 16 channels
 // of a head as two pieces of 8, so that every access is 16 bytes and neighbouring
@@ -190,6 +195,32 @@ __device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], const An
   }
 }
 
+// The norm of a head that the aligned `ipr` lanes of the warp hold (a power of two), 16 channels
+// each, in place.  All of them are here together: they work on the same token.
+__device__ __forceinline__ void norm_item(float (&a)[8], float (&b)[8], const float (&wa)[8],
+                                          const float (&wb)[8], int ipr, float eps) {
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], ss);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) ss = fmaf(b[i], b[i], ss);
+  const int lane = threadIdx.x & 31;
+  const unsigned of_head = ((1u << ipr) - 1u) << (lane & ~(ipr - 1));
+  for (int o = ipr >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(of_head, ss, o);
+  const float r = __frsqrt_rn(fmaf(ss, 1.f / (float)(16 * ipr), eps));
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    a[i] = __fmul_rn(__fmul_rn(a[i], r), wa[i]);
+    b[i] = __fmul_rn(__fmul_rn(b[i], r), wb[i]);
+  }
+}
+__device__ __forceinline__ void weights8(const float* w, int at, float (&x)[8]) {
+  const float4 a = __ldg(reinterpret_cast<const float4*>(w + at));
+  const float4 b = __ldg(reinterpret_cast<const float4*>(w + at) + 1);
+  x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+  x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
 // One row's item into the cache.  r0, r1: reciprocals of the scales of the two pieces;
 // inv_scale (MX4): the rounded reciprocals of the 127 block scales, by their byte.
 template <int CACHE>
@@ -296,7 +327,8 @@ __device__ __forceinline__ void copy16(uint4* to, const __half* from) {
 }
 
 // HQ: query heads per thread (1: a few tokens, where threads are short; else 4).
-template <int CACHE, int HQ>
+// NORM: queries and keys normed first where their weights are given, keys written out where asked.
+template <int CACHE, int HQ, bool NORM>
 __global__ void __launch_bounds__(kAppendThreads, 2)
 rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lanes) {
   __shared__ float inv_scale[CACHE == I8KV_CACHE_MX4 ? 128 : 1];
@@ -328,6 +360,14 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
   if (queries) {  // HQ heads of a token
     const Pieces x = pieces_of(p, j, true);
     const int h0 = unit * HQ;
+    float w0[8], w1[8];
+    const bool normed = NORM && p.q_weight != nullptr;
+    if constexpr (NORM) {
+      if (normed) {
+        weights8(p.q_weight, x.c0, w0);
+        weights8(p.q_weight, x.c1, w1);
+      }
+    }
     int next = p.R > 0 ? __ldg(p.positions + n0) : 0;  // a position ahead of its angles
     for (long long n = n0; n < p.num_tokens; n += lanes) {
       const int pos = next;
@@ -349,11 +389,14 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
 #pragma unroll
       for (int i = 0; i < HQ; ++i)
         if (h0 + i < p.Hq) {
-          if (x.turned) {
+          if (x.turned || normed) {
             float a[8], b[8];
             unpack8(ra[i], a);
             unpack8(rb[i], b);
-            turn_item(a, b, g, il);
+            if constexpr (NORM) {
+              if (normed) norm_item(a, b, w0, w1, ipr, p.eps);
+            }
+            if (!NORM || x.turned) turn_item(a, b, g, il);
             ra[i] = pack8(a);
             rb[i] = pack8(b);
           }
@@ -389,6 +432,15 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
       const float r = reciprocal<CACHE>(r0[0]);
 #pragma unroll
       for (int i = 0; i < 8; ++i) r0[i] = r1[i] = r;
+    }
+  }
+  float w0[8], w1[8];
+  const bool normed = NORM && !is_v && p.k_weight != nullptr;
+  const bool keys_out = NORM && !is_v && p.k_out != nullptr;
+  if constexpr (NORM) {
+    if (normed) {
+      weights8(p.k_weight, x.c0, w0);
+      weights8(p.k_weight, x.c1, w1);
     }
   }
   const __half* src = (is_v ? p.v : p.k) + (long long)h * p.D;
@@ -438,28 +490,42 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
     }
     Angles g[N];
     int at[N];
+    bool out[N];  // NORM: the token's keys are written out
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       at[i] = slot[i];
+      out[i] = keys_out && n + i * lanes < p.num_tokens;
       if (p.R > 0 && (pos[i] < 0 || (long long)pos[i] >= p.max_pos)) {
         // (one key item reports it)
         if (kv == 0 && j == 0 && slot[i] >= 0) flag_or(p.flags, I8KV_FLAG_BAD_POSITION);
         at[i] = -1;
+        out[i] = false;
       } else if ((long long)slot[i] >= p.num_slots) {
         if (kv == 0 && j == 0) flag_or(p.flags, I8KV_FLAG_BAD_SLOT);
         at[i] = -1;
       }
-      if (at[i] >= 0 && x.turned) g[i] = angles_of(p, x, pos[i]);
+      if ((at[i] >= 0 || out[i]) && x.turned) g[i] = angles_of(p, x, pos[i]);
     }
     look(n + N * lanes);
     if constexpr (RING) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (at[i] < 0) continue;
+      if (at[i] < 0 && !out[i]) continue;
       float a[8], b[8];
       unpack8(RING ? ring[st][i][0][threadIdx.x] : raw[i][0], a);
       unpack8(RING ? ring[st][i][1][threadIdx.x] : raw[i][1], b);
+      if constexpr (NORM) {
+        if (normed) norm_item(a, b, w0, w1, ipr, p.eps);
+      }
       if (x.turned) turn_item(a, b, g[i], il);
+      if constexpr (NORM) {
+        if (out[i]) {
+          __half* o = p.k_out + ((n + i * lanes) * p.Hkv + h) * p.D;
+          *reinterpret_cast<uint4*>(o + x.c0) = pack8(a);
+          *reinterpret_cast<uint4*>(o + x.c1) = pack8(b);
+        }
+        if (at[i] < 0) continue;
+      }
       store_item<CACHE>(p, x, h, is_v, at[i], a, b, r0, r1, sc, step, inv_scale);
     }
   }
@@ -620,7 +686,7 @@ namespace {
 template <int CACHE>
 constexpr double kKvShare = CACHE == I8KV_CACHE_FP16 ? 0.5 : 0.65;
 
-template <int CACHE, int HQ>
+template <int CACHE, int HQ, bool NORM>
 cudaError_t append_with(const AppendParams& p, int sms, cudaStream_t stream) {
   const long long q_items = (p.Hq + HQ - 1LL) / HQ * (p.D / 16), kv_items = 2LL * p.Hkv * (p.D / 16);
   const double per = 2. * sms * kAppendThreads / (q_items + kKvShare<CACHE> * kv_items);  // the resident CTAs
@@ -629,19 +695,19 @@ cudaError_t append_with(const AppendParams& p, int sms, cudaStream_t stream) {
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
       config_of(32 * (warps_of(q_lanes * q_items) + warps_of(kv_lanes * kv_items)), &attr, stream);
-  return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<CACHE, HQ>, p, q_lanes, kv_lanes);
+  return cudaLaunchKernelEx(&cfg, rope_and_cache_kernel<CACHE, HQ, NORM>, p, q_lanes, kv_lanes);
 }
 
 // Four query heads per thread where one head each would fill the GPU more than once
 // over (64 of 192 bytes saved per head); one head each spreads fewer tokens wider.
-template <int CACHE>
+template <int CACHE, bool NORM>
 cudaError_t append_of(const AppendParams& p, cudaStream_t stream) {
   int sms = 0;
   const cudaError_t e = sm_count(&sms);
   if (e != cudaSuccess) return e;
   const long long items = (long long)p.num_tokens * (p.Hq + 2 * p.Hkv) * (p.D / 16);
-  return items > 4LL * sms * kAppendThreads ? append_with<CACHE, 4>(p, sms, stream)
-                                            : append_with<CACHE, 1>(p, sms, stream);
+  return items > 4LL * sms * kAppendThreads ? append_with<CACHE, 4, NORM>(p, sms, stream)
+                                            : append_with<CACHE, 1, NORM>(p, sms, stream);
 }
 
 template <int CACHE>
@@ -659,14 +725,21 @@ cudaError_t gather_of(const AppendParams& p, void* k_out, void* v_out, cudaStrea
 
 }  // namespace
 
-cudaError_t launch_rope_and_cache(const AppendParams& p, int cache_dtype, cudaStream_t stream) {
+template <bool NORM>
+static cudaError_t launch_append(const AppendParams& p, int cache_dtype, cudaStream_t stream) {
   switch (cache_dtype) {
-    case I8KV_CACHE_INT8: return append_of<I8KV_CACHE_INT8>(p, stream);
-    case I8KV_CACHE_FP16: return append_of<I8KV_CACHE_FP16>(p, stream);
-    case I8KV_CACHE_FP8: return append_of<I8KV_CACHE_FP8>(p, stream);
-    case I8KV_CACHE_MX4: return append_of<I8KV_CACHE_MX4>(p, stream);
+    case I8KV_CACHE_INT8: return append_of<I8KV_CACHE_INT8, NORM>(p, stream);
+    case I8KV_CACHE_FP16: return append_of<I8KV_CACHE_FP16, NORM>(p, stream);
+    case I8KV_CACHE_FP8: return append_of<I8KV_CACHE_FP8, NORM>(p, stream);
+    case I8KV_CACHE_MX4: return append_of<I8KV_CACHE_MX4, NORM>(p, stream);
     default: return cudaErrorInvalidValue;
   }
+}
+
+cudaError_t launch_rope_and_cache(const AppendParams& p, int cache_dtype, cudaStream_t stream) {
+  return p.q_weight != nullptr || p.k_weight != nullptr || p.k_out != nullptr
+             ? launch_append<true>(p, cache_dtype, stream)
+             : launch_append<false>(p, cache_dtype, stream);
 }
 
 cudaError_t launch_gather_cache(const AppendParams& p, int cache_dtype, void* k_out, void* v_out,

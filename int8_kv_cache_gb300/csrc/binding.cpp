@@ -1,5 +1,6 @@
-// The compiled half of the Python binding, for the calls of a decode step:
-// rope_and_cache, gather_cache and paged_decode_mx4.  It checks the tensors, makes
+// The compiled half of the Python binding, for the calls of a serving step:
+// rope_and_cache, norm_rope_and_cache, gather_cache, packed_prefill, paged_prefill
+// and paged_decode_mx4.  It checks the tensors, makes
 // the outputs that were not passed and calls the C entry point of the same name on
 // the current stream; the same in Python costs about ten times as long (10 us a
 // call on Grace, more than the kernels of a small step).  A status other than
@@ -227,69 +228,133 @@ bool wrong_count(const char* name, Py_ssize_t got, Py_ssize_t want) {
   return true;
 }
 
+// The norms of norm_rope_and_cache; rope_and_cache has none.
+struct Norms {
+  float eps = 0.f;
+  PyObject* k_out = Py_None;
+  bool keys = false;  // k_out is made here
+};
+
+// What both appends do: a = (q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale,
+// v_scale, scale_kind, interleaved, q_out, flags, stream); returns q_out, with norms (q_out, k_out).
+PyObject* append(PyObject* const* a, const Norms* norms, PyObject* q_weight, PyObject* k_weight) {
+  const int32_t dtype = cache_type(a[6], a[7]);
+  const int dev = device_of(a[6], "k_cache");
+  const Cache c = cache_of(a[6], a[7], dtype, dev);
+  const at::Tensor& kt = tensor_of(a[1], "k_new");
+  if (kt.dim() != 3) refuse(PyExc_ValueError, "k_new: expected [T, Hkv, D], got " + text_of(kt.sizes()));
+  const int64_t T = kt.size(0);
+  const Rows k = rows_of(a[1], "k_new", dev, T, c.D), v = rows_of(a[2], "v_new", dev, T, c.D);
+  if (k.heads != c.Hkv || v.heads != c.Hkv)
+    refuse(PyExc_ValueError, "k_new / v_new have " + std::to_string(k.heads) + " / " +
+                                 std::to_string(v.heads) + " heads, the cache " + std::to_string(c.Hkv));
+  const void* pos = nullptr;
+  const void* cs = nullptr;
+  int64_t max_pos = 0, R = 0;
+  if (a[4] != Py_None) {
+    cs = dense(a[4], "cos_sin", at::kFloat, dev);
+    const at::Tensor& t = THPVariable_Unpack(a[4]);
+    if (t.dim() != 2) refuse(PyExc_ValueError, "cos_sin must be [max_pos, rot_dim]");
+    max_pos = t.size(0);
+    R = t.size(1);
+    pos = shaped(a[3], "positions", at::kInt, dev, {T});
+  }
+  const void* slots = shaped(a[5], "slot_mapping", at::kInt, dev, {T});
+  const int32_t kind = int_of(a[10], "scale_kind");
+  const Scales s = scales_of(a[8], a[9], kind, c, dev);
+  const int style = PyObject_IsTrue(a[11]);
+  if (style < 0) return nullptr;
+  void* flags = dense(a[13], "flags", at::kInt, dev);
+  const void *qw = nullptr, *kw = nullptr;
+  if (norms != nullptr) {
+    qw = shaped(q_weight, "q_weight", at::kFloat, dev, {c.D});
+    kw = shaped(k_weight, "k_weight", at::kFloat, dev, {c.D});
+  }
+  const Stream stream(a[14], dev);
+  Rows q{nullptr, 0, 0};
+  PyObject* out = a[12];
+  at::Tensor made, made_k;
+  void *qo = nullptr, *ko = nullptr;
+  if (a[0] != Py_None) {
+    q = rows_of(a[0], "q", dev, T, c.D);
+    if (out == Py_None) {
+      made = at::empty({T, q.heads, c.D}, THPVariable_Unpack(a[0]).options());
+      qo = made.data_ptr();
+    } else {
+      qo = shaped(out, "q_out", at::kHalf, dev, {T, q.heads, c.D});
+    }
+  } else if (out != Py_None) {
+    refuse(PyExc_ValueError, "q_out without q");
+  }
+  if (norms != nullptr) {
+    if (norms->k_out != Py_None) {
+      ko = shaped(norms->k_out, "k_out", at::kHalf, dev, {T, c.Hkv, c.D});
+    } else if (norms->keys) {
+      made_k = at::empty({T, c.Hkv, c.D}, kt.options());
+      ko = made_k.data_ptr();
+    }
+  }
+  const int32_t tokens = size32(T, "T"), Hq = size32(q.heads, "Hq"), Hkv = size32(c.Hkv, "Hkv");
+  const int32_t D = size32(c.D, "D"), rot = size32(R, "rot_dim");
+  const i8kv_status st = [&] {
+    const Unlocked other_threads_run;
+    if (norms != nullptr)
+      return norm_rope_and_cache(q.p, q.stride, k.p, k.stride, v.p, v.stride, static_cast<const float*>(qw),
+                                 static_cast<const float*>(kw), norms->eps, static_cast<const int32_t*>(pos),
+                                 static_cast<const float*>(cs), max_pos, rot,
+                                 style ? I8KV_ROPE_INTERLEAVED : I8KV_ROPE_HALVES,
+                                 static_cast<const int32_t*>(slots), tokens, Hq, Hkv, D,
+                                 static_cast<uint16_t*>(qo), static_cast<uint16_t*>(ko), c.k, c.v, c.dtype,
+                                 c.slots, c.block_size, s.k, s.v, kind, static_cast<uint32_t*>(flags),
+                                 stream.handle);
+    return rope_and_cache(q.p, q.stride, k.p, k.stride, v.p, v.stride,
+                          static_cast<const int32_t*>(pos), static_cast<const float*>(cs), max_pos,
+                          rot, style ? I8KV_ROPE_INTERLEAVED : I8KV_ROPE_HALVES,
+                          static_cast<const int32_t*>(slots), tokens, Hq, Hkv, D,
+                          static_cast<uint16_t*>(qo), c.k, c.v, c.dtype, c.slots, c.block_size,
+                          s.k, s.v, kind, static_cast<uint32_t*>(flags), stream.handle);
+  }();
+  if (st != I8KV_OK) return status(st);
+  PyObject* q_done = made.defined() ? THPVariable_Wrap(made) : Py_NewRef(out);
+  if (norms == nullptr || q_done == nullptr) return q_done;
+  PyObject* k_done = made_k.defined() ? THPVariable_Wrap(made_k) : Py_NewRef(norms->k_out);
+  PyObject* r = k_done != nullptr ? PyTuple_New(2) : nullptr;
+  if (r == nullptr) {
+    Py_DECREF(q_done);
+    Py_XDECREF(k_done);
+    return nullptr;
+  }
+  PyTuple_SET_ITEM(r, 0, q_done);
+  PyTuple_SET_ITEM(r, 1, k_done);
+  return r;
+}
+
 // (q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale,
 //  scale_kind, interleaved, q_out, flags, stream)
 PyObject* py_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
   HANDLE_TH_ERRORS
   if (wrong_count("rope_and_cache", n, 15)) return nullptr;
   try {
-    const int32_t dtype = cache_type(a[6], a[7]);
-    const int dev = device_of(a[6], "k_cache");
-    const Cache c = cache_of(a[6], a[7], dtype, dev);
-    const at::Tensor& kt = tensor_of(a[1], "k_new");
-    if (kt.dim() != 3) refuse(PyExc_ValueError, "k_new: expected [T, Hkv, D], got " + text_of(kt.sizes()));
-    const int64_t T = kt.size(0);
-    const Rows k = rows_of(a[1], "k_new", dev, T, c.D), v = rows_of(a[2], "v_new", dev, T, c.D);
-    if (k.heads != c.Hkv || v.heads != c.Hkv)
-      refuse(PyExc_ValueError, "k_new / v_new have " + std::to_string(k.heads) + " / " +
-                                   std::to_string(v.heads) + " heads, the cache " + std::to_string(c.Hkv));
-    const void* pos = nullptr;
-    const void* cs = nullptr;
-    int64_t max_pos = 0, R = 0;
-    if (a[4] != Py_None) {
-      cs = dense(a[4], "cos_sin", at::kFloat, dev);
-      const at::Tensor& t = THPVariable_Unpack(a[4]);
-      if (t.dim() != 2) refuse(PyExc_ValueError, "cos_sin must be [max_pos, rot_dim]");
-      max_pos = t.size(0);
-      R = t.size(1);
-      pos = shaped(a[3], "positions", at::kInt, dev, {T});
-    }
-    const void* slots = shaped(a[5], "slot_mapping", at::kInt, dev, {T});
-    const int32_t kind = int_of(a[10], "scale_kind");
-    const Scales s = scales_of(a[8], a[9], kind, c, dev);
-    const int style = PyObject_IsTrue(a[11]);
-    if (style < 0) return nullptr;
-    void* flags = dense(a[13], "flags", at::kInt, dev);
-    const Stream stream(a[14], dev);
-    Rows q{nullptr, 0, 0};
-    PyObject* out = a[12];
-    at::Tensor made;
-    void* qo = nullptr;
-    if (a[0] != Py_None) {
-      q = rows_of(a[0], "q", dev, T, c.D);
-      if (out == Py_None) {
-        made = at::empty({T, q.heads, c.D}, THPVariable_Unpack(a[0]).options());
-        qo = made.data_ptr();
-      } else {
-        qo = shaped(out, "q_out", at::kHalf, dev, {T, q.heads, c.D});
-      }
-    } else if (out != Py_None) {
-      refuse(PyExc_ValueError, "q_out without q");
-    }
-    const int32_t tokens = size32(T, "T"), Hq = size32(q.heads, "Hq"), Hkv = size32(c.Hkv, "Hkv");
-    const int32_t D = size32(c.D, "D"), rot = size32(R, "rot_dim");
-    const i8kv_status st = [&] {
-      const Unlocked other_threads_run;
-      return rope_and_cache(q.p, q.stride, k.p, k.stride, v.p, v.stride,
-                            static_cast<const int32_t*>(pos), static_cast<const float*>(cs), max_pos,
-                            rot, style ? I8KV_ROPE_INTERLEAVED : I8KV_ROPE_HALVES,
-                            static_cast<const int32_t*>(slots), tokens, Hq, Hkv, D,
-                            static_cast<uint16_t*>(qo), c.k, c.v, c.dtype, c.slots, c.block_size,
-                            s.k, s.v, kind, static_cast<uint32_t*>(flags), stream.handle);
-    }();
-    if (st != I8KV_OK) return status(st);
-    if (made.defined()) return THPVariable_Wrap(made);
-    return Py_NewRef(out);
+    return append(a, nullptr, nullptr, nullptr);
+  } catch (const Refusal& r) {
+    PyErr_SetString(r.type, r.text.c_str());
+    return nullptr;
+  }
+  END_HANDLE_TH_ERRORS
+}
+
+// (those of rope_and_cache, then q_weight, k_weight, eps, k_out, return_keys)
+PyObject* py_norm_rope_and_cache(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  HANDLE_TH_ERRORS
+  if (wrong_count("norm_rope_and_cache", n, 20)) return nullptr;
+  try {
+    Norms norms;
+    norms.eps = float_of(a[17], "eps");
+    norms.k_out = a[18];
+    const int keys = PyObject_IsTrue(a[19]);
+    if (keys < 0) return nullptr;
+    norms.keys = keys != 0;
+    return append(a, &norms, a[15], a[16]);
   } catch (const Refusal& r) {
     PyErr_SetString(r.type, r.text.c_str());
     return nullptr;
@@ -546,6 +611,7 @@ PyObject* py_paged_prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
 
 PyMethodDef kMethods[] = {
     {"rope_and_cache", reinterpret_cast<PyCFunction>(py_rope_and_cache), METH_FASTCALL, nullptr},
+    {"norm_rope_and_cache", reinterpret_cast<PyCFunction>(py_norm_rope_and_cache), METH_FASTCALL, nullptr},
     {"gather_cache", reinterpret_cast<PyCFunction>(py_gather_cache), METH_FASTCALL, nullptr},
     {"paged_decode_mx4", reinterpret_cast<PyCFunction>(py_paged_decode_mx4), METH_FASTCALL, nullptr},
     {"packed_prefill", reinterpret_cast<PyCFunction>(py_packed_prefill), METH_FASTCALL, nullptr},

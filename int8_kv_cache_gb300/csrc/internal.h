@@ -129,6 +129,11 @@ struct AppendParams {
   const float* v_scale;
   int32_t per_channel;
   uint32_t* flags;
+  // norm_rope_and_cache: [D] weights of the norms (or nullptr), and where keys go besides the cache
+  const float* q_weight;
+  const float* k_weight;
+  float eps;
+  __half* k_out;             // [num_tokens, Hkv, D] or nullptr
 };
 cudaError_t launch_rope_and_cache(const AppendParams& p, int cache_dtype, cudaStream_t stream);
 cudaError_t launch_gather_cache(const AppendParams& p, int cache_dtype, void* k_out, void* v_out,
