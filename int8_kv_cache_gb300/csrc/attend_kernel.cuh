@@ -63,10 +63,10 @@ namespace ap {
 
 constexpr int BM = 128;  // vectors of a tile (tensor-memory lanes)
 constexpr int BN = 128;  // positions of a block
-constexpr int kSoftThreads = 256;
 constexpr int kProdThreads = 128;
+constexpr int kSoftThreads = 256;
 constexpr int kThreads = 512;
-constexpr int kMmaWarp = 12, kTmaWarp = 13;
+constexpr int kMmaWarp = 12, kTmaWarp = 13, kLastWarp = 15;
 constexpr float kLazy = 7.f;   // powers of two that the maximum may outgrow the base
 constexpr float kShift = 8.f;  // P holds p 2^kShift: at most 2^15
 constexpr int kPoison = 8;     // blocks that a tile's rows can attend in part (6 at most)
@@ -88,19 +88,20 @@ struct Layout {
   static constexpr int kV = kK + kStages * kKV;
   static constexpr int kBars = kV + kStages * kKV;
   static constexpr int kSlots = kBars + 256;
-  static constexpr int kPois = kSlots + 64;              // [kPoison][4] bits of positions
+  static constexpr int kItem = kSlots + 64;
+  static constexpr int kPois = kItem + 128;              // [kPoison][4] bits of positions
   static constexpr int kRowScale = kPois + kPoison * 16;  // [kM] 2^e of each vector
-  static constexpr int kXchg = kRowScale + kM * 4;        // TILES == 1: [3][2][BM] floats
-  static constexpr int kVote = kXchg + (TILES == 1 ? 6 * BM * 4 : 0);
-  static constexpr int kBytes = kVote + 64;
+  static constexpr int kXchg = kRowScale + kM * 4;              // TILES == 1: [3][2][BM] floats
+  static constexpr int kVote = kXchg + (TILES == 1 ? 6 * BM * 4 : 0);  // TILES == 1: [3][4][2] ints
+  static constexpr int kBytes = kVote + 96;
   static constexpr int kOCol = 2 * BN;  // O behind the two score buffers
   static_assert(kOCol + TILES * D <= 512, "tensor memory");
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
 // barriers (8 bytes each); s: the stage, w: the tile (or, TILES == 1, the score buffer)
-enum Bar { kKFull = 0, kKFree = 4, kVFull = 8, kVFree = 12, kVOk = 16, kSFull = 20, kPFull = 22, kPVDone = 24, kDone = 26, kNumBars = 27 };
-enum Slot { kTmem, kAbort, kBadPage, kAnyPoison, kNumSlots };
+enum Bar { kKFull = 0, kKFree = 4, kVFull = 8, kVFree = 12, kVOk = 16, kSFull = 20, kPFull = 22, kPVDone = 24, kPHalf = 26, kDone = 28, kNumBars = 29 };
+enum Slot { kTmem, kAbort, kBadPage, kAnyPoison, kHas, kNumSlots };
 static_assert(kNumBars * 8 <= 256 && kNumSlots * 4 <= 64, "misc");
 
 __device__ __forceinline__ void sync_all() { asm volatile("bar.sync 0, 512;\n" ::: "memory"); }
@@ -141,6 +142,74 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
                : "memory");
   return v;
 }
+
+// tc::mbar_wait of a converged warp, with its clock and the others' news looked at every so often
+// only.  All lanes wait: one alone, and the others for it, hears of a phase some 300 cycles later.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
+  bool ok = false;
+#pragma unroll 1
+  for (int i = 0; !ok && i < 64; ++i) ok = tc::mbar_try_wait(bar, parity);
+  return __all_sync(0xffffffffu, ok || tc::mbar_wait(bar, parity, abort));
+}
+__device__ __forceinline__ void warp_arrive(uint32_t bar) {
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) tc::mbar_arrive(bar);
+}
+
+// The MMA warp works converged, so that descriptors and addresses stay in uniform registers (one
+// lane alone took 75 to 130 cycles to form and issue an instruction of 64); its elected lane issues.
+__device__ __forceinline__ uint32_t elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p;
+}
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+  asm volatile(
+      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lead)
+      : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
+  asm volatile(
+      "{\n .reg .pred q;\n setp.ne.b32 q, %1, 0;\n"
+      " @q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(bar),
+      "r"(lead)
+      : "memory");
+}
+
+// Two fp32 values as one operand, and two operations in one instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void unpair(uint64_t d, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(d));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ float sum4(const uint64_t (&p)[2]) {
+  float a, b;
+  unpair(add2(p[0], p[1]), a, b);
+  return a + b;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
 
 // Zero the non-finite ones of two fp16 values; returns whether there were any.
 __device__ __forceinline__ bool finite_only(uint32_t& x) {
@@ -226,13 +295,15 @@ __device__ __forceinline__ void place(const AttendParams& p, Item& it, int x, in
   it.blk1 = max(it.blk0, min(B1, it.B0 + y));
 }
 
-// The walk over this CTA's items.
+static_assert(sizeof(Item) <= 128, "item");
+
+// The walk over this CTA's items (of the last warp, which hands them out in shared memory).
 struct Walk {
   long long f, end, per, base;  // flat blocks; base: of sequence b's first
   int wt, tiles;
 };
 
-// Finds the CTA's first item (every warp for itself); false: there is none.
+// Finds where the CTA's items begin (a warp); false: it has none.
 template <int M>
 __device__ __forceinline__ bool first_item(const AttendParams& p, Item& it, Walk& w) {
   const int lane = threadIdx.x & 31;
@@ -245,7 +316,8 @@ __device__ __forceinline__ bool first_item(const AttendParams& p, Item& it, Walk
     return x;
   };
   long long at = 0;
-  if (p.nsplit > 1) {
+  const bool splits = M == BM && p.nsplit > 1;
+  if (splits) {
     long long total = 0;
     int most = 1;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
@@ -279,7 +351,7 @@ __device__ __forceinline__ bool first_item(const AttendParams& p, Item& it, Walk
       s = seq_of(p, b0 + lane);
       tiles = tiles_of<M>(p, s.n);
       wt = weight_of<M>(p, s);
-      x = p.nsplit > 1 ? (long long)tiles * p.Hkv * wt : tiles;
+      x = splits ? (long long)tiles * p.Hkv * wt : tiles;
     }
     const long long incl = before + scan(x);
     const unsigned hit = __ballot_sync(0xffffffffu, incl > at);
@@ -302,7 +374,7 @@ __device__ __forceinline__ bool first_item(const AttendParams& p, Item& it, Walk
 // The item at the walk's place; advances it.
 template <int M>
 __device__ __forceinline__ bool next_item(const AttendParams& p, Item& it, Walk& w) {
-  if (p.nsplit <= 1) {
+  if (M == 2 * BM || p.nsplit <= 1) {  // (two tiles are not split)
     if (w.tiles == 0) return false;
     it.g = blockIdx.x % p.Hkv;
     // a sequence's last tiles, the longest ones, first
@@ -408,10 +480,9 @@ struct Raw {
 };
 
 template <int D, int SRC>
-__device__ __forceinline__ void load_raw(const AttendParams& p, int g, int groups, bool is_v,
+__device__ __forceinline__ void load_raw(const AttendParams& p, int ct, int g, int groups, bool is_v,
                                          Raw<D, SRC>& r) {
   using R = Raw<D, SRC>;
-  const int ct = threadIdx.x - kSoftThreads;
 #pragma unroll
   for (int k = 0; k < R::kN; ++k) {
     const int q = ct + kProdThreads * k;
@@ -439,10 +510,9 @@ __device__ __forceinline__ void load_raw(const AttendParams& p, int g, int group
 
 // Into a stage, as fp16.  bits: where V's rows with a NaN are noted (nullptr: not looked at).
 template <int D, int SRC>
-__device__ __forceinline__ void store_raw(const Raw<D, SRC>& r, uint32_t dst, uint32_t* bits,
+__device__ __forceinline__ void store_raw(const Raw<D, SRC>& r, int ct, uint32_t dst, uint32_t* bits,
                                           volatile int* any) {
   using R = Raw<D, SRC>;
-  const int ct = threadIdx.x - kSoftThreads;
 #pragma unroll
   for (int k = 0; k < R::kN; ++k) {
     const int q = ct + kProdThreads * k;
@@ -506,6 +576,8 @@ struct Args {
   AttendParams p;
 };
 
+// Registers of a thread after the deal, which adds up to the 4 x 128 of the launch's four
+// warpgroups: 2 x 184 + 96 + 48 with two tiles, 2 x 144 + 176 + 48 with one.
 template <int D, int TILES, int SRC>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Args a) {
   using L = Layout<D, TILES>;
@@ -520,25 +592,33 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   float* rscale = reinterpret_cast<float*>(smem + L::kRowScale);
 
   grid_dependency_wait();  // inputs may come from the previous kernel of the stream
-  Item it;
+  const Item& it = *reinterpret_cast<const Item*>(smem + L::kItem);
+  Item* shared_item = reinterpret_cast<Item*>(smem + L::kItem);
   Walk walk;
-  if (!first_item<M>(p, it, walk)) return;
-
+  if (warp == kLastWarp) {
+    Item one;
+    const bool has = first_item<M>(p, one, walk) && next_item<M>(p, one, walk);
+    if (lane == 0) {
+      *shared_item = one;
+      slot[kHas] = has;
+    }
+  }
   if (warp == kMmaWarp) {
     tc::tmem_alloc(sbase + L::kSlots + 4 * kTmem, 512);
     tc::tmem_relinquish();
   }
   if (tid == 0) {
     for (int s = 0; s < S; ++s) {
-      tc::mbar_init(bar(kKFull + s), SRC == kF16 ? 1 : kProdThreads);
+      tc::mbar_init(bar(kKFull + s), SRC == kF16 ? 1 : kProdThreads / 32);
       tc::mbar_init(bar(kKFree + s), 1);
       tc::mbar_init(bar(kVFull + s), 1);
       tc::mbar_init(bar(kVFree + s), 1);
-      tc::mbar_init(bar(kVOk + s), kProdThreads);
+      tc::mbar_init(bar(kVOk + s), kProdThreads / 32);
     }
     for (int w = 0; w < 2; ++w) {
       tc::mbar_init(bar(kSFull + w), 1);
-      tc::mbar_init(bar(kPFull + w), TILES == 2 ? kSoftThreads / 2 : kSoftThreads);
+      tc::mbar_init(bar(kPFull + w), TILES == 2 ? 4 : 8);
+      tc::mbar_init(bar(kPHalf + w), 4);
       tc::mbar_init(bar(kPVDone + w), 1);
     }
     tc::mbar_init(bar(kDone), 1);
@@ -559,35 +639,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // -----------------------------------------------------------------------
     regs_up<TILES == 2 ? 184 : 144>();
     constexpr int COLS = TILES == 2 ? 128 : 64;  // positions of a block per thread
-    const int half = TILES == 2 ? 0 : warp >> 2;
-    const int tile = TILES == 2 ? warp >> 2 : 0;
+    const int half = TILES == 2 ? 0 : warp >> 2, tile = TILES == 2 ? warp >> 2 : 0;
     const int r = 32 * (warp & 3) + lane;  // the vector within its tile
     const uint32_t t_lane = (uint32_t)(32 * (warp & 3)) << 16;
     float* xchg = reinterpret_cast<float*>(smem + L::kXchg);
-    volatile int* votes = reinterpret_cast<volatile int*>(smem + L::kVote);
+    volatile int* votes = reinterpret_cast<volatile int*>(smem + L::kVote) + (warp & 3) * 2;
     auto pair_sync = [&]() {
       asm volatile("bar.sync %0, %1;\n" ::"r"(1 + (warp & 3)), "r"(64) : "memory");
     };
-    auto wait_all = [&](int b, uint32_t parity) -> bool {
-      return __all_sync(0xffffffffu, tc::mbar_wait(bar(b), parity, slot + kAbort));
+    // TILES == 1: the two warps of a lane quarter exchange a float each, and whether their waits succeeded: both
+    // go on only if both did.
+    auto exchange = [&](int buf, bool ok, float x, float& other) -> bool {
+      float* b = xchg + buf * 2 * BM;
+      b[half * BM + r] = x;
+      if (lane == 0) votes[8 * buf + half] = ok ? 1 : 0;
+      pair_sync();
+      other = b[(half ^ 1) * BM + r];
+      return votes[8 * buf] != 0 && votes[8 * buf + 1] != 0;
     };
-    // TILES == 1: the two warps of a lane quarter take the same branch after every wait
-    int nvote = 0;
-    auto agree = [&](bool ok) -> bool {
-      if constexpr (TILES == 2) {
-        return ok;
-      } else {
-        volatile int* v = votes + (nvote++ & 1) * 8 + (warp & 3) * 2;
-        if (lane == 0) v[half] = ok ? 1 : 0;
-        pair_sync();
-        return v[0] != 0 && v[1] != 0;
-      }
-    };
+    auto wait_all = [&](int b, uint32_t parity) -> bool { return warp_wait(bar(b), parity, slot + kAbort); };
     const float cap_k = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
     const bool folds = SRC != kF16 && p.per_channel;
     const float ks1 = SRC != kF16 && !p.per_channel ? __ldg(p.k_scale) : 1.f;
     int n = 0;  // blocks done by this CTA
-    while (next_item<M>(p, it, walk)) {
+    while (slot[kHas] != 0) {
       const int v0 = it.t * M, nvec = it.q.n * p.G;
       // ---- queries into shared memory ----
       {
@@ -677,119 +752,145 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // (a second tile without vectors is not worked on; with two tiles there is one item)
       const int nb = v0 + tile * BM < nvec ? it.blk1 - it.blk0 : 0;
       const bool warp_live = __any_sync(0xffffffffu, live && hi > lo);
+      const int blk0 = it.blk0, f0 = it.f0, f1 = it.f1;
       float m_run = neg_inf(), m_top = neg_inf(), l_run = 0.f;
       bool ok = true;
-      for (int i = 0; i < nb; ++i) {
-        const int blk = it.blk0 + i, nn = n + i;
+      // a warp without live rows takes part in the hand-overs only
+      for (int i = 0; !warp_live && i < nb; ++i) {
+        const int nn = n + i;
+        ok = wait_all(kSFull + (TILES == 2 ? tile : nn & 1), TILES == 2 ? nn & 1 : (nn >> 1) & 1) && ok;
+        if constexpr (TILES == 1) {
+          float none;
+          if (!(ok = exchange(nn & 1, ok, 0.f, none))) break;
+          ok = i == 0 || wait_all(kPVDone, (nn - 1) & 1);
+        } else {
+          if (!ok) break;
+          warp_arrive(bar(kPHalf + tile));
+        }
+        warp_arrive(bar(kPFull + tile));
+      }
+      for (int i = 0; warp_live && i < nb; ++i) {
+        const int blk = blk0 + i, nn = n + i;
         const int sb = TILES == 2 ? tile : nn & 1;
         const uint32_t par = TILES == 2 ? nn & 1 : (nn >> 1) & 1;
-        if (!(ok = agree(wait_all(kSFull + sb, par)))) break;
+        ok = wait_all(kSFull + sb, par) && ok;
+        if (TILES == 2 && !ok) break;
         tc::fence_after_sync();
-        if (warp_live) {
-          const uint32_t s_col = tbase + t_lane + sb * BN + 64 * half;
-          float s[COLS];
+        const uint32_t s_col = tbase + t_lane + sb * BN + 64 * half;
+        float s[COLS];
 #pragma unroll
-          for (int c = 0; c < COLS / 32; ++c) tc::tmem_ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
-          tc::tmem_wait_ld();
-          if (p.softcap > 0.f) {
+        for (int c = 0; c < COLS / 32; ++c) tc::tmem_ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
+        tc::tmem_wait_ld();
+        if (p.softcap > 0.f) {
 #pragma unroll
-            for (int j = 0; j < COLS; ++j) s[j] = soft_cap(s[j] * nat, p.softcap, cap_k);
-          }
-          if (it.partial(blk) || bad_pages) {
-            const int at = blk * BN + 64 * half;
+          for (int j = 0; j < COLS; ++j) s[j] = soft_cap(s[j] * nat, p.softcap, cap_k);
+        }
+        if (blk < f0 || blk >= f1 || bad_pages) {
+          const int at = blk * BN + 64 * half;
 #pragma unroll
-            for (int c = 0; c < COLS / 32; ++c) {
-              // positions [lo, hi) of these 32
-              const int a0 = min(max(lo - (at + 32 * c), 0), 32), a1 = min(max(hi - (at + 32 * c), 0), 32);
-              uint32_t w = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
-              if (bad_pages) {
-                if (group_of(p, it, at + 32 * c) < 0) w &= 0xffff0000u;
-                if (group_of(p, it, at + 32 * c + 16) < 0) w &= 0x0000ffffu;
-              }
-#pragma unroll
-              for (int j = 0; j < 32; ++j) s[32 * c + j] = (w >> j) & 1u ? s[32 * c + j] : neg_inf();
+          for (int c = 0; c < COLS / 32; ++c) {
+            // positions [lo, hi) of these 32
+            const int a0 = min(max(lo - (at + 32 * c), 0), 32), a1 = min(max(hi - (at + 32 * c), 0), 32);
+            uint32_t w = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
+            if (bad_pages) {
+              if (group_of(p, it, at + 32 * c) < 0) w &= 0xffff0000u;
+              if (group_of(p, it, at + 32 * c + 16) < 0) w &= 0x0000ffffu;
             }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) s[32 * c + j] = (w >> j) & 1u ? s[32 * c + j] : neg_inf();
           }
-          float mx4[4] = {neg_inf(), neg_inf(), neg_inf(), neg_inf()};
+        }
+        float top4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int j = 0; j < COLS; ++j) mx4[j & 3] = fmaxf(mx4[j & 3], s[j]);
-          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
-          if constexpr (TILES == 1) {
-            float* xb = xchg + (nn & 1) * 2 * BM;
-            xb[half * BM + r] = mx;
-            pair_sync();
-            mx = fmaxf(mx, xb[(half ^ 1) * BM + r]);
-          }
-          m_top = fmaxf(m_top, mx);
-          const bool moves = m_top * c2 > m_run * c2 + kLazy;  // (from -inf: any score does)
-          const float m_new = moves ? m_top : m_run;
-          const float base = m_new == neg_inf() ? 0.f : m_new * c2;
-          const float alpha = moves ? fast_exp2(m_run * c2 - base) : 1.f;
-          const float off = kShift - base;
-          float ps[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int j = 4; j < COLS; j += 8) {
 #pragma unroll
-          for (int c = 0; c < COLS / 64; ++c) {
-            uint32_t ph[32];
+          for (int e = 0; e < 4; ++e)
+            top4[e] = j + 4 < COLS ? max3(top4[e], s[j + e], s[j + 4 + e]) : fmaxf(top4[e], s[j + e]);
+        }
+        float mx = fmaxf(max3(top4[0], top4[1], top4[2]), top4[3]);
+        if constexpr (TILES == 1) {
+          float mx2;
+          if (!(ok = exchange(nn & 1, ok, mx, mx2))) break;
+          mx = fmaxf(mx, mx2);
+        }
+        m_top = fmaxf(m_top, mx);
+        const bool moves = m_top * c2 > m_run * c2 + kLazy;  // (from -inf: any score does)
+        const float m_new = moves ? m_top : m_run;
+        const float base = m_new == neg_inf() ? 0.f : m_new * c2;
+        const float alpha = moves ? fast_exp2(m_run * c2 - base) : 1.f;
+        const float off = kShift - base;
+        const uint64_t c22 = pair(c2, c2), off2 = pair(off, off);
+        uint64_t ps[2] = {0ull, 0ull};
+        // probabilities of 64 positions, over the scores' columns
+        auto probabilities = [&](int c0) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-              const float p0 = fast_exp2(fmaf(s[64 * c + 2 * j], c2, off));
-              const float p1 = fast_exp2(fmaf(s[64 * c + 2 * j + 1], c2, off));
-              ps[(2 * j) & 3] += p0;
-              ps[(2 * j + 1) & 3] += p1;
-              ph[j] = pack_h2(p0, p1);
+          for (int c = c0; c < c0 + 2; ++c) {
+            uint32_t ph[16];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+              float x, y;
+              unpair(fma2(pair(s[32 * c + 2 * j], s[32 * c + 2 * j + 1]), c22, off2), x, y);
+              x = fast_exp2(x);
+              y = fast_exp2(y);
+              ps[j & 1] = add2(ps[j & 1], pair(x, y));
+              ph[j] = pack_h2(x, y);
             }
-            tc::tmem_st32u(s_col + 64 * c, ph);
+            tc::tmem_st16u(s_col + 64 * (c >> 1) + 16 * (c & 1), ph);
           }
-          l_run = fmaf(l_run, alpha, (ps[0] + ps[1]) + (ps[2] + ps[3]));
-          const bool rescale = i > 0 && moves;
-          m_run = m_new;
-          // O is current: with two tiles QK(i) was issued after PV(i - 1) had completed
-          if constexpr (TILES == 1) {
-            if (!(ok = agree(i == 0 || wait_all(kPVDone, (nn - 1) & 1)))) break;
-            tc::fence_after_sync();
-          }
-          if (__any_sync(0xffffffffu, rescale)) {
-            constexpr int OC = TILES == 2 ? D : D / 2;  // channels of this thread
+        };
+        probabilities(0);
+        const bool rescale = i > 0 && moves;
+        m_run = m_new;
+        // O is current: with two tiles QK(i) was issued after PV(i - 1) had completed
+        if constexpr (TILES == 1) {
+          ok = i == 0 || wait_all(kPVDone, (nn - 1) & 1);
+          tc::fence_after_sync();
+        }
+        if (ok && __any_sync(0xffffffffu, rescale)) {
+          constexpr int OC = TILES == 2 ? D : D / 2;  // channels of this thread
 #pragma unroll 1
-            for (int c = 0; c < OC / 32; ++c) {
-              float o[32];
-              const uint32_t oc = tbase + t_lane + L::kOCol + tile * D + half * OC + 32 * c;
-              tc::tmem_ld32(oc, o);
-              tc::tmem_wait_ld();
+          for (int c = 0; c < OC / 32; ++c) {
+            float o[32];
+            const uint32_t oc = tbase + t_lane + L::kOCol + tile * D + half * OC + 32 * c;
+            tc::tmem_ld32(oc, o);
+            tc::tmem_wait_ld();
 #pragma unroll
-              for (int e = 0; e < 32; ++e) o[e] *= rescale ? alpha : 1.f;
-              tc::tmem_st32(oc, o);
-            }
+            for (int e = 0; e < 32; ++e) o[e] *= rescale ? alpha : 1.f;
+            tc::tmem_st32(oc, o);
           }
+        }
+        tc::tmem_wait_st();
+        tc::fence_before_sync();
+        if constexpr (TILES == 2) {
+          // the tensor cores take the first half while the second is made
+          warp_arrive(bar(kPHalf + tile));
+          probabilities(2);
           tc::tmem_wait_st();
           tc::fence_before_sync();
-        } else if constexpr (TILES == 1) {
-          if (!(ok = agree(i == 0 || wait_all(kPVDone, (nn - 1) & 1)))) break;
         }
-        tc::mbar_arrive(bar(kPFull + tile));
+        l_run = fmaf(l_run, alpha, sum4(ps));
+        warp_arrive(bar(kPFull + tile));
       }
       n += nb;
       // ---- epilogue ----
-      const int pv = TILES == 2 ? kPVDone + tile : kPVDone;
-      const bool done = ok && slot[kAbort] == 0;
-      ok = agree(__all_sync(0xffffffffu, done) && (nb == 0 || wait_all(pv, (n - 1) & 1)));
-      tc::fence_after_sync();
+      ok = ok && slot[kAbort] == 0 && (nb == 0 || wait_all(kPVDone + tile, (n - 1) & 1));
+      ok = __all_sync(0xffffffffu, ok);
       if constexpr (TILES == 1) {
-        float* lx = xchg + 4 * BM;
-        lx[half * BM + r] = l_run;
-        pair_sync();
-        l_run += lx[(half ^ 1) * BM + r];
+        float l_other;
+        ok = exchange(2, ok, l_run, l_other);
+        l_run += l_other;
       }
+      tc::fence_after_sync();
       const bool attends = live && max(lo, it.blk0 * BN) < min(hi, it.blk1 * BN);
       const bool some = attends && m_top != neg_inf();
       const bool nan = attends && l_run != l_run;
       const float lsum = l_run * 0.00390625f;  // 2^-kShift
       const float m_nat = m_run * c2 * kLn2;
-      constexpr int OC = TILES == 2 ? D : D / 2;
+      constexpr int OC = TILES == 2 ? D : D / 2;  // channels of this thread
       const int c_lo = half * OC;
       const float kNan = __int_as_float(0x7fc00000);
       const bool fix = slot[kAnyPoison] != 0;
-      if (p.nsplit > 1) {
+      if (TILES == 1 && p.nsplit > 1) {
         const long long u = ((it.q.s0 + (long long)tok) * p.Hkv + it.g) * p.nsplit + it.slot;
         const long long pvec = u * p.G + (h - it.g * p.G);
         float* acc = p.part_acc + pvec * D;
@@ -837,10 +938,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll 1
         for (int c = 0; c < OC / 32; ++c) {
           float o[32];
-          if (ok && nb > 0) {
-            tc::tmem_ld32(tbase + t_lane + L::kOCol + tile * D + c_lo + 32 * c, o);
-            tc::tmem_wait_ld();
-          }
+          tc::tmem_ld32(tbase + t_lane + L::kOCol + tile * D + c_lo + 32 * c, o);
+          tc::tmem_wait_ld();
           if (!live) continue;
           uint32_t w[16];
 #pragma unroll
@@ -879,18 +978,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // -----------------------------------------------------------------------
     // converters; of fp16 sources: the check of V blocks attended in part
     // -----------------------------------------------------------------------
-    // (shares add up to the 512 x 128 / 128 registers of the launch: 2 x 184 + 96 + 48, 2 x 144 + 176 + 48)
     if constexpr (TILES == 2) regs_down<96>(); else regs_up<176>();
     const int ct = tid - kSoftThreads;
     int n = 0;
-    while (next_item<M>(p, it, walk)) {
+    while (slot[kHas] != 0) {
       const int nb = it.blk1 - it.blk0;
       bool ok = true;
       if constexpr (SRC == kF16) {
         sync_all();
         for (int i = 0; i < nb; ++i) {
           const int nn = n + i, st = nn % S;
-          if (!(ok = tc::mbar_wait(bar(kVFull + st), (nn / S) & 1, slot + kAbort))) break;
+          if (!(ok = warp_wait(bar(kVFull + st), (nn / S) & 1, slot + kAbort))) break;
           const int blk = it.blk0 + i;
           if (it.partial(blk)) {
             const uint32_t at = sbase + L::kV + st * L::kKV;
@@ -908,7 +1006,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
             tc::fence_smem_to_async();
           }
-          tc::mbar_arrive(bar(kVOk + st));
+          warp_arrive(bar(kVOk + st));
         }
       } else {
         // K runs one block ahead of V; a block's codes are loaded while the one before is at work
@@ -918,41 +1016,41 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         };
         int g0 = groups_of(it.blk0), g1 = groups_of(it.blk0 + 1);
         if (nb > 0) {
-          load_raw<D, SRC>(p, it.g, g0, false, kr);
-          load_raw<D, SRC>(p, it.g, g0, true, vr);
+          load_raw<D, SRC>(p, ct, it.g, g0, false, kr);
+          load_raw<D, SRC>(p, ct, it.g, g0, true, vr);
         }
         sync_all();
         auto put_k = [&](int i) -> bool {
           const int nn = n + i, st = nn % S;
-          if (nn >= S && !tc::mbar_wait(bar(kKFree + st), ((nn / S) & 1) ^ 1, slot + kAbort)) return false;
-          store_raw<D, SRC>(kr, sbase + L::kK + st * L::kKV, nullptr, nullptr);
+          if (nn >= S && !warp_wait(bar(kKFree + st), ((nn / S) & 1) ^ 1, slot + kAbort)) return false;
+          store_raw<D, SRC>(kr, ct, sbase + L::kK + st * L::kKV, nullptr, nullptr);
           tc::fence_smem_to_async();
-          tc::mbar_arrive(bar(kKFull + st));
+          warp_arrive(bar(kKFull + st));
           return true;
         };
         auto put_v = [&](int i) -> bool {
           const int nn = n + i, st = nn % S;
-          if (nn >= S && !tc::mbar_wait(bar(kVFree + st), ((nn / S) & 1) ^ 1, slot + kAbort)) return false;
+          if (nn >= S && !warp_wait(bar(kVFree + st), ((nn / S) & 1) ^ 1, slot + kAbort)) return false;
           const int blk = it.blk0 + i;
-          store_raw<D, SRC>(vr, sbase + L::kV + st * L::kKV,
+          store_raw<D, SRC>(vr, ct, sbase + L::kV + st * L::kKV,
                             SRC != kI8 && it.partial(blk) ? poison + 4 * it.ordinal(blk) : nullptr,
                             slot + kAnyPoison);
           tc::fence_smem_to_async();
-          tc::mbar_arrive(bar(kVOk + st));
+          warp_arrive(bar(kVOk + st));
           return true;
         };
         if (nb > 0) {
-          ok = __all_sync(0xffffffffu, put_k(0));
-          if (ok) load_raw<D, SRC>(p, it.g, g1, false, kr);
+          ok = put_k(0);
+          if (ok) load_raw<D, SRC>(p, ct, it.g, g1, false, kr);
         }
         for (int i = 0; ok && i < nb; ++i) {
           const int g2 = groups_of(it.blk0 + i + 2);
           if (i + 1 < nb) {
-            if (!(ok = __all_sync(0xffffffffu, put_k(i + 1)))) break;
-            if (i + 2 < nb) load_raw<D, SRC>(p, it.g, g2, false, kr);
+            if (!(ok = put_k(i + 1))) break;
+            if (i + 2 < nb) load_raw<D, SRC>(p, ct, it.g, g2, false, kr);
           }
-          if (!(ok = __all_sync(0xffffffffu, put_v(i)))) break;
-          if (i + 1 < nb) load_raw<D, SRC>(p, it.g, g1, true, vr);
+          if (!(ok = put_v(i))) break;
+          if (i + 1 < nb) load_raw<D, SRC>(p, ct, it.g, g1, true, vr);
           g1 = g2;
         }
       }
@@ -970,35 +1068,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       // ---------------------------------------------------------------------
       constexpr uint32_t kIdQK = tc::idesc_f16(BM, BN, false, false);
       constexpr uint32_t kIdPV = tc::idesc_f16(BM, D, false, true);
+      const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tbase, 0);
       int n = 0, items = 0;
-      while (next_item<M>(p, it, walk)) {
-        const int nb = it.blk1 - it.blk0;
-        const int tiles = min(TILES, (it.q.n * p.G - it.t * M + BM - 1) / BM);  // with live vectors
+      while (slot[kHas] != 0) {
+        const int nb = __shfl_sync(0xffffffffu, it.blk1 - it.blk0, 0);
+        const int tiles = __shfl_sync(0xffffffffu, min(TILES, (it.q.n * p.G - it.t * M + BM - 1) / BM), 0);  // with live vectors
         sync_all();
         tc::fence_after_sync();
-        if (lane == 0) {
+        {
+          const uint64_t qd = tc::smem_desc_sw128(sbase + L::kQ, 1024);
+          const uint64_t kd = tc::smem_desc_sw128(sbase + L::kK, 1024);
+          const uint64_t vd = desc_mn_sw128(sbase + L::kV, L::kSlab);
           auto qk = [&](int w, int nn) {  // scores of tile w (or into buffer nn & 1)
-            const uint32_t qs = sbase + L::kQ + w * L::kSlabs * L::kSlab;
-            const uint32_t ks = sbase + L::kK + (nn % S) * L::kKV;
+            const uint64_t qs = qd + w * (L::kSlabs * L::kSlab >> 4);
+            const uint64_t ks = kd + (nn % S) * (L::kKV >> 4);
             const int buf = TILES == 2 ? w : nn & 1;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t at = (kk >> 2) * L::kSlab + (kk & 3) * 32;
-              tc::mma_f16(tbase + buf * BN, tc::smem_desc_sw128(qs + at, 1024),
-                          tc::smem_desc_sw128(ks + at, 1024), kIdQK, kk > 0);
+              const uint32_t at = ((kk >> 2) * L::kSlab + (kk & 3) * 32) >> 4;
+              mma_ss(lead, tm + buf * BN, qs + at, ks + at, kIdQK, kk > 0);
             }
-            tc::mma_commit(bar(kSFull + buf));
+            commit(lead, bar(kSFull + buf));
           };
-          auto pv = [&](int w, int nn, bool first) {
-            const uint32_t vs = sbase + L::kV + (nn % S) * L::kKV;
+          auto pv = [&](int w, int nn, bool first, int k0, int k1) {
+            const uint64_t vs = vd + (nn % S) * (L::kKV >> 4);
             const int buf = TILES == 2 ? w : nn & 1;
 #pragma unroll
-            for (int kk = 0; kk < BN / 16; ++kk)
-              tc::mma_f16_ts(tbase + L::kOCol + w * D, tbase + buf * BN + 64 * (kk >> 2) + 8 * (kk & 3),
-                             desc_mn_sw128(vs + kk * 2048, L::kSlab), kIdPV, !first || kk > 0);
-            tc::mma_commit(bar(kPVDone + w));
+            for (int kk = k0; kk < k1; ++kk)
+              mma_ts(lead, tm + L::kOCol + w * D, tm + buf * BN + 64 * (kk >> 2) + 8 * (kk & 3),
+                               vs + kk * (2048 >> 4), kIdPV, !first || kk > 0);
           };
-          auto wait = [&](int b, uint32_t par) -> bool { return tc::mbar_wait(bar(b), par, slot + kAbort); };
+          auto wait = [&](int b, uint32_t par) -> bool {
+            return warp_wait(bar(b), par, slot + kAbort);
+          };
           bool ok = true;
           if constexpr (TILES == 2) {
             for (int i = -1; ok && i < nb; ++i) {
@@ -1006,11 +1108,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               const bool more = i + 1 < nb;
               for (int w = 0; ok && w < tiles; ++w) {
                 if (i >= 0) {
-                  ok = wait(kPFull + w, nn & 1) && (w > 0 || wait(kVOk + nn % S, (nn / S) & 1));
+                  ok = (w > 0 || wait(kVOk + nn % S, (nn / S) & 1)) && wait(kPHalf + w, nn & 1);
                   if (!ok) break;
                   tc::fence_after_sync();
-                  pv(w, nn, i == 0);
-                  if (w == tiles - 1) tc::mma_commit(bar(kVFree + nn % S));
+                  pv(w, nn, i == 0, 0, 4);
+                  if (!(ok = wait(kPFull + w, nn & 1))) break;
+                  tc::fence_after_sync();
+                  pv(w, nn, i == 0, 4, 8);
+                  commit(lead, bar(kPVDone + w));
+                  if (w == tiles - 1) commit(lead, bar(kVFree + nn % S));
                 }
                 if (more) {
                   // the scores go over P(i): PV(i) must have read it
@@ -1018,7 +1124,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                   if (!ok) break;
                   tc::fence_after_sync();
                   qk(w, nx);
-                  if (w == tiles - 1) tc::mma_commit(bar(kKFree + nx % S));
+                  if (w == tiles - 1) commit(lead, bar(kKFree + nx % S));
                 }
               }
             }
@@ -1032,20 +1138,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                 if (!ok) break;
                 tc::fence_after_sync();
                 qk(0, nn);
-                tc::mma_commit(bar(kKFree + nn % S));
+                commit(lead, bar(kKFree + nn % S));
               }
               if (i > 0) {
                 ok = wait(kPFull, pr & 1) && wait(kVOk + pr % S, (pr / S) & 1);
                 if (!ok) break;
                 tc::fence_after_sync();
-                pv(0, pr, i == 1);
-                tc::mma_commit(bar(kVFree + pr % S));
+                pv(0, pr, i == 1, 0, 8);
+                commit(lead, bar(kPVDone));
+                commit(lead, bar(kVFree + pr % S));
               }
             }
           }
           if (!ok) slot[kAbort] = 1;
           // everything issued has completed before the item ends
-          tc::mma_commit(bar(kDone));
+          commit(lead, bar(kDone));
           if (!tc::mbar_wait(bar(kDone), items & 1)) slot[kAbort] = 1;
         }
         __syncwarp();
@@ -1055,14 +1162,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (slot[kAbort] != 0) break;
         sync_all();
       }
+    } else if (warp == kLastWarp) {
+      // ---------------------------------------------------------------------
+      // the items
+      // ---------------------------------------------------------------------
+      if (blockIdx.x == 0)  // lengths and starts that had to be clamped
+        for (int b = lane; b < p.B; b += 32) seq_of(p, b, true);
+      Item one = it;
+      while (slot[kHas] != 0) {
+        sync_all();
+        const bool has = next_item<M>(p, one, walk);
+        sync_all();
+        if (slot[kAbort] != 0) break;
+        if (lane == 0) {
+          *shared_item = one;
+          slot[kHas] = has;
+        }
+        sync_all();
+      }
     } else {
       // ---------------------------------------------------------------------
       // fp16 sources: copies
       // ---------------------------------------------------------------------
-      if (blockIdx.x == 0 && warp == kThreads / 32 - 1)  // lengths and starts that had to be clamped
-        for (int b = lane; b < p.B; b += 32) seq_of(p, b, true);
       int n = 0;
-      while (next_item<M>(p, it, walk)) {
+      while (slot[kHas] != 0) {
         const int nb = it.blk1 - it.blk0;
         sync_all();
         if (SRC == kF16 && warp == kTmaWarp) {
@@ -1089,7 +1212,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                       is_v ? &a.vm : &a.km, 64 * box_slab, it.g, row, bar(b));
           };
           auto free = [&](int b, int nn) -> bool {
-            return __all_sync(0xffffffffu, nn < S || tc::mbar_wait(bar(b + nn % S), ((nn / S) & 1) ^ 1, slot + kAbort));
+            return nn < S || warp_wait(bar(b + nn % S), ((nn / S) & 1) ^ 1, slot + kAbort);
           };
           int r0 = row_of(it.blk0), r1 = row_of(it.blk0 + 1);
           if (nb > 0) {
