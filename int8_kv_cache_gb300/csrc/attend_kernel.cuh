@@ -82,11 +82,17 @@ struct Layout {
   static constexpr int kSlab = 128 * 128;  // 64 channels of 128 rows
   static constexpr int kQ = 0;
   static constexpr int kQBytes = kM * D * 2;
-  static constexpr int kKV = BN * D * 2;
-  static constexpr int kStages = D == 256 ? 1 : D == 128 ? 2 : 3;
+  // K and V come in parts, each with barriers of its own: a block, or, where shared memory holds one
+  // block only (head_dim 256), half of one, so that a half is filled anew while the products of the
+  // other are at work: of K half the channels, of V half the positions
+  static constexpr int kParts = D == 256 ? 2 : 1;
+  static constexpr int kPart = BN * D * 2 / kParts;
+  static constexpr int kKSlabs = kSlabs / kParts;
+  static constexpr int kVRows = BN / kParts;
+  static constexpr int kRing = D == 64 ? 4 : 2;  // places for parts
   static constexpr int kK = kQ + kQBytes;
-  static constexpr int kV = kK + kStages * kKV;
-  static constexpr int kBars = kV + kStages * kKV;
+  static constexpr int kV = kK + kRing * kPart;
+  static constexpr int kBars = kV + kRing * kPart;
   static constexpr int kSlots = kBars + 256;
   static constexpr int kItem = kSlots + 64;
   static constexpr int kPois = kItem + 128;              // [kPoison][4] bits of positions
@@ -99,7 +105,8 @@ struct Layout {
   static_assert(kBytes <= 227 * 1024, "shared memory");
 };
 
-// barriers (8 bytes each); s: the stage, w: the tile (or, TILES == 1, the score buffer)
+// barriers (8 bytes each); the first five by a part's place, the others by tile (or, TILES == 1, by
+// score buffer)
 enum Bar { kKFull = 0, kKFree = 4, kVFull = 8, kVFree = 12, kVOk = 16, kSFull = 20, kPFull = 22, kPVDone = 24, kPHalf = 26, kDone = 28, kNumBars = 29 };
 enum Slot { kTmem, kAbort, kBadPage, kAnyPoison, kHas, kNumSlots };
 static_assert(kNumBars * 8 <= 256 && kNumSlots * 4 <= 64, "misc");
@@ -157,7 +164,8 @@ __device__ __forceinline__ void warp_arrive(uint32_t bar) {
 }
 
 // The MMA warp works converged, so that descriptors and addresses stay in uniform registers (one
-// lane alone took 75 to 130 cycles to form and issue an instruction of 64); its elected lane issues.
+// lane alone took 75 to 130 cycles to form and issue an instruction of 64); the lane that issues is
+// elected once (at each group of four instructions: 2665 us against 1520 for a prompt of 16384).
 __device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
@@ -468,55 +476,72 @@ __device__ __noinline__ void add_poison(const AttendParams& p, const Item& it, c
 // producers of a quantised cache
 // ---------------------------------------------------------------------------
 
-// Raw codes of one block of K or V, as thread ct of the producers holds them: pieces of 16 bytes,
-// piece k of row (ct + 128 k) / kPer.
+// The codes of one part as thread ct of the producers holds them: pieces of 16 bytes, piece k =
+// number ct + 128 k of the part's (slab of 64 channels, row, place in the slab's row).  Neighbouring lanes
+// are in one row and in neighbouring ones, so loads take whole sectors and the stores of a quarter
+// of a warp meet every bank once.
 template <int D, int SRC>
 struct Raw {
-  static constexpr int kVals = SRC == kMx4 ? 32 : 16;  // values of a piece
-  static constexpr int kPer = D / kVals;               // pieces of a row
-  static constexpr int kN = BN * kPer / kProdThreads;  // pieces of a thread
+  static constexpr int kVals = SRC == kMx4 ? 32 : 16;     // values of a piece
+  static constexpr int kPer = 64 / kVals;                 // pieces of a slab's row
+  static constexpr int kN = Layout<D, 1>::kPart / 2 / kVals / kProdThreads;  // pieces of a thread
   uint4 x[kN];
   uint16_t s[SRC == kMx4 ? kN : 1];  // MX4: the two block scales
 };
+// Where piece k of a thread is: its row in the part, slab in the part, place in the slab's row.
+template <int SRC>
+__device__ __forceinline__ void place_of(int ct, int k, int rows, int& row, int& slab, int& c) {
+  constexpr int kPer = Raw<64, SRC>::kPer;
+  const int q = ct + kProdThreads * k;
+  c = q % kPer;
+  row = (q / kPer) % rows;
+  slab = q / (kPer * rows);
+}
 
+// groups: lane i (mod 8) holds the 16-row group i of the block.  part: of K or V.
 template <int D, int SRC>
 __device__ __forceinline__ void load_raw(const AttendParams& p, int ct, int g, int groups, bool is_v,
-                                         Raw<D, SRC>& r) {
+                                         int part, Raw<D, SRC>& r) {
   using R = Raw<D, SRC>;
+  using L = Layout<D, 1>;
 #pragma unroll
   for (int k = 0; k < R::kN; ++k) {
-    const int q = ct + kProdThreads * k;
-    const int row = q / R::kPer, c = q % R::kPer;
+    int row, slab, c;
+    place_of<SRC>(ct, k, is_v ? L::kVRows : BN, row, slab, c);
+    if (is_v) row += part * L::kVRows; else slab += part * L::kKSlabs;
     const int grp = __shfl_sync(0xffffffffu, groups, row >> 4);
+    const int at = slab * R::kPer + c;  // piece of the whole row
     r.x[k] = make_uint4(0u, 0u, 0u, 0u);
     if constexpr (SRC == kMx4) r.s[k] = 0;
     if (grp >= 0) {
-    if constexpr (SRC == kMx4) {
-      const int tiles = p.bs >> 4;
-      const int blk = p.bs_log2 >= 0 ? grp >> (p.bs_log2 - 4) : grp / tiles;
-      const uint8_t* rec = reinterpret_cast<const uint8_t*>(p.k) +
-                           (((long long)blk * p.Hkv + g) * tiles + (grp - blk * tiles)) * (18LL * D) +
-                           (is_v ? 9 * D : 0);
-      r.x[k] = __ldg(reinterpret_cast<const uint4*>(rec + (row & 15) * (D / 2)) + c);
-      r.s[k] = __ldg(reinterpret_cast<const uint16_t*>(rec + 8 * D + (row & 15) * (D / 16)) + c);
-    } else {
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(is_v ? p.v : p.k) +
-                           (((long long)grp * 16 + (row & 15)) * p.Hkv + g) * D;
-      r.x[k] = __ldg(reinterpret_cast<const uint4*>(src) + c);
-    }
+      if constexpr (SRC == kMx4) {
+        const int tiles = p.bs >> 4;
+        const int blk = p.bs_log2 >= 0 ? grp >> (p.bs_log2 - 4) : grp / tiles;
+        const uint8_t* rec = reinterpret_cast<const uint8_t*>(p.k) +
+                             (((long long)blk * p.Hkv + g) * tiles + (grp - blk * tiles)) * (18LL * D) +
+                             (is_v ? 9 * D : 0);
+        r.x[k] = __ldg(reinterpret_cast<const uint4*>(rec + (row & 15) * (D / 2)) + at);
+        r.s[k] = __ldg(reinterpret_cast<const uint16_t*>(rec + 8 * D + (row & 15) * (D / 16)) + at);
+      } else {
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(is_v ? p.v : p.k) +
+                             (((long long)grp * 16 + (row & 15)) * p.Hkv + g) * D;
+        r.x[k] = __ldg(reinterpret_cast<const uint4*>(src) + at);
+      }
     }
   }
 }
 
-// Into a stage, as fp16.  bits: where V's rows with a NaN are noted (nullptr: not looked at).
+// Into a part's place, as fp16.  bits: where rows (of the block, from row0) with a NaN are noted
+// (nullptr: not looked at).
 template <int D, int SRC>
-__device__ __forceinline__ void store_raw(const Raw<D, SRC>& r, int ct, uint32_t dst, uint32_t* bits,
-                                          volatile int* any) {
+__device__ __forceinline__ void store_raw(const Raw<D, SRC>& r, int ct, uint32_t dst, bool is_v, uint32_t* bits,
+                                          int row0, volatile int* any) {
   using R = Raw<D, SRC>;
+  const int rows = is_v ? Layout<D, 1>::kVRows : BN;
 #pragma unroll
   for (int k = 0; k < R::kN; ++k) {
-    const int q = ct + kProdThreads * k;
-    const int row = q / R::kPer, c = q % R::kPer;
+    int row, slab, c;
+    place_of<SRC>(ct, k, rows, row, slab, c);
     constexpr int kChunks = R::kVals / 8;
     uint4 h[kChunks];
     if constexpr (SRC == kI8) {
@@ -552,18 +577,13 @@ __device__ __forceinline__ void store_raw(const Raw<D, SRC>& r, int ct, uint32_t
 #pragma unroll
       for (int j = 0; j < kChunks; ++j) bad |= finite_only(h[j]);
       if (bad) {
-        atomicOr(bits + (row >> 5), 1u << (row & 31));
+        atomicOr(bits + ((row0 + row) >> 5), 1u << ((row0 + row) & 31));
         *any = 1;
       }
     }
-    // chunk j of the row; the lanes of one row in turn from both ends of their pieces, so that the
-    // slabs' rows, which share banks, do not meet
+    const uint32_t line = dst + (slab * rows + row) * 128;
 #pragma unroll
-    for (int j = 0; j < kChunks; ++j) {
-      const int ch = c * kChunks + j;
-      const uint32_t at = dst + (ch >> 3) * (128 * 128) + row * 128 + (((ch & 7) ^ (row & 7)) << 4);
-      sts16(at, h[j]);
-    }
+    for (int j = 0; j < kChunks; ++j) sts16(line + (((c * kChunks + j) ^ (row & 7)) << 4), h[j]);
   }
 }
 
@@ -572,7 +592,7 @@ __device__ __forceinline__ void store_raw(const Raw<D, SRC>& r, int ct, uint32_t
 // ---------------------------------------------------------------------------
 
 struct Args {
-  CUtensorMap km, vm;  // fp16 sources: [rows, Hkv, D], box 128 (packed) or 16 (pages) x 1 x 64
+  CUtensorMap km, vm;  // fp16 sources: [rows, Hkv, D]; boxes of 64 channels of a part's rows (packed) or 16 (pages)
   AttendParams p;
 };
 
@@ -581,7 +601,7 @@ struct Args {
 template <int D, int TILES, int SRC>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Args a) {
   using L = Layout<D, TILES>;
-  constexpr int M = L::kM, S = L::kStages;
+  constexpr int M = L::kM, P = L::kParts, N = L::kRing;
   const AttendParams& p = a.p;
   extern __shared__ __align__(1024) uint8_t smem[];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -608,7 +628,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     tc::tmem_relinquish();
   }
   if (tid == 0) {
-    for (int s = 0; s < S; ++s) {
+    for (int s = 0; s < N; ++s) {
       tc::mbar_init(bar(kKFull + s), SRC == kF16 ? 1 : kProdThreads / 32);
       tc::mbar_init(bar(kKFree + s), 1);
       tc::mbar_init(bar(kVFull + s), 1);
@@ -632,6 +652,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   sync_all();
   tc::fence_after_sync();
   const uint32_t tbase = static_cast<uint32_t>(slot[kTmem]);
+  // part j of the CTA's block nn, of K and V alike: its place, and the parity of its filling (a place
+  // is free for it after the filling before: the other parity; the first ones need not wait)
+  auto spot = [](int nn, int j) -> int { return (nn * P + j) % N; };
+  auto turn = [](int nn, int j) -> uint32_t { return ((nn * P + j) / N) & 1; };
 
   if (warp < kSoftThreads / 32) {
     // -----------------------------------------------------------------------
@@ -986,72 +1010,74 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       bool ok = true;
       if constexpr (SRC == kF16) {
         sync_all();
-        for (int i = 0; i < nb; ++i) {
-          const int nn = n + i, st = nn % S;
-          if (!(ok = warp_wait(bar(kVFull + st), (nn / S) & 1, slot + kAbort))) break;
-          const int blk = it.blk0 + i;
-          if (it.partial(blk)) {
-            const uint32_t at = sbase + L::kV + st * L::kKV;
-            uint32_t* bits = poison + 4 * it.ordinal(blk);
+        for (int i = 0; ok && i < nb; ++i) {
+          const int nn = n + i, blk = it.blk0 + i;
+          const bool partial = it.partial(blk);
+          uint32_t* bits = poison + 4 * it.ordinal(blk);
+          for (int j = 0; j < P; ++j) {
+            const int at = spot(nn, j);
+            if (!(ok = warp_wait(bar(kVFull + at), turn(nn, j), slot + kAbort))) break;
+            if (partial) {
+              const uint32_t v = sbase + L::kV + at * L::kPart;
 #pragma unroll 4
-            for (int k = 0; k < L::kKV / 16 / kProdThreads; ++k) {
-              const int q = ct + kProdThreads * k;
-              uint4 x = lds16(at + 16 * q);
-              if (finite_only(x)) {
-                sts16(at + 16 * q, x);
-                const int row = (q >> 3) & 127;
-                atomicOr(bits + (row >> 5), 1u << (row & 31));
-                slot[kAnyPoison] = 1;
+              for (int k = 0; k < L::kPart / 16 / kProdThreads; ++k) {
+                const int q = ct + kProdThreads * k;
+                uint4 x = lds16(v + 16 * q);
+                if (finite_only(x)) {
+                  sts16(v + 16 * q, x);
+                  const int row = j * L::kVRows + (q >> 3) % L::kVRows;
+                  atomicOr(bits + (row >> 5), 1u << (row & 31));
+                  slot[kAnyPoison] = 1;
+                }
               }
+              tc::fence_smem_to_async();
             }
-            tc::fence_smem_to_async();
+            warp_arrive(bar(kVOk + at));
           }
-          warp_arrive(bar(kVOk + st));
         }
       } else {
-        // K runs one block ahead of V; a block's codes are loaded while the one before is at work
-        Raw<D, SRC> kr, vr;
+        // K runs one block ahead of V; codes are loaded a block before they are stored
+        constexpr int kAhead = P;  // parts of K, and of V
+        Raw<D, SRC> kr[kAhead], vr[kAhead];
         auto groups_of = [&](int blk) -> int {
           return blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
         };
-        int g0 = groups_of(it.blk0), g1 = groups_of(it.blk0 + 1);
-        if (nb > 0) {
-          load_raw<D, SRC>(p, ct, it.g, g0, false, kr);
-          load_raw<D, SRC>(p, ct, it.g, g0, true, vr);
-        }
+        // groups of the blocks that K (and V, a block behind) load from now, and of the next
+        int gk = groups_of(it.blk0), gk1 = groups_of(it.blk0 + 1), gv = gk;
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) load_raw<D, SRC>(p, ct, it.g, gk, false, j, kr[j]);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) load_raw<D, SRC>(p, ct, it.g, gv, true, j, vr[j]);
         sync_all();
-        auto put_k = [&](int i) -> bool {
-          const int nn = n + i, st = nn % S;
-          if (nn >= S && !warp_wait(bar(kKFree + st), ((nn / S) & 1) ^ 1, slot + kAbort)) return false;
-          store_raw<D, SRC>(kr, ct, sbase + L::kK + st * L::kKV, nullptr, nullptr);
-          tc::fence_smem_to_async();
-          warp_arrive(bar(kKFull + st));
-          return true;
-        };
-        auto put_v = [&](int i) -> bool {
-          const int nn = n + i, st = nn % S;
-          if (nn >= S && !warp_wait(bar(kVFree + st), ((nn / S) & 1) ^ 1, slot + kAbort)) return false;
+        // stores part j of block i, then loads the part kAhead further on
+        auto put = [&](int i, int j, bool is_v, Raw<D, SRC>& r, int now, int next) -> bool {
+          const int nn = n + i, at = spot(nn, j);
+          if (nn * P + j >= N && !warp_wait(bar((is_v ? kVFree : kKFree) + at), turn(nn, j) ^ 1, slot + kAbort))
+            return false;
           const int blk = it.blk0 + i;
-          store_raw<D, SRC>(vr, ct, sbase + L::kV + st * L::kKV,
-                            SRC != kI8 && it.partial(blk) ? poison + 4 * it.ordinal(blk) : nullptr,
-                            slot + kAnyPoison);
+          store_raw<D, SRC>(r, ct, sbase + (is_v ? L::kV : L::kK) + at * L::kPart, is_v,
+                            SRC != kI8 && is_v && it.partial(blk) ? poison + 4 * it.ordinal(blk) : nullptr,
+                            j * L::kVRows, slot + kAnyPoison);
           tc::fence_smem_to_async();
-          warp_arrive(bar(kVOk + st));
+          warp_arrive(bar((is_v ? kVOk : kKFull) + at));
+          const int f = j + kAhead;
+          load_raw<D, SRC>(p, ct, it.g, f < P ? now : next, is_v, f % P, r);
           return true;
         };
-        if (nb > 0) {
-          ok = put_k(0);
-          if (ok) load_raw<D, SRC>(p, ct, it.g, g1, false, kr);
-        }
-        for (int i = 0; ok && i < nb; ++i) {
-          const int g2 = groups_of(it.blk0 + i + 2);
-          if (i + 1 < nb) {
-            if (!(ok = put_k(i + 1))) break;
-            if (i + 2 < nb) load_raw<D, SRC>(p, ct, it.g, g2, false, kr);
+        for (int i = -1; ok && i < nb; ++i) {
+          const int gk2 = groups_of(it.blk0 + i + 3);  // (a block before it is loaded from)
+#pragma unroll
+          for (int j = 0; j < P; ++j)
+            if (ok && i + 1 < nb) ok = put(i + 1, j, false, kr[j % kAhead], gk, gk1);
+          if (i >= 0) {
+            const int gv1 = gk;  // of block i + 1
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+              if (ok) ok = put(i, j, true, vr[j % kAhead], gv, gv1);
+            gv = gv1;
           }
-          if (!(ok = put_v(i))) break;
-          if (i + 1 < nb) load_raw<D, SRC>(p, ct, it.g, g1, true, vr);
-          g1 = g2;
+          gk = gk1;
+          gk1 = gk2;
         }
       }
       n += nb;
@@ -1078,76 +1104,79 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         {
           const uint64_t qd = tc::smem_desc_sw128(sbase + L::kQ, 1024);
           const uint64_t kd = tc::smem_desc_sw128(sbase + L::kK, 1024);
-          const uint64_t vd = desc_mn_sw128(sbase + L::kV, L::kSlab);
-          auto qk = [&](int w, int nn) {  // scores of tile w (or into buffer nn & 1)
+          const uint64_t vd = desc_mn_sw128(sbase + L::kV, L::kVRows * 128);
+          auto wait = [&](int b, uint32_t par) -> bool { return warp_wait(bar(b), par, slot + kAbort); };
+          // scores of tile w (or into buffer nn & 1); the first tile waits for the parts, the last frees them
+          auto qk = [&](int w, int nn) -> bool {
             const uint64_t qs = qd + w * (L::kSlabs * L::kSlab >> 4);
-            const uint64_t ks = kd + (nn % S) * (L::kKV >> 4);
             const int buf = TILES == 2 ? w : nn & 1;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const uint32_t at = ((kk >> 2) * L::kSlab + (kk & 3) * 32) >> 4;
-              mma_ss(lead, tm + buf * BN, qs + at, ks + at, kIdQK, kk > 0);
+            for (int j = 0; j < P; ++j) {
+              const int at = spot(nn, j);
+              if (w == 0) {
+                if (!wait(kKFull + at, turn(nn, j))) return false;
+                tc::fence_after_sync();
+              }
+              const uint64_t ks = kd + at * (L::kPart >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4 * L::kKSlabs; ++kk) {
+                const int in_slab = (kk >> 2) * L::kSlab + (kk & 3) * 32;
+                mma_ss(lead, tm + buf * BN, qs + ((j * L::kKSlabs * L::kSlab + in_slab) >> 4), ks + (in_slab >> 4), kIdQK,
+                       j > 0 || kk > 0);
+              }
+              if (w == tiles - 1) commit(lead, bar(kKFree + at));
             }
             commit(lead, bar(kSFull + buf));
+            return true;
           };
-          auto pv = [&](int w, int nn, bool first, int k0, int k1) {
-            const uint64_t vs = vd + (nn % S) * (L::kKV >> 4);
+          // O of tile w; P in two halves with two tiles
+          auto pv = [&](int w, int nn, bool first) -> bool {
             const int buf = TILES == 2 ? w : nn & 1;
+            constexpr int kSteps = 8 / P;  // of 16 positions in a part
 #pragma unroll
-            for (int kk = k0; kk < k1; ++kk)
-              mma_ts(lead, tm + L::kOCol + w * D, tm + buf * BN + 64 * (kk >> 2) + 8 * (kk & 3),
-                               vs + kk * (2048 >> 4), kIdPV, !first || kk > 0);
-          };
-          auto wait = [&](int b, uint32_t par) -> bool {
-            return warp_wait(bar(b), par, slot + kAbort);
+            for (int j = 0; j < P; ++j) {
+              const int at = spot(nn, j);
+              const uint64_t vs = vd + at * (L::kPart >> 4);
+              if (w == 0 && !wait(kVOk + at, turn(nn, j))) return false;
+#pragma unroll
+              for (int k = 0; k < kSteps; ++k) {
+                const int kk = j * kSteps + k;
+                if (kk == 0 || (TILES == 2 && kk == 4))
+                  if (!wait((TILES == 2 && kk == 0 ? kPHalf : kPFull) + w, nn & 1)) return false;
+                if (k == 0 || (TILES == 2 && kk == 4)) tc::fence_after_sync();
+                mma_ts(lead, tm + L::kOCol + w * D, tm + buf * BN + 64 * (kk >> 2) + 8 * (kk & 3),
+                       vs + (k * 2048 >> 4), kIdPV, !first || kk > 0);
+              }
+              if (w == tiles - 1) commit(lead, bar(kVFree + at));
+            }
+            commit(lead, bar(kPVDone + w));
+            return true;
           };
           bool ok = true;
           if constexpr (TILES == 2) {
             for (int i = -1; ok && i < nb; ++i) {
-              const int nn = n + i, nx = nn + 1;
-              const bool more = i + 1 < nb;
+              const int nn = n + i;
               for (int w = 0; ok && w < tiles; ++w) {
-                if (i >= 0) {
-                  ok = (w > 0 || wait(kVOk + nn % S, (nn / S) & 1)) && wait(kPHalf + w, nn & 1);
-                  if (!ok) break;
-                  tc::fence_after_sync();
-                  pv(w, nn, i == 0, 0, 4);
-                  if (!(ok = wait(kPFull + w, nn & 1))) break;
-                  tc::fence_after_sync();
-                  pv(w, nn, i == 0, 4, 8);
-                  commit(lead, bar(kPVDone + w));
-                  if (w == tiles - 1) commit(lead, bar(kVFree + nn % S));
-                }
-                if (more) {
+                if (i >= 0 && !(ok = pv(w, nn, i == 0))) break;
+                if (i + 1 < nb) {
                   // the scores go over P(i): PV(i) must have read it
-                  ok = (w > 0 || wait(kKFull + nx % S, (nx / S) & 1)) && (i < 0 || wait(kPVDone + w, nn & 1));
-                  if (!ok) break;
+                  if (i >= 0 && !(ok = wait(kPVDone + w, nn & 1))) break;
                   tc::fence_after_sync();
-                  qk(w, nx);
-                  if (w == tiles - 1) commit(lead, bar(kKFree + nx % S));
+                  ok = qk(w, nn + 1);
                 }
               }
             }
           } else {
             // QK(0), QK(1), PV(0), QK(2), PV(1), ...
             for (int i = 0; ok && i <= nb; ++i) {
-              const int nn = n + i, pr = nn - 1;
+              const int nn = n + i;
               if (i < nb) {
                 // S(i) goes over P(i - 2)
-                ok = wait(kKFull + nn % S, (nn / S) & 1) && (i < 2 || wait(kPVDone, nn & 1));
-                if (!ok) break;
+                if (i >= 2 && !(ok = wait(kPVDone, nn & 1))) break;
                 tc::fence_after_sync();
-                qk(0, nn);
-                commit(lead, bar(kKFree + nn % S));
+                if (!(ok = qk(0, nn))) break;
               }
-              if (i > 0) {
-                ok = wait(kPFull, pr & 1) && wait(kVOk + pr % S, (pr / S) & 1);
-                if (!ok) break;
-                tc::fence_after_sync();
-                pv(0, pr, i == 1, 0, 8);
-                commit(lead, bar(kPVDone));
-                commit(lead, bar(kVFree + pr % S));
-              }
+              if (i > 0) ok = pv(0, nn - 1, i == 1);
             }
           }
           if (!ok) slot[kAbort] = 1;
@@ -1190,52 +1219,62 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         sync_all();
         if (SRC == kF16 && warp == kTmaWarp) {
           bool ok = true;
-          int nk = 0, nv = 0;  // copies begun
+          int nk = 0, nv = 0;  // parts begun
           const bool paged = p.table != nullptr;
-          // lane: one box (a packed prompt's of 128 rows: the slab; a page's: group and slab)
-          const int box_slab = paged ? lane >> 3 : lane;
-          const int rows_of_box = paged ? 16 : 128;
-          const bool mine = box_slab < L::kSlabs;
-          auto row_of = [&](int blk) -> int {
-            if (!mine || blk >= it.blk1) return 0;
-            if (!paged) return it.q.s0 + blk * BN;
-            const int grp = group_of(p, it, blk * BN + 16 * (lane & 7));
+          // pages: boxes of 16 rows, a lane each (slab-major: group i of the part, slab i / groups); packed rows: a box for
+          // each slab of the part
+          constexpr int kVGroups = L::kVRows / 16;
+          auto groups_of = [&](int blk) -> int {  // first row of group lane % 8
+            const int grp = blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
             return grp < 0 ? p.rows : grp * 16;  // (a row past the end is read as zeros)
           };
-          auto copy = [&](int nn, int row, bool is_v) {
-            const int st = nn % S, b = (is_v ? kVFull : kKFull) + st;
-            if (lane == 0) tc::mbar_arrive_expect_tx(bar(b), L::kKV);
-            __syncwarp();
-            if (mine)
-              tma_box(sbase + (is_v ? L::kV : L::kK) + st * L::kKV + box_slab * L::kSlab +
-                          (paged ? (lane & 7) * rows_of_box * 128 : 0),
-                      is_v ? &a.vm : &a.km, 64 * box_slab, it.g, row, bar(b));
-          };
-          auto free = [&](int b, int nn) -> bool {
-            return nn < S || warp_wait(bar(b + nn % S), ((nn / S) & 1) ^ 1, slot + kAbort);
-          };
-          int r0 = row_of(it.blk0), r1 = row_of(it.blk0 + 1);
-          if (nb > 0) {
-            ok = free(kKFree, n);
-            if (ok) copy(n, r0, false), ++nk;
-          }
-          for (int i = 0; ok && i < nb; ++i) {
-            const int r2 = row_of(it.blk0 + i + 2);
-            if (i + 1 < nb) {
-              if (!(ok = free(kKFree, n + i + 1))) break;
-              copy(n + i + 1, r1, false), ++nk;
+          auto copy = [&](int i, int j, bool is_v, int groups) -> bool {
+            const int nn = n + i, at = spot(nn, j), full = (is_v ? kVFull : kKFull) + at;
+            if (nn * P + j >= N && !warp_wait(bar((is_v ? kVFree : kKFree) + at), turn(nn, j) ^ 1, slot + kAbort))
+              return false;
+            ++(is_v ? nv : nk);
+            if (lane == 0) tc::mbar_arrive_expect_tx(bar(full), L::kPart);
+            int slab, row;
+            bool mine;
+            uint32_t dst = sbase + (is_v ? L::kV : L::kK) + at * L::kPart;
+            if (paged) {
+              const int groups_here = is_v ? kVGroups : 8;
+              const int grp = lane % groups_here;
+              slab = lane / groups_here;
+              row = __shfl_sync(0xffffffffu, groups, grp + (is_v ? j * kVGroups : 0));
+              mine = slab < (is_v ? L::kSlabs : L::kKSlabs);
+              dst += lane * 2048;
+            } else {
+              row = it.q.s0 + (it.blk0 + i) * BN + (is_v ? j * L::kVRows : 0);
+              slab = lane;
+              mine = slab < (is_v ? L::kSlabs : L::kKSlabs);
+              dst += slab * (is_v ? L::kVRows : BN) * 128;
             }
-            if (!(ok = free(kVFree, n + i))) break;
-            copy(n + i, r0, true), ++nv;
-            r0 = r1;
-            r1 = r2;
+            if (!is_v) slab += j * L::kKSlabs;
+            __syncwarp();
+            if (mine) tma_box(dst, is_v ? &a.vm : &a.km, 64 * slab, it.g, row, bar(full));
+            return true;
+          };
+          int g0 = 0, g1 = 0, g2 = 0;
+          if (paged) {
+            g0 = groups_of(it.blk0);
+            g1 = groups_of(it.blk0 + 1);
+          }
+          for (int i = -1; ok && i < nb; ++i) {  // K runs one block ahead of V
+            if (paged) g2 = groups_of(it.blk0 + i + 2);
+            for (int j = 0; ok && i + 1 < nb && j < P; ++j) ok = copy(i + 1, j, false, i < 0 ? g0 : g1);
+            for (int j = 0; ok && i >= 0 && j < P; ++j) ok = copy(i, j, true, g0);
+            if (i >= 0) {
+              g0 = g1;
+              g1 = g2;
+            }
           }
           if (!ok) slot[kAbort] = 1;
-          // every copy begun has landed before the item ends (the last S of each, by stage)
-          for (int k = max(0, nk - S); k < nk; ++k)
-            if (!tc::mbar_wait(bar(kKFull + (n + k) % S), ((n + k) / S) & 1)) slot[kAbort] = 1;
-          for (int k = max(0, nv - S); k < nv; ++k)
-            if (!tc::mbar_wait(bar(kVFull + (n + k) % S), ((n + k) / S) & 1)) slot[kAbort] = 1;
+          // every copy begun has landed before the item ends (the last ones of each place)
+          for (int k = max(0, nk - N); k < nk; ++k)
+            if (!tc::mbar_wait(bar(kKFull + (n * P + k) % N), ((n * P + k) / N) & 1)) slot[kAbort] = 1;
+          for (int k = max(0, nv - N); k < nv; ++k)
+            if (!tc::mbar_wait(bar(kVFull + (n * P + k) % N), ((n * P + k) / N) & 1)) slot[kAbort] = 1;
           __syncwarp();
         }
         n += nb;

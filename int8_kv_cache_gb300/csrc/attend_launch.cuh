@@ -70,7 +70,8 @@ cudaError_t launch_of(const AttendParams& p, bool two_tiles, unsigned ctas, cuda
     const bool paged = p.table != nullptr;
     const long long row = (long long)p.Hkv * p.D;
     cudaError_t e = map_of(&a.km, p.k, p.D, p.Hkv, paged ? row : p.k_stride, p.rows, paged ? 16 : 128);
-    if (e == cudaSuccess) e = map_of(&a.vm, p.v, p.D, p.Hkv, paged ? row : p.v_stride, p.rows, paged ? 16 : 128);
+    if (e == cudaSuccess)
+      e = map_of(&a.vm, p.v, p.D, p.Hkv, paged ? row : p.v_stride, p.rows, paged ? 16 : p.D == 256 ? 64 : 128);
     if (e != cudaSuccess) return e;
   }
   switch (p.D) {
