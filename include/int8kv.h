@@ -85,6 +85,7 @@ typedef enum {
 #define I8KV_PATH_DSA 1   /* sparse-candidate decode kernel */
 #define I8KV_PATH_PAGED 2 /* paged decode kernel            */
 
+#define I8KV_MAX_PIECES 1024 /* paged_prefill: at most 1024 pieces */
 #define I8KV_MAX_SPLITS 32 /* at most 32 splits (onnxruntime PR 33707, §2) */
 
 /* bits OR-ed into the optional device `flags` word */
@@ -624,12 +625,13 @@ i8kv_status packed_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* 
  *                I8KV_CACHE_MX4 with k_cache the record cache and v_cache NULL
  *   seq_lens     [B] int32, device, clamped to cap = max_blocks * block_size
  *                (I8KV_FLAG_LEN_CLAMPED); query_start [B + 1] as seq_start above
- *   num_splits   1: unsplit.  2 .. 32: the batch's blocks of 128 positions are cut
- *                into pieces of equal length, one per SM, and a (token, head)'s
- *                partials take up to num_splits slots, which the split_combine
- *                kernel merges.  0: automatic -- splits where the batch's vectors
- *                alone would leave SMs idle, as many slots as the workspace holds
- *                (unsplit where it does not hold two)
+ *   num_splits   1: every (tile of tokens, KV head) is worked on by one CTA.  2 ..
+ *                I8KV_MAX_PIECES: the batch's blocks of 128 positions are cut, on the
+ *                device, into that many pieces of about equal length, one per CTA,
+ *                whose ends fall anywhere in a tile's range; what belongs to one tile
+ *                is merged by a second kernel.  0: automatic -- as many pieces as the
+ *                device has SMs where the tiles alone are fewer than four rounds of
+ *                them, and the workspace is large enough; else unsplit
  *   workspace, workspace_bytes  paged_prefill_workspace_bytes(..., num_splits) for
  *                num_splits > 1 (16-byte aligned, else I8KV_EALIGN; too small
  *                I8KV_EWORKSPACE); may be NULL for 0 and 1.  Nothing in it
@@ -656,8 +658,10 @@ i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cac
 /*
  * paged_prefill_workspace_bytes -- bytes of the workspace of paged_prefill for T
  * new tokens of B sequences with at most cap positions and the given num_splits
- * (0: what the automatic choice takes on the current device; 0 bytes: it does
- * not split): T x Hq x splits x (D + 2) x 4.  0 for bad sizes.  Host only.
+ * (0: what the automatic choice takes on the current device): two tiles of 128 or
+ * 256 vectors' partials for each piece, splits x 2 x 128 (or 256) x (D + 2) x 4,
+ * about 41 MB at most for 152 SMs; 0 where it does not split, and for bad sizes.
+ * Host only.
  */
 size_t paged_prefill_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
                                      int64_t cap, int32_t num_splits);

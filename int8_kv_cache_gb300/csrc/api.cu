@@ -1169,17 +1169,35 @@ static i8kv::AttendParams attend_params(const uint16_t* q, int64_t q_stride, con
   p.out = reinterpret_cast<__half*>(out);
   p.lse = lse;
   p.flags = flags;
-  p.nsplit = 1;
   return p;
 }
 
-// Two tiles of 128 vectors per CTA where whole CTAs of them fill the GPU and sequences have that
-// many, else one.  Returns the CTAs of an unsplit call.
-static unsigned attend_tiles(const i8kv::AttendParams& p, int sms, bool* two) {
-  const int64_t vec = static_cast<int64_t>(p.T) * p.G;
-  const int32_t seqs = std::min(p.B, p.T);
-  *two = p.D <= 128 && vec / 256 * p.Hkv >= sms && vec / seqs >= 192;
-  return static_cast<unsigned>((vec / (*two ? 256 : 128) + seqs) * p.Hkv);
+// How a call of packed_prefill or paged_prefill is dealt out: two tiles of 128 vectors per CTA where
+// sequences have about that many and, whole, they fill the GPU (one tile at a time spreads wider);
+// pieces where the (tile, KV head)s alone are fewer than a few rounds of the SMs.
+struct AttendPlan {
+  bool two = false;
+  int32_t pieces = 0;   // 0: whole (tile, KV head)s
+  unsigned ctas = 0;
+  size_t workspace = 0;
+};
+static constexpr int kAttendRounds = 4;
+static AttendPlan attend_plan(int32_t T, int32_t B, int32_t G, int32_t Hkv, int32_t D, int64_t cap,
+                              int sms, int32_t num_splits) {
+  AttendPlan a;
+  const int64_t vec = static_cast<int64_t>(T) * G;
+  const int32_t seqs = std::min(B, T);
+  const bool pairs = D <= 128 && vec / seqs >= 192;
+  const int64_t tiles = std::max<int64_t>(vec / (pairs ? 256 : 128), seqs);
+  if (num_splits > 1)
+    a.pieces = num_splits;
+  else if (num_splits == 0 && cap > 128 && tiles * Hkv < static_cast<int64_t>(kAttendRounds) * sms)
+    a.pieces = sms;
+  a.two = pairs && (a.pieces > 0 || tiles * Hkv >= sms);
+  const int32_t M = a.two ? 256 : 128;
+  a.ctas = static_cast<unsigned>(a.pieces > 0 ? a.pieces : std::min<int64_t>((vec / M + seqs) * Hkv, sms));
+  a.workspace = static_cast<size_t>(a.pieces) * 2 * M * (D + 2) * 4;
+  return a;
 }
 
 i8kv_status packed_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* k,
@@ -1208,32 +1226,19 @@ i8kv_status packed_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* 
   p.rows = T;
   int sms = 0;
   if ((st = sm_count(&sms)) != I8KV_OK) return st;
-  bool two = false;
-  const unsigned ctas = attend_tiles(p, sms, &two);
-  const cudaError_t e = i8kv::launch_attend_f16(p, two, ctas, static_cast<cudaStream_t>(stream));
+  const AttendPlan plan = attend_plan(T, B, p.G, Hkv, D, 0, sms, 1);
+  const cudaError_t e = i8kv::launch_attend_f16(p, plan.two, plan.ctas, static_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
-}
-
-// Slots of partials that paged_prefill takes by itself: 1 where the batch's vectors fill the GPU
-// without splits or its sequences have one block at most.
-static int32_t attend_slots(int32_t T, int32_t B, int32_t G, int32_t Hkv, int64_t cap, int sms) {
-  const int64_t tiles = static_cast<int64_t>(T) * G / 128;
-  if (T < 1 || B < 1 || cap <= 128 || tiles * Hkv >= sms) return 1;
-  const int64_t units = std::max<int64_t>(tiles, std::min(B, T)) * Hkv;
-  return static_cast<int32_t>(std::min<int64_t>(I8KV_MAX_SPLITS, 2 + cdiv(2 * sms, units)));
 }
 
 size_t paged_prefill_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
                                      int64_t cap, int32_t num_splits) {
-  if (T < 1 || B < 1 || cap < 0 || num_splits < 0 || num_splits > I8KV_MAX_SPLITS ||
+  if (T < 1 || B < 1 || cap < 0 || num_splits < 0 || num_splits > I8KV_MAX_PIECES ||
       check_heads(Hq, Hkv, D) != I8KV_OK)
     return 0;
-  if (num_splits == 0) {
-    int sms = 0;
-    if (sm_count(&sms) != I8KV_OK) return 0;
-    num_splits = attend_slots(T, B, Hq / Hkv, Hkv, cap, sms);
-  }
-  return num_splits > 1 ? static_cast<size_t>(T) * Hq * num_splits * (D + 2) * 4 : 0;
+  int sms = 0;
+  if (num_splits == 0 && sm_count(&sms) != I8KV_OK) return 0;
+  return attend_plan(T, B, Hq / Hkv, Hkv, D, cap, sms, num_splits).workspace;
 }
 
 i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cache,
@@ -1249,7 +1254,7 @@ i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cac
                                 head_sink, softcap, window, out, lse, flags);
   if (st != I8KV_OK) return st;
   if (max_blocks < 0 || num_blocks < 0 || block_size < 1) return I8KV_EINVAL;
-  if (num_splits < 0 || num_splits > I8KV_MAX_SPLITS) return I8KV_EINVAL;
+  if (num_splits < 0 || num_splits > I8KV_MAX_PIECES) return I8KV_EINVAL;
   if (cache_dtype < I8KV_CACHE_INT8 || cache_dtype > I8KV_CACHE_MX4) return I8KV_EINVAL;
   if (block_size % 16 != 0) return I8KV_EUNSUPPORTED;
   const bool mx4 = cache_dtype == I8KV_CACHE_MX4, fp16c = cache_dtype == I8KV_CACHE_FP16;
@@ -1270,15 +1275,13 @@ i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cac
   if (!aligned(workspace, 16)) return I8KV_EALIGN;
   int sms = 0;
   if (works && (st = sm_count(&sms)) != I8KV_OK) return st;
-  const size_t per_slot = static_cast<size_t>(std::max(T, 1)) * Hq * (D + 2) * 4;
-  if (num_splits == 0) {  // as many as the workspace holds
-    num_splits = works ? attend_slots(T, B, Hq / Hkv, Hkv, cap, sms) : 1;
-    const size_t fit = workspace != nullptr ? workspace_bytes / per_slot : 0;
-    if (fit < static_cast<size_t>(num_splits)) num_splits = static_cast<int32_t>(fit);
-    if (num_splits < 2) num_splits = 1;
-  } else if (num_splits > 1 && works &&
-             (workspace == nullptr || workspace_bytes < per_slot * num_splits)) {
-    return I8KV_EWORKSPACE;
+  AttendPlan plan;
+  if (works) {
+    plan = attend_plan(T, B, Hq / Hkv, Hkv, D, cap, sms, num_splits);
+    if (plan.pieces > 0 && (workspace == nullptr || workspace_bytes < plan.workspace)) {
+      if (num_splits > 1) return I8KV_EWORKSPACE;
+      plan = attend_plan(T, B, Hq / Hkv, Hkv, D, cap, sms, 1);
+    }
   }
   if (!works) return I8KV_OK;
   i8kv::AttendParams p = attend_params(q, q_stride, query_start, T, B, Hq, Hkv, D, softmax_scale,
@@ -1298,15 +1301,14 @@ i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cac
   p.num_blocks = num_blocks;
   // (a tensor map has a row at least: without blocks it is not read)
   p.rows = fp16c ? static_cast<int32_t>(std::max<int64_t>(1, num_blocks * block_size)) : 0;
-  p.nsplit = num_splits;
-  bool two = false;
-  unsigned ctas = attend_tiles(p, sms, &two);
-  if (num_splits > 1) {
-    two = false;
-    ctas = static_cast<unsigned>(sms);
+  p.pieces = plan.pieces;
+  const bool two = plan.two;
+  const unsigned ctas = plan.ctas;
+  if (plan.pieces > 0) {
+    const size_t rows = static_cast<size_t>(plan.pieces) * 2 * (two ? 256 : 128);
     p.part_acc = static_cast<float*>(workspace);
-    p.part_m = p.part_acc + static_cast<size_t>(T) * Hq * num_splits * D;
-    p.part_l = p.part_m + static_cast<size_t>(T) * Hq * num_splits;
+    p.part_m = p.part_acc + rows * D;
+    p.part_l = p.part_m + rows;
   }
   const cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e = cudaErrorInvalidValue;
@@ -1316,9 +1318,7 @@ i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cac
     case I8KV_CACHE_MX4: e = i8kv::launch_attend_mx4(p, two, ctas, s); break;
     default: e = i8kv::launch_attend_f16(p, two, ctas, s);
   }
-  if (e == cudaSuccess && num_splits > 1)
-    e = i8kv::launch_combine(p.part_acc, p.part_m, p.part_l, T * Hkv, num_splits, Hq, Hkv, D,
-                             head_sink, out, lse, s, query_start, B);
+  if (e == cudaSuccess && plan.pieces > 1) e = i8kv::launch_attend_merge(p, two, s);
   return e == cudaSuccess ? I8KV_OK : cuda_fail(e);
 }
 

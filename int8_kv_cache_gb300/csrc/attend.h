@@ -23,10 +23,12 @@ struct AttendParams {
   __half* out;               // [T, Hq, D]
   float* lse;                // [T, Hq] or nullptr
   uint32_t* flags;
-  float* part_acc;           // nsplit > 1: [T * Hkv, nsplit, G, D]
-  float* part_m;             // [T * Hkv, nsplit, G]
+  // pieces > 0: the batch's blocks cut into so many pieces of equal length, one per CTA, each of which ends inside
+  // two (tile, KV head)s at most, whose partials go to the slots 2 * CTA (begun inside) and 2 * CTA + 1
+  float* part_acc;           // [2 * pieces, M, D] with M vectors per tile of a CTA
+  float* part_m;             // [2 * pieces, M]
   float* part_l;
-  int32_t nsplit;            // slots of partials per (token, KV head); 1: no splits
+  int32_t pieces;            // 0: whole tiles
   int32_t T, B, Hq, Hkv, G, D;
   int32_t per_channel;
   int32_t bs, bs_log2, max_blocks;
@@ -37,10 +39,12 @@ struct AttendParams {
   int32_t window;
 };
 
-// two_tiles: 256 vectors per CTA (D = 64 or 128, no splits); ctas: the grid.
+// two_tiles: 256 vectors per CTA (D = 64 or 128); ctas: the grid (pieces, if there are).  Pieces are merged by
+// launch_attend_merge on the same parameters.
 cudaError_t launch_attend_f16(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s);
 cudaError_t launch_attend_int8(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s);
 cudaError_t launch_attend_fp8(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s);
 cudaError_t launch_attend_mx4(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s);
+cudaError_t launch_attend_merge(const AttendParams& p, bool two_tiles, cudaStream_t s);
 
 }  // namespace i8kv

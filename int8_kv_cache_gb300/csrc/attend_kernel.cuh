@@ -67,6 +67,7 @@ constexpr int kProdThreads = 128;
 constexpr int kSoftThreads = 256;
 constexpr int kThreads = 512;
 constexpr int kMmaWarp = 12, kTmaWarp = 13, kLastWarp = 15;
+constexpr int kUsers = (kSoftThreads + kProdThreads) / 32 + 2;  // warps that work through the items
 constexpr float kLazy = 7.f;   // powers of two that the maximum may outgrow the base
 constexpr float kShift = 8.f;  // P holds p 2^kShift: at most 2^15
 constexpr int kPoison = 8;     // blocks that a tile's rows can attend in part (6 at most)
@@ -93,11 +94,12 @@ struct Layout {
   static constexpr int kK = kQ + kQBytes;
   static constexpr int kV = kK + kRing * kPart;
   static constexpr int kBars = kV + kRing * kPart;
-  static constexpr int kSlots = kBars + 256;
+  static constexpr int kSlots = kBars + 320;
+  // two items' worth of what belongs to one: the next is begun while the one before is written out
   static constexpr int kItem = kSlots + 64;
-  static constexpr int kPois = kItem + 128;              // [kPoison][4] bits of positions
-  static constexpr int kRowScale = kPois + kPoison * 16;  // [kM] 2^e of each vector
-  static constexpr int kXchg = kRowScale + kM * 4;              // TILES == 1: [3][2][BM] floats
+  static constexpr int kPois = kItem + 2 * 128;        // [2][kPoison][4] bits of positions
+  static constexpr int kRowScale = kPois + 2 * kPoison * 16;  // [2][kM] 2^e of each vector
+  static constexpr int kXchg = kRowScale + 2 * kM * 4;              // TILES == 1: [3][2][BM] floats
   static constexpr int kVote = kXchg + (TILES == 1 ? 6 * BM * 4 : 0);  // TILES == 1: [3][4][2] ints
   static constexpr int kBytes = kVote + 96;
   static constexpr int kOCol = 2 * BN;  // O behind the two score buffers
@@ -107,9 +109,13 @@ struct Layout {
 
 // barriers (8 bytes each); the first five by a part's place, the others by tile (or, TILES == 1, by
 // score buffer)
-enum Bar { kKFull = 0, kKFree = 4, kVFull = 8, kVFree = 12, kVOk = 16, kSFull = 20, kPFull = 22, kPVDone = 24, kPHalf = 26, kDone = 28, kNumBars = 29 };
-enum Slot { kTmem, kAbort, kBadPage, kAnyPoison, kHas, kNumSlots };
-static_assert(kNumBars * 8 <= 256 && kNumSlots * 4 <= 64, "misc");
+// kItemFull, kItemFree, kQFull, kOFree: by the item's parity
+enum Bar {
+  kKFull = 0, kKFree = 4, kVFull = 8, kVFree = 12, kVOk = 16, kSFull = 20, kPFull = 22, kPVDone = 24, kPHalf = 26,
+  kItemFull = 28, kItemFree = 30, kQFull = 32, kOFree = 34, kQFree = 36, kDone, kNumBars
+};
+enum Slot { kTmem, kAbort, kBadPage, kAnyPoison = kBadPage + 2, kNumSlots = kAnyPoison + 2 };  // the last two by parity
+static_assert(kNumBars * 8 <= 320 && kNumSlots * 4 <= 64, "misc");
 
 __device__ __forceinline__ void sync_all() { asm volatile("bar.sync 0, 512;\n" ::: "memory"); }
 template <int N>
@@ -119,12 +125,6 @@ __device__ __forceinline__ void regs_up() {
 template <int N>
 __device__ __forceinline__ void regs_down() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
-}
-
-// B operand, MN-major with the 128-byte swizzle: 128-byte rows of 64 channels, one per position,
-// 8 positions per 1024-byte atom (SBO), 64-channel slabs at LBO.
-__device__ __forceinline__ uint64_t desc_mn_sw128(uint32_t saddr, uint32_t lbo) {
-  return tc::smem_desc_sw128(saddr, 1024) + ((uint64_t)((lbo >> 4) - 1) << 16);
 }
 
 __device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int c, int h, int row,
@@ -152,11 +152,33 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
 
 // tc::mbar_wait of a converged warp, with its clock and the others' news looked at every so often
 // only.  All lanes wait: one alone, and the others for it, hears of a phase some 300 cycles later.
+// But every lane's poll takes its turn at the shared memory that the tensor cores read operands
+// from, so only the softmax and MMA warps, whose waits are one behind the other, do it ...
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  bool ok = false;
+  uint64_t t0 = 0;
+  bool ok = tc::mbar_try_wait(bar, parity);
 #pragma unroll 1
-  for (int i = 0; !ok && i < 64; ++i) ok = tc::mbar_try_wait(bar, parity);
-  return __all_sync(0xffffffffu, ok || tc::mbar_wait(bar, parity, abort));
+  for (uint32_t i = 1; !ok; ++i) {
+    ok = tc::mbar_try_wait(bar, parity);
+    if ((i & 63u) == 0u) {
+      const uint64_t now = tc::global_ns();
+      if (t0 == 0) t0 = now;
+      if (now - t0 > tc::kWaitNs || (abort != nullptr && *abort != 0)) break;
+    }
+  }
+  return __all_sync(0xffffffffu, ok);
+}
+// ... and the others, which work ahead, wait by one lane that sleeps between polls.
+__device__ __forceinline__ bool calm_wait(uint32_t bar, uint32_t parity, const volatile int* abort, unsigned ns) {
+  bool ok = (threadIdx.x & 31) != 0 || tc::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = tc::global_ns();
+    do {
+      __nanosleep(ns);
+      ok = tc::mbar_try_wait(bar, parity);
+    } while (!ok && !(abort != nullptr && *abort) && tc::global_ns() - t0 <= tc::kWaitNs);
+  }
+  return __all_sync(0xffffffffu, ok);
 }
 __device__ __forceinline__ void warp_arrive(uint32_t bar) {
   __syncwarp();
@@ -171,18 +193,24 @@ __device__ __forceinline__ uint32_t elect_one() {
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
   return p;
 }
-__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+// Operands as the low word of their descriptors (start address, and LBO in the upper half); the high
+// one is the same for all: 8 rows of 128 bytes per atom (SBO), 128-byte swizzle.
+constexpr uint32_t kDescHigh = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr, uint32_t lbo) { return saddr >> 4 | (lbo >> 4) << 16; }
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-      "l"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lead)
+      "{\n .reg .pred p, q;\n .reg .b64 a, b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " mov.b64 a, {%1, %6};\n mov.b64 b, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lead), "r"(kDescHigh)
       : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc) {
   asm volatile(
-      "{\n .reg .pred p, q;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
-      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d),
-      "r"(a), "l"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lead)
+      "{\n .reg .pred p, q;\n .reg .b64 b;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 q, %5, 0;\n"
+      " mov.b64 b, {%2, %6};\n"
+      " @q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b), "r"(idesc), "r"(acc ? 1u : 0u), "r"(lead), "r"(kDescHigh)
       : "memory");
 }
 __device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
@@ -261,9 +289,9 @@ struct Item {
   int b, t, g;
   int first, last;  // tokens of the tile
   int B0, f0, f1;   // its first block; every row attends all of the blocks [f0, f1)
-  int blk0, blk1;   // the piece
-  int slot;         // of the partials
-  bool ends;        // the piece is the last of its tile's
+  int blk0, blk1;   // those worked on here
+  int slot;         // of the partials; -1: all of the tile's blocks are worked on
+  bool has;         // false: there are no more
   __device__ __forceinline__ bool partial(int blk) const { return blk < f0 || blk >= f1; }
   __device__ __forceinline__ int ordinal(int blk) const {
     return min(blk < f0 ? blk - B0 : f0 - B0 + blk - f1, kPoison - 1);
@@ -275,19 +303,33 @@ __device__ __forceinline__ int tiles_of(const AttendParams& p, int n) {
   return (n * p.G + M - 1) / M;
 }
 
-// Blocks that stand for each of a sequence's tiles when its pieces are cut: those of its last
-// tile, or, under a window, what a tile can touch.
+// The length of a sequence's tiles in 64ths of a block, when the batch is cut into pieces of equal
+// length: that of tile 0 and what each further one has more.  (A tile's blocks are dealt out in
+// proportion, so the lengths need not be exact.)
+struct Length {
+  long long first;
+  int more;
+  __device__ __forceinline__ long long of(int t) const { return first + (long long)t * more; }
+  __device__ __forceinline__ long long before(int t) const { return t * first + (long long)t * (t - 1) / 2 * more; }
+};
 template <int M>
-__device__ __forceinline__ int weight_of(const AttendParams& p, const Seq& s) {
-  const int all = (s.len + BN - 1) / BN;
-  if (p.window < 0) return max(all, 1);
-  const long long w = ((long long)p.window + M / p.G + 1) / BN + 2;
-  return max((int)(w < all ? w : all), 1);
+__device__ __forceinline__ Length length_of(const AttendParams& p, const Seq& s) {
+  const int all = max((s.len + BN - 1) / BN, 1);
+  Length l;
+  if (p.window >= 0 && p.window < s.len) {
+    const long long w = ((long long)p.window + M / p.G) / BN + 1;
+    l.first = 64 * (w < all ? w : all);
+    l.more = 0;
+  } else {
+    l.first = 64LL * min(max((s.len - s.n + M / p.G) / BN + 1, 1), all);
+    l.more = M / (2 * p.G);
+  }
+  return l;
 }
 
-// Blocks [x, y) of the tile's range.
+// The part [x, y) of w of the tile's blocks.
 template <int M>
-__device__ __forceinline__ void place(const AttendParams& p, Item& it, int x, int y) {
+__device__ __forceinline__ void place(const AttendParams& p, Item& it, long long x, long long y, long long w) {
   const int v0 = it.t * M, v1 = min(it.q.n * p.G, v0 + M);
   it.first = v0 / p.G;
   it.last = (v1 - 1) / p.G;
@@ -299,122 +341,202 @@ __device__ __forceinline__ void place(const AttendParams& p, Item& it, int x, in
   const int B1 = (hi + BN - 1) / BN;
   it.f0 = max(it.B0, (lo_max + BN - 1) / BN);
   it.f1 = max(it.f0, hi_min / BN);
-  it.blk0 = min(it.B0 + x, max(B1, it.B0));
-  it.blk1 = max(it.blk0, min(B1, it.B0 + y));
+  const long long n = max(B1 - it.B0, 0);
+  it.blk0 = it.B0 + (int)(x * n / w);
+  it.blk1 = it.B0 + (int)(y * n / w);
 }
 
 static_assert(sizeof(Item) <= 128, "item");
 
-// The walk over this CTA's items (of the last warp, which hands them out in shared memory).
+// The walk over this CTA's items, of the last warp, which hands them out in shared memory.
 struct Walk {
-  long long f, end, per, base;  // flat blocks; base: of sequence b's first
-  int wt, tiles;
+  long long f, end, x;  // pieces: where the CTA's next one begins and its last one ends, and the place in the (tile, head)
+  Length len;           // of sequence b's tiles
+  int round, total, b0, base;
 };
 
-// Finds where the CTA's items begin (a warp); false: it has none.
-template <int M>
-__device__ __forceinline__ bool first_item(const AttendParams& p, Item& it, Walk& w) {
+__device__ __forceinline__ int scan(int x) {
   const int lane = threadIdx.x & 31;
-  auto scan = [&](long long x) -> long long {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const long long y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= o) x += y;
-    }
-    return x;
-  };
-  long long at = 0;
-  const bool splits = M == BM && p.nsplit > 1;
-  if (splits) {
-    long long total = 0;
-    int most = 1;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      if (b0 + lane < p.B) {
-        const Seq s = seq_of(p, b0 + lane);
-        const int wt = weight_of<M>(p, s);
-        total += (long long)tiles_of<M>(p, s.n) * p.Hkv * wt;
-        if (s.n > 0) most = max(most, wt);
-      }
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      total += __shfl_xor_sync(0xffffffffu, total, o);
-      most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    }
-    // pieces of equal length; a tile's cuts must not need more than nsplit slots
-    w.per = max((total + gridDim.x - 1) / gridDim.x, (long long)(most + p.nsplit - 2) / (p.nsplit - 1));
-    w.f = w.per * blockIdx.x;
-    w.end = min(w.f + w.per, total);
-    at = w.f;
-    if (w.f >= w.end) return false;
-  } else {
-    at = blockIdx.x / p.Hkv;
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
   }
+  return x;
+}
+__device__ __forceinline__ long long scan(long long x) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
+  return x;
+}
+__device__ __forceinline__ Seq of_lane(const Seq& s, int l) {
+  return Seq{__shfl_sync(0xffffffffu, s.s0, l), __shfl_sync(0xffffffffu, s.n, l), __shfl_sync(0xffffffffu, s.len, l)};
+}
+
+// Unsplit tiles are worked on in the order of falling length where there are few sequences (a count
+// of them costs a warp 0.1 us per 32), else sequence after sequence.
+constexpr int kSortedSeqs = 128;
+
+// Of a sequence's tiles, those of at least x blocks (without a window): the last ones.
+template <int M>
+__device__ __forceinline__ int longer_tiles(const AttendParams& p, const Seq& s, int x) {
+  const int tiles = tiles_of<M>(p, s.n);
+  const int need = (x - 1) * BN - (s.len - s.n);  // the tile's last token must reach this one
+  return x <= 0 || need <= 0 ? tiles : need > s.n - 1 ? 0 : tiles - need * p.G / M;
+}
+
+// The batch cut into pieces: the length of one (a warp, all lanes alike).
+template <int M>
+__device__ __forceinline__ long long piece_length(const AttendParams& p, int pieces, long long& total) {
+  const int lane = threadIdx.x & 31;
+  total = 0;
+  for (int b0 = 0; b0 < p.B; b0 += 32)
+    if (b0 + lane < p.B) {
+      const Seq s = seq_of(p, b0 + lane);
+      total += p.Hkv * length_of<M>(p, s).before(tiles_of<M>(p, s.n));
+    }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  return (total + pieces - 1) / pieces;
+}
+// The (tile, head) at place f < total of the batch: it.b, q, t, g, the lengths, and the place in it.
+template <int M>
+__device__ __forceinline__ long long find_place(const AttendParams& p, long long f, Item& it, Length& len) {
+  const int lane = threadIdx.x & 31;
   long long before = 0;
   for (int b0 = 0; b0 < p.B; b0 += 32) {
     Seq s{0, 0, 0};
+    Length l{0, 0};
     long long x = 0;
-    int tiles = 0, wt = 1;
     if (b0 + lane < p.B) {
       s = seq_of(p, b0 + lane);
-      tiles = tiles_of<M>(p, s.n);
-      wt = weight_of<M>(p, s);
-      x = splits ? (long long)tiles * p.Hkv * wt : tiles;
+      l = length_of<M>(p, s);
+      x = p.Hkv * l.before(tiles_of<M>(p, s.n));
     }
     const long long incl = before + scan(x);
-    const unsigned hit = __ballot_sync(0xffffffffu, incl > at);
+    const unsigned hit = __ballot_sync(0xffffffffu, incl > f);
     if (hit != 0) {
-      const int l = __ffs(hit) - 1;
-      it.b = b0 + l;
-      it.q.s0 = __shfl_sync(0xffffffffu, s.s0, l);
-      it.q.n = __shfl_sync(0xffffffffu, s.n, l);
-      it.q.len = __shfl_sync(0xffffffffu, s.len, l);
-      w.tiles = __shfl_sync(0xffffffffu, tiles, l);
-      w.wt = __shfl_sync(0xffffffffu, wt, l);
-      w.base = __shfl_sync(0xffffffffu, incl - x, l);
-      return true;
+      const int n = __ffs(hit) - 1;
+      it.b = b0 + n;
+      it.q = of_lane(s, n);
+      len.first = __shfl_sync(0xffffffffu, l.first, n);
+      len.more = __shfl_sync(0xffffffffu, l.more, n);
+      const long long in_seq = f - __shfl_sync(0xffffffffu, incl - x, n);
+      int t = 0, end = tiles_of<M>(p, it.q.n);  // the last tile that begins at in_seq or before
+      while (end - t > 1) {
+        const int mid = (t + end) >> 1;
+        if (p.Hkv * len.before(mid) <= in_seq) t = mid; else end = mid;
+      }
+      it.t = t;
+      const long long in_tile = in_seq - p.Hkv * len.before(t);
+      it.g = (int)(in_tile / len.of(t));
+      return in_tile - it.g * len.of(t);
     }
     before = __shfl_sync(0xffffffffu, incl, 31);
   }
-  return false;
+  return 0;
 }
 
-// The item at the walk's place; advances it.
+template <int M>
+__device__ __forceinline__ void start_walk(const AttendParams& p, Item& it, Walk& w) {
+  const int lane = threadIdx.x & 31;
+  w = Walk{};
+  it = Item{};
+  if (p.pieces == 0) {
+    for (int b0 = 0; b0 < p.B; b0 += 32)
+      w.total += __reduce_add_sync(0xffffffffu, b0 + lane < p.B ? tiles_of<M>(p, seq_of(p, b0 + lane).n) : 0);
+    w.total *= p.Hkv;
+    return;
+  }
+  long long total;
+  const long long one = piece_length<M>(p, p.pieces, total);
+  w.f = one * blockIdx.x;
+  w.end = min(w.f + one, total);
+  if (w.f < w.end) w.x = find_place<M>(p, w.f, it, w.len);
+}
+
+// The next item; false: there is none.
 template <int M>
 __device__ __forceinline__ bool next_item(const AttendParams& p, Item& it, Walk& w) {
-  if (M == 2 * BM || p.nsplit <= 1) {  // (two tiles are not split)
-    if (w.tiles == 0) return false;
-    it.g = blockIdx.x % p.Hkv;
-    // a sequence's last tiles, the longest ones, first
-    it.t = w.tiles - 1 - (int)(blockIdx.x / p.Hkv - w.base);
-    it.slot = 0;
-    it.ends = true;
-    place<M>(p, it, 0, INT_MAX / 2);
-    w.tiles = 0;  // one item
+  const int lane = threadIdx.x & 31;
+  if (p.pieces == 0) {
+    it.slot = -1;
+    const bool sorted = p.B <= kSortedSeqs;
+    // (sorted: back and forth over the CTAs, so that none always has the longer ones)
+    const int idx = w.round * gridDim.x + (sorted && (w.round & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+    if (idx >= w.total) return false;
+    ++w.round;
+    int r = idx / p.Hkv;
+    it.g = idx - r * p.Hkv;
+    int x = 0, next = 0;  // sorted: the tile's blocks, and how many tiles have more
+    if (sorted) {
+      int hi = (p.lens != nullptr ? p.cap : p.T) / BN + 2;
+      while (hi - x > 1) {
+        const int mid = (x + hi) >> 1;
+        int c = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32)
+          if (b0 + lane < p.B) c += longer_tiles<M>(p, seq_of(p, b0 + lane), mid);
+        c = __reduce_add_sync(0xffffffffu, c);
+        if (c > r) {
+          x = mid;
+        } else {
+          hi = mid;
+          next = c;
+        }
+      }
+      r -= next;
+      w.base = w.b0 = 0;
+    }
+    for (;; w.b0 += 32) {
+      Seq s{0, 0, 0};
+      int c = 0, tiles = 0;
+      if (w.b0 + lane < p.B) {
+        s = seq_of(p, w.b0 + lane);
+        tiles = tiles_of<M>(p, s.n);
+        c = sorted ? longer_tiles<M>(p, s, x) : tiles;
+      }
+      const int mine = sorted ? c - longer_tiles<M>(p, s, x + 1) : c;
+      const int incl = w.base + scan(mine);
+      const unsigned hit = __ballot_sync(0xffffffffu, incl > r);
+      if (hit != 0) {
+        const int l = __ffs(hit) - 1;
+        it.b = w.b0 + l;
+        it.q = of_lane(s, l);
+        // (of a sequence the later ones first)
+        it.t = __shfl_sync(0xffffffffu, sorted ? tiles - c + (r - (incl - mine)) : tiles - 1 - (r - (incl - mine)), l);
+        break;
+      }
+      w.base = __shfl_sync(0xffffffffu, incl, 31);
+      if (w.b0 + 32 >= p.B) return false;
+    }
+    place<M>(p, it, 0, 1, 1);
     return true;
   }
-  while (w.f < w.end) {
-    const long long in_seq = w.f - w.base;
-    const int unit = (int)(in_seq / w.wt);
-    if (unit >= w.tiles * p.Hkv) {  // the next sequence
-      w.base += (long long)w.tiles * p.Hkv * w.wt;
+  if (w.f >= w.end) return false;
+  while (w.x == w.len.of(it.t)) {  // the next head, tile or sequence
+    w.x = 0;
+    if (++it.g < p.Hkv) break;
+    it.g = 0;
+    if (++it.t < tiles_of<M>(p, it.q.n)) break;
+    it.t = 0;
+    do {
       if (++it.b >= p.B) return false;
       it.q = seq_of(p, it.b);
-      w.tiles = tiles_of<M>(p, it.q.n);
-      w.wt = weight_of<M>(p, it.q);
-      continue;
-    }
-    const int x = (int)(in_seq - (long long)unit * w.wt);
-    const int y = (int)min((long long)w.wt, x + (w.end - w.f));
-    it.t = unit / p.Hkv;
-    it.g = unit - it.t * p.Hkv;
-    it.slot = (int)(blockIdx.x - (w.base + (long long)unit * w.wt) / w.per);
-    it.ends = y == w.wt;
-    place<M>(p, it, x, y);
-    w.f += y - x;
-    return true;
+    } while (it.q.n == 0);
+    w.len = length_of<M>(p, it.q);
+    break;
   }
-  return false;
+  const long long all = w.len.of(it.t), y = min(all, w.x + (w.end - w.f));
+  // a CTA begins inside at most one tile and ends inside at most one
+  it.slot = w.x > 0 ? 2 * blockIdx.x : y < all ? 2 * blockIdx.x + 1 : -1;
+  place<M>(p, it, w.x, y, all);
+  w.f += y - w.x;
+  w.x = y;
+  return true;
 }
 
 // The 16-row group that holds position pos of sequence b, as a row number / 16 of the cache; -1
@@ -596,8 +718,16 @@ struct Args {
   AttendParams p;
 };
 
-// Registers of a thread after the deal, which adds up to the 4 x 128 of the launch's four
-// warpgroups: 2 x 184 + 96 + 48 with two tiles, 2 x 144 + 176 + 48 with one.
+// Registers of a thread after the deal between the four warpgroups (softmax, twice; producers; the
+// rest), which started with 128 each.
+template <int TILES, int SRC>
+struct Deal {
+  static constexpr int kSoft = TILES == 2 ? 176 : 136;
+  static constexpr int kProd = TILES == 1 ? 168 : SRC == kF16 ? 80 : 96;
+  static constexpr int kRest = TILES == 1 ? 72 : SRC == kF16 ? 80 : 64;
+  static_assert(2 * kSoft + kProd + kRest == 4 * 128, "what the launch has");
+};
+
 template <int D, int TILES, int SRC>
 __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_constant__ Args a) {
   using L = Layout<D, TILES>;
@@ -611,18 +741,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   uint32_t* poison = reinterpret_cast<uint32_t*>(smem + L::kPois);
   float* rscale = reinterpret_cast<float*>(smem + L::kRowScale);
 
-  grid_dependency_wait();  // inputs may come from the previous kernel of the stream
-  const Item& it = *reinterpret_cast<const Item*>(smem + L::kItem);
-  Item* shared_item = reinterpret_cast<Item*>(smem + L::kItem);
-  Walk walk;
-  if (warp == kLastWarp) {
-    Item one;
-    const bool has = first_item<M>(p, one, walk) && next_item<M>(p, one, walk);
-    if (lane == 0) {
-      *shared_item = one;
-      slot[kHas] = has;
-    }
-  }
   if (warp == kMmaWarp) {
     tc::tmem_alloc(sbase + L::kSlots + 4 * kTmem, 512);
     tc::tmem_relinquish();
@@ -640,18 +758,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       tc::mbar_init(bar(kPFull + w), TILES == 2 ? 4 : 8);
       tc::mbar_init(bar(kPHalf + w), 4);
       tc::mbar_init(bar(kPVDone + w), 1);
+      tc::mbar_init(bar(kItemFull + w), 1);
+      tc::mbar_init(bar(kItemFree + w), kUsers);
+      tc::mbar_init(bar(kQFull + w), kProdThreads / 32);
+      tc::mbar_init(bar(kOFree + w), kSoftThreads / 32);
     }
+    tc::mbar_init(bar(kQFree), 1);
     tc::mbar_init(bar(kDone), 1);
     tc::fence_mbar_init();
     slot[kAbort] = (sbase & 1023u) != 0u;  // the swizzled layouts want 1024-byte alignment
-    slot[kBadPage] = 0;
-    slot[kAnyPoison] = 0;
   }
-  if (tid < kPoison * 4) poison[tid] = 0u;
   tc::fence_before_sync();
   sync_all();
   tc::fence_after_sync();
   const uint32_t tbase = static_cast<uint32_t>(slot[kTmem]);
+  grid_dependency_wait();  // inputs may come from the previous kernel of the stream
+  // Every role goes through the CTA's items by itself; item `k` is read from shared memory, and given
+  // back when the role is done with it.  A role whose wait failed goes on through the items without
+  // working, so that the others' waits for it end.
+  auto item_of = [&](int k) -> const Item& {
+    return *reinterpret_cast<const Item*>(smem + L::kItem + 128 * (k & 1));
+  };
+  // (items of a very long context take their time: a limit of about two minutes)
+  auto wait_item = [&](int b, uint32_t parity) -> bool {
+    bool ok = false;
+    for (int i = 0; !ok && i < 10; ++i) ok = calm_wait(bar(b), parity, nullptr, 100);
+    if (!ok) slot[kAbort] = 1;
+    return ok;
+  };
+  auto take = [&](int k) -> bool {
+    const bool ok = wait_item(kItemFull + (k & 1), (k >> 1) & 1);
+    return __all_sync(0xffffffffu, ok && item_of(k).has);
+  };
+  auto give_back = [&](int k) { warp_arrive(bar(kItemFree + (k & 1))); };
   // part j of the CTA's block nn, of K and V alike: its place, and the parity of its filling (a place
   // is free for it after the filling before: the other parity; the first ones need not wait)
   auto spot = [](int nn, int j) -> int { return (nn * P + j) % N; };
@@ -661,7 +800,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // -----------------------------------------------------------------------
     // softmax and epilogue
     // -----------------------------------------------------------------------
-    regs_up<TILES == 2 ? 184 : 144>();
+    regs_up<Deal<TILES, SRC>::kSoft>();
     constexpr int COLS = TILES == 2 ? 128 : 64;  // positions of a block per thread
     const int half = TILES == 2 ? 0 : warp >> 2, tile = TILES == 2 ? warp >> 2 : 0;
     const int r = 32 * (warp & 3) + lane;  // the vector within its tile
@@ -686,80 +825,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     const bool folds = SRC != kF16 && p.per_channel;
     const float ks1 = SRC != kF16 && !p.per_channel ? __ldg(p.k_scale) : 1.f;
     int n = 0;  // blocks done by this CTA
-    while (slot[kHas] != 0) {
+    bool ok = true;
+    for (int k = 0; take(k); ++k) {
+      const Item& it = item_of(k);
       const int v0 = it.t * M, nvec = it.q.n * p.G;
-      // ---- queries into shared memory ----
-      {
-        constexpr int CPR = D / 8;  // 16-byte chunks of a vector
-#pragma unroll 4
-        for (int k = 0; k < M * CPR / kSoftThreads; ++k) {
-          const int idx = tid + kSoftThreads * k;
-          const int row = idx / CPR, c = idx % CPR;
-          const int v = v0 + row;
-          uint4 x = make_uint4(0u, 0u, 0u, 0u);
-          if (v < nvec) {
-            const int tok = v / p.G, j = v - tok * p.G;
-            x = __ldg(reinterpret_cast<const uint4*>(p.q + (it.q.s0 + (long long)tok) * p.q_stride +
-                                                     (long long)(it.g * p.G + j) * D) + c);
-          }
-          // a query that is not finite makes its row NaN whatever its scores come to
-          uint4 y = x;
-          const unsigned odd = __ballot_sync(0xffffffffu, finite_only(y));
-          const unsigned of_row = (CPR == 32 ? 0xffffffffu : ((1u << (CPR & 31)) - 1u) << (lane & ~(CPR - 1)));
-          float rsc = 1.f;
-          if (SRC != kF16) {
-            if (folds) {
-              const float4 k0 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * c));
-              const float4 k1 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * c) + 1);
-              const __half2* h = reinterpret_cast<const __half2*>(&x);
-              float f[8];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 y = __half22float2(h[e]);
-                f[2 * e] = y.x;
-                f[2 * e + 1] = y.y;
-              }
-              f[0] *= k0.x, f[1] *= k0.y, f[2] *= k0.z, f[3] *= k0.w;
-              f[4] *= k1.x, f[5] *= k1.y, f[6] *= k1.z, f[7] *= k1.w;
-              float top = 0.f;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
-#pragma unroll
-              for (int o = CPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-              // 2^e brings the largest entry into [2^14, 2^15): exponent fields, exact
-              const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
-              const int e = ex == 0 || ex == 255 ? 0 : min(max(ex - 127 - 14, -126), 126);
-              const float down = __uint_as_float((uint32_t)(127 - e) << 23);
-#pragma unroll
-              for (int i = 0; i < 8; ++i) f[i] *= down;
-              x = make_uint4(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]), pack_h2(f[4], f[5]), pack_h2(f[6], f[7]));
-              rsc = __uint_as_float((uint32_t)(127 + e) << 23);
-            } else if (ks1 < 0.f) {
-              x = make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u);
-            }
-          }
-          if (c == 0) rscale[row] = odd & of_row ? __int_as_float(0x7fc00000) : rsc;
-          sts16(sbase + L::kQ + ((row >> 7) * L::kSlabs + (c >> 3)) * L::kSlab + (row & 127) * 128 +
-                    (((c & 7) ^ (row & 7)) << 4),
-                x);
-        }
-        // pages out of range among those attended (their tokens are skipped)
-        if (p.table != nullptr) {
-          const int lo = p.window < 0 ? 0 : max(it.q.len - it.q.n + it.first - p.window, 0);
-          const int hi = min(it.blk1 * BN, it.q.len - it.q.n + it.last + 1);
-          const int step = min(p.bs, BN);
-          bool bad = false;
-          for (int t = max(it.blk0 * BN, lo) + step * tid; t < hi; t += step * kSoftThreads)
-            bad |= group_of(p, it, t) < 0;
-          if (tid == 0 && hi > max(it.blk0 * BN, lo)) bad |= group_of(p, it, hi - 1) < 0;
-          if (bad) {
-            slot[kBadPage] = 1;
-            flag_or(p.flags, I8KV_FLAG_BAD_BLOCK);
-          }
-        }
-        tc::fence_smem_to_async();
+      ok = ok && wait_all(kQFull + (k & 1), (k >> 1) & 1);
+      if constexpr (TILES == 1) {
+        float none;
+        ok = exchange((n + 1) & 1, ok, 0.f, none);
       }
-      sync_all();  // queries staged
+      const bool enter = ok;
       const int v = v0 + tile * BM + r;
       const bool live = v < nvec;
       const int tok = live ? v / p.G : 0;
@@ -767,20 +842,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int pos = it.q.len - it.q.n + tok;
       const int hi = live ? max(pos + 1, 0) : 0;
       const int lo = p.window < 0 ? 0 : max(pos - p.window, 0);
-      const bool bad_pages = slot[kBadPage] != 0;
+      const bool bad_pages = slot[kBadPage + (k & 1)] != 0;
       // scores to powers of two: s c2 (c2 > 0 keeps an unattended -inf what it is)
-      const float rs = rscale[tile * BM + r] * fabsf(ks1);
+      const float rs = rscale[(k & 1) * M + tile * BM + r] * fabsf(ks1);
       const float nat = p.sigma * rs;
       float c2 = p.softcap > 0.f ? kLog2e : nat * kLog2e;
       if (c2 < 1e-30f) c2 = 1e-30f;
-      // (a second tile without vectors is not worked on; with two tiles there is one item)
-      const int nb = v0 + tile * BM < nvec ? it.blk1 - it.blk0 : 0;
+      const int nb = it.blk1 - it.blk0;
       const bool warp_live = __any_sync(0xffffffffu, live && hi > lo);
       const int blk0 = it.blk0, f0 = it.f0, f1 = it.f1;
       float m_run = neg_inf(), m_top = neg_inf(), l_run = 0.f;
-      bool ok = true;
       // a warp without live rows takes part in the hand-overs only
-      for (int i = 0; !warp_live && i < nb; ++i) {
+      for (int i = 0; enter && !warp_live && i < nb; ++i) {
         const int nn = n + i;
         ok = wait_all(kSFull + (TILES == 2 ? tile : nn & 1), TILES == 2 ? nn & 1 : (nn >> 1) & 1) && ok;
         if constexpr (TILES == 1) {
@@ -793,7 +866,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         warp_arrive(bar(kPFull + tile));
       }
-      for (int i = 0; warp_live && i < nb; ++i) {
+      for (int i = 0; enter && warp_live && i < nb; ++i) {
         const int blk = blk0 + i, nn = n + i;
         const int sb = TILES == 2 ? tile : nn & 1;
         const uint32_t par = TILES == 2 ? nn & 1 : (nn >> 1) & 1;
@@ -801,29 +874,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (TILES == 2 && !ok) break;
         tc::fence_after_sync();
         const uint32_t s_col = tbase + t_lane + sb * BN + 64 * half;
+        const bool masks = blk < f0 || blk >= f1 || bad_pages;
+        if (masks || p.softcap > 0.f) {
+          // capped and masked in tensor memory, 32 at a time (less code for a loop that shares its
+          // instruction cache with the other roles')
+          const int at = blk * BN + 64 * half;
+#pragma unroll 1
+          for (int c = 0; c < COLS / 32; ++c) {
+            float x[32];
+            tc::tmem_ld32(s_col + 32 * c, x);
+            tc::tmem_wait_ld();
+            if (p.softcap > 0.f) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = soft_cap(x[j] * nat, p.softcap, cap_k);
+            }
+            if (masks) {
+              // positions [lo, hi) of these 32
+              const int a0 = min(max(lo - (at + 32 * c), 0), 32), a1 = min(max(hi - (at + 32 * c), 0), 32);
+              uint32_t w = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
+              if (bad_pages) {
+                if (group_of(p, it, at + 32 * c) < 0) w &= 0xffff0000u;
+                if (group_of(p, it, at + 32 * c + 16) < 0) w &= 0x0000ffffu;
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j) x[j] = (w >> j) & 1u ? x[j] : neg_inf();
+            }
+            tc::tmem_st32(s_col + 32 * c, x);
+          }
+          tc::tmem_wait_st();
+        }
         float s[COLS];
 #pragma unroll
         for (int c = 0; c < COLS / 32; ++c) tc::tmem_ld32(s_col + 32 * c, *reinterpret_cast<float(*)[32]>(&s[32 * c]));
         tc::tmem_wait_ld();
-        if (p.softcap > 0.f) {
-#pragma unroll
-          for (int j = 0; j < COLS; ++j) s[j] = soft_cap(s[j] * nat, p.softcap, cap_k);
-        }
-        if (blk < f0 || blk >= f1 || bad_pages) {
-          const int at = blk * BN + 64 * half;
-#pragma unroll
-          for (int c = 0; c < COLS / 32; ++c) {
-            // positions [lo, hi) of these 32
-            const int a0 = min(max(lo - (at + 32 * c), 0), 32), a1 = min(max(hi - (at + 32 * c), 0), 32);
-            uint32_t w = a1 > a0 ? (0xffffffffu >> (32 - (a1 - a0))) << a0 : 0u;
-            if (bad_pages) {
-              if (group_of(p, it, at + 32 * c) < 0) w &= 0xffff0000u;
-              if (group_of(p, it, at + 32 * c + 16) < 0) w &= 0x0000ffffu;
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) s[32 * c + j] = (w >> j) & 1u ? s[32 * c + j] : neg_inf();
-          }
-        }
         float top4[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
         for (int j = 4; j < COLS; j += 8) {
@@ -913,10 +996,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       constexpr int OC = TILES == 2 ? D : D / 2;  // channels of this thread
       const int c_lo = half * OC;
       const float kNan = __int_as_float(0x7fc00000);
-      const bool fix = slot[kAnyPoison] != 0;
-      if (TILES == 1 && p.nsplit > 1) {
-        const long long u = ((it.q.s0 + (long long)tok) * p.Hkv + it.g) * p.nsplit + it.slot;
-        const long long pvec = u * p.G + (h - it.g * p.G);
+      auto free_o = [&]() {  // the next item's products may go over O
+        tc::fence_before_sync();
+        warp_arrive(bar(kOFree + (k & 1)));
+      };
+      const bool fix = slot[kAnyPoison + (k & 1)] != 0;
+      const uint32_t* notes = poison + (k & 1) * kPoison * 4;
+      if (it.slot >= 0) {
+        const long long pvec = (long long)it.slot * M + tile * BM + r;
         float* acc = p.part_acc + pvec * D;
 #pragma unroll 1
         for (int c = 0; c < OC / 32; ++c) {
@@ -938,16 +1025,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                                                               o[4 * e + 2] * f * vs.z, o[4 * e + 3] * f * vs.w);
           }
         }
-        if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, poison, lo, hi, c_lo, c_lo + OC, acc);
+        free_o();
+        if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, notes, lo, hi, c_lo, c_lo + OC, acc);
         if (live && half == 0) {
           // a CTA that gave up, and a sum that is no number, make the merged row NaN
           p.part_m[pvec] = !ok || nan ? __int_as_float(0x7f800000) : some ? m_nat : neg_inf();
           p.part_l[pvec] = !ok || nan ? kNan : some ? lsum : 0.f;
-          if (it.ends)
-            for (int k = it.slot + 1; k < p.nsplit; ++k) {
-              p.part_m[pvec + (long long)(k - it.slot) * p.G] = neg_inf();
-              p.part_l[pvec + (long long)(k - it.slot) * p.G] = 0.f;
-            }
         }
       } else {
         float sc = 0.f, lse = neg_inf();
@@ -982,38 +1065,123 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll
           for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
         }
-        if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, poison, lo, hi, c_lo, c_lo + OC, out);
+        free_o();
+        if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, notes, lo, hi, c_lo, c_lo + OC, out);
         if (live && half == 0 && p.lse != nullptr)
           p.lse[(it.q.s0 + (long long)tok) * p.Hq + h] = lse;
       }
       if (!ok) slot[kAbort] = 1;
-      tc::fence_before_sync();
-      sync_all();  // the item is done
-      tc::fence_after_sync();
-      if (tid < kPoison * 4) poison[tid] = 0u;
-      if (tid == 0) slot[kBadPage] = slot[kAnyPoison] = 0;
-      if (slot[kAbort] != 0) {
-        if (tid == 0) flag_or(p.flags, I8KV_FLAG_WAIT_TIMEOUT);
-        break;
-      }
-      sync_all();  // (the notes are cleared)
+      give_back(k);
     }
+    if (!ok && tid == 0) flag_or(p.flags, I8KV_FLAG_WAIT_TIMEOUT);
   } else if (warp < (kSoftThreads + kProdThreads) / 32) {
     // -----------------------------------------------------------------------
     // converters; of fp16 sources: the check of V blocks attended in part
     // -----------------------------------------------------------------------
-    if constexpr (TILES == 2) regs_down<96>(); else regs_up<176>();
+    if constexpr (TILES == 2) regs_down<Deal<TILES, SRC>::kProd>(); else regs_up<Deal<TILES, SRC>::kProd>();
     const int ct = tid - kSoftThreads;
+    const bool folds = SRC != kF16 && p.per_channel;
+    const bool flips = SRC != kF16 && !p.per_channel && __ldg(p.k_scale) < 0.f;
     int n = 0;
-    while (slot[kHas] != 0) {
-      const int nb = it.blk1 - it.blk0;
-      bool ok = true;
+    bool ok = true;
+    for (int k = 0; take(k); ++k) {
+      const Item& it = item_of(k);
+      const int nb = ok ? it.blk1 - it.blk0 : 0;
+      uint32_t* notes = poison + (k & 1) * kPoison * 4;
+      volatile int* any = slot + kAnyPoison + (k & 1);
+      // ---- queries into shared memory, once the item before is done with its own ----
+      auto stage_queries = [&]() {
+        if (ok && k > 0) ok = warp_wait(bar(kQFree), (k - 1) & 1, slot + kAbort);
+        const int v0 = it.t * M, nvec = it.q.n * p.G;
+        constexpr int CPR = D / 8;  // 16-byte chunks of a vector
+        constexpr int kChunks = M * CPR / kProdThreads;
+        // chunk i of a thread: of vector (ct + 128 i) / CPR
+        auto at = [&](int i, int& row, int& c) -> uint32_t {
+          const int idx = ct + kProdThreads * i;
+          row = idx / CPR;
+          c = idx % CPR;
+          return sbase + L::kQ + ((row >> 7) * L::kSlabs + (c >> 3)) * L::kSlab + (row & 127) * 128 +
+                 (((c & 7) ^ (row & 7)) << 4);
+        };
+        if (ct < kPoison * 4) notes[ct] = 0u;
+        if (ct == 0) slot[kBadPage + (k & 1)] = *any = 0;
+#pragma unroll 4
+        for (int i = 0; i < kChunks; ++i) {
+          int row, c;
+          const uint32_t dst = at(i, row, c);
+          const int v = v0 + row, tok = v / p.G, j = v - tok * p.G;
+          const bool live = ok && v < nvec;
+          cp_async16(dst, live ? p.q + (it.q.s0 + (long long)tok) * p.q_stride + (long long)(it.g * p.G + j) * D + 8 * c : p.q,
+                     live ? 16 : 0);
+        }
+        asm volatile("bar.sync 9, 128;\n" ::: "memory");  // the notes are clear
+        // pages out of range among those attended (their tokens are skipped)
+        if (p.table != nullptr) {
+          const int lo = p.window < 0 ? 0 : max(it.q.len - it.q.n + it.first - p.window, 0);
+          const int hi = min(it.blk1 * BN, it.q.len - it.q.n + it.last + 1);
+          const int step = min(p.bs, BN);
+          bool bad = false;
+          for (int t = max(it.blk0 * BN, lo) + step * ct; t < hi; t += step * kProdThreads)
+            bad |= group_of(p, it, t) < 0;
+          if (ct == 0 && hi > max(it.blk0 * BN, lo)) bad |= group_of(p, it, hi - 1) < 0;
+          if (bad) {
+            slot[kBadPage + (k & 1)] = 1;
+            flag_or(p.flags, I8KV_FLAG_BAD_BLOCK);
+          }
+        }
+        cp_async_wait_all();
+        float* scales = rscale + (k & 1) * M;
+#pragma unroll 1
+        for (int i = 0; i < kChunks; ++i) {
+          int row, c;
+          const uint32_t dst = at(i, row, c);
+          uint4 x = lds16(dst);
+          // a query that is not finite makes its row NaN whatever its scores come to
+          uint4 y = x;
+          const unsigned odd = __ballot_sync(0xffffffffu, finite_only(y));
+          const unsigned of_row = (CPR == 32 ? 0xffffffffu : ((1u << (CPR & 31)) - 1u) << (lane & ~(CPR - 1)));
+          float rsc = 1.f;
+          if (folds) {
+            const float4 k0 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * c));
+            const float4 k1 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * c) + 1);
+            const __half2* h = reinterpret_cast<const __half2*>(&x);
+            float f[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 z = __half22float2(h[e]);
+              f[2 * e] = z.x;
+              f[2 * e + 1] = z.y;
+            }
+            f[0] *= k0.x, f[1] *= k0.y, f[2] *= k0.z, f[3] *= k0.w;
+            f[4] *= k1.x, f[5] *= k1.y, f[6] *= k1.z, f[7] *= k1.w;
+            float top = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+#pragma unroll
+            for (int o = CPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^e brings the largest entry into [2^14, 2^15): exponent fields, exact
+            const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
+            const int e = ex == 0 || ex == 255 ? 0 : min(max(ex - 127 - 14, -126), 126);
+            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) f[u] *= down;
+            x = make_uint4(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]), pack_h2(f[4], f[5]), pack_h2(f[6], f[7]));
+            rsc = __uint_as_float((uint32_t)(127 + e) << 23);
+            sts16(dst, x);
+          } else if (flips) {
+            sts16(dst, make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u));
+          }
+          if (c == 0) scales[row] = odd & of_row ? __int_as_float(0x7fc00000) : rsc;
+        }
+        tc::fence_smem_to_async();
+        warp_arrive(bar(kQFull + (k & 1)));
+      };
       if constexpr (SRC == kF16) {
-        sync_all();
+        stage_queries();
         for (int i = 0; ok && i < nb; ++i) {
           const int nn = n + i, blk = it.blk0 + i;
           const bool partial = it.partial(blk);
-          uint32_t* bits = poison + 4 * it.ordinal(blk);
+          uint32_t* bits = notes + 4 * it.ordinal(blk);
           for (int j = 0; j < P; ++j) {
             const int at = spot(nn, j);
             if (!(ok = warp_wait(bar(kVFull + at), turn(nn, j), slot + kAbort))) break;
@@ -1027,7 +1195,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                   sts16(v + 16 * q, x);
                   const int row = j * L::kVRows + (q >> 3) % L::kVRows;
                   atomicOr(bits + (row >> 5), 1u << (row & 31));
-                  slot[kAnyPoison] = 1;
+                  *any = 1;
                 }
               }
               tc::fence_smem_to_async();
@@ -1048,7 +1216,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int j = 0; j < kAhead; ++j) load_raw<D, SRC>(p, ct, it.g, gk, false, j, kr[j]);
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) load_raw<D, SRC>(p, ct, it.g, gv, true, j, vr[j]);
-        sync_all();
+        stage_queries();
         // stores part j of block i, then loads the part kAhead further on
         auto put = [&](int i, int j, bool is_v, Raw<D, SRC>& r, int now, int next) -> bool {
           const int nn = n + i, at = spot(nn, j);
@@ -1056,8 +1224,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             return false;
           const int blk = it.blk0 + i;
           store_raw<D, SRC>(r, ct, sbase + (is_v ? L::kV : L::kK) + at * L::kPart, is_v,
-                            SRC != kI8 && is_v && it.partial(blk) ? poison + 4 * it.ordinal(blk) : nullptr,
-                            j * L::kVRows, slot + kAnyPoison);
+                            SRC != kI8 && is_v && it.partial(blk) ? notes + 4 * it.ordinal(blk) : nullptr,
+                            j * L::kVRows, any);
           tc::fence_smem_to_async();
           warp_arrive(bar((is_v ? kVOk : kKFull) + at));
           const int f = j + kAhead;
@@ -1082,12 +1250,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       n += nb;
       if (!ok) slot[kAbort] = 1;
-      sync_all();
-      if (slot[kAbort] != 0) break;
-      sync_all();
+      give_back(k);
     }
   } else {
-    regs_down<48>();
+    regs_down<Deal<TILES, SRC>::kRest>();
     if (warp == kMmaWarp) {
       // ---------------------------------------------------------------------
       // MMA issue
@@ -1095,131 +1261,149 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       constexpr uint32_t kIdQK = tc::idesc_f16(BM, BN, false, false);
       constexpr uint32_t kIdPV = tc::idesc_f16(BM, D, false, true);
       const uint32_t lead = elect_one(), tm = __shfl_sync(0xffffffffu, tbase, 0);
-      int n = 0, items = 0;
-      while (slot[kHas] != 0) {
+      int n = 0;
+      for (int k = 0; take(k); ++k) {
+        const Item& it = item_of(k);
         const int nb = __shfl_sync(0xffffffffu, it.blk1 - it.blk0, 0);
-        const int tiles = __shfl_sync(0xffffffffu, min(TILES, (it.q.n * p.G - it.t * M + BM - 1) / BM), 0);  // with live vectors
-        sync_all();
-        tc::fence_after_sync();
         {
-          const uint64_t qd = tc::smem_desc_sw128(sbase + L::kQ, 1024);
-          const uint64_t kd = tc::smem_desc_sw128(sbase + L::kK, 1024);
-          const uint64_t vd = desc_mn_sw128(sbase + L::kV, L::kVRows * 128);
-          auto wait = [&](int b, uint32_t par) -> bool { return warp_wait(bar(b), par, slot + kAbort); };
+          // Q and K: K-major, 64 channels of a row together (the LBO is not used); V: MN-major, 64-channel
+          // slabs of the part's positions at LBO
+          const uint32_t qd = desc_low(sbase + L::kQ, 16), kd = desc_low(sbase + L::kK, 16);
+          const uint32_t vd = desc_low(sbase + L::kV, L::kVRows * 128);
+          // A wait in vain sets the flag and goes on: what is issued then reads and writes nothing but
+          // this CTA's own memory, the waits behind it end at once, and the rows become NaN.  (Branches on
+          // the outcome cost the loop its uniform registers.)
+          auto wait = [&](int b, uint32_t par) {
+            if (!warp_wait(bar(b), par, slot + kAbort)) slot[kAbort] = 1;
+          };
           // scores of tile w (or into buffer nn & 1); the first tile waits for the parts, the last frees them
-          auto qk = [&](int w, int nn) -> bool {
-            const uint64_t qs = qd + w * (L::kSlabs * L::kSlab >> 4);
+          auto qk = [&](int w, int nn) {
+            const uint32_t qs = qd + w * (L::kSlabs * L::kSlab >> 4);
             const int buf = TILES == 2 ? w : nn & 1;
 #pragma unroll
             for (int j = 0; j < P; ++j) {
               const int at = spot(nn, j);
-              if (w == 0) {
-                if (!wait(kKFull + at, turn(nn, j))) return false;
-                tc::fence_after_sync();
-              }
-              const uint64_t ks = kd + at * (L::kPart >> 4);
+              if (w == 0) wait(kKFull + at, turn(nn, j));
+              tc::fence_after_sync();
+              const uint32_t ks = kd + at * (L::kPart >> 4);
 #pragma unroll
               for (int kk = 0; kk < 4 * L::kKSlabs; ++kk) {
                 const int in_slab = (kk >> 2) * L::kSlab + (kk & 3) * 32;
                 mma_ss(lead, tm + buf * BN, qs + ((j * L::kKSlabs * L::kSlab + in_slab) >> 4), ks + (in_slab >> 4), kIdQK,
                        j > 0 || kk > 0);
               }
-              if (w == tiles - 1) commit(lead, bar(kKFree + at));
+              // (a commit takes its time: those that the softmax waits for come first)
+              if (j == P - 1) commit(lead, bar(kSFull + buf));
+              if (w == TILES - 1) commit(lead, bar(kKFree + at));
             }
-            commit(lead, bar(kSFull + buf));
-            return true;
           };
           // O of tile w; P in two halves with two tiles
-          auto pv = [&](int w, int nn, bool first) -> bool {
+          auto pv = [&](int w, int nn, bool first) {
             const int buf = TILES == 2 ? w : nn & 1;
             constexpr int kSteps = 8 / P;  // of 16 positions in a part
 #pragma unroll
             for (int j = 0; j < P; ++j) {
               const int at = spot(nn, j);
-              const uint64_t vs = vd + at * (L::kPart >> 4);
-              if (w == 0 && !wait(kVOk + at, turn(nn, j))) return false;
+              const uint32_t vs = vd + at * (L::kPart >> 4);
+              if (w == 0) wait(kVOk + at, turn(nn, j));
 #pragma unroll
               for (int k = 0; k < kSteps; ++k) {
                 const int kk = j * kSteps + k;
-                if (kk == 0 || (TILES == 2 && kk == 4))
-                  if (!wait((TILES == 2 && kk == 0 ? kPHalf : kPFull) + w, nn & 1)) return false;
+                if (kk == 0 || (TILES == 2 && kk == 4)) wait((TILES == 2 && kk == 0 ? kPHalf : kPFull) + w, nn & 1);
                 if (k == 0 || (TILES == 2 && kk == 4)) tc::fence_after_sync();
                 mma_ts(lead, tm + L::kOCol + w * D, tm + buf * BN + 64 * (kk >> 2) + 8 * (kk & 3),
                        vs + (k * 2048 >> 4), kIdPV, !first || kk > 0);
               }
-              if (w == tiles - 1) commit(lead, bar(kVFree + at));
+              if (j == P - 1) commit(lead, bar(kPVDone + w));
+              if (w == TILES - 1) commit(lead, bar(kVFree + at));
             }
-            commit(lead, bar(kPVDone + w));
-            return true;
           };
-          bool ok = true;
+          wait(kQFull + (k & 1), (k >> 1) & 1);
+          tc::fence_after_sync();
+          // the first product of an item goes over O: the item before must have been read
+          auto o_free = [&]() {
+            if (k > 0) wait(kOFree + ((k - 1) & 1), ((k - 1) >> 1) & 1);
+          };
           if constexpr (TILES == 2) {
-            for (int i = -1; ok && i < nb; ++i) {
-              const int nn = n + i;
-              for (int w = 0; ok && w < tiles; ++w) {
-                if (i >= 0 && !(ok = pv(w, nn, i == 0))) break;
-                if (i + 1 < nb) {
-                  // the scores go over P(i): PV(i) must have read it
-                  if (i >= 0 && !(ok = wait(kPVDone + w, nn & 1))) break;
-                  tc::fence_after_sync();
-                  ok = qk(w, nn + 1);
+            // (a tile without vectors is worked on too, so that the barriers keep step)
+            // Scores go over the probabilities of the block before, of the item before where this one
+            // begins: their product must have read them.
+            if (nb > 0) {
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                if (n > 0) wait(kPVDone + w, (n - 1) & 1);
+                qk(w, n);
+              }
+              if (nb == 1) commit(lead, bar(kQFree));
+              o_free();
+            }
+#pragma unroll 1
+            for (int nn = n; nn < n + nb; ++nn) {
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                pv(w, nn, nn == n);
+                if (nn + 1 < n + nb) {
+                  wait(kPVDone + w, nn & 1);
+                  qk(w, nn + 1);
                 }
               }
+              if (nn + 2 == n + nb) commit(lead, bar(kQFree));
             }
           } else {
-            // QK(0), QK(1), PV(0), QK(2), PV(1), ...
-            for (int i = 0; ok && i <= nb; ++i) {
+            // QK(0), QK(1), PV(0), QK(2), PV(1), ...; every PVDone is waited for once, and one at most is to come
+#pragma unroll 1
+            for (int i = 0; i <= nb; ++i) {
               const int nn = n + i;
+              // S(i) goes over P(i - 2); an item's first one waits for the last product of the item before
+              if (i >= 2) wait(kPVDone, nn & 1);
+              else if (i == 0 && nb > 0 && nn > 0) wait(kPVDone, (nn - 1) & 1);
               if (i < nb) {
-                // S(i) goes over P(i - 2)
-                if (i >= 2 && !(ok = wait(kPVDone, nn & 1))) break;
-                tc::fence_after_sync();
-                if (!(ok = qk(0, nn))) break;
+                qk(0, nn);
+                if (i == nb - 1) commit(lead, bar(kQFree));
               }
-              if (i > 0) ok = pv(0, nn - 1, i == 1);
+              if (i == 1) o_free();
+              if (i > 0) pv(0, nn - 1, i == 1);
             }
           }
-          if (!ok) slot[kAbort] = 1;
-          // everything issued has completed before the item ends
-          commit(lead, bar(kDone));
-          if (!tc::mbar_wait(bar(kDone), items & 1)) slot[kAbort] = 1;
+          if (nb == 0) {
+            o_free();
+            commit(lead, bar(kQFree));
+          }
         }
-        __syncwarp();
         n += nb;
-        ++items;
-        sync_all();
-        if (slot[kAbort] != 0) break;
-        sync_all();
+        give_back(k);
       }
+      // everything issued has completed before the tensor memory is given back
+      commit(lead, bar(kDone));
+      if (!tc::mbar_wait(bar(kDone), 0)) slot[kAbort] = 1;
+      __syncwarp();
     } else if (warp == kLastWarp) {
       // ---------------------------------------------------------------------
       // the items
       // ---------------------------------------------------------------------
+      Walk walk;
+      Item one;
+      start_walk<M>(p, one, walk);
+      for (int k = 0;; ++k) {
+        one.has = next_item<M>(p, one, walk);
+        if (k >= 2 && !wait_item(kItemFree + (k & 1), ((k >> 1) & 1) ^ 1)) break;
+        if (lane == 0) *reinterpret_cast<Item*>(smem + L::kItem + 128 * (k & 1)) = one;
+        warp_arrive(bar(kItemFull + (k & 1)));
+        if (!one.has) break;
+      }
       if (blockIdx.x == 0)  // lengths and starts that had to be clamped
         for (int b = lane; b < p.B; b += 32) seq_of(p, b, true);
-      Item one = it;
-      while (slot[kHas] != 0) {
-        sync_all();
-        const bool has = next_item<M>(p, one, walk);
-        sync_all();
-        if (slot[kAbort] != 0) break;
-        if (lane == 0) {
-          *shared_item = one;
-          slot[kHas] = has;
-        }
-        sync_all();
-      }
     } else {
       // ---------------------------------------------------------------------
       // fp16 sources: copies
       // ---------------------------------------------------------------------
       int n = 0;
-      while (slot[kHas] != 0) {
-        const int nb = it.blk1 - it.blk0;
-        sync_all();
-        if (SRC == kF16 && warp == kTmaWarp) {
-          bool ok = true;
-          int nk = 0, nv = 0;  // parts begun
+      bool ok = true;
+      int nk = 0, nv = 0;  // parts begun
+      for (int k = 0; warp == kTmaWarp && take(k); ++k) {
+        const Item& it = item_of(k);
+        const int nb = ok ? it.blk1 - it.blk0 : 0;
+        if (SRC == kF16) {
           const bool paged = p.table != nullptr;
           // pages: boxes of 16 rows, a lane each (slab-major: group i of the part, slab i / groups); packed rows: a box for
           // each slab of the part
@@ -1270,18 +1454,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             }
           }
           if (!ok) slot[kAbort] = 1;
-          // every copy begun has landed before the item ends (the last ones of each place)
-          for (int k = max(0, nk - N); k < nk; ++k)
-            if (!tc::mbar_wait(bar(kKFull + (n * P + k) % N), ((n * P + k) / N) & 1)) slot[kAbort] = 1;
-          for (int k = max(0, nv - N); k < nv; ++k)
-            if (!tc::mbar_wait(bar(kVFull + (n * P + k) % N), ((n * P + k) / N) & 1)) slot[kAbort] = 1;
-          __syncwarp();
         }
         n += nb;
-        sync_all();
-        if (slot[kAbort] != 0) break;
-        sync_all();
+        give_back(k);
       }
+      // every copy begun has landed before the CTA ends (the last ones of each place)
+      if (lane == 0) {
+        for (int k = max(0, nk - N); k < nk; ++k)
+          if (!tc::mbar_wait(bar(kKFull + k % N), (k / N) & 1)) slot[kAbort] = 1;
+        for (int k = max(0, nv - N); k < nv; ++k)
+          if (!tc::mbar_wait(bar(kVFull + k % N), (k / N) & 1)) slot[kAbort] = 1;
+      }
+      __syncwarp();
     }
   }
   tc::fence_before_sync();

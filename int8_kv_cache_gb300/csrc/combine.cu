@@ -28,15 +28,12 @@ template <int D>
 __global__ void __launch_bounds__(kCombineThreads)
 combine_kernel(const float* __restrict__ acc, const float* __restrict__ m,
                const float* __restrict__ l, int units, int ns, int Hkv, int G,
-               const float* __restrict__ sink, __half* __restrict__ out, float* __restrict__ lse,
-               const int32_t* __restrict__ starts, int B) {
+               const float* __restrict__ sink, __half* __restrict__ out, float* __restrict__ lse) {
   constexpr int V = D >= kCombineThreads ? D / kCombineThreads : 1;  // channels per thread
   const int wid = blockIdx.x;  // (unit, head) pair
   const int lane = threadIdx.x & 31;
   grid_dependency_wait();  // the partials come from the preceding decode kernel
   const int u = wid / G, j = wid - (wid / G) * G;
-  // packed rows: those of no sequence have no partials and stay as they are
-  if (starts != nullptr && (u / Hkv < starts[0] || u / Hkv >= starts[B])) return;
   const long long ml0 = (long long)u * ns * G + j;  // split k at ml0 + k*G
   const int c0 = threadIdx.x * V;                    // first channel of this thread
   const bool has = c0 < D;
@@ -104,7 +101,7 @@ combine_kernel(const float* __restrict__ acc, const float* __restrict__ m,
 
 cudaError_t launch_combine(const float* acc, const float* m, const float* l, int units,
                            int num_splits, int Hq, int Hkv, int D, const float* sink, void* out,
-                           float* lse, cudaStream_t stream, const int32_t* starts, int B) {
+                           float* lse, cudaStream_t stream) {
   const int G = Hq / Hkv;
   const long long pairs = (long long)units * G;
   if (pairs == 0) return cudaSuccess;
@@ -119,9 +116,9 @@ cudaError_t launch_combine(const float* acc, const float* m, const float* l, int
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   switch (D) {
-    case 64: return cudaLaunchKernelEx(&cfg, combine_kernel<64>, acc, m, l, units, num_splits, Hkv, G, sink, o, lse, starts, B);
-    case 128: return cudaLaunchKernelEx(&cfg, combine_kernel<128>, acc, m, l, units, num_splits, Hkv, G, sink, o, lse, starts, B);
-    case 256: return cudaLaunchKernelEx(&cfg, combine_kernel<256>, acc, m, l, units, num_splits, Hkv, G, sink, o, lse, starts, B);
+    case 64: return cudaLaunchKernelEx(&cfg, combine_kernel<64>, acc, m, l, units, num_splits, Hkv, G, sink, o, lse);
+    case 128: return cudaLaunchKernelEx(&cfg, combine_kernel<128>, acc, m, l, units, num_splits, Hkv, G, sink, o, lse);
+    case 256: return cudaLaunchKernelEx(&cfg, combine_kernel<256>, acc, m, l, units, num_splits, Hkv, G, sink, o, lse);
     default: return cudaErrorInvalidValue;
   }
 }

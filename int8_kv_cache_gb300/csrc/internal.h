@@ -158,8 +158,7 @@ int prefill_auto_splits(int rows, int G, int Hkv, int sms);
 
 cudaError_t launch_combine(const float* acc, const float* m, const float* l, int units,
                            int num_splits, int Hq, int Hkv, int D, const float* sink, void* out,
-                           float* lse, cudaStream_t stream, const int32_t* starts = nullptr,
-                           int B = 0);  // starts [B + 1]: rows outside [starts[0], starts[B]) are left alone
+                           float* lse, cudaStream_t stream);
 cudaError_t launch_int8_to_fp16(const int8_t* in, uint16_t* out, int64_t n, cudaStream_t stream);
 cudaError_t launch_reshape_and_cache(const void* k_new, const void* v_new, const int32_t* slots,
                                      int num_tokens, int Hkv, int D, void* k_cache,

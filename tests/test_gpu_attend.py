@@ -127,7 +127,7 @@ def test_paged(K, kind, D, lens, new, Hq, Hkv, bs):
 
 
 @pytest.mark.parametrize("kind", KINDS)
-@pytest.mark.parametrize("splits", [2, 3, 7, 32])
+@pytest.mark.parametrize("splits", [2, 3, 7, 32, 400])
 def test_paged_splits(K, kind, splits):
     paged_case(K, kind, 6, [1500, 7, 0, 640], [3, 7, 0, 40], 8, 2, 128, splits=splits, sink=True, window=700)
     paged_case(K, kind, 7, [2000, 90], [2, 60], 4, 1, 64, splits=splits, softcap=25.0)
