@@ -598,93 +598,105 @@ __device__ __noinline__ void add_poison(const AttendParams& p, const Item& it, c
 // producers of a quantised cache
 // ---------------------------------------------------------------------------
 
-// The codes of one part as thread ct of the producers holds them: pieces of 16 bytes, piece k =
-// number ct + 128 k of the part's (slab of 64 channels, row, place in the slab's row).  Neighbouring lanes
-// are in one row and in neighbouring ones, so loads take whole sectors and the stores of a quarter
-// of a warp meet every bank once.
-template <int D, int SRC>
+// The codes of a part come in units of 8192 values, copied asynchronously into a ring in shared memory
+// (a place for each thread's own pieces, so that no thread waits for another) some units before they
+// are converted.  A piece is 16 bytes: piece k of thread ct is number ct + 128 k of the unit's, and the
+// unit's are numbered on through the part by (slab of 64 channels, row, place in the slab's row), so
+// that neighbouring lanes are in one row and in neighbouring ones: copies take whole sectors, and the
+// stores of a quarter of a warp meet every bank once.
+constexpr int kUnit = 8192;  // values
+template <int D, int TILES, int SRC>
 struct Raw {
-  static constexpr int kVals = SRC == kMx4 ? 32 : 16;     // values of a piece
-  static constexpr int kPer = 64 / kVals;                 // pieces of a slab's row
-  static constexpr int kN = Layout<D, 1>::kPart / 2 / kVals / kProdThreads;  // pieces of a thread
-  uint4 x[kN];
-  uint16_t s[SRC == kMx4 ? kN : 1];  // MX4: the two block scales
+  using L = Layout<D, TILES>;
+  static constexpr int kVals = SRC == kMx4 ? 32 : 16;           // values of a piece
+  static constexpr int kPer = 64 / kVals;                       // pieces of a slab's row
+  static constexpr int kN = kUnit / kVals / kProdThreads;       // pieces of a thread
+  static constexpr int kUnits = L::kPart / 2 / kUnit;           // of a part
+  static constexpr int kCodes = 16 * kN * kProdThreads;
+  static constexpr int kBytes = kCodes + (SRC == kMx4 ? 4 * kN * kProdThreads : 0);  // MX4: a word with the block scales
+  static constexpr int kRoom = (227 * 1024 - L::kBytes) / kBytes;
+  static constexpr int kAhead = SRC == kF16 ? 0 : kRoom < 12 ? kRoom : 12;
+  static constexpr int kAt = L::kBytes;
+  static constexpr int kSmem = L::kBytes + kAhead * kBytes;
+  static_assert(kAhead == 0 || kAhead >= 3, "units on their way");
+  static_assert(L::kBytes % 16 == 0, "alignment");
+  // where piece k of thread ct of unit u is: its row and slab in the part, its place in the slab's row
+  static __device__ __forceinline__ void place(int ct, int u, int k, int rows, int& row, int& slab, int& c) {
+    const int q = ct + kProdThreads * (u * kN + k);
+    c = q % kPer;
+    row = (q / kPer) % rows;
+    slab = q / (kPer * rows);
+  }
 };
-// Where piece k of a thread is: its row in the part, slab in the part, place in the slab's row.
-template <int SRC>
-__device__ __forceinline__ void place_of(int ct, int k, int rows, int& row, int& slab, int& c) {
-  constexpr int kPer = Raw<64, SRC>::kPer;
-  const int q = ct + kProdThreads * k;
-  c = q % kPer;
-  row = (q / kPer) % rows;
-  slab = q / (kPer * rows);
+
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
-// groups: lane i (mod 8) holds the 16-row group i of the block.  part: of K or V.
-template <int D, int SRC>
-__device__ __forceinline__ void load_raw(const AttendParams& p, int ct, int g, int groups, bool is_v,
-                                         int part, Raw<D, SRC>& r) {
-  using R = Raw<D, SRC>;
-  using L = Layout<D, 1>;
+// Unit u of part `part` of K or V on its way to ring place `at`.  groups: lane i (mod 8) holds the
+// 16-row group i of the block (-1: zeros).
+template <int D, int TILES, int SRC>
+__device__ __forceinline__ void fetch_unit(const AttendParams& p, int ct, int g, int groups, bool is_v, int part,
+                                           int u, uint32_t at) {
+  using R = Raw<D, TILES, SRC>;
+  using L = Layout<D, TILES>;
 #pragma unroll
   for (int k = 0; k < R::kN; ++k) {
     int row, slab, c;
-    place_of<SRC>(ct, k, is_v ? L::kVRows : BN, row, slab, c);
+    R::place(ct, u, k, is_v ? L::kVRows : BN, row, slab, c);
     if (is_v) row += part * L::kVRows; else slab += part * L::kKSlabs;
     const int grp = __shfl_sync(0xffffffffu, groups, row >> 4);
-    const int at = slab * R::kPer + c;  // piece of the whole row
-    r.x[k] = make_uint4(0u, 0u, 0u, 0u);
-    if constexpr (SRC == kMx4) r.s[k] = 0;
-    if (grp >= 0) {
-      if constexpr (SRC == kMx4) {
-        const int tiles = p.bs >> 4;
-        const int blk = p.bs_log2 >= 0 ? grp >> (p.bs_log2 - 4) : grp / tiles;
-        const uint8_t* rec = reinterpret_cast<const uint8_t*>(p.k) +
-                             (((long long)blk * p.Hkv + g) * tiles + (grp - blk * tiles)) * (18LL * D) +
-                             (is_v ? 9 * D : 0);
-        r.x[k] = __ldg(reinterpret_cast<const uint4*>(rec + (row & 15) * (D / 2)) + at);
-        r.s[k] = __ldg(reinterpret_cast<const uint16_t*>(rec + 8 * D + (row & 15) * (D / 16)) + at);
-      } else {
-        const uint8_t* src = reinterpret_cast<const uint8_t*>(is_v ? p.v : p.k) +
-                             (((long long)grp * 16 + (row & 15)) * p.Hkv + g) * D;
-        r.x[k] = __ldg(reinterpret_cast<const uint4*>(src) + at);
-      }
+    const int piece = slab * R::kPer + c;  // of the whole row
+    const uint32_t dst = at + 16 * (k * kProdThreads + ct);
+    const uint8_t* base = reinterpret_cast<const uint8_t*>(is_v && SRC != kMx4 ? p.v : p.k);
+    const uint32_t size = grp >= 0 ? 16 : 0;
+    if constexpr (SRC == kMx4) {
+      const int tiles = p.bs >> 4, gr = max(grp, 0);
+      const int blk = p.bs_log2 >= 0 ? gr >> (p.bs_log2 - 4) : gr / tiles;
+      const uint8_t* rec = base + (((long long)blk * p.Hkv + g) * tiles + (gr - blk * tiles)) * (18LL * D) + (is_v ? 9 * D : 0);
+      cp_async16(dst, rec + (row & 15) * (D / 2) + 16 * piece, size);
+      // the two block scales of the piece are half of an aligned word
+      cp_async4(at + R::kCodes + 4 * (k * kProdThreads + ct), rec + 8 * D + (row & 15) * (D / 16) + ((2 * piece) & ~3), size >> 2);
+    } else {
+      cp_async16(dst, base + (((long long)max(grp, 0) * 16 + (row & 15)) * p.Hkv + g) * D + 16 * piece, size);
     }
   }
 }
 
-// Into a part's place, as fp16.  bits: where rows (of the block, from row0) with a NaN are noted
-// (nullptr: not looked at).
-template <int D, int SRC>
-__device__ __forceinline__ void store_raw(const Raw<D, SRC>& r, int ct, uint32_t dst, bool is_v, uint32_t* bits,
-                                          int row0, volatile int* any) {
-  using R = Raw<D, SRC>;
-  const int rows = is_v ? Layout<D, 1>::kVRows : BN;
+// A unit from ring place `at` into its part's place, as fp16.  bits: where rows (of the block, from
+// row0) with a NaN are noted (nullptr: not looked at).
+template <int D, int TILES, int SRC>
+__device__ __forceinline__ void convert_unit(int ct, uint32_t at, uint32_t dst, bool is_v, int u, uint32_t* bits,
+                                             int row0, volatile int* any) {
+  using R = Raw<D, TILES, SRC>;
+  const int rows = is_v ? Layout<D, TILES>::kVRows : BN;
 #pragma unroll
   for (int k = 0; k < R::kN; ++k) {
     int row, slab, c;
-    place_of<SRC>(ct, k, rows, row, slab, c);
+    R::place(ct, u, k, rows, row, slab, c);
+    const uint4 x = lds16(at + 16 * (k * kProdThreads + ct));
     constexpr int kChunks = R::kVals / 8;
     uint4 h[kChunks];
     if constexpr (SRC == kI8) {
-      const uint32_t x0 = flip_i8x4(r.x[k].x), x1 = flip_i8x4(r.x[k].y);
-      const uint32_t x2 = flip_i8x4(r.x[k].z), x3 = flip_i8x4(r.x[k].w);
+      const uint32_t x0 = flip_i8x4(x.x), x1 = flip_i8x4(x.y), x2 = flip_i8x4(x.z), x3 = flip_i8x4(x.w);
       h[0] = make_uint4(i8x2_to_h2(x0, 0x4140u), i8x2_to_h2(x0, 0x4342u), i8x2_to_h2(x1, 0x4140u),
                         i8x2_to_h2(x1, 0x4342u));
       h[1] = make_uint4(i8x2_to_h2(x2, 0x4140u), i8x2_to_h2(x2, 0x4342u), i8x2_to_h2(x3, 0x4140u),
                         i8x2_to_h2(x3, 0x4342u));
     } else if constexpr (SRC == kE4) {
-      e4m3x4_to_h2x2(r.x[k].x, h[0].x, h[0].y);
-      e4m3x4_to_h2x2(r.x[k].y, h[0].z, h[0].w);
-      e4m3x4_to_h2x2(r.x[k].z, h[1].x, h[1].y);
-      e4m3x4_to_h2x2(r.x[k].w, h[1].z, h[1].w);
+      e4m3x4_to_h2x2(x.x, h[0].x, h[0].y);
+      e4m3x4_to_h2x2(x.y, h[0].z, h[0].w);
+      e4m3x4_to_h2x2(x.z, h[1].x, h[1].y);
+      e4m3x4_to_h2x2(x.w, h[1].z, h[1].w);
     } else {
+      uint32_t both;
+      asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(both) : "r"(at + R::kCodes + 4 * (k * kProdThreads + ct)) : "memory");
       uint32_t s0, s1;  // the block scales, twice each
-      e4m3x4_to_h2x2(prmt(r.s[k], 0u, 0x1100u), s0, s1);
-      e2m1x8_to_h2x4(r.x[k].x, h[0].x, h[0].y, h[0].z, h[0].w);
-      e2m1x8_to_h2x4(r.x[k].y, h[1].x, h[1].y, h[1].z, h[1].w);
-      e2m1x8_to_h2x4(r.x[k].z, h[2].x, h[2].y, h[2].z, h[2].w);
-      e2m1x8_to_h2x4(r.x[k].w, h[3].x, h[3].y, h[3].z, h[3].w);
+      e4m3x4_to_h2x2(prmt(both, 0u, (c & 1) ? 0x3322u : 0x1100u), s0, s1);
+      e2m1x8_to_h2x4(x.x, h[0].x, h[0].y, h[0].z, h[0].w);
+      e2m1x8_to_h2x4(x.y, h[1].x, h[1].y, h[1].z, h[1].w);
+      e2m1x8_to_h2x4(x.z, h[2].x, h[2].y, h[2].z, h[2].w);
+      e2m1x8_to_h2x4(x.w, h[3].x, h[3].y, h[3].z, h[3].w);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const uint32_t s = j < 2 ? s0 : s1;
@@ -722,9 +734,9 @@ struct Args {
 // rest), which started with 128 each.
 template <int TILES, int SRC>
 struct Deal {
-  static constexpr int kSoft = TILES == 2 ? 176 : 136;
-  static constexpr int kProd = TILES == 1 ? 168 : SRC == kF16 ? 80 : 96;
-  static constexpr int kRest = TILES == 1 ? 72 : SRC == kF16 ? 80 : 64;
+  static constexpr int kSoft = TILES == 2 ? 176 : 152;
+  static constexpr int kProd = TILES == 2 ? 80 : 120;
+  static constexpr int kRest = TILES == 2 ? 80 : 88;
   static_assert(2 * kSoft + kProd + kRest == 4 * 128, "what the launch has");
 };
 
@@ -820,7 +832,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       other = b[(half ^ 1) * BM + r];
       return votes[8 * buf] != 0 && votes[8 * buf + 1] != 0;
     };
-    auto wait_all = [&](int b, uint32_t parity) -> bool { return warp_wait(bar(b), parity, slot + kAbort); };
+    auto wait_all = [&](int b, uint32_t parity) -> bool {
+      const bool ok = warp_wait(bar(b), parity, slot + kAbort);
+      if (!ok) slot[kAbort] = 1;
+      return ok;
+    };
     const float cap_k = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
     const bool folds = SRC != kF16 && p.per_channel;
     const float ks1 = SRC != kF16 && !p.per_channel ? __ldg(p.k_scale) : 1.f;
@@ -1078,7 +1094,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     // -----------------------------------------------------------------------
     // converters; of fp16 sources: the check of V blocks attended in part
     // -----------------------------------------------------------------------
-    if constexpr (TILES == 2) regs_down<Deal<TILES, SRC>::kProd>(); else regs_up<Deal<TILES, SRC>::kProd>();
+    regs_down<Deal<TILES, SRC>::kProd>();
     const int ct = tid - kSoftThreads;
     const bool folds = SRC != kF16 && p.per_channel;
     const bool flips = SRC != kF16 && !p.per_channel && __ldg(p.k_scale) < 0.f;
@@ -1204,49 +1220,71 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
       } else {
-        // K runs one block ahead of V; codes are loaded a block before they are stored
-        constexpr int kAhead = P;  // parts of K, and of V
-        Raw<D, SRC> kr[kAhead], vr[kAhead];
+        // K runs one block ahead of V: K(0), K(1), V(0), K(2), V(1), ...; a run is one block of one of the two
+        using R = Raw<D, TILES, SRC>;
+        constexpr int kUnits = P * R::kUnits;  // of a run
+        const uint32_t ring = sbase + R::kAt;
         auto groups_of = [&](int blk) -> int {
           return blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
         };
-        // groups of the blocks that K (and V, a block behind) load from now, and of the next
-        int gk = groups_of(it.blk0), gk1 = groups_of(it.blk0 + 1), gv = gk;
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) load_raw<D, SRC>(p, ct, it.g, gk, false, j, kr[j]);
-#pragma unroll
-        for (int j = 0; j < kAhead; ++j) load_raw<D, SRC>(p, ct, it.g, gv, true, j, vr[j]);
-        stage_queries();
-        // stores part j of block i, then loads the part kAhead further on
-        auto put = [&](int i, int j, bool is_v, Raw<D, SRC>& r, int now, int next) -> bool {
-          const int nn = n + i, at = spot(nn, j);
-          if (nn * P + j >= N && !warp_wait(bar((is_v ? kVFree : kKFree) + at), turn(nn, j) ^ 1, slot + kAbort))
-            return false;
-          const int blk = it.blk0 + i;
-          store_raw<D, SRC>(r, ct, sbase + (is_v ? L::kV : L::kK) + at * L::kPart, is_v,
-                            SRC != kI8 && is_v && it.partial(blk) ? notes + 4 * it.ordinal(blk) : nullptr,
-                            j * L::kVRows, any);
-          tc::fence_smem_to_async();
-          warp_arrive(bar((is_v ? kVOk : kKFull) + at));
-          const int f = j + kAhead;
-          load_raw<D, SRC>(p, ct, it.g, f < P ? now : next, is_v, f % P, r);
-          return true;
-        };
-        for (int i = -1; ok && i < nb; ++i) {
-          const int gk2 = groups_of(it.blk0 + i + 3);  // (a block before it is loaded from)
-#pragma unroll
-          for (int j = 0; j < P; ++j)
-            if (ok && i + 1 < nb) ok = put(i + 1, j, false, kr[j % kAhead], gk, gk1);
-          if (i >= 0) {
-            const int gv1 = gk;  // of block i + 1
-#pragma unroll
-            for (int j = 0; j < P; ++j)
-              if (ok) ok = put(i, j, true, vr[j % kAhead], gv, gv1);
-            gv = gv1;
+        // what is fetched next: unit fu of run fr, into ring place fa; groups of that run's block, of the
+        // block before (V's) and of the next
+        int fr = 0, fu = 0, fa = 0;
+        int gk = groups_of(it.blk0), gv = -1, gn = groups_of(it.blk0 + 1);
+        auto fetch = [&]() {
+          const bool is_v = fr > 0 && (fr & 1) == 0;
+          if (fr <= 2 * nb && (is_v || (fr + 1) / 2 < nb)) {
+            fetch_unit<D, TILES, SRC>(p, ct, it.g, is_v ? gv : gk, is_v, fu / R::kUnits, fu % R::kUnits, ring + fa * R::kBytes);
+            fa = fa + 1 == R::kAhead ? 0 : fa + 1;
+            ++fu;
+          } else {
+            fu = kUnits;  // (there is no K behind the last block's)
           }
-          gk = gk1;
-          gk1 = gk2;
+          if (fu == kUnits) {
+            fu = 0;
+            ++fr;
+            if (fr & 1) {  // K of the next block
+              gv = gk;
+              gk = gn;
+              gn = groups_of(it.blk0 + (fr + 1) / 2 + 1);
+            }
+          }
+        };
+        // (every fetch is a group of its own, empty ones too)
+        auto fetch_more = [&]() {
+          const int run = fr;
+          fetch();
+          if (fr != run && fu == 0 && run > 0 && (run & 1) == 1 && (run + 1) / 2 >= nb) fetch();  // that was no K: V instead
+          cp_async_commit();
+        };
+#pragma unroll 1
+        for (int i = 0; i < R::kAhead; ++i) fetch_more();
+        stage_queries();
+        int ca = 0;  // ring place of what is converted next
+#pragma unroll 1
+        for (int r = 0; ok && r <= 2 * nb; ++r) {
+          const bool is_v = r > 0 && (r & 1) == 0;
+          const int i = r == 0 ? 0 : is_v ? r / 2 - 1 : (r + 1) / 2;
+          if (nb == 0 || (!is_v && i >= nb)) continue;
+          const int nn = n + i, blk = it.blk0 + i;
+          uint32_t* bits = SRC != kI8 && is_v && it.partial(blk) ? notes + 4 * it.ordinal(blk) : nullptr;
+#pragma unroll 1
+          for (int j = 0; ok && j < P; ++j) {
+            const int at = spot(nn, j);
+            if (nn * P + j >= N) ok = warp_wait(bar((is_v ? kVFree : kKFree) + at), turn(nn, j) ^ 1, slot + kAbort);
+#pragma unroll 1
+            for (int u = 0; ok && u < R::kUnits; ++u) {
+              cp_async_wait<R::kAhead - 1>();
+              convert_unit<D, TILES, SRC>(ct, ring + ca * R::kBytes, sbase + (is_v ? L::kV : L::kK) + at * L::kPart, is_v, u,
+                                          bits, j * L::kVRows, any);
+              ca = ca + 1 == R::kAhead ? 0 : ca + 1;
+              fetch_more();
+            }
+            tc::fence_smem_to_async();
+            warp_arrive(bar((is_v ? kVOk : kKFull) + at));
+          }
         }
+        cp_async_wait_all();  // (nothing is on its way to the ring when the next item begins)
       }
       n += nb;
       if (!ok) slot[kAbort] = 1;
@@ -1270,12 +1308,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           // slabs of the part's positions at LBO
           const uint32_t qd = desc_low(sbase + L::kQ, 16), kd = desc_low(sbase + L::kK, 16);
           const uint32_t vd = desc_low(sbase + L::kV, L::kVRows * 128);
-          // A wait in vain sets the flag and goes on: what is issued then reads and writes nothing but
-          // this CTA's own memory, the waits behind it end at once, and the rows become NaN.  (Branches on
-          // the outcome cost the loop its uniform registers.)
-          auto wait = [&](int b, uint32_t par) {
-            if (!warp_wait(bar(b), par, slot + kAbort)) slot[kAbort] = 1;
-          };
+          // After a wait in vain the loop goes on: what is issued then reads and writes nothing but this CTA's
+          // own memory, the softmax's waits fail too and set the flag that ends the ones to come, and the rows
+          // become NaN.  (Branches on the outcome made the loop 15 % slower.)
+          bool fine = true;
+          auto wait = [&](int b, uint32_t par) { fine &= warp_wait(bar(b), par, slot + kAbort); };
           // scores of tile w (or into buffer nn & 1); the first tile waits for the parts, the last frees them
           auto qk = [&](int w, int nn) {
             const uint32_t qs = qd + w * (L::kSlabs * L::kSlab >> 4);
@@ -1369,6 +1406,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             o_free();
             commit(lead, bar(kQFree));
           }
+          if (!fine) slot[kAbort] = 1;
         }
         n += nb;
         give_back(k);

@@ -38,7 +38,7 @@ inline cudaError_t map_of(CUtensorMap* m, const void* base, int D, int Hkv, long
 template <int D, int TILES, int SRC>
 cudaError_t launch(const Args& a, unsigned ctas, cudaStream_t s) {
   auto kern = attend_kernel<D, TILES, SRC>;
-  constexpr int kSmem = Layout<D, TILES>::kBytes;
+  constexpr int kSmem = Raw<D, TILES, SRC>::kSmem;
   static std::atomic<unsigned long long> done{0};  // devices whose attribute is set
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
