@@ -1266,11 +1266,11 @@ i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cac
   if (mx4 && v_cache != nullptr) return I8KV_EINVAL;
   if (!aligned(k_cache, 16) || !aligned(v_cache, 16)) return I8KV_EALIGN;
   if (!aligned(block_table, 4) || !aligned(seq_lens, 4)) return I8KV_EALIGN;
-  // positions, rows of 16 tokens and the rows of an fp16 cache are 32-bit on the device
+  // positions, rows of 16 tokens and a plain cache's rows are 32-bit on the device
   const int64_t cap = static_cast<int64_t>(max_blocks) * block_size;
   if (cap > INT32_MAX - 512 || num_blocks > (INT64_C(1) << 31) ||
       num_blocks * (block_size / 16) > INT32_MAX ||
-      (fp16c && num_blocks * block_size > INT32_MAX))
+      (!mx4 && num_blocks * block_size > INT32_MAX))
     return I8KV_EUNSUPPORTED;
   if (!aligned(workspace, 16)) return I8KV_EALIGN;
   int sms = 0;
@@ -1300,7 +1300,7 @@ i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cac
   p.cap = static_cast<int32_t>(cap);
   p.num_blocks = num_blocks;
   // (a tensor map has a row at least: without blocks it is not read)
-  p.rows = fp16c ? static_cast<int32_t>(std::max<int64_t>(1, num_blocks * block_size)) : 0;
+  p.rows = mx4 ? 0 : static_cast<int32_t>(std::max<int64_t>(1, num_blocks * block_size));
   p.pieces = plan.pieces;
   const bool two = plan.two;
   const unsigned ctas = plan.ctas;

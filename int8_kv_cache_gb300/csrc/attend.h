@@ -34,7 +34,7 @@ struct AttendParams {
   int32_t bs, bs_log2, max_blocks;
   int32_t cap;               // max_blocks * bs
   int64_t num_blocks;
-  int32_t rows;              // of an fp16 source: T, or num_blocks * bs
+  int32_t rows;              // of a plain source: T, or num_blocks * bs
   float sigma, softcap;
   int32_t window;
 };

@@ -94,14 +94,14 @@ struct Layout {
   static constexpr int kK = kQ + kQBytes;
   static constexpr int kV = kK + kRing * kPart;
   static constexpr int kBars = kV + kRing * kPart;
-  static constexpr int kSlots = kBars + 320;
+  static constexpr int kSlots = kBars + 448;
   // two items' worth of what belongs to one: the next is begun while the one before is written out
   static constexpr int kItem = kSlots + 64;
   static constexpr int kPois = kItem + 2 * 128;        // [2][kPoison][4] bits of positions
   static constexpr int kRowScale = kPois + 2 * kPoison * 16;  // [2][kM] 2^e of each vector
   static constexpr int kXchg = kRowScale + 2 * kM * 4;              // TILES == 1: [3][2][BM] floats
   static constexpr int kVote = kXchg + (TILES == 1 ? 6 * BM * 4 : 0);  // TILES == 1: [3][4][2] ints
-  static constexpr int kBytes = kVote + 96;
+  static constexpr int kBytes = kVote + (TILES == 1 ? 96 : 0);
   static constexpr int kOCol = 2 * BN;  // O behind the two score buffers
   static_assert(kOCol + TILES * D <= 512, "tensor memory");
   static_assert(kBytes <= 227 * 1024, "shared memory");
@@ -109,13 +109,14 @@ struct Layout {
 
 // barriers (8 bytes each); the first five by a part's place, the others by tile (or, TILES == 1, by
 // score buffer)
-// kItemFull, kItemFree, kQFull, kOFree: by the item's parity
+// kItemFull, kItemFree, kQFull, kOFree: by the item's parity; kRawFull, kRawFree: by the place in the ring of codes
+constexpr int kRawMost = 8;
 enum Bar {
   kKFull = 0, kKFree = 4, kVFull = 8, kVFree = 12, kVOk = 16, kSFull = 20, kPFull = 22, kPVDone = 24, kPHalf = 26,
-  kItemFull = 28, kItemFree = 30, kQFull = 32, kOFree = 34, kQFree = 36, kDone, kNumBars
+  kItemFull = 28, kItemFree = 30, kQFull = 32, kOFree = 34, kQFree = 36, kDone, kRawFull, kRawFree = kRawFull + kRawMost, kNumBars = kRawFree + kRawMost
 };
 enum Slot { kTmem, kAbort, kBadPage, kAnyPoison = kBadPage + 2, kNumSlots = kAnyPoison + 2 };  // the last two by parity
-static_assert(kNumBars * 8 <= 320 && kNumSlots * 4 <= 64, "misc");
+static_assert(kNumBars * 8 <= 448 && kNumSlots * 4 <= 64, "misc");
 
 __device__ __forceinline__ void sync_all() { asm volatile("bar.sync 0, 512;\n" ::: "memory"); }
 template <int N>
@@ -598,9 +599,12 @@ __device__ __noinline__ void add_poison(const AttendParams& p, const Item& it, c
 // producers of a quantised cache
 // ---------------------------------------------------------------------------
 
-// The codes of a part come in units of 8192 values, copied asynchronously into a ring in shared memory
-// (a place for each thread's own pieces, so that no thread waits for another) some units before they
-// are converted.  A piece is 16 bytes: piece k of thread ct is number ct + 128 k of the unit's, and the
+// The codes of a part come in units of 8192 values, copied asynchronously into a ring in shared
+// memory some units before they are converted.
+// int8, e4m3fn: by TMA, boxes of 16 rows of a page by 128 bytes (64 with head_dim 64), 64 (128) rows to
+// a unit.
+// MX4: by the converters themselves (cp.async, a place for each thread's own pieces, so that no thread
+// waits for another).  A piece is 16 bytes: piece k of thread ct is number ct + 128 k of the unit's, and the
 // unit's are numbered on through the part by (slab of 64 channels, row, place in the slab's row), so
 // that neighbouring lanes are in one row and in neighbouring ones: copies take whole sectors, and the
 // stores of a quarter of a warp meet every bank once.
@@ -614,31 +618,34 @@ struct Raw {
   static constexpr int kUnits = L::kPart / 2 / kUnit;           // of a part
   static constexpr int kCodes = 16 * kN * kProdThreads;
   static constexpr int kBytes = kCodes + (SRC == kMx4 ? 4 * kN * kProdThreads : 0);  // MX4: a word with the block scales
-  static constexpr int kRoom = (227 * 1024 - L::kBytes) / kBytes;
-  static constexpr int kAhead = SRC == kF16 ? 0 : kRoom < 12 ? kRoom : 12;
-  static constexpr int kAt = L::kBytes;
-  static constexpr int kSmem = L::kBytes + kAhead * kBytes;
+  static constexpr int kAt = (L::kBytes + 127) / 128 * 128;
+  static constexpr int kRoom = (227 * 1024 - kAt) / kBytes, kMost = SRC == kMx4 ? 12 : kRawMost;
+  static constexpr int kAhead = SRC == kF16 ? 0 : kRoom < kMost ? kRoom : kMost;
+  static constexpr int kSmem = kAt + kAhead * kBytes;
   static_assert(kAhead == 0 || kAhead >= 3, "units on their way");
-  static_assert(L::kBytes % 16 == 0, "alignment");
-  // where piece k of thread ct of unit u is: its row and slab in the part, its place in the slab's row
+  // MX4: where piece k of thread ct of unit u is: its row and slab in the part, its place in the slab's row
   static __device__ __forceinline__ void place(int ct, int u, int k, int rows, int& row, int& slab, int& c) {
     const int q = ct + kProdThreads * (u * kN + k);
     c = q % kPer;
     row = (q / kPer) % rows;
     slab = q / (kPer * rows);
   }
+  // int8, e4m3fn: rows and channels of a unit, and where unit u of a part begins in the part
+  static constexpr int kWide = D < 128 ? D : 128, kRows = kUnit / kWide;
+  static __device__ __forceinline__ int first_row(int u, bool is_v) { return D == 256 && is_v ? 0 : u * kRows; }
+  static __device__ __forceinline__ int first_slab(int u, bool is_v) { return D == 256 && is_v ? 2 * u : 0; }
 };
 
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
-// Unit u of part `part` of K or V on its way to ring place `at`.  groups: lane i (mod 8) holds the
+// MX4: unit u of part `part` of K or V on its way to ring place `at`.  groups: lane i (mod 8) holds the
 // 16-row group i of the block (-1: zeros).
-template <int D, int TILES, int SRC>
+template <int D, int TILES>
 __device__ __forceinline__ void fetch_unit(const AttendParams& p, int ct, int g, int groups, bool is_v, int part,
                                            int u, uint32_t at) {
-  using R = Raw<D, TILES, SRC>;
+  using R = Raw<D, TILES, kMx4>;
   using L = Layout<D, TILES>;
 #pragma unroll
   for (int k = 0; k < R::kN; ++k) {
@@ -647,19 +654,14 @@ __device__ __forceinline__ void fetch_unit(const AttendParams& p, int ct, int g,
     if (is_v) row += part * L::kVRows; else slab += part * L::kKSlabs;
     const int grp = __shfl_sync(0xffffffffu, groups, row >> 4);
     const int piece = slab * R::kPer + c;  // of the whole row
-    const uint32_t dst = at + 16 * (k * kProdThreads + ct);
-    const uint8_t* base = reinterpret_cast<const uint8_t*>(is_v && SRC != kMx4 ? p.v : p.k);
     const uint32_t size = grp >= 0 ? 16 : 0;
-    if constexpr (SRC == kMx4) {
-      const int tiles = p.bs >> 4, gr = max(grp, 0);
-      const int blk = p.bs_log2 >= 0 ? gr >> (p.bs_log2 - 4) : gr / tiles;
-      const uint8_t* rec = base + (((long long)blk * p.Hkv + g) * tiles + (gr - blk * tiles)) * (18LL * D) + (is_v ? 9 * D : 0);
-      cp_async16(dst, rec + (row & 15) * (D / 2) + 16 * piece, size);
-      // the two block scales of the piece are half of an aligned word
-      cp_async4(at + R::kCodes + 4 * (k * kProdThreads + ct), rec + 8 * D + (row & 15) * (D / 16) + ((2 * piece) & ~3), size >> 2);
-    } else {
-      cp_async16(dst, base + (((long long)max(grp, 0) * 16 + (row & 15)) * p.Hkv + g) * D + 16 * piece, size);
-    }
+    const int tiles = p.bs >> 4, gr = max(grp, 0);
+    const int blk = p.bs_log2 >= 0 ? gr >> (p.bs_log2 - 4) : gr / tiles;
+    const uint8_t* rec = reinterpret_cast<const uint8_t*>(p.k) +
+                         (((long long)blk * p.Hkv + g) * tiles + (gr - blk * tiles)) * (18LL * D) + (is_v ? 9 * D : 0);
+    cp_async16(at + 16 * (k * kProdThreads + ct), rec + (row & 15) * (D / 2) + 16 * piece, size);
+    // the two block scales of the piece are half of an aligned word
+    cp_async4(at + R::kCodes + 4 * (k * kProdThreads + ct), rec + 8 * D + (row & 15) * (D / 16) + ((2 * piece) & ~3), size >> 2);
   }
 }
 
@@ -673,8 +675,27 @@ __device__ __forceinline__ void convert_unit(int ct, uint32_t at, uint32_t dst, 
 #pragma unroll
   for (int k = 0; k < R::kN; ++k) {
     int row, slab, c;
-    R::place(ct, u, k, rows, row, slab, c);
-    const uint4 x = lds16(at + 16 * (k * kProdThreads + ct));
+    uint32_t from = at + 16 * (k * kProdThreads + ct);
+    if constexpr (SRC == kMx4) {
+      R::place(ct, u, k, rows, row, slab, c);
+    } else {
+      // 8 lanes take 64 bytes of each of two rows, from different halves of them: neither their loads nor
+      // their stores meet a bank twice
+      const int q = ct + kProdThreads * k;
+      c = q & 3;
+      if constexpr (D == 64) {
+        row = q >> 2;
+        slab = 0;
+      } else {
+        const int odd = (q >> 2) & 1, pr = q >> 3;
+        row = 2 * (pr % (R::kRows / 2)) + odd;
+        slab = odd ^ (pr / (R::kRows / 2));
+      }
+      from = at + row * R::kWide + slab * 64 + c * 16;
+      row += R::first_row(u, is_v);
+      slab += R::first_slab(u, is_v);
+    }
+    const uint4 x = lds16(from);
     constexpr int kChunks = R::kVals / 8;
     uint4 h[kChunks];
     if constexpr (SRC == kI8) {
@@ -726,7 +747,9 @@ __device__ __forceinline__ void convert_unit(int ct, uint32_t at, uint32_t dst, 
 // ---------------------------------------------------------------------------
 
 struct Args {
-  CUtensorMap km, vm;  // fp16 sources: [rows, Hkv, D]; boxes of 64 channels of a part's rows (packed) or 16 (pages)
+  // [rows, Hkv, D] of fp16: boxes of 64 channels of a part's rows (packed) or 16 (pages); of int8 or e4m3fn pages: 16 rows of
+  // 128 bytes (64 with head_dim 64)
+  CUtensorMap km, vm;
   AttendParams p;
 };
 
@@ -774,6 +797,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       tc::mbar_init(bar(kItemFree + w), kUsers);
       tc::mbar_init(bar(kQFull + w), kProdThreads / 32);
       tc::mbar_init(bar(kOFree + w), kSoftThreads / 32);
+    }
+    for (int s = 0; s < kRawMost; ++s) {
+      tc::mbar_init(bar(kRawFull + s), 1);
+      tc::mbar_init(bar(kRawFree + s), kProdThreads / 32);
     }
     tc::mbar_init(bar(kQFree), 1);
     tc::mbar_init(bar(kDone), 1);
@@ -1098,7 +1125,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     const int ct = tid - kSoftThreads;
     const bool folds = SRC != kF16 && p.per_channel;
     const bool flips = SRC != kF16 && !p.per_channel && __ldg(p.k_scale) < 0.f;
-    int n = 0;
+    int n = 0, units = 0;  // units converted by this CTA (int8, e4m3fn)
     bool ok = true;
     for (int k = 0; take(k); ++k) {
       const Item& it = item_of(k);
@@ -1227,14 +1254,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         auto groups_of = [&](int blk) -> int {
           return blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
         };
-        // what is fetched next: unit fu of run fr, into ring place fa; groups of that run's block, of the
+        // MX4: what is fetched next: unit fu of run fr, into ring place fa; groups of that run's block, of the
         // block before (V's) and of the next
         int fr = 0, fu = 0, fa = 0;
-        int gk = groups_of(it.blk0), gv = -1, gn = groups_of(it.blk0 + 1);
+        int gk = -1, gv = -1, gn = -1;
         auto fetch = [&]() {
           const bool is_v = fr > 0 && (fr & 1) == 0;
           if (fr <= 2 * nb && (is_v || (fr + 1) / 2 < nb)) {
-            fetch_unit<D, TILES, SRC>(p, ct, it.g, is_v ? gv : gk, is_v, fu / R::kUnits, fu % R::kUnits, ring + fa * R::kBytes);
+            fetch_unit<D, TILES>(p, ct, it.g, is_v ? gv : gk, is_v, fu / R::kUnits, fu % R::kUnits, ring + fa * R::kBytes);
             fa = fa + 1 == R::kAhead ? 0 : fa + 1;
             ++fu;
           } else {
@@ -1257,10 +1284,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           if (fr != run && fu == 0 && run > 0 && (run & 1) == 1 && (run + 1) / 2 >= nb) fetch();  // that was no K: V instead
           cp_async_commit();
         };
+        if constexpr (SRC == kMx4) {
+          gk = groups_of(it.blk0);
+          gn = groups_of(it.blk0 + 1);
 #pragma unroll 1
-        for (int i = 0; i < R::kAhead; ++i) fetch_more();
+          for (int i = 0; i < R::kAhead; ++i) fetch_more();
+        }
         stage_queries();
-        int ca = 0;  // ring place of what is converted next
+        int ca = 0;  // MX4: ring place of what is converted next
 #pragma unroll 1
         for (int r = 0; ok && r <= 2 * nb; ++r) {
           const bool is_v = r > 0 && (r & 1) == 0;
@@ -1271,20 +1302,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
 #pragma unroll 1
           for (int j = 0; ok && j < P; ++j) {
             const int at = spot(nn, j);
+            const uint32_t dst = sbase + (is_v ? L::kV : L::kK) + at * L::kPart;
             if (nn * P + j >= N) ok = warp_wait(bar((is_v ? kVFree : kKFree) + at), turn(nn, j) ^ 1, slot + kAbort);
 #pragma unroll 1
             for (int u = 0; ok && u < R::kUnits; ++u) {
-              cp_async_wait<R::kAhead - 1>();
-              convert_unit<D, TILES, SRC>(ct, ring + ca * R::kBytes, sbase + (is_v ? L::kV : L::kK) + at * L::kPart, is_v, u,
-                                          bits, j * L::kVRows, any);
-              ca = ca + 1 == R::kAhead ? 0 : ca + 1;
-              fetch_more();
+              if constexpr (SRC == kMx4) {
+                cp_async_wait<R::kAhead - 1>();
+                convert_unit<D, TILES, SRC>(ct, ring + ca * R::kBytes, dst, is_v, u, bits, j * L::kVRows, any);
+                ca = ca + 1 == R::kAhead ? 0 : ca + 1;
+                fetch_more();
+              } else {
+                const int place = units % R::kAhead;
+                ok = warp_wait(bar(kRawFull + place), (units / R::kAhead) & 1, slot + kAbort);
+                convert_unit<D, TILES, SRC>(ct, ring + place * R::kBytes, dst, is_v, u, bits, j * L::kVRows, any);
+                warp_arrive(bar(kRawFree + place));
+                ++units;
+              }
             }
             tc::fence_smem_to_async();
             warp_arrive(bar((is_v ? kVOk : kKFull) + at));
           }
         }
-        cp_async_wait_all();  // (nothing is on its way to the ring when the next item begins)
+        if constexpr (SRC == kMx4) cp_async_wait_all();  // (nothing is on its way when the next item begins)
       }
       n += nb;
       if (!ok) slot[kAbort] = 1;
@@ -1433,11 +1472,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int b = lane; b < p.B; b += 32) seq_of(p, b, true);
     } else {
       // ---------------------------------------------------------------------
-      // fp16 sources: copies
+      // copies of fp16 parts, and of units of int8 and e4m3fn codes
       // ---------------------------------------------------------------------
       int n = 0;
       bool ok = true;
       int nk = 0, nv = 0;  // parts begun
+      int units = 0;       // units begun
       for (int k = 0; warp == kTmaWarp && take(k); ++k) {
         const Item& it = item_of(k);
         const int nb = ok ? it.blk1 - it.blk0 : 0;
@@ -1491,13 +1531,48 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               g1 = g2;
             }
           }
-          if (!ok) slot[kAbort] = 1;
+        } else if constexpr (SRC != kMx4) {
+          using R = Raw<D, TILES, SRC>;
+          auto groups_of = [&](int blk) -> int {  // first row of group lane % 8
+            const int grp = blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
+            return grp < 0 ? p.rows : grp * 16;  // (a row past the end is read as zeros)
+          };
+          int gk = groups_of(it.blk0), gv = 0, gn = groups_of(it.blk0 + 1);
+          for (int r = 0; ok && r <= 2 * nb; ++r) {  // runs as the converters take them
+            const bool is_v = r > 0 && (r & 1) == 0;
+            if (r & 1) {
+              gv = gk;
+              gk = gn;
+              gn = groups_of(it.blk0 + (r + 1) / 2 + 1);
+            }
+            if (nb == 0 || (!is_v && (r + 1) / 2 >= nb)) continue;
+            for (int ju = 0; ok && ju < P * R::kUnits; ++ju) {
+              const int j = ju / R::kUnits, u = ju % R::kUnits, place = units % R::kAhead;
+              if (units >= R::kAhead && !(ok = warp_wait(bar(kRawFree + place), ((units / R::kAhead) & 1) ^ 1, slot + kAbort)))
+                break;
+              ++units;
+              // rows of the block and channels that the unit has
+              const int row0 = (is_v ? j * L::kVRows : 0) + R::first_row(u, is_v);
+              const int c0 = 64 * ((is_v ? 0 : j * L::kKSlabs) + R::first_slab(u, is_v));
+              if (lane == 0) tc::mbar_arrive_expect_tx(bar(kRawFull + place), R::kBytes);
+              const int row = __shfl_sync(0xffffffffu, is_v ? gv : gk, row0 / 16 + (lane & 7));
+              __syncwarp();
+              if (lane < R::kRows / 16)
+                tma_box(sbase + R::kAt + place * R::kBytes + lane * 16 * R::kWide, is_v ? &a.vm : &a.km, c0, it.g, row,
+                        bar(kRawFull + place));
+            }
+          }
         }
+        if (!ok) slot[kAbort] = 1;
         n += nb;
         give_back(k);
       }
       // every copy begun has landed before the CTA ends (the last ones of each place)
       if (lane == 0) {
+        if constexpr (SRC == kI8 || SRC == kE4)
+          for (int k = max(0, units - Raw<D, TILES, SRC>::kAhead); k < units; ++k)
+            if (!tc::mbar_wait(bar(kRawFull + k % Raw<D, TILES, SRC>::kAhead), (k / Raw<D, TILES, SRC>::kAhead) & 1))
+              slot[kAbort] = 1;
         for (int k = max(0, nk - N); k < nk; ++k)
           if (!tc::mbar_wait(bar(kKFull + k % N), (k / N) & 1)) slot[kAbort] = 1;
         for (int k = max(0, nv - N); k < nv; ++k)

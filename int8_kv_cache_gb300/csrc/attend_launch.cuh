@@ -8,9 +8,10 @@
 namespace i8kv {
 namespace ap {
 
-// The tensor map of fp16 rows [rows, Hkv, D] whose tokens are `stride` elements apart: boxes of
-// `box` rows of one head by 64 channels, 128-byte swizzle, zeros out of range.
-inline cudaError_t map_of(CUtensorMap* m, const void* base, int D, int Hkv, long long stride, long long rows, int box) {
+// The tensor map of rows [rows, Hkv, D] (fp16, or bytes) whose tokens are `stride` elements apart: boxes
+// of `box` rows of one head by `wide` channels, zeros out of range; fp16 with the 128-byte swizzle.
+inline cudaError_t map_of(CUtensorMap* m, const void* base, bool fp16, int D, int Hkv, long long stride, long long rows,
+                          int box, int wide) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -26,11 +27,13 @@ inline cudaError_t map_of(CUtensorMap* m, const void* base, int D, int Hkv, long
     known.store(encode);
   }
   const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)Hkv, (cuuint64_t)rows};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t boxes[3] = {64, 1, (cuuint32_t)box};
+  const int size = fp16 ? 2 : 1;
+  const cuuint64_t strides[2] = {(cuuint64_t)D * size, (cuuint64_t)stride * size};
+  const cuuint32_t boxes[3] = {(cuuint32_t)wide, 1, (cuuint32_t)box};
   const cuuint32_t steps[3] = {1, 1, 1};
-  const CUresult r = encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base), dims, strides, boxes, steps,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+  const CUresult r = encode(m, fp16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, boxes, steps,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE,
+                            fp16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
@@ -66,12 +69,13 @@ template <int SRC>
 cudaError_t launch_of(const AttendParams& p, bool two_tiles, unsigned ctas, cudaStream_t s) {
   Args a{};
   a.p = p;
-  if (SRC == kF16) {
-    const bool paged = p.table != nullptr;
+  if (SRC != kMx4) {
+    const bool paged = p.table != nullptr, fp16 = SRC == kF16;
     const long long row = (long long)p.Hkv * p.D;
-    cudaError_t e = map_of(&a.km, p.k, p.D, p.Hkv, paged ? row : p.k_stride, p.rows, paged ? 16 : 128);
+    const int wide = fp16 ? 64 : p.D < 128 ? p.D : 128;
+    cudaError_t e = map_of(&a.km, p.k, fp16, p.D, p.Hkv, paged ? row : p.k_stride, p.rows, paged ? 16 : 128, wide);
     if (e == cudaSuccess)
-      e = map_of(&a.vm, p.v, p.D, p.Hkv, paged ? row : p.v_stride, p.rows, paged ? 16 : p.D == 256 ? 64 : 128);
+      e = map_of(&a.vm, p.v, fp16, p.D, p.Hkv, paged ? row : p.v_stride, p.rows, paged ? 16 : p.D == 256 ? 64 : 128, wide);
     if (e != cudaSuccess) return e;
   }
   switch (p.D) {
