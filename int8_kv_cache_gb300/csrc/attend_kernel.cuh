@@ -24,13 +24,15 @@
 //
 // Warp roles (512 threads, registers dealt out anew with setmaxnreg):
 //   warps 0-7    softmax and epilogue
-//   warps 8-11   fp16 sources: look at the V blocks that some row attends in part, where a NaN or
-//                infinity that is masked for a row must not reach it through 0 * NaN: such values
-//                become 0 and are added back to the rows that do attend them in the epilogue.
-//                int8, e4m3fn, MX4: load the codes a block ahead, convert them exactly to fp16
-//   warp 12      lane 0 issues the MMAs; the warp owns the tensor memory
-//   warp 13      fp16 sources: TMA copies (a box of 128 rows of a packed prompt, or of 16 rows of
-//                a page, by 64 channels, 128-byte swizzle); rows out of range are zeros
+//   warps 8-11   queries into shared memory; then, fp16 sources: look at the V blocks that some row
+//                attends in part, where a NaN or infinity that is masked for a row must not reach it
+//                through 0 * NaN: such values become 0 and are added back to the rows that do
+//                attend them in the epilogue.  int8, e4m3fn, MX4: convert the codes exactly to fp16
+//   warp 12      issues the MMAs and owns the tensor memory
+//   warp 13      copies: fp16 parts by TMA (a box of a part's rows of a packed prompt, or of 16 rows
+//                of a page, by 64 channels, 128-byte swizzle), codes into a ring; rows out of range
+//                are zeros
+//   warp 15      finds the CTA's next items
 // K is K-major, V MN-major, both as 128-byte rows of 64 channels with the 128-byte swizzle.
 //
 // Scales of a quantised cache: v_scale multiplies the finished sums.  k_scale per tensor joins
@@ -599,146 +601,112 @@ __device__ __noinline__ void add_poison(const AttendParams& p, const Item& it, c
 // producers of a quantised cache
 // ---------------------------------------------------------------------------
 
-// The codes of a part come in units of 8192 values, copied asynchronously into a ring in shared
-// memory some units before they are converted.
-// int8, e4m3fn: by TMA, boxes of 16 rows of a page by 128 bytes (64 with head_dim 64), 64 (128) rows to
-// a unit.
-// MX4: by the converters themselves (cp.async, a place for each thread's own pieces, so that no thread
-// waits for another).  A piece is 16 bytes: piece k of thread ct is number ct + 128 k of the unit's, and the
-// unit's are numbered on through the part by (slab of 64 channels, row, place in the slab's row), so
-// that neighbouring lanes are in one row and in neighbouring ones: copies take whole sectors, and the
-// stores of a quarter of a warp meet every bank once.
-constexpr int kUnit = 8192;  // values
+// Codes are copied into a ring in shared memory, unit by unit, some units before they are converted:
+// int8, e4m3fn: 8 KB, TMA boxes of 16 rows of a page by 128 bytes (64 with head_dim 64): 64 (128) rows
+// to a unit;
+// MX4: 64 rows, the K or V half of the records of four 16-row groups (a bulk copy each).
 template <int D, int TILES, int SRC>
 struct Raw {
   using L = Layout<D, TILES>;
-  static constexpr int kVals = SRC == kMx4 ? 32 : 16;           // values of a piece
-  static constexpr int kPer = 64 / kVals;                       // pieces of a slab's row
-  static constexpr int kN = kUnit / kVals / kProdThreads;       // pieces of a thread
-  static constexpr int kUnits = L::kPart / 2 / kUnit;           // of a part
-  static constexpr int kCodes = 16 * kN * kProdThreads;
-  static constexpr int kBytes = kCodes + (SRC == kMx4 ? 4 * kN * kProdThreads : 0);  // MX4: a word with the block scales
+  static constexpr int kWide = D < 128 ? D : 128;  // channels of a unit (MX4: all)
+  static constexpr int kRows = SRC == kMx4 ? 64 : 8192 / kWide;
+  static constexpr int kBytes = SRC == kMx4 ? 36 * D : 8192;
+  static constexpr int kRun = SRC == kMx4 ? 2 : BN * D / 8192;  // units of a block's K or V
   static constexpr int kAt = (L::kBytes + 127) / 128 * 128;
-  static constexpr int kRoom = (227 * 1024 - kAt) / kBytes, kMost = SRC == kMx4 ? 12 : kRawMost;
-  static constexpr int kAhead = SRC == kF16 ? 0 : kRoom < kMost ? kRoom : kMost;
+  static constexpr int kRoom = (227 * 1024 - kAt) / kBytes;
+  static constexpr int kAhead = SRC == kF16 ? 0 : kRoom < kRawMost ? kRoom : kRawMost;
   static constexpr int kSmem = kAt + kAhead * kBytes;
   static_assert(kAhead == 0 || kAhead >= 3, "units on their way");
-  // MX4: where piece k of thread ct of unit u is: its row and slab in the part, its place in the slab's row
-  static __device__ __forceinline__ void place(int ct, int u, int k, int rows, int& row, int& slab, int& c) {
-    const int q = ct + kProdThreads * (u * kN + k);
-    c = q % kPer;
-    row = (q / kPer) % rows;
-    slab = q / (kPer * rows);
-  }
-  // int8, e4m3fn: rows and channels of a unit, and where unit u of a part begins in the part
-  static constexpr int kWide = D < 128 ? D : 128, kRows = kUnit / kWide;
+  // int8, e4m3fn: where unit u of a part begins in the part
   static __device__ __forceinline__ int first_row(int u, bool is_v) { return D == 256 && is_v ? 0 : u * kRows; }
   static __device__ __forceinline__ int first_slab(int u, bool is_v) { return D == 256 && is_v ? 2 * u : 0; }
 };
 
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src, uint32_t src_bytes) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;\n" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-
-// MX4: unit u of part `part` of K or V on its way to ring place `at`.  groups: lane i (mod 8) holds the
-// 16-row group i of the block (-1: zeros).
-template <int D, int TILES>
-__device__ __forceinline__ void fetch_unit(const AttendParams& p, int ct, int g, int groups, bool is_v, int part,
-                                           int u, uint32_t at) {
-  using R = Raw<D, TILES, kMx4>;
-  using L = Layout<D, TILES>;
+// N chunks of 8 fp16 values into a line of a part (64 channels of a row); a NaN or infinity is noted
+// and zeroed where the rows are looked at (bits not nullptr).
+template <int N>
+__device__ __forceinline__ void store_chunks(uint4 (&h)[N], uint32_t line, int first, int row_in_part, uint32_t* bits,
+                                             int row, volatile int* any) {
+  if (bits != nullptr) {
+    bool bad = false;
 #pragma unroll
-  for (int k = 0; k < R::kN; ++k) {
-    int row, slab, c;
-    R::place(ct, u, k, is_v ? L::kVRows : BN, row, slab, c);
-    if (is_v) row += part * L::kVRows; else slab += part * L::kKSlabs;
-    const int grp = __shfl_sync(0xffffffffu, groups, row >> 4);
-    const int piece = slab * R::kPer + c;  // of the whole row
-    const uint32_t size = grp >= 0 ? 16 : 0;
-    const int tiles = p.bs >> 4, gr = max(grp, 0);
-    const int blk = p.bs_log2 >= 0 ? gr >> (p.bs_log2 - 4) : gr / tiles;
-    const uint8_t* rec = reinterpret_cast<const uint8_t*>(p.k) +
-                         (((long long)blk * p.Hkv + g) * tiles + (gr - blk * tiles)) * (18LL * D) + (is_v ? 9 * D : 0);
-    cp_async16(at + 16 * (k * kProdThreads + ct), rec + (row & 15) * (D / 2) + 16 * piece, size);
-    // the two block scales of the piece are half of an aligned word
-    cp_async4(at + R::kCodes + 4 * (k * kProdThreads + ct), rec + 8 * D + (row & 15) * (D / 16) + ((2 * piece) & ~3), size >> 2);
+    for (int j = 0; j < N; ++j) bad |= finite_only(h[j]);
+    if (bad) {
+      atomicOr(bits + (row >> 5), 1u << (row & 31));
+      *any = 1;
+    }
   }
+#pragma unroll
+  for (int j = 0; j < N; ++j) sts16(line + (((first + j) ^ (row_in_part & 7)) << 4), h[j]);
 }
 
-// A unit from ring place `at` into its part's place, as fp16.  bits: where rows (of the block, from
-// row0) with a NaN are noted (nullptr: not looked at).
+// int8, e4m3fn: unit u of a part, as fp16.  bits: of the block's rows, from row0 on, that have a NaN.
 template <int D, int TILES, int SRC>
-__device__ __forceinline__ void convert_unit(int ct, uint32_t at, uint32_t dst, bool is_v, int u, uint32_t* bits,
-                                             int row0, volatile int* any) {
+__device__ __forceinline__ void convert_bytes(int ct, uint32_t at, uint32_t dst, bool is_v, int u, uint32_t* bits,
+                                              int row0, volatile int* any) {
   using R = Raw<D, TILES, SRC>;
   const int rows = is_v ? Layout<D, TILES>::kVRows : BN;
 #pragma unroll
-  for (int k = 0; k < R::kN; ++k) {
-    int row, slab, c;
-    uint32_t from = at + 16 * (k * kProdThreads + ct);
-    if constexpr (SRC == kMx4) {
-      R::place(ct, u, k, rows, row, slab, c);
-    } else {
-      // 8 lanes take 64 bytes of each of two rows, from different halves of them: neither their loads nor
-      // their stores meet a bank twice
-      const int q = ct + kProdThreads * k;
-      c = q & 3;
-      if constexpr (D == 64) {
-        row = q >> 2;
-        slab = 0;
-      } else {
-        const int odd = (q >> 2) & 1, pr = q >> 3;
-        row = 2 * (pr % (R::kRows / 2)) + odd;
-        slab = odd ^ (pr / (R::kRows / 2));
-      }
-      from = at + row * R::kWide + slab * 64 + c * 16;
-      row += R::first_row(u, is_v);
-      slab += R::first_slab(u, is_v);
+  for (int k = 0; k < 4; ++k) {
+    // 8 lanes take 64 bytes of each of two rows, from different halves of them: neither their loads nor
+    // their stores meet a bank twice
+    const int q = ct + kProdThreads * k, c = q & 3;
+    int row = q >> 2, slab = 0;
+    if (D != 64) {
+      const int odd = row & 1, pr = q >> 3;
+      row = 2 * (pr % (R::kRows / 2)) + odd;
+      slab = odd ^ (pr / (R::kRows / 2));
     }
-    const uint4 x = lds16(from);
-    constexpr int kChunks = R::kVals / 8;
-    uint4 h[kChunks];
+    const uint4 x = lds16(at + row * R::kWide + slab * 64 + c * 16);
+    row += R::first_row(u, is_v);
+    slab += R::first_slab(u, is_v);
+    uint4 h[2];
     if constexpr (SRC == kI8) {
       const uint32_t x0 = flip_i8x4(x.x), x1 = flip_i8x4(x.y), x2 = flip_i8x4(x.z), x3 = flip_i8x4(x.w);
       h[0] = make_uint4(i8x2_to_h2(x0, 0x4140u), i8x2_to_h2(x0, 0x4342u), i8x2_to_h2(x1, 0x4140u),
                         i8x2_to_h2(x1, 0x4342u));
       h[1] = make_uint4(i8x2_to_h2(x2, 0x4140u), i8x2_to_h2(x2, 0x4342u), i8x2_to_h2(x3, 0x4140u),
                         i8x2_to_h2(x3, 0x4342u));
-    } else if constexpr (SRC == kE4) {
+    } else {
       e4m3x4_to_h2x2(x.x, h[0].x, h[0].y);
       e4m3x4_to_h2x2(x.y, h[0].z, h[0].w);
       e4m3x4_to_h2x2(x.z, h[1].x, h[1].y);
       e4m3x4_to_h2x2(x.w, h[1].z, h[1].w);
-    } else {
-      uint32_t both;
-      asm volatile("ld.shared.u32 %0, [%1];\n" : "=r"(both) : "r"(at + R::kCodes + 4 * (k * kProdThreads + ct)) : "memory");
-      uint32_t s0, s1;  // the block scales, twice each
-      e4m3x4_to_h2x2(prmt(both, 0u, (c & 1) ? 0x3322u : 0x1100u), s0, s1);
-      e2m1x8_to_h2x4(x.x, h[0].x, h[0].y, h[0].z, h[0].w);
-      e2m1x8_to_h2x4(x.y, h[1].x, h[1].y, h[1].z, h[1].w);
-      e2m1x8_to_h2x4(x.z, h[2].x, h[2].y, h[2].z, h[2].w);
-      e2m1x8_to_h2x4(x.w, h[3].x, h[3].y, h[3].z, h[3].w);
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const uint32_t s = j < 2 ? s0 : s1;
-        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].x) : "r"(s));  // exact: 6 significant bits
-        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].y) : "r"(s));
-        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].z) : "r"(s));
-        asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].w) : "r"(s));
-      }
     }
-    if (SRC != kI8 && bits != nullptr) {
-      bool bad = false;
+    store_chunks(h, dst + (slab * rows + row) * 128, 2 * c, row, SRC == kE4 ? bits : nullptr, row0 + row, any);
+  }
+}
+
+// MX4: N slabs, from slab0, of the 64 rows of a unit, as fp16, to the rows from row_in_part of a part.
+template <int D, int N>
+__device__ __forceinline__ void convert_mx4(int ct, uint32_t at, uint32_t dst, int rows, int row_in_part, int slab0,
+                                            uint32_t* bits, int row0, volatile int* any) {
+  const int row = ct >> 1, c = ct & 1;  // 32 channels of each slab
+  const uint32_t rec = at + (row >> 4) * (9 * D);
 #pragma unroll
-      for (int j = 0; j < kChunks; ++j) bad |= finite_only(h[j]);
-      if (bad) {
-        atomicOr(bits + ((row0 + row) >> 5), 1u << ((row0 + row) & 31));
-        *any = 1;
-      }
+  for (int k = 0; k < N; ++k) {
+    const uint4 x = lds16(rec + (row & 15) * (D / 2) + (slab0 + k) * 32 + c * 16);
+    uint16_t both;  // the block scales
+    asm volatile("ld.shared.u16 %0, [%1];\n"
+                 : "=h"(both)
+                 : "r"(rec + 8 * D + (row & 15) * (D / 16) + (slab0 + k) * 4 + 2 * c)
+                 : "memory");
+    uint32_t s0, s1;  // twice each
+    e4m3x4_to_h2x2(prmt(both, 0u, 0x1100u), s0, s1);
+    uint4 h[4];
+    e2m1x8_to_h2x4(x.x, h[0].x, h[0].y, h[0].z, h[0].w);
+    e2m1x8_to_h2x4(x.y, h[1].x, h[1].y, h[1].z, h[1].w);
+    e2m1x8_to_h2x4(x.z, h[2].x, h[2].y, h[2].z, h[2].w);
+    e2m1x8_to_h2x4(x.w, h[3].x, h[3].y, h[3].z, h[3].w);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t s = j < 2 ? s0 : s1;
+      asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].x) : "r"(s));  // exact: 6 significant bits
+      asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].y) : "r"(s));
+      asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].z) : "r"(s));
+      asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].w) : "r"(s));
     }
-    const uint32_t line = dst + (slab * rows + row) * 128;
-#pragma unroll
-    for (int j = 0; j < kChunks; ++j) sts16(line + (((c * kChunks + j) ^ (row & 7)) << 4), h[j]);
+    store_chunks(h, dst + (k * rows + row_in_part + row) * 128, 4 * c, row_in_part + row, bits, row0 + row, any);
   }
 }
 
@@ -1125,7 +1093,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     const int ct = tid - kSoftThreads;
     const bool folds = SRC != kF16 && p.per_channel;
     const bool flips = SRC != kF16 && !p.per_channel && __ldg(p.k_scale) < 0.f;
-    int n = 0, units = 0;  // units converted by this CTA (int8, e4m3fn)
+    int n = 0, units = 0;  // units converted by this CTA
     bool ok = true;
     for (int k = 0; take(k); ++k) {
       const Item& it = item_of(k);
@@ -1249,49 +1217,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       } else {
         // K runs one block ahead of V: K(0), K(1), V(0), K(2), V(1), ...; a run is one block of one of the two
         using R = Raw<D, TILES, SRC>;
-        constexpr int kUnits = P * R::kUnits;  // of a run
-        const uint32_t ring = sbase + R::kAt;
-        auto groups_of = [&](int blk) -> int {
-          return blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
-        };
-        // MX4: what is fetched next: unit fu of run fr, into ring place fa; groups of that run's block, of the
-        // block before (V's) and of the next
-        int fr = 0, fu = 0, fa = 0;
-        int gk = -1, gv = -1, gn = -1;
-        auto fetch = [&]() {
-          const bool is_v = fr > 0 && (fr & 1) == 0;
-          if (fr <= 2 * nb && (is_v || (fr + 1) / 2 < nb)) {
-            fetch_unit<D, TILES>(p, ct, it.g, is_v ? gv : gk, is_v, fu / R::kUnits, fu % R::kUnits, ring + fa * R::kBytes);
-            fa = fa + 1 == R::kAhead ? 0 : fa + 1;
-            ++fu;
-          } else {
-            fu = kUnits;  // (there is no K behind the last block's)
-          }
-          if (fu == kUnits) {
-            fu = 0;
-            ++fr;
-            if (fr & 1) {  // K of the next block
-              gv = gk;
-              gk = gn;
-              gn = groups_of(it.blk0 + (fr + 1) / 2 + 1);
-            }
-          }
-        };
-        // (every fetch is a group of its own, empty ones too)
-        auto fetch_more = [&]() {
-          const int run = fr;
-          fetch();
-          if (fr != run && fu == 0 && run > 0 && (run & 1) == 1 && (run + 1) / 2 >= nb) fetch();  // that was no K: V instead
-          cp_async_commit();
-        };
-        if constexpr (SRC == kMx4) {
-          gk = groups_of(it.blk0);
-          gn = groups_of(it.blk0 + 1);
-#pragma unroll 1
-          for (int i = 0; i < R::kAhead; ++i) fetch_more();
-        }
         stage_queries();
-        int ca = 0;  // MX4: ring place of what is converted next
 #pragma unroll 1
         for (int r = 0; ok && r <= 2 * nb; ++r) {
           const bool is_v = r > 0 && (r & 1) == 0;
@@ -1304,26 +1230,31 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             const int at = spot(nn, j);
             const uint32_t dst = sbase + (is_v ? L::kV : L::kK) + at * L::kPart;
             if (nn * P + j >= N) ok = warp_wait(bar((is_v ? kVFree : kKFree) + at), turn(nn, j) ^ 1, slot + kAbort);
+            // the part's units of the ring; MX4: both halves of the K of head_dim 256 are in the same two
+            constexpr bool kShares = SRC == kMx4 && P == 2;
+            const bool shares = kShares && !is_v;
+            const int here = shares ? 2 : R::kRun / P;
 #pragma unroll 1
-            for (int u = 0; ok && u < R::kUnits; ++u) {
+            for (int u = 0; ok && u < here; ++u) {
+              const int unit = units + (shares ? u : 0), place = unit % R::kAhead;
+              const uint32_t from = sbase + R::kAt + place * R::kBytes;
+              if (!shares || j == 0) ok = warp_wait(bar(kRawFull + place), (unit / R::kAhead) & 1, slot + kAbort);
               if constexpr (SRC == kMx4) {
-                cp_async_wait<R::kAhead - 1>();
-                convert_unit<D, TILES, SRC>(ct, ring + ca * R::kBytes, dst, is_v, u, bits, j * L::kVRows, any);
-                ca = ca + 1 == R::kAhead ? 0 : ca + 1;
-                fetch_more();
+                if (shares)
+                  convert_mx4<D, L::kKSlabs>(ct, from, dst, BN, 64 * u, j * L::kKSlabs, nullptr, 0, nullptr);
+                else
+                  convert_mx4<D, L::kSlabs>(ct, from, dst, is_v ? L::kVRows : BN, 64 * u, 0, bits, j * L::kVRows + 64 * u, any);
               } else {
-                const int place = units % R::kAhead;
-                ok = warp_wait(bar(kRawFull + place), (units / R::kAhead) & 1, slot + kAbort);
-                convert_unit<D, TILES, SRC>(ct, ring + place * R::kBytes, dst, is_v, u, bits, j * L::kVRows, any);
-                warp_arrive(bar(kRawFree + place));
-                ++units;
+                convert_bytes<D, TILES, SRC>(ct, from, dst, is_v, u, bits, j * L::kVRows, any);
               }
+              if (!shares || j == P - 1) warp_arrive(bar(kRawFree + place));
+              if (!shares) ++units;
             }
             tc::fence_smem_to_async();
             warp_arrive(bar((is_v ? kVOk : kKFull) + at));
           }
+          if (SRC == kMx4 && P == 2 && !is_v) units += 2;
         }
-        if constexpr (SRC == kMx4) cp_async_wait_all();  // (nothing is on its way when the next item begins)
       }
       n += nb;
       if (!ok) slot[kAbort] = 1;
@@ -1472,7 +1403,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         for (int b = lane; b < p.B; b += 32) seq_of(p, b, true);
     } else {
       // ---------------------------------------------------------------------
-      // copies of fp16 parts, and of units of int8 and e4m3fn codes
+      // copies of fp16 parts, and of units of codes
       // ---------------------------------------------------------------------
       int n = 0;
       bool ok = true;
@@ -1531,11 +1462,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               g1 = g2;
             }
           }
-        } else if constexpr (SRC != kMx4) {
+        } else {
           using R = Raw<D, TILES, SRC>;
-          auto groups_of = [&](int blk) -> int {  // first row of group lane % 8
-            const int grp = blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
-            return grp < 0 ? p.rows : grp * 16;  // (a row past the end is read as zeros)
+          auto groups_of = [&](int blk) -> int {  // group lane % 8 of the block
+            return blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
           };
           int gk = groups_of(it.blk0), gv = 0, gn = groups_of(it.blk0 + 1);
           for (int r = 0; ok && r <= 2 * nb; ++r) {  // runs as the converters take them
@@ -1546,20 +1476,41 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               gn = groups_of(it.blk0 + (r + 1) / 2 + 1);
             }
             if (nb == 0 || (!is_v && (r + 1) / 2 >= nb)) continue;
-            for (int ju = 0; ok && ju < P * R::kUnits; ++ju) {
-              const int j = ju / R::kUnits, u = ju % R::kUnits, place = units % R::kAhead;
+            for (int ru = 0; ru < R::kRun; ++ru) {
+              const int place = units % R::kAhead;
               if (units >= R::kAhead && !(ok = warp_wait(bar(kRawFree + place), ((units / R::kAhead) & 1) ^ 1, slot + kAbort)))
                 break;
               ++units;
-              // rows of the block and channels that the unit has
-              const int row0 = (is_v ? j * L::kVRows : 0) + R::first_row(u, is_v);
-              const int c0 = 64 * ((is_v ? 0 : j * L::kKSlabs) + R::first_slab(u, is_v));
-              if (lane == 0) tc::mbar_arrive_expect_tx(bar(kRawFull + place), R::kBytes);
-              const int row = __shfl_sync(0xffffffffu, is_v ? gv : gk, row0 / 16 + (lane & 7));
-              __syncwarp();
-              if (lane < R::kRows / 16)
-                tma_box(sbase + R::kAt + place * R::kBytes + lane * 16 * R::kWide, is_v ? &a.vm : &a.km, c0, it.g, row,
-                        bar(kRawFull + place));
+              const uint32_t dst = sbase + R::kAt + place * R::kBytes;
+              if constexpr (SRC == kMx4) {
+                const int grp = __shfl_sync(0xffffffffu, is_v ? gv : gk, 4 * ru + (lane & 3));
+                const uint32_t here = dst + lane * 9 * D;
+                const bool copies = lane < 4 && grp >= 0;
+                if (copies) {
+                  const int tiles = p.bs >> 4;
+                  const int page = p.bs_log2 >= 0 ? grp >> (p.bs_log2 - 4) : grp / tiles;
+                  tc::bulk_g2s(here, reinterpret_cast<const uint8_t*>(p.k) +
+                                         (((long long)page * p.Hkv + it.g) * tiles + (grp - page * tiles)) * (18LL * D) +
+                                         (is_v ? 9 * D : 0),
+                               9 * D, bar(kRawFull + place));
+                } else if (lane < 4) {
+                  for (int b = 0; b < 9 * D; b += 16) sts16(here + b, make_uint4(0u, 0u, 0u, 0u));
+                }
+                // (bytes that land before they are announced are counted all the same)
+                const unsigned mask = __ballot_sync(0xffffffffu, copies);
+                if (lane == 0) tc::mbar_arrive_expect_tx(bar(kRawFull + place), __popc(mask) * 9 * D);
+              } else {
+                // rows of the block and channels that the unit has
+                const int j = ru / (R::kRun / P), u = ru % (R::kRun / P);
+                const int row0 = (is_v ? j * L::kVRows : 0) + R::first_row(u, is_v);
+                const int c0 = 64 * ((is_v ? 0 : j * L::kKSlabs) + R::first_slab(u, is_v));
+                if (lane == 0) tc::mbar_arrive_expect_tx(bar(kRawFull + place), R::kBytes);
+                const int grp = __shfl_sync(0xffffffffu, is_v ? gv : gk, row0 / 16 + (lane & 7));
+                __syncwarp();
+                if (lane < R::kRows / 16)  // (a row past the end is read as zeros)
+                  tma_box(dst + lane * 16 * R::kWide, is_v ? &a.vm : &a.km, c0, it.g, grp < 0 ? p.rows : grp * 16,
+                          bar(kRawFull + place));
+              }
             }
           }
         }
@@ -1569,7 +1520,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       // every copy begun has landed before the CTA ends (the last ones of each place)
       if (lane == 0) {
-        if constexpr (SRC == kI8 || SRC == kE4)
+        if constexpr (SRC != kF16)
           for (int k = max(0, units - Raw<D, TILES, SRC>::kAhead); k < units; ++k)
             if (!tc::mbar_wait(bar(kRawFull + k % Raw<D, TILES, SRC>::kAhead), (k / Raw<D, TILES, SRC>::kAhead) & 1))
               slot[kAbort] = 1;
