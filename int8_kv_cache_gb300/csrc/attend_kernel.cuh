@@ -262,6 +262,30 @@ __device__ __forceinline__ bool finite_only(uint4& v) {
   return a || b || c || d;
 }
 
+// Whether one of 8 fp16 values is not finite: their magnitudes + 2^10 reach the sign's bit.
+__device__ __forceinline__ bool not_finite(const uint4& v) {
+  auto high = [](uint32_t x) { return (x & 0x7fff7fffu) + 0x04000400u; };
+  return ((high(v.x) | high(v.y) | high(v.z) | high(v.w)) & 0x80008000u) != 0u;
+}
+
+// Four lanes' 4 x 16 bytes the other way round: lane l of the four gets, at i, the 16 bytes l of lane i.
+__device__ __forceinline__ void across(uint32_t (&w)[16], int lane) {
+#pragma unroll
+  for (int bit = 1; bit < 4; bit *= 2) {
+    const bool up = (lane & bit) != 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      if (i & bit) continue;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        uint32_t &x = w[4 * i + e], &y = w[4 * (i + bit) + e];
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x : y, bit);
+        (up ? x : y) = got;
+      }
+    }
+  }
+}
+
 // ---------------------------------------------------------------------------
 // the work
 // ---------------------------------------------------------------------------
@@ -1052,13 +1076,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           sc = 0.00390625f / lsum;
           if (p.sink != nullptr) sc *= 1.f / (1.f + expf(__ldg(p.sink + h) - lse));
         }
-        __half* out = p.out + ((it.q.s0 + (long long)tok) * p.Hq + h) * D;
+        // Four lanes write 64 bytes of one row, not each 16 of its own (a store of 32 rows takes four
+        // times the turns at the L1 that one of 8 does)
+        const long long mine = live ? (it.q.s0 + (long long)tok) * p.Hq + h : -1;
+        __half* out = p.out + mine * D;
+        long long rows[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) rows[i] = __shfl_sync(0xffffffffu, mine, (lane & 28) + i);
 #pragma unroll 1
         for (int c = 0; c < OC / 32; ++c) {
           float o[32];
           tc::tmem_ld32(tbase + t_lane + L::kOCol + tile * D + c_lo + 32 * c, o);
           tc::tmem_wait_ld();
-          if (!live) continue;
           uint32_t w[16];
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
@@ -1072,10 +1101,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             w[2 * e] = z ? 0u : sc != sc ? 0x7e007e00u : pack_h2(o[4 * e] * sc * vs.x, o[4 * e + 1] * sc * vs.y);
             w[2 * e + 1] = z ? 0u : sc != sc ? 0x7e007e00u : pack_h2(o[4 * e + 2] * sc * vs.z, o[4 * e + 3] * sc * vs.w);
           }
-          uint4* dst = reinterpret_cast<uint4*>(out + c_lo + 32 * c);
+          across(w, lane);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) dst[e] = make_uint4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+          for (int i = 0; i < 4; ++i) {
+            if (rows[i] >= 0)
+              *reinterpret_cast<uint4*>(p.out + rows[i] * D + c_lo + 32 * c + 8 * (lane & 3)) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+          }
         }
+        __syncwarp();
         free_o();
         if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, notes, lo, hi, c_lo, c_lo + OC, out);
         if (live && half == 0 && p.lse != nullptr)
@@ -1115,6 +1149,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                  (((c & 7) ^ (row & 7)) << 4);
         };
         if (ct < kPoison * 4) notes[ct] = 0u;
+        if (!folds) {
+          for (int i = ct; i < M; i += kProdThreads) rscale[(k & 1) * M + i] = 1.f;
+        }
         if (ct == 0) slot[kBadPage + (k & 1)] = *any = 0;
         // token and head of the vector, and its address, go on by sums: with a division for each chunk
         // an item of 256 vectors spent 14 500 cycles here, more than on all else
@@ -1138,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             src += wrap;
           }
         }
-        asm volatile("bar.sync 9, 128;\n" ::: "memory");  // the notes are clear
+        asm volatile("bar.sync 9, 128;\n" ::: "memory");  // the notes are clear, the scales 1
         // pages out of range among those attended (their tokens are skipped)
         if (p.table != nullptr) {
           const int lo = p.window < 0 ? 0 : max(it.q.len - it.q.n + it.first - p.window, 0);
@@ -1154,20 +1191,34 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
         cp_async_wait_all();
+        // a query that is not finite makes its row NaN whatever its scores come to
         float* scales = rscale + (k & 1) * M;
-#pragma unroll(SRC == kF16 ? 4 : 1)
-        for (int i = 0; i < kChunks; ++i) {
-          int row, c;
-          const uint32_t dst = at(i, row, c);
-          uint4 x = lds16(dst);
-          // a query that is not finite makes its row NaN whatever its scores come to
-          uint4 y = x;
-          const unsigned odd = __ballot_sync(0xffffffffu, finite_only(y));
-          const unsigned of_row = (CPR == 32 ? 0xffffffffu : ((1u << (CPR & 31)) - 1u) << (lane & ~(CPR - 1)));
-          float rsc = 1.f;
-          if (folds) {
-            const float4 k0 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * c));
-            const float4 k1 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * c) + 1);
+        if (!folds) {
+          uint32_t odd = 0;  // the thread's chunks that hold such a value
+#pragma unroll 8
+          for (int i = 0; i < kChunks; ++i) {
+            int row, c;
+            const uint32_t dst = at(i, row, c);
+            const uint4 x = lds16(dst);
+            odd |= (uint32_t)not_finite(x) << i;
+            if (flips) sts16(dst, make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u));
+          }
+          for (; odd != 0; odd &= odd - 1) {
+            int row, c;
+            at(__ffs(odd) - 1, row, c);
+            scales[row] = __int_as_float(0x7fc00000);
+          }
+        } else {
+          // (a thread's chunks are all of the same channels)
+          const float4 k0 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * (ct % CPR)));
+          const float4 k1 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * (ct % CPR)) + 1);
+#pragma unroll 2
+          for (int i = 0; i < kChunks; ++i) {
+            int row, c;
+            const uint32_t dst = at(i, row, c);
+            uint4 x = lds16(dst);
+            const unsigned odd = __ballot_sync(0xffffffffu, not_finite(x));
+            const unsigned of_row = (CPR == 32 ? 0xffffffffu : ((1u << (CPR & 31)) - 1u) << (lane & ~(CPR - 1)));
             const __half2* h = reinterpret_cast<const __half2*>(&x);
             float f[8];
 #pragma unroll
@@ -1189,13 +1240,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
             for (int u = 0; u < 8; ++u) f[u] *= down;
-            x = make_uint4(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]), pack_h2(f[4], f[5]), pack_h2(f[6], f[7]));
-            rsc = __uint_as_float((uint32_t)(127 + e) << 23);
-            sts16(dst, x);
-          } else if (flips) {
-            sts16(dst, make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u));
+            sts16(dst, make_uint4(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]), pack_h2(f[4], f[5]), pack_h2(f[6], f[7])));
+            if (c == 0) scales[row] = odd & of_row ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(127 + e) << 23);
           }
-          if (c == 0) scales[row] = odd & of_row ? __int_as_float(0x7fc00000) : rsc;
         }
         tc::fence_smem_to_async();
         warp_arrive(bar(kQFull + (k & 1)));
