@@ -670,20 +670,27 @@ __device__ __forceinline__ void convert_bytes(int ct, uint32_t at, uint32_t dst,
                                               int row0, volatile int* any) {
   using R = Raw<D, TILES, SRC>;
   const int rows = is_v ? Layout<D, TILES>::kVRows : BN;
+  // 8 lanes take 64 bytes of each of two rows, from different halves of them: neither their loads nor
+  // their stores meet a bank twice
+  const int c = ct & 3;
+  int row_of[4], slab_of[4];
+  uint4 code[4];  // (all on their way before the first is used)
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    // 8 lanes take 64 bytes of each of two rows, from different halves of them: neither their loads nor
-    // their stores meet a bank twice
-    const int q = ct + kProdThreads * k, c = q & 3;
-    int row = q >> 2, slab = 0;
+    const int q = ct + kProdThreads * k;
+    row_of[k] = q >> 2;
+    slab_of[k] = 0;
     if (D != 64) {
-      const int odd = row & 1, pr = q >> 3;
-      row = 2 * (pr % (R::kRows / 2)) + odd;
-      slab = odd ^ (pr / (R::kRows / 2));
+      const int odd = row_of[k] & 1, pr = q >> 3;
+      row_of[k] = 2 * (pr % (R::kRows / 2)) + odd;
+      slab_of[k] = odd ^ (pr / (R::kRows / 2));
     }
-    const uint4 x = lds16(at + row * R::kWide + slab * 64 + c * 16);
-    row += R::first_row(u, is_v);
-    slab += R::first_slab(u, is_v);
+    code[k] = lds16(at + row_of[k] * R::kWide + slab_of[k] * 64 + c * 16);
+  }
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    const uint4 x = code[k];
+    const int row = row_of[k] + R::first_row(u, is_v), slab = slab_of[k] + R::first_slab(u, is_v);
     uint4 h[2];
     if constexpr (SRC == kI8) {
       const uint32_t x0 = flip_i8x4(x.x), x1 = flip_i8x4(x.y), x2 = flip_i8x4(x.z), x3 = flip_i8x4(x.w);
@@ -707,14 +714,20 @@ __device__ __forceinline__ void convert_mx4(int ct, uint32_t at, uint32_t dst, i
                                             uint32_t* bits, int row0, volatile int* any) {
   const int row = ct >> 1, c = ct & 1;  // 32 channels of each slab
   const uint32_t rec = at + (row >> 4) * (9 * D);
+  uint4 code[N];
+  uint16_t scale[N];  // two block scales each
 #pragma unroll
   for (int k = 0; k < N; ++k) {
-    const uint4 x = lds16(rec + (row & 15) * (D / 2) + (slab0 + k) * 32 + c * 16);
-    uint16_t both;  // the block scales
+    code[k] = lds16(rec + (row & 15) * (D / 2) + (slab0 + k) * 32 + c * 16);
     asm volatile("ld.shared.u16 %0, [%1];\n"
-                 : "=h"(both)
+                 : "=h"(scale[k])
                  : "r"(rec + 8 * D + (row & 15) * (D / 16) + (slab0 + k) * 4 + 2 * c)
                  : "memory");
+  }
+#pragma unroll
+  for (int k = 0; k < N; ++k) {
+    const uint4 x = code[k];
+    const uint16_t both = scale[k];
     uint32_t s0, s1;  // twice each
     e4m3x4_to_h2x2(prmt(both, 0u, 0x1100u), s0, s1);
     uint4 h[4];
@@ -1558,6 +1571,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
                 }
                 // (bytes that land before they are announced are counted all the same)
                 const unsigned mask = __ballot_sync(0xffffffffu, copies);
+                __syncwarp();  // the zeros are there
                 if (lane == 0) tc::mbar_arrive_expect_tx(bar(kRawFull + place), __popc(mask) * 9 * D);
               } else {
                 // rows of the block and channels that the unit has
