@@ -566,15 +566,20 @@ __device__ __forceinline__ bool next_item(const AttendParams& p, Item& it, Walk&
   return true;
 }
 
-// The 16-row group that holds position pos of sequence b, as a row number / 16 of the cache; -1
-// where the position is not attended by any (past the end) or its page is out of range.
-__device__ __forceinline__ int group_of(const AttendParams& p, const Item& it, int pos) {
+// The 16-row group that holds position pos of the item's sequence, as a row number / 16 of the cache; -1
+// where the position is not attended by any (past the end) or its page is out of range.  In two parts,
+// so that the table can be read well before its entry is needed.
+__device__ __forceinline__ int page_of(const AttendParams& p, const Item& it, int pos) {  // as the table has it
   if (pos >= it.q.len) return -1;
-  const int page = p.bs_log2 >= 0 ? pos >> p.bs_log2 : pos / p.bs;
-  const int off = pos - page * p.bs;
-  const int blk = __ldg(p.table + (long long)it.b * p.max_blocks + page);
-  if (blk < 0 || blk >= p.num_blocks) return -1;
-  return (int)((long long)blk * (p.bs >> 4)) + (off >> 4);
+  return __ldg(p.table + (long long)it.b * p.max_blocks + (p.bs_log2 >= 0 ? pos >> p.bs_log2 : pos / p.bs));
+}
+__device__ __forceinline__ int group_in(const AttendParams& p, int page, int pos) {
+  if (page < 0 || page >= p.num_blocks) return -1;
+  const int off = p.bs_log2 >= 0 ? pos & (p.bs - 1) : pos % p.bs;
+  return (int)((long long)page * (p.bs >> 4)) + (off >> 4);
+}
+__device__ __forceinline__ int group_of(const AttendParams& p, const Item& it, int pos) {
+  return group_in(p, page_of(p, it, pos), pos);
 }
 
 // V[t, g, d] as stored (without v_scale), for the values that are added back.
@@ -646,6 +651,26 @@ struct Raw {
   static __device__ __forceinline__ int first_slab(int u, bool is_v) { return D == 256 && is_v ? 2 * u : 0; }
 };
 
+// A place of the ring and the parity of its turn, one unit after another.
+template <int N>
+struct Place {
+  int place = 0;
+  uint32_t turn = 0;
+  __device__ __forceinline__ void next() {
+    if (++place >= N) {
+      place = 0;
+      turn ^= 1u;
+    }
+  }
+  __device__ __forceinline__ void back(int units) {
+    place -= units;
+    if (place < 0) {
+      place += N;
+      turn ^= 1u;
+    }
+  }
+};
+
 // N chunks of 8 fp16 values into a line of a part (64 channels of a row); a NaN or infinity is noted
 // and zeroed where the rows are looked at (bits not nullptr).
 template <int N>
@@ -664,33 +689,39 @@ __device__ __forceinline__ void store_chunks(uint4 (&h)[N], uint32_t line, int f
   for (int j = 0; j < N; ++j) sts16(line + (((first + j) ^ (row_in_part & 7)) << 4), h[j]);
 }
 
-// int8, e4m3fn: unit u of a part, as fp16.  bits: of the block's rows, from row0 on, that have a NaN.
-template <int D, int TILES, int SRC>
-__device__ __forceinline__ void convert_bytes(int ct, uint32_t at, uint32_t dst, bool is_v, int u, uint32_t* bits,
-                                              int row0, volatile int* any) {
+// int8, e4m3fn: U units of a part, from u on, as fp16.  bits: of the block's rows, from row0 on, that have a NaN.
+template <int D, int TILES, int SRC, int U>
+__device__ __forceinline__ void convert_bytes(int ct, const uint32_t (&at)[U], uint32_t dst, bool is_v, int u,
+                                              uint32_t* bits, int row0, volatile int* any) {
   using R = Raw<D, TILES, SRC>;
   const int rows = is_v ? Layout<D, TILES>::kVRows : BN;
   // 8 lanes take 64 bytes of each of two rows, from different halves of them: neither their loads nor
   // their stores meet a bank twice
   const int c = ct & 3;
-  int row_of[4], slab_of[4];
-  uint4 code[4];  // (all on their way before the first is used)
-#pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  auto place = [&](int k, int& row, int& slab) {
     const int q = ct + kProdThreads * k;
-    row_of[k] = q >> 2;
-    slab_of[k] = 0;
+    row = q >> 2;
+    slab = 0;
     if (D != 64) {
-      const int odd = row_of[k] & 1, pr = q >> 3;
-      row_of[k] = 2 * (pr % (R::kRows / 2)) + odd;
-      slab_of[k] = odd ^ (pr / (R::kRows / 2));
+      const int odd = row & 1, pr = q >> 3;
+      row = 2 * (pr % (R::kRows / 2)) + odd;
+      slab = odd ^ (pr / (R::kRows / 2));
     }
-    code[k] = lds16(at + row_of[k] * R::kWide + slab_of[k] * 64 + c * 16);
+  };
+  uint4 code[4 * U];  // (all on their way before the first is used)
+#pragma unroll
+  for (int k = 0; k < 4 * U; ++k) {
+    int row, slab;
+    place(k & 3, row, slab);
+    code[k] = lds16(at[k >> 2] + row * R::kWide + slab * 64 + c * 16);
   }
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 4 * U; ++k) {
     const uint4 x = code[k];
-    const int row = row_of[k] + R::first_row(u, is_v), slab = slab_of[k] + R::first_slab(u, is_v);
+    int row, slab;
+    place(k & 3, row, slab);
+    row += R::first_row(u + (k >> 2), is_v);
+    slab += R::first_slab(u + (k >> 2), is_v);
     uint4 h[2];
     if constexpr (SRC == kI8) {
       const uint32_t x0 = flip_i8x4(x.x), x1 = flip_i8x4(x.y), x2 = flip_i8x4(x.z), x3 = flip_i8x4(x.w);
@@ -1140,7 +1171,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
     const int ct = tid - kSoftThreads;
     const bool folds = SRC != kF16 && p.per_channel;
     const bool flips = SRC != kF16 && !p.per_channel && __ldg(p.k_scale) < 0.f;
-    int n = 0, units = 0;  // units converted by this CTA
+    int n = 0;
+    Place<Raw<D, TILES, SRC>::kAhead> ring;
     bool ok = true;
     for (int k = 0; take(k); ++k) {
       const Item& it = item_of(k);
@@ -1290,43 +1322,61 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       } else {
         // K runs one block ahead of V: K(0), K(1), V(0), K(2), V(1), ...; a run is one block of one of the two
         using R = Raw<D, TILES, SRC>;
+        // units to a turn: two, whose waits and loads then go together (of 3300 cycles for a block of 128
+        // positions half were waits), where the registers suffice
+        constexpr bool kShares = SRC == kMx4 && P == 2;  // both halves of a K block are in the same two units
+        constexpr int U = SRC == kI8 && TILES == 1 && R::kRun / P > 1 ? 2 : 1;
+        const int blk0 = it.blk0;
         stage_queries();
 #pragma unroll 1
         for (int r = 0; ok && r <= 2 * nb; ++r) {
           const bool is_v = r > 0 && (r & 1) == 0;
           const int i = r == 0 ? 0 : is_v ? r / 2 - 1 : (r + 1) / 2;
           if (nb == 0 || (!is_v && i >= nb)) continue;
-          const int nn = n + i, blk = it.blk0 + i;
+          const int nn = n + i, blk = blk0 + i;
           uint32_t* bits = SRC != kI8 && is_v && it.partial(blk) ? notes + 4 * it.ordinal(blk) : nullptr;
 #pragma unroll 1
           for (int j = 0; ok && j < P; ++j) {
             const int at = spot(nn, j);
             const uint32_t dst = sbase + (is_v ? L::kV : L::kK) + at * L::kPart;
             if (nn * P + j >= N) ok = warp_wait(bar((is_v ? kVFree : kKFree) + at), turn(nn, j) ^ 1, slot + kAbort);
-            // the part's units of the ring; MX4: both halves of the K of head_dim 256 are in the same two
-            constexpr bool kShares = SRC == kMx4 && P == 2;
             const bool shares = kShares && !is_v;
             const int here = shares ? 2 : R::kRun / P;
+            if (shares && j > 0) ring.back(2);
 #pragma unroll 1
-            for (int u = 0; ok && u < here; ++u) {
-              const int unit = units + (shares ? u : 0), place = unit % R::kAhead;
-              const uint32_t from = sbase + R::kAt + place * R::kBytes;
-              if (!shares || j == 0) ok = warp_wait(bar(kRawFull + place), (unit / R::kAhead) & 1, slot + kAbort);
-              if constexpr (SRC == kMx4) {
-                if (shares)
-                  convert_mx4<D, L::kKSlabs>(ct, from, dst, BN, 64 * u, j * L::kKSlabs, nullptr, 0, nullptr);
-                else
-                  convert_mx4<D, L::kSlabs>(ct, from, dst, is_v ? L::kVRows : BN, 64 * u, 0, bits, j * L::kVRows + 64 * u, any);
-              } else {
-                convert_bytes<D, TILES, SRC>(ct, from, dst, is_v, u, bits, j * L::kVRows, any);
+            for (int u = 0; ok && u < here; u += U) {
+              uint32_t from[U];
+              uint32_t freed[U];
+#pragma unroll
+              for (int w = 0; w < U; ++w) {
+                from[w] = sbase + R::kAt + ring.place * R::kBytes;
+                freed[w] = bar(kRawFree + ring.place);
+                if (!shares || j == 0) ok = warp_wait(bar(kRawFull + ring.place), ring.turn, slot + kAbort) && ok;
+                ring.next();
               }
-              if (!shares || j == P - 1) warp_arrive(bar(kRawFree + place));
-              if (!shares) ++units;
+              if constexpr (SRC == kMx4) {
+#pragma unroll
+                for (int w = 0; w < U; ++w) {
+                  if (shares)
+                    convert_mx4<D, L::kKSlabs>(ct, from[w], dst, BN, 64 * (u + w), j * L::kKSlabs, nullptr, 0, nullptr);
+                  else
+                    convert_mx4<D, L::kSlabs>(ct, from[w], dst, is_v ? L::kVRows : BN, 64 * (u + w), 0, bits,
+                                              j * L::kVRows + 64 * (u + w), any);
+                }
+              } else {
+                convert_bytes<D, TILES, SRC, U>(ct, from, dst, is_v, u, bits, j * L::kVRows, any);
+              }
+              if (!shares || j == P - 1) {
+                __syncwarp();
+                if (lane == 0) {
+#pragma unroll
+                  for (int w = 0; w < U; ++w) tc::mbar_arrive(freed[w]);
+                }
+              }
             }
             tc::fence_smem_to_async();
             warp_arrive(bar((is_v ? kVOk : kKFull) + at));
           }
-          if (SRC == kMx4 && P == 2 && !is_v) units += 2;
         }
       }
       n += nb;
@@ -1482,6 +1532,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       bool ok = true;
       int nk = 0, nv = 0;  // parts begun
       int units = 0;       // units begun
+      constexpr int kBoxes = SRC == kF16 ? 8 : Raw<D, TILES, SRC>::kRows / 16;  // of a unit of codes
+      constexpr int kStep = Raw<D, TILES, SRC>::kAhead >= 6 ? 8 / kBoxes : 1;
+      constexpr int kAsk = kBoxes * kStep;  // lanes that ask for data
+      const int my_unit = lane / kBoxes % kStep;  // of a step
+      Place<Raw<D, TILES, SRC>::kAhead> ring;
+      if (my_unit == 1) ring.next();
       for (int k = 0; warp == kTmaWarp && take(k); ++k) {
         const Item& it = item_of(k);
         const int nb = ok ? it.blk1 - it.blk0 : 0;
@@ -1490,8 +1546,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           // pages: boxes of 16 rows, a lane each (slab-major: group i of the part, slab i / groups); packed rows: a box for
           // each slab of the part
           constexpr int kVGroups = L::kVRows / 16;
-          auto groups_of = [&](int blk) -> int {  // first row of group lane % 8
-            const int grp = blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
+          // (the table is read a block before its pages are asked for)
+          const int blk0 = it.blk0, blk1 = it.blk1;
+          auto pages_of = [&](int blk) -> int { return blk < blk1 ? page_of(p, it, blk * BN + 16 * (lane & 7)) : -1; };
+          auto groups_of = [&](int blk, int page) -> int {  // first row of group lane % 8
+            const int grp = group_in(p, page, blk * BN + 16 * (lane & 7));
             return grp < 0 ? p.rows : grp * 16;  // (a row past the end is read as zeros)
           };
           auto copy = [&](int i, int j, bool is_v, int groups) -> bool {
@@ -1521,69 +1580,78 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             if (mine) tma_box(dst, is_v ? &a.vm : &a.km, 64 * slab, it.g, row, bar(full));
             return true;
           };
-          int g0 = 0, g1 = 0, g2 = 0;
+          int g0 = 0, g1 = 0, next = 0;
           if (paged) {
-            g0 = groups_of(it.blk0);
-            g1 = groups_of(it.blk0 + 1);
+            const int first = pages_of(blk0);
+            next = pages_of(blk0 + 1);
+            g1 = groups_of(blk0, first);
           }
           for (int i = -1; ok && i < nb; ++i) {  // K runs one block ahead of V
-            if (paged) g2 = groups_of(it.blk0 + i + 2);
-            for (int j = 0; ok && i + 1 < nb && j < P; ++j) ok = copy(i + 1, j, false, i < 0 ? g0 : g1);
+            for (int j = 0; ok && i + 1 < nb && j < P; ++j) ok = copy(i + 1, j, false, g1);
             for (int j = 0; ok && i >= 0 && j < P; ++j) ok = copy(i, j, true, g0);
-            if (i >= 0) {
+            if (paged) {
               g0 = g1;
-              g1 = g2;
+              g1 = groups_of(blk0 + i + 2, next);
+              next = pages_of(blk0 + i + 3);
             }
           }
         } else {
+          // Up to two units to a step, whose 8 boxes or record halves 8 lanes ask for, each after a look at its own
+          // unit's place (one unit at a time took 600 cycles each, and all others waited for the data)
           using R = Raw<D, TILES, SRC>;
-          auto groups_of = [&](int blk) -> int {  // group lane % 8 of the block
-            return blk < it.blk1 ? group_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
+          const int blk0 = it.blk0, blk1 = it.blk1;
+          auto pages_of = [&](int blk) -> int {  // of group lane % 8 of the block, read a block ahead
+            return blk < blk1 ? page_of(p, it, blk * BN + 16 * (lane & 7)) : -1;
           };
-          int gk = groups_of(it.blk0), gv = 0, gn = groups_of(it.blk0 + 1);
+          auto groups_of = [&](int blk, int page) -> int { return group_in(p, page, blk * BN + 16 * (lane & 7)); };
+          const int first = pages_of(blk0);
+          int next = pages_of(blk0 + 1);
+          int gk = groups_of(blk0, first), gv = 0;
           for (int r = 0; ok && r <= 2 * nb; ++r) {  // runs as the converters take them
             const bool is_v = r > 0 && (r & 1) == 0;
             if (r & 1) {
+              const int blk = blk0 + (r + 1) / 2;
               gv = gk;
-              gk = gn;
-              gn = groups_of(it.blk0 + (r + 1) / 2 + 1);
+              gk = groups_of(blk, next);
+              next = pages_of(blk + 1);
             }
             if (nb == 0 || (!is_v && (r + 1) / 2 >= nb)) continue;
-            for (int ru = 0; ru < R::kRun; ++ru) {
-              const int place = units % R::kAhead;
-              if (units >= R::kAhead && !(ok = warp_wait(bar(kRawFree + place), ((units / R::kAhead) & 1) ^ 1, slot + kAbort)))
-                break;
-              ++units;
-              const uint32_t dst = sbase + R::kAt + place * R::kBytes;
+            for (int ru = 0; ru < R::kRun; ru += kStep) {
+              const int full = bar(kRawFull + ring.place);
+              const uint32_t dst = sbase + R::kAt + ring.place * R::kBytes;
+              if (!(ok = warp_wait(bar(kRawFree + ring.place), ring.turn ^ 1, slot + kAbort))) break;
+              units += kStep;
+#pragma unroll
+              for (int w = 0; w < kStep; ++w) ring.next();
+              const int unit = ru + my_unit, box = lane % kBoxes;
               if constexpr (SRC == kMx4) {
-                const int grp = __shfl_sync(0xffffffffu, is_v ? gv : gk, 4 * ru + (lane & 3));
-                const uint32_t here = dst + lane * 9 * D;
-                const bool copies = lane < 4 && grp >= 0;
+                const int grp = __shfl_sync(0xffffffffu, is_v ? gv : gk, 4 * unit + box);
+                const uint32_t here = dst + box * 9 * D;
+                const bool copies = lane < kAsk && grp >= 0;
                 if (copies) {
                   const int tiles = p.bs >> 4;
                   const int page = p.bs_log2 >= 0 ? grp >> (p.bs_log2 - 4) : grp / tiles;
                   tc::bulk_g2s(here, reinterpret_cast<const uint8_t*>(p.k) +
                                          (((long long)page * p.Hkv + it.g) * tiles + (grp - page * tiles)) * (18LL * D) +
                                          (is_v ? 9 * D : 0),
-                               9 * D, bar(kRawFull + place));
-                } else if (lane < 4) {
+                               9 * D, full);
+                } else if (lane < kAsk) {
                   for (int b = 0; b < 9 * D; b += 16) sts16(here + b, make_uint4(0u, 0u, 0u, 0u));
                 }
                 // (bytes that land before they are announced are counted all the same)
-                const unsigned mask = __ballot_sync(0xffffffffu, copies);
+                const unsigned mask = __ballot_sync(0xffffffffu, copies) >> (lane & ~3) & 15u;
                 __syncwarp();  // the zeros are there
-                if (lane == 0) tc::mbar_arrive_expect_tx(bar(kRawFull + place), __popc(mask) * 9 * D);
+                if (lane < kAsk && box == 0) tc::mbar_arrive_expect_tx(full, __popc(mask) * 9 * D);
               } else {
                 // rows of the block and channels that the unit has
-                const int j = ru / (R::kRun / P), u = ru % (R::kRun / P);
+                const int j = unit / (R::kRun / P), u = unit % (R::kRun / P);
                 const int row0 = (is_v ? j * L::kVRows : 0) + R::first_row(u, is_v);
                 const int c0 = 64 * ((is_v ? 0 : j * L::kKSlabs) + R::first_slab(u, is_v));
-                if (lane == 0) tc::mbar_arrive_expect_tx(bar(kRawFull + place), R::kBytes);
-                const int grp = __shfl_sync(0xffffffffu, is_v ? gv : gk, row0 / 16 + (lane & 7));
+                if (lane < kAsk && box == 0) tc::mbar_arrive_expect_tx(full, R::kBytes);
+                const int grp = __shfl_sync(0xffffffffu, is_v ? gv : gk, row0 / 16 + box);
                 __syncwarp();
-                if (lane < R::kRows / 16)  // (a row past the end is read as zeros)
-                  tma_box(dst + lane * 16 * R::kWide, is_v ? &a.vm : &a.km, c0, it.g, grp < 0 ? p.rows : grp * 16,
-                          bar(kRawFull + place));
+                if (lane < kAsk)  // (a row past the end is read as zeros)
+                  tma_box(dst + box * 16 * R::kWide, is_v ? &a.vm : &a.km, c0, it.g, grp < 0 ? p.rows : grp * 16, full);
               }
             }
           }
