@@ -671,22 +671,23 @@ struct Place {
   }
 };
 
-// N chunks of 8 fp16 values into a line of a part (64 channels of a row); a NaN or infinity is noted
-// and zeroed where the rows are looked at (bits not nullptr).
+// N chunks of 8 fp16 values into a line of a part (64 channels of a row).
 template <int N>
-__device__ __forceinline__ void store_chunks(uint4 (&h)[N], uint32_t line, int first, int row_in_part, uint32_t* bits,
-                                             int row, volatile int* any) {
-  if (bits != nullptr) {
-    bool bad = false;
-#pragma unroll
-    for (int j = 0; j < N; ++j) bad |= finite_only(h[j]);
-    if (bad) {
-      atomicOr(bits + (row >> 5), 1u << (row & 31));
-      *any = 1;
-    }
-  }
+__device__ __forceinline__ void store_chunks(const uint4 (&h)[N], uint32_t line, int first, int row_in_part) {
 #pragma unroll
   for (int j = 0; j < N; ++j) sts16(line + (((first + j) ^ (row_in_part & 7)) << 4), h[j]);
+}
+
+// Zero the e4m3fn NaN codes (all ones but for the sign) among four; returns whether there were any.
+__device__ __forceinline__ bool numbers_only(uint32_t& x) {
+  const uint32_t nan = ((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+  x &= ~((nan >> 7) * 255u);
+  return nan != 0u;
+}
+// (bits, any: noted for a row of V where the rows are looked at)
+__device__ __forceinline__ void note_row(uint32_t* bits, int row, volatile int* any) {
+  atomicOr(bits + (row >> 5), 1u << (row & 31));
+  *any = 1;
 }
 
 // int8, e4m3fn: U units of a part, from u on, as fp16.  bits: of the block's rows, from row0 on, that have a NaN.
@@ -715,6 +716,22 @@ __device__ __forceinline__ void convert_bytes(int ct, const uint32_t (&at)[U], u
     place(k & 3, row, slab);
     code[k] = lds16(at[k >> 2] + row * R::kWide + slab * 64 + c * 16);
   }
+  if (SRC == kE4 && bits != nullptr) {
+#pragma unroll 1
+    for (int k = 0; k < 4 * U; ++k) {
+      // (a loop over registers: the chunk in turn is the first, the others move up)
+      uint4 x = code[0];
+      const bool a = numbers_only(x.x), b = numbers_only(x.y), c1 = numbers_only(x.z), d = numbers_only(x.w);
+      if (a || b || c1 || d) {
+        int row, slab;
+        place(k & 3, row, slab);
+        note_row(bits, row0 + row + R::first_row(u + (k >> 2), is_v), any);
+      }
+#pragma unroll
+      for (int e = 1; e < 4 * U; ++e) code[e - 1] = code[e];
+      code[4 * U - 1] = x;
+    }
+  }
 #pragma unroll
   for (int k = 0; k < 4 * U; ++k) {
     const uint4 x = code[k];
@@ -735,7 +752,7 @@ __device__ __forceinline__ void convert_bytes(int ct, const uint32_t (&at)[U], u
       e4m3x4_to_h2x2(x.z, h[1].x, h[1].y);
       e4m3x4_to_h2x2(x.w, h[1].z, h[1].w);
     }
-    store_chunks(h, dst + (slab * rows + row) * 128, 2 * c, row, SRC == kE4 ? bits : nullptr, row0 + row, any);
+    store_chunks(h, dst + (slab * rows + row) * 128, 2 * c, row);
   }
 }
 
@@ -754,6 +771,16 @@ __device__ __forceinline__ void convert_mx4(int ct, uint32_t at, uint32_t dst, i
                  : "=h"(scale[k])
                  : "r"(rec + 8 * D + (row & 15) * (D / 16) + (slab0 + k) * 4 + 2 * c)
                  : "memory");
+  }
+  if (bits != nullptr) {  // (a code is always a number, its scale perhaps not)
+    bool bad = false;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      uint32_t x = scale[k];
+      bad |= numbers_only(x);
+      scale[k] = (uint16_t)x;
+    }
+    if (bad) note_row(bits, row0 + row, any);
   }
 #pragma unroll
   for (int k = 0; k < N; ++k) {
@@ -774,7 +801,7 @@ __device__ __forceinline__ void convert_mx4(int ct, uint32_t at, uint32_t dst, i
       asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].z) : "r"(s));
       asm("mul.f16x2 %0, %0, %1;\n" : "+r"(h[j].w) : "r"(s));
     }
-    store_chunks(h, dst + (k * rows + row_in_part + row) * 128, 4 * c, row_in_part + row, bits, row0 + row, any);
+    store_chunks(h, dst + (k * rows + row_in_part + row) * 128, 4 * c, row_in_part + row);
   }
 }
 
@@ -1325,7 +1352,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // units to a turn: two, whose waits and loads then go together (of 3300 cycles for a block of 128
         // positions half were waits), where the registers suffice
         constexpr bool kShares = SRC == kMx4 && P == 2;  // both halves of a K block are in the same two units
-        constexpr int U = SRC == kI8 && TILES == 1 && R::kRun / P > 1 ? 2 : 1;
+        constexpr int U = SRC != kMx4 && TILES == 1 && R::kRun / P > 1 ? 2 : 1;
         const int blk0 = it.blk0;
         stage_queries();
 #pragma unroll 1
