@@ -1352,7 +1352,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         // units to a turn: two, whose waits and loads then go together (of 3300 cycles for a block of 128
         // positions half were waits), where the registers suffice
         constexpr bool kShares = SRC == kMx4 && P == 2;  // both halves of a K block are in the same two units
-        constexpr int U = SRC != kMx4 && TILES == 1 && R::kRun / P > 1 ? 2 : 1;
+        constexpr int U = TILES == 1 && R::kRun / P > 1 ? 2 : 1;
         const int blk0 = it.blk0;
         stage_queries();
 #pragma unroll 1
