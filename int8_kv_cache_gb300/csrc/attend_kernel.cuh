@@ -875,6 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   tc::fence_after_sync();
   const uint32_t tbase = static_cast<uint32_t>(slot[kTmem]);
   grid_dependency_wait();  // inputs may come from the previous kernel of the stream
+  if (p.pieces > 0) grid_launch_dependents();  // the merge, which waits for all of this kernel before it reads a partial
   // Every role goes through the CTA's items by itself; item `k` is read from shared memory, and given
   // back when the role is done with it.  A role whose wait failed goes on through the items without
   // working, so that the others' waits for it end.

@@ -17,7 +17,8 @@ template <int D, int M>
 __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const AttendParams p) {
   constexpr int V = D / 32;  // channels of a lane
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  grid_dependency_wait();
+  // The lengths are inputs of attend_kernel, which lets this kernel launch once it may read them itself:
+  // the cut is found while its last CTAs still work.
   const int cut = blockIdx.x + 1;
   long long total;
   const long long one = piece_length<M>(p, p.pieces, total);
@@ -27,6 +28,7 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Atten
   Length len;
   const long long x = find_place<M>(p, f, it, len);
   if (x == 0 || x > one) return;  // the cut is between two tiles, or not the first one in this one
+  grid_dependency_wait();  // the partials
   // pieces cut - 1 (its end), cut, ..., last (their beginnings)
   const int last = (int)((f + (len.of(it.t) - x) - 1) / one);
   const int v0 = it.t * M, nvec = it.q.n * p.G;

@@ -135,13 +135,17 @@ __device__ __forceinline__ uint32_t pack_h2(__half lo, __half hi) {
 __device__ __forceinline__ void grid_dependency_wait() {
   asm volatile("griddepcontrol.wait;\n" ::: "memory");
 }
+__device__ __forceinline__ void grid_launch_dependents() {
+  asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+}
 
-// One kernel lets its dependents launch early (griddepcontrol.
+// Two kernels let their dependents launch early (griddepcontrol.
 // launch_dependents): the 4-bit decode, when its loop is done
-// (mx4_kernel.cuh).  So a kernel that is launched with programmatic stream
-// serialization, whichever it is, may start while a 4-bit decode still
-// writes, and calls grid_dependency_wait before its first access to global
-// memory.  In the other kernels a trigger did not pay: measured on graphs of
+// (mx4_kernel.cuh), and the dense attention of a batch cut into pieces, at its
+// start (attend_kernel.cuh; only the merge of its partials follows it).  So a
+// kernel that is launched with programmatic stream serialization, whichever it
+// is, may start while a 4-bit decode still writes, and calls
+// grid_dependency_wait before its first access to global memory.  In the other kernels a trigger did not pay: measured on graphs of
 // decode calls, one at decode entry made the calls slower, and one at combine
 // entry took the sparse decode (S = 8) from 11.53 to 11.22 us per call but
 // the ragged paged decode from 37.3 to 40.8 us.
