@@ -22,6 +22,10 @@
 // head_dim 256, whose O fills tensor memory): one tile, scores double-buffered, two threads per
 // vector (64 positions each), which exchange their maxima through shared memory.
 //
+// A CTA stays for item after item (an item: a tile's, or two tiles', walk over the blocks of one KV
+// head), and every role goes on to the next by itself: its queries are staged and its first scores
+// made while the one before is still written out.  152 prompts of 64 tokens, 32 / 8 heads: 59 us.
+//
 // Warp roles (512 threads, registers dealt out anew with setmaxnreg):
 //   warps 0-7    softmax and epilogue
 //   warps 8-11   queries into shared memory; then, fp16 sources: look at the V blocks that some row
@@ -40,9 +44,15 @@
 // the largest entry comes to 2^14, so no range is lost; a score's error is at most
 // 2^-11 sum |q_d k_d|, what a cache of fp16 keys has).
 //
-// Splits (few vectors over long caches): the batch's blocks are cut into equal contiguous pieces,
-// one per CTA, whose ends fall anywhere in a (tile, KV head)'s range; a CTA works its
-// pieces one after another and writes partials that the combine kernel merges.
+// Pieces (few vectors over long caches): the batch's blocks are cut into equal contiguous pieces,
+// one per CTA, whose ends fall anywhere in a (tile, KV head)'s range; a CTA writes fp32 partials of
+// the two ranges at most that its piece's ends cut, which attend_merge.cu joins.
+//
+// What bounds it (32 / 8 heads x 128): a prompt of 16384 the tensor cores, at 73 % of their measured
+// rate, by the chain from a block's scores over its softmax to its product with V (2700 to 3000 cycles
+// for 2048 of products); a quantised cache with few new tokens its conversion, 2900 cycles per 128
+// positions of K and V of which 1800 are shared memory's (codes in and out, fp16 in, operands out);
+// a short call the way from the launch over the first item (2 us), its queries and a block's chain.
 //
 // Every wait is bounded; a CTA that gives up marks its outputs NaN and raises
 // I8KV_FLAG_WAIT_TIMEOUT.
@@ -171,15 +181,15 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const v
   }
   return __all_sync(0xffffffffu, ok);
 }
-// ... and the others, which work ahead, wait by one lane that sleeps between polls.
-__device__ __forceinline__ bool calm_wait(uint32_t bar, uint32_t parity, const volatile int* abort, unsigned ns) {
+// ... and for an item one lane waits, which sleeps between polls.
+__device__ __forceinline__ bool calm_wait(uint32_t bar, uint32_t parity) {
   bool ok = (threadIdx.x & 31) != 0 || tc::mbar_try_wait(bar, parity);
   if (!ok) {
     const uint64_t t0 = tc::global_ns();
     do {
-      __nanosleep(ns);
+      __nanosleep(100);
       ok = tc::mbar_try_wait(bar, parity);
-    } while (!ok && !(abort != nullptr && *abort) && tc::global_ns() - t0 <= tc::kWaitNs);
+    } while (!ok && tc::global_ns() - t0 <= tc::kWaitNs);
   }
   ok = __all_sync(0xffffffffu, ok);
   __syncwarp();  // (the vote orders no memory)
@@ -312,6 +322,13 @@ __device__ __forceinline__ Seq seq_of(const AttendParams& p, int b, bool report 
   return s;
 }
 
+// a / b of what is not negative, in 32 bits where that suffices (a division in 64 takes some 500 cycles where
+// nothing else runs).
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
 // One piece of a (tile, KV head)'s blocks.
 struct Item {
   Seq q;
@@ -430,7 +447,7 @@ __device__ __forceinline__ long long piece_length(const AttendParams& p, int pie
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  return (total + pieces - 1) / pieces;
+  return quotient(total + pieces - 1, pieces);
 }
 // The (tile, head) at place f < total of the batch: it.b, q, t, g, the lengths, and the place in it.
 template <int M>
@@ -462,7 +479,7 @@ __device__ __forceinline__ long long find_place(const AttendParams& p, long long
       }
       it.t = t;
       const long long in_tile = in_seq - p.Hkv * len.before(t);
-      it.g = (int)(in_tile / len.of(t));
+      it.g = (int)quotient(in_tile, len.of(t));
       return in_tile - it.g * len.of(t);
     }
     before = __shfl_sync(0xffffffffu, incl, 31);
@@ -561,7 +578,7 @@ __device__ __forceinline__ bool next_item(const AttendParams& p, Item& it, Walk&
   }
   const long long all = w.len.of(it.t), y = min(all, w.x + (w.end - w.f));
   // a CTA begins inside at most one tile and ends inside at most one
-  it.slot = w.x > 0 ? 2 * blockIdx.x : y < all ? 2 * blockIdx.x + 1 : -1;
+  it.slot = w.x > 0 ? 2 * (int)blockIdx.x : y < all ? 2 * (int)blockIdx.x + 1 : -1;
   place<M>(p, it, w.x, y, all);
   w.f += y - w.x;
   w.x = y;
@@ -887,7 +904,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   // (items of a very long context take their time: a limit of about two minutes)
   auto wait_item = [&](int b, uint32_t parity) -> bool {
     bool ok = false;
-    for (int i = 0; !ok && i < 10; ++i) ok = calm_wait(bar(b), parity, nullptr, 100);
+    for (int i = 0; !ok && i < 120; ++i) ok = calm_wait(bar(b), parity);
     if (!ok) slot[kAbort] = 1;
     return ok;
   };
@@ -931,7 +948,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       return ok;
     };
     const float cap_k = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
-    const bool folds = SRC != kF16 && p.per_channel;
     const float ks1 = SRC != kF16 && !p.per_channel ? __ldg(p.k_scale) : 1.f;
     int n = 0;  // blocks done by this CTA
     bool ok = true;
@@ -1251,6 +1267,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
         asm volatile("bar.sync 9, 128;\n" ::: "memory");  // the notes are clear, the scales 1
+        float4 k0 = make_float4(1.f, 1.f, 1.f, 1.f), k1 = k0;  // (a thread's chunks are all of the same channels)
+        if (folds) {
+          k0 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * (ct % CPR)));
+          k1 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * (ct % CPR)) + 1);
+        }
         // pages out of range among those attended (their tokens are skipped)
         if (p.table != nullptr) {
           const int lo = p.window < 0 ? 0 : max(it.q.len - it.q.n + it.first - p.window, 0);
@@ -1284,39 +1305,51 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             scales[row] = __int_as_float(0x7fc00000);
           }
         } else {
-          // (a thread's chunks are all of the same channels)
-          const float4 k0 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * (ct % CPR)));
-          const float4 k1 = __ldg(reinterpret_cast<const float4*>(p.k_scale + it.g * D + 8 * (ct % CPR)) + 1);
-#pragma unroll 2
-          for (int i = 0; i < kChunks; ++i) {
-            int row, c;
-            const uint32_t dst = at(i, row, c);
-            uint4 x = lds16(dst);
-            const unsigned odd = __ballot_sync(0xffffffffu, not_finite(x));
-            const unsigned of_row = (CPR == 32 ? 0xffffffffu : ((1u << (CPR & 31)) - 1u) << (lane & ~(CPR - 1)));
-            const __half2* h = reinterpret_cast<const __half2*>(&x);
-            float f[8];
+          // (chunks side by side: one after the other, each waits for its vector's maximum through the lanes)
+          constexpr int kSide = TILES == 2 ? 2 : 4;
+#pragma unroll 1
+          for (int i = 0; i < kChunks; i += kSide) {
+            float f[kSide][8], top[kSide];
+            uint32_t odd = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 z = __half22float2(h[e]);
-              f[2 * e] = z.x;
-              f[2 * e + 1] = z.y;
+            for (int w = 0; w < kSide; ++w) {
+              int row, c;
+              const uint4 x = lds16(at(i + w, row, c));
+              const __half2* h = reinterpret_cast<const __half2*>(&x);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 z = __half22float2(h[e]);
+                f[w][2 * e] = z.x;
+                f[w][2 * e + 1] = z.y;
+              }
+              odd |= (uint32_t)not_finite(x) << w;
+              f[w][0] *= k0.x, f[w][1] *= k0.y, f[w][2] *= k0.z, f[w][3] *= k0.w;
+              f[w][4] *= k1.x, f[w][5] *= k1.y, f[w][6] *= k1.z, f[w][7] *= k1.w;
+              top[w] = 0.f;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) top[w] = fmaxf(top[w], fabsf(f[w][e]));
             }
-            f[0] *= k0.x, f[1] *= k0.y, f[2] *= k0.z, f[3] *= k0.w;
-            f[4] *= k1.x, f[5] *= k1.y, f[6] *= k1.z, f[7] *= k1.w;
-            float top = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(f[e]));
+            for (int o = CPR / 2; o > 0; o >>= 1) {
 #pragma unroll
-            for (int o = CPR / 2; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // 2^e brings the largest entry into [2^14, 2^15): exponent fields, exact
-            const int ex = (int)((__float_as_uint(top) >> 23) & 255u);
-            const int e = ex == 0 || ex == 255 ? 0 : min(max(ex - 127 - 14, -126), 126);
-            const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+              for (int w = 0; w < kSide; ++w) top[w] = fmaxf(top[w], __shfl_xor_sync(0xffffffffu, top[w], o));
+              odd |= __shfl_xor_sync(0xffffffffu, odd, o);
+            }
 #pragma unroll
-            for (int u = 0; u < 8; ++u) f[u] *= down;
-            sts16(dst, make_uint4(pack_h2(f[0], f[1]), pack_h2(f[2], f[3]), pack_h2(f[4], f[5]), pack_h2(f[6], f[7])));
-            if (c == 0) scales[row] = odd & of_row ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(127 + e) << 23);
+            for (int w = 0; w < kSide; ++w) {
+              int row, c;
+              const uint32_t dst = at(i + w, row, c);
+              // 2^e brings the largest entry into [2^14, 2^15): exponent fields, exact
+              const int ex = (int)((__float_as_uint(top[w]) >> 23) & 255u);
+              const int e = ex == 0 || ex == 255 ? 0 : min(max(ex - 127 - 14, -126), 126);
+              const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+              for (int u = 0; u < 8; ++u) f[w][u] *= down;
+              sts16(dst, make_uint4(pack_h2(f[w][0], f[w][1]), pack_h2(f[w][2], f[w][3]), pack_h2(f[w][4], f[w][5]),
+                                    pack_h2(f[w][6], f[w][7])));
+              if (c == 0)
+                scales[row] = (odd >> w) & 1u ? __int_as_float(0x7fc00000) : __uint_as_float((uint32_t)(127 + e) << 23);
+            }
           }
         }
         tc::fence_smem_to_async();
