@@ -195,23 +195,85 @@ __device__ __forceinline__ void turn_item(float (&a)[8], float (&b)[8], const An
   }
 }
 
-// The norm of a head that the aligned `ipr` lanes of the warp hold (a power of two), 16 channels
-// each, in place.  All of them are here together: they work on the same token.
-__device__ __forceinline__ void norm_item(float (&a)[8], float (&b)[8], const float (&wa)[8],
-                                          const float (&wb)[8], int ipr, float eps) {
-  float ss = 0.f;
+// Two fp32 operations in one instruction, each rounded by itself.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+  uint64_t d;
+  asm("mov.b64 %0, {%1, %2};\n" : "=l"(d) : "f"(x), "f"(y));
+  return d;
+}
+__device__ __forceinline__ void from_two(uint64_t d, float& x, float& y) {
+  asm("mov.b64 {%0, %1}, %2;\n" : "=f"(x), "=f"(y) : "l"(d));
+}
+__device__ __forceinline__ uint64_t mul_two(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ uint64_t fma_two(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add_two(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// turn_item of halves two channels at a time, with the same roundings (a difference is a fused sum with
+// -1 times what is taken off).
+__device__ __forceinline__ void turn_halves(float (&a)[8], float (&b)[8], const Angles& g) {
+  const uint64_t c[4] = {two(g.c[0].x, g.c[0].y), two(g.c[0].z, g.c[0].w), two(g.c[1].x, g.c[1].y), two(g.c[1].z, g.c[1].w)};
+  const uint64_t s[4] = {two(g.s[0].x, g.s[0].y), two(g.s[0].z, g.s[0].w), two(g.s[1].x, g.s[1].y), two(g.s[1].z, g.s[1].w)};
+  const uint64_t minus = two(-1.f, -1.f);
 #pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(a[i], a[i], ss);
-#pragma unroll
-  for (int i = 0; i < 8; ++i) ss = fmaf(b[i], b[i], ss);
+  for (int i = 0; i < 4; ++i) {
+    const uint64_t x = two(a[2 * i], a[2 * i + 1]), y = two(b[2 * i], b[2 * i + 1]);
+    from_two(fma_two(mul_two(y, s[i]), minus, mul_two(x, c[i])), a[2 * i], a[2 * i + 1]);
+    from_two(add_two(mul_two(y, c[i]), mul_two(x, s[i])), b[2 * i], b[2 * i + 1]);
+  }
+}
+
+// The norms of N heads, each of which the aligned `ipr` lanes of the warp (a power of two) hold, 16
+// channels each, as fp16: r = 1 / sqrt(mean + eps).  All of those lanes are here together: they work
+// on the same tokens.  The heads side by side: one after the other, each waits for its sum through the
+// lanes, and rsqrtf, which is within 2 units of the last place, for the correctly rounded root, which
+// takes some 30 instructions (16384 tokens, 32/8 heads, head_dim 128, half of it turned: 105 us one by
+// one; side by side 83 into MX4 and 94 into int8; with rsqrtf 78 and 81; not normed 61 and 63).
+template <int N>
+__device__ __forceinline__ void norms_of(const uint4 (&a)[N], const uint4 (&b)[N], int ipr, float eps, float (&r)[N]) {
   const int lane = threadIdx.x & 31;
   const unsigned of_head = ((1u << ipr) - 1u) << (lane & ~(ipr - 1));
-  for (int o = ipr >> 1; o > 0; o >>= 1) ss += __shfl_xor_sync(of_head, ss, o);
-  const float r = __frsqrt_rn(fmaf(ss, 1.f / (float)(16 * ipr), eps));
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    a[i] = __fmul_rn(__fmul_rn(a[i], r), wa[i]);
-    b[i] = __fmul_rn(__fmul_rn(b[i], r), wb[i]);
+  for (int i = 0; i < N; ++i) {
+    float x[8], y[8];
+    unpack8(a[i], x);
+    unpack8(b[i], y);
+    uint64_t sum = 0;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const uint64_t u = two(x[e], x[e + 1]), v = two(y[e], y[e + 1]);
+      sum = fma_two(u, u, sum);
+      sum = fma_two(v, v, sum);
+    }
+    float lo, hi;
+    from_two(sum, lo, hi);
+    r[i] = lo + hi;
+  }
+  for (int o = ipr >> 1; o > 0; o >>= 1) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) r[i] += __shfl_xor_sync(of_head, r[i], o);
+  }
+  const float each = 0.0625f / (float)ipr;
+#pragma unroll
+  for (int i = 0; i < N; ++i) r[i] = rsqrtf(fmaf(r[i], each, eps));
+}
+__device__ __forceinline__ void norm_item(float (&a)[8], float (&b)[8], const float (&wa)[8],
+                                          const float (&wb)[8], float r) {
+  const uint64_t rr = two(r, r);
+#pragma unroll
+  for (int i = 0; i < 8; i += 2) {
+    from_two(mul_two(mul_two(two(a[i], a[i + 1]), rr), two(wa[i], wa[i + 1])), a[i], a[i + 1]);
+    from_two(mul_two(mul_two(two(b[i], b[i + 1]), rr), two(wb[i], wb[i + 1])), b[i], b[i + 1]);
   }
 }
 __device__ __forceinline__ void weights8(const float* w, int at, float (&x)[8]) {
@@ -375,17 +437,23 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
       const __half* row = p.q + n * p.q_stride + (long long)h0 * p.D;
       uint4 ra[HQ], rb[HQ];
 #pragma unroll
-      for (int i = 0; i < HQ; ++i)
+      for (int i = 0; i < HQ; ++i) {
+        if (NORM) ra[i] = rb[i] = make_uint4(0u, 0u, 0u, 0u);
         if (h0 + i < p.Hq) {
           ra[i] = *reinterpret_cast<const uint4*>(row + i * p.D + x.c0);
           rb[i] = *reinterpret_cast<const uint4*>(row + i * p.D + x.c1);
         }
+      }
       Angles g;
       if (p.R > 0) {
         if (pos < 0 || (long long)pos >= p.max_pos) continue;
         if (x.turned) g = angles_of(p, x, pos);
       }
       __half* out = p.q_out + (n * p.Hq + h0) * p.D;
+      float r[HQ];
+      if constexpr (NORM) {
+        if (normed) norms_of(ra, rb, ipr, p.eps, r);
+      }
 #pragma unroll
       for (int i = 0; i < HQ; ++i)
         if (h0 + i < p.Hq) {
@@ -394,9 +462,10 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
             unpack8(ra[i], a);
             unpack8(rb[i], b);
             if constexpr (NORM) {
-              if (normed) norm_item(a, b, w0, w1, ipr, p.eps);
+              if (normed) norm_item(a, b, w0, w1, r[i]);
             }
-            if (!NORM || x.turned) turn_item(a, b, g, il);
+            if (NORM && x.turned && !il) turn_halves(a, b, g);
+            else if (!NORM || x.turned) turn_item(a, b, g, il);
             ra[i] = pack8(a);
             rb[i] = pack8(b);
           }
@@ -475,7 +544,7 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
   look(n0);
   int st = 0;
   for (long long n = n0; n < p.num_tokens; n += N * lanes, st ^= 1) {
-    uint4 raw[N][2];
+    uint4 raw[N][2] = {};
     if constexpr (RING) {
       fetch(n + N * lanes, st ^ 1);
     } else {
@@ -508,6 +577,18 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
     }
     look(n + N * lanes);
     if constexpr (RING) asm volatile("cp.async.wait_group 1;\n" ::: "memory");
+    float r[N];
+    if constexpr (NORM) {
+      if (normed) {  // (of a token that is left out too, whatever its place holds)
+        uint4 ra[N], rb[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          ra[i] = RING ? ring[st][i][0][threadIdx.x] : raw[i][0];
+          rb[i] = RING ? ring[st][i][1][threadIdx.x] : raw[i][1];
+        }
+        norms_of(ra, rb, ipr, p.eps, r);
+      }
+    }
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       if (at[i] < 0 && !out[i]) continue;
@@ -515,9 +596,10 @@ rope_and_cache_kernel(const AppendParams p, long long q_lanes, long long kv_lane
       unpack8(RING ? ring[st][i][0][threadIdx.x] : raw[i][0], a);
       unpack8(RING ? ring[st][i][1][threadIdx.x] : raw[i][1], b);
       if constexpr (NORM) {
-        if (normed) norm_item(a, b, w0, w1, ipr, p.eps);
+        if (normed) norm_item(a, b, w0, w1, r[i]);
       }
-      if (x.turned) turn_item(a, b, g[i], il);
+      if (NORM && x.turned && !il) turn_halves(a, b, g[i]);
+      else if (x.turned) turn_item(a, b, g[i], il);
       if constexpr (NORM) {
         if (out[i]) {
           __half* o = p.k_out + ((n + i * lanes) * p.Hkv + h) * p.D;
@@ -683,15 +765,17 @@ namespace {
 // former do two a pass; 32768 tokens, 32/8 heads, head_dim 128, at 0.5 / 0.6 / 0.7 / 0.8: MX4 124 / 118 /
 // 121 / 126 us, int8 129 / 122 / 125 / 129, e4m3fn 118 / 120 / 124 / 129, fp16 128 / 130 / 132 / 136;
 // 4646 tokens, 128/8, 256, int8: 116 / 106 / 104 / 102).
-template <int CACHE>
-constexpr double kKvShare = CACHE == I8KV_CACHE_FP16 ? 0.5 : 0.65;
+// With norms, of which queries have more, 0.5 (16384 tokens, 32/8, 128 at 0.4 / 0.5 / 0.55 / 0.65: MX4 91 / 84.5 /
+// 88 / 93 us, int8 96 / 90.5 / 95.5 / 97.5).
+template <int CACHE, bool NORM>
+constexpr double kKvShare = NORM || CACHE == I8KV_CACHE_FP16 ? 0.5 : 0.65;
 
 template <int CACHE, int HQ, bool NORM>
 cudaError_t append_with(const AppendParams& p, int sms, cudaStream_t stream) {
   const long long q_items = (p.Hq + HQ - 1LL) / HQ * (p.D / 16), kv_items = 2LL * p.Hkv * (p.D / 16);
-  const double per = 2. * sms * kAppendThreads / (q_items + kKvShare<CACHE> * kv_items);  // the resident CTAs
+  const double per = 2. * sms * kAppendThreads / (q_items + kKvShare<CACHE, NORM> * kv_items);  // the resident CTAs
   const long long q_lanes = std::clamp<long long>((long long)per, 1, p.num_tokens);
-  const long long kv_lanes = std::clamp<long long>((long long)(kKvShare<CACHE> * per), 1, p.num_tokens);
+  const long long kv_lanes = std::clamp<long long>((long long)(kKvShare<CACHE, NORM> * per), 1, p.num_tokens);
   cudaLaunchAttribute attr;
   const cudaLaunchConfig_t cfg =
       config_of(32 * (warps_of(q_lanes * q_items) + warps_of(kv_lanes * kv_items)), &attr, stream);
