@@ -322,13 +322,6 @@ __device__ __forceinline__ Seq seq_of(const AttendParams& p, int b, bool report 
   return s;
 }
 
-// a / b of what is not negative, in 32 bits where that suffices (a division in 64 takes some 500 cycles where
-// nothing else runs).
-__device__ __forceinline__ long long quotient(long long a, long long b) {
-  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-
 // One piece of a (tile, KV head)'s blocks.
 struct Item {
   Seq q;
@@ -447,7 +440,7 @@ __device__ __forceinline__ long long piece_length(const AttendParams& p, int pie
     }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
-  return quotient(total + pieces - 1, pieces);
+  return (total + pieces - 1) / pieces;
 }
 // The (tile, head) at place f < total of the batch: it.b, q, t, g, the lengths, and the place in it.
 template <int M>
@@ -479,7 +472,7 @@ __device__ __forceinline__ long long find_place(const AttendParams& p, long long
       }
       it.t = t;
       const long long in_tile = in_seq - p.Hkv * len.before(t);
-      it.g = (int)quotient(in_tile, len.of(t));
+      it.g = (int)(in_tile / len.of(t));
       return in_tile - it.g * len.of(t);
     }
     before = __shfl_sync(0xffffffffu, incl, 31);
@@ -1306,7 +1299,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         } else {
           // (chunks side by side: one after the other, each waits for its vector's maximum through the lanes)
-          constexpr int kSide = TILES == 2 ? 2 : 4;
+          constexpr int kSide = 4;
 #pragma unroll 1
           for (int i = 0; i < kChunks; i += kSide) {
             float f[kSide][8], top[kSide];
