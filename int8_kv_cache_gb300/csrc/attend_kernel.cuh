@@ -369,6 +369,11 @@ __device__ __forceinline__ Length length_of(const AttendParams& p, const Seq& s)
   return l;
 }
 
+// The first position that a token at pos attends (one before the sequence's beginning attends none: the
+// difference of a negative one and a wide window would leave the range).
+__device__ __forceinline__ int first_seen(const AttendParams& p, int pos) {
+  return p.window < 0 ? 0 : max(max(pos, 0) - p.window, 0);
+}
 // The part [x, y) of w of the tile's blocks.
 template <int M>
 __device__ __forceinline__ void place(const AttendParams& p, Item& it, long long x, long long y, long long w) {
@@ -377,8 +382,7 @@ __device__ __forceinline__ void place(const AttendParams& p, Item& it, long long
   it.last = (v1 - 1) / p.G;
   const int p0 = it.q.len - it.q.n + it.first, p1 = it.q.len - it.q.n + it.last;
   const int hi_min = max(p0 + 1, 0), hi = max(p1 + 1, 0);
-  const int lo = p.window < 0 ? 0 : max(p0 - p.window, 0);
-  const int lo_max = p.window < 0 ? 0 : max(p1 - p.window, 0);
+  const int lo = first_seen(p, p0), lo_max = first_seen(p, p1);
   it.B0 = lo / BN;
   const int B1 = (hi + BN - 1) / BN;
   it.f0 = max(it.B0, (lo_max + BN - 1) / BN);
@@ -962,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       const int h = it.g * p.G + (live ? v - tok * p.G : 0);
       const int pos = it.q.len - it.q.n + tok;
       const int hi = live ? max(pos + 1, 0) : 0;
-      const int lo = p.window < 0 ? 0 : max(pos - p.window, 0);
+      const int lo = first_seen(p, pos);
       const bool bad_pages = slot[kBadPage + (k & 1)] != 0;
       // scores to powers of two: s c2 (c2 > 0 keeps an unattended -inf what it is)
       const float rs = rscale[(k & 1) * M + tile * BM + r] * fabsf(ks1);
@@ -1270,7 +1274,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         // pages out of range among those attended (their tokens are skipped)
         if (p.table != nullptr) {
-          const int lo = p.window < 0 ? 0 : max(it.q.len - it.q.n + it.first - p.window, 0);
+          const int lo = first_seen(p, it.q.len - it.q.n + it.first);
           const int hi = min(it.blk1 * BN, it.q.len - it.q.n + it.last + 1);
           const int step = min(p.bs, BN);
           bool bad = false;

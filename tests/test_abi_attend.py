@@ -36,6 +36,7 @@ SHARED = [
     (dict(cap=math.inf), 1), (dict(window=-2), 1), (dict(q=None), 1), (dict(out=None), 1), (dict(starts=None), 1),
     (dict(qs=504), 1), (dict(qs=516), 3), (dict(q=P8), 3), (dict(out=P8), 3), (dict(starts=P2), 3), (dict(lse=P2), 3),
     (dict(sink=P2), 3), (dict(flags=P2), 3),
+    (dict(Hq=34, Hkv=2, qs=34 * 64), 2), (dict(sigma=1.5), 2),
     # a KV head's vectors are numbered in 32 bits
     (dict(T=1 << 29, qs=512), 2), (dict(T=(1 << 31) - 1, Hq=2), 2),
 ]

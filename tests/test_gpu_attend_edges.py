@@ -157,6 +157,14 @@ def test_rows_that_attend_nothing(K, kind, splits):
 
 
 @pytest.mark.parametrize("splits", [1, 4])
+def test_a_window_wider_than_any_sequence(K, splits):
+    """The widest there is, where a tile's first tokens lie before the sequence's beginning."""
+    for D, new in ((64, [250, 20]), (128, [250, 20]), (256, [60, 20])):
+        p = Paged("fp16", 40, [40, 300], new, 4, 2, D)
+        p.check(*p.run(K, splits, window=(1 << 31) - 1))
+
+
+@pytest.mark.parametrize("splits", [1, 4])
 def test_lengths_and_starts_out_of_range(K, splits):
     p = Paged("int8", 26, [100, 64, 60], [10, 20, 5], 4, 2, 128)
     p.table = torch.where(p.table < 0, 0, p.table)
