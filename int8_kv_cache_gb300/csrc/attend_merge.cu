@@ -20,15 +20,16 @@ __global__ void __launch_bounds__(kMergeThreads) attend_merge_kernel(const Atten
   // The lengths are inputs of attend_kernel, which lets this kernel launch once it may read them itself:
   // the cut is found while its last CTAs still work.
   const int cut = blockIdx.x + 1;
-  long long total;
+  long long total, x = 0;
   const long long one = piece_length<M>(p, p.pieces, total);
   const long long f = one * cut;
-  if (f >= total) return;
   Item it;
   Length len;
-  const long long x = find_place<M>(p, f, it, len);
+  if (f < total) x = find_place<M>(p, f, it, len);
+  // the partials; also where there is nothing to do: the stream goes on when all of this grid has ended,
+  // and attend_kernel has to have ended by then
+  grid_dependency_wait();
   if (x == 0 || x > one) return;  // the cut is between two tiles, or not the first one in this one
-  grid_dependency_wait();  // the partials
   // pieces cut - 1 (its end), cut, ..., last (their beginnings)
   const int last = (int)((f + (len.of(it.t) - x) - 1) / one);
   const int v0 = it.t * M, nvec = it.q.n * p.G;
