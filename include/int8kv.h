@@ -630,8 +630,9 @@ i8kv_status packed_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* 
  *                device, into that many pieces of about equal length, one per CTA,
  *                whose ends fall anywhere in a tile's range; what belongs to one tile
  *                is merged by a second kernel.  0: automatic -- as many pieces as the
- *                device has SMs where the tiles alone are fewer than four rounds of
- *                them, and the workspace is large enough; else unsplit
+ *                device has SMs where the tiles alone would leave SMs idle (by T, B
+ *                and the heads: the lengths are not known here), and the workspace is
+ *                large enough; else unsplit
  *   workspace, workspace_bytes  paged_prefill_workspace_bytes(..., num_splits) for
  *                num_splits > 1 (16-byte aligned, else I8KV_EALIGN; too small
  *                I8KV_EWORKSPACE); may be NULL for 0 and 1.  Nothing in it

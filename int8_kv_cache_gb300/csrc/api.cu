@@ -1174,14 +1174,27 @@ static i8kv::AttendParams attend_params(const uint16_t* q, int64_t q_stride, con
 
 // How a call of packed_prefill or paged_prefill is dealt out: two tiles of 128 vectors per CTA where
 // sequences have about that many and, whole, they fill the GPU (one tile at a time spreads wider);
-// pieces where the (tile, KV head)s alone are fewer than a few rounds of the SMs.
+// pieces (see attend_cuts) where whole (tile, KV head)s would leave SMs idle.
 struct AttendPlan {
   bool two = false;
   int32_t pieces = 0;   // 0: whole (tile, KV head)s
   unsigned ctas = 0;
   size_t workspace = 0;
 };
-static constexpr int kAttendRounds = 4;
+// Whether the automatic choice cuts the batch into pieces, given how many (tile, KV head)s it has (us, int8,
+// 32 / 8 heads x 128 unless said, whole / cut; 152 SMs):
+//   one tile per CTA: below three rounds of the SMs (single tokens over 512 to 8192 in 20 sequences 84 / 57, in 48
+//     129 / 123, in 64 143 / 148, in 256 213 / 325; 24 / 2 x 256, 200 to 300 over 1000 to 8192 in four 210 / 195)
+//   two, one sequence, whose tiles are of about one length: where the last round is not nearly full
+//     (1216 tokens over 16384 245 / 280, 1400 453 / 324, 2048 453 / 438, 2432 453 / 500, 4096 826 / 774)
+//   two, several: below one round (128 tokens over 1024 to 16384 in four 167 / 120; 512 in eight 244 / 307;
+//     1 to 512 in twelve, MX4, 141 / 179): beyond, the longest first fill the gaps, and the merge costs more
+static bool attend_cuts(int64_t items, bool pairs, int32_t seqs, int sms) {
+  if (!pairs) return items < INT64_C(3) * sms;
+  if (seqs > 1) return items < sms;
+  const int64_t rounds = (items + sms - 1) / sms;
+  return rounds <= 4 && items * 10 < rounds * sms * 9;
+}
 static AttendPlan attend_plan(int32_t T, int32_t B, int32_t G, int32_t Hkv, int32_t D, int64_t cap,
                               int sms, int32_t num_splits) {
   AttendPlan a;
@@ -1191,7 +1204,7 @@ static AttendPlan attend_plan(int32_t T, int32_t B, int32_t G, int32_t Hkv, int3
   const int64_t tiles = std::max<int64_t>(vec / (pairs ? 256 : 128), seqs);
   if (num_splits > 1)
     a.pieces = num_splits;
-  else if (num_splits == 0 && cap > 128 && tiles * Hkv < static_cast<int64_t>(kAttendRounds) * sms)
+  else if (num_splits == 0 && cap > 128 && attend_cuts(tiles * Hkv, pairs, seqs, sms))
     a.pieces = sms;
   a.two = pairs && (a.pieces > 0 || tiles * Hkv >= sms);
   const int32_t M = a.two ? 256 : 128;
