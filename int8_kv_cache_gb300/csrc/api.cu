@@ -1187,11 +1187,13 @@ struct AttendPlan {
 //     129 / 123, in 64 143 / 148, in 256 213 / 325; 24 / 2 x 256, 200 to 300 over 1000 to 8192 in four 210 / 195)
 //   two, one sequence, whose tiles are of about one length: where the last round is not nearly full
 //     (1216 tokens over 16384 245 / 280, 1400 453 / 324, 2048 453 / 438, 2432 453 / 500, 4096 826 / 774)
-//   two, several: below one round (128 tokens over 1024 to 16384 in four 167 / 120; 512 in eight 244 / 307;
-//     1 to 512 in twelve, MX4, 141 / 179): beyond, the longest first fill the gaps, and the merge costs more
+//   two, several: below nine tenths of a round (128 tokens over 1024 to 16384 in four 167 / 120; 512 in eight 244 / 307;
+//     1 to 512 in twelve, MX4, 141 / 179; 300 to 1001 over 1001 to 4096 in four, e4m3fn, 16 / 2 x 64, 50 / 70):
+//     beyond, the longest first fill the gaps, and the merge costs more (not so where one sequence is far longer:
+//     512 over 16384 and over 600 in eleven more 298 / 254, which only the device knows)
 static bool attend_cuts(int64_t items, bool pairs, int32_t seqs, int sms) {
   if (!pairs) return items < INT64_C(3) * sms;
-  if (seqs > 1) return items < sms;
+  if (seqs > 1) return items * 10 < INT64_C(9) * sms;
   const int64_t rounds = (items + sms - 1) / sms;
   return rounds <= 4 && items * 10 < rounds * sms * 9;
 }
@@ -1206,7 +1208,7 @@ static AttendPlan attend_plan(int32_t T, int32_t B, int32_t G, int32_t Hkv, int3
     a.pieces = num_splits;
   else if (num_splits == 0 && cap > 128 && attend_cuts(tiles * Hkv, pairs, seqs, sms))
     a.pieces = sms;
-  a.two = pairs && (a.pieces > 0 || tiles * Hkv >= sms);
+  a.two = pairs && (a.pieces > 0 || tiles * Hkv * 10 >= INT64_C(9) * sms);
   const int32_t M = a.two ? 256 : 128;
   a.ctas = static_cast<unsigned>(a.pieces > 0 ? a.pieces : std::min<int64_t>((vec / M + seqs) * Hkv, sms));
   a.workspace = static_cast<size_t>(a.pieces) * 2 * M * (D + 2) * 4;
