@@ -1280,11 +1280,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         if (p.table != nullptr) {
           const int lo = first_seen(p, it.q.len - it.q.n + it.first);
           const int hi = min(it.blk1 * BN, it.q.len - it.q.n + it.last + 1);
-          const int step = min(p.bs, BN);
+          const int step = min(p.bs, BN), from = max(it.blk0 * BN, lo);
           bool bad = false;
-          for (int t = max(it.blk0 * BN, lo) + step * ct; t < hi; t += step * kProdThreads)
-            bad |= group_of(p, it, t) < 0;
-          if (ct == 0 && hi > max(it.blk0 * BN, lo)) bad |= group_of(p, it, hi - 1) < 0;
+          // (unsigned: a thread's next step may lie past 2^31)
+          if (hi > from)
+            for (unsigned t = (unsigned)from + step * ct; t < (unsigned)hi; t += step * kProdThreads)
+              bad |= group_of(p, it, (int)t) < 0;
+          if (ct == 0 && hi > from) bad |= group_of(p, it, hi - 1) < 0;
           if (bad) {
             slot[kBadPage + (k & 1)] = 1;
             flag_or(p.flags, I8KV_FLAG_BAD_BLOCK);
