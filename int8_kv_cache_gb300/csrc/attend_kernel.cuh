@@ -1140,19 +1140,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           float o[32];
           tc::tmem_ld32(tbase + t_lane + L::kOCol + tile * D + c_lo + 32 * c, o);
           tc::tmem_wait_ld();
-          if (!some && !nan) continue;
+          // (lanes whose vectors hold nothing skip the stores, not the turn: all of a warp load together)
+          if (some || nan) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const int d = c_lo + 32 * c + 4 * e;
-            float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
-            if (SRC != kF16) {
-              if (p.per_channel) vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + it.g * D + d));
-              else vs.x = vs.y = vs.z = vs.w = __ldg(p.v_scale);
+            for (int e = 0; e < 8; ++e) {
+              const int d = c_lo + 32 * c + 4 * e;
+              float4 vs = make_float4(1.f, 1.f, 1.f, 1.f);
+              if (SRC != kF16) {
+                if (p.per_channel) vs = __ldg(reinterpret_cast<const float4*>(p.v_scale + it.g * D + d));
+                else vs.x = vs.y = vs.z = vs.w = __ldg(p.v_scale);
+              }
+              const float f = 0.00390625f;
+              *reinterpret_cast<float4*>(acc + d) = make_float4(o[4 * e] * f * vs.x, o[4 * e + 1] * f * vs.y,
+                                                                o[4 * e + 2] * f * vs.z, o[4 * e + 3] * f * vs.w);
             }
-            const float f = 0.00390625f;
-            *reinterpret_cast<float4*>(acc + d) = make_float4(o[4 * e] * f * vs.x, o[4 * e + 1] * f * vs.y,
-                                                              o[4 * e + 2] * f * vs.z, o[4 * e + 3] * f * vs.w);
           }
+          __syncwarp();
         }
         free_o();
         if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, notes, lo, hi, c_lo, c_lo + OC, acc);

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 from attend64 import attend64, bounds, cache_of, check, values
-from test_gpu_attend import K, firsts, gen, ints  # noqa: F401
+from test_gpu_attend import K, gen, ints, paged_case  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -37,3 +37,13 @@ def test_a_sequence_that_ends_just_below_2_31(K, kind, bs, splits):
     k, v = values(c)
     ref = attend64(q, [0, n], [tail], lambda b: (k[rows], v[rows], None), 0.125, window)
     check(out, lse, ref, bounds(ref, D, window, True), kind)
+
+
+@pytest.mark.parametrize("kind", ["int8", "fp16"])
+@pytest.mark.parametrize("D,Hq,Hkv", [(64, 2, 2), (128, 3, 1), (256, 2, 1)])
+def test_pieces_that_hold_nothing_for_some_lanes_of_a_warp(K, kind, D, Hq, Hkv):
+    """A narrow window, blocks that begin inside a warp's 32 vectors, last vectors of a tile that are not there: the
+    lanes of a warp write their partials, or nothing, side by side."""
+    for window in (0, 3):
+        for lens, new in (([403], [200]), ([403, 77], [19, 70])):
+            paged_case(K, kind, 61, lens, new, Hq, Hkv, D, splits=9, window=window)
