@@ -58,7 +58,8 @@
 // a short call the way from the launch over the first item (2 us), its queries and a block's chain.
 //
 // Every wait is bounded; a CTA that gives up marks its outputs NaN and raises
-// I8KV_FLAG_WAIT_TIMEOUT.
+// I8KV_FLAG_WAIT_TIMEOUT.  tests/attend_withheld.cu builds the kernel with a shorter limit and copies or arrivals
+// that do not come, by the two macros below.
 #pragma once
 
 #include <cuda.h>
@@ -72,6 +73,13 @@
 #include "codes.cuh"
 #include "device.cuh"
 #include "tc.cuh"
+
+#ifndef I8KV_ATTEND_WAIT_NS
+#define I8KV_ATTEND_WAIT_NS ::i8kv::tc::kWaitNs
+#endif
+#ifndef I8KV_ATTEND_WITHHELD  // whether what belongs to a block of the CTA's item does not come
+#define I8KV_ATTEND_WITHHELD(what, item, block) false
+#endif
 
 namespace i8kv {
 namespace ap {
@@ -88,6 +96,8 @@ constexpr float kShift = 8.f;  // P holds p 2^kShift: at most 2^15
 constexpr int kPoison = 8;     // blocks that a tile's rows can attend in part (6 at most)
 constexpr float kLn2 = 0.6931471805599453f;
 
+// What a test keeps from coming: the queries' hand-over, copies of K or V, probabilities (of tile 0 or 1).
+enum Hold { kHoldQ, kHoldK, kHoldV, kHoldP };
 // What a K or V value is read from.
 enum Src { kF16 = 0, kI8 = 1, kE4 = 2, kMx4 = 3 };
 
@@ -166,20 +176,25 @@ __device__ __forceinline__ uint4 lds16(uint32_t a) {
   return v;
 }
 
-// tc::mbar_wait of a converged warp, with its clock and the others' news looked at every so often
-// only.  All lanes wait: one alone, and the others for it, hears of a phase some 300 cycles later.
+// tc::mbar_wait of a converged warp.  All lanes wait: one alone, and the others for it, hears of a phase some 300
+// cycles later.
 // But every lane's poll takes its turn at the shared memory that the tensor cores read operands
-// from, so only the softmax and MMA warps, whose waits are one behind the other, do it ...
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, const volatile int* abort) {
-  uint64_t t0 = 0;
+// from, so only the softmax and MMA warps, whose waits are one behind the other, do it ...  A wait in vain is told in
+// *abort before the warp does anything else: whoever sees an arrival or a product behind it sees that too.  kFence:
+// what follows is issued to the tensor cores, which orders no memory (elsewhere arrivals do; a fence there cost the
+// converters 3 %).
+template <bool kFence = false>
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort) {
   bool ok = tc::mbar_try_wait(bar, parity);
+  if (!ok) {
+    const uint64_t t0 = tc::global_ns();
 #pragma unroll 1
-  for (uint32_t i = 1; !ok; ++i) {
-    ok = tc::mbar_try_wait(bar, parity);
-    if ((i & 63u) == 0u) {
-      const uint64_t now = tc::global_ns();
-      if (t0 == 0) t0 = now;
-      if (now - t0 > tc::kWaitNs || (abort != nullptr && *abort != 0)) break;
+    while (!(ok = tc::mbar_try_wait(bar, parity))) {
+      if (*abort != 0 || tc::global_ns() - t0 > I8KV_ATTEND_WAIT_NS) {
+        *abort = 1;
+        if (kFence) __threadfence_block();
+        break;
+      }
     }
   }
   return __all_sync(0xffffffffu, ok);
@@ -192,7 +207,7 @@ __device__ __forceinline__ bool calm_wait(uint32_t bar, uint32_t parity) {
     do {
       __nanosleep(100);
       ok = tc::mbar_try_wait(bar, parity);
-    } while (!ok && tc::global_ns() - t0 <= tc::kWaitNs);
+    } while (!ok && tc::global_ns() - t0 <= I8KV_ATTEND_WAIT_NS);
   }
   ok = __all_sync(0xffffffffu, ok);
   __syncwarp();  // (the vote orders no memory)
@@ -946,11 +961,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       other = b[(half ^ 1) * BM + r];
       return votes[8 * buf] != 0 && votes[8 * buf + 1] != 0;
     };
-    auto wait_all = [&](int b, uint32_t parity) -> bool {
-      const bool ok = warp_wait(bar(b), parity, slot + kAbort);
-      if (!ok) slot[kAbort] = 1;
-      return ok;
-    };
+    auto wait_all = [&](int b, uint32_t parity) -> bool { return warp_wait(bar(b), parity, slot + kAbort); };
     const float cap_k = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
     const float ks1 = SRC != kF16 && !p.per_channel ? __ldg(p.k_scale) : 1.f;
     int n = 0;  // blocks done by this CTA
@@ -1105,12 +1116,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           tc::fence_before_sync();
         }
         l_run = fmaf(l_run, alpha, sum4(ps));
-        warp_arrive(bar(kPFull + tile));
+        if (!I8KV_ATTEND_WITHHELD(kHoldP + tile, k, i)) warp_arrive(bar(kPFull + tile));
       }
       n += nb;
       // ---- epilogue ----
-      ok = ok && slot[kAbort] == 0 && (nb == 0 || wait_all(kPVDone + tile, (n - 1) & 1));
-      ok = __all_sync(0xffffffffu, ok);
+      ok = ok && (nb == 0 || wait_all(kPVDone + tile, (n - 1) & 1));
       if constexpr (TILES == 1) {
         float l_other;
         ok = exchange(2, ok, l_run, l_other);
@@ -1125,7 +1135,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       constexpr int OC = TILES == 2 ? D : D / 2;  // channels of this thread
       const int c_lo = half * OC;
       const float kNan = __int_as_float(0x7fc00000);
-      auto free_o = [&]() {  // the next item's products may go over O
+      // The next item's products may go over O.  What was read of it counts if by now nobody has waited in vain: whoever
+      // had a part in it, or issued the next item's products without waiting for this, would have told it before.
+      auto free_o = [&]() {
+        ok = __all_sync(0xffffffffu, ok && slot[kAbort] == 0);
         tc::fence_before_sync();
         warp_arrive(bar(kOFree + (k & 1)));
       };
@@ -1166,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
       } else {
         float sc = 0.f, lse = neg_inf();
-        if (!ok || nan) {
+        if (nan) {
           sc = lse = kNan;
         } else if (some) {
           lse = m_nat + logf(lsum);
@@ -1208,6 +1221,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         }
         __syncwarp();
         free_o();
+        if (!ok) {
+          lse = kNan;
+          for (int d = c_lo; live && d < c_lo + OC; d += 8)
+            *reinterpret_cast<uint4*>(out + d) = make_uint4(0x7e007e00u, 0x7e007e00u, 0x7e007e00u, 0x7e007e00u);
+        }
         if (SRC != kI8 && fix && ok && some) add_poison<D, SRC>(p, it, notes, lo, hi, c_lo, c_lo + OC, out);
         if (live && half == 0 && p.lse != nullptr)
           p.lse[(it.q.s0 + (long long)tok) * p.Hq + h] = lse;
@@ -1363,7 +1381,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           }
         }
         tc::fence_smem_to_async();
-        warp_arrive(bar(kQFull + (k & 1)));
+        if (!I8KV_ATTEND_WITHHELD(kHoldQ, k, 0)) warp_arrive(bar(kQFull + (k & 1)));
       };
       if constexpr (SRC == kF16) {
         stage_queries();
@@ -1489,11 +1507,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
           // slabs of the part's positions at LBO
           const uint32_t qd = desc_low(sbase + L::kQ, 16), kd = desc_low(sbase + L::kK, 16);
           const uint32_t vd = desc_low(sbase + L::kV, L::kVRows * 128);
-          // After a wait in vain the loop goes on: what is issued then reads and writes nothing but this CTA's
-          // own memory, the softmax's waits fail too and set the flag that ends the ones to come, and the rows
-          // become NaN.  (Branches on the outcome made the loop 15 % slower.)
-          bool fine = true;
-          auto wait = [&](int b, uint32_t par) { fine &= warp_wait(bar(b), par, slot + kAbort); };
+          // After a wait in vain the loop goes on: what is issued then reads and writes nothing but this CTA's own
+          // memory, and the wait told the others before, who look once they have read O: its rows become NaN.
+          // (Branches on the outcome made the loop 15 % slower, a predicate of the instructions 13 to 25 %.)
+          auto wait = [&](int b, uint32_t par) { warp_wait<true>(bar(b), par, slot + kAbort); };
           // scores of tile w (or into buffer nn & 1); the first tile waits for the parts, the last frees them
           auto qk = [&](int w, int nn) {
             const uint32_t qs = qd + w * (L::kSlabs * L::kSlab >> 4);
@@ -1587,7 +1604,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             o_free();
             commit(lead, bar(kQFree));
           }
-          if (!fine) slot[kAbort] = 1;
         }
         n += nb;
         give_back(k);
@@ -1646,6 +1662,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             if (nn * P + j >= N && !warp_wait(bar((is_v ? kVFree : kKFree) + at), turn(nn, j) ^ 1, slot + kAbort))
               return false;
             ++(is_v ? nv : nk);
+            if (I8KV_ATTEND_WITHHELD(is_v ? kHoldV : kHoldK, k, i)) return true;
             if (lane == 0) tc::mbar_arrive_expect_tx(bar(full), L::kPart);
             int slab, row;
             bool mine;
@@ -1708,6 +1725,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
               const int full = bar(kRawFull + ring.place);
               const uint32_t dst = sbase + R::kAt + ring.place * R::kBytes;
               if (!(ok = warp_wait(bar(kRawFree + ring.place), ring.turn ^ 1, slot + kAbort))) break;
+              if (I8KV_ATTEND_WITHHELD(is_v ? kHoldV : kHoldK, k, is_v ? r / 2 - 1 : (r + 1) / 2)) {
+                r = 2 * nb;
+                break;
+              }
               units += kStep;
 #pragma unroll
               for (int w = 0; w < kStep; ++w) ring.next();
@@ -1750,14 +1771,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       }
       // every copy begun has landed before the CTA ends (the last ones of each place)
       if (lane == 0) {
+        auto landed = [&](int b, int turn) {
+          if (!tc::mbar_wait(bar(b), turn & 1, nullptr, I8KV_ATTEND_WAIT_NS)) slot[kAbort] = 1;
+        };
+        constexpr int kAhead = Raw<D, TILES, SRC>::kAhead;
         if constexpr (SRC != kF16)
-          for (int k = max(0, units - Raw<D, TILES, SRC>::kAhead); k < units; ++k)
-            if (!tc::mbar_wait(bar(kRawFull + k % Raw<D, TILES, SRC>::kAhead), (k / Raw<D, TILES, SRC>::kAhead) & 1))
-              slot[kAbort] = 1;
-        for (int k = max(0, nk - N); k < nk; ++k)
-          if (!tc::mbar_wait(bar(kKFull + k % N), (k / N) & 1)) slot[kAbort] = 1;
-        for (int k = max(0, nv - N); k < nv; ++k)
-          if (!tc::mbar_wait(bar(kVFull + k % N), (k / N) & 1)) slot[kAbort] = 1;
+          for (int k = max(0, units - kAhead); k < units; ++k) landed(kRawFull + k % kAhead, k / kAhead);
+        for (int k = max(0, nk - N); k < nk; ++k) landed(kKFull + k % N, k / N);
+        for (int k = max(0, nv - N); k < nv; ++k) landed(kVFull + k % N, k / N);
       }
       __syncwarp();
     }

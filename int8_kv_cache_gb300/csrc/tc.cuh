@@ -78,16 +78,17 @@ __device__ __forceinline__ uint64_t global_ns() {
 }
 
 // Bounded wait for the phase with the given parity to complete: gives up after
-// about a second, or at once when *abort (a shared-memory word) is set by
+// `limit` (about a second), or at once when *abort (a shared-memory word) is set by
 // another thread that gave up; the caller then abandons its work.
 constexpr uint64_t kWaitNs = 1000000000ull;
 __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity,
-                                          const volatile int* abort = nullptr) {
+                                          const volatile int* abort = nullptr,
+                                          uint64_t limit = kWaitNs) {
   if (mbar_try_wait(bar, parity)) return true;
   const uint64_t t0 = global_ns();
   while (!mbar_try_wait(bar, parity)) {
     if (abort != nullptr && *abort) return false;
-    if (global_ns() - t0 > kWaitNs) return false;
+    if (global_ns() - t0 > limit) return false;
   }
   return true;
 }
