@@ -97,10 +97,11 @@ typedef enum {
 #define I8KV_FLAG_BAD_SLOT 0x8u    /* reshape_and_cache: a slot >= num_slots was skipped      */
 #define I8KV_FLAG_FP32_PATH 0x10u  /* some CTA evaluated its heads on the FP32 path (see the
                                       numerical eligibility rules below)                     */
-#define I8KV_FLAG_WAIT_TIMEOUT 0x20u /* dsa_prefill's tensor-core kernel and paged_decode_mx4: a
-                                        CTA gave up waiting (about a second) for its own
-                                        asynchronous copies or tensor-core products; its
-                                        outputs are NaN                                    */
+#define I8KV_FLAG_WAIT_TIMEOUT 0x20u /* dsa_prefill's tensor-core kernel, paged_decode_mx4,
+                                        packed_prefill and paged_prefill: a CTA gave up waiting
+                                        (about a second) for its own asynchronous copies or
+                                        tensor-core products; its outputs are NaN (of the last
+                                        two, rows that it had not come to may be as they were) */
 
 #define I8KV_FLAG_BAD_POSITION 0x40u /* rope_and_cache: a position outside [0, max_pos): that token
                                         was skipped                                         */

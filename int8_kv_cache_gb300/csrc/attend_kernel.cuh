@@ -1233,7 +1233,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       if (!ok) slot[kAbort] = 1;
       give_back(k);
     }
-    if (!ok && tid == 0) flag_or(p.flags, I8KV_FLAG_WAIT_TIMEOUT);
   } else if (warp < (kSoftThreads + kProdThreads) / 32) {
     // -----------------------------------------------------------------------
     // converters; of fp16 sources: the check of V blocks attended in part
@@ -1785,6 +1784,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
   }
   tc::fence_before_sync();
   sync_all();
+  if (tid == 0 && slot[kAbort] != 0) flag_or(p.flags, I8KV_FLAG_WAIT_TIMEOUT);  // whichever role gave up
   if (warp == kMmaWarp) {
     tc::fence_after_sync();
     tc::tmem_dealloc(tbase, 512);

@@ -91,6 +91,21 @@ def test_a_prompt(withheld, D, two):
     assert torch.equal(p.run(NONE, 0, 0)[0], clean[0])
 
 
+def test_the_second_tile_alone(withheld):
+    """Its rows are NaN and the flag is raised also where the first one had been written by then."""
+    p = Prompt(withheld, 128, 1)
+    clean = p.run(NONE, 0, 0)
+    last = len(p.items) - 1
+    for block in (0, 1):
+        out, lse, flags = p.run(P1, last, block)
+        assert flags == TIMEOUT
+        r, h = p.rows(last)
+        assert bool(out[r, h][128:].isnan().all() & lse[r, h][128:].isnan().all())
+        first = out[r, h][:128]
+        done = ~first.isnan().any(-1)
+        assert torch.equal(first[done], clean[0][r, h][:128][done])
+
+
 @pytest.mark.parametrize("two", [0, 1])
 @pytest.mark.parametrize("pieces", [0, 3])
 def test_a_quantised_cache(withheld, two, pieces):
