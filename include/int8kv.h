@@ -344,7 +344,9 @@ i8kv_status paged_decode(const uint16_t* q, const void* k_cache, const void* v_c
  * names them without a definition; the meanings taken are:
  *   softcap  >= 0, finite.  > 0: each scaled score s becomes
  *            softcap * tanh(s / softcap) before the softmax; 0: off.  The
- *            head-sink logit is not capped.
+ *            head-sink logit is not capped.  (Computed as softcap - 2 softcap /
+ *            (1 + e^(2 s / softcap)): the error is up to 2^-21 of softcap, not of
+ *            s, so a cap far above the scores makes them coarse.)
  *   window   >= -1.  >= 0: the query of sequence b (at position L - 1, L its
  *            clamped live length) attends positions [max(0, L-1-window), L):
  *            itself and the window positions before it; -1: off.
@@ -597,7 +599,8 @@ i8kv_status paged_decode_mx4(const uint16_t* q, const void* cache, const float* 
  *                outside are clamped (I8KV_FLAG_LEN_CLAMPED); rows before the
  *                first sequence and behind the last stay as they are in out and
  *                lse; a sequence may be empty
- *   head_sink, softcap, window  as for paged_decode_ex
+ *   head_sink, softcap, window  as for paged_decode_ex (with caps above 128 a
+ *                capped score is within 2^-18.9 of itself, however far below it)
  *   out          [T, Hq, D] fp16, dense;  lse [T, Hq] fp32 or NULL
  * Work: one kernel on the tensor cores (tcgen05); its grid depends on T, B and
  * the heads only.  The probabilities are rounded to fp16 (by at most a relative

@@ -268,6 +268,11 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   asm("fma.rn.f32x2 %0, %1, %2, %3;\n" : "=l"(d) : "l"(a), "l"(b), "l"(c));
   return d;
 }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("mul.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
   uint64_t d;
   asm("add.rn.f32x2 %0, %1, %2;\n" : "=l"(d) : "l"(a), "l"(b));
@@ -279,6 +284,20 @@ __device__ __forceinline__ float sum4(const uint64_t (&p)[2]) {
   return a + b;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) { return fmaxf(fmaxf(a, b), c); }
+
+// Caps.  soft_cap takes 2 c / (1 + e^(2 y)), y = x / c, from c: up to 2^-21 of c off.  With caps up to kCapExp that is
+// 2^-14 at most, an eighth of what a weight's rounding to fp16 is.  A higher cap, which would leave nothing of scores far
+// below it, takes the series of c tanh y = x (1 - y^2 / 3 + 2 y^4 / 15 - 17 y^6 / 315 + ...) for |y| < 1/4, within 2^-21
+// of the result; beyond, soft_cap is within 2^-18.9 of it.  (For all caps the choice cost 8 to 16 %; now prompts
+// of 1000 to 4097 tokens, 32 / 8 heads x 128, take 322 us with a cap of 30, 326 to 349 with one of 300.  Each score's
+// choice is its own: what lies beside it, masked perhaps, has no part in it.)
+constexpr float kCapExp = 128.f, kSeries = 0.25f;
+__device__ __forceinline__ void cap_small(float& x0, float& x1, float inv_c) {
+  const uint64_t x = pair(x0, x1), y = mul2(x, pair(inv_c, inv_c)), y2 = mul2(y, y);
+  uint64_t t = fma2(y2, pair(-17.f / 315.f, -17.f / 315.f), pair(2.f / 15.f, 2.f / 15.f));
+  t = fma2(y2, t, pair(-1.f / 3.f, -1.f / 3.f));
+  unpair(fma2(mul2(x, y2), t, x), x0, x1);
+}
 
 // Zero the non-finite ones of two fp16 values; returns whether there were any.
 __device__ __forceinline__ bool finite_only(uint32_t& x) {
@@ -962,7 +981,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
       return votes[8 * buf] != 0 && votes[8 * buf + 1] != 0;
     };
     auto wait_all = [&](int b, uint32_t parity) -> bool { return warp_wait(bar(b), parity, slot + kAbort); };
-    const float cap_k = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
+    const float cap_inv = p.softcap > 0.f ? fminf(1.f / p.softcap, 1e38f) : 0.f, cap_k = 2.f * kLog2e * cap_inv;
+    const float cap_near = kSeries * p.softcap;
+    const bool cap_exp = p.softcap > 0.f && p.softcap <= kCapExp;
     const float ks1 = SRC != kF16 && !p.per_channel ? __ldg(p.k_scale) : 1.f;
     int n = 0;  // blocks done by this CTA
     bool ok = true;
@@ -1015,7 +1036,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
         tc::fence_after_sync();
         const uint32_t s_col = tbase + t_lane + sb * BN + 64 * half;
         const bool masks = blk < f0 || blk >= f1 || bad_pages;
-        if (masks || p.softcap > 0.f) {
+        if (p.softcap > kCapExp) {  // (by 16: it is seldom used, and the others' code makes way for it)
+#pragma unroll 1
+          for (int c = 0; c < COLS / 16; ++c) {
+            float x[16];
+            tc::tmem_ld16(s_col + 16 * c, x);
+            tc::tmem_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 16; j += 2) {
+              float y0 = x[j] * nat, y1 = x[j + 1] * nat;
+              x[j] = soft_cap(y0, p.softcap, cap_k);
+              x[j + 1] = soft_cap(y1, p.softcap, cap_k);
+              const bool near0 = fabsf(y0) < cap_near, near1 = fabsf(y1) < cap_near;
+              cap_small(y0, y1, cap_inv);
+              x[j] = near0 ? y0 : x[j];
+              x[j + 1] = near1 ? y1 : x[j + 1];
+            }
+            tc::tmem_st16(s_col + 16 * c, x);
+          }
+          tc::tmem_wait_st();
+        }
+        if (masks || cap_exp) {
           // capped and masked in tensor memory, 32 at a time (less code for a loop that shares its
           // instruction cache with the other roles')
           const int at = blk * BN + 64 * half;
@@ -1024,7 +1065,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const __grid_consta
             float x[32];
             tc::tmem_ld32(s_col + 32 * c, x);
             tc::tmem_wait_ld();
-            if (p.softcap > 0.f) {
+            if (cap_exp) {
 #pragma unroll
               for (int j = 0; j < 32; ++j) x[j] = soft_cap(x[j] * nat, p.softcap, cap_k);
             }

@@ -4,8 +4,8 @@ import math
 import pytest
 import torch
 
-from attend64 import attend64, bounds, cache_of, check, values
-from test_gpu_attend import K, gen, ints, paged_case  # noqa: F401
+from attend64 import attend64, bounds, cache_of, check, context_of, tables, values
+from test_gpu_attend import K, firsts, gen, ints, paged_case, projection, run_packed  # noqa: F401
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +47,50 @@ def test_pieces_that_hold_nothing_for_some_lanes_of_a_warp(K, kind, D, Hq, Hkv):
     for window in (0, 3):
         for lens, new in (([403], [200]), ([403, 77], [19, 70])):
             paged_case(K, kind, 61, lens, new, Hq, Hkv, D, splits=9, window=window)
+
+
+def capped_bounds(ref, D, starts, lens, context, cap):
+    """Those of scores without a cap, and a cap's own error relative to the score: its series is cut off at 2^-21.5 and
+    has four roundings; beyond a quarter of the cap c, tanh is above 0.2449 and 2^-21 of c off at most (the exponential
+    and the reciprocal 2^-22 and 2^-23, of a slope of at most 1/2 and 1; four roundings): 2^-18.9 of the score.  Caps up to
+    128 are taken so for all scores: 2^-21 of the cap.
+    Scores of some tens leave weights far below the largest one, w = 1 (so the sum of all is 1 at least).  They are held
+    as fp16 numbers w 2^8 or larger ones, whose half steps below the smallest normal are 2^-25: 2^-33 of the largest
+    weight for each value attended.  (It shows where the values of the large weights are zeros.)"""
+    o, z = bounds(ref, D, max(lens), False)
+    d = ref[3] * 2.0 ** -18.9 + (cap * 2.0 ** -21 if cap <= 128 else 0.0)
+    o = o + ref[2] * 2 * d[..., None] * 1.01
+    for b, L in enumerate(lens):
+        v = context(b)[1][:L].abs().sum(0)
+        rows = slice(starts[b], starts[b + 1])
+        o[rows] += 2.0 ** -33 * v.repeat_interleave(o.shape[1] // v.shape[0], 0)
+    return o, z + d
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("cap", [0.25, 4.0, 30.0, 128.0, 300.0, 1e4, 1e5, 1e6, 3e38])
+def test_caps_small_and_far_above_the_scores(K, D, cap):
+    """c tanh(s / c) is s where c is far above it."""
+    g = gen(62)
+    new = [300, 45]
+    starts = firsts(new)
+    q, k, v = projection(g, starts[-1], 4, 2, D)
+    q = q * 8  # scores of some tens
+    ctx = lambda b: (k[starts[b]:starts[b + 1]].double(), v[starts[b]:starts[b + 1]].double(), None)  # noqa: E731,B023
+    ref = attend64(q, starts, new, ctx, D ** -0.5, softcap=cap)
+    out, lse = run_packed(K, q, k, v, starts, D ** -0.5, softcap=cap)
+    check(out, lse, ref, capped_bounds(ref, D, starts, new, ctx, cap))
+    lens, new, bs = [400, 300, 77], [70, 1, 3], 16
+    starts = firsts(new)
+    for kind in ("int8", "mx4"):
+        table, pool = tables(g, lens, bs)
+        c = cache_of(kind, g, pool, bs, 2, D, False)
+        q = (torch.randn((starts[-1], 4, D), generator=g, device="cuda") * 4).half()
+        ctx = context_of(c, table, *values(c))
+        ref = attend64(q, starts, lens, ctx, D ** -0.5, softcap=cap)
+        for splits in (1, 5):
+            out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+            n = K.paged_prefill_workspace_bytes(starts[-1], 3, 4, 2, D, table.shape[1] * bs, splits)
+            K.paged_prefill(q, c["kc"], c["vc"], c["ks"], c["vs"], 1, table, ints(lens), ints(starts), D ** -0.5,
+                            num_splits=splits, workspace=torch.empty(n // 4 + 4, device="cuda"), out=out, lse=lse, softcap=cap)
+            check(out, lse, ref, capped_bounds(ref, D, starts, lens, ctx, cap), kind)
