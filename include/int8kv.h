@@ -505,9 +505,13 @@ i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* 
  * norm_rope_and_cache -- rope_and_cache with the heads of queries and keys normed
  * before the rotation, in the same pass.  For every head of D channels, in fp32:
  *     x' = x * r * weight[d],  r = 1 / sqrt(sum_d x^2 / D + eps)
- * (r rounded once; the squares are summed 16 channels at a time, then by halves;
- * each product rounded on its own), then the rotation and the stores as for
- * rope_and_cache.  Values are not normed.
+ * then the rotation and the stores as for rope_and_cache.  Values are not normed.
+ * The products are rounded each on its own, and r is within 2 units of the last
+ * place of 1 / sqrt of the fp32 mean + eps (rsqrtf; the squares of 16 channels are
+ * summed in two chains of fused products, the even channels and the odd ones, then
+ * over the head by halves).  So a normed head's rows are determined to 24 roundings
+ * of 2^-24, not bit for bit as rope_and_cache's are: a code whose value lies that
+ * near to a boundary may be either of two.  The same call gives the same bits.
  *   q_weight, k_weight  [D] fp32, 16-byte aligned; NULL: not normed
  *   eps          finite, >= 0
  *   k_out        [num_tokens, Hkv, D] fp16, dense, or NULL: the normed and turned
@@ -517,7 +521,8 @@ i8kv_status rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* 
  *                = Hkv * D
  *   D 64, 128 or 256 where a weight is given (I8KV_EUNSUPPORTED otherwise).
  *   The other arguments as for rope_and_cache.  A head with a NaN is NaN, one with an
- *   infinity is NaN there and zero elsewhere (before it is turned); a NaN stores 0.
+ *   infinity is NaN there and zero elsewhere (before it is turned), a head of zeros
+ *   with eps = 0 is NaN; a NaN stores code 0 (an fp16 cache keeps it).
  */
 i8kv_status norm_rope_and_cache(const uint16_t* q, int64_t q_stride, const uint16_t* k_new,
                                 int64_t k_stride, const uint16_t* v_new, int64_t v_stride,

@@ -446,7 +446,8 @@ def norm_rope_and_cache(q, k_new, v_new, q_weight, k_weight, eps: float, positio
     x / sqrt(mean(x^2) + eps) * weight, q_weight and k_weight [D] fp32 (None: not
     normed).  Returns (q_out, k_out): k_out [T, Hkv, D] fp16 holds the normed and
     turned keys, for ``packed_prefill`` over the new tokens; it is the tensor passed,
-    or one made here with return_keys, else None."""
+    or one made here with return_keys, else None.  (The root is within 2 units of the
+    last place, so a normed row is not determined bit for bit by the formula.)"""
     r = (_BINDING or _compiled()).norm_rope_and_cache(
         q, k_new, v_new, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scale, v_scale,
         scale_kind, interleaved, q_out, flags, None if stream is None else _stream(stream), q_weight,

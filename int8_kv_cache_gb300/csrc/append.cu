@@ -4,8 +4,8 @@
 //
 // Rotation of a pair (a, b) of channels by the angle of its position:
 //   a' = a cos - b sin,  b' = b cos + a sin
-// in fp32, every product and sum rounded on its own, so that the stored codes
-// follow from the formula bit for bit.  Queries leave as fp16; keys and values
+// in fp32, every product and sum rounded on its own, so that the stored codes of heads
+// that are not normed follow from the formula bit for bit.  Queries leave as fp16; keys and values
 // are stored in the cache's type:
 //   int8, e4m3fn  the codes of the IEEE quotient x / scale (as the plain
 //                 quantize-on-write stores them)
@@ -13,9 +13,9 @@
 //   MX4           y = x fl(1/scale); block scale s = e4m3(min(max|y| fl(1/6), 448)),
 //                 code = e2m1(y fl(1/s))
 //
-// The norm of a head: y = x r w with r = 1 / sqrt(mean x^2 + eps), rounded once, in fp32; the
-// squares of a thread's 16 channels are summed in order, then over the D / 16 lanes that hold the
-// head by halves.
+// The norm of a head: y = x r w with r = 1 / sqrt(mean x^2 + eps) in fp32, the root by rsqrtf (within 2
+// units of the last place); the squares of a thread's 16 channels are summed in two chains of fused products,
+// the even channels and the odd ones, which are added, then over the D / 16 lanes that hold the head by halves.
 //
 // Bound: HBM, rows in and rows out once each.  A thread keeps one item -- 16 channels
 // of a head as two pieces of 8, so that every access is 16 bytes and neighbouring
