@@ -638,15 +638,23 @@ i8kv_status packed_prefill(const uint16_t* q, int64_t q_stride, const uint16_t* 
  *                I8KV_MAX_PIECES: the batch's blocks of 128 positions are cut, on the
  *                device, into that many pieces of about equal length, one per CTA,
  *                whose ends fall anywhere in a tile's range; what belongs to one tile
- *                is merged by a second kernel.  0: automatic -- as many pieces as the
- *                device has SMs where the tiles alone would leave SMs idle (by T, B
- *                and the heads: the lengths are not known here), and the workspace is
- *                large enough; else unsplit
+ *                is merged by a second kernel.  0: automatic, by T, B and the heads
+ *                (the lengths are not known here) -- as many pieces as the device has
+ *                SMs where the whole (tile, KV head)s would leave many of them idle:
+ *                with tiles of 128 vectors (sequences below 192 on average, or D =
+ *                256) fewer than three to an SM, with tiles of 256 fewer than nine
+ *                tenths to an SM (of one sequence: a last round that is not nearly
+ *                full, of up to four); and cap > 128.  Unsplit else, and where the
+ *                workspace is too small for it
  *   workspace, workspace_bytes  paged_prefill_workspace_bytes(..., num_splits) for
  *                num_splits > 1 (16-byte aligned, else I8KV_EALIGN; too small
  *                I8KV_EWORKSPACE); may be NULL for 0 and 1.  Nothing in it
  *                outlives the call
  *   out, lse, head_sink, softcap, window  as for packed_prefill
+ * For a batch of single tokens alone paged_decode (MX4: paged_decode_mx4) is the
+ * faster call: it works on the vectors that are there, this one on tiles of 128 (16
+ * sequences of 512 to 8192, 32 / 8 heads x 128: int8 50 us against 75, MX4 30
+ * against 67, fp16 71 against 78).
  * A block-table entry of an attended position outside [0, num_blocks) is skipped
  * (I8KV_FLAG_BAD_BLOCK); entries of positions that nobody attends are not used.
  * Numerics: the cache's values are exact in the fp16 products, v_scale is applied
@@ -669,9 +677,14 @@ i8kv_status paged_prefill(const uint16_t* q, int64_t q_stride, const void* k_cac
  * paged_prefill_workspace_bytes -- bytes of the workspace of paged_prefill for T
  * new tokens of B sequences with at most cap positions and the given num_splits
  * (0: what the automatic choice takes on the current device): two tiles of 128 or
- * 256 vectors' partials for each piece, splits x 2 x 128 (or 256) x (D + 2) x 4,
- * about 41 MB at most for 152 SMs; 0 where it does not split, and for bad sizes.
- * Host only.
+ * 256 vectors' partials for each piece, splits x 2 x 128 (or 256) x (D + 2) x 4;
+ * 0 where it does not split, and for bad sizes.  Host only.
+ * This does not grow with T and B: a large batch may run whole and need nothing
+ * where a smaller one is split, and the same T in fewer sequences may take the
+ * larger tiles.  A workspace for all batches of a serving loop has
+ *     pieces x 2 x M x (D + 2) x 4 bytes, M = 256 for D 64 and 128, 128 for D 256
+ * (pieces: num_splits, or for 0 the device's SMs; 41 MB for 152 SMs at most), as
+ * this function gives for T = 256, B = 1 and num_splits = pieces.
  */
 size_t paged_prefill_workspace_bytes(int32_t T, int32_t B, int32_t Hq, int32_t Hkv, int32_t D,
                                      int64_t cap, int32_t num_splits);

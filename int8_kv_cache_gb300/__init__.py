@@ -508,7 +508,9 @@ def packed_prefill(q, k, v, seq_start, softmax_scale: float, head_sink=None, out
 def paged_prefill_workspace_bytes(T: int, B: int, Hq: int, Hkv: int, D: int, cap: int,
                                   num_splits: int = 0) -> int:
     """Bytes of paged_prefill's workspace for T new tokens of B sequences whose
-    block tables hold cap positions (0: the automatic choice does not split)."""
+    block tables hold cap positions (0: the automatic choice does not split).  The
+    need does not grow with T and B; T = 256, B = 1 and num_splits = the device's
+    SMs (or the num_splits that is used) gives what suits every batch."""
     return int(load().paged_prefill_workspace_bytes(T, B, Hq, Hkv, D, cap, num_splits))
 
 
@@ -523,7 +525,9 @@ def paged_prefill(q, k_cache, v_cache, k_scale, v_scale, scale_kind: int, block_
     tokens included) and query_start [B + 1] int32 on the device: sequence b's new
     tokens are the rows query_start[b] .. query_start[b + 1] - 1 of q and the last
     ones of its seq_lens[b].  With a workspace (paged_prefill_workspace_bytes) few
-    tokens over long caches are split over the GPU.  Returns ``out`` [T, Hq, D]."""
+    tokens over long caches are split over the GPU; too small a one is not used, with
+    num_splits 0.  (Single tokens alone are for ``paged_decode`` or
+    ``paged_decode_mx4``, which are faster there.)  Returns ``out`` [T, Hq, D]."""
     r = (_BINDING or _compiled()).paged_prefill(
         q, k_cache, v_cache, k_scale, v_scale, scale_kind, block_table, seq_lens, query_start,
         softmax_scale, head_sink, num_splits, workspace, out, lse, flags,
