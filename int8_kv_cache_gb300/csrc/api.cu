@@ -1190,7 +1190,11 @@ struct AttendPlan {
 //   two, several: below nine tenths of a round (128 tokens over 1024 to 16384 in four 167 / 120; 512 in eight 244 / 307;
 //     1 to 512 in twelve, MX4, 141 / 179; 300 to 1001 over 1001 to 4096 in four, e4m3fn, 16 / 2 x 64, 50 / 70):
 //     beyond, the longest first fill the gaps, and the merge costs more (not so where one sequence is far longer:
-//     512 over 16384 and over 600 in eleven more 298 / 254, which only the device knows)
+//     512 over 16384 and over 600 in eleven more 298 / 254, which only the device knows).  288 batches of 3 and 8 sequences
+//     of 0.37 to 1.15 rounds, each kind of cache, 32 / 8 x 128 and 16 / 2 x 64, whole's time over cut's (geometric mean):
+//     over prefixes of 2000 to 8000 tokens 1.14 below nine tenths (81 of 104 faster cut), 0.90 beyond (35 of 40 faster
+//     whole); over prefixes of one to three times the new tokens 0.52 and 0.61.  So the border is where whole tiles begin to
+//     win for either; below it the lengths decide, which the host does not know
 static bool attend_cuts(int64_t items, bool pairs, int32_t seqs, int sms) {
   if (!pairs) return items < INT64_C(3) * sms;
   if (seqs > 1) return items * 10 < INT64_C(9) * sms;
