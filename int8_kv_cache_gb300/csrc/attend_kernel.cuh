@@ -44,16 +44,17 @@
 // the largest entry comes to 2^14, so no range is lost; a score's error is at most
 // 2^-11 sum |q_d k_d|, what a cache of fp16 keys has).  Relative error against 64 bits (of the outputs'
 // norm): 2.1e-4 by their rounding to fp16 alone, 2.9e-4 with P's, 3.8e-4 with the folded queries'.  The
-// rest of that rounding as a second product would take half as many tensor-core cycles again, and with
-// two tiles of head_dim 128 shared memory has no room for it.
+// rest of that rounding as a second product would take half as many tensor-core cycles again; with two tiles of
+// head_dim 128, and with head_dim 256, neither memory has room for it beside K and V, and the forms that have it
+// (tensor memory with one tile, or head_dim 64) round as those do.
 //
 // Pieces (few vectors over long caches): the batch's blocks are cut into equal contiguous pieces,
 // one per CTA, whose ends fall anywhere in a (tile, KV head)'s range; a CTA writes fp32 partials of
 // the two ranges at most that its piece's ends cut, which attend_merge.cu joins.
 //
-// What bounds it (32 / 8 heads x 128): a prompt of 16384 the tensor cores, at 73 % of their measured
-// rate, by the chain from a block's scores over its softmax to its product with V (2700 to 3000 cycles
-// for 2048 of products); a quantised cache with few new tokens its conversion, 2900 cycles per 128
+// What bounds it (32 / 8 heads x 128): a prompt of 16384 the tensor cores, at 76 % of their measured
+// rate (1510 us), by the chain from a block's scores over its softmax to its product with V, which is longer than
+// the products of two tiles; a quantised cache with few new tokens its conversion, 2900 cycles per 128
 // positions of K and V of which 1800 are shared memory's (codes in and out, fp16 in, operands out);
 // a short call the way from the launch over the first item (2 us), its queries and a block's chain.
 //
