@@ -1,5 +1,7 @@
 // The dense causal attention with copies or arrivals that do not come, for test_gpu_attend_waits.py: a wait for them
-// runs out after 20 ms, and the kernel returns.  Every access stays in the buffers that the whole kernel uses.
+// runs out after 20 ms, and the kernel returns.  No access is other than the whole kernel's, and every wait ends: those for
+// barriers in memory by their limit or by the word in which one that ran out is told, the named barriers because all of
+// their warps come to them whatever became of their waits.
 #include <cuda_runtime.h>
 
 namespace {
